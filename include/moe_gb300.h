@@ -30,7 +30,7 @@
  *     are skipped; kernels never trap.  The caller zeroes it and reads it back.
  *   - Shapes are limited to hidden % 128 == 0, intermediate % 128 == 0,
  *     block_token == 128, 1 <= n_experts <= MOE_MAX_EXPERTS,
- *     num_blocks_m <= MOE_MAX_BLOCKS.
+ *     num_blocks_m <= MOE_MAX_BLOCKS, unless a call says otherwise.
  */
 #ifndef MOE_GB300_H
 #define MOE_GB300_H
@@ -46,7 +46,7 @@ typedef int32_t moe_status_t;
 
 #define MOE_OK            0
 #define MOE_ERR_NULL     -1  /* a required pointer is NULL                          */
-#define MOE_ERR_SHAPE    -2  /* a size is negative, inconsistent or not a multiple of 128 */
+#define MOE_ERR_SHAPE    -2  /* a size is negative, inconsistent or not the multiple asked for */
 #define MOE_ERR_ALIGN    -3  /* a pointer is not 16-byte aligned (TMA needs it)      */
 #define MOE_ERR_BLOCK    -4  /* block_token != 128                                   */
 #define MOE_ERR_DEVICE   -5  /* no usable sm_103 device / driver entry point         */
@@ -285,6 +285,65 @@ moe_status_t moe_fused_forward_static_workspace(
     const int32_t* group_sizes, const int32_t* group_offsets,
     const int32_t* group_padded_offsets, const int32_t* group_idx_for_bx, int64_t num_blocks_m,
     uint16_t* out, int32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense gated feed-forward block: the shared expert that every token passes
+ * beside its routed experts, and the dense layers, with gradients.
+ *
+ * One 16-bit type for all arrays of a call (`dtype`: MOE_DTYPE_F16 or
+ * MOE_DTYPE_BF16; bf16 data is passed as uint16_t bit patterns too).  Sums are
+ * fp32.  hidden and intermediate are multiples of 8 (16-byte rows), at most
+ * MOE_FFN_MAX_WIDTH; n_tokens is any number from 0 to MOE_FFN_MAX_TOKENS.
+ * Arrays are row-major and contiguous, 16-byte aligned, and must not overlap
+ * unless both are only read.
+ * ------------------------------------------------------------------------- */
+#define MOE_DTYPE_F16  0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F32  2
+
+#define MOE_FFN_MAX_TOKENS (1 << 24)
+#define MOE_FFN_MAX_WIDTH  (1 << 20)
+
+/* Forward:
+ *     G = x·gate_wᵀ, U = x·up_wᵀ           fp32
+ *     up_logits = round16( G·sigmoid(G) ⊙ U )
+ *     out       = round16( up_logits·down_wᵀ )
+ *   x                [n_tokens, hidden]
+ *   gate_w, up_w     [intermediate, hidden]
+ *   down_w           [hidden, intermediate]
+ *   gate, up         out, both or neither (NULL): [n_tokens, intermediate],
+ *                    round16(G) and round16(U), what the backward reads
+ *   up_logits        out: [n_tokens, intermediate] (workspace of a forward alone)
+ *   out              out: [n_tokens, hidden]
+ * Two kernel launches (the second with programmatic dependent launch).  Every
+ * wait inside is bounded (2 s); one that runs out sets MOE_DEV_TIMEOUT in
+ * status_dev (nullable) and leaves the outputs invalid. */
+moe_status_t moe_ffn_forward(int32_t dtype, const uint16_t* x, int64_t n_tokens, int32_t hidden,
+                             const uint16_t* gate_w, const uint16_t* up_w, const uint16_t* down_w,
+                             int32_t intermediate, uint16_t* gate, uint16_t* up, uint16_t* up_logits,
+                             uint16_t* out, int32_t* status_dev, void* stream);
+
+/* Workspace bytes of moe_ffn_backward (the gradients of G and U, 16-bit).
+ * Returns -1 for negative arguments. */
+int64_t moe_ffn_backward_workspace_bytes(int64_t n_tokens, int32_t intermediate);
+
+/* Gradients of the forward, from what it stored (gate, up, up_logits), with
+ * s = sigmoid(G) and d_h = d_out·down_w in fp32:
+ *     d_G = round16( d_h ⊙ U·s·(1 + G·(1 − s)) ),  d_U = round16( d_h ⊙ G·s )
+ *     d_x      = round16( d_G·gate_w + d_U·up_w )    [n_tokens, hidden]
+ *     d_gate_w = round16( d_Gᵀ·x )                   [intermediate, hidden]
+ *     d_up_w   = round16( d_Uᵀ·x )                   [intermediate, hidden]
+ *     d_down_w = round16( d_outᵀ·up_logits )         [hidden, intermediate]
+ * The weights' gradients are written, not added to (zeros for n_tokens == 0).
+ * workspace: device memory of moe_ffn_backward_workspace_bytes() bytes,
+ * caller-owned; calls that overlap on the GPU must not share it.  Two kernel
+ * launches; waits and status_dev as in the forward. */
+moe_status_t moe_ffn_backward(int32_t dtype, const uint16_t* d_out, const uint16_t* x, int64_t n_tokens,
+                              int32_t hidden, const uint16_t* gate_w, const uint16_t* up_w,
+                              const uint16_t* down_w, int32_t intermediate, const uint16_t* gate,
+                              const uint16_t* up, const uint16_t* up_logits, void* workspace,
+                              size_t workspace_bytes, uint16_t* d_x, uint16_t* d_gate_w, uint16_t* d_up_w,
+                              uint16_t* d_down_w, int32_t* status_dev, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,12 @@ Calls (names follow "Fused MoE GEMM æäº¤è¯´æ˜", Â§æäº¤æ–‡ä»¶ / Â§å®Œæ•´ç®—å
   pack_routed(topk_ids, topk_weights, x_tokens, tables)  -> grouped, padded inputs
   combine_routed(out, pair_rows)                -> token-major sum of the expert rows
   router_topk(x_tokens, router_w, top_k)        -> topk_ids, topk_weights
+
+The dense gated feed-forward block (fp16 or bf16):
+
+  gated_ffn(x, gate_w, up_w, down_w)            -> out (and, into given buffers, what the backward reads)
+  gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits)
+                                                -> d_x, d_gate_w, d_up_w, d_down_w
 """
 from __future__ import annotations
 
@@ -46,6 +52,9 @@ MOE_RUN_PHASE1 = 0x1
 MOE_RUN_PHASE2 = 0x2
 MOE_NO_PDL = 0x4
 MOE_TEST_DROP_SIGNAL = 0x100
+MOE_DTYPE_F16 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F32 = 2
 
 _lock = threading.Lock()
 _lib = None
@@ -109,6 +118,13 @@ def lib():
         L.moe_fused_forward_single_launch.argtypes = [P, i64, i32, P, P, P, i32, i32, P, i64,
                                                       P, P, P, P, i64, P, P, P, ctypes.c_size_t, P, P]
         L.moe_fused_forward_single_launch.restype = i32
+        L.moe_ffn_forward.argtypes = [i32, P, i64, i32, P, P, P, i32, P, P, P, P, P, P]
+        L.moe_ffn_forward.restype = i32
+        L.moe_ffn_backward_workspace_bytes.argtypes = [i64, i32]
+        L.moe_ffn_backward_workspace_bytes.restype = i64
+        L.moe_ffn_backward.argtypes = [i32, P, P, i64, i32, P, P, P, i32, P, P, P, P, ctypes.c_size_t,
+                                       P, P, P, P, P, P]
+        L.moe_ffn_backward.restype = i32
         _lib = L
         return L
 
@@ -350,3 +366,94 @@ def run_kernel(stacked_expert_tokens, gate_w, up_w, down_w, routed_expert_weight
         _WORKSPACE[key] = ws
     fused_forward(stacked_expert_tokens, gate_w, up_w, down_w, routed_expert_weights,
                   group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, ws, out)
+
+
+def _dtype_code(t, name, f32=False):
+    """MOE_DTYPE_* of a tensor's type."""
+    import torch
+    if t is torch.float16:
+        return MOE_DTYPE_F16
+    if t is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if f32 and t is torch.float32:
+        return MOE_DTYPE_F32
+    raise TypeError(f"{name} must be float16{', bfloat16 or float32' if f32 else ' or bfloat16'}, got {t}")
+
+
+def _ffn_weights(x, gate_w, up_w, down_w):
+    """The block's sizes, with every weight's type and shape checked against x."""
+    T, H = x.shape
+    dt = x.dtype
+    g = _dev(gate_w, "gate_w", dt, 2)
+    u = _dev(up_w, "up_w", dt, 2)
+    d = _dev(down_w, "down_w", dt, 2)
+    I = g.shape[0]
+    if g.shape[1] != H or tuple(u.shape) != (I, H) or tuple(d.shape) != (H, I):
+        raise ValueError("weight shapes do not match [intermediate, hidden] / [hidden, intermediate]")
+    return T, H, I
+
+
+def _shaped(t, name, dtype, shape):
+    """A caller's buffer of this type and shape."""
+    t = _dev(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=None, status=None, stream=None):
+    """The dense gated feed-forward block: ``out = (silu(xÂ·gate_wáµ€) âŠ™ (xÂ·up_wáµ€))Â·down_wáµ€``.
+
+    x [T, hidden], gate_w / up_w [intermediate, hidden], down_w [hidden,
+    intermediate], all float16 or all bfloat16; any T, hidden and intermediate
+    multiples of 8.  ``out`` [T, hidden] and ``up_logits`` [T, intermediate] (the
+    gated product, rounded) may be supplied.  For gradients supply ``gate`` and
+    ``up`` [T, intermediate] too: they receive the rounded projections, which
+    gated_ffn_backward reads with ``up_logits``."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    dt = x.dtype
+    x = _dev(x, "x", dt, 2)
+    T, H, I = _ffn_weights(x, gate_w, up_w, down_w)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are stored together: supply both or neither")
+    if gate is not None:
+        gate, up = _shaped(gate, "gate", dt, (T, I)), _shaped(up, "up", dt, (T, I))
+    up_logits = (torch.empty((T, I), dtype=dt, device=x.device) if up_logits is None
+                 else _shaped(up_logits, "up_logits", dt, (T, I)))
+    out = torch.empty((T, H), dtype=dt, device=x.device) if out is None else _shaped(out, "out", dt, (T, H))
+    _check(lib().moe_ffn_forward(code, _ptr(x), T, H, _ptr(gate_w), _ptr(up_w), _ptr(down_w), I, _ptr(gate), _ptr(up),
+                                 _ptr(up_logits), _ptr(out), _ptr(status), _stream(stream)), "moe_ffn_forward")
+    return out
+
+
+def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=None, d_gate_w=None, d_up_w=None,
+                       d_down_w=None, workspace=None, status=None, stream=None):
+    """Gradients of gated_ffn from d_out [T, hidden] and what the forward stored
+    (``gate``, ``up``, ``up_logits``): returns (d_x, d_gate_w, d_up_w, d_down_w) in
+    the inputs' type and shapes.  Supplied buffers are written, not added to.
+    ``workspace``: a device tensor of at least ffn_backward_workspace_bytes(T,
+    intermediate) bytes."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    dt = x.dtype
+    x = _dev(x, "x", dt, 2)
+    T, H, I = _ffn_weights(x, gate_w, up_w, down_w)
+    d_out = _shaped(d_out, "d_out", dt, (T, H))
+    gate, up = _shaped(gate, "gate", dt, (T, I)), _shaped(up, "up", dt, (T, I))
+    up_logits = _shaped(up_logits, "up_logits", dt, (T, I))
+    grads = []
+    for t, name, shape in ((d_x, "d_x", (T, H)), (d_gate_w, "d_gate_w", (I, H)), (d_up_w, "d_up_w", (I, H)),
+                           (d_down_w, "d_down_w", (H, I))):
+        grads.append(torch.empty(shape, dtype=dt, device=x.device) if t is None else _shaped(t, name, dt, shape))
+    if workspace is None:
+        workspace = torch.empty(max(ffn_backward_workspace_bytes(T, I), 16), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_ffn_backward(code, _ptr(d_out), _ptr(x), T, H, _ptr(gate_w), _ptr(up_w), _ptr(down_w), I,
+                                  _ptr(gate), _ptr(up), _ptr(up_logits), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), *[_ptr(g) for g in grads],
+                                  _ptr(status), _stream(stream)), "moe_ffn_backward")
+    return tuple(grads)
+
+
+def ffn_backward_workspace_bytes(n_tokens: int, intermediate: int) -> int:
+    return int(lib().moe_ffn_backward_workspace_bytes(int(n_tokens), int(intermediate)))

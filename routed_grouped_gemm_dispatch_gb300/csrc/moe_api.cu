@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/moe_gb300.h"
+#include "ffn_internal.h"
 #include "moe_internal.h"
 
 namespace {
@@ -41,7 +42,7 @@ const char* moe_status_string(moe_status_t s) {
     switch (s) {
         case MOE_OK: return "MOE_OK";
         case MOE_ERR_NULL: return "MOE_ERR_NULL: a required pointer is NULL";
-        case MOE_ERR_SHAPE: return "MOE_ERR_SHAPE: a size is negative, inconsistent or not a multiple of 128";
+        case MOE_ERR_SHAPE: return "MOE_ERR_SHAPE: a size is negative, inconsistent or not the multiple asked for";
         case MOE_ERR_ALIGN: return "MOE_ERR_ALIGN: a pointer is not 16-byte aligned";
         case MOE_ERR_BLOCK: return "MOE_ERR_BLOCK: block_token must be 128";
         case MOE_ERR_DEVICE: return "MOE_ERR_DEVICE: no usable sm_103 device or driver entry point";
@@ -249,6 +250,112 @@ moe_status_t moe_fused_forward(const uint16_t* stacked_expert_tokens, int64_t to
                                 group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx,
                                 num_blocks_m, up_logits, out, status_dev, stream,
                                 MOE_RUN_PHASE1 | MOE_RUN_PHASE2);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// dense gated feed-forward block
+// ---------------------------------------------------------------------------
+
+namespace {
+
+moe_status_t check_ffn_sizes(int32_t dtype, int64_t n_tokens, int32_t hidden, int32_t intermediate) {
+    if (dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_BF16) return MOE_ERR_SHAPE;
+    if (n_tokens < 0 || hidden <= 0 || intermediate <= 0 || hidden % 8 != 0 || intermediate % 8 != 0)
+        return MOE_ERR_SHAPE;
+    if (n_tokens > MOE_FFN_MAX_TOKENS || hidden > MOE_FFN_MAX_WIDTH || intermediate > MOE_FFN_MAX_WIDTH)
+        return MOE_ERR_LIMIT;
+    return MOE_OK;
+}
+
+// Bytes of one [n_tokens, intermediate] array of the backward's workspace.
+int64_t ffn_grad_bytes(int64_t n_tokens, int32_t intermediate) {
+    return (n_tokens * intermediate * 2 + 255) / 256 * 256;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_ffn_forward(int32_t dtype, const uint16_t* x, int64_t n_tokens, int32_t hidden,
+                             const uint16_t* gate_w, const uint16_t* up_w, const uint16_t* down_w,
+                             int32_t intermediate, uint16_t* gate, uint16_t* up, uint16_t* up_logits, uint16_t* out,
+                             int32_t* status_dev, void* stream) {
+    if (moe_status_t s = check_ffn_sizes(dtype, n_tokens, hidden, intermediate)) return s;
+    if (n_tokens == 0) return MOE_OK;
+    if (!x || !gate_w || !up_w || !down_w || !up_logits || !out || !gate != !up) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(gate_w) || !aligned16(up_w) || !aligned16(down_w) || !aligned16(gate) ||
+        !aligned16(up) || !aligned16(up_logits) || !aligned16(out))
+        return MOE_ERR_ALIGN;
+    if (moe_status_t s = check_device()) return s;
+    moe::FfnForward a{};
+    a.bf16 = dtype == MOE_DTYPE_BF16;
+    a.x = x;
+    a.n_tokens = n_tokens;
+    a.hidden = hidden;
+    a.gate_w = gate_w;
+    a.up_w = up_w;
+    a.down_w = down_w;
+    a.intermediate = intermediate;
+    a.gate = gate;
+    a.up = up;
+    a.up_logits = up_logits;
+    a.out = out;
+    a.status = status_dev;
+    return from_cuda(moe::launch_ffn_forward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_ffn_backward_workspace_bytes(int64_t n_tokens, int32_t intermediate) {
+    if (n_tokens < 0 || intermediate < 0) return -1;
+    return 2 * ffn_grad_bytes(n_tokens, intermediate);
+}
+
+moe_status_t moe_ffn_backward(int32_t dtype, const uint16_t* d_out, const uint16_t* x, int64_t n_tokens,
+                              int32_t hidden, const uint16_t* gate_w, const uint16_t* up_w, const uint16_t* down_w,
+                              int32_t intermediate, const uint16_t* gate, const uint16_t* up,
+                              const uint16_t* up_logits, void* workspace, size_t workspace_bytes, uint16_t* d_x,
+                              uint16_t* d_gate_w, uint16_t* d_up_w, uint16_t* d_down_w, int32_t* status_dev,
+                              void* stream) {
+    if (moe_status_t s = check_ffn_sizes(dtype, n_tokens, hidden, intermediate)) return s;
+    if (!d_gate_w || !d_up_w || !d_down_w) return MOE_ERR_NULL;
+    if (!aligned16(d_gate_w) || !aligned16(d_up_w) || !aligned16(d_down_w)) return MOE_ERR_ALIGN;
+    if (n_tokens == 0) {
+        // a sum over no tokens
+        if (moe_status_t s = check_device()) return s;
+        const size_t bytes = static_cast<size_t>(hidden) * static_cast<size_t>(intermediate) * 2;
+        for (uint16_t* d : {d_gate_w, d_up_w, d_down_w})
+            if (cudaMemsetAsync(d, 0, bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_ERR_LAUNCH;
+        return MOE_OK;
+    }
+    if (!d_out || !x || !gate_w || !up_w || !down_w || !gate || !up || !up_logits || !d_x) return MOE_ERR_NULL;
+    if (!aligned16(d_out) || !aligned16(x) || !aligned16(gate_w) || !aligned16(up_w) || !aligned16(down_w) ||
+        !aligned16(gate) || !aligned16(up) || !aligned16(up_logits) || !aligned16(d_x) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_ffn_backward_workspace_bytes(n_tokens, intermediate))
+        return MOE_ERR_WORKSPACE;
+    if (moe_status_t s = check_device()) return s;
+    moe::FfnBackward a{};
+    a.bf16 = dtype == MOE_DTYPE_BF16;
+    a.d_out = d_out;
+    a.x = x;
+    a.n_tokens = n_tokens;
+    a.hidden = hidden;
+    a.gate_w = gate_w;
+    a.up_w = up_w;
+    a.down_w = down_w;
+    a.intermediate = intermediate;
+    a.gate = gate;
+    a.up = up;
+    a.up_logits = up_logits;
+    a.d_gate = static_cast<uint16_t*>(workspace);
+    a.d_up = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + ffn_grad_bytes(n_tokens, intermediate));
+    a.d_x = d_x;
+    a.d_gate_w = d_gate_w;
+    a.d_up_w = d_up_w;
+    a.d_down_w = d_down_w;
+    a.status = status_dev;
+    return from_cuda(moe::launch_ffn_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -384,6 +384,22 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
     return d;
 }
 
+// Descriptor for an M/N-major operand (M or N contiguous) in 128-byte swizzled
+// atoms of 64 elements (16-bit) along M/N by 8 along K, as TMA boxes 64 wide
+// leave it: K rows of 128 bytes, so 1024 bytes between 8-row groups along K
+// (the stride-dimension offset) and `mn_stride` bytes between 64-element
+// chunks along M/N (the leading-dimension offset).  K = 16 further is 2048
+// bytes further.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, fp32
 // accumulation, both operands K-major, no negation, dense.
 //   bits 4-5 D format (1 = f32), 7-9 A format (0 = f16), 10-12 B format,
@@ -391,6 +407,12 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc_f16_f32acc(uint32_t m, uint32_t n) {
     return (1u << 4) | (0u << 7) | (0u << 10) | (0u << 15) | (0u << 16) |
            ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// The same for either 16-bit type (A and B alike) and either major-ness.
+__host__ __device__ constexpr uint32_t idesc_16bit_f32acc(uint32_t m, uint32_t n, bool bf16, bool a_mn, bool b_mn) {
+    return idesc_f16_f32acc(m, n) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+           (b_mn ? 1u << 16 : 0u);
 }
 
 }  // namespace moe
