@@ -345,6 +345,91 @@ moe_status_t moe_ffn_backward(int32_t dtype, const uint16_t* d_out, const uint16
                               size_t workspace_bytes, uint16_t* d_x, uint16_t* d_gate_w, uint16_t* d_up_w,
                               uint16_t* d_down_w, int32_t* status_dev, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit microscaled values (e2m1 codes, an e8m0 scale per 32 values of a row;
+ * OCP Microscaling Formats 1.0) and products of them.
+ *
+ * An array of [rows, cols] values, cols a multiple of 128, is held as
+ *   codes   [rows, cols/2] bytes, column 2i in the low half of byte i.  A code
+ *           is sign (8) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (0..7).
+ *   scales  one byte s per 32 columns, 2^(s-127), 255 = NaN, in tiles of 128 rows
+ *           x 4 blocks: [ceil(rows/128), cols/128, 32, 4, 4] with the byte of
+ *           row r, block b at [r/128, b/4, r%32, r/32%4, b%4] (the order in which
+ *           the tensor cores take them).
+ * A weight stack [n_experts, n, k] is an array of n_experts*n rows.  Pointers are
+ * 16-byte aligned; at most MOE_MX4_MAX_ROWS rows and MOE_MX4_MAX_COLS columns.
+ * ------------------------------------------------------------------------- */
+#define MOE_MX4_MAX_ROWS (1 << 24)
+#define MOE_MX4_MAX_COLS (1 << 17)
+
+/* Bytes of the scale tiles of [rows, cols]; -1 for arguments out of range. */
+int64_t moe_mx4_scale_bytes(int64_t rows, int32_t cols);
+
+/* Conversion to 4 bits.  With a = max |x| of a block of 32 and
+ * e = max(floor(log2 a) - 2, -127), the scale byte is e + 127 and a code is
+ * x·2^-e rounded to nearest even, saturated at ±6.  A block of zeros has scale
+ * byte 0; a block with an infinity or NaN has scale byte 255 and codes 0.
+ *   x          [n_src_rows, cols], `dtype` MOE_DTYPE_F16, _BF16 or _F32
+ *   src_rows   nullable: [n_rows] int32, the rows of x to convert (otherwise
+ *              n_rows must be n_src_rows); negative entries are skipped
+ *   dest_rows  nullable: [n_rows, copies] int32, the row(s) of the result that
+ *              each converted row goes to; negative entries are skipped, and no
+ *              row may be named twice.  Otherwise copies must be 1 and row i of
+ *              the list goes to row i, n_dest_rows must be n_rows, and scales
+ *              past the last row of the last tile are written as 0.
+ *   codes, scales  out: [n_dest_rows, cols] in 4 bits.  With dest_rows, rows not
+ *              named are left as they are.
+ * Entries at or past n_src_rows / n_dest_rows are skipped and set
+ * MOE_DEV_BAD_TABLE.  With dest_rows = moe_pack_routed's pair_padded_rows and
+ * copies = top_k this places quantised tokens in the grouped, padded layout.
+ * One kernel launch. */
+moe_status_t moe_mx4_quantize(int32_t dtype, const void* x, int64_t n_src_rows, int32_t cols,
+                              const int32_t* src_rows, int64_t n_rows, const int32_t* dest_rows, int32_t copies,
+                              int64_t n_dest_rows, uint8_t* codes, uint8_t* scales, int32_t* status_dev,
+                              void* stream);
+
+/* The values that codes and scales stand for, rounded to nearest even in
+ * `dtype` where that cannot hold them: out [rows, cols].  One kernel launch. */
+moe_status_t moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                                int32_t dtype, void* out, void* stream);
+
+/* Products of 4-bit operands with fp32 sums, on the block-scaled tensor cores;
+ * results are fp16 or bf16 (`dtype`).  k, n, hidden and intermediate are
+ * multiples of 128.  One kernel launch each; waits inside are bounded (2 s) as in
+ * the other products (MOE_DEV_TIMEOUT).  A NaN scale of a row of A reaches only
+ * that row's results.
+ *
+ * moe_mx4_matmul: out[i, j] = Σ_k a[i, k]·b[j, k]; a [rows, k], b [n, k], any
+ * number of rows up to 128 * MOE_MAX_BLOCKS. */
+moe_status_t moe_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t rows, int32_t k, const uint8_t* b,
+                            const uint8_t* b_scales, int32_t n, int32_t dtype, uint16_t* out,
+                            int32_t* status_dev, void* stream);
+
+/* moe_mx4_gate_up: the first half of the routed experts with 4-bit operands, in
+ * the layout and with the tables of moe_fused_forward: for valid rows
+ *     up_logits[p, :] = round16( silu(x[p]·gate[e]ᵀ) ⊙ (x[p]·up[e]ᵀ) )
+ * x [total_padded_tokens, hidden]; gate, up [n_experts, intermediate, hidden];
+ * up_logits [total_padded_tokens, intermediate], padding rows not written. */
+moe_status_t moe_mx4_gate_up(const uint8_t* x, const uint8_t* x_scales, int64_t total_padded_tokens,
+                             int32_t hidden, const uint8_t* gate, const uint8_t* gate_scales, const uint8_t* up,
+                             const uint8_t* up_scales, int32_t n_experts, int32_t intermediate,
+                             const int32_t* group_sizes, const int32_t* group_padded_offsets,
+                             const int32_t* group_idx_for_bx, int64_t num_blocks_m, int32_t dtype,
+                             uint16_t* up_logits, int32_t* status_dev, void* stream);
+
+/* moe_mx4_down: the second half,
+ *     out[p, :] = round16( (h[p]·down[e]ᵀ) · routed_expert_weights[c] )
+ * h [total_padded_tokens, intermediate] (up_logits after moe_mx4_quantize), down
+ * [n_experts, hidden, intermediate], c the row's compact index as in
+ * moe_fused_forward; out [total_padded_tokens, hidden], padding rows not
+ * written. */
+moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t total_padded_tokens,
+                          int32_t intermediate, const uint8_t* down, const uint8_t* down_scales,
+                          int32_t n_experts, int32_t hidden, const float* routed_expert_weights,
+                          int64_t total_valid_tokens, const int32_t* group_sizes, const int32_t* group_offsets,
+                          const int32_t* group_padded_offsets, const int32_t* group_idx_for_bx,
+                          int64_t num_blocks_m, int32_t dtype, uint16_t* out, int32_t* status_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,14 @@ The dense gated feed-forward block (fp16 or bf16):
   gated_ffn(x, gate_w, up_w, down_w)            -> out (and, into given buffers, what the backward reads)
   gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits)
                                                 -> d_x, d_gate_w, d_up_w, d_down_w
+
+4-bit microscaled values (codes and scales) and products of them:
+
+  mx4_quantize(x)                               -> codes, scales
+  mx4_dequantize(codes, scales, dtype)          -> the values they stand for
+  mx4_matmul(a, a_scales, b, b_scales)          -> a·bᵀ
+  mx4_gate_up(...), mx4_down(...)               the routed experts' two halves, in the
+                                                layout and with the tables of fused_forward
 """
 from __future__ import annotations
 
@@ -125,6 +133,18 @@ def lib():
         L.moe_ffn_backward.argtypes = [i32, P, P, i64, i32, P, P, P, i32, P, P, P, P, ctypes.c_size_t,
                                        P, P, P, P, P, P]
         L.moe_ffn_backward.restype = i32
+        L.moe_mx4_scale_bytes.argtypes = [i64, i32]
+        L.moe_mx4_scale_bytes.restype = i64
+        L.moe_mx4_quantize.argtypes = [i32, P, i64, i32, P, i64, P, i32, i64, P, P, P, P]
+        L.moe_mx4_quantize.restype = i32
+        L.moe_mx4_dequantize.argtypes = [P, P, i64, i32, i32, P, P]
+        L.moe_mx4_dequantize.restype = i32
+        L.moe_mx4_matmul.argtypes = [P, P, i64, i32, P, P, i32, i32, P, P, P]
+        L.moe_mx4_matmul.restype = i32
+        L.moe_mx4_gate_up.argtypes = [P, P, i64, i32, P, P, P, P, i32, i32, P, P, P, i64, i32, P, P, P]
+        L.moe_mx4_gate_up.restype = i32
+        L.moe_mx4_down.argtypes = [P, P, i64, i32, P, P, i32, i32, P, i64, P, P, P, P, i64, i32, P, P, P]
+        L.moe_mx4_down.restype = i32
         _lib = L
         return L
 
@@ -457,3 +477,157 @@ def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=
 
 def ffn_backward_workspace_bytes(n_tokens: int, intermediate: int) -> int:
     return int(lib().moe_ffn_backward_workspace_bytes(int(n_tokens), int(intermediate)))
+
+
+def _mx4_scale_shape(rows, cols):
+    return (-(-rows // 128), cols // 128, 32, 4, 4)
+
+
+def _mx4(codes, scales, name, ndim):
+    """Checked codes and scales of a 4-bit array; returns its leading sizes and its columns."""
+    import torch
+    c = _dev(codes, name, torch.uint8, ndim)
+    s = _dev(scales, f"{name}_scales", torch.uint8)
+    cols = 2 * c.shape[-1]
+    rows = c.numel() // max(c.shape[-1], 1)
+    if cols == 0 or cols % 128:
+        raise ValueError(f"{name} must hold a multiple of 128 columns, got {cols}")
+    if s.numel() != -(-rows // 128) * (cols // 128) * 512:
+        raise ValueError(f"{name}_scales must hold the tiles {_mx4_scale_shape(rows, cols)}, got {tuple(s.shape)}")
+    return (*c.shape[:-1], cols)
+
+
+def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scales=None, status=None, stream=None):
+    """4-bit microscaled form of x ([rows, cols], or a weight stack [experts, n,
+    cols]), float16, bfloat16 or float32, cols a multiple of 128: returns
+    (codes uint8 [..., cols/2], scales uint8 [ceil(rows/128), cols/128, 32, 4, 4]),
+    the scale of row r, block b at [r//128, b//4, r%32, r//32%4, b%4].
+
+    For a 2-D x, ``src_rows`` [n] int32 picks the rows to convert and ``dest_rows``
+    [n] or [n, copies] int32 the rows of a result of ``n_dest`` rows that each goes
+    to (negative entries are skipped; result rows not named keep what the given
+    ``codes`` and ``scales`` held, and are undefined in new ones).  With
+    dest_rows = pack_routed's pair_padded_rows the tokens land in the grouped,
+    padded layout."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x", f32=True)
+    x = _dev(x, "x", x.dtype)
+    if x.dim() not in (2, 3) or (x.dim() == 3 and (src_rows is not None or dest_rows is not None)):
+        raise ValueError("x must have 2 dims, or 3 without row lists")
+    cols = x.shape[-1]
+    if cols == 0 or cols % 128:
+        raise ValueError(f"x must have a multiple of 128 columns, got {cols}")
+    n_src = x.numel() // cols
+    n, copies = n_src, 1
+    if src_rows is not None:
+        n = _dev(src_rows, "src_rows", torch.int32, 1).numel()
+    lead = x.shape[:-1]
+    if dest_rows is not None:
+        d = _dev(dest_rows, "dest_rows", torch.int32)
+        if d.dim() not in (1, 2) or d.shape[0] != n:
+            raise ValueError("dest_rows must be [rows converted] or [rows converted, copies]")
+        copies = d.shape[1] if d.dim() == 2 else 1
+        if codes is not None:
+            n_dest = codes.shape[0]
+        if n_dest is None:
+            raise ValueError("dest_rows needs n_dest (or codes and scales to write)")
+        lead = (int(n_dest),)
+    elif src_rows is not None:
+        lead = (n,)
+    n_out = n_src if x.dim() == 3 else lead[0]
+    if codes is None:
+        codes = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device)
+    else:
+        codes = _shaped(codes, "codes", torch.uint8, (*lead, cols // 2))
+    if scales is None:
+        scales = torch.empty(_mx4_scale_shape(n_out, cols), dtype=torch.uint8, device=x.device)
+    else:
+        scales = _shaped(scales, "scales", torch.uint8, _mx4_scale_shape(n_out, cols))
+    if copies == 0:
+        return codes, scales
+    _check(lib().moe_mx4_quantize(code, _ptr(x), n_src, cols, _ptr(src_rows), n, _ptr(dest_rows), copies, n_out,
+                                  _ptr(codes), _ptr(scales), _ptr(status), _stream(stream)), "moe_mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, dtype, out=None, stream=None):
+    """The values that 4-bit codes [..., cols/2] and their scales stand for, in
+    ``dtype`` (float16, bfloat16 or float32): [..., cols]."""
+    import torch
+    code = _dtype_code(dtype, "dtype", f32=True)
+    shape = _mx4(codes, scales, "codes", None)
+    out = torch.empty(shape, dtype=dtype, device=codes.device) if out is None else _shaped(out, "out", dtype, shape)
+    cols = shape[-1]
+    _check(lib().moe_mx4_dequantize(_ptr(codes), _ptr(scales), out.numel() // cols, cols, code, _ptr(out),
+                                    _stream(stream)), "moe_mx4_dequantize")
+    return out
+
+
+def mx4_matmul(a, a_scales, b, b_scales, out=None, dtype=None, status=None, stream=None):
+    """out = a·bᵀ of 4-bit a [rows, k] and b [n, k] (codes and scales), fp32 sums,
+    float16 or bfloat16 result [rows, n] (``dtype``, float16 unless ``out`` says)."""
+    import torch
+    rows, k = _mx4(a, a_scales, "a", 2)
+    n, kb = _mx4(b, b_scales, "b", 2)
+    if kb != k:
+        raise ValueError(f"a and b must have the same columns, got {k} and {kb}")
+    if out is None:
+        out = torch.empty((rows, n), dtype=dtype or torch.float16, device=a.device)
+    code = _dtype_code(getattr(out, "dtype", None), "out")
+    _shaped(out, "out", out.dtype, (rows, n))
+    _check(lib().moe_mx4_matmul(_ptr(a), _ptr(a_scales), rows, k, _ptr(b), _ptr(b_scales), n, code, _ptr(out),
+                                _ptr(status), _stream(stream)), "moe_mx4_matmul")
+    return out
+
+
+def _mx4_tables(group_sizes, group_padded_offsets, group_idx_for_bx, n_experts):
+    import torch
+    s = _dev(group_sizes, "group_sizes", torch.int32, 1)
+    p = _dev(group_padded_offsets, "group_padded_offsets", torch.int32, 1)
+    g = _dev(group_idx_for_bx, "group_idx_for_bx", torch.int32, 1)
+    if s.numel() != n_experts or p.numel() < n_experts:
+        raise ValueError("table lengths do not match n_experts")
+    return g.numel()
+
+
+def mx4_gate_up(x, x_scales, gate, gate_scales, up, up_scales, group_sizes, group_padded_offsets, group_idx_for_bx,
+                up_logits, status=None, stream=None):
+    """First half of the routed experts with 4-bit operands: x [padded rows, hidden],
+    gate / up [experts, intermediate, hidden] (codes and scales).  Writes ``up_logits``
+    [padded rows, intermediate] (float16 or bfloat16) on valid rows and returns it."""
+    rows, H = _mx4(x, x_scales, "x", 2)
+    E, I, Hg = _mx4(gate, gate_scales, "gate", 3)
+    if Hg != H or _mx4(up, up_scales, "up", 3) != (E, I, H):
+        raise ValueError("weight shapes do not match [E, I, H]")
+    code = _dtype_code(getattr(up_logits, "dtype", None), "up_logits")
+    _shaped(up_logits, "up_logits", up_logits.dtype, (rows, I))
+    m = _mx4_tables(group_sizes, group_padded_offsets, group_idx_for_bx, E)
+    _check(lib().moe_mx4_gate_up(_ptr(x), _ptr(x_scales), rows, H, _ptr(gate), _ptr(gate_scales), _ptr(up),
+                                 _ptr(up_scales), E, I, _ptr(group_sizes), _ptr(group_padded_offsets),
+                                 _ptr(group_idx_for_bx), m, code, _ptr(up_logits), _ptr(status), _stream(stream)),
+           "moe_mx4_gate_up")
+    return up_logits
+
+
+def mx4_down(h, h_scales, down, down_scales, routed_expert_weights, group_sizes, group_offsets,
+             group_padded_offsets, group_idx_for_bx, out, status=None, stream=None):
+    """Second half of the routed experts with 4-bit operands: h [padded rows,
+    intermediate], down [experts, hidden, intermediate] (codes and scales).  Writes
+    ``out`` [padded rows, hidden] (float16 or bfloat16), each valid row times its routed
+    weight, and returns it."""
+    import torch
+    rows, I = _mx4(h, h_scales, "h", 2)
+    E, H, Id = _mx4(down, down_scales, "down", 3)
+    if Id != I:
+        raise ValueError("weight shapes do not match [E, H, I]")
+    w = _dev(routed_expert_weights, "routed_expert_weights", torch.float32, 1)
+    offs = _dev(group_offsets, "group_offsets", torch.int32, 1)
+    code = _dtype_code(getattr(out, "dtype", None), "out")
+    _shaped(out, "out", out.dtype, (rows, H))
+    m = _mx4_tables(group_sizes, group_padded_offsets, group_idx_for_bx, E)
+    if offs.numel() < E:
+        raise ValueError("table lengths do not match n_experts")
+    _check(lib().moe_mx4_down(_ptr(h), _ptr(h_scales), rows, I, _ptr(down), _ptr(down_scales), E, H, _ptr(w), w.numel(),
+                              _ptr(group_sizes), _ptr(offs), _ptr(group_padded_offsets), _ptr(group_idx_for_bx), m,
+                              code, _ptr(out), _ptr(status), _stream(stream)), "moe_mx4_down")
+    return out

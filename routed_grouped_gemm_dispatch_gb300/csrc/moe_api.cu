@@ -8,6 +8,7 @@
 #include "../../include/moe_gb300.h"
 #include "ffn_internal.h"
 #include "moe_internal.h"
+#include "mx4_internal.h"
 
 namespace {
 
@@ -356,6 +357,183 @@ moe_status_t moe_ffn_backward(int32_t dtype, const uint16_t* d_out, const uint16
     a.d_down_w = d_down_w;
     a.status = status_dev;
     return from_cuda(moe::launch_ffn_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 4-bit microscaled values
+// ---------------------------------------------------------------------------
+
+namespace {
+
+moe_status_t check_mx4_array(int64_t rows, int32_t cols) {
+    if (rows < 0 || cols <= 0 || cols % 128 != 0) return MOE_ERR_SHAPE;
+    if (rows > MOE_MX4_MAX_ROWS || cols > MOE_MX4_MAX_COLS) return MOE_ERR_LIMIT;
+    return MOE_OK;
+}
+
+moe_status_t check_16bit(int32_t dtype) {
+    return dtype == MOE_DTYPE_F16 || dtype == MOE_DTYPE_BF16 ? MOE_OK : MOE_ERR_SHAPE;
+}
+
+// Sizes, limits, pointers and alignment of a product, in that order.
+moe_status_t check_mx4_product(const moe::Mx4Product& a, bool grouped) {
+    if (moe_status_t s = check_mx4_array(a.rows, a.k)) return s;
+    if (a.n <= 0 || a.n % 128 != 0 || a.num_blocks < 0 || a.valid_total < 0) return MOE_ERR_SHAPE;
+    if (a.n_experts <= 0 || a.n_experts > MOE_MAX_EXPERTS || a.n > MOE_MX4_MAX_COLS ||
+        static_cast<int64_t>(a.n_experts) * a.n > MOE_MX4_MAX_ROWS || a.num_blocks > MOE_MAX_BLOCKS)
+        return MOE_ERR_LIMIT;
+    if (grouped && a.rows < a.num_blocks * MOE_BLOCK_TOKEN) return MOE_ERR_SHAPE;
+    if (a.num_blocks == 0) return MOE_OK;
+    const bool gate_up = a.form == moe::MX4_GATE_UP;
+    if (!a.a || !a.a_scales || !a.b || !a.b_scales || (gate_up && (!a.b2 || !a.b2_scales)) || !a.out)
+        return MOE_ERR_NULL;
+    if (grouped && (!a.sizes || !a.padded || !a.gidx)) return MOE_ERR_NULL;
+    if (a.form == moe::MX4_DOWN && (!a.offsets || (a.valid_total > 0 && !a.weights))) return MOE_ERR_NULL;
+    if (!aligned16(a.a) || !aligned16(a.a_scales) || !aligned16(a.b) || !aligned16(a.b_scales) ||
+        !aligned16(a.b2) || !aligned16(a.b2_scales) || !aligned16(a.out))
+        return MOE_ERR_ALIGN;
+    return check_device();
+}
+
+moe_status_t run_mx4_product(const moe::Mx4Product& a, bool grouped, void* stream) {
+    if (moe_status_t s = check_mx4_product(a, grouped)) return s;
+    if (a.num_blocks == 0) return MOE_OK;
+    return from_cuda(moe::launch_mx4_product(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_mx4_scale_bytes(int64_t rows, int32_t cols) {
+    if (check_mx4_array(rows, cols) != MOE_OK) return -1;
+    return (rows + 127) / 128 * (cols / 128) * 512;
+}
+
+moe_status_t moe_mx4_quantize(int32_t dtype, const void* x, int64_t n_src_rows, int32_t cols, const int32_t* src_rows,
+                              int64_t n_rows, const int32_t* dest_rows, int32_t copies, int64_t n_dest_rows,
+                              uint8_t* codes, uint8_t* scales, int32_t* status_dev, void* stream) {
+    if (dtype != MOE_DTYPE_F32)
+        if (moe_status_t s = check_16bit(dtype)) return s;
+    if (copies < 1 || n_rows < 0 || (!src_rows && n_rows != n_src_rows) ||
+        (!dest_rows && (copies != 1 || n_dest_rows != n_rows)))
+        return MOE_ERR_SHAPE;
+    if (moe_status_t s = check_mx4_array(n_src_rows, cols)) return s;
+    if (moe_status_t s = check_mx4_array(n_dest_rows, cols)) return s;
+    if (n_rows > MOE_MX4_MAX_ROWS) return MOE_ERR_LIMIT;
+    if (n_rows == 0) return MOE_OK;
+    if (!x || !codes || !scales) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_ALIGN;
+    if (moe_status_t s = check_device()) return s;
+    moe::Mx4Quantize a{};
+    a.dtype = dtype;
+    a.x = x;
+    a.n_src = n_src_rows;
+    a.n_rows = n_rows;
+    a.cols = cols;
+    a.src_rows = src_rows;
+    a.dest_rows = dest_rows;
+    a.copies = copies;
+    a.n_dest = n_dest_rows;
+    a.codes = codes;
+    a.scales = scales;
+    a.status = status_dev;
+    return from_cuda(moe::launch_mx4_quantize(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, int32_t dtype,
+                                void* out, void* stream) {
+    if (dtype != MOE_DTYPE_F32)
+        if (moe_status_t s = check_16bit(dtype)) return s;
+    if (moe_status_t s = check_mx4_array(rows, cols)) return s;
+    if (rows == 0) return MOE_OK;
+    if (!codes || !scales || !out) return MOE_ERR_NULL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return MOE_ERR_ALIGN;
+    if (moe_status_t s = check_device()) return s;
+    return from_cuda(
+        moe::launch_mx4_dequantize(codes, scales, rows, cols, dtype, out, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t rows, int32_t k, const uint8_t* b,
+                            const uint8_t* b_scales, int32_t n, int32_t dtype, uint16_t* out, int32_t* status_dev,
+                            void* stream) {
+    if (moe_status_t s = check_16bit(dtype)) return s;
+    moe::Mx4Product m{};
+    m.form = moe::MX4_MATMUL;
+    m.bf16 = dtype == MOE_DTYPE_BF16;
+    m.a = a;
+    m.a_scales = a_scales;
+    m.rows = rows;
+    m.k = k;
+    m.b = b;
+    m.b_scales = b_scales;
+    m.n_experts = 1;
+    m.n = n;
+    m.num_blocks = rows < 0 ? 0 : (rows + MOE_BLOCK_TOKEN - 1) / MOE_BLOCK_TOKEN;
+    m.out = out;
+    m.status = status_dev;
+    return run_mx4_product(m, false, stream);
+}
+
+moe_status_t moe_mx4_gate_up(const uint8_t* x, const uint8_t* x_scales, int64_t total_padded_tokens, int32_t hidden,
+                             const uint8_t* gate, const uint8_t* gate_scales, const uint8_t* up,
+                             const uint8_t* up_scales, int32_t n_experts, int32_t intermediate,
+                             const int32_t* group_sizes, const int32_t* group_padded_offsets,
+                             const int32_t* group_idx_for_bx, int64_t num_blocks_m, int32_t dtype,
+                             uint16_t* up_logits, int32_t* status_dev, void* stream) {
+    if (moe_status_t s = check_16bit(dtype)) return s;
+    moe::Mx4Product m{};
+    m.form = moe::MX4_GATE_UP;
+    m.bf16 = dtype == MOE_DTYPE_BF16;
+    m.a = x;
+    m.a_scales = x_scales;
+    m.rows = total_padded_tokens;
+    m.k = hidden;
+    m.b = gate;
+    m.b_scales = gate_scales;
+    m.b2 = up;
+    m.b2_scales = up_scales;
+    m.n_experts = n_experts;
+    m.n = intermediate;
+    m.sizes = group_sizes;
+    m.padded = group_padded_offsets;
+    m.gidx = group_idx_for_bx;
+    m.num_blocks = num_blocks_m;
+    m.out = up_logits;
+    m.status = status_dev;
+    return run_mx4_product(m, true, stream);
+}
+
+moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t total_padded_tokens, int32_t intermediate,
+                          const uint8_t* down, const uint8_t* down_scales, int32_t n_experts, int32_t hidden,
+                          const float* routed_expert_weights, int64_t total_valid_tokens, const int32_t* group_sizes,
+                          const int32_t* group_offsets, const int32_t* group_padded_offsets,
+                          const int32_t* group_idx_for_bx, int64_t num_blocks_m, int32_t dtype, uint16_t* out,
+                          int32_t* status_dev, void* stream) {
+    if (moe_status_t s = check_16bit(dtype)) return s;
+    moe::Mx4Product m{};
+    m.form = moe::MX4_DOWN;
+    m.bf16 = dtype == MOE_DTYPE_BF16;
+    m.a = h;
+    m.a_scales = h_scales;
+    m.rows = total_padded_tokens;
+    m.k = intermediate;
+    m.b = down;
+    m.b_scales = down_scales;
+    m.n_experts = n_experts;
+    m.n = hidden;
+    m.weights = routed_expert_weights;
+    m.valid_total = total_valid_tokens;
+    m.sizes = group_sizes;
+    m.offsets = group_offsets;
+    m.padded = group_padded_offsets;
+    m.gidx = group_idx_for_bx;
+    m.num_blocks = num_blocks_m;
+    m.out = out;
+    m.status = status_dev;
+    return run_mx4_product(m, true, stream);
 }
 
 }  // extern "C"

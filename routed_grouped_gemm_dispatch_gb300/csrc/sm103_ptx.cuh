@@ -415,4 +415,49 @@ __host__ __device__ constexpr uint32_t idesc_16bit_f32acc(uint32_t m, uint32_t n
            (b_mn ? 1u << 16 : 0u);
 }
 
+// ---------------------------------------------------------------------------
+// 4-bit operands with a scale per 32 values along K (kind::mxf4)
+// ---------------------------------------------------------------------------
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Copy 32 rows of 16 bytes (512 contiguous bytes at the descriptor's address)
+// into four TMEM columns of lanes 0-31, repeated in the other three lane
+// quarters: the layout in which the block-scaled MMA reads the scales of 128
+// rows x 4 blocks, row r in lane r % 32, column r / 32, a byte per block.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of such a 512-byte tile: no swizzle, 8-row groups of 128 bytes.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128u >> 4) << 32 |
+           static_cast<uint64_t>(1u) << 46;
+}
+
+// D[tmem] (+)= (A ⊙ scales)·(B ⊙ scales)ᵀ for one K = 64 slice of e2m1 values.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::mxf4, K = 64: e2m1 A and B (format 1, bits
+// 7-9 and 10-11), both K-major, e8m0 scales (bit 23), N >> 3 in bits 17-22,
+// M >> 4 in bits 24-28.  `half` picks the scale bytes inside each 32-bit TMEM
+// word: 0 the first two blocks of 32, 1 the last two (data id 0 or 2, bits 4-5
+// for B and 29-30 for A).
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32_t half) {
+    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | ((2u * half) << 4) |
+           ((2u * half) << 29);
+}
+
 }  // namespace moe
