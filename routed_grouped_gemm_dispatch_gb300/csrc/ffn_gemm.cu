@@ -170,12 +170,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         tmem_alloc_pair(sbase + OFF_TMEM_SLOT, TMEM_COLS);
         tmem_relinquish_pair();
     }
-    // Everything above overlaps the kernel before; every global access is below.
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    // Everything above overlaps the kernel before; every global access is below.
+    // The next kernel may start only now that this CTA holds its TMEM.
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
     const uint32_t tmem_base = *tmem_slot;
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
@@ -513,6 +514,7 @@ bool box_map(Maps& maps, int i, const void* base, int64_t rows, int64_t cols) {
 }  // namespace
 
 cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream) {
+    if (a.n_tokens <= FFN_SMALL_TOKENS) return launch_ffn_forward_small(a, stream);
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
     const int64_t T = a.n_tokens;
     const int32_t H = a.hidden, I = a.intermediate;

@@ -46,6 +46,9 @@ struct FfnBackward {
 
 // Arguments already validated, n_tokens > 0.
 cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream);
+// The forward for at most FFN_SMALL_TOKENS tokens.
+constexpr int64_t FFN_SMALL_TOKENS = 128;
+cudaError_t launch_ffn_forward_small(const FfnForward& a, cudaStream_t stream);
 cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream);
 
 }  // namespace moe
