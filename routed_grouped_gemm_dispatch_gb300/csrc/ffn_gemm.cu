@@ -20,7 +20,7 @@
 //  * Persistent clusters of two CTAs, one 2-SM MMA tile of M = 256 x N = 256 at
 //    a time: each CTA holds 128 rows of A and 128 of B per stage (K = 128, 64 KB,
 //    ring of three), warp 0 feeds the ring by TMA, warp 1 of the even CTA issues
-//    the MMAs into one of two TMEM accumulators, and warps 2-5 of both CTAs turn
+//    the MMAs into one of two TMEM accumulators, and warps 2-9 of both CTAs turn
 //    the other one into 16-bit rows meanwhile.  With 128 x 256 tiles on one SM
 //    the operands' way into and out of shared memory, not the tensor core, is
 //    the bound; the pair halves the bytes of B each SM moves.
@@ -41,6 +41,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <utility>
 
 #include "../../include/moe_gb300.h"
 #include "ffn_internal.h"
@@ -60,10 +61,11 @@ constexpr int OP_BYTES = BM * BK * 2;          // one operand's stage: two boxes
 constexpr int BOX_BYTES = OP_BYTES / 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int NUM_THREADS = 192;
-constexpr int NUM_EPI_THREADS = 128;
-constexpr int CLUSTER = 2;
-constexpr uint16_t CLUSTER_MASK = 0x3;
+constexpr int NUM_THREADS = 320;               // producer, MMA and eight epilogue warps
+constexpr int NUM_EPI_THREADS = 256;
+constexpr int PAIR = 2;                        // CTAs of one MMA tile
+constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
+constexpr int MIN_STEPS = 3;                   // stages each of them keeps at least
 constexpr int GROUP_M = 8;                     // tile rows (of 256) that are walked together
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
@@ -99,6 +101,8 @@ struct Plan {
     Problem pr[MAX_PROBLEMS];
     int32_t n_problems;
     int32_t total_tiles;
+    int32_t split;                 // pairs per cluster
+    int32_t split_tiles;           // the first so many tiles are shared by a cluster's pairs
     int32_t tile_cols;             // output columns of a tile: 128 (gate and up side by side) or 256
     const uint16_t* gate_in;       // EPI_GRAD: stored G, U [m, n]
     const uint16_t* up_in;
@@ -132,7 +136,27 @@ __device__ __forceinline__ Tile tile_at(const Plan& p, int32_t t) {
     return ti;
 }
 
-template <int EPI, bool BF16>
+__device__ __forceinline__ void store_remote4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Adds the other pairs' partial sums of 32 columns (`at`: this row's first quad
+// in the first pair's slot, quads 128 rows apart) in pair order.
+__device__ __forceinline__ void add_partials(uint32_t (&v)[32], const uint8_t* at, int slots, uint32_t slot_bytes) {
+    for (int s = 0; s < slots; ++s) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(at + s * slot_bytes + q * (BM * 16));
+            v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + x.x);
+            v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + x.y);
+            v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + x.z);
+            v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + x.w);
+        }
+    }
+}
+
+template <int EPI, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan p) {
     extern __shared__ uint8_t smem_raw[];
@@ -150,8 +174,11 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    const uint32_t rank = cluster_cta_rank();
+    const uint32_t cluster_rank = cluster_cta_rank();
+    const uint32_t pair = SPLIT ? cluster_rank >> 1 : 0;         // of the cluster
+    const uint32_t rank = cluster_rank & 1u;                     // inside the pair
     const bool leader = rank == 0;
+    const uint16_t pair_mask = static_cast<uint16_t>(0x3u << (2 * pair));
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -160,7 +187,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar_tfull + 8 * a, 1);
-            mbar_init(bar_tempty + 8 * a, CLUSTER * NUM_EPI_THREADS);
+            mbar_init(bar_tempty + 8 * a, PAIR * NUM_EPI_THREADS);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -180,233 +207,327 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     const uint32_t tmem_base = *tmem_slot;
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
-    const int32_t cluster_id = static_cast<int32_t>(blockIdx.x) / CLUSTER;
-    const int32_t n_clusters = static_cast<int32_t>(gridDim.x) / CLUSTER;
+    const int32_t split = SPLIT ? p.split : 1;
+    const int32_t cluster_id = static_cast<int32_t>(blockIdx.x) / (PAIR * split);
+    const int32_t n_clusters = static_cast<int32_t>(gridDim.x) / (PAIR * split);
+    const int32_t pair_id = static_cast<int32_t>(blockIdx.x) / PAIR;
+    const int32_t n_pairs = static_cast<int32_t>(gridDim.x) / PAIR;
 
-    if (warp == 0) {
-        // ===================== TMA producer (both CTAs) =====================
-        if (lane == 0) {
-            const uint64_t policy = l2_policy_evict_normal();
-            const uint32_t leader_full = mapa_shared(bar_full, 0);
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            bool ok = true;
-            for (int32_t t = cluster_id; t < p.total_tiles && ok; t += n_clusters) {
-                const Tile ti = tile_at(p, t);
-                const Problem& pr = p.pr[ti.q];
-                const int32_t arow = ti.m * 2 * BM + static_cast<int32_t>(rank) * BM;
-                // gate and up side by side: both CTAs take the same 128 columns, of different weights
-                const int32_t brow = EPI == EPI_GATE_UP ? ti.n * BM : ti.n * BN + static_cast<int32_t>(rank) * BM;
-                for (int seg = 0; seg < 2 && ok; ++seg) {
-                    const CUtensorMap* am = &maps.m[pr.a_map[seg]];
-                    const CUtensorMap* bm = &maps.m[pr.b_map[seg][rank]];
-                    for (int32_t kb = 0; kb < pr.steps[seg]; ++kb) {
-                        if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = leader_full + 8 * stage;
-                        const uint32_t sa = sbase + stage * STAGE_BYTES;
-                        const uint32_t sb = sa + OP_BYTES;
-                        const int32_t k0 = kb * BK;
-                        if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, CLUSTER * STAGE_BYTES);
-                        // K-major: two boxes of 64 along K x 128 rows; M/N-major:
-                        // two boxes of 64 along M/N x 128 rows of K
+    // Pipeline state of whichever role this warp has.
+    uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    const uint64_t policy = l2_policy_evict_normal();
+    const uint32_t leader_full = mapa_shared(bar_full, 2 * pair);
+    const uint32_t leader_tempty = mapa_shared(bar_tempty, 2 * pair);
+
+    // TMA producer (warp 0, one lane, both CTAs): stages [s0, s1) of a tile.
+    auto produce = [&](const Tile& ti, int32_t s0, int32_t s1) {
+        const Problem& pr = p.pr[ti.q];
+        const int32_t arow = ti.m * 2 * BM + static_cast<int32_t>(rank) * BM;
+        // gate and up side by side: both CTAs take the same 128 columns, of different weights
+        const int32_t brow = EPI == EPI_GATE_UP ? ti.n * BM : ti.n * BN + static_cast<int32_t>(rank) * BM;
+        const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
+        const int32_t steps0 = pr.steps[0];
+#pragma unroll 1
+        for (int seg = 0; seg < 2; ++seg) {
+            const CUtensorMap* am = &maps.m[pr.a_map[seg]];
+            const CUtensorMap* bm = &maps.m[pr.b_map[seg][rank]];
+            int32_t k0 = ((seg == 0 ? s0 : (s0 > steps0 ? s0 : steps0)) - (seg == 0 ? 0 : steps0)) * BK;
+            const int32_t k1 = (seg == 0 ? (s1 < steps0 ? s1 : steps0) : s1 - steps0) * BK;
+            for (; k0 < k1; k0 += BK) {
+                if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                    ok = false;
+                    return;
+                }
+                const uint32_t fb = leader_full + 8 * stage;
+                const uint32_t sa = sbase + stage * STAGE_BYTES;
+                const uint32_t sb = sa + OP_BYTES;
+                if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, PAIR * STAGE_BYTES);
+                // K-major: two boxes of 64 along K x 128 rows; M/N-major: two
+                // boxes of 64 along M/N x 128 rows of K
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (pr.a_mn) tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, arow + b * 64, k0, policy);
-                            else tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, k0 + b * 64, arow, policy);
-                            if (pr.b_mn) tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, brow + b * 64, k0, policy);
-                            else tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, k0 + b * 64, brow, policy);
-                        }
-                        ++issued;
-                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    }
+                for (int b = 0; b < 2; ++b) {
+                    if (a_mn) tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, arow + b * 64, k0, policy);
+                    else tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, k0 + b * 64, arow, policy);
+                    if (b_mn) tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, brow + b * 64, k0, policy);
+                    else tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, k0 + b * 64, brow, policy);
                 }
-            }
-            if (!ok) {
-                // Let the copies already in flight land before the CTA exits.
-                volatile int never = 0;
-                if (leader) {
-                    const int64_t n = issued < STAGES ? issued : STAGES;
-                    for (int64_t i = 0; i < n; ++i) {
-                        const int64_t idx = issued - 1 - i;
-                        mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % STAGES),
-                                          static_cast<uint32_t>((idx / STAGES) & 1), &never, DRAIN_LIMIT_NS);
-                    }
-                } else {
-                    // the odd CTA's copies report to the even CTA's barriers
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 1000000ull) { }
-                }
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ===================== MMA issuer (even CTA only) =====================
-        if (lane == 0 && leader) {
-            uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
-            bool ok = true;
-            for (int32_t t = cluster_id; t < p.total_tiles && ok; t += n_clusters) {
-                if (!mbar_wait_bounded(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const Problem& pr = p.pr[tile_at(p, t).q];
-                const uint32_t d_tmem = tmem_base + acc * BN;
-                const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
-                const uint32_t idesc = idesc_16bit_f32acc(2 * BM, BN, BF16, a_mn, b_mn);
-                const int32_t steps = pr.steps[0] + pr.steps[1];
-                for (int32_t kb = 0; kb < steps; ++kb) {
-                    if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t sa = sbase + stage * STAGE_BYTES;
-                    const uint32_t sb = sa + OP_BYTES;
-                    const uint64_t da = a_mn ? smem_desc_mn_sw128(sa, BOX_BYTES) : smem_desc_k_sw128(sa);
-                    const uint64_t db = b_mn ? smem_desc_mn_sw128(sb, BOX_BYTES) : smem_desc_k_sw128(sb);
-#pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        // a K = 16 slice further, in 16-byte units: M/N-major 16 rows of
-                        // 128 bytes; K-major 32 bytes inside a box of four slices
-                        constexpr int MN_STEP = 2048 >> 4;
-                        const int k_off = (kk / 4) * (BOX_BYTES >> 4) + (kk % 4) * (32 >> 4);
-                        tc_mma_f16_pair(d_tmem, da + (a_mn ? kk * MN_STEP : k_off), db + (b_mn ? kk * MN_STEP : k_off),
-                                        idesc, (kb | kk) != 0 ? 1u : 0u);
-                    }
-                    tc_commit_pair_mc(bar_empty + 8 * stage, CLUSTER_MASK);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                }
-                if (!ok) break;
-                tc_commit_pair_mc(bar_tfull + 8 * acc, CLUSTER_MASK);
-                acc ^= 1u;
-                if (acc == 0) aphase ^= 1u;
+    };
+
+    // MMA issuer (warp 1, one lane, even CTA): the same stages into an accumulator.
+    auto multiply = [&](const Tile& ti, int32_t s0, int32_t s1) {
+        if (!mbar_wait_bounded(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+            ok = false;
+            return;
+        }
+        tc_fence_after_sync();
+        const Problem& pr = p.pr[ti.q];
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
+        const uint32_t idesc = idesc_16bit_f32acc(2 * BM, BN, BF16, a_mn, b_mn);
+        for (int32_t st = s0; st < s1; ++st) {
+            if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
+                ok = false;
+                return;
             }
+            tc_fence_after_sync();
+            const uint32_t sa = sbase + stage * STAGE_BYTES;
+            const uint32_t sb = sa + OP_BYTES;
+            const uint64_t da = a_mn ? smem_desc_mn_sw128(sa, BOX_BYTES) : smem_desc_k_sw128(sa);
+            const uint64_t db = b_mn ? smem_desc_mn_sw128(sb, BOX_BYTES) : smem_desc_k_sw128(sb);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+                // a K = 16 slice further, in 16-byte units: M/N-major 16 rows of
+                // 128 bytes; K-major 32 bytes inside a box of four slices
+                constexpr int MN_STEP = 2048 >> 4;
+                const int k_off = (kk / 4) * (BOX_BYTES >> 4) + (kk % 4) * (32 >> 4);
+                tc_mma_f16_pair(d_tmem, da + (a_mn ? kk * MN_STEP : k_off), db + (b_mn ? kk * MN_STEP : k_off), idesc,
+                                (st != s0 || kk != 0) ? 1u : 0u);
+            }
+            tc_commit_pair_mc(bar_empty + 8 * stage, pair_mask);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        tc_commit_pair_mc(bar_tfull + 8 * acc, pair_mask);
+        acc ^= 1u;
+        if (acc == 0) aphase ^= 1u;
+    };
+
+    // Epilogue (warps 2-9, both CTAs): thread = row, 64 output columns a pass; of
+    // the two warps with the same rows one takes the even passes, one the odd.
+    const int quarter = warp & 3;                                // TMEM lanes 32*quarter .. +31
+    const int odd = warp >= 6 ? 1 : 0;
+    constexpr int PASSES = EPI == EPI_GATE_UP ? 2 : 4;
+    const int row = quarter * 32 + lane;                         // of this CTA's 128
+    struct Rows {
+        int64_t at;            // first element of the warp's rows in C
+        int32_t rows;          // of the warp's 32 that exist
+    };
+    auto rows_of = [&](const Tile& ti) {
+        const Problem& pr = p.pr[ti.q];
+        const int64_t row0 = static_cast<int64_t>(ti.m) * (2 * BM) + static_cast<int64_t>(rank) * BM + quarter * 32;
+        const int64_t left = pr.m - row0;
+        return Rows{row0 * pr.n + ti.n * p.tile_cols, left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left))};
+    };
+    // A shared tile: pass c belongs to pair c * split / PASSES.  The others'
+    // partial sums wait in that pair's ring, a slot per pair.
+    const uint32_t slot_bytes = static_cast<uint32_t>(BM * BN * 4) / static_cast<uint32_t>(split);
+    auto finish = [&](const Tile& ti, bool shared) {
+        const Problem& pr = p.pr[ti.q];
+        const Rows r = rows_of(ti);
+        const int32_t rows = r.rows;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
+        const int c0 = SPLIT && shared ? static_cast<int>(pair) * PASSES / split : 0;
+        const int c1 = SPLIT && shared ? (static_cast<int>(pair) + 1) * PASSES / split : PASSES;
+#pragma unroll 1
+        for (int c = c0 + odd; c < c1 && rows > 0; c += 2) {
+            const int32_t cols = pr.n - ti.n * p.tile_cols - c * 64;             // columns left
+            if (cols <= 0) break;
+            const int64_t at = r.at + c * 64;
+            // this pass's first quad of the partial sums
+            const uint8_t* part = smem + (c - c0) * ((EPI == EPI_GATE_UP ? 32 : 16) * BM * 16) + row * 16;
+            if (EPI == EPI_STORE) {
+                uint4 el[8];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, v);
+                    tmem_ld_wait();
+                    if (SPLIT && shared) add_partials(v, part + hh * 8 * BM * 16, split - 1, slot_bytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = pack_16bit2<BF16>(__uint_as_float(v[8 * k + 2 * j]),
+                                                     __uint_as_float(v[8 * k + 2 * j + 1]));
+                        el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                store_rows_64(el, pr.dst + at, pr.n, lane, rows, cols);
+            } else if (EPI == EPI_GATE_UP) {
+                // 32 columns of one projection (0 gate, 1 up)
+                auto load32 = [&](uint32_t (&v)[32], int which, int hh) {
+                    tmem_ld_32x32b_x32(taddr + which * 128 + c * 64 + hh * 32, v);
+                    tmem_ld_wait();
+                    if (SPLIT && shared)
+                        add_partials(v, part + (which * 16 + hh * 8) * BM * 16, split - 1, slot_bytes);
+                };
+                uint4 el[8];
+                auto round32 = [&](const uint32_t (&v)[32], int hh) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = pack_16bit2<BF16>(__uint_as_float(v[8 * k + 2 * j]),
+                                                     __uint_as_float(v[8 * k + 2 * j + 1]));
+                        el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                };
+                if (p.dst_gate != nullptr) {
+#pragma unroll 1
+                    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t v[32];
+                            load32(v, which, hh);
+                            round32(v, hh);
+                        }
+                        store_rows_64(el, (which ? p.dst_up : p.dst_gate) + at, pr.n, lane, rows, cols);
+                    }
+                }
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t g[32], u[32];
+                    load32(g, 0, hh);
+                    load32(u, 1, hh);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x = __uint_as_float(g[j]);
+                        g[j] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u[j]));
+                    }
+                    round32(g, hh);
+                }
+                store_rows_64(el, pr.dst + at, pr.n, lane, rows, cols);
+            } else {
+                // eg and eu hold G and U, then d_G and d_U
+                uint4 eg[8], eu[8];
+                load_rows_64(eg, p.gate_in + at, pr.n, lane, rows, cols);
+                load_rows_64(eu, p.up_in + at, pr.n, lane, rows, cols);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, d);
+                    tmem_ld_wait();
+                    if (SPLIT && shared) add_partials(d, part + hh * 8 * BM * 16, split - 1, slot_bytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t* pg = reinterpret_cast<uint32_t*>(&eg[4 * hh + k]);
+                        uint32_t* pu = reinterpret_cast<uint32_t*>(&eu[4 * hh + k]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 g = unpack_16bit2<BF16>(pg[j]);
+                            const float2 u = unpack_16bit2<BF16>(pu[j]);
+                            const float d0 = __uint_as_float(d[8 * k + 2 * j]);
+                            const float d1 = __uint_as_float(d[8 * k + 2 * j + 1]);
+                            const float s0 = __fdividef(1.0f, 1.0f + __expf(-g.x));
+                            const float s1 = __fdividef(1.0f, 1.0f + __expf(-g.y));
+                            pg[j] = pack_16bit2<BF16>(d0 * u.x * s0 * (1.0f + g.x * (1.0f - s0)),
+                                                      d1 * u.y * s1 * (1.0f + g.y * (1.0f - s1)));
+                            pu[j] = pack_16bit2<BF16>(d0 * g.x * s0, d1 * g.y * s1);
+                        }
+                    }
+                }
+                store_rows_64(eg, p.dst_gate + at, pr.n, lane, rows, cols);
+                store_rows_64(eu, p.dst_up + at, pr.n, lane, rows, cols);
+            }
+        }
+        tc_fence_before_sync();
+        // the accumulator may be reused once both CTAs have read their rows
+        if (leader) mbar_arrive(bar_tempty + 8 * acc);
+        else mbar_arrive_cluster(leader_tempty + 8 * acc);
+        acc ^= 1u;
+        if (acc == 0) aphase ^= 1u;
+    };
+    // Sends this CTA's sums of the passes that other pairs finish.
+    auto push_partials = [&](const Tile& ti) {
+        const Problem& pr = p.pr[ti.q];
+        if (rows_of(ti).rows == 0) return;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
+#pragma unroll 1
+        for (int c = odd; c < PASSES; c += 2) {
+            const int owner = c * split / PASSES;
+            if (owner == static_cast<int>(pair) || pr.n - ti.n * p.tile_cols - c * 64 <= 0) continue;
+            const int slot = static_cast<int>(pair) - (static_cast<int>(pair) > owner ? 1 : 0);
+            const int first = owner * PASSES / split;
+            uint32_t dst = mapa_shared(sbase, static_cast<uint32_t>(owner) * 2 + rank) + slot * slot_bytes +
+                           (c - first) * ((EPI == EPI_GATE_UP ? 32 : 16) * BM * 16) + row * 16;
+#pragma unroll 1
+            for (int hh = 0; hh < (EPI == EPI_GATE_UP ? 4 : 2); ++hh) {
+                uint32_t v[32];
+                // gate and up: 64 columns of gate, then the same of up
+                tmem_ld_32x32b_x32(taddr + c * 64 + (hh & 1) * 32 + (hh >> 1) * 128, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    store_remote4(dst + (hh * 8 + q) * (BM * 16), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+        }
+    };
+
+    // First the tiles that the cluster's pairs share, each with its part of the K
+    // axis, then tiles of one pair each.  Nothing leaves the loop while there are
+    // shared tiles: every thread meets every barrier.
+    int32_t t = SPLIT && cluster_id < p.split_tiles ? cluster_id : p.split_tiles + pair_id;
+    while (t < p.total_tiles && (ok || t < p.split_tiles)) {
+        const bool shared = SPLIT && t < p.split_tiles;
+        const Tile ti = tile_at(p, t);
+        const int32_t steps = p.pr[ti.q].steps[0] + p.pr[ti.q].steps[1];
+        const int32_t s0 = shared ? steps * static_cast<int32_t>(pair) / split : 0;
+        const int32_t s1 = shared ? steps * (static_cast<int32_t>(pair) + 1) / split : steps;
+        if (warp == 0) {
+            if (lane == 0 && ok) produce(ti, s0, s1);
+        } else if (warp == 1) {
+            if (lane == 0 && leader && ok) multiply(ti, s0, s1);
+        } else if (ok) {
+            // one answer for the whole warp, whose TMEM loads are collective
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS));
+            tc_fence_after_sync();
+        }
+        if (shared) {
+            __syncwarp();
+            cluster_sync_all();                    // every ring of the cluster is free
+            if (warp >= 2 && ok) push_partials(ti);
+            __syncwarp();
+            cluster_sync_all();                    // the partial sums are there
+        }
+        if (warp >= 2 && ok) finish(ti, shared);
+        if (shared) {
+            // the ring's next writer is TMA
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            t += n_clusters;
+            if (t >= p.split_tiles) t = p.split_tiles + pair_id;
+        } else {
+            t += n_pairs;
+        }
+    }
+    if (warp == 0) {
+        if (lane == 0 && !ok) {
+            // Let the copies already in flight land before the CTA exits.
+            volatile int never = 0;
+            if (leader) {
+                const int64_t n = issued < STAGES ? issued : STAGES;
+                for (int64_t i = 0; i < n; ++i) {
+                    const int64_t idx = issued - 1 - i;
+                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % STAGES),
+                                      static_cast<uint32_t>((idx / STAGES) & 1), &never, DRAIN_LIMIT_NS);
+                }
+            } else {
+                // the odd CTA's copies report to the even CTA's barriers
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) { }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
             // Every MMA this thread issued has finished once this arrives.
             volatile int never = 0;
             tc_commit_pair(bar_drain);
             mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
         }
-        __syncwarp();
-    } else {
-        // ===================== epilogue (warps 2..5, both CTAs) =====================
-        const int quarter = warp & 3;                // TMEM lanes 32*quarter .. +31
-        const uint32_t leader_tempty = mapa_shared(bar_tempty, 0);
-        uint32_t acc = 0, aphase = 0;
-        for (int32_t t = cluster_id; t < p.total_tiles; t += n_clusters) {
-            const Tile ti = tile_at(p, t);
-            const Problem& pr = p.pr[ti.q];
-            const int64_t row0 = static_cast<int64_t>(ti.m) * (2 * BM) + static_cast<int64_t>(rank) * BM + quarter * 32;
-            const int64_t left = pr.m - row0;
-            const int32_t rows = left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left));
-            const int32_t col0 = ti.n * p.tile_cols;
-            const int64_t at = row0 * pr.n + col0;
-            if (!mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS)) break;
-            tc_fence_after_sync();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
-            const int passes = rows > 0 ? (EPI == EPI_GATE_UP ? 2 : 4) : 0;    // of 64 output columns
-#pragma unroll 1
-            for (int c = 0; c < passes; ++c) {
-                const int32_t cols = pr.n - col0 - c * 64;                      // columns left
-                if (cols <= 0) break;
-                if (EPI == EPI_STORE) {
-                    uint4 el[8];
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_16bit2<BF16>(__uint_as_float(v[8 * k + 2 * j]),
-                                                         __uint_as_float(v[8 * k + 2 * j + 1]));
-                            el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    store_rows_64(el, pr.dst + at + c * 64, pr.n, lane, rows, cols);
-                } else if (EPI == EPI_GATE_UP) {
-                    uint4 eh[8], eg[8], eu[8];
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t g[32], u[32];
-                        tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, g);
-                        tmem_ld_32x32b_x32(taddr + 128 + c * 64 + hh * 32, u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t w[4], wg[4], wu[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float g0 = __uint_as_float(g[8 * k + 2 * j]);
-                                const float g1 = __uint_as_float(g[8 * k + 2 * j + 1]);
-                                const float u0 = __uint_as_float(u[8 * k + 2 * j]);
-                                const float u1 = __uint_as_float(u[8 * k + 2 * j + 1]);
-                                w[j] = pack_16bit2<BF16>(__fdividef(g0, 1.0f + __expf(-g0)) * u0,
-                                                         __fdividef(g1, 1.0f + __expf(-g1)) * u1);
-                                wg[j] = pack_16bit2<BF16>(g0, g1);
-                                wu[j] = pack_16bit2<BF16>(u0, u1);
-                            }
-                            eh[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
-                            eg[4 * hh + k] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-                            eu[4 * hh + k] = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-                        }
-                    }
-                    store_rows_64(eh, pr.dst + at + c * 64, pr.n, lane, rows, cols);
-                    if (p.dst_gate != nullptr) {
-                        store_rows_64(eg, p.dst_gate + at + c * 64, pr.n, lane, rows, cols);
-                        store_rows_64(eu, p.dst_up + at + c * 64, pr.n, lane, rows, cols);
-                    }
-                } else {
-                    // eg and eu hold G and U, then d_G and d_U
-                    uint4 eg[8], eu[8];
-                    load_rows_64(eg, p.gate_in + at + c * 64, pr.n, lane, rows, cols);
-                    load_rows_64(eu, p.up_in + at + c * 64, pr.n, lane, rows, cols);
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t d[32];
-                        tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, d);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t* pg = reinterpret_cast<uint32_t*>(&eg[4 * hh + k]);
-                            uint32_t* pu = reinterpret_cast<uint32_t*>(&eu[4 * hh + k]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 g = unpack_16bit2<BF16>(pg[j]);
-                                const float2 u = unpack_16bit2<BF16>(pu[j]);
-                                const float d0 = __uint_as_float(d[8 * k + 2 * j]);
-                                const float d1 = __uint_as_float(d[8 * k + 2 * j + 1]);
-                                const float s0 = __fdividef(1.0f, 1.0f + __expf(-g.x));
-                                const float s1 = __fdividef(1.0f, 1.0f + __expf(-g.y));
-                                pg[j] = pack_16bit2<BF16>(d0 * u.x * s0 * (1.0f + g.x * (1.0f - s0)),
-                                                          d1 * u.y * s1 * (1.0f + g.y * (1.0f - s1)));
-                                pu[j] = pack_16bit2<BF16>(d0 * g.x * s0, d1 * g.y * s1);
-                            }
-                        }
-                    }
-                    store_rows_64(eg, p.dst_gate + at + c * 64, pr.n, lane, rows, cols);
-                    store_rows_64(eu, p.dst_up + at + c * 64, pr.n, lane, rows, cols);
-                }
-            }
-            tc_fence_before_sync();
-            // the accumulator may be reused once both CTAs have read their rows
-            if (leader) mbar_arrive(bar_tempty + 8 * acc);
-            else mbar_arrive_cluster(leader_tempty + 8 * acc);
-            acc ^= 1u;
-            if (acc == 0) aphase ^= 1u;
-        }
     }
+    __syncwarp();
 
     tc_fence_before_sync();
     __syncthreads();
-    // Neither CTA leaves (or frees the pair's TMEM) while the other may still
-    // write into its shared memory, arrive on its barriers or use the TMEM.
+    // No CTA leaves (or frees the pair's TMEM) while another may still write
+    // into its shared memory, arrive on its barriers or use the TMEM.
     cluster_sync_all();
     if (*abort_flag && tid == 0 && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
     if (warp == 1) {
@@ -419,66 +540,81 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
 // host side
 // ---------------------------------------------------------------------------
 
-// Clusters of two that fit on the device at once, after opting in to the
-// kernel's shared memory (once per device and kernel).
-template <int EPI, bool BF16>
-cudaError_t resident_clusters(int* n) {
+// Clusters of `split` pairs that fit on the device at once, after opting in to
+// the kernel's shared memory (asked once per device, kernel and split).
+template <int EPI, bool BF16, bool SPLIT>
+cudaError_t resident_clusters(int split, int* n) {
     static std::mutex mu;
-    static std::map<int, int> cache;
+    static std::map<std::pair<int, int>, int> cache;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find(dev);
+    auto it = cache.find({dev, split});
     if (it != cache.end()) {
         *n = it->second;
         return cudaSuccess;
     }
-    err = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    err = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, BF16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CLUSTER;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(PAIR * split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(CLUSTER * 64);
+    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * split * 64));
     cfg.blockDim = dim3(NUM_THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(n, ffn_gemm_kernel<EPI, BF16>, &cfg);
+    err = cudaOccupancyMaxActiveClusters(n, ffn_gemm_kernel<EPI, BF16, SPLIT>, &cfg);
     if (err != cudaSuccess) return err;
     if (*n <= 0) return cudaErrorNoDevice;
-    cache[dev] = *n;
+    cache[{dev, split}] = *n;
     return cudaSuccess;
 }
 
 template <int EPI, bool BF16>
-cudaError_t launch(const Maps& maps, const Plan& p, cudaStream_t stream) {
+cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
+    // The first problem's tiles are shared by 4 or 2 pairs where all of them
+    // then still run at once and every pair keeps a few stages of the K axis.
+    const int32_t tiles = p.pr[0].m_tiles * p.pr[0].n_tiles;
+    const int32_t steps = p.pr[0].steps[0] + p.pr[0].steps[1];
     int nc = 0;
-    cudaError_t err = resident_clusters<EPI, BF16>(&nc);
-    if (err != cudaSuccess) return err;
-    if (nc > p.total_tiles) nc = p.total_tiles;
+    p.split = 1;
+    for (int split = EPI == EPI_GATE_UP ? 2 : MAX_SPLIT; split >= 1; split /= 2) {
+        cudaError_t err = split > 1 ? resident_clusters<EPI, BF16, true>(split, &nc)
+                                    : resident_clusters<EPI, BF16, false>(1, &nc);
+        if (err != cudaSuccess) return err;
+        p.split = split;
+        if (tiles <= nc && steps >= MIN_STEPS * split) break;
+    }
+    p.split_tiles = p.split > 1 ? tiles : 0;
+    // clusters that have work: a shared tile each, or a tile for each of their pairs
+    const int32_t own = (p.total_tiles - p.split_tiles + p.split - 1) / p.split;
+    const int32_t want = own > p.split_tiles ? own : p.split_tiles;
+    if (nc > want) nc = want;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CLUSTER;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(PAIR * p.split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(CLUSTER * nc));
+    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * p.split * nc));
     cfg.blockDim = dim3(NUM_THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, BF16>, maps, p);
+    return p.split > 1 ? cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, BF16, true>, maps, p)
+                       : cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, BF16, false>, maps, p);
 }
 
 template <int EPI>
-cudaError_t launch(bool bf16, const Maps& maps, const Plan& p, cudaStream_t stream) {
+cudaError_t launch(bool bf16, const Maps& maps, Plan& p, cudaStream_t stream) {
     return bf16 ? launch<EPI, true>(maps, p, stream) : launch<EPI, false>(maps, p, stream);
 }
 

@@ -18,7 +18,9 @@ DTYPES = [torch.float16, torch.bfloat16]
 # tokens, hidden, intermediate: one row and tile edges in every direction, smallest widths
 SHAPES = [(1, 8, 8), (3, 16, 24), (1, 256, 384), (2, 136, 264), (7, 512, 136), (31, 264, 520), (32, 128, 128),
           (33, 1024, 256), (63, 264, 392), (64, 256, 1032), (65, 520, 136), (127, 256, 128), (128, 128, 256),
-          (129, 384, 640), (255, 520, 264), (257, 128, 1288), (300, 2048, 408), (513, 776, 512), (1025, 256, 264)]
+          (129, 384, 640), (255, 520, 264), (257, 128, 1288), (300, 2048, 408), (513, 776, 512), (1025, 256, 264),
+          # few tiles and a long K axis: tiles shared by two and four pairs
+          (260, 520, 2056), (520, 1544, 1288), (200, 4104, 136)]
 
 
 def half_step(dt):
