@@ -11,19 +11,28 @@
 // The tensor cores take e2m1 operands with an e8m0 scale per 32 values along K
 // directly (tcgen05.mma kind::mxf4): per K = 64 slice the bytes that move are
 // those of a K = 16 slice of 16-bit operands, for four times the products.
-//  * A persistent CTA per SM walks 128 x 256 tiles: the active blocks (rows of
-//    some expert) are compacted first, and tiles run slice by slice inside
-//    groups of blocks, so that concurrent CTAs share a weight slice in L2.
-//  * Per stage (K = 256): 16 KB of A and 32 KB of B codes by TMA (128-byte swizzle),
-//    and their scale tiles (512 bytes for 128 rows x 128 values) by plain bulk
-//    copies.  The MMA warp copies the scale tiles into TMEM (tcgen05.cp,
-//    in order with the MMAs that read them).
-//  * TMEM: columns 0-255 accumulate, the stages' scales sit behind them.
+//  * Persistent pairs of CTAs (one per SM) walk 2-SM tiles of M = 256 x N = 256: up to
+//    two consecutive blocks of one expert (a unit), 128 rows in each CTA, against
+//    256 columns, half of whose codes each CTA loads.  A 128 x 256 tile on one
+//    SM moves 96 bytes per cycle out of and 100 into shared memory at the MMAs'
+//    full rate, more than it has; the pair moves 64 and 68.  A lone block runs
+//    with the other CTA's rows empty: nothing is loaded for them.
+//  * The units are compacted first; tiles run slice by slice inside groups of
+//    units (about an expert's), so that concurrent pairs share a weight slice in
+//    L2.
+//  * Per stage (K = 256) and CTA: 16 KB of A and 16 KB of B codes (128-byte
+//    swizzle), and their scale tiles (512 bytes for 128 rows x 128 values: A's own,
+//    all of B's), everything by TMA onto the even CTA's barrier.  The MMA thread
+//    copies the scale tiles to TMEM, to columns of their stage, ahead of the
+//    MMAs that read them.
+//  * TMEM: columns 0-255 accumulate, the stages' scales sit behind them; two
+//    accumulators would leave no room for scales.  Instead the eight epilogue warps
+//    take a finished tile into registers (128 values a thread) and hand the
+//    accumulator back before they round and store.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <map>
 #include <mutex>
 
 #include "../../include/moe_gb300.h"
@@ -36,33 +45,44 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;
+constexpr int BM = 128;                         // rows of A (and of B) per CTA
 constexpr int BN = 256;                         // columns of B per tile
 constexpr int BOX = 128;                        // bytes of codes of a row per stage (K = 256)
-constexpr int A_BYTES = BM * BOX;
-constexpr int B_BYTES = BN * BOX;
+constexpr int OP_BYTES = BM * BOX;
 constexpr int SCALE_TILE = 512;                 // scales of 128 rows x 128 values
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SCALE_TILE + 4 * SCALE_TILE;
-constexpr int MAX_STAGES = 4;
-constexpr int NUM_THREADS = 192;
-constexpr int NUM_EPI_THREADS = 128;
+constexpr int SFA_BYTES = 2 * SCALE_TILE;
+constexpr int SFB_BYTES = 4 * SCALE_TILE;
+constexpr int STAGE_BYTES = 2 * OP_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int MAX_STAGES = 6;
+constexpr int SMALL_ROWS = 32;                  // a block with at most this many rows loads a box of 32
+constexpr int NUM_THREADS = 320;                // producer, MMA and eight epilogue warps
+constexpr int NUM_EPI_THREADS = 256;
+constexpr int PAIR = 2;
+constexpr uint16_t PAIR_MASK = 0x3;
+constexpr uint16_t TWO_BLOCKS = 0x8000;         // in the unit list
+constexpr int MAX_GROUP = 8;                    // units walked together at most (2048 rows)
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 256;                // first scale column
 constexpr int STAGE_SCALE_COLS = 2 * (4 + 8);   // per K = 128: 4 columns of A's, 8 of B's scales
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 
+static_assert(STAGE_BYTES % 1024 == 0, "stages keep the swizzle's alignment");
+static_assert(TMEM_SCALES + MAX_STAGES * STAGE_SCALE_COLS <= TMEM_COLS, "scales fit in TMEM");
+static_assert(MOE_MAX_BLOCKS <= 0x7FFF, "block indices leave the list's flag free");
+
 constexpr int OFF_BARS = 0;                     // full, empty [MAX_STAGES]; tfull, tempty, drain
 constexpr int OFF_TMEM_SLOT = OFF_BARS + (2 * MAX_STAGES + 3) * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
-constexpr int OFF_WSUM = OFF_ABORT + 4;
-constexpr int OFF_RUNS = OFF_WSUM + (NUM_THREADS / 32) * 4;
-constexpr int OFF_BLOCKS = (OFF_RUNS + 4 + 15) / 16 * 16;
+constexpr int OFF_RUNS = OFF_ABORT + 4;
+constexpr int OFF_WSUM = OFF_RUNS + 4;
+constexpr int OFF_UNITS = (OFF_WSUM + (NUM_THREADS / 32) * 4 + 15) / 16 * 16;
+
+struct Maps {
+    CUtensorMap a, a_small, b, b2, sfa, sfb, sfb2;
+};
 
 struct Params {
-    const uint8_t* a_scales;
-    const uint8_t* b_scales;
-    const uint8_t* b2_scales;
     const float* weights;
     const int32_t* sizes;
     const int32_t* offsets;
@@ -85,11 +105,12 @@ struct Params {
 // and raise MOE_DEV_BAD_TABLE.
 template <int FORM>
 __device__ __forceinline__ int32_t block_rows(const Params& p, int32_t bx, int32_t* e_out, int32_t* tok_out) {
+    *e_out = -1;
+    *tok_out = 0;
     if (FORM == MX4_MATMUL) {
         *e_out = 0;
-        *tok_out = 0;
         const int64_t left = p.rows - static_cast<int64_t>(bx) * BM;
-        return left > BM ? BM : static_cast<int32_t>(left);
+        return left > BM ? BM : (left < 0 ? 0 : static_cast<int32_t>(left));
     }
     const int32_t e = __ldg(p.gidx + bx);
     bool bad = e < 0 || e >= p.n_experts;
@@ -115,47 +136,65 @@ __device__ __forceinline__ int32_t block_rows(const Params& p, int32_t bx, int32
     return static_cast<int32_t>(rows);
 }
 
+// Whether block bx + 1 goes on where block bx (of expert e, `tok` rows in) ends.
+template <int FORM>
+__device__ __forceinline__ bool continues(const Params& p, int32_t bx, int32_t e, int32_t tok) {
+    if (bx + 1 >= p.num_blocks) return false;
+    int32_t e1, tok1;
+    return block_rows<FORM>(p, bx + 1, &e1, &tok1) > 0 && e1 == e && (FORM == MX4_MATMUL || tok1 == tok + BM);
+}
+
 struct Tile {
-    int32_t bx, n;
+    int32_t bx, n;                              // the unit's first block
+    bool two;                                   // it has a second one
 };
 
-// Groups of `group` active blocks, slice by slice inside a group.
-__device__ __forceinline__ Tile tile_at(int32_t t, const uint16_t* blocks, int32_t nact, int32_t n_tiles,
-                                        int32_t group) {
+// Groups of `group` units, slice by slice inside a group.
+template <int FORM>
+__device__ __forceinline__ Tile tile_at(int32_t t, const uint16_t* units, int32_t num_units, int32_t num_blocks,
+                                        int32_t n_tiles, int32_t group) {
     const int32_t per_group = group * n_tiles;
     const int32_t g = t / per_group;
     const int32_t l = t - g * per_group;
-    const int32_t left = nact - g * group;
+    const int32_t left = num_units - g * group;
     const int32_t gs = left < group ? left : group;
     Tile ti;
     ti.n = l / gs;
-    ti.bx = blocks[g * group + (l - ti.n * gs)];
+    const int32_t u = g * group + (l - ti.n * gs);
+    if (FORM == MX4_MATMUL) {
+        ti.bx = 2 * u;
+        ti.two = 2 * u + 1 < num_blocks;
+    } else {
+        ti.bx = units[u] & ~TWO_BLOCKS;
+        ti.two = (units[u] & TWO_BLOCKS) != 0;
+    }
     return ti;
 }
 
 template <int FORM, bool BF16>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ CUtensorMap map_b2, const Params p) {
+mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* ctl = smem + p.stages * STAGE_BYTES;
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t bar_full = smem_u32(ctl) + OFF_BARS;
+    const uint32_t bar_full = smem_u32(ctl) + OFF_BARS;          // (used in the even CTA)
     const uint32_t bar_empty = bar_full + 8 * MAX_STAGES;
     const uint32_t bar_tfull = bar_empty + 8 * MAX_STAGES;
-    const uint32_t bar_tempty = bar_tfull + 8;
+    const uint32_t bar_tempty = bar_tfull + 8;                   // (used in the even CTA)
     const uint32_t bar_drain = bar_tempty + 8;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + OFF_TMEM_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + OFF_ABORT);
     int32_t* wsum = reinterpret_cast<int32_t*>(ctl + OFF_WSUM);
     int32_t* runs = reinterpret_cast<int32_t*>(ctl + OFF_RUNS);
-    uint16_t* blocks = reinterpret_cast<uint16_t*>(ctl + OFF_BLOCKS);
+    uint16_t* units = reinterpret_cast<uint16_t*>(ctl + OFF_UNITS);
 
     const int tid = threadIdx.x;
-    const int warp = tid >> 5;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // known to be warp-uniform
     const int lane = tid & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const bool leader = rank == 0;
     const uint32_t stages = static_cast<uint32_t>(p.stages);
 
     if (tid == 0) {
@@ -164,32 +203,47 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             mbar_init(bar_empty + 8 * s, 1);
         }
         mbar_init(bar_tfull, 1);
-        mbar_init(bar_tempty, NUM_EPI_THREADS);
+        mbar_init(bar_tempty, PAIR * NUM_EPI_THREADS);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
         *runs = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(ctl) + OFF_TMEM_SLOT, TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(ctl) + OFF_TMEM_SLOT, TMEM_COLS);
+        tmem_relinquish_pair();
     }
+    tc_fence_before_sync();
     __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // The next kernel may start only now that this CTA holds its TMEM.
     pdl_wait_prior_grid();
     pdl_launch_dependents();
 
-    // ---- active blocks, in order, and the number of experts they belong to ----
-    int32_t nact = 0;
+    // ---- units, in block order, and the number of experts they belong to ----
+    int32_t num_units = 0;
     if (FORM == MX4_MATMUL) {
-        nact = p.num_blocks;
-        for (int32_t b = tid; b < nact; b += NUM_THREADS) blocks[b] = static_cast<uint16_t>(b);
+        num_units = (p.num_blocks + 1) / 2;
     } else {
         for (int32_t base = 0; base < p.num_blocks; base += NUM_THREADS) {
             const int32_t bx = base + tid;
-            int32_t flag = 0, e = 0, tok = 0;
-            if (bx < p.num_blocks) flag = block_rows<FORM>(p, bx, &e, &tok) > 0;
-            const uint32_t ballot = __ballot_sync(0xffffffffu, flag);
-            const uint32_t first = __ballot_sync(0xffffffffu, flag && tok == 0);
+            int32_t starts = 0, e = 0, tok = 0;
+            uint16_t unit = 0;
+            if (bx < p.num_blocks && block_rows<FORM>(p, bx, &e, &tok) > 0) {
+                // an expert's blocks pair up from its first; a block is a unit's
+                // second if it is an odd one and the block before it leads up to it
+                starts = 1;
+                if ((tok / BM) & 1) {
+                    int32_t e0, tok0;
+                    if (bx > 0 && block_rows<FORM>(p, bx - 1, &e0, &tok0) > 0 && e0 == e && tok0 == tok - BM) starts = 0;
+                } else if (continues<FORM>(p, bx, e, tok)) {
+                    unit = TWO_BLOCKS;
+                }
+                unit |= static_cast<uint16_t>(bx);
+            }
+            const uint32_t ballot = __ballot_sync(0xffffffffu, starts);
+            const uint32_t first = __ballot_sync(0xffffffffu, starts && tok == 0);
             if (lane == 0) {
                 wsum[warp] = __popc(ballot);
                 if (first) atomicAdd(runs, __popc(first));
@@ -202,59 +256,63 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 before += (w < warp) ? c : 0;
                 total += c;
             }
-            if (flag) blocks[nact + before + __popc(ballot & ((1u << lane) - 1u))] = static_cast<uint16_t>(bx);
-            nact += total;
+            if (starts) units[num_units + before + __popc(ballot & ((1u << lane) - 1u))] = unit;
+            num_units += total;
             __syncthreads();
         }
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem_base = *tmem_slot;
-    // blocks walked together: about an expert's, at most 16 (2048 rows)
-    int32_t group = FORM == MX4_MATMUL ? 16 : (*runs > 0 ? (nact + *runs - 1) / *runs : 1);
-    group = group > 16 ? 16 : group;
-    const int32_t total_tiles = nact * p.n_tiles;
+    int32_t group = FORM == MX4_MATMUL ? MAX_GROUP : (*runs > 0 ? (num_units + *runs - 1) / *runs : 1);
+    group = group > MAX_GROUP ? MAX_GROUP : group;
+    const int32_t total_tiles = num_units * p.n_tiles;
     const int32_t k_steps = (p.k_tiles + 1) / 2;
+    const int32_t pair_id = static_cast<int32_t>(blockIdx.x) / PAIR;
+    const int32_t n_pairs = static_cast<int32_t>(gridDim.x) / PAIR;
+    cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
     if (warp == 0) {
-        // ===================== producer =====================
+        // ===================== producer (both CTAs) =====================
         if (lane == 0) {
             const uint64_t policy = l2_policy_evict_normal();
+            const uint32_t leader_full = mapa_shared(bar_full, 0);
             uint32_t stage = 0, phase = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
-                const Tile ti = tile_at(t, blocks, nact, p.n_tiles, group);
-                const int32_t e = FORM == MX4_MATMUL ? 0 : __ldg(p.gidx + ti.bx);
-                // first weight row of the tile (of gate and of up: 128 rows each)
-                const int32_t brow = e * p.n + ti.n * (FORM == MX4_GATE_UP ? 128 : BN);
-                // the last slice of a matrix may be half a tile: its second scale tile is another matrix's or none
-                const bool two = FORM == MX4_GATE_UP || ti.n * BN + 128 < p.n;
-                const uint8_t* as = p.a_scales + static_cast<int64_t>(ti.bx) * p.k_tiles * SCALE_TILE;
-                const uint8_t* bs = p.b_scales + static_cast<int64_t>(brow / 128) * p.k_tiles * SCALE_TILE;
-                const uint8_t* bs2 = FORM == MX4_GATE_UP
-                                         ? p.b2_scales + static_cast<int64_t>(brow / 128) * p.k_tiles * SCALE_TILE
-                                         : bs + static_cast<int64_t>(p.k_tiles) * SCALE_TILE;
+            for (int32_t t = pair_id; t < total_tiles && ok; t += n_pairs) {
+                const Tile ti = tile_at<FORM>(t, units, num_units, p.num_blocks, p.n_tiles, group);
+                int32_t e, tok;
+                const int32_t bx = ti.bx + static_cast<int32_t>(rank);
+                const int32_t rows0 = block_rows<FORM>(p, ti.bx, &e, &tok);
+                int32_t rows1 = 0, e1, tok1;
+                if (ti.two) rows1 = block_rows<FORM>(p, ti.bx + 1, &e1, &tok1);
+                // a block's codes: 128 rows, 32 where it has no more, none where it has none
+                const uint32_t a0 = rows0 > SMALL_ROWS ? OP_BYTES : SMALL_ROWS * BOX;
+                const uint32_t a1 = rows1 > SMALL_ROWS ? OP_BYTES : (rows1 > 0 ? SMALL_ROWS * BOX : 0);
+                const int32_t rows = leader ? rows0 : rows1;
+                const uint32_t bytes = a0 + SFA_BYTES + (rows1 > 0 ? a1 + SFA_BYTES : 0) + 2 * (OP_BYTES + SFB_BYTES);
+                const CUtensorMap* am = rows > SMALL_ROWS ? &maps.a : &maps.a_small;
+                // weight rows: the same 128 of gate (even CTA) and up (odd), or this CTA's half of 256
+                const int32_t tile_row = e * p.n + ti.n * (FORM == MX4_GATE_UP ? BM : BN);
+                const CUtensorMap* bm = FORM == MX4_GATE_UP && !leader ? &maps.b2 : &maps.b;
+                const int32_t brow = tile_row + (FORM == MX4_GATE_UP ? 0 : static_cast<int32_t>(rank) * BM);
                 for (int32_t kb = 0; kb < k_steps; ++kb) {
                     if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = bar_full + 8 * stage;
+                    const uint32_t fb = leader_full + 8 * stage;
                     const uint32_t sa = sbase + stage * STAGE_BYTES;
-                    const uint32_t sb = sa + A_BYTES;
-                    const uint32_t ss = sb + B_BYTES;
-                    const uint32_t kt = p.k_tiles - 2 * kb >= 2 ? 2 : 1;       // scale tiles along K
-                    const uint32_t sbytes = kt * SCALE_TILE;
-                    mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES + sbytes * (two ? 3 : 2));
-                    tma_load_2d(sa, &map_a, fb, kb * BOX, ti.bx * BM, policy);
-                    tma_load_2d(sb, &map_b, fb, kb * BOX, brow, policy);
-                    tma_load_2d(sb + B_BYTES / 2, FORM == MX4_GATE_UP ? &map_b2 : &map_b, fb, kb * BOX,
-                                FORM == MX4_GATE_UP ? brow : brow + 128, policy);
-                    bulk_load(ss, as + kb * 2 * SCALE_TILE, sbytes, fb);
-                    bulk_load(ss + 2 * SCALE_TILE, bs + kb * 2 * SCALE_TILE, sbytes, fb);
-                    if (two) bulk_load(ss + 4 * SCALE_TILE, bs2 + kb * 2 * SCALE_TILE, sbytes, fb);
+                    const uint32_t sb = sa + OP_BYTES;
+                    const uint32_t ss = sb + OP_BYTES;
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, bytes);
+                    tma_load_2d_pair(sb, bm, fb, kb * BOX, brow, policy);
+                    if (rows > 0) {
+                        tma_load_2d_pair(sa, am, fb, kb * BOX, bx * BM, policy);
+                        tma_load_2d_pair(ss, &maps.sfa, fb, kb * 256, bx, policy);
+                    }
+                    // every CTA needs the scales of all of B's rows
+                    tma_load_2d_pair(ss + SFA_BYTES, &maps.sfb, fb, kb * 256, tile_row / BM, policy);
+                    if (FORM == MX4_GATE_UP)
+                        tma_load_2d_pair(ss + SFA_BYTES + SFB_BYTES / 2, &maps.sfb2, fb, kb * 256, tile_row / BM, policy);
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
@@ -262,120 +320,165 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             if (!ok) {
                 // Let the copies already in flight land before the CTA exits.
                 volatile int never = 0;
-                const int64_t n = issued < stages ? issued : stages;
-                for (int64_t i = 0; i < n; ++i) {
-                    const int64_t idx = issued - 1 - i;
-                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
-                                      static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
+                if (leader) {
+                    const int64_t n = issued < stages ? issued : stages;
+                    for (int64_t i = 0; i < n; ++i) {
+                        const int64_t idx = issued - 1 - i;
+                        mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
+                                          static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
+                    }
+                } else {
+                    // the odd CTA's copies report to the even CTA's barriers
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 1000000ull) { }
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ===================== MMA issuer =====================
-        if (lane == 0) {
+        // ===================== MMA issuer (even CTA only) =====================
+        if (leader) {
+            const uint32_t issue = elect_one();
+            const int32_t my_tiles = __shfl_sync(0xffffffffu, total_tiles, 0);
             uint32_t stage = 0, phase = 0, aphase = 0;
             bool ok = true;
-            for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
-                if (!mbar_wait_bounded(bar_tempty, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
+            for (int32_t t = pair_id; t < my_tiles && ok; t += n_pairs) {
+                if (!mbar_wait_warp(bar_tempty, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
                 tc_fence_after_sync();
                 for (int32_t kb = 0; kb < k_steps; ++kb) {
-                    if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
+                    if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint32_t sa = sbase + stage * STAGE_BYTES;
-                    const uint32_t sb = sa + A_BYTES;
-                    const uint32_t ss = sb + B_BYTES;
+                    // this stage's scale columns: free since the stage's last MMAs finished
                     const uint32_t tsc = tmem_base + TMEM_SCALES + stage * STAGE_SCALE_COLS;
-                    const int kt = p.k_tiles - 2 * kb >= 2 ? 2 : 1;
-                    for (int i = 0; i < kt; ++i) {
-                        tc_cp_scales(tsc + i * 12, smem_desc_scales(ss + i * SCALE_TILE));
-                        tc_cp_scales(tsc + i * 12 + 4, smem_desc_scales(ss + (2 + i) * SCALE_TILE));
-                        tc_cp_scales(tsc + i * 12 + 8, smem_desc_scales(ss + (4 + i) * SCALE_TILE));
+                    const uint64_t da = smem_desc_k_sw128(sa), db = smem_desc_k_sw128(sa + OP_BYTES);
+                    const uint64_t ds = smem_desc_scales(sa + 2 * OP_BYTES);
+                    const bool both = p.k_tiles - 2 * kb >= 2;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {                                // K = 128 each
+                        if (i == 1 && !both) break;
+                        constexpr uint32_t TILE16 = SCALE_TILE >> 4;
+                        tc_cp_scales_pair(issue, tsc + i * 12, ds + i * TILE16);
+                        tc_cp_scales_pair(issue, tsc + i * 12 + 4, ds + (SFA_BYTES >> 4) + i * TILE16);
+                        tc_cp_scales_pair(issue, tsc + i * 12 + 8, ds + (SFA_BYTES >> 4) + (2 + i) * TILE16);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)                              // K = 64 each
+                            tc_mma_mxf4_pair(issue, tmem_base, da + (2 * i + j) * 2, db + (2 * i + j) * 2,
+                                             idesc_mxf4(2 * BM, BN, j), tsc + i * 12, tsc + i * 12 + 4,
+                                             (kb | i | j) != 0 ? 1u : 0u);
                     }
-                    const uint64_t da = smem_desc_k_sw128(sa), db = smem_desc_k_sw128(sb);
-                    for (int i = 0; i < 2 * kt; ++i)                             // K = 64 each
-                        tc_mma_mxf4(tmem_base, da + i * 2, db + i * 2, idesc_mxf4(BM, BN, i & 1), tsc + (i >> 1) * 12,
-                                    tsc + (i >> 1) * 12 + 4, (kb | i) != 0 ? 1u : 0u);
-                    tc_commit(bar_empty + 8 * stage);
+                    tc_commit_pair_mc_if(issue, bar_empty + 8 * stage, PAIR_MASK);
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                tc_commit(bar_tfull);
+                tc_commit_pair_mc_if(issue, bar_tfull, PAIR_MASK);
                 aphase ^= 1u;
             }
+            // Every MMA issued here has finished once this arrives.
             volatile int never = 0;
-            tc_commit(bar_drain);
-            mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
+            if (issue) {
+                tc_commit_pair(bar_drain);
+                mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
+            }
         }
         __syncwarp();
     } else {
-        // ===================== epilogue (warps 2..5) =====================
-        const int quarter = warp & 3;
+        // ===================== epilogue (warps 2..9, both CTAs) =====================
+        const int quarter = warp & 3;                            // TMEM lanes 32*quarter .. +31
+        const int half = warp >= 6 ? 1 : 0;                      // of the tile's columns
+        const uint32_t leader_tempty = mapa_shared(bar_tempty, 0);
         uint32_t aphase = 0;
-        for (int32_t t = blockIdx.x; t < total_tiles; t += gridDim.x) {
-            const Tile ti = tile_at(t, blocks, nact, p.n_tiles, group);
-            int32_t e = 0, tok = 0;
-            const int32_t rows = block_rows<FORM>(p, ti.bx, &e, &tok) - quarter * 32;   // of this warp
-            const int64_t row0 = static_cast<int64_t>(ti.bx) * BM + quarter * 32;
-            const int32_t col0 = ti.n * (FORM == MX4_GATE_UP ? 128 : BN);
-            uint16_t* dst = p.out + row0 * p.n + col0;
+        for (int32_t t = pair_id; t < total_tiles; t += n_pairs) {
+            const Tile ti = tile_at<FORM>(t, units, num_units, p.num_blocks, p.n_tiles, group);
+            const int32_t bx = ti.bx + static_cast<int32_t>(rank);
+            int32_t e = 0, tok = 0, rows = 0;
+            if (leader || ti.two) rows = block_rows<FORM>(p, bx, &e, &tok) - quarter * 32;   // of this warp
+            const int64_t row0 = static_cast<int64_t>(bx) * BM + quarter * 32;
+            // 64 output columns of gate and up, or 128 plain ones
+            const int32_t col0 = FORM == MX4_GATE_UP ? ti.n * BM + half * 64 : ti.n * BN + half * 128;
             float w = 1.0f;
             if (FORM == MX4_DOWN && lane < rows) w = __ldg(p.weights + (__ldg(p.offsets + e) + tok + quarter * 32 + lane));
-            if (!mbar_wait_bounded(bar_tfull, aphase, abort_flag, WAIT_LIMIT_NS)) break;
+            // one answer for the whole warp, whose TMEM loads are collective
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull, aphase, abort_flag, WAIT_LIMIT_NS))) break;
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-            const int passes = rows > 0 ? (FORM == MX4_GATE_UP ? 2 : 4) : 0;
-#pragma unroll 1
-            for (int c = 0; c < passes; ++c) {
-                const int32_t cols = p.n - col0 - c * 64;
-                if (cols <= 0) break;
+            const bool any = rows > 0 && col0 < p.n;
+            uint16_t* dst = p.out + row0 * p.n + col0;
+            auto release = [&]() {
+                tc_fence_before_sync();
+                if (leader) mbar_arrive(bar_tempty);
+                else mbar_arrive_cluster(leader_tempty);
+                aphase ^= 1u;
+            };
+            if (!any) {
+                release();
+                continue;
+            }
+            // eight columns as one 16-byte piece
+            auto piece = [](const uint32_t* x) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = pack_16bit2<BF16>(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                return make_uint4(o[0], o[1], o[2], o[3]);
+            };
+            if (FORM == MX4_GATE_UP) {
+                // the activation takes longer than the loads: hand the accumulator back first
+                uint32_t g[2][32], u[2][32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    tmem_ld_32x32b_x32(taddr + half * 64 + i * 32, g[i]);
+                    tmem_ld_32x32b_x32(taddr + 128 + half * 64 + i * 32, u[i]);
+                }
+                tmem_ld_wait();
+                release();
                 uint4 el[8];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + c * 64 + hh * 32, v);
-                    if (FORM == MX4_GATE_UP) {
-                        uint32_t u[32];
-                        tmem_ld_32x32b_x32(taddr + 128 + c * 64 + hh * 32, u);
-                        tmem_ld_wait();
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t x[8];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float g = __uint_as_float(v[j]);
-                            v[j] = __float_as_uint(__fdividef(g, 1.0f + __expf(-g)) * __uint_as_float(u[j]));
-                        }
-                    } else {
-                        tmem_ld_wait();
-                        if (FORM == MX4_DOWN) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * w);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        const float f = __uint_as_float(g[k >> 2][8 * (k & 3) + j]);
+                        x[j] = __float_as_uint(__fdividef(f, 1.0f + __expf(-f)) *
+                                               __uint_as_float(u[k >> 2][8 * (k & 3) + j]));
                     }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[j] = pack_16bit2<BF16>(__uint_as_float(v[8 * k + 2 * j]), __uint_as_float(v[8 * k + 2 * j + 1]));
-                        el[4 * hh + k] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    el[k] = piece(x);
                 }
-                store_rows_64(el, dst + c * 64, p.n, lane, rows, cols);
+                store_rows_64(el, dst, p.n, lane, rows, 64);
+            } else {
+                uint4 el[2][8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + half * 128 + i * 32, v);
+                    tmem_ld_wait();
+                    if (FORM == MX4_DOWN) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * w);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) el[i >> 1][4 * (i & 1) + k] = piece(v + 8 * k);
+                }
+                release();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) store_rows_64(el[c], dst + c * 64, p.n, lane, rows, p.n - col0 - c * 64);
             }
-            tc_fence_before_sync();
-            mbar_arrive(bar_tempty);
-            aphase ^= 1u;
         }
+        __syncwarp();
     }
 
     tc_fence_before_sync();
     __syncthreads();
+    // Neither CTA leaves (or frees the pair's TMEM) while the other may still
+    // write into its shared memory, arrive on its barriers or use the TMEM.
+    cluster_sync_all();
     if (*abort_flag && tid == 0 && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
     }
 }
 
@@ -384,58 +487,78 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 // ---------------------------------------------------------------------------
 
 template <int FORM, bool BF16>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb2, Params& p, cudaStream_t stream) {
-    int dev = 0, max_smem = 0;
+cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
+    int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (err != cudaSuccess) return err;
-    const int control = 1024 + OFF_BLOCKS + (2 * p.num_blocks + 15) / 16 * 16;
-    p.stages = (max_smem - control) / STAGE_BYTES;
-    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-    const int smem = control + p.stages * STAGE_BYTES;
-    // the attribute only ever grows to the device's limit: set it once
-    static std::once_flag once[16];
-    if (dev >= 16) return cudaErrorNoDevice;
-    std::call_once(once[dev], [&] {
-        err = cudaFuncSetAttribute(mx4_gemm_kernel<FORM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
-    });
-    if (err != cudaSuccess) return err;
-    const int64_t tiles = static_cast<int64_t>(p.num_blocks) * p.n_tiles;
-    const int sms = device_sm_count();
-    if (sms <= 0) return cudaErrorNoDevice;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    constexpr int MAX_DEVICES = 16;
+    if (dev >= MAX_DEVICES) return cudaErrorNoDevice;
+    // Once per device: the most shared memory, and the pairs that fit at once.
+    struct Limits {
+        std::once_flag once;
+        cudaError_t err;
+        int smem, pairs;
+    };
+    static Limits limits[MAX_DEVICES];
+    Limits& lim = limits[dev];
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles < sms ? tiles : sms));
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<FORM, BF16>, ma, mb, mb2, p);
+    std::call_once(lim.once, [&] {
+        lim.err = cudaDeviceGetAttribute(&lim.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (lim.err == cudaSuccess)
+            lim.err = cudaFuncSetAttribute(mx4_gemm_kernel<FORM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           lim.smem);
+        cfg.gridDim = dim3(PAIR * 64);
+        cfg.dynamicSmemBytes = static_cast<size_t>(lim.smem);
+        cfg.numAttrs = 1;
+        if (lim.err == cudaSuccess) lim.err = cudaOccupancyMaxActiveClusters(&lim.pairs, mx4_gemm_kernel<FORM, BF16>, &cfg);
+        if (lim.err == cudaSuccess && lim.pairs <= 0) lim.err = cudaErrorNoDevice;
+    });
+    if (lim.err != cudaSuccess) return lim.err;
+    const int control = 1024 + OFF_UNITS + (2 * p.num_blocks + 15) / 16 * 16;
+    p.stages = (lim.smem - control) / STAGE_BYTES;
+    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    // a unit has one block at least (two, but for the last, in a plain product)
+    const int64_t units = FORM == MX4_MATMUL ? (p.num_blocks + 1) / 2 : p.num_blocks;
+    const int64_t tiles = units * p.n_tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * (tiles < lim.pairs ? tiles : lim.pairs)));
+    cfg.dynamicSmemBytes = static_cast<size_t>(control + p.stages * STAGE_BYTES);
+    cfg.stream = stream;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<FORM, BF16>, maps, p);
 }
 
 template <int FORM>
-cudaError_t launch(bool bf16, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb2, Params& p,
-                   cudaStream_t stream) {
-    return bf16 ? launch<FORM, true>(ma, mb, mb2, p, stream) : launch<FORM, false>(ma, mb, mb2, p, stream);
+cudaError_t launch(bool bf16, const Maps& maps, Params& p, cudaStream_t stream) {
+    return bf16 ? launch<FORM, true>(maps, p, stream) : launch<FORM, false>(maps, p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4Product& a, cudaStream_t stream) {
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
-    CUtensorMap ma, mb, mb2;
-    const uint64_t kb = static_cast<uint64_t>(a.k) / 2;
+    Maps maps;
+    const bool gate_up = a.form == MX4_GATE_UP;
+    const uint64_t rows = static_cast<uint64_t>(a.rows), kb = static_cast<uint64_t>(a.k) / 2,
+                   kt = static_cast<uint64_t>(a.k) / 128;
     const uint64_t brows = static_cast<uint64_t>(a.n_experts) * static_cast<uint64_t>(a.n);
-    if (!tensor_map_2d(&ma, a.a, static_cast<uint64_t>(a.rows), kb, 1, BM) || !tensor_map_2d(&mb, a.b, brows, kb, 1, 128) ||
-        !tensor_map_2d(&mb2, a.form == MX4_GATE_UP ? a.b2 : a.b, brows, kb, 1, 128))
-        return cudaErrorInvalidValue;
+    bool made = tensor_map_2d(&maps.a, a.a, rows, kb, 1, BM) && tensor_map_2d(&maps.a_small, a.a, rows, kb, 1, SMALL_ROWS) &&
+                tensor_map_2d(&maps.b, a.b, brows, kb, 1, BM) &&
+                tensor_map_scales(&maps.sfa, a.a_scales, (rows + BM - 1) / BM, kt, 1) &&
+                tensor_map_scales(&maps.sfb, a.b_scales, brows / BM, kt, gate_up ? 1 : 2);
+    if (gate_up)
+        made = made && tensor_map_2d(&maps.b2, a.b2, brows, kb, 1, BM) &&
+               tensor_map_scales(&maps.sfb2, a.b2_scales, brows / BM, kt, 1);
+    if (!made) return cudaErrorInvalidValue;
     Params p{};
-    p.a_scales = a.a_scales;
-    p.b_scales = a.b_scales;
-    p.b2_scales = a.b2_scales;
     p.weights = a.weights;
     p.sizes = a.sizes;
     p.offsets = a.offsets;
@@ -448,12 +571,12 @@ cudaError_t launch_mx4_product(const Mx4Product& a, cudaStream_t stream) {
     p.num_blocks = static_cast<int32_t>(a.num_blocks);
     p.n_experts = a.n_experts;
     p.n = a.n;
-    p.n_tiles = a.form == MX4_GATE_UP ? a.n / 128 : (a.n + BN - 1) / BN;
+    p.n_tiles = gate_up ? a.n / BM : (a.n + BN - 1) / BN;
     p.k_tiles = a.k / 128;
     switch (a.form) {
-        case MX4_MATMUL: return launch<MX4_MATMUL>(a.bf16, ma, mb, mb2, p, stream);
-        case MX4_GATE_UP: return launch<MX4_GATE_UP>(a.bf16, ma, mb, mb2, p, stream);
-        default: return launch<MX4_DOWN>(a.bf16, ma, mb, mb2, p, stream);
+        case MX4_MATMUL: return launch<MX4_MATMUL>(a.bf16, maps, p, stream);
+        case MX4_GATE_UP: return launch<MX4_GATE_UP>(a.bf16, maps, p, stream);
+        default: return launch<MX4_DOWN>(a.bf16, maps, p, stream);
     }
 }
 

@@ -152,6 +152,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// The same for a whole warp: one answer for all lanes, which the compiler
+// knows to be warp-uniform.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, limit_ns)) != 0;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
 // ---------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), completion counted on an mbarrier
 // ---------------------------------------------------------------------------
@@ -309,6 +322,30 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint32_t bar, uint16_t cta_mas
         " [%0], %1;" ::"r"(bar), "h"(cta_mask) : "memory");
 }
 
+// The warp-uniform forms of the pair's MMA and commit: executed by a converged
+// warp, issued by the lane with `issue` set.  With the operands computed by the
+// whole warp the compiler keeps descriptors and addresses in uniform registers;
+// computed inside a one-lane branch each has to be moved there first, which
+// takes longer than a 4-bit MMA.
+__device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                   uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair_mc_if(uint32_t issue, uint32_t bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(bar), "h"(cta_mask), "r"(issue) : "memory");
+}
+
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  ::"r"(bar) : "memory");
@@ -419,18 +456,17 @@ __host__ __device__ constexpr uint32_t idesc_16bit_f32acc(uint32_t m, uint32_t n
 // 4-bit operands with a scale per 32 values along K (kind::mxf4)
 // ---------------------------------------------------------------------------
 
-// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
 // Copy 32 rows of 16 bytes (512 contiguous bytes at the descriptor's address)
 // into four TMEM columns of lanes 0-31, repeated in the other three lane
 // quarters: the layout in which the block-scaled MMA reads the scales of 128
-// rows x 4 blocks, row r in lane r % 32, column r / 32, a byte per block.
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// rows x 4 blocks, row r in lane r % 32, column r / 32, a byte per block.  Issued
+// by the even CTA of a pair; each CTA's TMEM is filled from its own shared memory.
+// Executed by a converged warp; the lane with `issue` set issues it.
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t issue, uint32_t taddr, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(issue) : "memory");
 }
 
 // Descriptor of such a 512-byte tile: no swizzle, 8-row groups of 128 bytes.
@@ -439,14 +475,18 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
            static_cast<uint64_t>(1u) << 46;
 }
 
-// D[tmem] (+)= (A ⊙ scales)·(B ⊙ scales)ᵀ for one K = 64 slice of e2m1 values.
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+// D[tmem] (+)= (A ⊙ scales)·(B ⊙ scales)ᵀ for one K = 64 slice of e2m1 values, on a
+// CTA pair (operands as in tc_mma_f16_pair).  Each CTA's TMEM holds the scales
+// of its own rows of A and of all rows of B.
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t a_scales, uint32_t b_scales,
+                                                 uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        "setp.ne.b32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate), "r"(issue)
         : "memory");
 }
 

@@ -43,4 +43,16 @@ inline bool tensor_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint6
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as a 2-D array of `tiles` rows of 512-byte tiles, `k_tiles` in a
+// row; box of two tiles x box_rows, no swizzle, zeros outside.
+inline bool tensor_map_scales(CUtensorMap* m, const void* base, uint64_t rows, uint64_t k_tiles, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {k_tiles * 128, rows};
+    const cuuint64_t strides[1] = {k_tiles * 512};
+    const cuuint32_t box[2] = {256, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
