@@ -172,7 +172,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
     const int tid = threadIdx.x;
-    const int warp = tid >> 5;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // known to be warp-uniform
     const int lane = tid & 31;
     const uint32_t cluster_rank = cluster_cta_rank();
     const uint32_t pair = SPLIT ? cluster_rank >> 1 : 0;         // of the cluster
@@ -204,7 +204,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     // The next kernel may start only now that this CTA holds its TMEM.
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
     const int32_t split = SPLIT ? p.split : 1;
@@ -259,9 +259,10 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         }
     };
 
-    // MMA issuer (warp 1, one lane, even CTA): the same stages into an accumulator.
+    // MMA issuer (warp 1 of the even CTA): the same stages into an accumulator.
+    const uint32_t issue = elect_one();
     auto multiply = [&](const Tile& ti, int32_t s0, int32_t s1) {
-        if (!mbar_wait_bounded(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+        if (!mbar_wait_warp(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
             ok = false;
             return;
         }
@@ -271,7 +272,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
         const uint32_t idesc = idesc_16bit_f32acc(2 * BM, BN, BF16, a_mn, b_mn);
         for (int32_t st = s0; st < s1; ++st) {
-            if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
+            if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                 ok = false;
                 return;
             }
@@ -286,13 +287,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                 // 128 bytes; K-major 32 bytes inside a box of four slices
                 constexpr int MN_STEP = 2048 >> 4;
                 const int k_off = (kk / 4) * (BOX_BYTES >> 4) + (kk % 4) * (32 >> 4);
-                tc_mma_f16_pair(d_tmem, da + (a_mn ? kk * MN_STEP : k_off), db + (b_mn ? kk * MN_STEP : k_off), idesc,
-                                (st != s0 || kk != 0) ? 1u : 0u);
+                tc_mma_f16_pair_if(issue, d_tmem, da + (a_mn ? kk * MN_STEP : k_off), db + (b_mn ? kk * MN_STEP : k_off),
+                                   idesc, (st != s0 || kk != 0) ? 1u : 0u);
             }
-            tc_commit_pair_mc(bar_empty + 8 * stage, pair_mask);
+            tc_commit_pair_mc_if(issue, bar_empty + 8 * stage, pair_mask);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        tc_commit_pair_mc(bar_tfull + 8 * acc, pair_mask);
+        tc_commit_pair_mc_if(issue, bar_tfull + 8 * acc, pair_mask);
         acc ^= 1u;
         if (acc == 0) aphase ^= 1u;
     };
@@ -473,7 +474,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         if (warp == 0) {
             if (lane == 0 && ok) produce(ti, s0, s1);
         } else if (warp == 1) {
-            if (lane == 0 && leader && ok) multiply(ti, s0, s1);
+            if (leader && ok) multiply(ti, s0, s1);
         } else if (ok) {
             // one answer for the whole warp, whose TMEM loads are collective
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS));
@@ -515,8 +516,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            // Every MMA this thread issued has finished once this arrives.
+        if (leader && issue) {
+            // Every MMA this warp issued has finished once this arrives.
             volatile int never = 0;
             tc_commit_pair(bar_drain);
             mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
