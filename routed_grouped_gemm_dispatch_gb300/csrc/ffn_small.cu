@@ -38,9 +38,11 @@ constexpr int BK = 64;                         // K per stage: one 128-byte swiz
 constexpr int W_BYTES = BM * BK * 2;
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_NP = static_cast<int>((FFN_SMALL_TOKENS + 15) / 16 * 16);
 constexpr int NUM_THREADS = 192;
 constexpr int NUM_EPI_THREADS = 128;
 constexpr int SMEM_LIMIT = 112 * 1024;         // two CTAs per SM
+constexpr int64_t PREFETCH_BYTES = 24ll << 20; // launches of at most so many weight bytes ask for them ahead
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 
@@ -61,6 +63,7 @@ struct Params {
     int32_t np;                // tokens rounded up to 16
     int32_t stages;
     int32_t tmem_cols;
+    int32_t prefetch;          // ask for the weights ahead of the wait
 };
 
 __device__ __forceinline__ float4 load_remote4(uint32_t cluster_addr) {
@@ -135,6 +138,15 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
                 tma_load_2d(sbase + s * stage_bytes + W_BYTES, &map_x, bar_full + 8 * s, c * BK, 0, policy);
             };
             const int32_t first = c1 - c0 < stages ? c1 - c0 : stages;
+            // Weight lines on their way into L2 while the grid before still works.
+            for (int32_t c = c0 + (GATE_UP ? 0 : first); p.prefetch && c < c1; ++c) {
+                if (GATE_UP) {
+                    tma_prefetch_2d(&map_w, c * BK, tile * (BM / 2));
+                    tma_prefetch_2d(&map_w2, c * BK, tile * (BM / 2));
+                } else {
+                    tma_prefetch_2d(&map_w, c * BK, tile * BM);
+                }
+            }
             if (GATE_UP) pdl_wait_prior_grid();
             // Behind the gate and up launch of the same call the weights may be
             // read at once: that launch lets this one start only after its own
@@ -222,15 +234,21 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
              i += static_cast<int32_t>(nranks) * NUM_EPI_THREADS) {
             const int32_t t = i / QUADS, q = i - t * QUADS;
             const uint32_t at = mine + static_cast<uint32_t>((t * BM + q * 4) * 4);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            for (uint32_t r = 0; r < nranks; ++r) {
+            // all ranks' loads in flight together, then added in rank order
+            float4 v[MAX_CLUSTER], u[GATE_UP ? MAX_CLUSTER : 1];
+#pragma unroll
+            for (uint32_t r = 0; r < MAX_CLUSTER; ++r) {
+                if (r >= nranks) break;
                 const uint32_t src = mapa_shared(at, r);
-                const float4 v = load_remote4(src);
-                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-                if (GATE_UP) {
-                    const float4 u = load_remote4(src + BM / 2 * 4);
-                    b.x += u.x; b.y += u.y; b.z += u.z; b.w += u.w;
-                }
+                v[r] = load_remote4(src);
+                if (GATE_UP) u[r] = load_remote4(src + BM / 2 * 4);
+            }
+            float4 a = v[0], b = u[0];
+#pragma unroll
+            for (uint32_t r = 1; r < MAX_CLUSTER; ++r) {
+                if (r >= nranks) break;
+                a.x += v[r].x; a.y += v[r].y; a.z += v[r].z; a.w += v[r].w;
+                if (GATE_UP) { b.x += u[r].x; b.y += u[r].y; b.z += u[r].z; b.w += u[r].w; }
             }
             const int32_t col = col0 + q * 4;
             if (col >= p.n) continue;
@@ -286,6 +304,8 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
     if (s > MAX_CLUSTER) s = MAX_CLUSTER;
     if (s > p.chunks) s = p.chunks;
     if (s < 1) s = 1;
+    const int64_t weights = static_cast<int64_t>(p.n) * k * 2 * (GATE_UP ? 2 : 1);
+    p.prefetch = weights <= PREFETCH_BYTES ? 1 : 0;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(s);
@@ -296,6 +316,10 @@ cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorM
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(s * tiles));
     cfg.blockDim = dim3(NUM_THREADS);
+    // the ring, which later holds the partial sums
+    static_assert(3 * (W_BYTES + MAX_NP * BK * 2) >= MAX_NP * BM * 4 &&
+                      1024 + CTL_BYTES + 3 * (W_BYTES + MAX_NP * BK * 2) <= SMEM_LIMIT,
+                  "three stages fit and hold the partial sums of the widest tile");
     cfg.dynamicSmemBytes = static_cast<size_t>(1024 + CTL_BYTES + p.stages * stage_bytes);
     cfg.stream = stream;
     cfg.attrs = attr;

@@ -192,6 +192,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Ask for a box's lines to be brought into L2.  A hint that moves no data to the
+// SM: safe before the kernels that may still write the array have finished.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1) : "memory");
+}
+
 // Pair variants (two CTAs feeding one 2-SM MMA): the box lands in this CTA's
 // shared memory and its byte count is reported to the mbarrier at the
 // shared::cluster address `bar`, which may be the peer CTA's.
