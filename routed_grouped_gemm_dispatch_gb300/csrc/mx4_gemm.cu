@@ -64,6 +64,12 @@ constexpr int MAX_GROUP = 8;                    // units walked together at most
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 256;                // first scale column
 constexpr int STAGE_SCALE_COLS = 2 * (4 + 8);   // per K = 128: 4 columns of A's, 8 of B's scales
+// Rows per expert up to which the few-rows kernel runs (measured with 2048 / 768,
+// 128 experts: gate_up 60 -> 49 us at 64 rows, 68 -> 63 at 128 but slower at 128
+// with 4096 / 2048; down 41 -> 36 us at 32 rows, 46 -> 50 at 64).
+constexpr int64_t FEW_AVERAGE_GATE_UP = 64;
+constexpr int64_t FEW_AVERAGE = 32;
+constexpr int64_t FEW_MAX_BLOCKS = 4096;        // (its unit list stays small)
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 
@@ -79,7 +85,7 @@ constexpr int OFF_WSUM = OFF_RUNS + 4;
 constexpr int OFF_UNITS = (OFF_WSUM + (NUM_THREADS / 32) * 4 + 15) / 16 * 16;
 
 struct Maps {
-    CUtensorMap a, a_small, b, b2, sfa, sfb, sfb2;
+    CUtensorMap a, a_small, b, b2, sfa, sfb, sfb2;       // few rows: a has boxes of 64 rows
 };
 
 struct Params {
@@ -483,6 +489,277 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 }
 
 // ---------------------------------------------------------------------------
+// few rows per block
+// ---------------------------------------------------------------------------
+
+// With a handful of rows per expert the weights' bytes bound the product, and a
+// tile that spends its MMA time on 256 rows of A would not keep up with them.
+// Here the weights are the M side: a CTA takes 128 weight rows (gate_up: 128 of
+// gate and the same 128 of up, two accumulators) against the N side of at most 64
+// rows of a block, rounded up to 16.  MMA time goes with the rows that are there;
+// what is left is the stream of weights through the ring.  The results lie
+// transposed in TMEM (a lane is an output column), so a warp writes 64
+// consecutive bytes of a row at a time.
+constexpr int FEW_ROWS = 64;                    // rows of a block per unit
+constexpr uint16_t SECOND_HALF = 0x8000;        // unit flag: the block's rows from 64 on
+constexpr int FEW_THREADS = 320;                // producer, MMA and eight epilogue warps
+constexpr int FEW_MAX_STAGES = 8;
+constexpr int FEW_OFF_TMEM_SLOT = (2 * FEW_MAX_STAGES + 5) * 8;   // full, empty; tfull, tempty [2]; drain
+constexpr int FEW_OFF_ABORT = FEW_OFF_TMEM_SLOT + 4;
+constexpr int FEW_OFF_WSUM = FEW_OFF_ABORT + 4;
+constexpr int FEW_OFF_UNITS = (FEW_OFF_WSUM + (FEW_THREADS / 32) * 4 + 15) / 16 * 16;
+
+template <int FORM>
+struct Few {
+    static constexpr int ACCS = FORM == MX4_GATE_UP ? 2 : 1;
+    static constexpr int W_BYTES = ACCS * BM * BOX;
+    static constexpr int X_BYTES = FEW_ROWS * BOX;
+    static constexpr int STAGE = W_BYTES + X_BYTES + (ACCS + 1) * 2 * SCALE_TILE;
+    static constexpr int SCALE_COLS = 2 * 4 * (ACCS + 1);            // of a stage
+    static constexpr int TMEM_SCALE0 = 2 * ACCS * FEW_ROWS;          // behind two sets of accumulators
+    static_assert(STAGE % 1024 == 0, "stages keep the swizzle's alignment");
+    static_assert(TMEM_SCALE0 + FEW_MAX_STAGES * SCALE_COLS <= TMEM_COLS, "scales fit in TMEM");
+};
+
+template <int FORM, bool BF16>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
+    using F = Few<FORM>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* ctl = smem + p.stages * F::STAGE;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = smem_u32(ctl);
+    const uint32_t bar_empty = bar_full + 8 * FEW_MAX_STAGES;
+    const uint32_t bar_tfull = bar_empty + 8 * FEW_MAX_STAGES;   // [2]
+    const uint32_t bar_tempty = bar_tfull + 16;                  // [2]
+    const uint32_t bar_drain = bar_tempty + 16;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + FEW_OFF_TMEM_SLOT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + FEW_OFF_ABORT);
+    int32_t* wsum = reinterpret_cast<int32_t*>(ctl + FEW_OFF_WSUM);
+    uint16_t* units = reinterpret_cast<uint16_t*>(ctl + FEW_OFF_UNITS);
+
+    const int tid = threadIdx.x;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int lane = tid & 31;
+    const uint32_t stages = static_cast<uint32_t>(p.stages);
+    if (tid == 0) {
+        for (int s = 0; s < FEW_MAX_STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar_tfull + 8 * a, 1);
+            mbar_init(bar_tempty + 8 * a, FEW_THREADS - 64);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(ctl) + FEW_OFF_TMEM_SLOT, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // The next kernel may start only now that this CTA holds its TMEM.
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+
+    // ---- units: the active blocks, a second entry for rows 64 and up ----
+    int32_t num_units = 0;
+    for (int32_t base = 0; base < p.num_blocks; base += FEW_THREADS) {
+        const int32_t bx = base + tid;
+        int32_t e = 0, tok = 0;
+        const int32_t rows = bx < p.num_blocks ? block_rows<FORM>(p, bx, &e, &tok) : 0;
+        const int32_t mine = rows > FEW_ROWS ? 2 : (rows > 0 ? 1 : 0);
+        const uint32_t one = __ballot_sync(0xffffffffu, mine > 0), two = __ballot_sync(0xffffffffu, mine > 1);
+        if (lane == 0) wsum[warp] = __popc(one) + __popc(two);
+        __syncthreads();
+        int32_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < FEW_THREADS / 32; ++w) {
+            const int32_t c = wsum[w];
+            before += (w < warp) ? c : 0;
+            total += c;
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        const int32_t at = num_units + before + __popc(one & below) + __popc(two & below);
+        if (mine > 0) units[at] = static_cast<uint16_t>(bx);
+        if (mine > 1) units[at + 1] = static_cast<uint16_t>(bx) | SECOND_HALF;
+        num_units += total;
+        __syncthreads();
+    }
+    const int32_t total_tiles = __shfl_sync(0xffffffffu, num_units * p.n_tiles, 0);
+    const int32_t k_steps = (p.k_tiles + 1) / 2;
+
+    // A unit's weight slices follow one another, so its few rows stay in L2.
+    struct FewTile {
+        int32_t bx, n, first, rows, e, tok;      // first: of the block's rows
+    };
+    auto tile = [&](int32_t t) {
+        FewTile ti;
+        const int32_t u = t / p.n_tiles;
+        ti.n = t - u * p.n_tiles;
+        ti.bx = units[u] & ~SECOND_HALF;
+        ti.first = (units[u] & SECOND_HALF) ? FEW_ROWS : 0;
+        const int32_t rows = block_rows<FORM>(p, ti.bx, &ti.e, &ti.tok) - ti.first;
+        ti.rows = rows > FEW_ROWS ? FEW_ROWS : rows;
+        return ti;
+    };
+
+    if (warp == 0) {
+        // ===================== producer =====================
+        if (lane == 0) {
+            const uint64_t policy = l2_policy_evict_normal();
+            uint32_t stage = 0, phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+                const FewTile ti = tile(t);
+                const int32_t wrow = ti.e * p.n + ti.n * BM;
+                const bool small = ti.rows <= SMALL_ROWS;
+                const uint32_t bytes = F::W_BYTES + (small ? SMALL_ROWS : FEW_ROWS) * BOX + (F::ACCS + 1) * 2 * SCALE_TILE;
+                for (int32_t kb = 0; kb < k_steps; ++kb) {
+                    if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = bar_full + 8 * stage;
+                    const uint32_t sw = sbase + stage * F::STAGE;
+                    const uint32_t sx = sw + F::W_BYTES;
+                    const uint32_t ss = sx + F::X_BYTES;
+                    mbar_arrive_expect_tx(fb, bytes);
+                    tma_load_2d(sw, &maps.b, fb, kb * BOX, wrow, policy);
+                    tma_load_2d(ss + 2 * SCALE_TILE, &maps.sfb, fb, kb * 256, wrow / BM, policy);
+                    if (FORM == MX4_GATE_UP) {
+                        tma_load_2d(sw + BM * BOX, &maps.b2, fb, kb * BOX, wrow, policy);
+                        tma_load_2d(ss + 4 * SCALE_TILE, &maps.sfb2, fb, kb * 256, wrow / BM, policy);
+                    }
+                    tma_load_2d(sx, small ? &maps.a_small : &maps.a, fb, kb * BOX, ti.bx * BM + ti.first, policy);
+                    tma_load_2d(ss, &maps.sfa, fb, kb * 256, ti.bx, policy);
+                    ++issued;
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok) {
+                // Let the copies already in flight land before the CTA exits.
+                volatile int never = 0;
+                const int64_t n = issued < stages ? issued : stages;
+                for (int64_t i = 0; i < n; ++i) {
+                    const int64_t idx = issued - 1 - i;
+                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
+                                      static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ===================== MMA issuer =====================
+        const uint32_t issue = elect_one();
+        uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
+        bool ok = true;
+        for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+            const FewTile ti = tile(t);
+            const uint32_t n = __shfl_sync(0xffffffffu, static_cast<uint32_t>((ti.rows + 15) & ~15), 0);
+            const uint32_t first = __shfl_sync(0xffffffffu, static_cast<uint32_t>(ti.first), 0);
+            if (!mbar_wait_warp(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + acc * F::ACCS * FEW_ROWS;
+            for (int32_t kb = 0; kb < k_steps; ++kb) {
+                if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sw = sbase + stage * F::STAGE;
+                const uint64_t dw = smem_desc_k_sw128(sw), dx = smem_desc_k_sw128(sw + F::W_BYTES);
+                const uint64_t ds = smem_desc_scales(sw + F::W_BYTES + F::X_BYTES);
+                // this stage's scale columns: free since the stage's last MMAs finished
+                const uint32_t tsc = tmem_base + F::TMEM_SCALE0 + stage * F::SCALE_COLS;
+                const bool both = p.k_tiles - 2 * kb >= 2;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {                                    // K = 128 each
+                    if (i == 1 && !both) break;
+                    constexpr uint32_t TILE16 = SCALE_TILE >> 4;
+                    const uint32_t ts = tsc + i * 4 * (F::ACCS + 1);             // rows', then the weights' scales
+#pragma unroll
+                    for (int a = 0; a <= F::ACCS; ++a) tc_cp_scales(issue, ts + 4 * a, ds + (2 * a + i) * TILE16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)                                  // K = 64 each
+#pragma unroll
+                        for (int a = 0; a < F::ACCS; ++a)
+                            tc_mma_mxf4(issue, d + a * FEW_ROWS, dw + a * (BM * BOX >> 4) + (2 * i + j) * 2,
+                                        dx + (2 * i + j) * 2, idesc_mxf4(BM, n, j), ts + 4 * (a + 1), ts + first / 32,
+                                        (kb | i | j) != 0 ? 1u : 0u);
+                }
+                tc_commit_if(issue, bar_empty + 8 * stage);
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            tc_commit_if(issue, bar_tfull + 8 * acc);
+            acc ^= 1u;
+            if (acc == 0) aphase ^= 1u;
+        }
+        // Every MMA issued here has finished once this arrives.
+        volatile int never = 0;
+        if (issue) {
+            tc_commit(bar_drain);
+            mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
+        }
+        __syncwarp();
+    } else {
+        // ===================== epilogue (warps 2..9) =====================
+        // of the two warps with the same columns one takes the even groups of
+        // eight rows, one the odd
+        const int quarter = warp & 3;
+        const int odd = warp >= 6 ? 1 : 0;
+        uint32_t acc = 0, aphase = 0;
+        for (int32_t t = blockIdx.x; t < total_tiles; t += gridDim.x) {
+            const FewTile ti = tile(t);
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS))) break;
+            tc_fence_after_sync();
+            const uint32_t taddr =
+                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * F::ACCS * FEW_ROWS;
+            const int32_t col = ti.n * BM + quarter * 32 + lane;
+            uint16_t* dst = p.out + (static_cast<int64_t>(ti.bx) * BM + ti.first) * p.n + col;
+            const float* rw = FORM == MX4_DOWN ? p.weights + (__ldg(p.offsets + ti.e) + ti.tok + ti.first) : nullptr;
+#pragma unroll 1
+            for (int32_t r0 = odd * 8; r0 < ti.rows; r0 += 16) {
+                uint32_t v[8], u[8];
+                tmem_ld_32x32b_x8(taddr + r0, v);
+                if (FORM == MX4_GATE_UP) tmem_ld_32x32b_x8(taddr + FEW_ROWS + r0, u);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r0 + j >= ti.rows) break;
+                    float x = __uint_as_float(v[j]);
+                    if (FORM == MX4_GATE_UP) x = __fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u[j]);
+                    if (FORM == MX4_DOWN) x *= __ldg(rw + r0 + j);
+                    dst[static_cast<int64_t>(r0 + j) * p.n] = static_cast<uint16_t>(pack_16bit2<BF16>(x, 0.0f) & 0xffffu);
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(bar_tempty + 8 * acc);
+            acc ^= 1u;
+            if (acc == 0) aphase ^= 1u;
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (*abort_flag && tid == 0 && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
@@ -536,8 +813,49 @@ cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<FORM, BF16>, maps, p);
 }
 
+template <int FORM, bool BF16>
+cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    constexpr int MAX_DEVICES = 16;
+    if (dev >= MAX_DEVICES) return cudaErrorNoDevice;
+    struct Limits {
+        std::once_flag once;
+        cudaError_t err;
+        int smem, sms;
+    };
+    static Limits limits[MAX_DEVICES];
+    Limits& lim = limits[dev];
+    std::call_once(lim.once, [&] {
+        lim.err = cudaDeviceGetAttribute(&lim.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (lim.err == cudaSuccess) lim.err = cudaDeviceGetAttribute(&lim.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (lim.err == cudaSuccess)
+            lim.err = cudaFuncSetAttribute(mx4_few_rows_kernel<FORM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           lim.smem);
+    });
+    if (lim.err != cudaSuccess) return lim.err;
+    p.n_tiles = p.n / BM;
+    const int control = 1024 + FEW_OFF_UNITS + (4 * p.num_blocks + 15) / 16 * 16;
+    p.stages = (lim.smem - control) / Few<FORM>::STAGE;
+    if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
+    const int64_t tiles = 2 * static_cast<int64_t>(p.num_blocks) * p.n_tiles;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles < lim.sms ? tiles : lim.sms));
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(control + p.stages * Few<FORM>::STAGE);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx4_few_rows_kernel<FORM, BF16>, maps, p);
+}
+
 template <int FORM>
-cudaError_t launch(bool bf16, const Maps& maps, Params& p, cudaStream_t stream) {
+cudaError_t launch(bool bf16, bool few, const Maps& maps, Params& p, cudaStream_t stream) {
+    if (few) return bf16 ? launch_few_rows<FORM, true>(maps, p, stream) : launch_few_rows<FORM, false>(maps, p, stream);
     return bf16 ? launch<FORM, true>(maps, p, stream) : launch<FORM, false>(maps, p, stream);
 }
 
@@ -547,13 +865,20 @@ cudaError_t launch_mx4_product(const Mx4Product& a, cudaStream_t stream) {
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
     Maps maps;
     const bool gate_up = a.form == MX4_GATE_UP;
+    // Rows per expert are on the device; num_blocks_m (a block per 128 pairs and one
+    // per expert) bounds the pairs, and so the average.
+    const int64_t pair_blocks = a.form == MX4_MATMUL ? a.num_blocks : a.num_blocks - a.n_experts;
+    const int64_t average = gate_up ? FEW_AVERAGE_GATE_UP : FEW_AVERAGE;
+    const bool few = (pair_blocks <= 1 || pair_blocks * BM <= average * a.n_experts) &&
+                     a.num_blocks <= FEW_MAX_BLOCKS;
     const uint64_t rows = static_cast<uint64_t>(a.rows), kb = static_cast<uint64_t>(a.k) / 2,
                    kt = static_cast<uint64_t>(a.k) / 128;
     const uint64_t brows = static_cast<uint64_t>(a.n_experts) * static_cast<uint64_t>(a.n);
-    bool made = tensor_map_2d(&maps.a, a.a, rows, kb, 1, BM) && tensor_map_2d(&maps.a_small, a.a, rows, kb, 1, SMALL_ROWS) &&
+    bool made = tensor_map_2d(&maps.a, a.a, rows, kb, 1, few ? FEW_ROWS : BM) &&
+                tensor_map_2d(&maps.a_small, a.a, rows, kb, 1, SMALL_ROWS) &&
                 tensor_map_2d(&maps.b, a.b, brows, kb, 1, BM) &&
                 tensor_map_scales(&maps.sfa, a.a_scales, (rows + BM - 1) / BM, kt, 1) &&
-                tensor_map_scales(&maps.sfb, a.b_scales, brows / BM, kt, gate_up ? 1 : 2);
+                tensor_map_scales(&maps.sfb, a.b_scales, brows / BM, kt, few || gate_up ? 1 : 2);
     if (gate_up)
         made = made && tensor_map_2d(&maps.b2, a.b2, brows, kb, 1, BM) &&
                tensor_map_scales(&maps.sfb2, a.b2_scales, brows / BM, kt, 1);
@@ -574,9 +899,9 @@ cudaError_t launch_mx4_product(const Mx4Product& a, cudaStream_t stream) {
     p.n_tiles = gate_up ? a.n / BM : (a.n + BN - 1) / BN;
     p.k_tiles = a.k / 128;
     switch (a.form) {
-        case MX4_MATMUL: return launch<MX4_MATMUL>(a.bf16, maps, p, stream);
-        case MX4_GATE_UP: return launch<MX4_GATE_UP>(a.bf16, maps, p, stream);
-        default: return launch<MX4_DOWN>(a.bf16, maps, p, stream);
+        case MX4_MATMUL: return launch<MX4_MATMUL>(a.bf16, few, maps, p, stream);
+        case MX4_GATE_UP: return launch<MX4_GATE_UP>(a.bf16, few, maps, p, stream);
+        default: return launch<MX4_DOWN>(a.bf16, few, maps, p, stream);
     }
 }
 

@@ -476,6 +476,14 @@ __device__ __forceinline__ void tc_cp_scales_pair(uint32_t issue, uint32_t taddr
         "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(issue) : "memory");
 }
 
+// The same for one CTA.
+__device__ __forceinline__ void tc_cp_scales(uint32_t issue, uint32_t taddr, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(issue) : "memory");
+}
+
 // Descriptor of such a 512-byte tile: no swizzle, 8-row groups of 128 bytes.
 __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128u >> 4) << 32 |
@@ -494,6 +502,26 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t issue, uint32_t d_tmem
         "setp.ne.b32 e, %7, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+// The same for one CTA.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_if(uint32_t issue, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(issue)
         : "memory");
 }
 
