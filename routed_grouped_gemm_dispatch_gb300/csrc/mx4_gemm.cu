@@ -59,7 +59,6 @@ constexpr int NUM_THREADS = 320;                // producer, MMA and eight epilo
 constexpr int NUM_EPI_THREADS = 256;
 constexpr int PAIR = 2;
 constexpr uint16_t PAIR_MASK = 0x3;
-constexpr uint16_t TWO_BLOCKS = 0x8000;         // in the unit list
 constexpr int MAX_GROUP = 8;                    // units walked together at most (2048 rows)
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 256;                // first scale column
@@ -75,7 +74,7 @@ constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 
 static_assert(STAGE_BYTES % 1024 == 0, "stages keep the swizzle's alignment");
 static_assert(TMEM_SCALES + MAX_STAGES * STAGE_SCALE_COLS <= TMEM_COLS, "scales fit in TMEM");
-static_assert(MOE_MAX_BLOCKS <= 0x7FFF, "block indices leave the list's flag free");
+static_assert(MOE_MAX_BLOCKS <= 1 << 16 && MOE_MAX_EXPERTS <= 1 << 16, "indices fit the unit list");
 
 constexpr int OFF_BARS = 0;                     // full, empty [MAX_STAGES]; tfull, tempty, drain
 constexpr int OFF_TMEM_SLOT = OFF_BARS + (2 * MAX_STAGES + 3) * 8;
@@ -142,24 +141,37 @@ __device__ __forceinline__ int32_t block_rows(const Params& p, int32_t bx, int32
     return static_cast<int32_t>(rows);
 }
 
-// Whether block bx + 1 goes on where block bx (of expert e, `tok` rows in) ends.
+// Rows of block bx + 1 if it goes on where block bx (of expert e, `tok` rows in)
+// ends, else 0.
 template <int FORM>
-__device__ __forceinline__ bool continues(const Params& p, int32_t bx, int32_t e, int32_t tok) {
-    if (bx + 1 >= p.num_blocks) return false;
+__device__ __forceinline__ int32_t rows_after(const Params& p, int32_t bx, int32_t e, int32_t tok) {
+    if (bx + 1 >= p.num_blocks) return 0;
     int32_t e1, tok1;
-    return block_rows<FORM>(p, bx + 1, &e1, &tok1) > 0 && e1 == e && (FORM == MX4_MATMUL || tok1 == tok + BM);
+    const int32_t rows = block_rows<FORM>(p, bx + 1, &e1, &tok1);
+    return e1 == e && tok1 == tok + BM ? rows : 0;
+}
+
+// A unit: one or two blocks of an expert.  The list keeps what every role needs
+// to know of it, so that no tile starts with a chain of table loads.
+struct Unit {
+    int32_t bx, e;                              // first block, expert
+    int32_t rows[2];                            // of the first and of the second block (0: there is none)
+};
+
+__device__ __forceinline__ uint2 pack_unit(int32_t bx, int32_t e, int32_t rows0, int32_t rows1) {
+    return make_uint2(static_cast<uint32_t>(bx) | static_cast<uint32_t>(e) << 16,
+                      static_cast<uint32_t>(rows0) | static_cast<uint32_t>(rows1) << 16);
 }
 
 struct Tile {
-    int32_t bx, n;                              // the unit's first block
-    bool two;                                   // it has a second one
+    Unit u;
+    int32_t n;
 };
 
 // Groups of `group` units, slice by slice inside a group.
 template <int FORM>
-__device__ __forceinline__ Tile tile_at(int32_t t, const uint16_t* units, int32_t num_units, int32_t num_blocks,
-                                        int32_t n_tiles, int32_t group) {
-    const int32_t per_group = group * n_tiles;
+__device__ __forceinline__ Tile tile_at(const Params& p, int32_t t, const uint2* units, int32_t num_units, int32_t group) {
+    const int32_t per_group = group * p.n_tiles;
     const int32_t g = t / per_group;
     const int32_t l = t - g * per_group;
     const int32_t left = num_units - g * group;
@@ -168,11 +180,17 @@ __device__ __forceinline__ Tile tile_at(int32_t t, const uint16_t* units, int32_
     ti.n = l / gs;
     const int32_t u = g * group + (l - ti.n * gs);
     if (FORM == MX4_MATMUL) {
-        ti.bx = 2 * u;
-        ti.two = 2 * u + 1 < num_blocks;
+        int32_t e, tok;
+        ti.u.bx = 2 * u;
+        ti.u.e = 0;
+        ti.u.rows[0] = block_rows<FORM>(p, 2 * u, &e, &tok);
+        ti.u.rows[1] = block_rows<FORM>(p, 2 * u + 1, &e, &tok);
     } else {
-        ti.bx = units[u] & ~TWO_BLOCKS;
-        ti.two = (units[u] & TWO_BLOCKS) != 0;
+        const uint2 v = units[u];
+        ti.u.bx = static_cast<int32_t>(v.x & 0xffffu);
+        ti.u.e = static_cast<int32_t>(v.x >> 16);
+        ti.u.rows[0] = static_cast<int32_t>(v.y & 0xffffu);
+        ti.u.rows[1] = static_cast<int32_t>(v.y >> 16);
     }
     return ti;
 }
@@ -194,7 +212,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + OFF_ABORT);
     int32_t* wsum = reinterpret_cast<int32_t*>(ctl + OFF_WSUM);
     int32_t* runs = reinterpret_cast<int32_t*>(ctl + OFF_RUNS);
-    uint16_t* units = reinterpret_cast<uint16_t*>(ctl + OFF_UNITS);
+    uint2* units = reinterpret_cast<uint2*>(ctl + OFF_UNITS);
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // known to be warp-uniform
@@ -234,19 +252,18 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     } else {
         for (int32_t base = 0; base < p.num_blocks; base += NUM_THREADS) {
             const int32_t bx = base + tid;
-            int32_t starts = 0, e = 0, tok = 0;
-            uint16_t unit = 0;
-            if (bx < p.num_blocks && block_rows<FORM>(p, bx, &e, &tok) > 0) {
+            int32_t starts = 0, e = 0, tok = 0, rows1 = 0;
+            const int32_t rows0 = bx < p.num_blocks ? block_rows<FORM>(p, bx, &e, &tok) : 0;
+            if (rows0 > 0) {
                 // an expert's blocks pair up from its first; a block is a unit's
                 // second if it is an odd one and the block before it leads up to it
                 starts = 1;
                 if ((tok / BM) & 1) {
                     int32_t e0, tok0;
                     if (bx > 0 && block_rows<FORM>(p, bx - 1, &e0, &tok0) > 0 && e0 == e && tok0 == tok - BM) starts = 0;
-                } else if (continues<FORM>(p, bx, e, tok)) {
-                    unit = TWO_BLOCKS;
+                } else {
+                    rows1 = rows_after<FORM>(p, bx, e, tok);
                 }
-                unit |= static_cast<uint16_t>(bx);
             }
             const uint32_t ballot = __ballot_sync(0xffffffffu, starts);
             const uint32_t first = __ballot_sync(0xffffffffu, starts && tok == 0);
@@ -262,7 +279,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
                 before += (w < warp) ? c : 0;
                 total += c;
             }
-            if (starts) units[num_units + before + __popc(ballot & ((1u << lane) - 1u))] = unit;
+            if (starts) units[num_units + before + __popc(ballot & ((1u << lane) - 1u))] = pack_unit(bx, e, rows0, rows1);
             num_units += total;
             __syncthreads();
         }
@@ -284,12 +301,9 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             int64_t issued = 0;
             bool ok = true;
             for (int32_t t = pair_id; t < total_tiles && ok; t += n_pairs) {
-                const Tile ti = tile_at<FORM>(t, units, num_units, p.num_blocks, p.n_tiles, group);
-                int32_t e, tok;
-                const int32_t bx = ti.bx + static_cast<int32_t>(rank);
-                const int32_t rows0 = block_rows<FORM>(p, ti.bx, &e, &tok);
-                int32_t rows1 = 0, e1, tok1;
-                if (ti.two) rows1 = block_rows<FORM>(p, ti.bx + 1, &e1, &tok1);
+                const Tile ti = tile_at<FORM>(p, t, units, num_units, group);
+                const int32_t e = ti.u.e, rows0 = ti.u.rows[0], rows1 = ti.u.rows[1];
+                const int32_t bx = ti.u.bx + static_cast<int32_t>(rank);
                 // a block's codes: 128 rows, 32 where it has no more, none where it has none
                 const uint32_t a0 = rows0 > SMALL_ROWS ? OP_BYTES : SMALL_ROWS * BOX;
                 const uint32_t a1 = rows1 > SMALL_ROWS ? OP_BYTES : (rows1 > 0 ? SMALL_ROWS * BOX : 0);
@@ -398,15 +412,15 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         const uint32_t leader_tempty = mapa_shared(bar_tempty, 0);
         uint32_t aphase = 0;
         for (int32_t t = pair_id; t < total_tiles; t += n_pairs) {
-            const Tile ti = tile_at<FORM>(t, units, num_units, p.num_blocks, p.n_tiles, group);
-            const int32_t bx = ti.bx + static_cast<int32_t>(rank);
-            int32_t e = 0, tok = 0, rows = 0;
-            if (leader || ti.two) rows = block_rows<FORM>(p, bx, &e, &tok) - quarter * 32;   // of this warp
+            const Tile ti = tile_at<FORM>(p, t, units, num_units, group);
+            const int32_t bx = ti.u.bx + static_cast<int32_t>(rank);
+            const int32_t rows = (leader ? ti.u.rows[0] : ti.u.rows[1]) - quarter * 32;   // of this warp
             const int64_t row0 = static_cast<int64_t>(bx) * BM + quarter * 32;
             // 64 output columns of gate and up, or 128 plain ones
             const int32_t col0 = FORM == MX4_GATE_UP ? ti.n * BM + half * 64 : ti.n * BN + half * 128;
             float w = 1.0f;
-            if (FORM == MX4_DOWN && lane < rows) w = __ldg(p.weights + (__ldg(p.offsets + e) + tok + quarter * 32 + lane));
+            if (FORM == MX4_DOWN && lane < rows)
+                w = __ldg(p.weights + (static_cast<int64_t>(__ldg(p.offsets + ti.u.e)) + row0 - __ldg(p.padded + ti.u.e) + lane));
             // one answer for the whole warp, whose TMEM loads are collective
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull, aphase, abort_flag, WAIT_LIMIT_NS))) break;
             tc_fence_after_sync();
@@ -501,7 +515,6 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 // transposed in TMEM (a lane is an output column), so a warp writes 64
 // consecutive bytes of a row at a time.
 constexpr int FEW_ROWS = 64;                    // rows of a block per unit
-constexpr uint16_t SECOND_HALF = 0x8000;        // unit flag: the block's rows from 64 on
 constexpr int FEW_THREADS = 320;                // producer, MMA and eight epilogue warps
 constexpr int FEW_MAX_STAGES = 8;
 constexpr int FEW_OFF_TMEM_SLOT = (2 * FEW_MAX_STAGES + 5) * 8;   // full, empty; tfull, tempty [2]; drain
@@ -538,7 +551,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + FEW_OFF_TMEM_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + FEW_OFF_ABORT);
     int32_t* wsum = reinterpret_cast<int32_t*>(ctl + FEW_OFF_WSUM);
-    uint16_t* units = reinterpret_cast<uint16_t*>(ctl + FEW_OFF_UNITS);
+    uint2* units = reinterpret_cast<uint2*>(ctl + FEW_OFF_UNITS);
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -588,8 +601,8 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         const uint32_t below = (1u << lane) - 1u;
         const int32_t at = num_units + before + __popc(one & below) + __popc(two & below);
-        if (mine > 0) units[at] = static_cast<uint16_t>(bx);
-        if (mine > 1) units[at + 1] = static_cast<uint16_t>(bx) | SECOND_HALF;
+        if (mine > 0) units[at] = pack_unit(bx, e, rows > FEW_ROWS ? FEW_ROWS : rows, 0);
+        if (mine > 1) units[at + 1] = pack_unit(bx, e, rows - FEW_ROWS, 1);
         num_units += total;
         __syncthreads();
     }
@@ -598,16 +611,17 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     // A unit's weight slices follow one another, so its few rows stay in L2.
     struct FewTile {
-        int32_t bx, n, first, rows, e, tok;      // first: of the block's rows
+        int32_t bx, n, first, rows, e;           // first: of the block's rows
     };
     auto tile = [&](int32_t t) {
         FewTile ti;
         const int32_t u = t / p.n_tiles;
+        const uint2 v = units[u];
         ti.n = t - u * p.n_tiles;
-        ti.bx = units[u] & ~SECOND_HALF;
-        ti.first = (units[u] & SECOND_HALF) ? FEW_ROWS : 0;
-        const int32_t rows = block_rows<FORM>(p, ti.bx, &ti.e, &ti.tok) - ti.first;
-        ti.rows = rows > FEW_ROWS ? FEW_ROWS : rows;
+        ti.bx = static_cast<int32_t>(v.x & 0xffffu);
+        ti.e = static_cast<int32_t>(v.x >> 16);
+        ti.rows = static_cast<int32_t>(v.y & 0xffffu);
+        ti.first = static_cast<int32_t>(v.y >> 16) * FEW_ROWS;
         return ti;
     };
 
@@ -720,13 +734,15 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         uint32_t acc = 0, aphase = 0;
         for (int32_t t = blockIdx.x; t < total_tiles; t += gridDim.x) {
             const FewTile ti = tile(t);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS))) break;
-            tc_fence_after_sync();
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * F::ACCS * FEW_ROWS;
             const int32_t col = ti.n * BM + quarter * 32 + lane;
-            uint16_t* dst = p.out + (static_cast<int64_t>(ti.bx) * BM + ti.first) * p.n + col;
-            const float* rw = FORM == MX4_DOWN ? p.weights + (__ldg(p.offsets + ti.e) + ti.tok + ti.first) : nullptr;
+            const int64_t row0 = static_cast<int64_t>(ti.bx) * BM + ti.first;
+            uint16_t* dst = p.out + row0 * p.n + col;
+            const float* rw = nullptr;
+            if (FORM == MX4_DOWN) rw = p.weights + (static_cast<int64_t>(__ldg(p.offsets + ti.e)) + row0 - __ldg(p.padded + ti.e));
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS))) break;
+            tc_fence_after_sync();
 #pragma unroll 1
             for (int32_t r0 = odd * 8; r0 < ti.rows; r0 += 16) {
                 uint32_t v[8], u[8];
@@ -800,7 +816,7 @@ cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
         if (lim.err == cudaSuccess && lim.pairs <= 0) lim.err = cudaErrorNoDevice;
     });
     if (lim.err != cudaSuccess) return lim.err;
-    const int control = 1024 + OFF_UNITS + (2 * p.num_blocks + 15) / 16 * 16;
+    const int control = 1024 + OFF_UNITS + 8 * p.num_blocks;
     p.stages = (lim.smem - control) / STAGE_BYTES;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     // a unit has one block at least (two, but for the last, in a plain product)
@@ -836,7 +852,7 @@ cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
     });
     if (lim.err != cudaSuccess) return lim.err;
     p.n_tiles = p.n / BM;
-    const int control = 1024 + FEW_OFF_UNITS + (4 * p.num_blocks + 15) / 16 * 16;
+    const int control = 1024 + FEW_OFF_UNITS + 16 * p.num_blocks;
     p.stages = (lim.smem - control) / Few<FORM>::STAGE;
     if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
     const int64_t tiles = 2 * static_cast<int64_t>(p.num_blocks) * p.n_tiles;
