@@ -56,7 +56,7 @@ constexpr int STAGE_BYTES = 2 * OP_BYTES + SFA_BYTES + SFB_BYTES;
 constexpr int MAX_STAGES = 6;
 constexpr int SMALL_ROWS = 32;                  // a block with at most this many rows loads a box of 32
 constexpr int NUM_THREADS = 320;                // producer, MMA and eight epilogue warps
-constexpr int NUM_EPI_THREADS = 256;
+constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;
 constexpr uint16_t PAIR_MASK = 0x3;
 constexpr int MAX_GROUP = 8;                    // units walked together at most (2048 rows)
@@ -227,7 +227,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             mbar_init(bar_empty + 8 * s, 1);
         }
         mbar_init(bar_tfull, 1);
-        mbar_init(bar_tempty, PAIR * NUM_EPI_THREADS);
+        mbar_init(bar_tempty, PAIR * NUM_EPI_WARPS);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
         *runs = 0;
@@ -363,8 +363,6 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             uint32_t stage = 0, phase = 0, aphase = 0;
             bool ok = true;
             for (int32_t t = pair_id; t < my_tiles && ok; t += n_pairs) {
-                if (!mbar_wait_warp(bar_tempty, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
-                tc_fence_after_sync();
                 for (int32_t kb = 0; kb < k_steps; ++kb) {
                     if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                         ok = false;
@@ -376,19 +374,28 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
                     const uint32_t tsc = tmem_base + TMEM_SCALES + stage * STAGE_SCALE_COLS;
                     const uint64_t da = smem_desc_k_sw128(sa), db = smem_desc_k_sw128(sa + OP_BYTES);
                     const uint64_t ds = smem_desc_scales(sa + 2 * OP_BYTES);
-                    const bool both = p.k_tiles - 2 * kb >= 2;
+                    constexpr uint32_t TILE16 = SCALE_TILE >> 4;
+                    // (the second K = 128 of a last odd stage is zeros that TMA filled in)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {                                // K = 128 each
-                        if (i == 1 && !both) break;
-                        constexpr uint32_t TILE16 = SCALE_TILE >> 4;
                         tc_cp_scales_pair(issue, tsc + i * 12, ds + i * TILE16);
                         tc_cp_scales_pair(issue, tsc + i * 12 + 4, ds + (SFA_BYTES >> 4) + i * TILE16);
                         tc_cp_scales_pair(issue, tsc + i * 12 + 8, ds + (SFA_BYTES >> 4) + (2 + i) * TILE16);
+                    }
+                    if (kb == 0) {
+                        // the scales do not have to wait for the accumulator
+                        if (!mbar_wait_warp(bar_tempty, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                    }
+                    const bool both = p.k_tiles - 2 * kb >= 2;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)                              // K = 64 each
-                            tc_mma_mxf4_pair(issue, tmem_base, da + (2 * i + j) * 2, db + (2 * i + j) * 2,
-                                             idesc_mxf4(2 * BM, BN, j), tsc + i * 12, tsc + i * 12 + 4,
-                                             (kb | i | j) != 0 ? 1u : 0u);
+                    for (int i = 0; i < 4; ++i) {                                // K = 64 each
+                        if (i == 2 && !both) break;
+                        tc_mma_mxf4_pair(issue, tmem_base, da + i * 2, db + i * 2, idesc_mxf4(2 * BM, BN, i & 1),
+                                         tsc + (i >> 1) * 12, tsc + (i >> 1) * 12 + 4, (kb | i) != 0 ? 1u : 0u);
                     }
                     tc_commit_pair_mc_if(issue, bar_empty + 8 * stage, PAIR_MASK);
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -428,9 +435,14 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             const bool any = rows > 0 && col0 < p.n;
             uint16_t* dst = p.out + row0 * p.n + col0;
             auto release = [&]() {
+                // one arrival a warp: 512 single ones, half of them from the other
+                // SM, would take longer than the loads before them
                 tc_fence_before_sync();
-                if (leader) mbar_arrive(bar_tempty);
-                else mbar_arrive_cluster(leader_tempty);
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(bar_tempty);
+                    else mbar_arrive_cluster(leader_tempty);
+                }
                 aphase ^= 1u;
             };
             if (!any) {
@@ -564,7 +576,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar_tfull + 8 * a, 1);
-            mbar_init(bar_tempty + 8 * a, FEW_THREADS - 64);
+            mbar_init(bar_tempty + 8 * a, FEW_THREADS / 32 - 2);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -759,7 +771,8 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                 }
             }
             tc_fence_before_sync();
-            mbar_arrive(bar_tempty + 8 * acc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tempty + 8 * acc);
             acc ^= 1u;
             if (acc == 0) aphase ^= 1u;
         }
