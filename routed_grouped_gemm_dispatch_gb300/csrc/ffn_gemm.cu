@@ -62,7 +62,7 @@ constexpr int BOX_BYTES = OP_BYTES / 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int NUM_THREADS = 320;               // producer, MMA and eight epilogue warps
-constexpr int NUM_EPI_THREADS = 256;
+constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;                        // CTAs of one MMA tile
 constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
 constexpr int MIN_STEPS = 3;                   // stages each of them keeps at least
@@ -187,7 +187,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar_tfull + 8 * a, 1);
-            mbar_init(bar_tempty + 8 * a, PAIR * NUM_EPI_THREADS);
+            mbar_init(bar_tempty + 8 * a, PAIR * NUM_EPI_WARPS);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -430,8 +430,11 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         }
         tc_fence_before_sync();
         // the accumulator may be reused once both CTAs have read their rows
-        if (leader) mbar_arrive(bar_tempty + 8 * acc);
-        else mbar_arrive_cluster(leader_tempty + 8 * acc);
+        __syncwarp();
+        if (lane == 0) {
+            if (leader) mbar_arrive(bar_tempty + 8 * acc);
+            else mbar_arrive_cluster_relaxed(leader_tempty + 8 * acc);
+        }
         acc ^= 1u;
         if (acc == 0) aphase ^= 1u;
     };

@@ -441,7 +441,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
                 __syncwarp();
                 if (lane == 0) {
                     if (leader) mbar_arrive(bar_tempty);
-                    else mbar_arrive_cluster(leader_tempty);
+                    else mbar_arrive_cluster_relaxed(leader_tempty);
                 }
                 aphase ^= 1u;
             };
