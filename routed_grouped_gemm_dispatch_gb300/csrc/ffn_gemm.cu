@@ -39,9 +39,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "../../include/moe_gb300.h"
 #include "ffn_internal.h"
@@ -66,6 +64,8 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;                        // CTAs of one MMA tile
 constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
 constexpr int MIN_STEPS = 3;                   // stages each of them keeps at least
+constexpr float JOIN_STEPS = 4.0f;             // time to join a shared tile (about 2.5 us), in stages
+constexpr float JOIN_STEPS_AHEAD = 12.0f;      // the same ahead of unshared tiles, whose loads have to wait for it
 constexpr int GROUP_M = 8;                     // tile rows (of 256) that are walked together
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
@@ -103,6 +103,8 @@ struct Plan {
     int32_t total_tiles;
     int32_t split;                 // pairs per cluster
     int32_t split_tiles;           // the first so many tiles are shared by a cluster's pairs
+    int32_t n_maps;
+    int32_t early_weights;         // B of problem 0 is no result of the launch before: see the producer
     int32_t tile_cols;             // output columns of a tile: 128 (gate and up side by side) or 256
     const uint16_t* gate_in;       // EPI_GRAD: stored G, U [m, n]
     const uint16_t* up_in;
@@ -193,6 +195,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (warp == 0 && lane < p.n_maps) tma_prefetch_map(&maps.m[lane]);
     if (warp == 1) {
         tmem_alloc_pair(sbase + OFF_TMEM_SLOT, TMEM_COLS);
         tmem_relinquish_pair();
@@ -200,10 +203,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    // Everything above overlaps the kernel before; every global access is below.
-    // The next kernel may start only now that this CTA holds its TMEM.
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
+    // Everything above overlaps the kernel before; every global access is below
+    // (with early_weights the producer waits, after its first weights).  The next
+    // kernel may start only now that this CTA holds its TMEM.
+    if (!p.early_weights) {
+        pdl_wait_prior_grid();
+        pdl_launch_dependents();
+    }
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
@@ -222,6 +228,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     const uint32_t leader_tempty = mapa_shared(bar_tempty, 2 * pair);
 
     // TMA producer (warp 0, one lane, both CTAs): stages [s0, s1) of a tile.
+    bool early = p.early_weights != 0;
     auto produce = [&](const Tile& ti, int32_t s0, int32_t s1) {
         const Problem& pr = p.pr[ti.q];
         const int32_t arow = ti.m * 2 * BM + static_cast<int32_t>(rank) * BM;
@@ -229,6 +236,32 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const int32_t brow = EPI == EPI_GATE_UP ? ti.n * BM : ti.n * BN + static_cast<int32_t>(rank) * BM;
         const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
         const int32_t steps0 = pr.steps[0];
+        // K-major: two boxes of 64 along K x 128 rows; M/N-major: two boxes of 64
+        // along M/N x 128 rows of K
+        auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t fb, bool mn, int32_t row, int32_t k0) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (mn) tma_load_2d_pair(dst + b * BOX_BYTES, m, fb, row + b * 64, k0, policy);
+                else tma_load_2d_pair(dst + b * BOX_BYTES, m, fb, k0 + b * 64, row, policy);
+            }
+        };
+        // The first tile of a launch right behind the one that makes its A: the
+        // ring's first weights are on their way before that one has finished.
+        // (It lets this launch start only after its own wait for everything
+        // before it, and writes no weights.)
+        int32_t have_b = 0;
+        if (early) {
+            have_b = s1 - s0 < STAGES ? s1 - s0 : STAGES;
+            have_b = s0 + have_b <= steps0 ? have_b : (s0 < steps0 ? steps0 - s0 : 0);   // of the first K segment
+            for (int32_t i = 0; i < have_b; ++i) {
+                if (leader) mbar_arrive_expect_tx(bar_full + 8 * i, PAIR * STAGE_BYTES);
+                load(&maps.m[pr.b_map[0][rank]], sbase + i * STAGE_BYTES + OP_BYTES, leader_full + 8 * i, b_mn, brow,
+                     (s0 + i) * BK);
+            }
+            pdl_wait_prior_grid();
+            pdl_launch_dependents();
+            early = false;
+        }
 #pragma unroll 1
         for (int seg = 0; seg < 2; ++seg) {
             const CUtensorMap* am = &maps.m[pr.a_map[seg]];
@@ -242,17 +275,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                 }
                 const uint32_t fb = leader_full + 8 * stage;
                 const uint32_t sa = sbase + stage * STAGE_BYTES;
-                const uint32_t sb = sa + OP_BYTES;
-                if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, PAIR * STAGE_BYTES);
-                // K-major: two boxes of 64 along K x 128 rows; M/N-major: two
-                // boxes of 64 along M/N x 128 rows of K
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (a_mn) tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, arow + b * 64, k0, policy);
-                    else tma_load_2d_pair(sa + b * BOX_BYTES, am, fb, k0 + b * 64, arow, policy);
-                    if (b_mn) tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, brow + b * 64, k0, policy);
-                    else tma_load_2d_pair(sb + b * BOX_BYTES, bm, fb, k0 + b * 64, brow, policy);
+                if (have_b == 0) {
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, PAIR * STAGE_BYTES);
+                    load(bm, sa + OP_BYTES, fb, b_mn, brow, k0);
+                } else {
+                    --have_b;
                 }
+                load(am, sa, fb, a_mn, arow, k0);
                 ++issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
@@ -316,21 +345,40 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     };
     // A shared tile: pass c belongs to pair c * split / PASSES.  The others'
     // partial sums wait in that pair's ring, a slot per pair.
-    const uint32_t slot_bytes = static_cast<uint32_t>(BM * BN * 4) / static_cast<uint32_t>(split);
+    constexpr uint32_t PASS_BYTES = BM * BN * 4 / PASSES;
+    const uint32_t slot_bytes = PASS_BYTES * static_cast<uint32_t>((PASSES + split - 1) / split);
+    static_assert(PASS_BYTES * ((PASSES + 1) / 2) <= STAGES * STAGE_BYTES &&
+                      PASS_BYTES * ((PASSES + 2) / 3) * 2 <= STAGES * STAGE_BYTES &&
+                      PASS_BYTES * ((PASSES + 3) / 4) * 3 <= STAGES * STAGE_BYTES && MAX_SPLIT == 4,
+                  "the slots fit in the ring for 2, 3 and 4 pairs");
+    auto first_pass = [&](int owner) { return (owner * PASSES + split - 1) / split; };
+    // EPI_GRAD: G and U of a warp's first pass are asked for before the tile is
+    // finished, and turned from lines to rows when they are needed.
+    uint4 eg[EPI == EPI_GRAD ? 8 : 1], eu[EPI == EPI_GRAD ? 8 : 1];
+    auto ask_gate_up = [&](const Tile& ti, bool shared) {
+        if constexpr (EPI == EPI_GRAD) {
+            const Problem& pr = p.pr[ti.q];
+            const Rows r = rows_of(ti);
+            const int c = (SPLIT && shared ? first_pass(static_cast<int>(pair)) : 0) + odd;
+            const int32_t cols = pr.n - ti.n * p.tile_cols - c * 64;
+            load_lines_64(eg, p.gate_in + r.at + c * 64, pr.n, lane, r.rows, cols);
+            load_lines_64(eu, p.up_in + r.at + c * 64, pr.n, lane, r.rows, cols);
+        }
+    };
     auto finish = [&](const Tile& ti, bool shared) {
         const Problem& pr = p.pr[ti.q];
         const Rows r = rows_of(ti);
         const int32_t rows = r.rows;
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
-        const int c0 = SPLIT && shared ? static_cast<int>(pair) * PASSES / split : 0;
-        const int c1 = SPLIT && shared ? (static_cast<int>(pair) + 1) * PASSES / split : PASSES;
+        const int c0 = SPLIT && shared ? first_pass(static_cast<int>(pair)) : 0;
+        const int c1 = SPLIT && shared ? first_pass(static_cast<int>(pair) + 1) : PASSES;
 #pragma unroll 1
         for (int c = c0 + odd; c < c1 && rows > 0; c += 2) {
             const int32_t cols = pr.n - ti.n * p.tile_cols - c * 64;             // columns left
             if (cols <= 0) break;
             const int64_t at = r.at + c * 64;
             // this pass's first quad of the partial sums
-            const uint8_t* part = smem + (c - c0) * ((EPI == EPI_GATE_UP ? 32 : 16) * BM * 16) + row * 16;
+            const uint8_t* part = smem + (c - c0) * PASS_BYTES + row * 16;
             if (EPI == EPI_STORE) {
                 uint4 el[8];
 #pragma unroll
@@ -395,11 +443,14 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                     round32(g, hh);
                 }
                 store_rows_64(el, pr.dst + at, pr.n, lane, rows, cols);
-            } else {
+            } else if constexpr (EPI == EPI_GRAD) {
                 // eg and eu hold G and U, then d_G and d_U
-                uint4 eg[8], eu[8];
-                load_rows_64(eg, p.gate_in + at, pr.n, lane, rows, cols);
-                load_rows_64(eu, p.up_in + at, pr.n, lane, rows, cols);
+                if (c != c0 + odd) {
+                    load_lines_64(eg, p.gate_in + at, pr.n, lane, rows, cols);
+                    load_lines_64(eu, p.up_in + at, pr.n, lane, rows, cols);
+                }
+                transpose_pieces(eg, lane);
+                transpose_pieces(eu, lane);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t d[32];
@@ -448,9 +499,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             const int owner = c * split / PASSES;
             if (owner == static_cast<int>(pair) || pr.n - ti.n * p.tile_cols - c * 64 <= 0) continue;
             const int slot = static_cast<int>(pair) - (static_cast<int>(pair) > owner ? 1 : 0);
-            const int first = owner * PASSES / split;
+            const int first = first_pass(owner);
             uint32_t dst = mapa_shared(sbase, static_cast<uint32_t>(owner) * 2 + rank) + slot * slot_bytes +
-                           (c - first) * ((EPI == EPI_GATE_UP ? 32 : 16) * BM * 16) + row * 16;
+                           (c - first) * PASS_BYTES + row * 16;
 #pragma unroll 1
             for (int hh = 0; hh < (EPI == EPI_GATE_UP ? 4 : 2); ++hh) {
                 uint32_t v[32];
@@ -479,6 +530,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         } else if (warp == 1) {
             if (leader && ok) multiply(ti, s0, s1);
         } else if (ok) {
+            ask_gate_up(ti, shared);
             // one answer for the whole warp, whose TMEM loads are collective
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS));
             tc_fence_after_sync();
@@ -544,57 +596,81 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
 // host side
 // ---------------------------------------------------------------------------
 
-// Clusters of `split` pairs that fit on the device at once, after opting in to
-// the kernel's shared memory (asked once per device, kernel and split).
-template <int EPI, bool BF16, bool SPLIT>
-cudaError_t resident_clusters(int split, int* n) {
-    static std::mutex mu;
-    static std::map<std::pair<int, int>, int> cache;
+// Clusters of 1 .. MAX_SPLIT pairs that fit on the device at once, after opting
+// in to the kernels' shared memory; asked once per device.
+struct Resident {
+    std::once_flag once;
+    cudaError_t err;
+    int clusters[MAX_SPLIT + 1];
+};
+
+template <int EPI, bool BF16>
+const Resident* resident() {
+    constexpr int MAX_DEVICES = 16;
+    static Resident table[MAX_DEVICES];
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find({dev, split});
-    if (it != cache.end()) {
-        *n = it->second;
-        return cudaSuccess;
-    }
-    err = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, BF16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(PAIR * split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(PAIR * split * 64));
-    cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(n, ffn_gemm_kernel<EPI, BF16, SPLIT>, &cfg);
-    if (err != cudaSuccess) return err;
-    if (*n <= 0) return cudaErrorNoDevice;
-    cache[{dev, split}] = *n;
-    return cudaSuccess;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= MAX_DEVICES) return nullptr;
+    Resident& r = table[dev];
+    std::call_once(r.once, [&r] {
+        for (int split = 1; split <= MAX_SPLIT; ++split) {
+            const auto kernel = split > 1 ? ffn_gemm_kernel<EPI, BF16, true> : ffn_gemm_kernel<EPI, BF16, false>;
+            r.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+            if (r.err != cudaSuccess) return;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(PAIR * split);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(PAIR * split * 64));
+            cfg.blockDim = dim3(NUM_THREADS);
+            cfg.dynamicSmemBytes = SMEM_BYTES;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            r.err = cudaOccupancyMaxActiveClusters(&r.clusters[split], kernel, &cfg);
+            if (r.err == cudaSuccess && r.clusters[split] <= 0) r.err = cudaErrorNoDevice;
+            if (r.err != cudaSuccess) return;
+        }
+    });
+    return &r;
 }
 
 template <int EPI, bool BF16>
 cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
-    // The first problem's tiles are shared by 4 or 2 pairs where all of them
-    // then still run at once and every pair keeps a few stages of the K axis.
+    // How many pairs share a tile, and how many tiles are shared, goes by the time
+    // of the launch in K steps: rounds of unshared tiles, plus rounds of shared
+    // ones at steps / split each and JOIN_STEPS for joining them.  Of a launch of
+    // one problem the tiles that do not fill a round are shared (all of them
+    // where there is no full round); of several, the first problem's if they are
+    // one round at most.  Splitting also leaves SMs without a cluster: 144, 138
+    // and 120 of 152 are in one of 4, 6 and 8 CTAs.
     const int32_t tiles = p.pr[0].m_tiles * p.pr[0].n_tiles;
     const int32_t steps = p.pr[0].steps[0] + p.pr[0].steps[1];
-    int nc = 0;
+    const Resident* r = resident<EPI, BF16>();
+    if (!r) return cudaErrorNoDevice;
+    if (r->err != cudaSuccess) return r->err;
+    int nc = r->clusters[1];
     p.split = 1;
-    for (int split = EPI == EPI_GATE_UP ? 2 : MAX_SPLIT; split >= 1; split /= 2) {
-        cudaError_t err = split > 1 ? resident_clusters<EPI, BF16, true>(split, &nc)
-                                    : resident_clusters<EPI, BF16, false>(1, &nc);
-        if (err != cudaSuccess) return err;
-        p.split = split;
-        if (tiles <= nc && steps >= MIN_STEPS * split) break;
+    p.split_tiles = 0;
+    float best = static_cast<float>((tiles + nc - 1) / nc * steps);
+    for (int split = 2; split <= MAX_SPLIT; ++split) {
+        // (three pairs would leave one of them without a part of gate and up to finish)
+        if (steps < MIN_STEPS * split || (EPI == EPI_GATE_UP && split == 3)) continue;
+        const int n = r->clusters[split];
+        const int32_t full = p.n_problems == 1 ? tiles / (n * split) : 0;
+        const int32_t rest = tiles - full * n * split;
+        if (p.n_problems > 1 && rest > n) continue;
+        const float t = static_cast<float>(full * steps) +
+                        static_cast<float>((rest + n - 1) / n) *
+                            (static_cast<float>(steps) / static_cast<float>(split) +
+                             (full > 0 ? JOIN_STEPS_AHEAD : JOIN_STEPS));
+        if (rest > 0 && t < best) {
+            best = t;
+            p.split = split;
+            p.split_tiles = rest;
+            nc = n;
+        }
     }
-    p.split_tiles = p.split > 1 ? tiles : 0;
     // clusters that have work: a shared tile each, or a tile for each of their pairs
     const int32_t own = (p.total_tiles - p.split_tiles + p.split - 1) / p.split;
     const int32_t want = own > p.split_tiles ? own : p.split_tiles;
@@ -664,6 +740,7 @@ cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     Problem& gu = add_problem(p, a.up_logits, T, I, BM);
     set_operands(gu, 0, H, 0, 1, 2);
+    p.n_maps = 3;
     p.dst_gate = a.gate;
     p.dst_up = a.up;
     p.status = a.status;
@@ -674,6 +751,8 @@ cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream) {
     if (!box_map(maps, 0, a.up_logits, T, I) || !box_map(maps, 1, a.down_w, H, I)) return cudaErrorInvalidValue;
     Problem& dn = add_problem(p2, a.out, T, H, BN);
     set_operands(dn, 0, I, 0, 1, 1);
+    p2.n_maps = 2;
+    p2.early_weights = 1;
     p2.status = a.status;
     return launch<EPI_STORE>(a.bf16, maps, p2, stream);
 }
@@ -693,6 +772,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     Problem& dh = add_problem(p, nullptr, T, I, BN);
     set_operands(dh, 0, H, DY, DOWN, DOWN);
     dh.b_mn = 1;
+    p.n_maps = HG + 1;
     p.gate_in = a.gate;
     p.up_in = a.up;
     p.dst_gate = a.d_gate;
@@ -703,6 +783,8 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
 
     Plan q{};
     q.status = a.status;
+    q.n_maps = HG + 1;
+    q.early_weights = 1;
     Problem& dx = add_problem(q, a.d_x, T, H, BN);
     set_operands(dx, 0, I, DG, GATE, GATE);
     set_operands(dx, 1, I, DU, UP, UP);

@@ -3,6 +3,7 @@
 // check returns a MOE_ERR_* code and launches nothing.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/moe_gb300.h"
@@ -19,11 +20,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 moe_status_t check_device() {
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_DEVICE;
+    // A device's architecture is asked for once.
+    static std::atomic<bool> usable[64];
+    const bool kept = dev >= 0 && dev < 64;
+    if (kept && usable[dev].load(std::memory_order_relaxed)) return MOE_OK;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return MOE_ERR_DEVICE;
     // The library is compiled for sm_103a only.
     if (major != 10 || minor != 3) return MOE_ERR_DEVICE;
+    if (kept) usable[dev].store(true, std::memory_order_relaxed);
     return MOE_OK;
 }
 

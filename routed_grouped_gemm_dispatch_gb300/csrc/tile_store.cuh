@@ -70,10 +70,11 @@ __device__ __forceinline__ void store_rows_64(uint4 (&el)[8], uint16_t* dst0, in
     }
 }
 
-// The reverse for reading: thread `lane` receives row `lane`'s 64 columns.
-// Rows and columns outside the given extents read as zero.
-__device__ __forceinline__ void load_rows_64(uint4 (&el)[8], const uint16_t* src0, int64_t stride, int lane,
-                                             int32_t rows, int32_t cols) {
+// The reverse for reading: lane 8g + i receives piece i of rows 8g .. 8g + 7;
+// transpose_pieces then leaves thread `lane` with row `lane`.  Rows and columns
+// outside the given extents read as zero.
+__device__ __forceinline__ void load_lines_64(uint4 (&el)[8], const uint16_t* src0, int64_t stride, int lane,
+                                              int32_t rows, int32_t cols) {
     const int g8 = lane & ~7;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -81,7 +82,6 @@ __device__ __forceinline__ void load_rows_64(uint4 (&el)[8], const uint16_t* src
         if (g8 + r < rows && (lane & 7) * 8 < cols)
             el[r] = __ldg(reinterpret_cast<const uint4*>(src0 + static_cast<int64_t>(g8 + r) * stride + (lane & 7) * 8));
     }
-    transpose_pieces(el, lane);
 }
 
 }  // namespace moe
