@@ -388,37 +388,39 @@ def run_kernel(stacked_expert_tokens, gate_w, up_w, down_w, routed_expert_weight
                   group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, ws, out)
 
 
+_CODES = {}
+
+
 def _dtype_code(t, name, f32=False):
-    """MOE_DTYPE_* of a tensor's type."""
-    import torch
-    if t is torch.float16:
-        return MOE_DTYPE_F16
-    if t is torch.bfloat16:
-        return MOE_DTYPE_BF16
-    if f32 and t is torch.float32:
-        return MOE_DTYPE_F32
-    raise TypeError(f"{name} must be float16{', bfloat16 or float32' if f32 else ' or bfloat16'}, got {t}")
-
-
-def _ffn_weights(x, gate_w, up_w, down_w):
-    """The block's sizes, with every weight's type and shape checked against x."""
-    T, H = x.shape
-    dt = x.dtype
-    g = _dev(gate_w, "gate_w", dt, 2)
-    u = _dev(up_w, "up_w", dt, 2)
-    d = _dev(down_w, "down_w", dt, 2)
-    I = g.shape[0]
-    if g.shape[1] != H or tuple(u.shape) != (I, H) or tuple(d.shape) != (H, I):
-        raise ValueError("weight shapes do not match [intermediate, hidden] / [hidden, intermediate]")
-    return T, H, I
+    """MOE_DTYPE_* of a torch type."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32})
+    code = _CODES.get(t)
+    if code is None or (code == MOE_DTYPE_F32 and not f32):
+        raise TypeError(f"{name} must be float16{', bfloat16 or float32' if f32 else ' or bfloat16'}, got {t}")
+    return code
 
 
 def _shaped(t, name, dtype, shape):
-    """A caller's buffer of this type and shape."""
+    """A device tensor of this type and shape."""
+    # the common case in one expression; what follows names what is wrong
+    if (getattr(t, "is_cuda", False) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return t
     t = _dev(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _ffn_sizes(x, gate_w, up_w, down_w):
+    """The block's type code and sizes, with every array checked."""
+    dt = getattr(x, "dtype", None)
+    code = _dtype_code(dt, "x")
+    T, H = _dev(x, "x", dt, 2).shape
+    I = _dev(gate_w, "gate_w", dt, 2).shape[0]
+    _shaped(gate_w, "gate_w", dt, (I, H))
+    _shaped(up_w, "up_w", dt, (I, H))
+    _shaped(down_w, "down_w", dt, (H, I))
+    return code, dt, T, H, I
 
 
 def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=None, status=None, stream=None):
@@ -431,19 +433,24 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
     ``up`` [T, intermediate] too: they receive the rounded projections, which
     gated_ffn_backward reads with ``up_logits``."""
     import torch
-    code = _dtype_code(getattr(x, "dtype", None), "x")
-    dt = x.dtype
-    x = _dev(x, "x", dt, 2)
-    T, H, I = _ffn_weights(x, gate_w, up_w, down_w)
-    if (gate is None) != (up is None):
-        raise ValueError("gate and up are stored together: supply both or neither")
-    if gate is not None:
-        gate, up = _shaped(gate, "gate", dt, (T, I)), _shaped(up, "up", dt, (T, I))
-    up_logits = (torch.empty((T, I), dtype=dt, device=x.device) if up_logits is None
-                 else _shaped(up_logits, "up_logits", dt, (T, I)))
-    out = torch.empty((T, H), dtype=dt, device=x.device) if out is None else _shaped(out, "out", dt, (T, H))
-    _check(lib().moe_ffn_forward(code, _ptr(x), T, H, _ptr(gate_w), _ptr(up_w), _ptr(down_w), I, _ptr(gate), _ptr(up),
-                                 _ptr(up_logits), _ptr(out), _ptr(status), _stream(stream)), "moe_ffn_forward")
+    code, dt, T, H, I = _ffn_sizes(x, gate_w, up_w, down_w)
+    if gate is not None or up is not None:
+        if gate is None or up is None:
+            raise ValueError("gate and up are stored together: supply both or neither")
+        _shaped(gate, "gate", dt, (T, I))
+        _shaped(up, "up", dt, (T, I))
+    if up_logits is None:
+        up_logits = torch.empty((T, I), dtype=dt, device=x.device)
+    else:
+        _shaped(up_logits, "up_logits", dt, (T, I))
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _shaped(out, "out", dt, (T, H))
+    st = lib().moe_ffn_forward(code, x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(), down_w.data_ptr(), I,
+                               _ptr(gate), _ptr(up), up_logits.data_ptr(), out.data_ptr(), _ptr(status),
+                               _stream(stream))
+    _check(st, "moe_ffn_forward")
     return out
 
 
@@ -455,23 +462,20 @@ def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=
     ``workspace``: a device tensor of at least ffn_backward_workspace_bytes(T,
     intermediate) bytes."""
     import torch
-    code = _dtype_code(getattr(x, "dtype", None), "x")
-    dt = x.dtype
-    x = _dev(x, "x", dt, 2)
-    T, H, I = _ffn_weights(x, gate_w, up_w, down_w)
-    d_out = _shaped(d_out, "d_out", dt, (T, H))
-    gate, up = _shaped(gate, "gate", dt, (T, I)), _shaped(up, "up", dt, (T, I))
-    up_logits = _shaped(up_logits, "up_logits", dt, (T, I))
+    code, dt, T, H, I = _ffn_sizes(x, gate_w, up_w, down_w)
+    _shaped(d_out, "d_out", dt, (T, H))
+    for t, name in ((gate, "gate"), (up, "up"), (up_logits, "up_logits")):
+        _shaped(t, name, dt, (T, I))
     grads = []
-    for t, name, shape in ((d_x, "d_x", (T, H)), (d_gate_w, "d_gate_w", (I, H)), (d_up_w, "d_up_w", (I, H)),
-                           (d_down_w, "d_down_w", (H, I))):
-        grads.append(torch.empty(shape, dtype=dt, device=x.device) if t is None else _shaped(t, name, dt, shape))
+    for t, name, like in ((d_x, "d_x", x), (d_gate_w, "d_gate_w", gate_w), (d_up_w, "d_up_w", up_w),
+                          (d_down_w, "d_down_w", down_w)):
+        grads.append(torch.empty_like(like) if t is None else _shaped(t, name, dt, like.shape))
     if workspace is None:
         workspace = torch.empty(max(ffn_backward_workspace_bytes(T, I), 16), dtype=torch.uint8, device=x.device)
-    _check(lib().moe_ffn_backward(code, _ptr(d_out), _ptr(x), T, H, _ptr(gate_w), _ptr(up_w), _ptr(down_w), I,
-                                  _ptr(gate), _ptr(up), _ptr(up_logits), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), *[_ptr(g) for g in grads],
-                                  _ptr(status), _stream(stream)), "moe_ffn_backward")
+    _check(lib().moe_ffn_backward(code, d_out.data_ptr(), x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(),
+                                  down_w.data_ptr(), I, gate.data_ptr(), up.data_ptr(), up_logits.data_ptr(),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  *[g.data_ptr() for g in grads], _ptr(status), _stream(stream)), "moe_ffn_backward")
     return tuple(grads)
 
 
@@ -480,21 +484,24 @@ def ffn_backward_workspace_bytes(n_tokens: int, intermediate: int) -> int:
 
 
 def _mx4_scale_shape(rows, cols):
-    return (-(-rows // 128), cols // 128, 32, 4, 4)
+    return ((rows + 127) >> 7, cols >> 7, 32, 4, 4)
 
 
-def _mx4(codes, scales, name, ndim):
-    """Checked codes and scales of a 4-bit array; returns its leading sizes and its columns."""
+def _mx4(codes, scales, name, ndim=None):
+    """Checked codes and scales of a 4-bit array: its leading sizes and its columns."""
     import torch
-    c = _dev(codes, name, torch.uint8, ndim)
-    s = _dev(scales, f"{name}_scales", torch.uint8)
-    cols = 2 * c.shape[-1]
-    rows = c.numel() // max(c.shape[-1], 1)
+    u8 = torch.uint8
+    shape = _dev(codes, name, u8, ndim).shape
+    if not shape:
+        raise ValueError(f"{name} must have a dim of columns")
+    cols = 2 * shape[-1]
+    rows = shape[0] if len(shape) == 2 else codes.numel() // max(shape[-1], 1)
     if cols == 0 or cols % 128:
         raise ValueError(f"{name} must hold a multiple of 128 columns, got {cols}")
-    if s.numel() != -(-rows // 128) * (cols // 128) * 512:
-        raise ValueError(f"{name}_scales must hold the tiles {_mx4_scale_shape(rows, cols)}, got {tuple(s.shape)}")
-    return (*c.shape[:-1], cols)
+    _dev(scales, f"{name}_scales", u8)
+    if scales.numel() != ((rows + 127) >> 7) * (cols >> 7) * 512:
+        raise ValueError(f"{name}_scales must hold the tiles {_mx4_scale_shape(rows, cols)}, got {tuple(scales.shape)}")
+    return (*shape[:-1], cols)
 
 
 def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scales=None, status=None, stream=None):
@@ -510,43 +517,46 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
     dest_rows = pack_routed's pair_padded_rows the tokens land in the grouped,
     padded layout."""
     import torch
-    code = _dtype_code(getattr(x, "dtype", None), "x", f32=True)
-    x = _dev(x, "x", x.dtype)
-    if x.dim() not in (2, 3) or (x.dim() == 3 and (src_rows is not None or dest_rows is not None)):
+    dt = getattr(x, "dtype", None)
+    code = _dtype_code(dt, "x", f32=True)
+    shape = _dev(x, "x", dt).shape
+    lists = src_rows is not None or dest_rows is not None
+    if len(shape) != 2 and (len(shape) != 3 or lists):
         raise ValueError("x must have 2 dims, or 3 without row lists")
-    cols = x.shape[-1]
+    cols = shape[-1]
     if cols == 0 or cols % 128:
         raise ValueError(f"x must have a multiple of 128 columns, got {cols}")
-    n_src = x.numel() // cols
-    n, copies = n_src, 1
-    if src_rows is not None:
-        n = _dev(src_rows, "src_rows", torch.int32, 1).numel()
-    lead = x.shape[:-1]
-    if dest_rows is not None:
-        d = _dev(dest_rows, "dest_rows", torch.int32)
-        if d.dim() not in (1, 2) or d.shape[0] != n:
-            raise ValueError("dest_rows must be [rows converted] or [rows converted, copies]")
-        copies = d.shape[1] if d.dim() == 2 else 1
-        if codes is not None:
-            n_dest = codes.shape[0]
-        if n_dest is None:
-            raise ValueError("dest_rows needs n_dest (or codes and scales to write)")
-        lead = (int(n_dest),)
-    elif src_rows is not None:
-        lead = (n,)
-    n_out = n_src if x.dim() == 3 else lead[0]
+    n = n_src = n_out = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    copies, lead = 1, shape[:-1]
+    if lists:
+        if src_rows is not None:
+            n = _dev(src_rows, "src_rows", torch.int32, 1).numel()
+        if dest_rows is not None:
+            d = _dev(dest_rows, "dest_rows", torch.int32)
+            if d.dim() not in (1, 2) or d.shape[0] != n:
+                raise ValueError("dest_rows must be [rows converted] or [rows converted, copies]")
+            copies = d.shape[1] if d.dim() == 2 else 1
+            if codes is not None:
+                n_dest = codes.shape[0]
+            if n_dest is None:
+                raise ValueError("dest_rows needs n_dest (or codes and scales to write)")
+            n_out = int(n_dest)
+        else:
+            n_out = n
+        lead = (n_out,)
     if codes is None:
-        codes = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((*lead, cols >> 1), dtype=torch.uint8, device=x.device)
     else:
-        codes = _shaped(codes, "codes", torch.uint8, (*lead, cols // 2))
+        _shaped(codes, "codes", torch.uint8, (*lead, cols >> 1))
     if scales is None:
         scales = torch.empty(_mx4_scale_shape(n_out, cols), dtype=torch.uint8, device=x.device)
     else:
-        scales = _shaped(scales, "scales", torch.uint8, _mx4_scale_shape(n_out, cols))
+        _shaped(scales, "scales", torch.uint8, _mx4_scale_shape(n_out, cols))
     if copies == 0:
         return codes, scales
-    _check(lib().moe_mx4_quantize(code, _ptr(x), n_src, cols, _ptr(src_rows), n, _ptr(dest_rows), copies, n_out,
-                                  _ptr(codes), _ptr(scales), _ptr(status), _stream(stream)), "moe_mx4_quantize")
+    st = lib().moe_mx4_quantize(code, x.data_ptr(), n_src, cols, _ptr(src_rows), n, _ptr(dest_rows), copies, n_out,
+                                codes.data_ptr(), scales.data_ptr(), _ptr(status), _stream(stream))
+    _check(st, "moe_mx4_quantize")
     return codes, scales
 
 
@@ -555,11 +565,16 @@ def mx4_dequantize(codes, scales, dtype, out=None, stream=None):
     ``dtype`` (float16, bfloat16 or float32): [..., cols]."""
     import torch
     code = _dtype_code(dtype, "dtype", f32=True)
-    shape = _mx4(codes, scales, "codes", None)
-    out = torch.empty(shape, dtype=dtype, device=codes.device) if out is None else _shaped(out, "out", dtype, shape)
+    shape = _mx4(codes, scales, "codes")
     cols = shape[-1]
-    _check(lib().moe_mx4_dequantize(_ptr(codes), _ptr(scales), out.numel() // cols, cols, code, _ptr(out),
-                                    _stream(stream)), "moe_mx4_dequantize")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    else:
+        _shaped(out, "out", dtype, shape)
+    rows = shape[0] if len(shape) == 2 else out.numel() // cols
+    st = lib().moe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, code, out.data_ptr(),
+                                  _stream(stream))
+    _check(st, "moe_mx4_dequantize")
     return out
 
 
