@@ -64,13 +64,16 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;                        // CTAs of one MMA tile
 constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
 constexpr int MIN_STEPS = 3;                   // stages each of them keeps at least
+constexpr int MIN_TILE_STEPS = 4;              // stages' worth of time that a tile's epilogue takes
 constexpr float JOIN_STEPS = 4.0f;             // time to join a shared tile (about 2.5 us), in stages
 constexpr float JOIN_STEPS_AHEAD = 12.0f;      // the same ahead of unshared tiles, whose loads have to wait for it
 constexpr int GROUP_M = 8;                     // tile rows (of 256) that are walked together
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 
-constexpr int OFF_BARS = STAGES * STAGE_BYTES;
+constexpr int OFF_STAGING = STAGES * STAGE_BYTES;  // 4 KB per epilogue warp
+constexpr int STAGING_BYTES = 32 * 128;
+constexpr int OFF_BARS = OFF_STAGING + NUM_EPI_WARPS * STAGING_BYTES;
 constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1;   // full, empty, tfull, tempty, drain
 constexpr int OFF_TMEM_SLOT = OFF_BARS + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
@@ -103,6 +106,7 @@ struct Plan {
     int32_t total_tiles;
     int32_t split;                 // pairs per cluster
     int32_t split_tiles;           // the first so many tiles are shared by a cluster's pairs
+    int32_t lead;                  // tiles a pair without a shared one does before the others join
     int32_t n_maps;
     int32_t early_weights;         // B of problem 0 is no result of the launch before: see the producer
     int32_t tile_cols;             // output columns of a tile: 128 (gate and up side by side) or 256
@@ -331,6 +335,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     // the two warps with the same rows one takes the even passes, one the odd.
     const int quarter = warp & 3;                                // TMEM lanes 32*quarter .. +31
     const int odd = warp >= 6 ? 1 : 0;
+    uint8_t* staging = smem + OFF_STAGING + (warp >= 2 ? warp - 2 : 0) * STAGING_BYTES;
     constexpr int PASSES = EPI == EPI_GATE_UP ? 2 : 4;
     const int row = quarter * 32 + lane;                         // of this CTA's 128
     struct Rows {
@@ -397,7 +402,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                         el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                store_rows_64(el, pr.dst + at, pr.n, lane, rows, cols);
+                store_staged_64(el, staging, pr.dst + at, pr.n, lane, rows, cols);
             } else if (EPI == EPI_GATE_UP) {
                 // 32 columns of one projection (0 gate, 1 up)
                 auto load32 = [&](uint32_t (&v)[32], int which, int hh) {
@@ -427,7 +432,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                             load32(v, which, hh);
                             round32(v, hh);
                         }
-                        store_rows_64(el, (which ? p.dst_up : p.dst_gate) + at, pr.n, lane, rows, cols);
+                        store_staged_64(el, staging, (which ? p.dst_up : p.dst_gate) + at, pr.n, lane, rows, cols);
                     }
                 }
 #pragma unroll
@@ -442,15 +447,15 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                     }
                     round32(g, hh);
                 }
-                store_rows_64(el, pr.dst + at, pr.n, lane, rows, cols);
+                store_staged_64(el, staging, pr.dst + at, pr.n, lane, rows, cols);
             } else if constexpr (EPI == EPI_GRAD) {
                 // eg and eu hold G and U, then d_G and d_U
                 if (c != c0 + odd) {
                     load_lines_64(eg, p.gate_in + at, pr.n, lane, rows, cols);
                     load_lines_64(eu, p.up_in + at, pr.n, lane, rows, cols);
                 }
-                transpose_pieces(eg, lane);
-                transpose_pieces(eu, lane);
+                lines_to_rows(eg, staging, lane);
+                lines_to_rows(eu, staging, lane);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t d[32];
@@ -475,8 +480,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                         }
                     }
                 }
-                store_rows_64(eg, p.dst_gate + at, pr.n, lane, rows, cols);
-                store_rows_64(eu, p.dst_up + at, pr.n, lane, rows, cols);
+                store_staged_64(eg, staging, p.dst_gate + at, pr.n, lane, rows, cols);
+                store_staged_64(eu, staging, p.dst_up + at, pr.n, lane, rows, cols);
             }
         }
         tc_fence_before_sync();
@@ -518,7 +523,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     // First the tiles that the cluster's pairs share, each with its part of the K
     // axis, then tiles of one pair each.  Nothing leaves the loop while there are
     // shared tiles: every thread meets every barrier.
-    int32_t t = SPLIT && cluster_id < p.split_tiles ? cluster_id : p.split_tiles + pair_id;
+    // (Pairs of clusters without a shared tile start on `lead` rounds of the others.)
+    const int32_t busy = SPLIT && p.split_tiles < n_clusters ? p.split_tiles * split : n_pairs;
+    const int32_t idle = n_pairs - busy;
+    const int32_t joint = p.split_tiles + p.lead * idle;        // from here on the tiles go around all pairs
+    int32_t t = SPLIT && cluster_id < p.split_tiles ? cluster_id
+                : SPLIT && pair_id >= busy && p.lead > 0 ? p.split_tiles + pair_id - busy
+                                                         : joint + pair_id;
     while (t < p.total_tiles && (ok || t < p.split_tiles)) {
         const bool shared = SPLIT && t < p.split_tiles;
         const Tile ti = tile_at(p, t);
@@ -548,7 +559,10 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
             t += n_clusters;
-            if (t >= p.split_tiles) t = p.split_tiles + pair_id;
+            if (t >= p.split_tiles) t = joint + pair_id;
+        } else if (t < joint) {
+            t += idle;
+            if (t >= joint) t = joint + pair_id;
         } else {
             t += n_pairs;
         }
@@ -670,6 +684,14 @@ cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
             p.split_tiles = rest;
             nc = n;
         }
+    }
+    if (p.split_tiles > 0 && p.split_tiles < nc && p.n_problems > 1) {
+        // while the shared tiles run, the other clusters' pairs are this many tiles ahead
+        const float own_steps = static_cast<float>(p.pr[1].steps[0] > MIN_TILE_STEPS ? p.pr[1].steps[0] : MIN_TILE_STEPS);
+        p.lead = static_cast<int32_t>((static_cast<float>(steps) / static_cast<float>(p.split) + JOIN_STEPS) / own_steps);
+        const int32_t idle = (nc - p.split_tiles) * p.split;
+        const int32_t most = (p.total_tiles - p.split_tiles) / idle;
+        if (p.lead > most) p.lead = most;
     }
     // clusters that have work: a shared tile each, or a tile for each of their pairs
     const int32_t own = (p.total_tiles - p.split_tiles + p.split - 1) / p.split;
