@@ -411,6 +411,14 @@ def _shaped(t, name, dtype, shape):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _used_on(t, stream):
+    """Keep a tensor that this module allocated, and does not return, from being
+    handed out again before ``stream``'s work on it is done."""
+    if stream is not None:
+        import torch
+        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
+
+
 def _ffn_sizes(x, gate_w, up_w, down_w):
     """The block's type code and sizes, with every array checked."""
     dt = getattr(x, "dtype", None)
@@ -428,8 +436,9 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
 
     x [T, hidden], gate_w / up_w [intermediate, hidden], down_w [hidden,
     intermediate], all float16 or all bfloat16; any T, hidden and intermediate
-    multiples of 8.  ``out`` [T, hidden] and ``up_logits`` [T, intermediate] (the
-    gated product, rounded) may be supplied.  For gradients supply ``gate`` and
+    multiples of 8, contiguous.  ``out`` [T, hidden] and ``up_logits`` [T,
+    intermediate] (the gated product, rounded) may be supplied; what is not comes
+    from the current stream's memory, which another ``stream`` has to wait for.  For gradients supply ``gate`` and
     ``up`` [T, intermediate] too: they receive the rounded projections, which
     gated_ffn_backward reads with ``up_logits``."""
     import torch
@@ -441,6 +450,7 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
         _shaped(up, "up", dt, (T, I))
     if up_logits is None:
         up_logits = torch.empty((T, I), dtype=dt, device=x.device)
+        _used_on(up_logits, stream)
     else:
         _shaped(up_logits, "up_logits", dt, (T, I))
     if out is None:
@@ -472,6 +482,7 @@ def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=
         grads.append(torch.empty_like(like) if t is None else _shaped(t, name, dt, like.shape))
     if workspace is None:
         workspace = torch.empty(max(ffn_backward_workspace_bytes(T, I), 16), dtype=torch.uint8, device=x.device)
+        _used_on(workspace, stream)
     _check(lib().moe_ffn_backward(code, d_out.data_ptr(), x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(),
                                   down_w.data_ptr(), I, gate.data_ptr(), up.data_ptr(), up_logits.data_ptr(),
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),

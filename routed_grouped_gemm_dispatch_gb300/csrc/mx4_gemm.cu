@@ -38,7 +38,7 @@
 #include "../../include/moe_gb300.h"
 #include "moe_internal.h"
 #include "mx4_internal.h"
-#include "sm103_ptx.cuh"
+#include "sm103_products.cuh"
 #include "tensor_map.h"
 #include "tile_store.cuh"
 

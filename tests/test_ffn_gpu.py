@@ -284,3 +284,57 @@ def test_streams_and_graph_capture(T):
     torch.cuda.synchronize()
     for k in bufs:
         assert torch.equal(bufs[k].view(torch.int16), want[k].view(torch.int16)), k
+
+
+def test_refusals():
+    """What the checks name: types, shapes, strides, half of what is stored, a short workspace."""
+    dt = torch.float16
+    m = make(3, 16, 24, dt)
+    w = (m["gate_w"], m["up_w"], m["down_w"])
+    e = torch.empty((3, 24), dtype=dt, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.gated_ffn(torch.empty((16, 3), dtype=dt, device="cuda").t(), *w)
+    with pytest.raises(TypeError, match="gate_w"):
+        moe.gated_ffn(m["x"], w[0].bfloat16(), *w[1:])
+    with pytest.raises(ValueError, match="up_w"):
+        moe.gated_ffn(m["x"], w[0], w[1][:8], w[2])
+    with pytest.raises(ValueError, match="down_w"):
+        moe.gated_ffn(m["x"], w[0], w[1], w[1])
+    with pytest.raises(ValueError, match="both or neither"):
+        moe.gated_ffn(m["x"], *w, gate=e)
+    with pytest.raises(ValueError, match="out"):
+        moe.gated_ffn(m["x"], *w, out=e)
+    with pytest.raises(ValueError, match="2 dims"):
+        moe.gated_ffn(m["x"][0], *w)
+    with pytest.raises(moe.MoeError, match="MOE_ERR_SHAPE"):
+        odd = torch.zeros((3, 12), dtype=dt, device="cuda")
+        moe.gated_ffn(odd, odd, odd, torch.zeros((12, 3), dtype=dt, device="cuda"))
+    with pytest.raises(ValueError, match="d_out"):
+        moe.gated_ffn_backward(e, m["x"], *w, e, e, e)
+    with pytest.raises(moe.MoeError, match="MOE_ERR_WORKSPACE"):
+        moe.gated_ffn_backward(m["x"], m["x"], *w, e, e, e, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(moe.MoeError, match="MOE_ERR_ALIGN"):
+        moe.gated_ffn(m["x"], *w, up_logits=torch.empty(3 * 24 + 1, dtype=dt, device="cuda")[1:].view(3, 24))
+
+
+@pytest.mark.parametrize("T", [2, 200])
+def test_own_buffers_on_a_given_stream(T):
+    """Buffers that the calls allocate themselves hold until the given stream is done with them."""
+    dt = torch.bfloat16
+    m = make(T, 264, 392, dt, seed=21)
+    s = stored(m, dt)
+    args = (m["d_out"], m["x"], m["gate_w"], m["up_w"], m["down_w"], s["gate"], s["up"], s["up_logits"])
+    want = (moe.gated_ffn(*args[1:5]), *moe.gated_ffn_backward(*args))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = []
+        for _ in range(8):
+            got.append((moe.gated_ffn(*args[1:5], stream=stream), *moe.gated_ffn_backward(*args, stream=stream)))
+            # other work on the current stream that would take a freed buffer
+            torch.full((T, 392), float("nan"), dtype=dt, device="cuda")
+            torch.full((moe.ffn_backward_workspace_bytes(T, 392),), 0xFF, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for g in got:
+            for a, b in zip(g, want):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -139,7 +139,8 @@ def check(got, ref, tol, what):
 @pytest.mark.parametrize("dt", OUT, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("rows,k,n", [(1, 128, 128), (2, 256, 256), (3, 384, 384), (31, 640, 128), (33, 128, 640),
                                       (127, 256, 1152), (128, 1408, 256), (129, 2048, 384), (257, 896, 512),
-                                      (300, 256, 2048), (1111, 512, 640)])
+                                      (300, 256, 2048), (1111, 512, 640), (17, 256, 128), (48, 128, 128),
+                                      (64, 1152, 256), (65, 256, 384), (4500, 256, 384)])
 def test_matmul(rows, k, n, dt):
     rng = np.random.default_rng(rows + k + n)
     a, sa, va = random_operand(rng, rows, k, spread=1.0)
@@ -190,7 +191,11 @@ def test_nan_stays_in_its_row():
 GROUPED = [  # tokens, top_k, experts, k, n, expert popularity exponent
     (1, 1, 1, 128, 128, 0.0), (1, 2, 4, 256, 256, 0.0), (5, 2, 8, 384, 384, 0.0), (40, 2, 4, 256, 640, 1.0),
     (130, 1, 2, 512, 128, 0.0), (300, 2, 3, 256, 384, 0.0), (600, 4, 8, 640, 256, 1.2), (33, 8, 128, 256, 256, 1.2),
-    (1000, 1, 1, 1408, 512, 0.0), (700, 2, 64, 128, 896, 1.0)]
+    (1000, 1, 1, 1408, 512, 0.0), (700, 2, 64, 128, 896, 1.0),
+    # one expert with few rows: the two halves of a block, and a short last one
+    (64, 1, 1, 256, 128, 0.0), (65, 1, 1, 256, 256, 0.0), (127, 1, 1, 384, 128, 0.0), (128, 1, 1, 128, 128, 0.0),
+    # many experts, some with several blocks, several groups of units
+    (2600, 2, 3, 256, 640, 1.2), (400, 8, 256, 128, 128, 1.2)]
 
 
 def grouped(T, top_k, E, seed, zipf):
@@ -319,3 +324,55 @@ def test_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[valid], want[valid])
+
+
+def test_refusals():
+    x = torch.randn((4, 256), device="cuda").half()
+    c, s = moe.mx4_quantize(x)
+    with pytest.raises(ValueError, match="multiple of 128"):
+        moe.mx4_quantize(x[:, :64].contiguous())
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.mx4_quantize(x.t())
+    with pytest.raises(ValueError, match="without row lists"):
+        moe.mx4_quantize(x[None], src_rows=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="n_dest"):
+        moe.mx4_quantize(x, dest_rows=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="dest_rows"):
+        moe.mx4_quantize(x, dest_rows=torch.zeros(3, dtype=torch.int32, device="cuda"), n_dest=4)
+    with pytest.raises(ValueError, match="codes"):
+        moe.mx4_quantize(x, codes=c[:2])
+    with pytest.raises(ValueError, match="must hold the tiles"):
+        moe.mx4_dequantize(c, s[:, :1].contiguous(), torch.float16)
+    with pytest.raises(TypeError, match="uint8"):
+        moe.mx4_dequantize(c.int(), s, torch.float16)
+    with pytest.raises(ValueError, match="same columns"):
+        moe.mx4_matmul(c, s, *moe.mx4_quantize(torch.zeros((128, 128), device="cuda")))
+    with pytest.raises(moe.MoeError, match="MOE_ERR_SHAPE"):
+        moe.mx4_matmul(c, s, c, s)               # 4 columns of result
+    w, ws = moe.mx4_quantize(torch.zeros((2, 128, 256), device="cuda"))
+    t = moe.build_dispatch(torch.zeros((4, 1), dtype=torch.int32, device="cuda"), 2)
+    tab = (t["group_sizes"], t["group_padded_offsets"], t["group_idx_for_bx"])
+    with pytest.raises(moe.MoeError, match="MOE_ERR_SHAPE"):                 # 4 rows for 3 blocks
+        moe.mx4_gate_up(c, s, w, ws, w, ws, *tab, torch.empty((4, 128), device="cuda").half())
+    with pytest.raises(ValueError, match="up_logits"):
+        moe.mx4_gate_up(c, s, w, ws, w, ws, *tab, torch.empty((4, 64), device="cuda").half())
+    with pytest.raises(ValueError, match="n_experts"):
+        moe.mx4_gate_up(c, s, w, ws, w, ws, tab[0][:1], *tab[1:], torch.empty((4, 128), device="cuda").half())
+
+
+def test_no_rows():
+    c, s = moe.mx4_quantize(torch.empty((0, 256), device="cuda"))
+    assert c.shape == (0, 128) and s.shape == (0, 2, 32, 4, 4)
+    assert moe.mx4_dequantize(c, s, torch.bfloat16).shape == (0, 256)
+    b, sb = moe.mx4_quantize(torch.randn((128, 256), device="cuda"))
+    assert moe.mx4_matmul(c, s, b, sb).shape == (0, 128)
+    # tables without a pair
+    t = moe.build_dispatch(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 3)
+    rows = t["group_idx_for_bx"].numel() * 128
+    a, sa = moe.mx4_quantize(torch.zeros((rows, 256), device="cuda"))
+    out = sentinel(rows, 128)
+    w, sw = moe.mx4_quantize(torch.zeros((3, 128, 256), device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.mx4_gate_up(a, sa, w, sw, w, sw, t["group_sizes"], t["group_padded_offsets"], t["group_idx_for_bx"], out, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and bool((out.view(torch.int16) == SENTINEL).all())
