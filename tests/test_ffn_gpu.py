@@ -338,3 +338,44 @@ def test_own_buffers_on_a_given_stream(T):
         for g in got:
             for a, b in zip(g, want):
                 assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^31: the last rows' results are those of a call on them alone,
+    and the weights' gradients are the sum of those of two halves."""
+    dt, T, H, I = torch.bfloat16, 280_001, 8, 8192
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dt)
+    d_out = torch.randn((T, H), generator=g, device="cuda").to(dt)
+    w = [torch.randn((I, H), generator=g, device="cuda").to(dt) for _ in range(2)]
+    w.append((torch.randn((H, I), generator=g, device="cuda") * I ** -0.5).to(dt))
+    s = {k: torch.empty((T, I), dtype=dt, device="cuda") for k in ("gate", "up", "up_logits")}
+    out = moe.gated_ffn(x, *w, **s)
+    d_x, *dw = moe.gated_ffn_backward(d_out, x, *w, s["gate"], s["up"], s["up_logits"])
+    # from the last full tile of 256 rows on, so that the rows sit alike in their tiles
+    at = T // 256 * 256 - 256
+    assert at * I > 2 ** 31
+    t = {k: torch.empty((T - at, I), dtype=dt, device="cuda") for k in s}
+    want = moe.gated_ffn(x[at:], *w, **t)
+    want_x = moe.gated_ffn_backward(d_out[at:], x[at:], *w, t["gate"], t["up"], t["up_logits"])[0]
+    tail = (x[at:].double() @ w[0].double().t(), x[at:].double() @ w[1].double().t())
+    check(s["gate"][at:], tail[0], rounding(tail[0], dt) + 2 * acc(H) * (x[at:].double().abs() @ w[0].double().abs().t()), "gate")
+    check(s["up"][at:], tail[1], rounding(tail[1], dt) + 2 * acc(H) * (x[at:].double().abs() @ w[1].double().abs().t()), "up")
+    # the two calls may split their sums differently: an fp32 sum and one rounding apart
+    y = t["up_logits"].double() @ w[2].double().t()
+    tol = 2 * rounding(y, dt) + 4 * acc(I) * (t["up_logits"].double().abs() @ w[2].double().abs().t())
+    # up_logits of the two calls differ by a rounding where an fp32 sum fell on either side of it
+    tol = tol + 2 * half_step(dt) * (t["up_logits"].double().abs() @ w[2].double().abs().t())
+    check(out[at:], want.double(), tol, "out")
+    assert float((d_x[at:].double() - want_x.double()).norm()) <= 8 * half_step(dt) * float(want_x.double().norm())
+    # gradients of the weights: two halves added in fp32, each rounded once
+    half = T // 2
+    parts = [moe.gated_ffn_backward(d_out[a:b], x[a:b], *w, s["gate"][a:b], s["up"][a:b], s["up_logits"][a:b])[1:]
+             for a, b in ((0, half), (half, T))]
+    for got, p, q in zip(dw, *parts):
+        ref = p.double() + q.double()
+        tol = half_step(dt) * (p.double().abs() + q.double().abs() + 2 * ref.abs())
+        err = (got.double() - ref).norm()
+        # (a random walk's partial sums are about as large as its end: acc(T) of it for the fp32 sum)
+        assert float(err) <= float(tol.norm()) + acc(T) * float(got.double().norm())

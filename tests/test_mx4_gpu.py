@@ -376,3 +376,31 @@ def test_no_rows():
     moe.mx4_gate_up(a, sa, w, sw, w, sw, t["group_sizes"], t["group_padded_offsets"], t["group_idx_for_bx"], out, status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 0 and bool((out.view(torch.int16) == SENTINEL).all())
+
+
+def test_offsets_past_32_bits():
+    """Values past element 2^31: the last rows' results are those of a call on them alone."""
+    rows, cols = (1 << 20) + 131, 2176
+    assert rows * cols > 2 ** 31
+    x = torch.zeros((rows, cols), dtype=torch.float16, device="cuda")
+    last = rows - rows % 128 - 128                # a whole scale tile from here
+    x[last:] = torch.randn((rows - last, cols), device="cuda").half()
+    c, s = moe.mx4_quantize(x)
+    want_c, want_s = moe.mx4_quantize(x[last:].contiguous())
+    assert torch.equal(c[last:], want_c) and torch.equal(s[last // 128:], want_s)
+    back = moe.mx4_dequantize(c, s, torch.float16)
+    assert torch.equal(back[last:], moe.mx4_dequantize(want_c, want_s, torch.float16))
+    assert not bool(back[:last].any())
+    del x, c, s, back
+
+    rows, k, n = 128 * 16384, 128, 1152            # the most blocks
+    assert rows * n > 2 ** 31
+    codes = torch.zeros((rows, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows // 128, 1, 32, 4, 4), 127, dtype=torch.uint8, device="cuda")
+    codes[-300:] = torch.randint(0, 256, (300, k // 2), dtype=torch.uint8, device="cuda")
+    b, sb = moe.mx4_quantize(torch.randn((n, k), device="cuda"))
+    out = moe.mx4_matmul(codes, scales, b, sb)
+    want = moe.mx4_matmul(codes[-384:].contiguous(), scales[-3:].contiguous(), b, sb)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-384:], want)
+    assert not bool(out[:-384].any())
