@@ -18,8 +18,8 @@
 // launch, so that its last wave is one and not four.
 //
 //  * Persistent clusters of two CTAs, one 2-SM MMA tile of M = 256 x N = 256 at
-//    a time: each CTA holds 128 rows of A and 128 of B per stage (K = 128, 64 KB,
-//    ring of three), warp 0 feeds the ring by TMA, warp 1 of the even CTA issues
+//    a time: each CTA holds 128 rows of A and 128 of B per stage (K = 64, 32 KB,
+//    ring of six), warp 0 feeds the ring by TMA, warp 1 of the even CTA issues
 //    the MMAs into one of two TMEM accumulators, and warps 2-9 of both CTAs turn
 //    the other one into 16-bit rows meanwhile.  With 128 x 256 tiles on one SM
 //    the operands' way into and out of shared memory, not the tensor core, is
@@ -53,20 +53,21 @@ namespace {
 
 constexpr int BM = 128;                        // rows of A (and of B) per CTA
 constexpr int BN = 256;                        // columns of a tile
-constexpr int BK = 128;                        // K per stage
-constexpr int STAGES = 3;
-constexpr int OP_BYTES = BM * BK * 2;          // one operand's stage: two boxes of 16 KB
-constexpr int BOX_BYTES = OP_BYTES / 2;
+constexpr int BK = 64;                         // K per stage
+constexpr int STAGES = 384 / BK;
+constexpr int OP_BYTES = BM * BK * 2;          // one operand's stage
+constexpr int K_BOX_BYTES = BM * 128;          // K-major: boxes of 64 along K x 128 rows
+constexpr int MN_BOX_BYTES = BK * 128;         // M/N-major: two boxes of 64 along M/N x BK rows of K
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int NUM_THREADS = 320;               // producer, MMA and eight epilogue warps
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;                        // CTAs of one MMA tile
 constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
-constexpr int MIN_STEPS = 3;                   // stages each of them keeps at least
-constexpr int MIN_TILE_STEPS = 4;              // stages' worth of time that a tile's epilogue takes
-constexpr float JOIN_STEPS = 4.0f;             // time to join a shared tile (about 2.5 us), in stages
-constexpr float JOIN_STEPS_AHEAD = 12.0f;      // the same ahead of unshared tiles, whose loads have to wait for it
+constexpr int MIN_STEPS = 384 / BK;            // stages each of them keeps at least
+constexpr int MIN_TILE_STEPS = 512 / BK;       // stages' worth of time that a tile's epilogue takes
+constexpr float JOIN_STEPS = 512.0f / BK;             // time to join a shared tile (about 2.5 us), in stages
+constexpr float JOIN_STEPS_AHEAD = 1536.0f / BK;      // the same ahead of unshared tiles, whose loads have to wait for it
 constexpr int GROUP_M = 8;                     // tile rows (of 256) that are walked together
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
@@ -79,7 +80,7 @@ constexpr int OFF_TMEM_SLOT = OFF_BARS + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
 constexpr int SMEM_BYTES = 1024 + OFF_ABORT + 4;
 
-constexpr int MAX_MAPS = 10;
+constexpr int MAX_MAPS = 12;
 constexpr int MAX_PROBLEMS = 4;
 
 enum Epilogue { EPI_STORE = 0, EPI_GATE_UP = 1, EPI_GRAD = 2 };
@@ -231,7 +232,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     const uint32_t leader_full = mapa_shared(bar_full, 2 * pair);
     const uint32_t leader_tempty = mapa_shared(bar_tempty, 2 * pair);
 
-    // TMA producer (warp 0, one lane, both CTAs): stages [s0, s1) of a tile.
+    // TMA producer (warp 0 of both CTAs): stages [s0, s1) of a tile.
+    const uint32_t issue = elect_one();
+    const uint32_t leader_issue = leader ? issue : 0;
     bool early = p.early_weights != 0;
     auto produce = [&](const Tile& ti, int32_t s0, int32_t s1) {
         const Problem& pr = p.pr[ti.q];
@@ -240,13 +243,14 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const int32_t brow = EPI == EPI_GATE_UP ? ti.n * BM : ti.n * BN + static_cast<int32_t>(rank) * BM;
         const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
         const int32_t steps0 = pr.steps[0];
-        // K-major: two boxes of 64 along K x 128 rows; M/N-major: two boxes of 64
-        // along M/N x 128 rows of K
         auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t fb, bool mn, int32_t row, int32_t k0) {
+            if (mn) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (mn) tma_load_2d_pair(dst + b * BOX_BYTES, m, fb, row + b * 64, k0, policy);
-                else tma_load_2d_pair(dst + b * BOX_BYTES, m, fb, k0 + b * 64, row, policy);
+                for (int b = 0; b < 2; ++b) tma_load_2d_pair_if(issue, dst + b * MN_BOX_BYTES, m, fb, row + b * 64, k0, policy);
+            } else {
+#pragma unroll
+                for (int b = 0; b < BK / 64; ++b)
+                    tma_load_2d_pair_if(issue, dst + b * K_BOX_BYTES, m, fb, k0 + b * 64, row, policy);
             }
         };
         // The first tile of a launch right behind the one that makes its A: the
@@ -258,12 +262,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             have_b = s1 - s0 < STAGES ? s1 - s0 : STAGES;
             have_b = s0 + have_b <= steps0 ? have_b : (s0 < steps0 ? steps0 - s0 : 0);   // of the first K segment
             for (int32_t i = 0; i < have_b; ++i) {
-                if (leader) mbar_arrive_expect_tx(bar_full + 8 * i, PAIR * STAGE_BYTES);
+                mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * i, PAIR * STAGE_BYTES);
                 load(&maps.m[pr.b_map[0][rank]], sbase + i * STAGE_BYTES + OP_BYTES, leader_full + 8 * i, b_mn, brow,
                      (s0 + i) * BK);
             }
             pdl_wait_prior_grid();
             pdl_launch_dependents();
+            __syncwarp();
             early = false;
         }
 #pragma unroll 1
@@ -273,14 +278,14 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             int32_t k0 = ((seg == 0 ? s0 : (s0 > steps0 ? s0 : steps0)) - (seg == 0 ? 0 : steps0)) * BK;
             const int32_t k1 = (seg == 0 ? (s1 < steps0 ? s1 : steps0) : s1 - steps0) * BK;
             for (; k0 < k1; k0 += BK) {
-                if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
                     ok = false;
                     return;
                 }
                 const uint32_t fb = leader_full + 8 * stage;
                 const uint32_t sa = sbase + stage * STAGE_BYTES;
                 if (have_b == 0) {
-                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, PAIR * STAGE_BYTES);
+                    mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * stage, PAIR * STAGE_BYTES);
                     load(bm, sa + OP_BYTES, fb, b_mn, brow, k0);
                 } else {
                     --have_b;
@@ -293,7 +298,6 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     };
 
     // MMA issuer (warp 1 of the even CTA): the same stages into an accumulator.
-    const uint32_t issue = elect_one();
     auto multiply = [&](const Tile& ti, int32_t s0, int32_t s1) {
         if (!mbar_wait_warp(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
             ok = false;
@@ -312,14 +316,14 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             tc_fence_after_sync();
             const uint32_t sa = sbase + stage * STAGE_BYTES;
             const uint32_t sb = sa + OP_BYTES;
-            const uint64_t da = a_mn ? smem_desc_mn_sw128(sa, BOX_BYTES) : smem_desc_k_sw128(sa);
-            const uint64_t db = b_mn ? smem_desc_mn_sw128(sb, BOX_BYTES) : smem_desc_k_sw128(sb);
+            const uint64_t da = a_mn ? smem_desc_mn_sw128(sa, MN_BOX_BYTES) : smem_desc_k_sw128(sa);
+            const uint64_t db = b_mn ? smem_desc_mn_sw128(sb, MN_BOX_BYTES) : smem_desc_k_sw128(sb);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk) {
                 // a K = 16 slice further, in 16-byte units: M/N-major 16 rows of
                 // 128 bytes; K-major 32 bytes inside a box of four slices
                 constexpr int MN_STEP = 2048 >> 4;
-                const int k_off = (kk / 4) * (BOX_BYTES >> 4) + (kk % 4) * (32 >> 4);
+                const int k_off = (kk / 4) * (K_BOX_BYTES >> 4) + (kk % 4) * (32 >> 4);
                 tc_mma_f16_pair_if(issue, d_tmem, da + (a_mn ? kk * MN_STEP : k_off), db + (b_mn ? kk * MN_STEP : k_off),
                                    idesc, (st != s0 || kk != 0) ? 1u : 0u);
             }
@@ -537,7 +541,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const int32_t s0 = shared ? steps * static_cast<int32_t>(pair) / split : 0;
         const int32_t s1 = shared ? steps * (static_cast<int32_t>(pair) + 1) / split : steps;
         if (warp == 0) {
-            if (lane == 0 && ok) produce(ti, s0, s1);
+            if (ok) produce(ti, s0, s1);
         } else if (warp == 1) {
             if (leader && ok) multiply(ti, s0, s1);
         } else if (ok) {
@@ -743,10 +747,10 @@ void set_operands(Problem& pr, int seg, int64_t k, int a, int b_even, int b_odd)
     pr.b_map[seg][1] = static_cast<int8_t>(b_odd);
 }
 
-// Boxes: 128 rows x 64 columns (K-major operand) or, of the same array read
-// M/N-major, 128 rows of K x 64 columns of M/N: the same box either way.
-bool box_map(Maps& maps, int i, const void* base, int64_t rows, int64_t cols) {
-    return tensor_map_2d(&maps.m[i], base, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), 2, BM);
+// Boxes of 64 columns: 128 rows of a K-major operand, or BK rows of K of an
+// M/N-major one.
+bool box_map(Maps& maps, int i, const void* base, int64_t rows, int64_t cols, bool mn = false) {
+    return tensor_map_2d(&maps.m[i], base, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), 2, mn ? BK : BM);
 }
 
 }  // namespace
@@ -784,17 +788,20 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     const int64_t T = a.n_tokens;
     const int32_t H = a.hidden, I = a.intermediate;
     Maps maps;
-    enum { DY, DOWN, DG, DU, GATE, UP, X, HG };
-    if (!box_map(maps, DY, a.d_out, T, H) || !box_map(maps, DOWN, a.down_w, H, I) ||
-        !box_map(maps, DG, a.d_gate, T, I) || !box_map(maps, DU, a.d_up, T, I) ||
-        !box_map(maps, GATE, a.gate_w, I, H) || !box_map(maps, UP, a.up_w, I, H) || !box_map(maps, X, a.x, T, H) ||
-        !box_map(maps, HG, a.up_logits, T, I))
+    // K-major operands, then M/N-major ones
+    enum { DY, DG, DU, DOWN_T, GATE_T, UP_T, X_T, H_T, DY_T, DG_T, DU_T, MAPS };
+    static_assert(MAPS <= MAX_MAPS, "maps fit");
+    if (!box_map(maps, DY, a.d_out, T, H) || !box_map(maps, DG, a.d_gate, T, I) || !box_map(maps, DU, a.d_up, T, I) ||
+        !box_map(maps, DOWN_T, a.down_w, H, I, true) || !box_map(maps, GATE_T, a.gate_w, I, H, true) ||
+        !box_map(maps, UP_T, a.up_w, I, H, true) || !box_map(maps, X_T, a.x, T, H, true) ||
+        !box_map(maps, H_T, a.up_logits, T, I, true) || !box_map(maps, DY_T, a.d_out, T, H, true) ||
+        !box_map(maps, DG_T, a.d_gate, T, I, true) || !box_map(maps, DU_T, a.d_up, T, I, true))
         return cudaErrorInvalidValue;
     Plan p{};
     Problem& dh = add_problem(p, nullptr, T, I, BN);
-    set_operands(dh, 0, H, DY, DOWN, DOWN);
+    set_operands(dh, 0, H, DY, DOWN_T, DOWN_T);
     dh.b_mn = 1;
-    p.n_maps = HG + 1;
+    p.n_maps = MAPS;
     p.gate_in = a.gate;
     p.up_in = a.up;
     p.dst_gate = a.d_gate;
@@ -805,14 +812,14 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
 
     Plan q{};
     q.status = a.status;
-    q.n_maps = HG + 1;
+    q.n_maps = MAPS;
     q.early_weights = 1;
     Problem& dx = add_problem(q, a.d_x, T, H, BN);
-    set_operands(dx, 0, I, DG, GATE, GATE);
-    set_operands(dx, 1, I, DU, UP, UP);
+    set_operands(dx, 0, I, DG, GATE_T, GATE_T);
+    set_operands(dx, 1, I, DU, UP_T, UP_T);
     dx.b_mn = 1;
     struct { uint16_t* dst; int32_t m, n; int a, b; } w[3] = {
-        {a.d_gate_w, I, H, DG, X}, {a.d_up_w, I, H, DU, X}, {a.d_down_w, H, I, DY, HG}};
+        {a.d_gate_w, I, H, DG_T, X_T}, {a.d_up_w, I, H, DU_T, X_T}, {a.d_down_w, H, I, DY_T, H_T}};
     for (const auto& d : w) {
         Problem& pr = add_problem(q, d.dst, d.m, d.n, BN);
         set_operands(pr, 0, T, d.a, d.b, d.b);

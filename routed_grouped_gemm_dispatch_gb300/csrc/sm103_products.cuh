@@ -38,14 +38,49 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t 
 }
 
 // ---------------------------------------------------------------------------
+// warp-uniform issue
+// ---------------------------------------------------------------------------
+
+// The `_if` forms of copies, MMAs and commits are executed by a converged warp and
+// issued by the lane with `issue` set.  With the operands computed by the whole
+// warp the compiler keeps addresses, coordinates and descriptors in uniform
+// registers, where these instructions want them; computed inside a one-lane
+// branch each has to be moved there first, about 90 cycles an instruction, which
+// is longer than a 4-bit MMA takes and leaves a ring of copies short of work.
+__device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t issue, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_if(uint32_t issue, uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                               int32_t c0, int32_t c1, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %6, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_pair_if(uint32_t issue, uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                    int32_t c0, int32_t c1, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %6, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy), "r"(issue)
+        : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // 16-bit operands
 // ---------------------------------------------------------------------------
 
-// The warp-uniform forms of the pair's MMA and commit: executed by a converged
-// warp, issued by the lane with `issue` set.  With the operands computed by the
-// whole warp the compiler keeps descriptors and addresses in uniform registers;
-// computed inside a one-lane branch each has to be moved there first, which
-// takes longer than a 4-bit MMA.
 __device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                    uint32_t idesc, uint32_t accumulate) {
     asm volatile(
