@@ -91,7 +91,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + OFF_ABORT);
 
     const int tid = threadIdx.x;
-    const int warp = tid >> 5;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);     // known to be warp-uniform
     const int lane = tid & 31;
     const uint32_t rank = cluster_cta_rank();
     uint32_t nranks;
@@ -118,83 +118,83 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == 0) {
         // ===================== producer =====================
-        if (lane == 0) {
-            const uint64_t policy = l2_policy_evict_normal();
-            auto load_w = [&](int32_t c, int32_t s) {
-                const uint32_t fb = bar_full + 8 * s, dst = sbase + s * stage_bytes;
-                mbar_arrive_expect_tx(fb, stage_bytes);
-                if (GATE_UP) {
-                    tma_load_2d(dst, &map_w, fb, c * BK, tile * (BM / 2), policy);
-                    tma_load_2d(dst + W_BYTES / 2, &map_w2, fb, c * BK, tile * (BM / 2), policy);
-                } else {
-                    tma_load_2d(dst, &map_w, fb, c * BK, tile * BM, policy);
-                }
-            };
-            auto load_x = [&](int32_t c, int32_t s) {
-                tma_load_2d(sbase + s * stage_bytes + W_BYTES, &map_x, bar_full + 8 * s, c * BK, 0, policy);
-            };
-            const int32_t first = c1 - c0 < stages ? c1 - c0 : stages;
-            // Weight lines on their way into L2 while the grid before still works.
-            for (int32_t c = c0 + (GATE_UP ? 0 : first); p.prefetch && c < c1; ++c) {
-                if (GATE_UP) {
-                    tma_prefetch_2d(&map_w, c * BK, tile * (BM / 2));
-                    tma_prefetch_2d(&map_w2, c * BK, tile * (BM / 2));
-                } else {
-                    tma_prefetch_2d(&map_w, c * BK, tile * BM);
-                }
+        const uint32_t issue = elect_one();
+        const uint64_t policy = l2_policy_evict_normal();
+        auto load_w = [&](int32_t c, int32_t s) {
+            const uint32_t fb = bar_full + 8 * s, dst = sbase + s * stage_bytes;
+            mbar_arrive_expect_tx_if(issue, fb, stage_bytes);
+            if (GATE_UP) {
+                tma_load_2d_if(issue, dst, &map_w, fb, c * BK, tile * (BM / 2), policy);
+                tma_load_2d_if(issue, dst + W_BYTES / 2, &map_w2, fb, c * BK, tile * (BM / 2), policy);
+            } else {
+                tma_load_2d_if(issue, dst, &map_w, fb, c * BK, tile * BM, policy);
             }
-            if (GATE_UP) pdl_wait_prior_grid();
-            // Behind the gate and up launch of the same call the weights may be
-            // read at once: that launch lets this one start only after its own
-            // wait for everything before it, and writes no weights.
-            for (int32_t i = 0; i < first; ++i) load_w(c0 + i, i);
-            if (!GATE_UP) pdl_wait_prior_grid();
-            for (int32_t i = 0; i < first; ++i) load_x(c0 + i, i);
-            int32_t stage = first == stages ? 0 : first;
-            uint32_t phase = first == stages ? 1u : 0u;
-            int32_t c = c0 + first;
-            for (; c < c1; ++c) {
-                if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
-                load_w(c, stage);
-                load_x(c, stage);
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
+        };
+        auto load_x = [&](int32_t c, int32_t s) {
+            tma_load_2d_if(issue, sbase + s * stage_bytes + W_BYTES, &map_x, bar_full + 8 * s, c * BK, 0, policy);
+        };
+        const int32_t first = c1 - c0 < stages ? c1 - c0 : stages;
+        // Weight lines on their way into L2 while the grid before still works.
+        for (int32_t c = c0 + (GATE_UP ? 0 : first); p.prefetch && c < c1; ++c) {
+            if (!issue) break;
+            if (GATE_UP) {
+                tma_prefetch_2d(&map_w, c * BK, tile * (BM / 2));
+                tma_prefetch_2d(&map_w2, c * BK, tile * (BM / 2));
+            } else {
+                tma_prefetch_2d(&map_w, c * BK, tile * BM);
             }
-            if (c < c1) {
-                // Let the copies already in flight land before the CTA exits.
-                volatile int never = 0;
-                const int32_t issued = c - c0;
-                const int32_t n = issued < stages ? issued : stages;
-                for (int32_t i = 0; i < n; ++i) {
-                    const int32_t idx = issued - 1 - i;
-                    mbar_wait_bounded(bar_full + 8 * (idx % stages), static_cast<uint32_t>((idx / stages) & 1), &never,
-                                      DRAIN_LIMIT_NS);
-                }
+        }
+        __syncwarp();
+        if (GATE_UP) pdl_wait_prior_grid();
+        // Behind the gate and up launch of the same call the weights may be
+        // read at once: that launch lets this one start only after its own
+        // wait for everything before it, and writes no weights.
+        for (int32_t i = 0; i < first; ++i) load_w(c0 + i, i);
+        if (!GATE_UP) pdl_wait_prior_grid();
+        for (int32_t i = 0; i < first; ++i) load_x(c0 + i, i);
+        int32_t stage = first == stages ? 0 : first;
+        uint32_t phase = first == stages ? 1u : 0u;
+        int32_t c = c0 + first;
+        for (; c < c1; ++c) {
+            if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
+            load_w(c, stage);
+            load_x(c, stage);
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (c < c1 && lane == 0) {
+            // Let the copies already in flight land before the CTA exits.
+            volatile int never = 0;
+            const int32_t issued = c - c0;
+            const int32_t n = issued < stages ? issued : stages;
+            for (int32_t i = 0; i < n; ++i) {
+                const int32_t idx = issued - 1 - i;
+                mbar_wait_bounded(bar_full + 8 * (idx % stages), static_cast<uint32_t>((idx / stages) & 1), &never,
+                                  DRAIN_LIMIT_NS);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ===================== MMA issuer =====================
-        if (lane == 0) {
-            const uint32_t idesc = idesc_16bit_f32acc(BM, static_cast<uint32_t>(p.np), BF16, false, false);
-            int32_t stage = 0;
-            uint32_t phase = 0;
-            for (int32_t c = c0; c < c1; ++c) {
-                if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) break;
-                tc_fence_after_sync();
-                const uint64_t dw = smem_desc_k_sw128(sbase + stage * stage_bytes);
-                const uint64_t dx = smem_desc_k_sw128(sbase + stage * stage_bytes + W_BYTES);
+        const uint32_t issue = elect_one();
+        const uint32_t idesc = idesc_16bit_f32acc(BM, static_cast<uint32_t>(p.np), BF16, false, false);
+        int32_t stage = 0;
+        uint32_t phase = 0;
+        for (int32_t c = c0; c < c1; ++c) {
+            if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) break;
+            tc_fence_after_sync();
+            const uint64_t dw = smem_desc_k_sw128(sbase + stage * stage_bytes);
+            const uint64_t dx = smem_desc_k_sw128(sbase + stage * stage_bytes + W_BYTES);
 #pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk)
-                    tc_mma_f16(tmem_base, dw + kk * 2, dx + kk * 2, idesc, (c != c0 || kk != 0) ? 1u : 0u);
-                tc_commit(bar_empty + 8 * stage);
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
-            }
-            tc_commit(bar_done);
+            for (int kk = 0; kk < BK / 16; ++kk)
+                tc_mma_f16_if(issue, tmem_base, dw + kk * 2, dx + kk * 2, idesc, (c != c0 || kk != 0) ? 1u : 0u);
+            tc_commit_if(issue, bar_empty + 8 * stage);
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
+        tc_commit_if(issue, bar_done);
         __syncwarp();
     } else {
         // ===================== partial sums to shared memory =====================

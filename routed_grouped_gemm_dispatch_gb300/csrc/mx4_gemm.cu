@@ -297,67 +297,65 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     if (warp == 0) {
         // ===================== producer (both CTAs) =====================
-        {
-            const uint32_t issue = elect_one();
-            const uint32_t leader_issue = leader ? issue : 0;
-            const uint64_t policy = l2_policy_evict_normal();
-            const uint32_t leader_full = mapa_shared(bar_full, 0);
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            bool ok = true;
-            const int32_t my_tiles = __shfl_sync(0xffffffffu, total_tiles, 0);
-            for (int32_t t = pair_id; t < my_tiles && ok; t += n_pairs) {
-                const Tile ti = tile_at<FORM>(p, t, units, num_units, group);
-                const int32_t e = uniform(ti.u.e), rows0 = uniform(ti.u.rows[0]), rows1 = uniform(ti.u.rows[1]);
-                const int32_t bx = uniform(ti.u.bx) + static_cast<int32_t>(rank), slice = uniform(ti.n);
-                // a block's codes: 128 rows, 32 where it has no more, none where it has none
-                const uint32_t a0 = rows0 > SMALL_ROWS ? OP_BYTES : SMALL_ROWS * BOX;
-                const uint32_t a1 = rows1 > SMALL_ROWS ? OP_BYTES : (rows1 > 0 ? SMALL_ROWS * BOX : 0);
-                const int32_t rows = leader ? rows0 : rows1;
-                const uint32_t bytes = a0 + SFA_BYTES + (rows1 > 0 ? a1 + SFA_BYTES : 0) + 2 * (OP_BYTES + SFB_BYTES);
-                const CUtensorMap* am = rows > SMALL_ROWS ? &maps.a : &maps.a_small;
-                // weight rows: the same 128 of gate (even CTA) and up (odd), or this CTA's half of 256
-                const int32_t tile_row = e * p.n + slice * (FORM == MX4_GATE_UP ? BM : BN);
-                const CUtensorMap* bm = FORM == MX4_GATE_UP && !leader ? &maps.b2 : &maps.b;
-                const int32_t brow = tile_row + (FORM == MX4_GATE_UP ? 0 : static_cast<int32_t>(rank) * BM);
-                for (int32_t kb = 0; kb < k_steps; ++kb) {
-                    if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = leader_full + 8 * stage;
-                    const uint32_t sa = sbase + stage * STAGE_BYTES;
-                    const uint32_t sb = sa + OP_BYTES;
-                    const uint32_t ss = sb + OP_BYTES;
-                    mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * stage, bytes);
-                    tma_load_2d_pair_if(issue, sb, bm, fb, kb * BOX, brow, policy);
-                    if (rows > 0) {
-                        tma_load_2d_pair_if(issue, sa, am, fb, kb * BOX, bx * BM, policy);
-                        tma_load_2d_pair_if(issue, ss, &maps.sfa, fb, kb * 256, bx, policy);
-                    }
-                    // every CTA needs the scales of all of B's rows
-                    tma_load_2d_pair_if(issue, ss + SFA_BYTES, &maps.sfb, fb, kb * 256, tile_row / BM, policy);
-                    if (FORM == MX4_GATE_UP)
-                        tma_load_2d_pair_if(issue, ss + SFA_BYTES + SFB_BYTES / 2, &maps.sfb2, fb, kb * 256, tile_row / BM, policy);
-                    ++issued;
-                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+        const uint32_t issue = elect_one();
+        const uint32_t leader_issue = leader ? issue : 0;
+        const uint64_t policy = l2_policy_evict_normal();
+        const uint32_t leader_full = mapa_shared(bar_full, 0);
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        const int32_t my_tiles = __shfl_sync(0xffffffffu, total_tiles, 0);
+        for (int32_t t = pair_id; t < my_tiles && ok; t += n_pairs) {
+            const Tile ti = tile_at<FORM>(p, t, units, num_units, group);
+            const int32_t e = uniform(ti.u.e), rows0 = uniform(ti.u.rows[0]), rows1 = uniform(ti.u.rows[1]);
+            const int32_t bx = uniform(ti.u.bx) + static_cast<int32_t>(rank), slice = uniform(ti.n);
+            // a block's codes: 128 rows, 32 where it has no more, none where it has none
+            const uint32_t a0 = rows0 > SMALL_ROWS ? OP_BYTES : SMALL_ROWS * BOX;
+            const uint32_t a1 = rows1 > SMALL_ROWS ? OP_BYTES : (rows1 > 0 ? SMALL_ROWS * BOX : 0);
+            const int32_t rows = leader ? rows0 : rows1;
+            const uint32_t bytes = a0 + SFA_BYTES + (rows1 > 0 ? a1 + SFA_BYTES : 0) + 2 * (OP_BYTES + SFB_BYTES);
+            const CUtensorMap* am = rows > SMALL_ROWS ? &maps.a : &maps.a_small;
+            // weight rows: the same 128 of gate (even CTA) and up (odd), or this CTA's half of 256
+            const int32_t tile_row = e * p.n + slice * (FORM == MX4_GATE_UP ? BM : BN);
+            const CUtensorMap* bm = FORM == MX4_GATE_UP && !leader ? &maps.b2 : &maps.b;
+            const int32_t brow = tile_row + (FORM == MX4_GATE_UP ? 0 : static_cast<int32_t>(rank) * BM);
+            for (int32_t kb = 0; kb < k_steps; ++kb) {
+                if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t fb = leader_full + 8 * stage;
+                const uint32_t sa = sbase + stage * STAGE_BYTES;
+                const uint32_t sb = sa + OP_BYTES;
+                const uint32_t ss = sb + OP_BYTES;
+                mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * stage, bytes);
+                tma_load_2d_pair_if(issue, sb, bm, fb, kb * BOX, brow, policy);
+                if (rows > 0) {
+                    tma_load_2d_pair_if(issue, sa, am, fb, kb * BOX, bx * BM, policy);
+                    tma_load_2d_pair_if(issue, ss, &maps.sfa, fb, kb * 256, bx, policy);
+                }
+                // every CTA needs the scales of all of B's rows
+                tma_load_2d_pair_if(issue, ss + SFA_BYTES, &maps.sfb, fb, kb * 256, tile_row / BM, policy);
+                if (FORM == MX4_GATE_UP)
+                    tma_load_2d_pair_if(issue, ss + SFA_BYTES + SFB_BYTES / 2, &maps.sfb2, fb, kb * 256, tile_row / BM, policy);
+                ++issued;
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
-            if (!ok && lane == 0) {
-                // Let the copies already in flight land before the CTA exits.
-                volatile int never = 0;
-                if (leader) {
-                    const int64_t n = issued < stages ? issued : stages;
-                    for (int64_t i = 0; i < n; ++i) {
-                        const int64_t idx = issued - 1 - i;
-                        mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
-                                          static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
-                    }
-                } else {
-                    // the odd CTA's copies report to the even CTA's barriers
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 1000000ull) { }
+        }
+        if (!ok && lane == 0) {
+            // Let the copies already in flight land before the CTA exits.
+            volatile int never = 0;
+            if (leader) {
+                const int64_t n = issued < stages ? issued : stages;
+                for (int64_t i = 0; i < n; ++i) {
+                    const int64_t idx = issued - 1 - i;
+                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
+                                      static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
                 }
+            } else {
+                // the odd CTA's copies report to the even CTA's barriers
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) { }
             }
         }
         __syncwarp();
@@ -645,49 +643,47 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     if (warp == 0) {
         // ===================== producer =====================
-        {
-            const uint32_t issue = elect_one();
-            const uint64_t policy = l2_policy_evict_normal();
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            bool ok = true;
-            for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
-                const FewTile ti = tile(t);
-                const int32_t wrow = uniform(ti.e) * p.n + uniform(ti.n) * BM;
-                const int32_t xrow = uniform(ti.bx) * BM + uniform(ti.first), bx = uniform(ti.bx);
-                const bool small = uniform(ti.rows) <= SMALL_ROWS;
-                const uint32_t bytes = F::W_BYTES + (small ? SMALL_ROWS : FEW_ROWS) * BOX + (F::ACCS + 1) * 2 * SCALE_TILE;
-                for (int32_t kb = 0; kb < k_steps; ++kb) {
-                    if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = bar_full + 8 * stage;
-                    const uint32_t sw = sbase + stage * F::STAGE;
-                    const uint32_t sx = sw + F::W_BYTES;
-                    const uint32_t ss = sx + F::X_BYTES;
-                    mbar_arrive_expect_tx_if(issue, fb, bytes);
-                    tma_load_2d_if(issue, sw, &maps.b, fb, kb * BOX, wrow, policy);
-                    tma_load_2d_if(issue, ss + 2 * SCALE_TILE, &maps.sfb, fb, kb * 256, wrow / BM, policy);
-                    if (FORM == MX4_GATE_UP) {
-                        tma_load_2d_if(issue, sw + BM * BOX, &maps.b2, fb, kb * BOX, wrow, policy);
-                        tma_load_2d_if(issue, ss + 4 * SCALE_TILE, &maps.sfb2, fb, kb * 256, wrow / BM, policy);
-                    }
-                    tma_load_2d_if(issue, sx, small ? &maps.a_small : &maps.a, fb, kb * BOX, xrow, policy);
-                    tma_load_2d_if(issue, ss, &maps.sfa, fb, kb * 256, bx, policy);
-                    ++issued;
-                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+        const uint32_t issue = elect_one();
+        const uint64_t policy = l2_policy_evict_normal();
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+            const FewTile ti = tile(t);
+            const int32_t wrow = uniform(ti.e) * p.n + uniform(ti.n) * BM;
+            const int32_t xrow = uniform(ti.bx) * BM + uniform(ti.first), bx = uniform(ti.bx);
+            const bool small = uniform(ti.rows) <= SMALL_ROWS;
+            const uint32_t bytes = F::W_BYTES + (small ? SMALL_ROWS : FEW_ROWS) * BOX + (F::ACCS + 1) * 2 * SCALE_TILE;
+            for (int32_t kb = 0; kb < k_steps; ++kb) {
+                if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t fb = bar_full + 8 * stage;
+                const uint32_t sw = sbase + stage * F::STAGE;
+                const uint32_t sx = sw + F::W_BYTES;
+                const uint32_t ss = sx + F::X_BYTES;
+                mbar_arrive_expect_tx_if(issue, fb, bytes);
+                tma_load_2d_if(issue, sw, &maps.b, fb, kb * BOX, wrow, policy);
+                tma_load_2d_if(issue, ss + 2 * SCALE_TILE, &maps.sfb, fb, kb * 256, wrow / BM, policy);
+                if (FORM == MX4_GATE_UP) {
+                    tma_load_2d_if(issue, sw + BM * BOX, &maps.b2, fb, kb * BOX, wrow, policy);
+                    tma_load_2d_if(issue, ss + 4 * SCALE_TILE, &maps.sfb2, fb, kb * 256, wrow / BM, policy);
+                }
+                tma_load_2d_if(issue, sx, small ? &maps.a_small : &maps.a, fb, kb * BOX, xrow, policy);
+                tma_load_2d_if(issue, ss, &maps.sfa, fb, kb * 256, bx, policy);
+                ++issued;
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
-            if (!ok && lane == 0) {
-                // Let the copies already in flight land before the CTA exits.
-                volatile int never = 0;
-                const int64_t n = issued < stages ? issued : stages;
-                for (int64_t i = 0; i < n; ++i) {
-                    const int64_t idx = issued - 1 - i;
-                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
-                                      static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
-                }
+        }
+        if (!ok && lane == 0) {
+            // Let the copies already in flight land before the CTA exits.
+            volatile int never = 0;
+            const int64_t n = issued < stages ? issued : stages;
+            for (int64_t i = 0; i < n; ++i) {
+                const int64_t idx = issued - 1 - i;
+                mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
+                                  static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
             }
         }
         __syncwarp();

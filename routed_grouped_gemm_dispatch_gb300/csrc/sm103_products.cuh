@@ -92,6 +92,17 @@ __device__ __forceinline__ void tc_mma_f16_pair_if(uint32_t issue, uint32_t d_tm
         : "memory");
 }
 
+__device__ __forceinline__ void tc_mma_f16_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
 __device__ __forceinline__ void tc_commit_pair_mc_if(uint32_t issue, uint32_t bar, uint16_t cta_mask) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
