@@ -423,6 +423,15 @@ def _ffn_sizes(x, gate_w, up_w, down_w):
     """The block's type code and sizes, with every array checked."""
     dt = getattr(x, "dtype", None)
     code = _dtype_code(dt, "x")
+    # the common case in one expression; the checks below name what is wrong
+    if x.is_cuda and x.dim() == 2 and x.is_contiguous() and getattr(gate_w, "is_cuda", False) and gate_w.dim() == 2:
+        T, H = x.shape
+        I = gate_w.shape[0]
+        if (gate_w.dtype is dt and gate_w.shape == (I, H) and gate_w.is_contiguous()
+                and getattr(up_w, "is_cuda", False) and up_w.dtype is dt and up_w.shape == (I, H)
+                and up_w.is_contiguous() and getattr(down_w, "is_cuda", False) and down_w.dtype is dt
+                and down_w.shape == (H, I) and down_w.is_contiguous()):
+            return code, dt, T, H, I
     T, H = _dev(x, "x", dt, 2).shape
     I = _dev(gate_w, "gate_w", dt, 2).shape[0]
     _shaped(gate_w, "gate_w", dt, (I, H))

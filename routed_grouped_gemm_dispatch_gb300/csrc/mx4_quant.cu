@@ -111,7 +111,7 @@ __device__ __forceinline__ uint32_t max_exponent(const Eight<DTYPE>& e) {
 // runs along y.  Without row lists (LISTS), rows n_rows .. pad_rows - 1 (the
 // rest of the last scale tile) get zero scales.
 template <int DTYPE, bool LISTS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 6)
 quantize_kernel(const Mx4Quantize a, int64_t pad_rows) {
     pdl_wait_prior_grid();
     pdl_launch_dependents();
