@@ -24,6 +24,12 @@
 //    the other one into 16-bit rows meanwhile.  With 128 x 256 tiles on one SM
 //    the operands' way into and out of shared memory, not the tensor core, is
 //    the bound; the pair halves the bytes of B each SM moves.
+//  * Launches with few tiles share a tile's K axis among two to four pairs of a
+//    cluster: each pair computes its part, sends the columns that others finish
+//    to them through distributed shared memory, and adds what it receives in
+//    pair order.  300 tokens, 7168 / 2048: 59.7 -> 46.6 us when it came.
+//  * Copies and MMAs are issued by converged warps (warp 0 and warp 1): from a
+//    one-lane branch the copies alone held a stage up.
 //  * Rows past T, columns past H or I and the end of K are zeros that TMA fills
 //    in: no size needs padding, only whole 16-byte rows (H and I multiples of 8).
 //  * First forward launch: a tile is 128 columns of gate (held by the even CTA)
@@ -31,6 +37,12 @@
 //    one pass over x, and h is formed in registers from the fp32 accumulators.
 //  * First backward launch: d_h stays in TMEM; the epilogue reads G and U of the
 //    tile and writes d_G and d_U.
+//
+// Measured (GPU time, bf16): forward of 8192 tokens, 7168 / 2048, 387 us = 1.86
+// PFLOP/s, its gradients 793 us = 1.82; training forward of 4097 tokens, 2048 /
+// 2816, 88 us = 1.6 (tensor pipe active 81% in gate and up, 76% in down).  Bound:
+// the tensor pipe for many tokens (back to back, the power cap), the chain of
+// fill, K loop, join and epilogue for few hundred.
 //
 // Roundings to 16 bits: h, y and every gradient once from fp32; G and U when the
 // caller stores them for the backward (half the bytes of fp32 and the type the

@@ -16,7 +16,8 @@
 // hardware's conversion rounds two values at a time.  Four lanes share a block,
 // 8 values each: the loads are 16 bytes a lane and consecutive across the warp,
 // two shuffles give the block's maximum, and a lane's 8 codes are one 4-byte
-// store.
+// store.  16384 x 7168: bf16 to 4 bits 53 us (5.6 TB/s, instructions 70% busy), fp32
+// 78 us (6.8 TB/s), 4 bits to bf16 48 us (6.2 TB/s), to fp32 86 us (6.2 TB/s).
 #include <cuda_runtime.h>
 
 #include <cstdint>
