@@ -121,7 +121,7 @@ struct Plan {
     int32_t split_tiles;           // the first so many tiles are shared by a cluster's pairs
     int32_t lead;                  // tiles a pair without a shared one does before the others join
     int32_t n_maps;
-    int32_t early_weights;         // B of problem 0 is no result of the launch before: see the producer
+    int32_t early_weights;         // no B is a result of the launch before: see the producer
     int32_t tile_cols;             // output columns of a tile: 128 (gate and up side by side) or 256
     const uint16_t* gate_in;       // EPI_GRAD: stored G, U [m, n]
     const uint16_t* up_in;
@@ -226,6 +226,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     if (!p.early_weights) {
         pdl_wait_prior_grid();
         pdl_launch_dependents();
+    } else if (warp != 0) {
+        pdl_wait_prior_grid();     // no bounded wait runs while the launch before still works
     }
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross

@@ -186,6 +186,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
         __syncwarp();
     } else if (warp == 1) {
         // ===================== MMA issuer =====================
+        pdl_wait_prior_grid();     // no bounded wait runs while the launch before still works
         const uint32_t issue = elect_one();
         const uint32_t idesc = idesc_16bit_f32acc(BM, static_cast<uint32_t>(p.np), BF16, false, false);
         int32_t stage = 0;
@@ -206,6 +207,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     } else {
         // ===================== partial sums to shared memory =====================
         // after the last MMA the ring is free: [token][weight row] in fp32
+        pdl_wait_prior_grid();
         if (mbar_wait_bounded(bar_done, 0, abort_flag, WAIT_LIMIT_NS)) {
             tc_fence_after_sync();
             const int row = (warp & 3) * 32 + lane;
