@@ -5,8 +5,8 @@
 //     y = h·down_wᵀ                                              second launch
 // Backward, from d_y and the stored G, U, h, with s = sigmoid(G):
 //     d_h = d_y·down_w (fp32), d_U = d_h·G·s, d_G = d_h·U·s·(1 + G·(1 − s))   first launch
-//     d_x = d_G·gate_w + d_U·up_w;  d_gate_w = d_Gᵀ·x;  d_up_w = d_Uᵀ·x;
-//     d_down_w = d_yᵀ·h                                          second launch
+//     d_x = d_G·gate_w + d_U·up_w;  d_gate_w = d_Gᵀ·x;  d_up_w = d_Uᵀ·x        second launch
+//     d_down_w = d_yᵀ·h             with whichever launch leaves pairs idle
 //
 // One kernel serves them all: C[m, n] = Σ_k A[m, k]·B[n, k] over up to four
 // problems a launch, each with its own extents, operands and order of operands:
@@ -14,8 +14,8 @@
 // weights as B) or M/N-major (M or N contiguous: the transposed ones), which
 // the tensor cores read from shared memory as TMA leaves it, so nothing is ever
 // transposed in memory.  d_x sums over two K segments (gate, then up) in one
-// accumulator, and the four products of the backward's second half share one
-// launch, so that its last wave is one and not four.
+// accumulator, and the products of the backward's second half share one
+// launch, so that its last wave is one and not one each.
 //
 //  * Persistent clusters of two CTAs, one 2-SM MMA tile of M = 256 x N = 256 at
 //    a time: each CTA holds 128 rows of A and 128 of B per stage (K = 64, 32 KB,
@@ -77,9 +77,10 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int PAIR = 2;                        // CTAs of one MMA tile
 constexpr int MAX_SPLIT = 4;                   // pairs that may share a tile's K axis
 constexpr int MIN_STEPS = 384 / BK;            // stages each of them keeps at least
-constexpr int MIN_TILE_STEPS = 512 / BK;       // stages' worth of time that a tile's epilogue takes
+constexpr int MIN_TILE_STEPS = 448 / BK;       // stages' worth of time that a tile takes at least (its epilogue)
 constexpr float JOIN_STEPS = 512.0f / BK;             // time to join a shared tile (about 2.5 us), in stages
 constexpr float JOIN_STEPS_AHEAD = 1536.0f / BK;      // the same ahead of unshared tiles, whose loads have to wait for it
+constexpr float SHARED_STEPS = 1280.0f / BK;          // first data, join and epilogue of a shared tile
 constexpr int GROUP_M = 8;                     // tile rows (of 256) that are walked together
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
@@ -380,6 +381,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     uint4 eg[EPI == EPI_GRAD ? 8 : 1], eu[EPI == EPI_GRAD ? 8 : 1];
     auto ask_gate_up = [&](const Tile& ti, bool shared) {
         if constexpr (EPI == EPI_GRAD) {
+            if (ti.q != 0) return;
             const Problem& pr = p.pr[ti.q];
             const Rows r = rows_of(ti);
             const int c = (SPLIT && shared ? first_pass(static_cast<int>(pair)) : 0) + odd;
@@ -402,7 +404,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             const int64_t at = r.at + c * 64;
             // this pass's first quad of the partial sums
             const uint8_t* part = smem + (c - c0) * PASS_BYTES + row * 16;
-            if (EPI == EPI_STORE) {
+            if (EPI == EPI_STORE || (EPI == EPI_GRAD && ti.q != 0)) {
                 uint4 el[8];
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
@@ -461,7 +463,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float x = __uint_as_float(g[j]);
-                        g[j] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u[j]));
+                        g[j] = __float_as_uint(x * sigmoid_approx(x) * __uint_as_float(u[j]));
                     }
                     round32(g, hh);
                 }
@@ -490,8 +492,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                             const float2 u = unpack_16bit2<BF16>(pu[j]);
                             const float d0 = __uint_as_float(d[8 * k + 2 * j]);
                             const float d1 = __uint_as_float(d[8 * k + 2 * j + 1]);
-                            const float s0 = __fdividef(1.0f, 1.0f + __expf(-g.x));
-                            const float s1 = __fdividef(1.0f, 1.0f + __expf(-g.y));
+                            const float s0 = sigmoid_approx(g.x);
+                            const float s1 = sigmoid_approx(g.y);
                             pg[j] = pack_16bit2<BF16>(d0 * u.x * s0 * (1.0f + g.x * (1.0f - s0)),
                                                       d1 * u.y * s1 * (1.0f + g.y * (1.0f - s1)));
                             pu[j] = pack_16bit2<BF16>(d0 * g.x * s0, d1 * g.y * s1);
@@ -674,8 +676,9 @@ cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
     // ones at steps / split each and JOIN_STEPS for joining them.  Of a launch of
     // one problem the tiles that do not fill a round are shared (all of them
     // where there is no full round); of several, the first problem's if they are
-    // one round at most.  Splitting also leaves SMs without a cluster: 144, 138
-    // and 120 of 152 are in one of 4, 6 and 8 CTAs.
+    // one round at most, while the pairs left over work on the other problems'.
+    // Splitting also leaves SMs without a cluster: 144, 138 and 120 of 152 are in
+    // one of 4, 6 and 8 CTAs.
     const int32_t tiles = p.pr[0].m_tiles * p.pr[0].n_tiles;
     const int32_t steps = p.pr[0].steps[0] + p.pr[0].steps[1];
     const Resident* r = resident<EPI, BF16>();
@@ -684,36 +687,44 @@ cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
     int nc = r->clusters[1];
     p.split = 1;
     p.split_tiles = 0;
-    float best = static_cast<float>((tiles + nc - 1) / nc * steps);
+    const bool several = p.n_problems > 1;
+    const int32_t others = p.total_tiles - tiles;
+    const int32_t own = several && p.pr[1].steps[0] > MIN_TILE_STEPS ? p.pr[1].steps[0] : MIN_TILE_STEPS;
+    auto rounds = [](int32_t n, int32_t per_round) { return static_cast<float>((n + per_round - 1) / per_round); };
+    float best = rounds(tiles, nc) * static_cast<float>(steps);
+    if (several) {
+        const float work = (static_cast<float>(tiles) * steps + static_cast<float>(others) * own) / nc;
+        const float longest = 1.25f * static_cast<float>(steps);     // one pair's K loop beside the others' stores
+        best = (work > longest ? work : longest) + SHARED_STEPS;
+    }
     for (int split = 2; split <= MAX_SPLIT; ++split) {
         // (three pairs would leave one of them without a part of gate and up to finish)
         if (steps < MIN_STEPS * split || (EPI == EPI_GATE_UP && split == 3)) continue;
         const int n = r->clusters[split];
-        const int32_t full = p.n_problems == 1 ? tiles / (n * split) : 0;
+        const float part = static_cast<float>(steps) / static_cast<float>(split);
+        const int32_t full = several ? 0 : tiles / (n * split);
         const int32_t rest = tiles - full * n * split;
-        if (p.n_problems > 1 && rest > n) continue;
-        const float t = static_cast<float>(full * steps) +
-                        static_cast<float>((rest + n - 1) / n) *
-                            (static_cast<float>(steps) / static_cast<float>(split) +
-                             (full > 0 ? JOIN_STEPS_AHEAD : JOIN_STEPS));
-        if (rest > 0 && t < best) {
+        if (rest == 0 || (several && rest > n)) continue;
+        float t = static_cast<float>(full * steps) + rounds(rest, n) * (part + (full > 0 ? JOIN_STEPS_AHEAD : JOIN_STEPS));
+        int32_t lead = 0;
+        if (several) {
+            // meanwhile the other clusters' pairs are `lead` tiles ahead
+            const int32_t idle = (n - rest) * split;
+            lead = static_cast<int32_t>((part + SHARED_STEPS) / static_cast<float>(own));
+            if (idle > 0 && lead > others / idle) lead = others / idle;
+            t = part + SHARED_STEPS + rounds(others - lead * idle, n * split) * static_cast<float>(own);
+        }
+        if (t < best) {
             best = t;
             p.split = split;
             p.split_tiles = rest;
+            p.lead = lead;
             nc = n;
         }
     }
-    if (p.split_tiles > 0 && p.split_tiles < nc && p.n_problems > 1) {
-        // while the shared tiles run, the other clusters' pairs are this many tiles ahead
-        const float own_steps = static_cast<float>(p.pr[1].steps[0] > MIN_TILE_STEPS ? p.pr[1].steps[0] : MIN_TILE_STEPS);
-        p.lead = static_cast<int32_t>((static_cast<float>(steps) / static_cast<float>(p.split) + JOIN_STEPS) / own_steps);
-        const int32_t idle = (nc - p.split_tiles) * p.split;
-        const int32_t most = (p.total_tiles - p.split_tiles) / idle;
-        if (p.lead > most) p.lead = most;
-    }
     // clusters that have work: a shared tile each, or a tile for each of their pairs
-    const int32_t own = (p.total_tiles - p.split_tiles + p.split - 1) / p.split;
-    const int32_t want = own > p.split_tiles ? own : p.split_tiles;
+    const int32_t unshared = (p.total_tiles - p.split_tiles + p.split - 1) / p.split;
+    const int32_t want = unshared > p.split_tiles ? unshared : p.split_tiles;
     if (nc > want) nc = want;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -815,6 +826,26 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     Problem& dh = add_problem(p, nullptr, T, I, BN);
     set_operands(dh, 0, H, DY, DOWN_T, DOWN_T);
     dh.b_mn = 1;
+    // d_down needs nothing of either launch.  The first takes it where d_h has more
+    // than a round of tiles, of which the last leaves pairs idle, and a tile of
+    // d_down is neither shorter than its stores nor longer than one of d_h (2048 /
+    // 2816: 1024 tokens 70.6 -> 66.2 us, 2048 tokens 109.8 -> 101.8).  Elsewhere the
+    // second launch's first pairs start, with their weights, where d_h leaves room
+    // (400 tokens, 768 / 2048: 31 us, 35 with d_down in the first; 1200: 42.6, 46.3;
+    // 128 tokens, 4096 / 14336: 169, 177).
+    const Resident* r = a.bf16 ? resident<EPI_GRAD, true>() : resident<EPI_GRAD, false>();
+    if (!r) return cudaErrorNoDevice;
+    if (r->err != cudaSuccess) return r->err;
+    const int32_t dh_steps = dh.steps[0], dd_steps = ceil_div(T, BK);
+    const bool down_first = dh.m_tiles * dh.n_tiles > r->clusters[2] && dd_steps >= MIN_TILE_STEPS &&
+                            dd_steps <= dh_steps + dh_steps / 4;
+    auto weight_gradient = [&](Plan& plan, uint16_t* dst, int32_t m, int32_t n, int a_map, int b_map) {
+        Problem& pr = add_problem(plan, dst, m, n, BN);
+        set_operands(pr, 0, T, a_map, b_map, b_map);
+        pr.a_mn = 1;
+        pr.b_mn = 1;
+    };
+    if (down_first) weight_gradient(p, a.d_down_w, H, I, DY_T, H_T);
     p.n_maps = MAPS;
     p.gate_in = a.gate;
     p.up_in = a.up;
@@ -832,14 +863,9 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     set_operands(dx, 0, I, DG, GATE_T, GATE_T);
     set_operands(dx, 1, I, DU, UP_T, UP_T);
     dx.b_mn = 1;
-    struct { uint16_t* dst; int32_t m, n; int a, b; } w[3] = {
-        {a.d_gate_w, I, H, DG_T, X_T}, {a.d_up_w, I, H, DU_T, X_T}, {a.d_down_w, H, I, DY_T, H_T}};
-    for (const auto& d : w) {
-        Problem& pr = add_problem(q, d.dst, d.m, d.n, BN);
-        set_operands(pr, 0, T, d.a, d.b, d.b);
-        pr.a_mn = 1;
-        pr.b_mn = 1;
-    }
+    weight_gradient(q, a.d_gate_w, I, H, DG_T, X_T);
+    weight_gradient(q, a.d_up_w, I, H, DU_T, X_T);
+    if (!down_first) weight_gradient(q, a.d_down_w, H, I, DY_T, H_T);
     return launch<EPI_STORE>(a.bf16, maps, q, stream);
 }
 

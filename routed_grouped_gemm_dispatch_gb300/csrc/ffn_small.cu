@@ -270,10 +270,10 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
                     put(p.dst_gate, a);
                     put(p.dst_up, b);
                 }
-                a.x = __fdividef(a.x, 1.0f + __expf(-a.x)) * b.x;
-                a.y = __fdividef(a.y, 1.0f + __expf(-a.y)) * b.y;
-                a.z = __fdividef(a.z, 1.0f + __expf(-a.z)) * b.z;
-                a.w = __fdividef(a.w, 1.0f + __expf(-a.w)) * b.w;
+                a.x *= sigmoid_approx(a.x) * b.x;
+                a.y *= sigmoid_approx(a.y) * b.y;
+                a.z *= sigmoid_approx(a.z) * b.z;
+                a.w *= sigmoid_approx(a.w) * b.w;
             }
             put(p.dst, a);
         }

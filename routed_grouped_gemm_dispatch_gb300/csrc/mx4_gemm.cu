@@ -485,7 +485,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float f = __uint_as_float(g[k >> 2][8 * (k & 3) + j]);
-                        x[j] = __float_as_uint(__fdividef(f, 1.0f + __expf(-f)) *
+                        x[j] = __float_as_uint(f * sigmoid_approx(f) *
                                                __uint_as_float(u[k >> 2][8 * (k & 3) + j]));
                     }
                     el[k] = piece(x);
@@ -778,7 +778,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                 for (int j = 0; j < 8; ++j) {
                     if (r0 + j >= ti.rows) break;
                     float x = __uint_as_float(v[j]);
-                    if (FORM == MX4_GATE_UP) x = __fdividef(x, 1.0f + __expf(-x)) * __uint_as_float(u[j]);
+                    if (FORM == MX4_GATE_UP) x = x * sigmoid_approx(x) * __uint_as_float(u[j]);
                     if (FORM == MX4_DOWN) x *= __ldg(rw + r0 + j);
                     dst[static_cast<int64_t>(r0 + j) * p.n] = static_cast<uint16_t>(pack_16bit2<BF16>(x, 0.0f) & 0xffffu);
                 }

@@ -30,6 +30,16 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// 1 / (1 + 2^(-x log2 e)): two approximate instructions (2 ulp together) that flush
+// subnormals, which spares the compiler's range handling around each (4-bit gate_up of 4096
+// tokens, top-6 of 64: 69.2 -> 67.3 us; gradients of 2048 tokens: 109.5 -> 107.0).
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
+
 // Ask for a box's lines to be brought into L2.  A hint that moves no data to the
 // SM: safe before the kernels that may still write the array have finished.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
