@@ -93,6 +93,7 @@ constexpr int OFF_TMEM_SLOT = OFF_BARS + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
 constexpr int SMEM_BYTES = 1024 + OFF_ABORT + 4;
 
+constexpr int SMALL_ROWS = 32;                 // boxes of a K-major A that has no more rows
 constexpr int MAX_MAPS = 12;
 constexpr int MAX_PROBLEMS = 4;
 
@@ -123,6 +124,7 @@ struct Plan {
     int32_t lead;                  // tiles a pair without a shared one does before the others join
     int32_t n_maps;
     int32_t early_weights;         // no B is a result of the launch before: see the producer
+    int32_t a_box_bytes;           // of a K-major A
     int32_t tile_cols;             // output columns of a tile: 128 (gate and up side by side) or 256
     const uint16_t* gate_in;       // EPI_GRAD: stored G, U [m, n]
     const uint16_t* up_in;
@@ -258,6 +260,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const int32_t brow = EPI == EPI_GATE_UP ? ti.n * BM : ti.n * BN + static_cast<int32_t>(rank) * BM;
         const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
         const int32_t steps0 = pr.steps[0];
+        const uint32_t bytes = PAIR * (OP_BYTES + (a_mn ? OP_BYTES : static_cast<uint32_t>(p.a_box_bytes)));
         auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t fb, bool mn, int32_t row, int32_t k0) {
             if (mn) {
 #pragma unroll
@@ -277,7 +280,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             have_b = s1 - s0 < STAGES ? s1 - s0 : STAGES;
             have_b = s0 + have_b <= steps0 ? have_b : (s0 < steps0 ? steps0 - s0 : 0);   // of the first K segment
             for (int32_t i = 0; i < have_b; ++i) {
-                mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * i, PAIR * STAGE_BYTES);
+                mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * i, bytes);
                 load(&maps.m[pr.b_map[0][rank]], sbase + i * STAGE_BYTES + OP_BYTES, leader_full + 8 * i, b_mn, brow,
                      (s0 + i) * BK);
             }
@@ -300,7 +303,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
                 const uint32_t fb = leader_full + 8 * stage;
                 const uint32_t sa = sbase + stage * STAGE_BYTES;
                 if (have_b == 0) {
-                    mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * stage, PAIR * STAGE_BYTES);
+                    mbar_arrive_expect_tx_if(leader_issue, bar_full + 8 * stage, bytes);
                     load(bm, sa + OP_BYTES, fb, b_mn, brow, k0);
                 } else {
                     --have_b;
@@ -772,10 +775,16 @@ void set_operands(Problem& pr, int seg, int64_t k, int a, int b_even, int b_odd)
     pr.b_map[seg][1] = static_cast<int8_t>(b_odd);
 }
 
+// Rows of a K-major A's boxes.  Of an array of few rows a box of 128 lies mostly
+// outside, which TMA is slow at: gradients of one token, 2048 / 2816, 48.5 -> 33.5
+// us, of 16 tokens 44 -> 34.  (The other rows' sums are never read.)
+int a_box_rows(int64_t tokens) { return tokens <= SMALL_ROWS ? SMALL_ROWS : BM; }
+
 // Boxes of 64 columns: 128 rows of a K-major operand, or BK rows of K of an
 // M/N-major one.
-bool box_map(Maps& maps, int i, const void* base, int64_t rows, int64_t cols, bool mn = false) {
-    return tensor_map_2d(&maps.m[i], base, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), 2, mn ? BK : BM);
+bool box_map(Maps& maps, int i, const void* base, int64_t rows, int64_t cols, int box_rows = BM) {
+    return tensor_map_2d(&maps.m[i], base, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), 2,
+                         static_cast<uint32_t>(box_rows));
 }
 
 }  // namespace
@@ -792,6 +801,7 @@ cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream) {
     Problem& gu = add_problem(p, a.up_logits, T, I, BM);
     set_operands(gu, 0, H, 0, 1, 2);
     p.n_maps = 3;
+    p.a_box_bytes = BM * 128;
     p.dst_gate = a.gate;
     p.dst_up = a.up;
     p.status = a.status;
@@ -803,6 +813,7 @@ cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream) {
     Problem& dn = add_problem(p2, a.out, T, H, BN);
     set_operands(dn, 0, I, 0, 1, 1);
     p2.n_maps = 2;
+    p2.a_box_bytes = BM * 128;
     p2.early_weights = 1;
     p2.status = a.status;
     return launch<EPI_STORE>(a.bf16, maps, p2, stream);
@@ -816,11 +827,13 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     // K-major operands, then M/N-major ones
     enum { DY, DG, DU, DOWN_T, GATE_T, UP_T, X_T, H_T, DY_T, DG_T, DU_T, MAPS };
     static_assert(MAPS <= MAX_MAPS, "maps fit");
-    if (!box_map(maps, DY, a.d_out, T, H) || !box_map(maps, DG, a.d_gate, T, I) || !box_map(maps, DU, a.d_up, T, I) ||
-        !box_map(maps, DOWN_T, a.down_w, H, I, true) || !box_map(maps, GATE_T, a.gate_w, I, H, true) ||
-        !box_map(maps, UP_T, a.up_w, I, H, true) || !box_map(maps, X_T, a.x, T, H, true) ||
-        !box_map(maps, H_T, a.up_logits, T, I, true) || !box_map(maps, DY_T, a.d_out, T, H, true) ||
-        !box_map(maps, DG_T, a.d_gate, T, I, true) || !box_map(maps, DU_T, a.d_up, T, I, true))
+    const int a_rows = a_box_rows(T);
+    if (!box_map(maps, DY, a.d_out, T, H, a_rows) || !box_map(maps, DG, a.d_gate, T, I, a_rows) ||
+        !box_map(maps, DU, a.d_up, T, I, a_rows) ||
+        !box_map(maps, DOWN_T, a.down_w, H, I, BK) || !box_map(maps, GATE_T, a.gate_w, I, H, BK) ||
+        !box_map(maps, UP_T, a.up_w, I, H, BK) || !box_map(maps, X_T, a.x, T, H, BK) ||
+        !box_map(maps, H_T, a.up_logits, T, I, BK) || !box_map(maps, DY_T, a.d_out, T, H, BK) ||
+        !box_map(maps, DG_T, a.d_gate, T, I, BK) || !box_map(maps, DU_T, a.d_up, T, I, BK))
         return cudaErrorInvalidValue;
     Plan p{};
     Problem& dh = add_problem(p, nullptr, T, I, BN);
@@ -847,6 +860,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     };
     if (down_first) weight_gradient(p, a.d_down_w, H, I, DY_T, H_T);
     p.n_maps = MAPS;
+    p.a_box_bytes = a_rows * 128;
     p.gate_in = a.gate;
     p.up_in = a.up;
     p.dst_gate = a.d_gate;
@@ -858,6 +872,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream) {
     Plan q{};
     q.status = a.status;
     q.n_maps = MAPS;
+    q.a_box_bytes = a_rows * 128;
     q.early_weights = 1;
     Problem& dx = add_problem(q, a.d_x, T, H, BN);
     set_operands(dx, 0, I, DG, GATE_T, GATE_T);
