@@ -110,6 +110,7 @@ struct Params {
     int32_t n_tiles;
     int32_t k_tiles;                            // K / 128
     int32_t stages;
+    int32_t split;                              // few rows: CTAs that share a tile
 };
 
 // Rows of block bx that hold data, its expert and the row's place inside the
@@ -539,9 +540,18 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 // consecutive bytes of a row at a time.  32 tokens, top-8 of 128 experts, 2048 / 768:
 // 33.6 us on the pair kernel, 23 here (116 MB from memory; the unit list and the
 // first fill take about 4 of them).
+//
+// SPLIT (a plain product with fewer tiles than SMs): a cluster of CTAs shares a
+// tile, each with its part of the K axis.  They exchange fp32 sums through
+// distributed shared memory, in the rings that the MMAs have emptied; groups of
+// 16 rows go around the CTAs, and an owner adds the parts in rank order.  The
+// join costs about 1 us: one row, K 7168 / N 1408 8.9 -> 5.5 us, 7168 / 4096 9.6 ->
+// 8.3, 4096 / 2048 6.0 -> 5.0, but K 2048 / N 4096 4.5 -> 5.1: from K = 4096 on.
 constexpr int FEW_ROWS = 64;                    // rows of a block per unit
 constexpr int FEW_THREADS = 320;                // producer, MMA and eight epilogue warps
 constexpr int FEW_MAX_STAGES = 8;
+constexpr int FEW_MAX_SPLIT = 4;                // CTAs that share a tile
+constexpr int FEW_SPLIT_STEPS = 16;             // K / 256 from which they do
 constexpr int FEW_OFF_TMEM_SLOT = (2 * FEW_MAX_STAGES + 5) * 8;   // full, empty; tfull, tempty [2]; drain
 constexpr int FEW_OFF_ABORT = FEW_OFF_TMEM_SLOT + 4;
 constexpr int FEW_OFF_WSUM = FEW_OFF_ABORT + 4;
@@ -559,7 +569,11 @@ struct Few {
     static_assert(TMEM_SCALE0 + FEW_MAX_STAGES * SCALE_COLS <= TMEM_COLS, "scales fit in TMEM");
 };
 
-template <int FORM, bool BF16>
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+template <int FORM, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
 mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
     using F = Few<FORM>;
@@ -633,6 +647,12 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     const int32_t total_tiles = __shfl_sync(0xffffffffu, num_units * p.n_tiles, 0);
     const int32_t k_steps = (p.k_tiles + 1) / 2;
+    // this CTA's tiles and its part of their K axis (SPLIT: one tile per cluster)
+    const int32_t split = SPLIT ? p.split : 1;
+    const int32_t crank = SPLIT ? static_cast<int32_t>(cluster_cta_rank()) : 0;
+    const int32_t kb0 = k_steps * crank / split, kb1 = k_steps * (crank + 1) / split;
+    const int32_t t0 = static_cast<int32_t>(blockIdx.x) / split;
+    const int32_t t_step = static_cast<int32_t>(gridDim.x) / split;
 
     // A unit's weight slices follow one another, so its few rows stay in L2.
     struct FewTile {
@@ -657,13 +677,13 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         uint32_t stage = 0, phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+        for (int32_t t = t0; t < total_tiles && ok; t += t_step) {
             const FewTile ti = tile(t);
             const int32_t wrow = uniform(ti.e) * p.n + uniform(ti.n) * BM;
             const int32_t xrow = uniform(ti.bx) * BM + uniform(ti.first), bx = uniform(ti.bx);
             const bool small = uniform(ti.rows) <= SMALL_ROWS;
             const uint32_t bytes = F::W_BYTES + (small ? SMALL_ROWS : FEW_ROWS) * BOX + (F::ACCS + 1) * 2 * SCALE_TILE;
-            for (int32_t kb = 0; kb < k_steps; ++kb) {
+            for (int32_t kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_warp(bar_empty + 8 * stage, phase ^ 1u, abort_flag, WAIT_LIMIT_NS)) {
                     ok = false;
                     break;
@@ -696,19 +716,23 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
             }
         }
         __syncwarp();
+        if (SPLIT) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
     } else if (warp == 1) {
         // ===================== MMA issuer =====================
         const uint32_t issue = elect_one();
         uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
         bool ok = true;
-        for (int32_t t = blockIdx.x; t < total_tiles && ok; t += gridDim.x) {
+        for (int32_t t = t0; t < total_tiles && ok; t += t_step) {
             const FewTile ti = tile(t);
             const uint32_t n = __shfl_sync(0xffffffffu, static_cast<uint32_t>((ti.rows + 15) & ~15), 0);
             const uint32_t first = __shfl_sync(0xffffffffu, static_cast<uint32_t>(ti.first), 0);
             if (!mbar_wait_warp(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + acc * F::ACCS * FEW_ROWS;
-            for (int32_t kb = 0; kb < k_steps; ++kb) {
+            for (int32_t kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                     ok = false;
                     break;
@@ -733,7 +757,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                         for (int a = 0; a < F::ACCS; ++a)
                             tc_mma_mxf4(issue, d + a * FEW_ROWS, dw + a * (BM * BOX >> 4) + (2 * i + j) * 2,
                                         dx + (2 * i + j) * 2, idesc_mxf4(BM, n, j), ts + 4 * (a + 1), ts + first / 32,
-                                        (kb | i | j) != 0 ? 1u : 0u);
+                                        ((kb - kb0) | i | j) != 0 ? 1u : 0u);
                 }
                 tc_commit_if(issue, bar_empty + 8 * stage);
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -750,6 +774,10 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
             mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
         }
         __syncwarp();
+        if (SPLIT) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
     } else {
         // ===================== epilogue (warps 2..9) =====================
         // of the two warps with the same columns one takes the even groups of
@@ -757,7 +785,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int quarter = warp & 3;
         const int odd = warp >= 6 ? 1 : 0;
         uint32_t acc = 0, aphase = 0;
-        for (int32_t t = blockIdx.x; t < total_tiles; t += gridDim.x) {
+        for (int32_t t = t0; t < total_tiles; t += t_step) {
             const FewTile ti = tile(t);
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * F::ACCS * FEW_ROWS;
@@ -766,14 +794,46 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
             uint16_t* dst = p.out + row0 * p.n + col;
             const float* rw = nullptr;
             if (FORM == MX4_DOWN) rw = p.weights + (static_cast<int64_t>(__ldg(p.offsets + ti.e)) + row0 - __ldg(p.padded + ti.e));
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS))) break;
+            const bool done =
+                __all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS)) != 0;
             tc_fence_after_sync();
+            if (SPLIT) {
+                // [rank that sends][row][column of 128] in the owner's ring
+                __syncwarp();
+                cluster_sync_all();                    // every ring of the cluster is free
+                const uint32_t slot = sbase + (crank * FEW_ROWS * BM + quarter * 32 + lane) * 4;
+#pragma unroll 1
+                for (int32_t r0 = odd * 8; r0 < ti.rows && done; r0 += 16) {
+                    const int32_t owner = (r0 >> 4) % split;
+                    if (owner == crank) continue;
+                    uint32_t v[8];
+                    tmem_ld_32x32b_x8(taddr + r0, v);
+                    tmem_ld_wait();
+                    const uint32_t at = mapa_shared(slot + r0 * BM * 4, static_cast<uint32_t>(owner));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) store_remote(at + j * BM * 4, v[j]);
+                }
+                __syncwarp();
+                cluster_sync_all();                    // the partial sums are there
+            }
+            if (!done) break;
 #pragma unroll 1
             for (int32_t r0 = odd * 8; r0 < ti.rows; r0 += 16) {
+                if (SPLIT && (r0 >> 4) % split != crank) continue;
                 uint32_t v[8], u[8];
                 tmem_ld_32x32b_x8(taddr + r0, v);
                 if (FORM == MX4_GATE_UP) tmem_ld_32x32b_x8(taddr + FEW_ROWS + r0, u);
                 tmem_ld_wait();
+                if (SPLIT) {
+                    float sum[8] = {};
+                    for (int32_t c = 0; c < split; ++c) {
+                        const float* from = reinterpret_cast<const float*>(smem) + (c * FEW_ROWS + r0) * BM + quarter * 32 + lane;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[j] += c == crank ? __uint_as_float(v[j]) : from[j * BM];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(sum[j]);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (r0 + j >= ti.rows) break;
@@ -866,6 +926,7 @@ cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
         std::once_flag once;
         cudaError_t err;
         int smem, sms;
+        int clusters[FEW_MAX_SPLIT + 1];       // that fit at once, by CTAs of one
     };
     static Limits limits[MAX_DEVICES];
     Limits& lim = limits[dev];
@@ -873,8 +934,27 @@ cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
         lim.err = cudaDeviceGetAttribute(&lim.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
         if (lim.err == cudaSuccess) lim.err = cudaDeviceGetAttribute(&lim.sms, cudaDevAttrMultiProcessorCount, dev);
         if (lim.err == cudaSuccess)
-            lim.err = cudaFuncSetAttribute(mx4_few_rows_kernel<FORM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           lim.smem);
+            lim.err = cudaFuncSetAttribute(mx4_few_rows_kernel<FORM, BF16, false>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, lim.smem);
+        if (FORM == MX4_MATMUL && lim.err == cudaSuccess) {
+            lim.err = cudaFuncSetAttribute(mx4_few_rows_kernel<FORM, BF16, FORM == MX4_MATMUL>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, lim.smem);
+            for (int split = 2; split <= FEW_MAX_SPLIT && lim.err == cudaSuccess; split *= 2) {
+                cudaLaunchAttribute size[1];
+                size[0].id = cudaLaunchAttributeClusterDimension;
+                size[0].val.clusterDim.x = static_cast<unsigned>(split);
+                size[0].val.clusterDim.y = 1;
+                size[0].val.clusterDim.z = 1;
+                cudaLaunchConfig_t probe{};
+                probe.gridDim = dim3(static_cast<unsigned>(split * 64));
+                probe.blockDim = dim3(FEW_THREADS);
+                probe.dynamicSmemBytes = static_cast<size_t>(lim.smem);
+                probe.attrs = size;
+                probe.numAttrs = 1;
+                lim.err = cudaOccupancyMaxActiveClusters(
+                    &lim.clusters[split], mx4_few_rows_kernel<FORM, BF16, FORM == MX4_MATMUL>, &probe);
+            }
+        }
     });
     if (lim.err != cudaSuccess) return lim.err;
     p.n_tiles = p.n / BM;
@@ -882,7 +962,7 @@ cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
     p.stages = (lim.smem - control) / Few<FORM>::STAGE;
     if (p.stages > FEW_MAX_STAGES) p.stages = FEW_MAX_STAGES;
     const int64_t tiles = 2 * static_cast<int64_t>(p.num_blocks) * p.n_tiles;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
@@ -892,7 +972,26 @@ cudaError_t launch_few_rows(const Maps& maps, Params& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx4_few_rows_kernel<FORM, BF16>, maps, p);
+    p.split = 1;
+    if constexpr (FORM == MX4_MATMUL) {
+        // a plain product's tiles are known here (one block, 64 rows a unit)
+        const int32_t k_steps = (p.k_tiles + 1) / 2;
+        const int64_t exact = p.num_blocks == 1 ? (p.rows > FEW_ROWS ? 2 : 1) * static_cast<int64_t>(p.n_tiles) : tiles;
+        for (int split = 2; split <= FEW_MAX_SPLIT; split *= 2)
+            if (exact <= lim.clusters[split] && k_steps >= FEW_SPLIT_STEPS &&
+                p.stages * Few<FORM>::STAGE >= split * FEW_ROWS * BM * 4)
+                p.split = split;
+        if (p.split > 1) {
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+            attr[1].val.clusterDim.y = 1;
+            attr[1].val.clusterDim.z = 1;
+            cfg.numAttrs = 2;
+            cfg.gridDim = dim3(static_cast<unsigned>(exact * p.split));
+            return cudaLaunchKernelEx(&cfg, mx4_few_rows_kernel<FORM, BF16, true>, maps, p);
+        }
+    }
+    return cudaLaunchKernelEx(&cfg, mx4_few_rows_kernel<FORM, BF16, false>, maps, p);
 }
 
 template <int FORM>

@@ -157,6 +157,15 @@ def test_matmul(rows, k, n, dt):
     assert torch.equal(again.view(torch.int16), out.contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("dt", OUT, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("rows,k,n", [(1, 3840, 128), (1, 4096, 128), (16, 4224, 640), (17, 4480, 256), (33, 6272, 384),
+                                      (64, 4096, 4736), (65, 7168, 256), (100, 4096, 1152), (128, 4224, 384),
+                                      (3, 4096, 4608), (2, 4096, 9856), (128, 4096, 2432)])
+def test_matmul_few_rows_long_k(rows, k, n, dt):
+    """Few rows against few weight slices: several blocks share a tile's K axis, unevenly too."""
+    test_matmul(rows, k, n, dt)
+
+
 def test_matmul_single_products():
     """One value a row: every pair of codes, at different places along K and scales, is exact."""
     k = 512
