@@ -165,6 +165,16 @@ def test_backward(T, H, I, dt):
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("T,H,I", [(520, 512, 3336), (1025, 904, 2056), (900, 640, 2560), (448, 384, 7176),
+                                   (33, 512, 1024), (32, 1032, 776), (24, 2048, 520), (400, 768, 2048),
+                                   (257, 4096, 520)])
+def test_backward_where_the_launches_differ(T, H, I, dt):
+    """More tiles of d_h than one shared round (d_down joins the first launch) or fewer; boxes of
+    few rows; pairs without a shared tile ahead of the others."""
+    test_backward(T, H, I, dt)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("T,H,I", [(5, 64, 72), (130, 72, 136)])
 def test_gradients_against_differences(T, H, I, dt):
     """Σ d_out ⊙ out in 64 bits, differenced along each gradient's own direction.
