@@ -38,11 +38,12 @@
 //  * First backward launch: d_h stays in TMEM; the epilogue reads G and U of the
 //    tile and writes d_G and d_U.
 //
-// Measured (GPU time, bf16): forward of 8192 tokens, 7168 / 2048, 387 us = 1.86
-// PFLOP/s, its gradients 793 us = 1.82; training forward of 4097 tokens, 2048 /
-// 2816, 88 us = 1.6 (tensor pipe active 81% in gate and up, 76% in down).  Bound:
-// the tensor pipe for many tokens (back to back, the power cap), the chain of
-// fill, K loop, join and epilogue for few hundred.
+// Measured (GPU time, bf16): forward of 8192 tokens, 7168 / 2048, 380 us = 1.90
+// PFLOP/s, its gradients 780 us = 1.85; training forward of 4097 tokens, 2048 /
+// 2816, 88 us = 1.6 (tensor pipe active 81% in gate and up, 76% in down);
+// gradients of 301 tokens, 45 us.  Bound: the tensor pipe and close behind it the
+// operands' way from L2 for many tokens (back to back, the power cap), the chain
+// of fill, K loop, join and epilogue for few hundred.
 //
 // Roundings to 16 bits: h, y and every gradient once from fp32; G and U when the
 // caller stores them for the backward (half the bytes of fp32 and the type the

@@ -33,9 +33,10 @@
 //    accumulator back before they round and store.
 //
 // Measured (GPU time): 4096 x 7168 x 4096 40.6 us = 5.9 PFLOP/s; routed gate_up of
-// 4096 tokens, top-6 of 64 experts, 2048 / 1408, 69 us = 4.1 PFLOP/s at 4.2 TB/s.  Bound:
-// about 700 cycles a stage of MMAs and scale copies (512 of MMAs alone), and
-// 600 between tiles while the accumulator changes hands.
+// 4096 tokens, top-6 of 64 experts, 2048 / 1408, 67 us = 4.2 PFLOP/s at 4.4 TB/s.  Bound:
+// the operands' way from L2 (with one MMA in sixteen 35 and 61 us: 48 bytes a cycle
+// and SM), under about 700 cycles a stage where the MMAs alone are 512, and 600
+// between tiles while the accumulator changes hands.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
