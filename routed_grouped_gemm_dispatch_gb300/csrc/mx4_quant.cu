@@ -109,8 +109,9 @@ __device__ __forceinline__ uint32_t max_exponent(const Eight<DTYPE>& e) {
 }
 
 // A warp takes one row's run of SEG * UNROLL values: rows along the grid's x,
-// runs along y.  Without row lists (LISTS), rows n_rows .. pad_rows - 1 (the
-// rest of the last scale tile) get zero scales.
+// runs along y.  Without destination rows, rows n_rows .. pad_rows - 1 (the rest
+// of the last scale tile) get zero scales; with them pad_rows is n_rows.  LISTS:
+// there is a list of source or of destination rows.
 template <int DTYPE, bool LISTS>
 __global__ void __launch_bounds__(THREADS, 6)
 quantize_kernel(const Mx4Quantize a, int64_t pad_rows) {
@@ -159,14 +160,14 @@ quantize_kernel(const Mx4Quantize a, int64_t pad_rows) {
             if ((lane & 15) == 0)
                 *reinterpret_cast<uint32_t*>(a.scales + scale_word(dst, c >> 7, k_tiles)) = given ? word : 0u;
         };
-        if constexpr (LISTS) {
+        if (LISTS && a.dest_rows) {
             for (int32_t j = 0; j < a.copies; ++j) {
-                const int64_t dst = a.dest_rows ? __ldg(a.dest_rows + row * a.copies + j) : row;
+                const int64_t dst = __ldg(a.dest_rows + row * a.copies + j);
                 if (dst >= a.n_dest && a.status && lane == 0) atomicOr(a.status, MOE_DEV_BAD_TABLE);
                 if (dst >= 0 && dst < a.n_dest) put(dst);
             }
         } else {
-            put(row);
+            put(row);                                      // the padding's rows too: their scale words alone
         }
     }
 }
