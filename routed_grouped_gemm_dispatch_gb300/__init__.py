@@ -518,8 +518,9 @@ def _mx4(codes, scales, name, ndim=None):
     rows = shape[0] if len(shape) == 2 else codes.numel() // max(shape[-1], 1)
     if cols == 0 or cols % 128:
         raise ValueError(f"{name} must hold a multiple of 128 columns, got {cols}")
-    _dev(scales, f"{name}_scales", u8)
-    if scales.numel() != ((rows + 127) >> 7) * (cols >> 7) * 512:
+    tiles = _dev(scales, f"{name}_scales", u8).shape
+    # row-major scales can be as many bytes: the tiles' own dims tell them apart
+    if tiles[-4:] != (cols >> 7, 32, 4, 4) or scales.numel() != ((rows + 127) >> 7) * (cols >> 7) * 512:
         raise ValueError(f"{name}_scales must hold the tiles {_mx4_scale_shape(rows, cols)}, got {tuple(scales.shape)}")
     return (*shape[:-1], cols)
 

@@ -1,0 +1,47 @@
+"""What the binding refuses before it reaches the library, on tensors without data: device
+tensors of every shape exist, and nothing is launched."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import routed_grouped_gemm_dispatch_gb300 as moe
+
+
+@pytest.fixture
+def fake():
+    """Tensors made inside have a device, a type, sizes and strides, and no memory."""
+    moe.build()
+    moe.lib()
+    with FakeTensorMode():
+        yield lambda *shape, dt=torch.uint8: torch.empty(shape, dtype=dt, device="cuda")
+
+
+def test_scales_in_another_order_are_refused(fake):
+    """Row-major scales, [rows, columns / 32], are as many bytes as the tiles where rows are a
+    multiple of 128; so are tiles of another shape."""
+    c, t = fake(256, 256), fake(2, 4, 32, 4, 4)
+    assert moe._mx4(c, t, "a", 2) == (256, 512)
+    assert moe._mx4(fake(2, 128, 256), t, "a", 3) == (2, 128, 512)
+    assert moe._mx4(fake(2, 128, 256), fake(2, 1, 4, 32, 4, 4), "a", 3) == (2, 128, 512)     # a stack's tiles apart
+    assert moe._mx4(fake(0, 256), fake(0, 4, 32, 4, 4), "a", 2) == (0, 512)
+    other = [fake(256, 16), fake(4096), fake(4, 2, 32, 4, 4), fake(2, 4, 4, 32, 4), fake(2, 4, 512), fake(8, 32, 4, 4)]
+    w, ws, h = fake(1, 128, 256), fake(1, 4, 32, 4, 4), fake(256, 128, dt=torch.float16)
+    i32 = [fake(n, dt=torch.int32) for n in (1, 2, 2, 2)]
+    for s in other:
+        with pytest.raises(ValueError, match="must hold the tiles"):
+            moe.mx4_dequantize(c, s, torch.float16)
+        with pytest.raises(ValueError, match="a_scales must hold the tiles"):
+            moe.mx4_matmul(c, s, c, t)
+        with pytest.raises(ValueError, match="b_scales must hold the tiles"):
+            moe.mx4_matmul(c, t, c, s)
+        with pytest.raises(ValueError, match="x_scales must hold the tiles"):
+            moe.mx4_gate_up(c, s, w, ws, w, ws, i32[0], i32[2], i32[3], h)
+        with pytest.raises(ValueError, match="h_scales must hold the tiles"):
+            moe.mx4_down(c, s, w, ws, fake(5, dt=torch.float32), *i32, h)
+    # a weight stack's
+    with pytest.raises(ValueError, match="gate_scales must hold the tiles"):
+        moe.mx4_gate_up(c, t, w, fake(128, 16), w, ws, i32[0], i32[2], i32[3], h)
+    with pytest.raises(ValueError, match="up_scales must hold the tiles"):
+        moe.mx4_gate_up(c, t, w, ws, w, fake(128, 16), i32[0], i32[2], i32[3], h)
+    with pytest.raises(ValueError, match="down_scales must hold the tiles"):
+        moe.mx4_down(c, t, w, fake(128, 16), fake(5, dt=torch.float32), *i32, h)
