@@ -532,8 +532,8 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
     the scale of row r, block b at [r//128, b//4, r%32, r//32%4, b%4].
 
     For a 2-D x, ``src_rows`` [n] int32 picks the rows to convert and ``dest_rows``
-    [n] or [n, copies] int32 the rows of a result of ``n_dest`` rows that each goes
-    to (negative entries are skipped; result rows not named keep what the given
+    [n] or [n, copies] int32 the rows of a result of ``n_dest`` rows (those of
+    ``codes``, where given) that each goes to (negative entries are skipped; result rows not named keep what the given
     ``codes`` and ``scales`` held, and are undefined in new ones).  With
     dest_rows = pack_routed's pair_padded_rows the tokens land in the grouped,
     padded layout."""
@@ -549,6 +549,8 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
         raise ValueError(f"x must have a multiple of 128 columns, got {cols}")
     n = n_src = n_out = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     copies, lead = 1, shape[:-1]
+    if n_dest is not None and dest_rows is None:
+        raise ValueError("n_dest goes with dest_rows: without it the result has the converted rows")
     if lists:
         if src_rows is not None:
             n = _dev(src_rows, "src_rows", torch.int32, 1).numel()
@@ -557,11 +559,13 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
             if d.dim() not in (1, 2) or d.shape[0] != n:
                 raise ValueError("dest_rows must be [rows converted] or [rows converted, copies]")
             copies = d.shape[1] if d.dim() == 2 else 1
-            if codes is not None:
-                n_dest = codes.shape[0]
             if n_dest is None:
-                raise ValueError("dest_rows needs n_dest (or codes and scales to write)")
+                if codes is None:
+                    raise ValueError("dest_rows needs n_dest (or codes and scales to write)")
+                n_dest = _dev(codes, "codes", torch.uint8, 2).shape[0]
             n_out = int(n_dest)
+            if n_out < 0:
+                raise ValueError(f"n_dest must not be negative, got {n_out}")
         else:
             n_out = n
         lead = (n_out,)

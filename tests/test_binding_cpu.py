@@ -45,3 +45,26 @@ def test_scales_in_another_order_are_refused(fake):
         moe.mx4_gate_up(c, t, w, ws, w, fake(128, 16), i32[0], i32[2], i32[3], h)
     with pytest.raises(ValueError, match="down_scales must hold the tiles"):
         moe.mx4_down(c, t, w, fake(128, 16), fake(5, dt=torch.float32), *i32, h)
+
+
+def test_n_dest_has_to_agree(fake):
+    """n_dest is the rows of the result that dest_rows points into: not another number than the given
+    codes have, and nothing without dest_rows."""
+    x, dest = fake(4, 256, dt=torch.float16), fake(4, dt=torch.int32)
+    codes, scales = fake(20, 128), fake(1, 2, 32, 4, 4)
+    for n in (10, 0, 21):
+        with pytest.raises(ValueError, match="codes must have shape"):
+            moe.mx4_quantize(x, dest_rows=dest, n_dest=n, codes=codes, scales=scales)
+    for n in (0, 4, 7):
+        with pytest.raises(ValueError, match="n_dest goes with dest_rows"):
+            moe.mx4_quantize(x, n_dest=n)
+        with pytest.raises(ValueError, match="n_dest goes with dest_rows"):
+            moe.mx4_quantize(x, src_rows=dest, n_dest=n)
+    with pytest.raises(ValueError, match="n_dest"):
+        moe.mx4_quantize(x, dest_rows=dest, n_dest=-1)
+    with pytest.raises(ValueError, match="codes must have 2 dims"):
+        moe.mx4_quantize(x, dest_rows=dest, codes=fake(2, 20, 128))
+    with pytest.raises(TypeError, match="codes"):
+        moe.mx4_quantize(x, dest_rows=dest, codes=[1, 2])
+    with pytest.raises(ValueError, match="scales must have shape"):
+        moe.mx4_quantize(x, dest_rows=dest, n_dest=20, codes=codes, scales=fake(2, 2, 32, 4, 4))
