@@ -449,9 +449,14 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
     intermediate] (the gated product, rounded) may be supplied; what is not comes
     from the current stream's memory, which another ``stream`` has to wait for.  For gradients supply ``gate`` and
     ``up`` [T, intermediate] too: they receive the rounded projections, which
-    gated_ffn_backward reads with ``up_logits``."""
+    gated_ffn_backward reads with ``up_logits``.  No autograd graph is recorded:
+    inputs that require grad are refused while gradients are being recorded."""
     import torch
     code, dt, T, H, I = _ffn_sizes(x, gate_w, up_w, down_w)
+    if ((x.requires_grad or gate_w.requires_grad or up_w.requires_grad or down_w.requires_grad)
+            and torch.is_grad_enabled()):
+        raise RuntimeError("gated_ffn records no autograd graph, but an input requires grad: call it under "
+                           "torch.no_grad() and take the gradients from gated_ffn_backward")
     if gate is not None or up is not None:
         if gate is None or up is None:
             raise ValueError("gate and up are stored together: supply both or neither")

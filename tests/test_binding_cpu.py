@@ -68,3 +68,21 @@ def test_n_dest_has_to_agree(fake):
         moe.mx4_quantize(x, dest_rows=dest, codes=[1, 2])
     with pytest.raises(ValueError, match="scales must have shape"):
         moe.mx4_quantize(x, dest_rows=dest, n_dest=20, codes=codes, scales=fake(2, 2, 32, 4, 4))
+
+
+@pytest.mark.parametrize("which", ["x", "gate_w", "up_w", "down_w"])
+def test_autograd_is_not_lost_silently(fake, which):
+    """gated_ffn records no graph: with an input that asks for gradients it says so, unless none are
+    being recorded."""
+    dt = torch.bfloat16
+    a = {"x": fake(3, 16, dt=dt), "gate_w": fake(24, 16, dt=dt), "up_w": fake(24, 16, dt=dt), "down_w": fake(16, 24, dt=dt)}
+    a[which].requires_grad_()
+    h = fake(3, 16, dt=dt)                        # a wrong up_logits: refused next, where the call goes on
+    with pytest.raises(RuntimeError, match="gated_ffn_backward"):
+        moe.gated_ffn(**a, up_logits=h)
+    for quiet in (torch.no_grad(), torch.inference_mode()):
+        with quiet, pytest.raises(ValueError, match="up_logits"):
+            moe.gated_ffn(**a, up_logits=h)
+    a[which] = a[which].detach()
+    with pytest.raises(ValueError, match="up_logits"):
+        moe.gated_ffn(**a, up_logits=h)
