@@ -32,6 +32,11 @@ The dense gated feed-forward block (fp16 or bf16):
   mx4_matmul(a, a_scales, b, b_scales)          -> a·bᵀ
   mx4_gate_up(...), mx4_down(...)               the routed experts' two halves, in the
                                                 layout and with the tables of fused_forward
+
+Work goes to the current stream, or to the ``stream`` that a call is given (an
+object with cuda_stream, or the handle).  What a call allocates comes from the
+current stream's memory, so a given stream has to wait for the current one
+first; it is not handed out again before the given stream is done with it.
 """
 from __future__ import annotations
 
@@ -173,6 +178,19 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _used_on(stream, *tensors):
+    """Keep tensors that a call allocated from being handed out again before
+    ``stream``'s work on them is done."""
+    if stream is None:
+        return
+    import torch
+    for t in tensors:
+        s = stream
+        if not hasattr(s, "cuda_stream"):        # a handle; 0 is the default stream's
+            s = torch.cuda.ExternalStream(s, t.device) if s else torch.cuda.default_stream(t.device)
+        t.record_stream(s)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -219,6 +237,7 @@ def build_dispatch(topk_ids, n_experts: int, block_token: int = BLOCK_TOKEN,
             "group_padded_offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
             "group_idx_for_bx": torch.empty(max(m, 0), dtype=torch.int32, device=dev),
         }
+        _used_on(stream, *out.values())
     st = lib().moe_build_dispatch(
         _ptr(ids), T, k, E, int(block_token), _ptr(out["group_sizes"]), _ptr(out["group_offsets"]),
         _ptr(out["group_padded_offsets"]), _ptr(out["group_idx_for_bx"]), m,
@@ -318,13 +337,17 @@ def pack_routed(topk_ids, topk_weights, x_tokens, tables, rows_total: int | None
     dev = ids.device
     if stacked is None and x is not None:
         stacked = torch.full((rows_total, H), float("nan"), dtype=torch.float16, device=dev)
+        _used_on(stream, stacked)
     if routed_weights is None and tw is not None:
         routed_weights = torch.empty(T * k, dtype=torch.float32, device=dev)
+        _used_on(stream, routed_weights)
     if pair_rows is None:
         pair_rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+        _used_on(stream, pair_rows)
     need = int(lib().moe_pack_workspace_bytes(T * k, E))
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _used_on(stream, workspace)
     st = lib().moe_pack_routed(
         _ptr(ids), _ptr(tw), T, k, E, _ptr(x), H, _ptr(tables["group_offsets"]),
         _ptr(tables["group_padded_offsets"]), rows_total, _ptr(stacked), _ptr(routed_weights),
@@ -342,6 +365,7 @@ def combine_routed(out, pair_rows, y=None, stream=None):
     T, k = pr.shape
     if y is None:
         y = torch.empty((T, o.shape[1]), dtype=torch.float16, device=o.device)
+        _used_on(stream, y)
     st = lib().moe_combine_routed(_ptr(o), o.shape[0], o.shape[1], _ptr(pr), T, k, _ptr(y),
                                   _stream(stream))
     _check(st, "moe_combine_routed")
@@ -361,8 +385,10 @@ def router_topk(x_tokens, router_w, top_k: int, topk_ids=None, topk_weights=None
         raise ValueError("router_w must be [n_experts, hidden]")
     if topk_ids is None:
         topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        _used_on(stream, topk_ids)
     if topk_weights is None:
         topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        _used_on(stream, topk_weights)
     st = lib().moe_router_topk(_ptr(x), T, H, _ptr(w), E, int(top_k), _ptr(topk_ids),
                                _ptr(topk_weights), _ptr(status), _stream(stream))
     _check(st, "moe_router_topk")
@@ -411,14 +437,6 @@ def _shaped(t, name, dtype, shape):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _used_on(t, stream):
-    """Keep a tensor that this module allocated, and does not return, from being
-    handed out again before ``stream``'s work on it is done."""
-    if stream is not None:
-        import torch
-        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
-
-
 def _ffn_sizes(x, gate_w, up_w, down_w):
     """The block's type code and sizes, with every array checked."""
     dt = getattr(x, "dtype", None)
@@ -446,9 +464,8 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
     x [T, hidden], gate_w / up_w [intermediate, hidden], down_w [hidden,
     intermediate], all float16 or all bfloat16; any T, hidden and intermediate
     multiples of 8, contiguous.  ``out`` [T, hidden] and ``up_logits`` [T,
-    intermediate] (the gated product, rounded) may be supplied; what is not comes
-    from the current stream's memory, which another ``stream`` has to wait for.  For gradients supply ``gate`` and
-    ``up`` [T, intermediate] too: they receive the rounded projections, which
+    intermediate] (the gated product, rounded) may be supplied.  For gradients supply
+    ``gate`` and ``up`` [T, intermediate] too: they receive the rounded projections, which
     gated_ffn_backward reads with ``up_logits``.  No autograd graph is recorded:
     inputs that require grad are refused while gradients are being recorded."""
     import torch
@@ -464,11 +481,12 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
         _shaped(up, "up", dt, (T, I))
     if up_logits is None:
         up_logits = torch.empty((T, I), dtype=dt, device=x.device)
-        _used_on(up_logits, stream)
+        _used_on(stream, up_logits)
     else:
         _shaped(up_logits, "up_logits", dt, (T, I))
     if out is None:
         out = torch.empty_like(x)
+        _used_on(stream, out)
     else:
         _shaped(out, "out", dt, (T, H))
     st = lib().moe_ffn_forward(code, x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(), down_w.data_ptr(), I,
@@ -493,10 +511,15 @@ def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=
     grads = []
     for t, name, like in ((d_x, "d_x", x), (d_gate_w, "d_gate_w", gate_w), (d_up_w, "d_up_w", up_w),
                           (d_down_w, "d_down_w", down_w)):
-        grads.append(torch.empty_like(like) if t is None else _shaped(t, name, dt, like.shape))
+        if t is None:
+            t = torch.empty_like(like)
+            _used_on(stream, t)
+        else:
+            _shaped(t, name, dt, like.shape)
+        grads.append(t)
     if workspace is None:
         workspace = torch.empty(max(ffn_backward_workspace_bytes(T, I), 16), dtype=torch.uint8, device=x.device)
-        _used_on(workspace, stream)
+        _used_on(stream, workspace)
     _check(lib().moe_ffn_backward(code, d_out.data_ptr(), x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(),
                                   down_w.data_ptr(), I, gate.data_ptr(), up.data_ptr(), up_logits.data_ptr(),
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -576,10 +599,12 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
         lead = (n_out,)
     if codes is None:
         codes = torch.empty((*lead, cols >> 1), dtype=torch.uint8, device=x.device)
+        _used_on(stream, codes)
     else:
         _shaped(codes, "codes", torch.uint8, (*lead, cols >> 1))
     if scales is None:
         scales = torch.empty(_mx4_scale_shape(n_out, cols), dtype=torch.uint8, device=x.device)
+        _used_on(stream, scales)
     else:
         _shaped(scales, "scales", torch.uint8, _mx4_scale_shape(n_out, cols))
     if copies == 0:
@@ -599,6 +624,7 @@ def mx4_dequantize(codes, scales, dtype, out=None, stream=None):
     cols = shape[-1]
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=codes.device)
+        _used_on(stream, out)
     else:
         _shaped(out, "out", dtype, shape)
     rows = shape[0] if len(shape) == 2 else out.numel() // cols
@@ -618,6 +644,7 @@ def mx4_matmul(a, a_scales, b, b_scales, out=None, dtype=None, status=None, stre
         raise ValueError(f"a and b must have the same columns, got {k} and {kb}")
     if out is None:
         out = torch.empty((rows, n), dtype=dtype or torch.float16, device=a.device)
+        _used_on(stream, out)
     code = _dtype_code(getattr(out, "dtype", None), "out")
     _shaped(out, "out", out.dtype, (rows, n))
     _check(lib().moe_mx4_matmul(_ptr(a), _ptr(a_scales), rows, k, _ptr(b), _ptr(b_scales), n, code, _ptr(out),
