@@ -214,6 +214,16 @@ def _dev(t, name, dtype, ndim=None):
     return t
 
 
+def _status(t):
+    """Address of a status word that was given, an int32 on the device."""
+    if t is None:
+        return None
+    import torch
+    if not _dev(t, "status", torch.int32).numel():
+        raise ValueError("status must hold an element")
+    return t.data_ptr()
+
+
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -490,7 +500,7 @@ def gated_ffn(x, gate_w, up_w, down_w, out=None, up_logits=None, gate=None, up=N
     else:
         _shaped(out, "out", dt, (T, H))
     st = lib().moe_ffn_forward(code, x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(), down_w.data_ptr(), I,
-                               _ptr(gate), _ptr(up), up_logits.data_ptr(), out.data_ptr(), _ptr(status),
+                               _ptr(gate), _ptr(up), up_logits.data_ptr(), out.data_ptr(), _status(status),
                                _stream(stream))
     _check(st, "moe_ffn_forward")
     return out
@@ -520,10 +530,12 @@ def gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits, d_x=
     if workspace is None:
         workspace = torch.empty(max(ffn_backward_workspace_bytes(T, I), 16), dtype=torch.uint8, device=x.device)
         _used_on(stream, workspace)
+    else:
+        _dev(workspace, "workspace", getattr(workspace, "dtype", None))
     _check(lib().moe_ffn_backward(code, d_out.data_ptr(), x.data_ptr(), T, H, gate_w.data_ptr(), up_w.data_ptr(),
                                   down_w.data_ptr(), I, gate.data_ptr(), up.data_ptr(), up_logits.data_ptr(),
                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  *[g.data_ptr() for g in grads], _ptr(status), _stream(stream)), "moe_ffn_backward")
+                                  *[g.data_ptr() for g in grads], _status(status), _stream(stream)), "moe_ffn_backward")
     return tuple(grads)
 
 
@@ -610,7 +622,7 @@ def mx4_quantize(x, src_rows=None, dest_rows=None, n_dest=None, codes=None, scal
     if copies == 0:
         return codes, scales
     st = lib().moe_mx4_quantize(code, x.data_ptr(), n_src, cols, _ptr(src_rows), n, _ptr(dest_rows), copies, n_out,
-                                codes.data_ptr(), scales.data_ptr(), _ptr(status), _stream(stream))
+                                codes.data_ptr(), scales.data_ptr(), _status(status), _stream(stream))
     _check(st, "moe_mx4_quantize")
     return codes, scales
 
@@ -648,7 +660,7 @@ def mx4_matmul(a, a_scales, b, b_scales, out=None, dtype=None, status=None, stre
     code = _dtype_code(getattr(out, "dtype", None), "out")
     _shaped(out, "out", out.dtype, (rows, n))
     _check(lib().moe_mx4_matmul(_ptr(a), _ptr(a_scales), rows, k, _ptr(b), _ptr(b_scales), n, code, _ptr(out),
-                                _ptr(status), _stream(stream)), "moe_mx4_matmul")
+                                _status(status), _stream(stream)), "moe_mx4_matmul")
     return out
 
 
@@ -676,7 +688,7 @@ def mx4_gate_up(x, x_scales, gate, gate_scales, up, up_scales, group_sizes, grou
     m = _mx4_tables(group_sizes, group_padded_offsets, group_idx_for_bx, E)
     _check(lib().moe_mx4_gate_up(_ptr(x), _ptr(x_scales), rows, H, _ptr(gate), _ptr(gate_scales), _ptr(up),
                                  _ptr(up_scales), E, I, _ptr(group_sizes), _ptr(group_padded_offsets),
-                                 _ptr(group_idx_for_bx), m, code, _ptr(up_logits), _ptr(status), _stream(stream)),
+                                 _ptr(group_idx_for_bx), m, code, _ptr(up_logits), _status(status), _stream(stream)),
            "moe_mx4_gate_up")
     return up_logits
 
@@ -701,5 +713,5 @@ def mx4_down(h, h_scales, down, down_scales, routed_expert_weights, group_sizes,
         raise ValueError("table lengths do not match n_experts")
     _check(lib().moe_mx4_down(_ptr(h), _ptr(h_scales), rows, I, _ptr(down), _ptr(down_scales), E, H, _ptr(w), w.numel(),
                               _ptr(group_sizes), _ptr(offs), _ptr(group_padded_offsets), _ptr(group_idx_for_bx), m,
-                              code, _ptr(out), _ptr(status), _stream(stream)), "moe_mx4_down")
+                              code, _ptr(out), _status(status), _stream(stream)), "moe_mx4_down")
     return out

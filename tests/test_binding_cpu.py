@@ -6,6 +6,8 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 
 import routed_grouped_gemm_dispatch_gb300 as moe
 
+pytestmark = pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+
 
 @pytest.fixture
 def fake():
@@ -86,3 +88,31 @@ def test_autograd_is_not_lost_silently(fake, which):
     a[which] = a[which].detach()
     with pytest.raises(ValueError, match="up_logits"):
         moe.gated_ffn(**a, up_logits=h)
+
+
+def test_status_and_workspace_are_device_memory(fake):
+    """The kernels write to both: a status word is one int32 on the device at least, a workspace is there too."""
+    dt = torch.float16
+    x, w, d, h = fake(3, 16, dt=dt), fake(24, 16, dt=dt), fake(16, 24, dt=dt), fake(3, 24, dt=dt)
+    c, s = fake(128, 64), fake(1, 1, 32, 4, 4)
+    cw, sw, i32 = fake(1, 128, 64), fake(1, 1, 32, 4, 4), [fake(n, dt=torch.int32) for n in (1, 2, 2, 1)]
+    out = fake(128, 128, dt=dt)
+    calls = [lambda st: moe.gated_ffn(x, w, w, d, status=st),
+             lambda st: moe.gated_ffn_backward(x, x, w, w, d, h, h, h, status=st),
+             lambda st: moe.mx4_quantize(fake(3, 128, dt=dt), status=st),
+             lambda st: moe.mx4_matmul(c, s, c, s, status=st),
+             lambda st: moe.mx4_gate_up(c, s, cw, sw, cw, sw, i32[0], i32[2], i32[3], out, status=st),
+             lambda st: moe.mx4_down(c, s, cw, sw, fake(5, dt=torch.float32), *i32, out, status=st)]
+    for call in calls:
+        with pytest.raises(ValueError, match="status must be a CUDA tensor"):
+            call(torch.zeros(1, dtype=torch.int32))
+        with pytest.raises(TypeError, match="status must be torch.int32"):
+            call(fake(4))
+        with pytest.raises(ValueError, match="status must hold"):
+            call(fake(0, dt=torch.int32))
+        with pytest.raises(TypeError, match="status must be a torch.Tensor"):
+            call(0x1000)
+    for ws, error, text in ((torch.zeros(1 << 16, dtype=torch.uint8), ValueError, "CUDA"), (0x1000, TypeError, "Tensor"),
+                            (fake(1 << 17)[::2], ValueError, "contiguous")):
+        with pytest.raises(error, match=f"workspace must be .*{text}"):
+            moe.gated_ffn_backward(x, x, w, w, d, h, h, h, workspace=ws)
