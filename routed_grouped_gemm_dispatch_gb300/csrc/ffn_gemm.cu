@@ -591,35 +591,23 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             t += n_pairs;
         }
     }
-    if (warp == 0) {
-        if (lane == 0 && !ok) {
-            // Let the copies already in flight land before the CTA exits.
-            volatile int never = 0;
-            if (leader) {
-                const int64_t n = issued < STAGES ? issued : STAGES;
-                for (int64_t i = 0; i < n; ++i) {
-                    const int64_t idx = issued - 1 - i;
-                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % STAGES),
-                                      static_cast<uint32_t>((idx / STAGES) & 1), &never, DRAIN_LIMIT_NS);
-                }
-            } else {
-                // the odd CTA's copies report to the even CTA's barriers
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 1000000ull) { }
-            }
-        }
-    } else if (warp == 1) {
-        if (leader && issue) {
-            // Every MMA this warp issued has finished once this arrives.
-            volatile int never = 0;
-            tc_commit_pair(bar_drain);
-            mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
-        }
+    if (warp == 1 && leader && issue) {
+        // Every MMA this warp issued has finished once this arrives.
+        volatile int never = 0;
+        tc_commit_pair(bar_drain);
+        mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
     }
     __syncwarp();
 
     tc_fence_before_sync();
     __syncthreads();
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        // Whichever role gave up: copies in flight land before the CTA exits.
+        // (The odd CTA's report to the even CTA's barriers.)
+        if (leader) drain_copies(bar_full, issued, STAGES, DRAIN_LIMIT_NS);
+        else spin_ns(1000000ull);
+    }
+    __syncwarp();
     // No CTA leaves (or frees the pair's TMEM) while another may still write
     // into its shared memory, arrive on its barriers or use the TMEM.
     cluster_sync_all();

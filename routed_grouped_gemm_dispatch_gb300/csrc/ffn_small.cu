@@ -127,6 +127,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     tc_fence_after_sync();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+    int32_t issued = 0;            // stages fed, by warp 0
     if (warp == 0) {
         // ===================== producer =====================
         const uint32_t issue = elect_one();
@@ -172,17 +173,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
             load_x(c, stage);
             if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
-        if (c < c1 && lane == 0) {
-            // Let the copies already in flight land before the CTA exits.
-            volatile int never = 0;
-            const int32_t issued = c - c0;
-            const int32_t n = issued < stages ? issued : stages;
-            for (int32_t i = 0; i < n; ++i) {
-                const int32_t idx = issued - 1 - i;
-                mbar_wait_bounded(bar_full + 8 * (idx % stages), static_cast<uint32_t>((idx / stages) & 1), &never,
-                                  DRAIN_LIMIT_NS);
-            }
-        }
+        issued = c - c0;
         __syncwarp();
     } else if (warp == 1) {
         // ===================== MMA issuer =====================
@@ -232,6 +223,8 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     pdl_launch_dependents();
     __syncwarp();
     cluster_sync_all();
+    // Whichever role gave up: copies in flight land before the CTA exits.
+    if (warp == 0 && lane == 0 && *abort_flag) drain_copies(bar_full, issued, stages, DRAIN_LIMIT_NS);
 
     // ===================== join and store =====================
     if (warp >= 2 && !*abort_flag) {

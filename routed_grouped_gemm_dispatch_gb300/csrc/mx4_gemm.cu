@@ -304,6 +304,7 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
     const int32_t n_pairs = static_cast<int32_t>(gridDim.x) / PAIR;
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
+    int64_t issued = 0;            // stages fed, by warp 0
     if (warp == 0) {
         // ===================== producer (both CTAs) =====================
         const uint32_t issue = elect_one();
@@ -311,7 +312,6 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
         const uint64_t policy = l2_policy_evict_normal();
         const uint32_t leader_full = mapa_shared(bar_full, 0);
         uint32_t stage = 0, phase = 0;
-        int64_t issued = 0;
         bool ok = true;
         const int32_t my_tiles = __shfl_sync(0xffffffffu, total_tiles, 0);
         for (int32_t t = pair_id; t < my_tiles && ok; t += n_pairs) {
@@ -349,22 +349,6 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
                     tma_load_2d_pair_if(issue, ss + SFA_BYTES + SFB_BYTES / 2, &maps.sfb2, fb, kb * 256, tile_row / BM, policy);
                 ++issued;
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
-            }
-        }
-        if (!ok && lane == 0) {
-            // Let the copies already in flight land before the CTA exits.
-            volatile int never = 0;
-            if (leader) {
-                const int64_t n = issued < stages ? issued : stages;
-                for (int64_t i = 0; i < n; ++i) {
-                    const int64_t idx = issued - 1 - i;
-                    mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
-                                      static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
-                }
-            } else {
-                // the odd CTA's copies report to the even CTA's barriers
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 1000000ull) { }
             }
         }
         __syncwarp();
@@ -517,6 +501,13 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     tc_fence_before_sync();
     __syncthreads();
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        // Whichever role gave up: copies in flight land before the CTA exits.
+        // (The odd CTA's report to the even CTA's barriers.)
+        if (leader) drain_copies(bar_full, issued, p.stages, DRAIN_LIMIT_NS);
+        else spin_ns(1000000ull);
+    }
+    __syncwarp();
     // Neither CTA leaves (or frees the pair's TMEM) while the other may still
     // write into its shared memory, arrive on its barriers or use the TMEM.
     cluster_sync_all();
@@ -671,12 +662,12 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         return ti;
     };
 
+    int64_t issued = 0;            // stages fed, by warp 0
     if (warp == 0) {
         // ===================== producer =====================
         const uint32_t issue = elect_one();
         const uint64_t policy = l2_policy_evict_normal();
         uint32_t stage = 0, phase = 0;
-        int64_t issued = 0;
         bool ok = true;
         for (int32_t t = t0; t < total_tiles && ok; t += t_step) {
             const FewTile ti = tile(t);
@@ -704,16 +695,6 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                 tma_load_2d_if(issue, ss, &maps.sfa, fb, kb * 256, bx, policy);
                 ++issued;
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
-            }
-        }
-        if (!ok && lane == 0) {
-            // Let the copies already in flight land before the CTA exits.
-            volatile int never = 0;
-            const int64_t n = issued < stages ? issued : stages;
-            for (int64_t i = 0; i < n; ++i) {
-                const int64_t idx = issued - 1 - i;
-                mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages),
-                                  static_cast<uint32_t>((idx / stages) & 1), &never, DRAIN_LIMIT_NS);
             }
         }
         __syncwarp();
@@ -855,6 +836,9 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     tc_fence_before_sync();
     __syncthreads();
+    // Whichever role gave up: copies in flight land before the CTA exits.
+    if (warp == 0 && lane == 0 && *abort_flag) drain_copies(bar_full, issued, p.stages, DRAIN_LIMIT_NS);
+    __syncwarp();
     if (*abort_flag && tid == 0 && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
     if (warp == 1) {
         tc_fence_after_sync();

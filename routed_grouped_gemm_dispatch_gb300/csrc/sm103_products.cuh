@@ -16,6 +16,23 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, limit_ns)) != 0;
 }
 
+// For one thread, once every role of the CTA has stopped: waits, at most `limit_ns`
+// each, until the copies of the last `stages` of `issued` ring stages have landed.
+__device__ __forceinline__ void drain_copies(uint32_t bar_full, int64_t issued, int32_t stages, uint64_t limit_ns) {
+    volatile int never = 0;
+    const int64_t n = issued < stages ? issued : stages;
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t idx = issued - 1 - i;
+        mbar_wait_bounded(bar_full + 8 * static_cast<uint32_t>(idx % stages), static_cast<uint32_t>((idx / stages) & 1),
+                          &never, limit_ns);
+    }
+}
+
+__device__ __forceinline__ void spin_ns(uint64_t ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < ns) { }
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t e;
