@@ -199,7 +199,8 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
         // ===================== partial sums to shared memory =====================
         // after the last MMA the ring is free: [token][weight row] in fp32
         pdl_wait_prior_grid();
-        if (mbar_wait_bounded(bar_done, 0, abort_flag, WAIT_LIMIT_NS)) {
+        // one answer for the whole warp, whose TMEM loads are collective
+        if (mbar_wait_warp(bar_done, 0, abort_flag, WAIT_LIMIT_NS)) {
             tc_fence_after_sync();
             const int row = (warp & 3) * 32 + lane;
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
