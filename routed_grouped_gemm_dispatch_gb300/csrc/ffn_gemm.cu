@@ -230,11 +230,12 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
     if (!p.early_weights) {
         pdl_wait_prior_grid();
         pdl_launch_dependents();
-    } else if (warp != 0) {
-        pdl_wait_prior_grid();     // no bounded wait runs while the launch before still works
     }
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
+    // No bounded wait runs while the launch before still works.  (Behind the cluster's
+    // barrier, which the producer has to pass before its first weights.)
+    if (p.early_weights && warp != 0) pdl_wait_prior_grid();
 
     const int32_t split = SPLIT ? p.split : 1;
     const int32_t cluster_id = static_cast<int32_t>(blockIdx.x) / (PAIR * split);
