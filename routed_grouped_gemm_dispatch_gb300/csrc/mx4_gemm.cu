@@ -887,7 +887,8 @@ cudaError_t launch(const Maps& maps, Params& p, cudaStream_t stream) {
         if (lim.err == cudaSuccess && lim.pairs <= 0) lim.err = cudaErrorNoDevice;
     });
     if (lim.err != cudaSuccess) return lim.err;
-    const int control = 1024 + OFF_UNITS + 8 * p.num_blocks;
+    // (a plain product's units need no list: with one, 2 M rows would leave two stages of six)
+    const int control = 1024 + OFF_UNITS + (FORM == MX4_MATMUL ? 0 : 8 * p.num_blocks);
     p.stages = (lim.smem - control) / STAGE_BYTES;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     // a unit has one block at least (two, but for the last, in a plain product)
