@@ -47,9 +47,12 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-// 1 / (1 + 2^(-x log2 e)): two approximate instructions (2 ulp together) that flush
-// subnormals, which spares the compiler's range handling around each (4-bit gate_up of 4096
-// tokens, top-6 of 64: 69.2 -> 67.3 us; gradients of 2048 tokens: 109.5 -> 107.0).
+// 1 / (1 + 2^(-x log2 e)) by two approximate instructions that flush subnormals, which
+// spares the compiler's range handling around each (4-bit gate_up of 4096 tokens, top-6
+// of 64: 69.2 -> 67.3 us; gradients of 2048 tokens: 109.5 -> 107.0).  The relative error is
+// below 2^-21 + 2^-23.7 |x|: the rounding of x log2 e before the power is an absolute
+// error of the exponent, so it grows with |x| (2^-16 at x = -87, where the result is
+// next rounded to 8 or 11 bits).  Below about x = -87.3 the result, less than 2^-126, is 0.
 __device__ __forceinline__ float sigmoid_approx(float x) {
     float e, s;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
