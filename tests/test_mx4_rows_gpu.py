@@ -1,11 +1,14 @@
-"""4-bit conversion of listed rows into a result of its own: codes, scales and what
-is left alone have to be equal to the byte."""
+"""4-bit conversion of listed rows into a result of its own, and tables that point outside
+their arrays in both grouped forms and on both kernels: what is written and what is left
+alone have to be equal to the byte."""
 import numpy as np
 import pytest
 import torch
 
 import mx4_ref
 import routed_grouped_gemm_dispatch_gb300 as moe
+from gpu_side import sentinel
+from moe_cases import SENTINEL
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +55,51 @@ def test_source_rows_alone_with_bad_entries():
                 want_c[i], want_s[i] = mx4_ref.pack(c[r:r + 1])[0], s[r]
         assert np.array_equal(codes.cpu().numpy(), want_c)
         assert np.array_equal(scales.cpu().numpy(), mx4_ref.tiles(want_s))
+
+
+def operand(rng, rows, cols):
+    c, s = mx4_ref.quantize(rng.standard_normal((rows, cols)))
+    return torch.from_numpy(mx4_ref.pack(c)).cuda(), torch.from_numpy(mx4_ref.tiles(s)).cuda()
+
+
+@pytest.mark.parametrize("form", ["gate_up", "down"])
+@pytest.mark.parametrize("T,top_k,E", [(5, 2, 8), (100, 2, 8), (300, 2, 4)], ids=["few rows", "few rows, two blocks", "pairs"])
+def test_bad_tables(T, top_k, E, form):
+    """An entry that points outside its array leaves its block out, sets the bit and changes no other block."""
+    rng = np.random.default_rng(T)
+    k, n = 256, 384
+    ids = torch.from_numpy(np.argsort(rng.random((T, E)), axis=1)[:, :top_k].astype(np.int32).copy()).cuda()
+    t = moe.build_dispatch(ids, E)
+    rows = t["group_idx_for_bx"].numel() * 128
+    a, sa = operand(rng, rows, k)
+    b, sb = operand(rng, E * n, k)
+    b2, sb2 = operand(rng, E * n, k)
+    w = torch.from_numpy(rng.random(T * top_k).astype(np.float32)).cuda()
+    names = ("group_sizes", "group_offsets", "group_padded_offsets", "group_idx_for_bx")
+
+    def run(tab, status=None):
+        out = sentinel(rows, n)
+        if form == "down":
+            moe.mx4_down(a, sa, b.view(E, n, -1), sb, w, *(tab[x] for x in names), out, status=status)
+        else:
+            moe.mx4_gate_up(a, sa, b.view(E, n, -1), sb, b2.view(E, n, -1), sb2, tab[names[0]], tab[names[2]],
+                            tab[names[3]], out, status=status)
+        torch.cuda.synchronize()
+        return out.view(torch.int16)
+
+    want = run(t)
+    assert int(t["group_sizes"][0]) > 0 and not bool((want[0] == SENTINEL).all())
+    # where expert 0's rows end
+    after = int(t["group_padded_offsets"][1])
+    cases = [("group_idx_for_bx", E, 128), ("group_idx_for_bx", -1, 128), ("group_idx_for_bx", 1 << 30, 128),
+             ("group_padded_offsets", 128, after)]
+    if form == "down":
+        cases += [("group_offsets", 1 << 20, after), ("group_offsets", -T * top_k - 5, after)]
+    for name, value, first in cases:
+        bad = {x: v.clone() for x, v in t.items()}
+        bad[name][0] = value
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = run(bad, status)
+        assert int(status.item()) == moe.MOE_DEV_BAD_TABLE, (name, value)
+        assert bool((got[:128] == SENTINEL).all()), (name, value)
+        assert torch.equal(got[first:], want[first:]), (name, value)
