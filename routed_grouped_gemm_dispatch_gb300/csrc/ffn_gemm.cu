@@ -691,7 +691,10 @@ cudaError_t launch(const Maps& maps, Plan& p, cudaStream_t stream) {
         best = (work > longest ? work : longest) + SHARED_STEPS;
     }
     for (int split = 2; split <= MAX_SPLIT; ++split) {
-        // (three pairs would leave one of them without a part of gate and up to finish)
+        // Gate and up finish in two parts, so three pairs join no faster than two and only
+        // the K loop gets shorter.  Measured with three allowed: 200 tokens 2048 / 2816 27.5
+        // -> 28.8 us, 300 tokens 2048 / 1408 25.1 -> 26.5, 450 tokens 4104 / 1024 29.1 ->
+        // 30.4; with the longest K alone it wins (200 tokens 7168 / 2048 39.8 -> 37.7).
         if (steps < MIN_STEPS * split || (EPI == EPI_GATE_UP && split == 3)) continue;
         const int n = r->clusters[split];
         const float part = static_cast<float>(steps) / static_cast<float>(split);
@@ -767,7 +770,8 @@ void set_operands(Problem& pr, int seg, int64_t k, int a, int b_even, int b_odd)
 
 // Rows of a K-major A's boxes.  Of an array of few rows a box of 128 lies mostly
 // outside, which TMA is slow at: gradients of one token, 2048 / 2816, 48.5 -> 33.5
-// us, of 16 tokens 44 -> 34.  (The other rows' sums are never read.)
+// us, of 16 tokens 44 -> 34.  (The other rows' sums are never read.)  33 to 64 tokens
+// take 34.8 to 35.1 us with boxes of 128, 32 tokens 33.4: no third size.
 int a_box_rows(int64_t tokens) { return tokens <= SMALL_ROWS ? SMALL_ROWS : BM; }
 
 // Boxes of 64 columns: 128 rows of a K-major operand, or BK rows of K of an

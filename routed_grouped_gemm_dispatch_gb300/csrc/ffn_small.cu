@@ -49,7 +49,13 @@ constexpr int MAX_NP = static_cast<int>((FFN_SMALL_TOKENS + 15) / 16 * 16);
 constexpr int NUM_THREADS = 192;
 constexpr int NUM_EPI_THREADS = 128;
 constexpr int SMEM_LIMIT = 112 * 1024;         // two CTAs per SM
-constexpr int64_t PREFETCH_BYTES = 24ll << 20; // launches of at most so many weight bytes ask for them ahead
+// Launches of at most so many weight bytes ask L2 for all of them ahead of the wait.  Up
+// to there it saves 0.2 to 1.3 us a forward (hidden / intermediate 2048 / 1408, 64 tokens
+// 14.8 -> 14.4; 2048 / 2816 17.3 -> 16.1; one token of 2048 / 1024 alone loses 0.2).
+// Gate and up of 32 to 48 MB go either way (4096 / 2816, one token 17.2 -> 17.7; 2048 /
+// 4096, 64 tokens 19.1 -> 18.3; 6144 / 2048 27.8 -> 27.2), and above 56 MB the lines asked
+// for hold up the stages' own loads (7168 / 2048 24.7 -> 26.9; 4096 / 8192 40.8 -> 46.6).
+constexpr int64_t PREFETCH_BYTES = 24ll << 20;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 

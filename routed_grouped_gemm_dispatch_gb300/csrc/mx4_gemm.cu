@@ -71,9 +71,20 @@ constexpr int MAX_GROUP = 8;                    // units walked together at most
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 256;                // first scale column
 constexpr int STAGE_SCALE_COLS = 2 * (4 + 8);   // per K = 128: 4 columns of A's, 8 of B's scales
-// Rows per expert up to which the few-rows kernel runs (measured with 2048 / 768,
-// 128 experts: gate_up 60 -> 49 us at 64 rows, 68 -> 63 at 128 but slower at 128
-// with 4096 / 2048; down 41 -> 36 us at 32 rows, 46 -> 50 at 64).
+// Average rows per expert up to which the few-rows kernel runs.  Pair kernel against
+// few-rows kernel, us (experts, K / N):
+//   gate_up  rows       64            96            128
+//     128, 2048 / 768   47.1 / 44.2   47.6 / 46.8   48.9 / 50.9
+//     64, 2048 / 1408   43.0 / 39.2   43.8 / 42.4   45.1 / 47.1
+//     8, 4096 / 2048    21.2 / 20.8   21.5 / 20.6   21.9 / 20.7
+//     32, 7168 / 2048   87.6 / 87.2   88.5 / 93.1   90.0 / 108
+//     16, 1024 / 4096   22.6 / 19.7   22.8 / 21.3   23.6 / 24.7
+//   down     rows       32            48            64
+//     128, 768 / 2048   36.6 / 31.0   36.8 / 37.4   39.6 / 47.8
+//     64, 1408 / 2048   27.1 / 25.0   27.8 / 28.0   28.4 / 33.0
+//     32, 2048 / 7168   49.6 / 46.5   51.4 / 49.8   51.9 / 58.9
+//     8, 2048 / 4096    13.5 / 10.5   14.1 / 11.3   14.5 / 14.5
+//     16, 4096 / 1024   13.3 / 10.4   13.8 / 11.3   13.8 / 15.5
 constexpr int64_t FEW_AVERAGE_GATE_UP = 64;
 constexpr int64_t FEW_AVERAGE = 32;
 constexpr int64_t FEW_MAX_BLOCKS = 4096;        // (its unit list stays small)
