@@ -263,6 +263,10 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const bool a_mn = pr.a_mn != 0, b_mn = pr.b_mn != 0;
         const int32_t steps0 = pr.steps[0];
         const uint32_t bytes = PAIR * (OP_BYTES + (a_mn ? OP_BYTES : static_cast<uint32_t>(p.a_box_bytes)));
+        MOE_DCHECK(pr.a_map[0] < p.n_maps && pr.a_map[1] < p.n_maps && pr.b_map[0][rank] < p.n_maps &&
+                       pr.b_map[1][rank] < p.n_maps,
+                   p.status);
+        MOE_DCHECK(s0 >= 0 && s0 < s1 && s1 <= pr.steps[0] + pr.steps[1], p.status);
         auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t fb, bool mn, int32_t row, int32_t k0) {
             if (mn) {
 #pragma unroll
@@ -370,6 +374,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const Problem& pr = p.pr[ti.q];
         const int64_t row0 = static_cast<int64_t>(ti.m) * (2 * BM) + static_cast<int64_t>(rank) * BM + quarter * 32;
         const int64_t left = pr.m - row0;
+        MOE_DCHECK(row0 >= 0 && left > -2 * BM && ti.n * p.tile_cols < pr.n, p.status);
         return Rows{row0 * pr.n + ti.n * p.tile_cols, left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left))};
     };
     // A shared tile: pass c belongs to pair c * split / PASSES.  The others'
@@ -407,6 +412,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             const int32_t cols = pr.n - ti.n * p.tile_cols - c * 64;             // columns left
             if (cols <= 0) break;
             const int64_t at = r.at + c * 64;
+            MOE_DCHECK(c * 64 < p.tile_cols && cols % 8 == 0 && at >= 0 &&
+                           at + static_cast<int64_t>(rows - 1) * pr.n + (cols < 64 ? cols : 64) <= pr.m * pr.n,
+                       p.status);
             // this pass's first quad of the partial sums
             const uint8_t* part = smem + (c - c0) * PASS_BYTES + row * 16;
             if (EPI == EPI_STORE || (EPI == EPI_GRAD && ti.q != 0)) {
@@ -530,6 +538,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
             if (owner == static_cast<int>(pair) || pr.n - ti.n * p.tile_cols - c * 64 <= 0) continue;
             const int slot = static_cast<int>(pair) - (static_cast<int>(pair) > owner ? 1 : 0);
             const int first = first_pass(owner);
+            MOE_DCHECK(owner >= 0 && owner < split && slot >= 0 && slot < split - 1 && c >= first &&
+                           slot * slot_bytes + (c - first + 1) * PASS_BYTES <= STAGES * STAGE_BYTES,
+                       p.status);
             uint32_t dst = mapa_shared(sbase, static_cast<uint32_t>(owner) * 2 + rank) + slot * slot_bytes +
                            (c - first) * PASS_BYTES + row * 16;
 #pragma unroll 1
@@ -559,6 +570,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan 
         const bool shared = SPLIT && t < p.split_tiles;
         const Tile ti = tile_at(p, t);
         const int32_t steps = p.pr[ti.q].steps[0] + p.pr[ti.q].steps[1];
+        MOE_DCHECK(ti.q < p.n_problems && ti.m >= 0 && ti.m < p.pr[ti.q].m_tiles && ti.n >= 0 &&
+                       ti.n < p.pr[ti.q].n_tiles,
+                   p.status);
         const int32_t s0 = shared ? steps * static_cast<int32_t>(pair) / split : 0;
         const int32_t s1 = shared ? steps * (static_cast<int32_t>(pair) + 1) / split : steps;
         if (warp == 0) {

@@ -114,6 +114,9 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
     const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * rank / nranks);
     const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * (rank + 1) / nranks);
     const int32_t stages = p.stages;
+    MOE_DCHECK(c0 < c1 && c1 <= p.chunks && tile * (GATE_UP ? BM / 2 : BM) < p.n && nranks <= MAX_CLUSTER, p.status);
+    MOE_DCHECK(p.tokens <= p.np && p.np * BM * 4 <= stages * static_cast<int32_t>(stage_bytes) && p.np <= p.tmem_cols,
+               p.status);
 
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -262,6 +265,7 @@ ffn_small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constan
             const int32_t col = col0 + q * 4;
             if (col >= p.n) continue;
             const int64_t o = static_cast<int64_t>(t) * p.n + col;
+            MOE_DCHECK(t >= 0 && t < p.tokens && col >= 0 && col + 4 <= p.n, p.status);
             auto put = [&](uint16_t* d, const float4& v) {
                 *reinterpret_cast<uint2*>(d + o) = make_uint2(pack_16bit2<BF16>(v.x, v.y), pack_16bit2<BF16>(v.z, v.w));
             };

@@ -215,6 +215,11 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int32_t t, const uint2*
         ti.u.rows[0] = static_cast<int32_t>(v.y & 0xffffu);
         ti.u.rows[1] = static_cast<int32_t>(v.y >> 16);
     }
+    MOE_DCHECK(u >= 0 && u < num_units && ti.n >= 0 && ti.n < p.n_tiles, p.status);
+    MOE_DCHECK(ti.u.bx >= 0 && ti.u.bx < p.num_blocks && ti.u.e >= 0 && ti.u.e < p.n_experts, p.status);
+    MOE_DCHECK(ti.u.rows[0] > 0 && ti.u.rows[0] <= BM && ti.u.rows[1] >= 0 && ti.u.rows[1] <= BM, p.status);
+    MOE_DCHECK(static_cast<int64_t>(ti.u.bx) * BM + (ti.u.rows[1] > 0 ? BM + ti.u.rows[1] : ti.u.rows[0]) <= p.rows,
+               p.status);
     return ti;
 }
 
@@ -434,13 +439,18 @@ mx4_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
             // 64 output columns of gate and up, or 128 plain ones
             const int32_t col0 = FORM == MX4_GATE_UP ? ti.n * BM + half * 64 : ti.n * BN + half * 128;
             float w = 1.0f;
-            if (FORM == MX4_DOWN && lane < rows)
-                w = __ldg(p.weights + (static_cast<int64_t>(__ldg(p.offsets + ti.u.e)) + row0 - __ldg(p.padded + ti.u.e) + lane));
+            if (FORM == MX4_DOWN && lane < rows) {
+                const int64_t c = static_cast<int64_t>(__ldg(p.offsets + ti.u.e)) + row0 - __ldg(p.padded + ti.u.e) + lane;
+                MOE_DCHECK(c >= 0 && c < p.valid_total, p.status);
+                w = __ldg(p.weights + c);
+            }
             // one answer for the whole warp, whose TMEM loads are collective
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_tfull, aphase, abort_flag, WAIT_LIMIT_NS))) break;
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
             const bool any = rows > 0 && col0 < p.n;
+            MOE_DCHECK(!any || row0 + (rows < 32 ? rows : 32) <= p.rows, p.status);
+            MOE_DCHECK(FORM != MX4_GATE_UP || col0 + 64 <= p.n, p.status);
             uint16_t* dst = p.out + row0 * p.n + col0;
             auto release = [&]() {
                 // one arrival a warp: 512 single ones, half of them from the other
@@ -670,6 +680,10 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         ti.e = static_cast<int32_t>(v.x >> 16);
         ti.rows = static_cast<int32_t>(v.y & 0xffffu);
         ti.first = static_cast<int32_t>(v.y >> 16) * FEW_ROWS;
+        MOE_DCHECK(u >= 0 && u < num_units && ti.bx < p.num_blocks && ti.e < p.n_experts, p.status);
+        MOE_DCHECK(ti.rows > 0 && ti.rows <= FEW_ROWS && ti.first <= FEW_ROWS &&
+                       static_cast<int64_t>(ti.bx) * BM + ti.first + ti.rows <= p.rows,
+                   p.status);
         return ti;
     };
 
@@ -799,6 +813,7 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                 for (int32_t r0 = odd * 8; r0 < ti.rows && done; r0 += 16) {
                     const int32_t owner = (r0 >> 4) % split;
                     if (owner == crank) continue;
+                    MOE_DCHECK(r0 + 8 <= FEW_ROWS && split * FEW_ROWS * BM * 4 <= p.stages * F::STAGE, p.status);
                     uint32_t v[8];
                     tmem_ld_32x32b_x8(taddr + r0, v);
                     tmem_ld_wait();
@@ -832,6 +847,9 @@ mx4_few_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
                     if (r0 + j >= ti.rows) break;
                     float x = __uint_as_float(v[j]);
                     if (FORM == MX4_GATE_UP) x = x * sigmoid_approx(x) * __uint_as_float(u[j]);
+                    MOE_DCHECK(row0 + r0 + j < p.rows && col < p.n, p.status);
+                    MOE_DCHECK(FORM != MX4_DOWN || (rw + r0 + j >= p.weights && rw + r0 + j < p.weights + p.valid_total),
+                               p.status);
                     if (FORM == MX4_DOWN) x *= __ldg(rw + r0 + j);
                     dst[static_cast<int64_t>(r0 + j) * p.n] = static_cast<uint16_t>(pack_16bit2<BF16>(x, 0.0f) & 0xffffu);
                 }

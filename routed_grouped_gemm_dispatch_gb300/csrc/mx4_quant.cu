@@ -156,6 +156,8 @@ quantize_kernel(const Mx4Quantize a, int64_t pad_rows) {
         word |= __shfl_xor_sync(0xffffffffu, word, 8);
         if (c >= a.cols) continue;                         // a last piece of 128 values is 16 lanes
         auto put = [&](int64_t dst) {
+            MOE_DCHECK(dst >= 0 && dst < (given ? a.n_dest : (a.n_dest + 127) / 128 * 128) && c + 8 <= a.cols, a.status);
+            MOE_DCHECK(!given || (src >= 0 && src < a.n_src), a.status);
             if (given) *reinterpret_cast<uint32_t*>(a.codes + (dst * a.cols + c) / 2) = codes;
             if ((lane & 15) == 0)
                 *reinterpret_cast<uint32_t*>(a.scales + scale_word(dst, c >> 7, k_tiles)) = given ? word : 0u;
