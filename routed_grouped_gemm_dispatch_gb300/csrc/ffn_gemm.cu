@@ -39,9 +39,9 @@
 //    tile and writes d_G and d_U.
 //
 // Measured (GPU time, bf16): forward of 8192 tokens, 7168 / 2048, 380 us = 1.90
-// PFLOP/s, its gradients 780 us = 1.85; training forward of 4097 tokens, 2048 /
-// 2816, 88 us = 1.6 (tensor pipe active 81% in gate and up, 76% in down);
-// gradients of 301 tokens, 45 us.  Bound: the tensor pipe and close behind it the
+// PFLOP/s, its gradients 780 us = 1.85 (calls back to back, under the power cap: 447 and
+// 905); training forward of 4097 tokens, 2048 / 2816, 87.5 us = 1.6 (tensor pipe active
+// 81% in gate and up, 75% in down); gradients of 301 tokens, 44.3 us.  Bound: the tensor pipe and close behind it the
 // operands' way from L2 for many tokens (back to back, the power cap), the chain
 // of fill, K loop, join and epilogue for few hundred.
 //

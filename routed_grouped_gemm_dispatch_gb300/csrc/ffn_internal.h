@@ -47,8 +47,8 @@ struct FfnBackward {
 // Arguments already validated, n_tokens > 0.
 cudaError_t launch_ffn_forward(const FfnForward& a, cudaStream_t stream);
 // The forward for at most FFN_SMALL_TOKENS tokens, by weight rows instead of token
-// tiles: 128 tokens of 7168 / 2048 take 31 us, 129 on the tiles 45 us; beyond, a
-// second tile of tokens made it slower than they are (512 tokens 64 against 50 us).
+// tiles: 128 tokens of 7168 / 2048 take 31 us, 129 on the tiles 39.5 us; beyond, a
+// second tile of tokens was slower than they were (512 tokens 64 against 50 us).
 constexpr int64_t FFN_SMALL_TOKENS = 128;
 cudaError_t launch_ffn_forward_small(const FfnForward& a, cudaStream_t stream);
 cudaError_t launch_ffn_backward(const FfnBackward& a, cudaStream_t stream);

@@ -32,8 +32,9 @@
 //    take a finished tile into registers (128 values a thread) and hand the
 //    accumulator back before they round and store.
 //
-// Measured (GPU time): 4096 x 7168 x 4096 40.6 us = 5.9 PFLOP/s; routed gate_up of
-// 4096 tokens, top-6 of 64 experts, 2048 / 1408, 67 us = 4.2 PFLOP/s at 4.4 TB/s.  Bound:
+// Measured (GPU time): 4096 x 7168 x 4096 40.0 us = 6.0 PFLOP/s; routed gate_up of
+// 4096 tokens, top-6 of 64 experts, 2048 / 1408, 66.4 us = 4.3 PFLOP/s at 4.4 TB/s.  (The
+// dense K = 96 form of the MMA, half as fast again, is not used.)  Bound:
 // the operands' way from L2 (with one MMA in sixteen 35 and 61 us: 48 bytes a cycle
 // and SM), under about 700 cycles a stage where the MMAs alone are 512, and 600
 // between tiles while the accumulator changes hands.
