@@ -197,6 +197,12 @@ moe_status_t moe_router_topk(const uint16_t* x_tokens, int64_t n_tokens, int32_t
                              const uint16_t* router_w, int32_t n_experts, int32_t top_k,
                              int32_t* topk_ids, float* topk_weights, int32_t* status_dev, void* stream);
 
+/* moe_router_topk that also keeps the logits, for the losses and gradients below:
+ *   logits        out, nullable: [n_tokens, n_experts] fp32, 16-byte aligned */
+moe_status_t moe_router_topk_logits(const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
+                                    const uint16_t* router_w, int32_t n_experts, int32_t top_k, int32_t* topk_ids,
+                                    float* topk_weights, float* logits, int32_t* status_dev, void* stream);
+
 /* Flags of moe_fused_forward_ex. */
 #define MOE_RUN_PHASE1   0x1u  /* gate+up GEMM and SiLU·up epilogue into up_logits   */
 #define MOE_RUN_PHASE2   0x2u  /* down GEMM and routed-weight epilogue into out       */
@@ -429,6 +435,106 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
                           int64_t total_valid_tokens, const int32_t* group_sizes, const int32_t* group_offsets,
                           const int32_t* group_padded_offsets, const int32_t* group_idx_for_bx,
                           int64_t num_blocks_m, int32_t dtype, uint16_t* out, int32_t* status_dev, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Training of a routed layer: the router's losses with its per-expert counts, the
+ * router's gradients, and orthogonalised updates of weight matrices.
+ *
+ * Tokens may be packed sequences: seq_offsets [n_seqs + 1] int32, not decreasing, in
+ * [0, n_tokens]; sequence s holds tokens seq_offsets[s] .. seq_offsets[s + 1] - 1.  NULL with
+ * n_seqs = 1: all tokens are one sequence.  token_mask [n_tokens] bytes, nullable: tokens with
+ * 0 do not count.  A token that is masked or in no sequence enters no sum and gets a
+ * gradient of zero, and its logits, ids, routed weights and x are not used whatever they
+ * hold.  Below, T is the number of tokens that count, T_s that of sequence s, k = top_k,
+ * E = n_experts, z the logits, p = softmax(z).  Offsets that decrease or leave the range
+ * set MOE_DEV_BAD_TABLE and leave the outputs undefined.  Negative ids (moe_router_topk's for a token with too few
+ * ranked logits) are skipped, ids >= n_experts too, which set MOE_DEV_BAD_EXPERT_ID.
+ * ------------------------------------------------------------------------- */
+#define MOE_TRAIN_MAX_TOKENS (1 << 24)
+#define MOE_TRAIN_MAX_SEQS   65535
+
+/* Workspace bytes of moe_router_balance; -1 for arguments out of range. */
+int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_seqs);
+
+/* Balance loss, z loss and per-expert counts:
+ *     counts[s, e] = pairs (t, j) of sequence s with id e
+ *     losses[0]    = E / (k·T) · Σ_s 1/T_s · Σ_e counts[s, e] · Σ_t∈s p[t, e]
+ *     losses[1]    = 1/T · Σ_t logsumexp(z[t])²
+ * With one sequence losses[0] is E·Σ_e f_e·P_e, f_e the share of pairs and P_e the mean
+ * probability of expert e; with several, the mean of theirs weighted by T_s.  Both are 0 where T is.
+ *   logits      [n_tokens, n_experts] fp32 (moe_router_topk_logits'), 16-byte aligned
+ *   topk_ids    [n_tokens, top_k] int32
+ *   losses      out: [2] fp32
+ *   counts      out: [n_seqs, n_experts] int32
+ *   seq_tokens  out: [n_seqs + 1] int32, T_s of each sequence, then T
+ *   workspace   device memory of moe_router_balance_workspace_bytes() bytes, caller-owned;
+ *               calls that overlap on the GPU must not share it
+ * Limits: n_experts <= MOE_MAX_EXPERTS, top_k <= min(n_experts, MOE_ROUTER_MAX_TOPK).
+ * Sums over tokens are taken in an order that does not change between calls.  Two kernel launches. */
+moe_status_t moe_router_balance(const float* logits, const int32_t* topk_ids, int64_t n_tokens, int32_t n_experts,
+                                int32_t top_k, const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seqs,
+                                float* losses, int32_t* counts, int32_t* seq_tokens, void* workspace,
+                                size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/* Workspace bytes of moe_router_backward; -1 for arguments out of range. */
+int64_t moe_router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t hidden);
+
+/* Gradients of the router, from those of the routed weights w[t, j] = p[t, id[t, j]] and of
+ * the two losses (in which the counts are constants):
+ *     g[t, e] = d_losses[0]·E / (k·T·T_s)·counts[s, e] + Σ_j [id[t, j] = e]·d_topk_weights[t, j]
+ *     d_z     = p ⊙ (g − Σ_e p·g) + d_losses[1]·2/T·logsumexp(z)·p            fp32
+ *     d_x        = round16( round16(d_z)·router_w )     [n_tokens, hidden]
+ *     d_router_w = round16( round16(d_z)ᵀ·x )           [n_experts, hidden]
+ * All 16-bit arrays are of `dtype` (MOE_DTYPE_F16 or _BF16).  (In fp16 d_z is rounded times a
+ * power of two that depends on its largest magnitude, so none of it is lost to fp16's range.)
+ *   x_tokens        [n_tokens, hidden], hidden a multiple of 8, at most MOE_FFN_MAX_WIDTH
+ *   router_w        [n_experts, hidden]
+ *   logits, topk_ids as in moe_router_balance
+ *   d_topk_weights  nullable: [n_tokens, top_k] fp32
+ *   d_losses        nullable: [2] fp32, in device memory; then counts and seq_tokens of
+ *                   moe_router_balance on the same tokens are needed
+ *   d_x, d_router_w out, written, not added to (d_router_w zeros for n_tokens == 0)
+ *   d_logits        out, nullable: d_z, [n_tokens, n_experts] fp32
+ *   workspace       device memory of moe_router_backward_workspace_bytes() bytes, caller-owned;
+ *                   calls that overlap on the GPU must not share it
+ * Limits as in moe_router_balance.  Three kernel launches, four in fp16; waits and status_dev as
+ * in the feed-forward block. */
+moe_status_t moe_router_backward(int32_t dtype, const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
+                                 const uint16_t* router_w, int32_t n_experts, const float* logits,
+                                 const int32_t* topk_ids, int32_t top_k, const float* d_topk_weights,
+                                 const float* d_losses, const int32_t* counts, const int32_t* seq_tokens,
+                                 const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seqs, void* workspace,
+                                 size_t workspace_bytes, uint16_t* d_x, uint16_t* d_router_w, float* d_logits,
+                                 int32_t* status_dev, void* stream);
+
+#define MOE_ORTHO_MAX_SIZE  (1 << 16)
+#define MOE_ORTHO_MAX_BATCH 65535
+#define MOE_ORTHO_MAX_STEPS 64
+#define MOE_ORTHO_MAX_COEFFICIENT 64.0f
+
+/* Workspace bytes of moe_orthogonalize; -1 for arguments out of range. */
+int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols);
+
+/* Orthogonalised update: for each matrix G of the stack
+ *     X = G / max(‖G‖, eps)                     (Frobenius norm)
+ *     X ← a·X + (b·A + c·A²)·X, A = X·Xᵀ        `steps` times
+ *     out = round16( X )                        bf16
+ * which brings the singular values of G near 1 and keeps its singular vectors (a, b, c =
+ * 3.4445, -4.775, 2.0315 in five steps: into about 0.7 .. 1.2 from 0.01 of the norm on).
+ *   update  [batch, rows, cols], `dtype` MOE_DTYPE_F16, _BF16 or _F32
+ *   out     out: [batch, rows, cols] bf16; must not overlap update
+ * Any rows and cols.  Products are of fp16 operands with fp32 sums: with such coefficients the result is
+ * within about 2e-3 of its root mean square, root mean square, whatever G's spectrum, so no
+ * finer type is offered.  A matrix that holds an infinity or a NaN, or whose norm leaves fp32's
+ * squares (1.8e19), becomes NaN; one of zeros stays zeros; the others of the stack do not see it.
+ * Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude; where they let a norm grow past 2^9 the
+ * result overflows.
+ * workspace: device memory of moe_orthogonalize_workspace_bytes() bytes, caller-owned;
+ * calls that overlap on the GPU must not share it.  2 + 3·steps kernel launches; waits and
+ * status_dev as in the feed-forward block. */
+moe_status_t moe_orthogonalize(int32_t dtype, const void* update, int64_t batch, int32_t rows, int32_t cols, int32_t steps,
+                               float a, float b, float c, float eps, void* workspace, size_t workspace_bytes,
+                               uint16_t* out, int32_t* status_dev, void* stream);
 
 #ifdef __cplusplus
 }

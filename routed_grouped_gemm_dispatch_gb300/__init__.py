@@ -25,6 +25,13 @@ The dense gated feed-forward block (fp16 or bf16):
   gated_ffn_backward(d_out, x, gate_w, up_w, down_w, gate, up, up_logits)
                                                 -> d_x, d_gate_w, d_up_w, d_down_w
 
+Training of a routed layer:
+
+  router_balance(logits, topk_ids)              -> losses, counts, seq_tokens
+  router_backward(x_tokens, router_w, logits, topk_ids, ...)
+                                                -> d_x, d_router_w
+  orthogonalize(update)                         -> the update with singular values near 1
+
 4-bit microscaled values (codes and scales) and products of them:
 
   mx4_quantize(x)                               -> codes, scales
@@ -126,6 +133,22 @@ def lib():
         L.moe_combine_routed.restype = i32
         L.moe_router_topk.argtypes = [P, i64, i32, P, i32, i32, P, P, P, P]
         L.moe_router_topk.restype = i32
+        L.moe_router_topk_logits.argtypes = [P, i64, i32, P, i32, i32, P, P, P, P, P]
+        L.moe_router_topk_logits.restype = i32
+        L.moe_router_balance_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_router_balance_workspace_bytes.restype = i64
+        L.moe_router_balance.argtypes = [P, P, i64, i32, i32, P, P, i32, P, P, P, P, ctypes.c_size_t, P, P]
+        L.moe_router_balance.restype = i32
+        L.moe_router_backward_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_router_backward_workspace_bytes.restype = i64
+        L.moe_router_backward.argtypes = [i32, P, i64, i32, P, i32, P, P, i32, P, P, P, P, P, P, i32, P,
+                                          ctypes.c_size_t, P, P, P, P, P]
+        L.moe_router_backward.restype = i32
+        L.moe_orthogonalize_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_orthogonalize_workspace_bytes.restype = i64
+        L.moe_orthogonalize.argtypes = [i32, P, i64, i32, i32, i32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                        ctypes.c_float, P, ctypes.c_size_t, P, P, P]
+        L.moe_orthogonalize.restype = i32
         L.moe_single_launch_workspace_bytes.argtypes = [i64]
         L.moe_single_launch_workspace_bytes.restype = i64
         L.moe_fused_forward_single_launch.argtypes = [P, i64, i32, P, P, P, i32, i32, P, i64,
@@ -383,9 +406,10 @@ def combine_routed(out, pair_rows, y=None, stream=None):
 
 
 def router_topk(x_tokens, router_w, top_k: int, topk_ids=None, topk_weights=None,
-                status=None, stream=None):
+                status=None, stream=None, logits=None):
     """Router logits (x·W_gᵀ), softmax over all experts, top-k: returns
-    (topk_ids int32 [T, k], topk_weights fp32 [T, k])."""
+    (topk_ids int32 [T, k], topk_weights fp32 [T, k]).  ``logits`` (fp32 [T, n_experts])
+    receives the logits, which router_balance and router_backward read."""
     import torch
     x = _dev(x_tokens, "x_tokens", torch.float16, 2)
     w = _dev(router_w, "router_w", torch.float16, 2)
@@ -399,6 +423,11 @@ def router_topk(x_tokens, router_w, top_k: int, topk_ids=None, topk_weights=None
     if topk_weights is None:
         topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
         _used_on(stream, topk_weights)
+    if logits is not None:
+        _shaped(logits, "logits", torch.float32, (T, E))
+        _check(lib().moe_router_topk_logits(_ptr(x), T, H, _ptr(w), E, int(top_k), _ptr(topk_ids), _ptr(topk_weights),
+                                            _ptr(logits), _ptr(status), _stream(stream)), "moe_router_topk_logits")
+        return topk_ids, topk_weights
     st = lib().moe_router_topk(_ptr(x), T, H, _ptr(w), E, int(top_k), _ptr(topk_ids),
                                _ptr(topk_weights), _ptr(status), _stream(stream))
     _check(st, "moe_router_topk")
@@ -715,3 +744,159 @@ def mx4_down(h, h_scales, down, down_scales, routed_expert_weights, group_sizes,
                               _ptr(group_sizes), _ptr(offs), _ptr(group_padded_offsets), _ptr(group_idx_for_bx), m,
                               code, _ptr(out), _status(status), _stream(stream)), "moe_mx4_down")
     return out
+
+
+def _routing(logits, topk_ids, token_mask, seq_offsets):
+    """Checked sizes (T, E, k, sequences) of what the router's losses and gradients read."""
+    import torch
+    T, E = _dev(logits, "logits", torch.float32, 2).shape
+    k = _dev(topk_ids, "topk_ids", torch.int32, 2).shape[1]
+    if topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must have a row per token, {T}, got {topk_ids.shape[0]}")
+    if token_mask is not None:
+        dt = getattr(token_mask, "dtype", None)
+        if dt not in (torch.bool, torch.uint8):
+            raise TypeError(f"token_mask must be bool or uint8, got {dt}")
+        _shaped(token_mask, "token_mask", dt, (T,))
+    if seq_offsets is None:
+        return T, E, k, 1
+    n = _dev(seq_offsets, "seq_offsets", torch.int32, 1).numel()
+    if n < 2:
+        raise ValueError(f"seq_offsets must hold the bounds of a sequence at least, got {n} of them")
+    return T, E, k, n - 1
+
+
+def _workspace(t, nbytes, device, stream):
+    """A workspace of that many bytes, or the given one."""
+    import torch
+    if t is None:
+        t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        _used_on(stream, t)
+    else:
+        _dev(t, "workspace", getattr(t, "dtype", None))
+    return t
+
+
+def router_balance(logits, topk_ids, token_mask=None, seq_offsets=None, losses=None, counts=None, seq_tokens=None,
+                   workspace=None, status=None, stream=None):
+    """The router's losses and per-expert counts from its logits [T, E] fp32 and chosen
+    experts [T, k] int32 (router_topk's): returns (losses, counts, seq_tokens).
+
+    losses [2] fp32: the balance loss E/(k·T)·Σ_s 1/T_s·Σ_e counts[s, e]·Σ_t p[t, e] and the z loss
+    mean(logsumexp(z)²).  counts [S, E] int32: pairs of sequence s at expert e.  seq_tokens
+    [S + 1] int32: the tokens that count in each sequence, then in all.
+    ``token_mask`` [T] (bool or uint8): tokens with 0 do not count.  ``seq_offsets`` [S + 1]
+    int32: packed sequences, each balanced by itself (one of all tokens without);
+    tokens in none do not count.  ``workspace``: a device tensor of at least
+    router_balance_workspace_bytes(T, E, S) bytes."""
+    import torch
+    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets)
+    dev = logits.device
+    outs = []
+    for t, name, dt, shape in ((losses, "losses", torch.float32, (2,)), (counts, "counts", torch.int32, (S, E)),
+                               (seq_tokens, "seq_tokens", torch.int32, (S + 1,))):
+        if t is None:
+            t = torch.empty(shape, dtype=dt, device=dev)
+            _used_on(stream, t)
+        else:
+            _shaped(t, name, dt, shape)
+        outs.append(t)
+    workspace = _workspace(workspace, router_balance_workspace_bytes(T, E, S), dev, stream)
+    _check(lib().moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, _ptr(token_mask), _ptr(seq_offsets),
+                                    S, *[t.data_ptr() for t in outs], workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
+           "moe_router_balance")
+    return tuple(outs)
+
+
+def router_balance_workspace_bytes(n_tokens: int, n_experts: int, n_seqs: int = 1) -> int:
+    return int(lib().moe_router_balance_workspace_bytes(int(n_tokens), int(n_experts), int(n_seqs)))
+
+
+def router_backward(x_tokens, router_w, logits, topk_ids, d_topk_weights=None, d_losses=None, counts=None,
+                    seq_tokens=None, token_mask=None, seq_offsets=None, d_x=None, d_router_w=None, d_logits=None,
+                    workspace=None, status=None, stream=None):
+    """Gradients of the router from those of its routed weights (``d_topk_weights`` [T, k] fp32) and of
+    router_balance's losses (``d_losses`` [2] fp32 on the device, with the ``counts``
+    and ``seq_tokens`` it returned), either or both: returns (d_x, d_router_w) in the inputs' type
+    and shapes, float16 or bfloat16; hidden a multiple of 8.  ``token_mask`` and
+    ``seq_offsets`` as in router_balance: a token that does not count has a gradient of zero.
+    ``d_logits`` (fp32 [T, E]) receives the gradients of the logits.  Supplied buffers are
+    written, not added to.  ``workspace``: a device tensor of at least
+    router_backward_workspace_bytes(T, E, hidden) bytes."""
+    import torch
+    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets)
+    dt = getattr(x_tokens, "dtype", None)
+    code = _dtype_code(dt, "x_tokens")
+    H = _dev(x_tokens, "x_tokens", dt, 2).shape[1]
+    if x_tokens.shape[0] != T:
+        raise ValueError(f"x_tokens must have a row per token, {T}, got {x_tokens.shape[0]}")
+    _shaped(router_w, "router_w", dt, (E, H))
+    if d_topk_weights is not None:
+        _shaped(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
+    if d_losses is not None:
+        _shaped(d_losses, "d_losses", torch.float32, (2,))
+        if counts is None or seq_tokens is None:
+            raise ValueError("d_losses goes with the counts and seq_tokens that router_balance returned")
+    if counts is not None:
+        _shaped(counts, "counts", torch.int32, (S, E))
+    if seq_tokens is not None:
+        _shaped(seq_tokens, "seq_tokens", torch.int32, (S + 1,))
+    if d_logits is not None:
+        _shaped(d_logits, "d_logits", torch.float32, (T, E))
+    grads = []
+    for t, name, like in ((d_x, "d_x", x_tokens), (d_router_w, "d_router_w", router_w)):
+        if t is None:
+            t = torch.empty_like(like)
+            _used_on(stream, t)
+        else:
+            _shaped(t, name, dt, like.shape)
+        grads.append(t)
+    workspace = _workspace(workspace, router_backward_workspace_bytes(T, E, H), logits.device, stream)
+    _check(lib().moe_router_backward(code, x_tokens.data_ptr(), T, H, router_w.data_ptr(), E, logits.data_ptr(),
+                                     topk_ids.data_ptr(), k, _ptr(d_topk_weights), _ptr(d_losses), _ptr(counts),
+                                     _ptr(seq_tokens), _ptr(token_mask), _ptr(seq_offsets), S, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), grads[0].data_ptr(),
+                                     grads[1].data_ptr(), _ptr(d_logits), _status(status), _stream(stream)),
+           "moe_router_backward")
+    return tuple(grads)
+
+
+def router_backward_workspace_bytes(n_tokens: int, n_experts: int, hidden: int) -> int:
+    return int(lib().moe_router_backward_workspace_bytes(int(n_tokens), int(n_experts), int(hidden)))
+
+
+def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None,
+                  workspace=None, status=None, stream=None):
+    """Orthogonalised update: X = update / max(‖update‖, eps), then ``steps`` times X ← a·X + (b·A + c·A²)·X
+    with A = X·Xᵀ and a, b, c the ``coefficients``: the singular vectors stay and the
+    singular values come near 1.  ``update`` [rows, cols] or a stack [batch, rows, cols] of any sizes,
+    float16, bfloat16 or float32 (a gradient, or a momentum); returns bfloat16 of its shape
+    (``out`` may be supplied).  Each matrix of a stack is taken by itself.  Products
+    are of 16-bit operands with fp32 sums: the result is within about 2e-3 of its size.
+    ``workspace``: a device tensor of at least orthogonalize_workspace_bytes(batch, rows, cols) bytes."""
+    import torch
+    dt = getattr(update, "dtype", None)
+    code = _dtype_code(dt, "update", f32=True)
+    shape = _dev(update, "update", dt).shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"update must have 2 or 3 dims, got {len(shape)}")
+    rows, cols = shape[-2:]
+    batch = shape[0] if len(shape) == 3 else 1
+    if rows == 0 or cols == 0:
+        raise ValueError(f"update must have rows and columns, got {tuple(shape)}")
+    a, b, c = (float(v) for v in coefficients)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=update.device)
+        _used_on(stream, out)
+    else:
+        _shaped(out, "out", torch.bfloat16, shape)
+    workspace = _workspace(workspace, orthogonalize_workspace_bytes(batch, rows, cols), update.device, stream)
+    _check(lib().moe_orthogonalize(code, update.data_ptr(), batch, rows, cols, int(steps), a, b, c, float(eps),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
+                                   _status(status), _stream(stream)), "moe_orthogonalize")
+    return out
+
+
+def orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(lib().moe_orthogonalize_workspace_bytes(int(batch), int(rows), int(cols)))

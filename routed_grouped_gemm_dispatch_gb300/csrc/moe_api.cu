@@ -9,6 +9,7 @@
 #include "../../include/moe_gb300.h"
 #include "ffn_internal.h"
 #include "moe_internal.h"
+#include "train_internal.h"
 #include "mx4_internal.h"
 
 namespace {
@@ -135,15 +136,22 @@ moe_status_t moe_combine_routed(const uint16_t* out, int64_t total_padded_tokens
 moe_status_t moe_router_topk(const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
                              const uint16_t* router_w, int32_t n_experts, int32_t top_k, int32_t* topk_ids,
                              float* topk_weights, int32_t* status_dev, void* stream) {
+    return moe_router_topk_logits(x_tokens, n_tokens, hidden, router_w, n_experts, top_k, topk_ids, topk_weights,
+                                  nullptr, status_dev, stream);
+}
+
+moe_status_t moe_router_topk_logits(const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
+                                    const uint16_t* router_w, int32_t n_experts, int32_t top_k, int32_t* topk_ids,
+                                    float* topk_weights, float* logits, int32_t* status_dev, void* stream) {
     if (n_tokens < 0 || hidden <= 0 || hidden % 128 != 0) return MOE_ERR_SHAPE;
     if (n_experts <= 0 || n_experts > MOE_ROUTER_MAX_EXPERTS) return MOE_ERR_LIMIT;
     if (top_k <= 0 || top_k > n_experts || top_k > MOE_ROUTER_MAX_TOPK) return MOE_ERR_LIMIT;
     if (n_tokens == 0) return MOE_OK;
     if (!x_tokens || !router_w || !topk_ids || !topk_weights) return MOE_ERR_NULL;
-    if (!aligned16(x_tokens) || !aligned16(router_w)) return MOE_ERR_ALIGN;
+    if (!aligned16(x_tokens) || !aligned16(router_w) || !aligned16(logits)) return MOE_ERR_ALIGN;
     if (moe_status_t s = check_device()) return s;
     return from_cuda(moe::launch_router(x_tokens, n_tokens, hidden, router_w, n_experts, top_k, topk_ids,
-                                        topk_weights, status_dev, static_cast<cudaStream_t>(stream)));
+                                        topk_weights, logits, status_dev, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -540,6 +548,128 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
     m.out = out;
     m.status = status_dev;
     return run_mx4_product(m, true, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// training of a routed layer
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Sizes and limits of what the losses and gradients know of the tokens.
+moe_status_t check_routing(const moe::Routing& r) {
+    if (r.n_tokens < 0 || r.n_experts <= 0 || r.top_k <= 0 || r.n_seqs <= 0 || r.top_k > r.n_experts)
+        return MOE_ERR_SHAPE;
+    if (r.n_tokens > MOE_TRAIN_MAX_TOKENS || r.n_experts > MOE_MAX_EXPERTS || r.top_k > MOE_ROUTER_MAX_TOPK ||
+        r.n_seqs > MOE_TRAIN_MAX_SEQS)
+        return MOE_ERR_LIMIT;
+    if (!r.seq_offsets && r.n_seqs != 1) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
+    if (n_tokens < 0 || n_tokens > MOE_TRAIN_MAX_TOKENS || n_experts <= 0 || n_experts > MOE_MAX_EXPERTS || n_seqs <= 0 ||
+        n_seqs > MOE_TRAIN_MAX_SEQS)
+        return -1;
+    return moe::router_balance_workspace_bytes(n_tokens, n_experts, n_seqs);
+}
+
+moe_status_t moe_router_balance(const float* logits, const int32_t* topk_ids, int64_t n_tokens, int32_t n_experts,
+                                int32_t top_k, const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seqs,
+                                float* losses, int32_t* counts, int32_t* seq_tokens, void* workspace,
+                                size_t workspace_bytes, int32_t* status_dev, void* stream) {
+    moe::RouterBalance a{};
+    a.r = moe::Routing{logits, topk_ids, n_tokens, n_experts, top_k, token_mask, seq_offsets, n_seqs};
+    if (moe_status_t s = check_routing(a.r)) return s;
+    if ((n_tokens > 0 && (!logits || !topk_ids)) || !losses || !counts || !seq_tokens) return MOE_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+    if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_router_balance_workspace_bytes(n_tokens, n_experts, n_seqs))
+        return MOE_ERR_WORKSPACE;
+    if (moe_status_t s = check_device()) return s;
+    a.losses = losses;
+    a.counts = counts;
+    a.seq_tokens = seq_tokens;
+    a.workspace = workspace;
+    a.status = status_dev;
+    return from_cuda(moe::launch_router_balance(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
+    if (n_tokens < 0 || n_tokens > MOE_TRAIN_MAX_TOKENS || n_experts <= 0 || n_experts > MOE_MAX_EXPERTS || hidden <= 0 ||
+        hidden > MOE_FFN_MAX_WIDTH)
+        return -1;
+    return moe::router_backward_workspace_bytes(n_tokens, n_experts, hidden);
+}
+
+moe_status_t moe_router_backward(int32_t dtype, const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
+                                 const uint16_t* router_w, int32_t n_experts, const float* logits,
+                                 const int32_t* topk_ids, int32_t top_k, const float* d_topk_weights,
+                                 const float* d_losses, const int32_t* counts, const int32_t* seq_tokens,
+                                 const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seqs, void* workspace,
+                                 size_t workspace_bytes, uint16_t* d_x, uint16_t* d_router_w, float* d_logits,
+                                 int32_t* status_dev, void* stream) {
+    moe::RouterBackward a{};
+    a.r = moe::Routing{logits, topk_ids, n_tokens, n_experts, top_k, token_mask, seq_offsets, n_seqs};
+    if (dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_BF16) return MOE_ERR_SHAPE;
+    if (moe_status_t s = check_routing(a.r)) return s;
+    if (hidden <= 0 || hidden % 8 != 0) return MOE_ERR_SHAPE;
+    if (hidden > MOE_FFN_MAX_WIDTH) return MOE_ERR_LIMIT;
+    if (!d_router_w || (d_losses && (!counts || !seq_tokens))) return MOE_ERR_NULL;
+    if (n_tokens > 0 && (!x_tokens || !router_w || !logits || !topk_ids || !d_x)) return MOE_ERR_NULL;
+    if (!aligned16(x_tokens) || !aligned16(router_w) || !aligned16(logits) || !aligned16(d_x) || !aligned16(d_router_w) ||
+        !aligned16(d_logits) || !aligned16(workspace))
+        return MOE_ERR_ALIGN;
+    if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_router_backward_workspace_bytes(n_tokens, n_experts, hidden))
+        return MOE_ERR_WORKSPACE;
+    if (moe_status_t s = check_device()) return s;
+    a.bf16 = dtype == MOE_DTYPE_BF16;
+    a.x = x_tokens;
+    a.hidden = hidden;
+    a.router_w = router_w;
+    a.d_topk_weights = d_topk_weights;
+    a.d_losses = d_losses;
+    a.counts = counts;
+    a.seq_tokens = seq_tokens;
+    a.d_x = d_x;
+    a.d_router_w = d_router_w;
+    a.d_logits = d_logits;
+    a.workspace = workspace;
+    a.status = status_dev;
+    return from_cuda(moe::launch_router_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols) {
+    if (batch < 0 || rows <= 0 || cols <= 0 || batch > MOE_ORTHO_MAX_BATCH || rows > MOE_ORTHO_MAX_SIZE ||
+        cols > MOE_ORTHO_MAX_SIZE)
+        return -1;
+    return moe::orthogonalize_workspace_bytes(batch, rows, cols);
+}
+
+moe_status_t moe_orthogonalize(int32_t dtype, const void* update, int64_t batch, int32_t rows, int32_t cols, int32_t steps,
+                               float a, float b, float c, float eps, void* workspace, size_t workspace_bytes,
+                               uint16_t* out, int32_t* status_dev, void* stream) {
+    if (dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_SHAPE;
+    // (a NaN fails the comparisons too)
+    if (batch < 0 || rows <= 0 || cols <= 0 || steps <= 0 || !(eps >= 0.0f) || !(eps <= 3.0e38f)) return MOE_ERR_SHAPE;
+    for (float v : {a, b, c})
+        if (!(v >= -MOE_ORTHO_MAX_COEFFICIENT && v <= MOE_ORTHO_MAX_COEFFICIENT)) return MOE_ERR_LIMIT;
+    if (batch > MOE_ORTHO_MAX_BATCH || rows > MOE_ORTHO_MAX_SIZE || cols > MOE_ORTHO_MAX_SIZE || steps > MOE_ORTHO_MAX_STEPS)
+        return MOE_ERR_LIMIT;
+    if (batch * ((rows + 127) / 128) * ((cols + 127) / 128) > (int64_t{1} << 30)) return MOE_ERR_LIMIT;
+    if (batch == 0) return MOE_OK;
+    if (!update || !out) return MOE_ERR_NULL;
+    if (!aligned16(update) || !aligned16(out) || !aligned16(workspace)) return MOE_ERR_ALIGN;
+    if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_orthogonalize_workspace_bytes(batch, rows, cols))
+        return MOE_ERR_WORKSPACE;
+    if (moe_status_t s = check_device()) return s;
+    moe::Orthogonalize o{dtype, update, batch, rows, cols, steps, a, b, c, eps, out, workspace, status_dev};
+    return from_cuda(moe::launch_orthogonalize(o, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -85,6 +85,7 @@ struct RouterParams {
     int32_t off_bars;
     int32_t* topk_ids;
     float* topk_weights;
+    float* logits;         // nullable: [n_tokens, n_experts]
     int32_t* status;
 };
 
@@ -615,6 +616,22 @@ router_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     }
                 }
             }
+            // the logits themselves, for a loss and its gradient
+            if (p.logits != nullptr && live) {
+                float* out = p.logits + t * n_e;
+                for (int q = 0; q < nq; ++q) {
+                    const float4 v = chunk(q);
+                    const int e0 = 4 * (j + q * T);
+                    if ((n_e & 3) == 0) {
+                        if (e0 < n_e) *reinterpret_cast<float4*>(out + e0) = v;
+                    } else {
+                        if (e0 < n_e) out[e0] = v.x;
+                        if (e0 + 1 < n_e) out[e0 + 1] = v.y;
+                        if (e0 + 2 < n_e) out[e0 + 2] = v.z;
+                        if (e0 + 3 < n_e) out[e0 + 3] = v.w;
+                    }
+                }
+            }
         }
     }
 
@@ -666,7 +683,7 @@ bool router_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, 
 
 cudaError_t launch_router(const uint16_t* x, int64_t n_tokens, int32_t hidden, const uint16_t* router_w,
                           int32_t n_experts, int32_t top_k, int32_t* topk_ids, float* topk_weights,
-                          int32_t* status, cudaStream_t stream) {
+                          float* logits, int32_t* status, cudaStream_t stream) {
     if (n_tokens == 0) return cudaSuccess;
     if (!router_encode_fn()) return cudaErrorNotSupported;
     RouterParams p{};
@@ -680,6 +697,7 @@ cudaError_t launch_router(const uint16_t* x, int64_t n_tokens, int32_t hidden, c
     p.k_blocks = hidden / R_BK;
     p.topk_ids = topk_ids;
     p.topk_weights = topk_weights;
+    p.logits = logits;
     p.status = status;
     CUtensorMap map_x, map_w;
     if (!router_map(&map_x, x, static_cast<uint64_t>(n_tokens), static_cast<uint64_t>(hidden), R_BM) ||

@@ -1,0 +1,324 @@
+// The router's gradients: from those of the logits (router_loss.cu), rounded to 16 bits,
+//     d_x = d_z·W_g       [T, H]     K = experts
+//     d_W = d_zᵀ·x        [E, H]     K = tokens
+// in one launch of tiles of 256 x 256 (pair_tiles.cuh), and a second that adds up the parts of
+// d_W.  x is read once, d_x written once; d_z and W_g stay in L2.
+//
+//  * d_W has few tiles (DeepSeek-V3-shaped: 28) and a long K, so its steps are laid end to
+//    end, tile after tile, and cut into as many equal pieces as there are pairs.  The sums
+//    of a pair's part of a tile go to fp32 slot pair + tile: from one part to the next
+//    either of them grows, so no two share a slot.  They are added in pair order.
+//  * Operands are read as they lie: d_z by token rows for d_x, transposed for d_W.
+//  * Rows of x whose token does not count are cleared in shared memory (their d_z is zero, but
+//    zero times a NaN is not).
+//
+// Rounding: d_z once (an operand of 16-bit products), d_x and d_W once from fp32.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/moe_gb300.h"
+#include "moe_internal.h"
+#include "pair_tiles.cuh"
+#include "train_internal.h"
+
+namespace moe {
+namespace {
+
+using pairs::Tile;
+
+constexpr int TILE = 256;
+constexpr int MIN_PART = 8;          // K steps of a part of d_W at least
+
+struct GradProducts {
+    int32_t total_tiles, n_maps;
+    int32_t* status;
+    int64_t n_tokens;
+    int32_t n_experts, hidden;
+    int32_t x_tiles_n;               // column tiles, of both products
+    int32_t w_tiles;                 // tiles of d_W
+    int32_t w_steps;                 // K steps of one
+    int32_t w_pairs;                 // pieces that all of them are cut into
+    int32_t w_parts;                 // tiles that a piece touches at most
+    uint16_t* d_x;
+    float* slots;                    // [w_pairs + w_tiles][256][256]
+    const float* scale;              // [1]: what undoes the power of two in d_z
+    const uint32_t* valid;           // a bit per token; null: all count
+};
+
+// Steps of d_W before piece i.
+__host__ __device__ __forceinline__ int64_t piece_start(int32_t i, int32_t w_pairs, int64_t all_steps) {
+    return all_steps * i / w_pairs;
+}
+
+// Part `part` of piece `piece` of d_W: a tile and steps of it (none: steps 0).
+struct Part {
+    int32_t tile, k0, steps;
+};
+__device__ __forceinline__ Part part_of(const GradProducts& p, int32_t piece, int32_t part) {
+    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
+    const int64_t b0 = piece_start(piece, p.w_pairs, all), b1 = piece_start(piece + 1, p.w_pairs, all);
+    const int32_t tile = static_cast<int32_t>(b0 / p.w_steps) + part;
+    const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps;
+    const int64_t from = b0 > t0 ? b0 : t0;
+    const int64_t to = b1 < t0 + p.w_steps ? b1 : t0 + p.w_steps;
+    return Part{tile, static_cast<int32_t>(from - t0), to > from ? static_cast<int32_t>(to - from) : 0};
+}
+
+template <bool BF16_, bool MASKED_>
+struct GradOp {
+    static constexpr int BN = TILE;
+    static constexpr bool BF16 = BF16_;
+    static constexpr bool MASKED = MASKED_;
+    using Params = GradProducts;
+    enum { DZ, W_T, DZ_T, X_T, MAPS };
+
+    // tiles: first the parts of d_W, part by part over the pieces, then d_x row by row
+    static __device__ __forceinline__ Tile tile(const Params& p, int32_t t) {
+        Tile ti{};
+        const int32_t parts = p.w_pairs * p.w_parts;
+        if (t < parts) {
+            const Part w = part_of(p, t % p.w_pairs, t / p.w_pairs);
+            const int32_t m = w.tile / p.x_tiles_n;
+            ti.a_map = DZ_T;
+            ti.b_map = X_T;
+            ti.a_mn = ti.b_mn = true;
+            ti.a_row = m * TILE;
+            ti.b_row = (w.tile - m * p.x_tiles_n) * TILE;
+            ti.k0 = w.k0;
+            ti.steps = w.steps;
+        } else {
+            const int32_t m = (t - parts) / p.x_tiles_n;
+            ti.a_map = DZ;
+            ti.b_map = W_T;
+            ti.b_mn = true;
+            ti.a_row = m * TILE;
+            ti.b_row = (t - parts - m * p.x_tiles_n) * TILE;
+            ti.steps = (p.n_experts + pairs::BK - 1) / pairs::BK;
+        }
+        return ti;
+    }
+    static __device__ __forceinline__ bool masked(const Params&, const Tile& ti) { return ti.b_map == X_T; }
+    static __device__ __forceinline__ void valid64(const Params& p, int32_t step, uint32_t& w0, uint32_t& w1) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.valid) + step);
+        w0 = v.x;
+        w1 = v.y;
+    }
+
+    struct Finish {
+        const Params& p;
+        uint8_t* staging;
+        int32_t row, lane;           // first of the warp's rows inside the tile
+        float inv;
+        bool part;
+        int64_t at;                  // of the warp's first row in d_x, or in the slots
+        int32_t rows, cols;
+
+        __device__ __forceinline__ Finish(const Params& p_, uint8_t* staging_, int32_t row_, int, int lane_)
+            : p(p_), staging(staging_), row(row_), lane(lane_) {
+            inv = __ldg(p.scale + 1);
+        }
+        __device__ __forceinline__ bool before(int32_t t) {
+            const int32_t parts = p.w_pairs * p.w_parts;
+            part = t < parts;
+            if (part) {
+                const int32_t piece = t % p.w_pairs;
+                const Part w = part_of(p, piece, t / p.w_pairs);
+                at = (static_cast<int64_t>(piece + w.tile) * TILE + row) * TILE;
+                rows = 32;
+                cols = TILE;
+                MOE_DCHECK(w.steps == 0 || (w.tile < p.w_tiles && piece + w.tile < p.w_pairs + p.w_tiles), p.status);
+                return w.steps > 0;
+            }
+            const int32_t m = (t - parts) / p.x_tiles_n;
+            const int32_t col = (t - parts - m * p.x_tiles_n) * TILE;
+            const int64_t first = static_cast<int64_t>(m) * TILE + row;
+            const int64_t left = p.n_tokens - first;
+            rows = left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left));
+            cols = p.hidden - col;
+            at = first * p.hidden + col;
+            return true;
+        }
+        __device__ __forceinline__ void pass(int c, uint32_t taddr) {
+            if (rows <= 0 || c * 64 >= cols) return;
+            uint4 el[8];
+            if (part) {
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + hh * 32, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) el[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    // 32 fp32 columns are a line of 64 16-bit ones
+                    store_staged_64(el, staging, reinterpret_cast<uint16_t*>(p.slots + at + c * 64 + hh * 32), 2 * TILE,
+                                    lane, 32, 64);
+                }
+                return;
+            }
+            MOE_DCHECK(at >= 0 && at + static_cast<int64_t>(rows - 1) * p.hidden + c * 64 +
+                                      (cols - c * 64 < 64 ? cols - c * 64 : 64) <= p.n_tokens * p.hidden,
+                       p.status);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + hh * 32, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = pack_16bit2<BF16>(__uint_as_float(v[8 * i + 2 * j]) * inv,
+                                                 __uint_as_float(v[8 * i + 2 * j + 1]) * inv);
+                    el[4 * hh + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            store_staged_64(el, staging, p.d_x + at + c * 64, p.hidden, lane, rows, cols - c * 64);
+        }
+    };
+};
+
+// d_W from its parts: a thread has four columns of a row.
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_parts_kernel(const GradProducts p, uint16_t* d_w) {
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) >> 6;
+    const int32_t at = (static_cast<int32_t>(blockIdx.x) & 63) * 1024 + static_cast<int32_t>(threadIdx.x) * 4;
+    const int32_t m = tile / p.x_tiles_n;
+    const int32_t e = m * TILE + (at >> 8), h = (tile - m * p.x_tiles_n) * TILE + (at & 255);
+    if (e >= p.n_experts || h >= p.hidden) return;
+    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
+    const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps, t1 = t0 + p.w_steps;
+    // the piece that holds the tile's first step, and the ones after it
+    int32_t i = static_cast<int32_t>(t0 * p.w_pairs / all);
+    while (piece_start(i + 1, p.w_pairs, all) <= t0) ++i;
+    const float inv = __ldg(p.scale + 1);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (; i < p.w_pairs && piece_start(i, p.w_pairs, all) < t1; ++i) {
+        MOE_DCHECK(i + tile < p.w_pairs + p.w_tiles, p.status);
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p.slots + static_cast<int64_t>(i + tile) * TILE * TILE + at));
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(d_w + static_cast<int64_t>(e) * p.hidden + h) =
+        make_uint2(pack_16bit2<BF16>(v.x * inv, v.y * inv), pack_16bit2<BF16>(v.z * inv, v.w * inv));
+}
+
+struct GradLayout {
+    int32_t ld;
+    int64_t dz, scale, block_max, valid, slots, bytes;
+};
+
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+int32_t weight_tiles(int32_t n_experts, int32_t hidden) {
+    return pairs::ceil_div(n_experts, TILE) * pairs::ceil_div(hidden, TILE);
+}
+
+// Pieces that the steps of d_W are cut into: one a pair, of MIN_PART steps at least, never
+// fewer than there are tiles (or pairs).
+constexpr int32_t MAX_PAIRS = 76;
+int32_t weight_pieces(int64_t n_tokens, int32_t tiles, int32_t pairs_) {
+    const int64_t steps = static_cast<int64_t>(tiles) * pairs::ceil_div(n_tokens, pairs::BK);
+    int64_t n = steps / MIN_PART;
+    if (n < tiles) n = tiles;
+    return static_cast<int32_t>(n < pairs_ ? n : pairs_);
+}
+
+GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
+    GradLayout l;
+    l.ld = (n_experts + 7) / 8 * 8;
+    int64_t at = 0;
+    auto take = [&at](int64_t n) {
+        const int64_t r = at;
+        at += round256(n);
+        return r;
+    };
+    l.dz = take(n_tokens * l.ld * 2);
+    l.scale = take(8);
+    l.block_max = take(int64_t{4} * router_grad_blocks(n_tokens));
+    l.valid = take((n_tokens + 63) / 64 * 8);
+    const int32_t tiles = weight_tiles(n_experts, hidden);
+    l.slots = take(static_cast<int64_t>(weight_pieces(n_tokens, tiles, MAX_PAIRS) + tiles) * TILE * TILE * 4);
+    l.bytes = at;
+    return l;
+}
+
+template <bool BF16, bool MASKED>
+cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, float* slots, cudaStream_t stream) {
+    using Op = GradOp<BF16, MASKED>;
+    if (!tensor_map_encoder()) return cudaErrorNotSupported;
+    const int64_t T = a.r.n_tokens;
+    const int32_t E = a.r.n_experts, H = a.hidden;
+    pairs::Maps maps;
+    if (!pairs::map_3d(&maps.m[Op::DZ], g.dz, 1, T, E, g.ld, pairs::BM) ||
+        !pairs::map_3d(&maps.m[Op::W_T], a.router_w, 1, E, H, H, pairs::BK) ||
+        !pairs::map_3d(&maps.m[Op::DZ_T], g.dz, 1, T, E, g.ld, pairs::BK) ||
+        !pairs::map_3d(&maps.m[Op::X_T], a.x, 1, T, H, H, pairs::BK))
+        return cudaErrorInvalidValue;
+    int n_pairs = pairs::resident_pairs<Op>();
+    if (n_pairs == 0) return cudaErrorNoDevice;
+    if (n_pairs > MAX_PAIRS) n_pairs = MAX_PAIRS;
+    GradProducts p{};
+    p.n_maps = Op::MAPS;
+    p.status = a.status;
+    p.n_tokens = T;
+    p.n_experts = E;
+    p.hidden = H;
+    p.x_tiles_n = pairs::ceil_div(H, TILE);
+    p.w_tiles = weight_tiles(E, H);
+    p.w_steps = pairs::ceil_div(T, pairs::BK);
+    p.w_pairs = weight_pieces(T, p.w_tiles, n_pairs);
+    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
+    p.w_parts = static_cast<int32_t>((all + p.w_pairs - 1) / p.w_pairs + p.w_steps - 2) / p.w_steps + 1;
+    p.total_tiles = p.w_pairs * p.w_parts + pairs::ceil_div(T, TILE) * p.x_tiles_n;
+    p.d_x = a.d_x;
+    p.slots = slots;
+    p.scale = g.scale;
+    p.valid = MASKED ? g.valid : nullptr;
+    cudaError_t err = pairs::launch<Op>(maps, p, stream);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles) * 64);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<BF16>, p, a.d_router_w);
+}
+
+}  // namespace
+
+int64_t router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
+    return grad_layout(n_tokens, n_experts, hidden).bytes;
+}
+
+cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream) {
+    if (a.r.n_tokens == 0)
+        return cudaMemsetAsync(a.d_router_w, 0, static_cast<size_t>(a.r.n_experts) * a.hidden * 2, stream);
+    const GradLayout l = grad_layout(a.r.n_tokens, a.r.n_experts, a.hidden);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    LogitGradients g;
+    g.dz = reinterpret_cast<uint16_t*>(ws + l.dz);
+    g.ld = l.ld;
+    g.scale = reinterpret_cast<float*>(ws + l.scale);
+    g.block_max = reinterpret_cast<float*>(ws + l.block_max);
+    g.valid = reinterpret_cast<uint32_t*>(ws + l.valid);
+    cudaError_t err = launch_logit_gradients(a, g, stream);
+    if (err != cudaSuccess) return err;
+    float* slots = reinterpret_cast<float*>(ws + l.slots);
+    const bool masked = a.r.token_mask != nullptr || a.r.seq_offsets != nullptr;
+    if (a.bf16)
+        return masked ? launch_products<true, true>(a, g, slots, stream) : launch_products<true, false>(a, g, slots, stream);
+    return masked ? launch_products<false, true>(a, g, slots, stream) : launch_products<false, false>(a, g, slots, stream);
+}
+
+}  // namespace moe
