@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(SUM_THREADS) square_sum_kernel(const Prepare p
 template <int DTYPE, bool TALL>
 __global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
     __shared__ float tile[64][65];
-    __shared__ double part[8];
+    __shared__ float part[8];
     __shared__ float power;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int64_t matrix = blockIdx.z;
-    double sum = 0.0;
+    float sum = 0.0f;
     for (int i = threadIdx.x; i < p.sum_blocks; i += 256) sum += p.sums[matrix * p.sum_blocks + i];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -139,17 +139,13 @@ __global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 8; ++w) sum += part[w];
-        double norm = sqrt(sum);
+        float norm = sqrtf(sum);
         if (norm < p.eps) norm = p.eps;                       // a NaN stays
         float two_e = 0.0f, rest = 0.0f;
-        if (norm != 0.0) {
+        if (norm != 0.0f) {
             int e = 0;
-            if (norm < 1e300) {
-                frexp(norm, &e);                              // norm = f·2^e, f in [0.5, 1)
-                rest = static_cast<float>(ldexp(1.0, e) / norm);
-            } else {
-                rest = __int_as_float(0x7fffffff);            // infinite (or NaN): so is the result, NaN
-            }
+            rest = __int_as_float(0x7fffffff);                // infinite (or NaN): so is the result, NaN
+            if (norm <= 3.4e38f) rest = 1.0f / frexpf(norm, &e);   // norm = f·2^e, f in [0.5, 1)
             two_e = ldexpf(1.0f, X_EXPONENT - e);
         }
         power = two_e;
@@ -256,7 +252,7 @@ template <int KIND>
 struct OrthoOp {
     static constexpr int BN = 256;
     static constexpr bool BF16 = false;
-    static constexpr bool MASKED = false;
+    static constexpr bool MASKABLE = false;
     using Params = OrthoProducts;
     enum { LEFT, RIGHT, MAPS };
 
@@ -290,8 +286,7 @@ struct OrthoOp {
         ti.steps = p.steps;
         return ti;
     }
-    static __device__ __forceinline__ bool masked(const Params&, const Tile&) { return false; }
-    static __device__ __forceinline__ void valid64(const Params&, int32_t, uint32_t&, uint32_t&) {}
+    static __device__ __forceinline__ bool dirty(const Params&) { return false; }
 
     struct Finish {
         const Params& p;

@@ -14,15 +14,16 @@
 //    runs out ends the launch as in the other products.
 //
 // An operation `Op` has
-//     BN, BF16, MASKED         tile columns, operand type, see below
+//     BN, BF16, MASKABLE       tile columns, operand type, see below
 //     Params                   with int32_t total_tiles, n_maps, *status
 //     tile(p, t)               what tile t multiplies (nothing where it has no steps)
 //     Finish(p, smem, ...)     per epilogue warp: before(t) ahead of the sums (false where
 //                              there are none), pass(c, taddr) for 64 columns of its 32 rows
-// MASKED: rows of an M/N-major B (rows of K) whose bit in Params::valid is 0 are set to
-// zero in shared memory before they are multiplied, so that what stands there, a NaN
-// say, meets nothing.  Each CTA then has its own "full" barriers, its warp 1 clears
-// the rows, and the odd CTA's reports its half to the even one.
+// MASKABLE: where Op::dirty(p) says so, rows of an M/N-major B (rows of K) whose bit
+// Op::valid64 gives as 0 are set to zero in shared memory before they are multiplied, so
+// that what stands there, a NaN say, meets nothing.  Each CTA then has its own "full"
+// barriers, its warp 1 clears the rows, and the odd CTA's reports its half to the even one's.
+// (That hop doubles the time of a launch, so it is taken only if there is something to remove.)
 #pragma once
 
 #include <cuda.h>
@@ -94,7 +95,6 @@ template <class Op>
 __global__ void __launch_bounds__(THREADS, 1)
 pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename Op::Params p) {
     constexpr int BN = Op::BN;
-    constexpr bool MASKED = Op::MASKED;
     using L = Layout<BN>;
     constexpr int STAGES = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -103,7 +103,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + L::OFF_BARS;               // [STAGES]
     const uint32_t bar_empty = bar_full + 8 * STAGES;            // [STAGES]
-    const uint32_t bar_peer = bar_empty + 8 * STAGES;            // [STAGES] MASKED: the odd CTA's half is there
+    const uint32_t bar_peer = bar_empty + 8 * STAGES;            // [STAGES] masked: the odd CTA's half is there
     const uint32_t bar_tfull = bar_peer + 8 * STAGES;            // [2]
     const uint32_t bar_tempty = bar_tfull + 16;                  // [2] (used in the even CTA)
     const uint32_t bar_drain = bar_tempty + 16;                  // [1]
@@ -142,6 +142,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     // next kernel may start only now that this CTA holds its TMEM.
     pdl_wait_prior_grid();
     pdl_launch_dependents();
+    const bool masked = Op::MASKABLE && __syncthreads_or(Op::dirty(p)) != 0;       // the same in all CTAs
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     cluster_sync_all();            // both CTAs' barriers exist before copies and commits cross
 
@@ -153,9 +154,9 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     if (warp == 0) {
         // ---- TMA producer, both CTAs
         const uint64_t policy = l2_policy_evict_normal();
-        const uint32_t full0 = MASKED ? mapa_shared(bar_full, rank) : mapa_shared(bar_full, 0);
-        const uint32_t expect = MASKED || leader ? issue : 0;
-        constexpr uint32_t BYTES = (MASKED ? 1 : 2) * L::STAGE_BYTES;
+        const uint32_t full0 = mapa_shared(bar_full, masked ? rank : 0u);
+        const uint32_t expect = masked || leader ? issue : 0;
+        const uint32_t bytes = (masked ? 1 : 2) * L::STAGE_BYTES;
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         for (int32_t t = pair; t < p.total_tiles && ok; t += n_pairs) {
@@ -177,7 +178,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 const uint32_t sa = sbase + stage * L::STAGE_BYTES;
                 const uint32_t sb = sa + A_BYTES;
                 const int32_t k = (ti.k0 + st) * BK;
-                mbar_arrive_expect_tx_if(expect, bar_full + 8 * stage, BYTES);
+                mbar_arrive_expect_tx_if(expect, bar_full + 8 * stage, bytes);
                 if (ti.a_mn) {
 #pragma unroll
                     for (int b = 0; b < BM / 64; ++b)
@@ -197,11 +198,11 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             }
         }
     } else if (warp == 1) {
-        // ---- MMA issuer: warp 1 of the even CTA (MASKED: the odd CTA's clears its rows)
+        // ---- MMA issuer: warp 1 of the even CTA (masked: the odd CTA's clears its rows)
         const uint32_t leader_peer = mapa_shared(bar_peer, 0);
         uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
         bool ok = true;
-        for (int32_t t = pair; t < p.total_tiles && ok && (leader || MASKED); t += n_pairs) {
+        for (int32_t t = pair; t < p.total_tiles && ok && (leader || masked); t += n_pairs) {
             const Tile ti = Op::tile(p, t);
             if (ti.steps == 0) continue;
             if (leader) {
@@ -210,14 +211,14 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             }
             const uint32_t d_tmem = tmem_base + acc * BN;
             const uint32_t idesc = idesc_16bit_f32acc(2 * BM, BN, Op::BF16, ti.a_mn, ti.b_mn);
-            uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;         // MASKED: the stage's 64 valid bits
-            if constexpr (MASKED) {
-                if (ti.b_mn && Op::masked(p, ti)) Op::valid64(p, ti.k0, w0, w1);
+            uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;         // the stage's 64 valid bits
+            if constexpr (Op::MASKABLE) {
+                if (masked && Op::maskable(ti)) Op::valid64(p, ti.k0, w0, w1);
             }
             for (int32_t st = 0; st < ti.steps; ++st) {
                 uint32_t n0 = 0xffffffffu, n1 = 0xffffffffu;
-                if constexpr (MASKED) {
-                    if (st + 1 < ti.steps && Op::masked(p, ti)) Op::valid64(p, ti.k0 + st + 1, n0, n1);
+                if constexpr (Op::MASKABLE) {
+                    if (masked && st + 1 < ti.steps && Op::maskable(ti)) Op::valid64(p, ti.k0 + st + 1, n0, n1);
                 }
                 if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                     ok = false;
@@ -225,7 +226,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 }
                 const uint32_t sa = sbase + stage * L::STAGE_BYTES;
                 const uint32_t sb = sa + A_BYTES;
-                if constexpr (MASKED) {
+                if (Op::MASKABLE && masked) {
                     if ((w0 & w1) != 0xffffffffu) {
                         // K rows are whole 128-byte lines of each box
                         uint8_t* b0 = smem + stage * L::STAGE_BYTES + A_BYTES;
@@ -310,7 +311,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     if (warp == 0 && lane == 0 && *abort_flag) {
         // Whichever role gave up: copies in flight land before the CTA exits.
         // (The odd CTA's report to the even CTA's barriers, unless each has its own.)
-        if (leader || MASKED) drain_copies(bar_full, issued, STAGES, DRAIN_LIMIT_NS);
+        if (leader || masked) drain_copies(bar_full, issued, STAGES, DRAIN_LIMIT_NS);
         else spin_ns(1000000ull);
     }
     __syncwarp();

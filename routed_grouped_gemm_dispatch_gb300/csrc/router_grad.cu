@@ -9,8 +9,9 @@
 //    of a pair's part of a tile go to fp32 slot pair + tile: from one part to the next
 //    either of them grows, so no two share a slot.  They are added in pair order.
 //  * Operands are read as they lie: d_z by token rows for d_x, transposed for d_W.
-//  * Rows of x whose token does not count are cleared in shared memory (their d_z is zero, but
-//    zero times a NaN is not).
+//  * Rows of x whose token does not count are multiplied by a d_z of zero.  If one of them holds an
+//    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
+//    memory first.
 //
 // Rounding: d_z once (an operand of 16-bit products), d_x and d_W once from fp32.
 #include <cuda.h>
@@ -45,6 +46,8 @@ struct GradProducts {
     float* slots;                    // [w_pairs + w_tiles][256][256]
     const float* scale;              // [1]: what undoes the power of two in d_z
     const uint32_t* valid;           // a bit per token; null: all count
+    const int32_t* dirty;            // [n_dirty] is there something to remove from x
+    int32_t n_dirty;
 };
 
 // Steps of d_W before piece i.
@@ -66,11 +69,11 @@ __device__ __forceinline__ Part part_of(const GradProducts& p, int32_t piece, in
     return Part{tile, static_cast<int32_t>(from - t0), to > from ? static_cast<int32_t>(to - from) : 0};
 }
 
-template <bool BF16_, bool MASKED_>
+template <bool BF16_>
 struct GradOp {
     static constexpr int BN = TILE;
     static constexpr bool BF16 = BF16_;
-    static constexpr bool MASKED = MASKED_;
+    static constexpr bool MASKABLE = true;
     using Params = GradProducts;
     enum { DZ, W_T, DZ_T, X_T, MAPS };
 
@@ -99,7 +102,12 @@ struct GradOp {
         }
         return ti;
     }
-    static __device__ __forceinline__ bool masked(const Params&, const Tile& ti) { return ti.b_map == X_T; }
+    static __device__ __forceinline__ bool dirty(const Params& p) {
+        bool any = false;
+        for (int32_t i = threadIdx.x; i < p.n_dirty; i += pairs::THREADS) any |= p.dirty[i] != 0;
+        return any;
+    }
+    static __device__ __forceinline__ bool maskable(const Tile& ti) { return ti.b_map == X_T; }
     static __device__ __forceinline__ void valid64(const Params& p, int32_t step, uint32_t& w0, uint32_t& w1) {
         const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.valid) + step);
         w0 = v.x;
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const GradProducts p, u
 
 struct GradLayout {
     int32_t ld;
-    int64_t dz, scale, block_max, valid, slots, bytes;
+    int64_t dz, scale, block_max, block_dirty, valid, slots, bytes;
 };
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -242,6 +250,7 @@ GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
     l.dz = take(n_tokens * l.ld * 2);
     l.scale = take(8);
     l.block_max = take(int64_t{4} * router_grad_blocks(n_tokens));
+    l.block_dirty = take(int64_t{4} * router_grad_blocks(n_tokens));
     l.valid = take((n_tokens + 63) / 64 * 8);
     const int32_t tiles = weight_tiles(n_experts, hidden);
     l.slots = take(static_cast<int64_t>(weight_pieces(n_tokens, tiles, MAX_PAIRS) + tiles) * TILE * TILE * 4);
@@ -249,9 +258,9 @@ GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
     return l;
 }
 
-template <bool BF16, bool MASKED>
+template <bool BF16>
 cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, float* slots, cudaStream_t stream) {
-    using Op = GradOp<BF16, MASKED>;
+    using Op = GradOp<BF16>;
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
     const int64_t T = a.r.n_tokens;
     const int32_t E = a.r.n_experts, H = a.hidden;
@@ -280,7 +289,9 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     p.d_x = a.d_x;
     p.slots = slots;
     p.scale = g.scale;
-    p.valid = MASKED ? g.valid : nullptr;
+    p.valid = g.valid;
+    p.dirty = g.block_dirty;
+    p.n_dirty = g.valid ? router_grad_blocks(T) : 0;
     cudaError_t err = pairs::launch<Op>(maps, p, stream);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[1];
@@ -311,14 +322,13 @@ cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream)
     g.ld = l.ld;
     g.scale = reinterpret_cast<float*>(ws + l.scale);
     g.block_max = reinterpret_cast<float*>(ws + l.block_max);
-    g.valid = reinterpret_cast<uint32_t*>(ws + l.valid);
-    cudaError_t err = launch_logit_gradients(a, g, stream);
+    const bool some = a.r.token_mask != nullptr || a.r.seq_offsets != nullptr;
+    g.valid = some ? reinterpret_cast<uint32_t*>(ws + l.valid) : nullptr;
+    g.block_dirty = some ? reinterpret_cast<int32_t*>(ws + l.block_dirty) : nullptr;
+    const cudaError_t err = launch_logit_gradients(a, g, stream);
     if (err != cudaSuccess) return err;
     float* slots = reinterpret_cast<float*>(ws + l.slots);
-    const bool masked = a.r.token_mask != nullptr || a.r.seq_offsets != nullptr;
-    if (a.bf16)
-        return masked ? launch_products<true, true>(a, g, slots, stream) : launch_products<true, false>(a, g, slots, stream);
-    return masked ? launch_products<false, true>(a, g, slots, stream) : launch_products<false, false>(a, g, slots, stream);
+    return a.bf16 ? launch_products<true>(a, g, slots, stream) : launch_products<false>(a, g, slots, stream);
 }
 
 }  // namespace moe

@@ -7,10 +7,11 @@
 //     g[t, e] = d_losses[0]·E / (k T T_s)·counts[s, e] + Σ_j [id[t, j] = e]·d_w[t, j]
 //     d_z = p ⊙ (g − Σ_e p g) + d_losses[1]·2/T·logsumexp(z)·p
 //
-// A warp has a token: its lanes hold the token's logits in registers, lane for
-// lane the same experts, so that column sums over a warp's tokens stay in
-// registers until the end of a piece.  All is read once; sums over tokens are fp32 over the
-// tokens of a warp and of a block, fp64 beyond, always in the same order.
+// A group of 4 to 32 lanes has a token, 8 logits a lane (up to 32 above 256 experts), and a lane
+// has the same experts of every token, so that column sums over a warp's tokens stay in
+// registers until the end of a piece.  All is read once.  Sums over tokens are fp32 over the
+// tokens of a warp and of a block and pairs of fp32 (Sum) beyond, always in the same
+// order.  (FP64 is slow here: with it the second launch took 16 us, by itself, for 32 tokens.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -26,22 +27,22 @@ namespace {
 
 constexpr int WARPS = 16;
 constexpr int THREADS = 32 * WARPS;
-constexpr int REDUCE_WARPS = 8;
+constexpr int REDUCE_WARPS = 32;
 constexpr int HALF = WARPS / 2;
 
-// A token's logits in the lanes of a warp: value i of a lane is expert
-// `expert(i)`.  VEC: E is a multiple of 4 and rows are whole 16-byte pieces.
-template <int PER, bool VEC>
-__device__ __forceinline__ int expert(int lane, int i) {
-    return VEC ? 4 * lane + 128 * (i >> 2) + (i & 3) : lane + 32 * i;
+// Value i of lane l of a token's L lanes is expert `expert(l, i)`.  VEC: E is a multiple of 4 and rows
+// are whole 16-byte pieces.
+template <int L, bool VEC>
+__device__ __forceinline__ int expert(int l, int i) {
+    return VEC ? (i >> 3) * 8 * L + 8 * l + (i & 7) : l + L * i;
 }
 
-template <int PER, bool VEC>
-__device__ __forceinline__ void load_row(float (&z)[PER], const float* row, int lane, int32_t n_experts) {
+template <int L, int PER, bool VEC>
+__device__ __forceinline__ void load_row(float (&z)[PER], const float* row, int l, int32_t n_experts) {
     if (VEC) {
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
-            const int e = expert<PER, VEC>(lane, i);
+            const int e = expert<L, VEC>(l, i);
             float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (e < n_experts) v = __ldg(reinterpret_cast<const float4*>(row + e));
             z[i] = v.x;
@@ -52,33 +53,38 @@ __device__ __forceinline__ void load_row(float (&z)[PER], const float* row, int 
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = expert<PER, VEC>(lane, i);
+            const int e = expert<L, VEC>(l, i);
             z[i] = e < n_experts ? __ldg(row + e) : -INFINITY;
         }
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over a token's lanes; all lanes of the warp take part.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
 
-// The row becomes its softmax; returns its logsumexp.
-template <int PER>
+// The row becomes its softmax; returns its logsumexp.  An exponential is 2^(z log2 e - top log2 e), the
+// difference rounded once more and ex2.approx (2^-22): its rounding is an absolute error of the exponent, so the
+// relative error grows with the distance from the row's maximum, by 2^-24 of it.
+template <int L, int PER>
 __device__ __forceinline__ float softmax_row(float (&z)[PER]) {
     float top = z[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) top = fmaxf(top, z[i]);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = L / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    constexpr float LOG2E = 1.4426950408889634f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        z[i] = expf(z[i] - top);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z[i]) : "f"((z[i] - top) * LOG2E));
         sum += z[i];
     }
-    sum = warp_sum(sum);
+    sum = lanes_sum<L>(sum);
     const float inv = 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < PER; ++i) z[i] *= inv;
@@ -96,15 +102,53 @@ struct Seqs {
         const int64_t v = __ldg(offsets + i);
         return v < 0 ? 0 : (v > n_tokens ? n_tokens : v);
     }
-    // the last sequence that starts at or before token t (-1: none)
+    // the last sequence that starts at or before token t (-1: none); by a whole warp, 32 bounds at a time
     __device__ __forceinline__ int32_t find(int64_t t) const {
-        int32_t lo = 0, hi = n;
+        if (offsets == nullptr) return 0;
+        int32_t lo = 0, hi = n;                  // the first bound past t is in [lo, hi]
         while (lo < hi) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (bound(mid) <= t) lo = mid + 1;
-            else hi = mid;
+            const int32_t step = (hi - lo + 31) / 32;
+            const int32_t i = lo + static_cast<int32_t>(threadIdx.x & 31) * step;
+            const int c = __popc(__ballot_sync(0xffffffffu, i < hi && bound(i) <= t));
+            if (c == 0) {
+                hi = lo;
+            } else {
+                hi = lo + c * step < hi ? lo + c * step : hi;
+                lo += (c - 1) * step + 1;
+            }
         }
         return lo - 1;
+    }
+};
+
+// An fp32 sum with what its additions lost (an exact sum of two, and of a product).
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(hi, x);
+        const float b = __fsub_rn(s, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        hi = s;
+    }
+    __device__ __forceinline__ void add(const Sum& o) {
+        add(o.hi);
+        lo += o.lo;
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+    __device__ __forceinline__ Sum times(float f) const {
+        Sum r;
+        r.hi = __fmul_rn(hi, f);
+        r.lo = __fmaf_rn(hi, f, -r.hi) + lo * f;
+        return r;
+    }
+    __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            Sum o;
+            o.hi = __shfl_xor_sync(0xffffffffu, hi, d);
+            o.lo = __shfl_xor_sync(0xffffffffu, lo, d);
+            add(o);
+        }
     }
 };
 
@@ -114,12 +158,10 @@ struct BalanceParams {
     Routing r;
     int32_t chunk;                // tokens of a block
     int32_t n_slots;
-    float* psum;                  // [n_slots, E] Σ p of a block's tokens of one sequence
-    int32_t* pcount;              // [n_slots, E]
-    float* pz;                    // [n_slots] Σ logsumexp²
-    int32_t* pn;                  // [n_slots] valid tokens
-    double* dots;                 // [n_seqs, expert blocks] Σ_e counts·Σ p
-    double* zsum;                 // [n_seqs]
+    float2* part;                 // [n_slots, E] Σ p of a block's tokens of one sequence, and (as an int) their pairs
+    float2* tokens;               // [n_slots] Σ logsumexp², and (as an int) the tokens that count
+    Sum* dots;                    // [n_seqs, expert blocks] Σ_e counts·Σ p
+    Sum* zsum;                    // [n_seqs]
     unsigned* done;
     float* losses;
     int32_t* counts;
@@ -129,14 +171,16 @@ struct BalanceParams {
 
 // One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
 // from one part to the next either b or s grows, so no two share a slot.
-template <int PER, bool VEC>
+template <int L, int PER, bool VEC>
 __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(const BalanceParams p) {
     extern __shared__ float sums[];                               // [HALF][E], then int [E]
     __shared__ float zpart[WARPS];
     __shared__ int npart[WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int PACK = 32 / L;                                  // tokens a warp has at a time
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1);
     const int32_t E = p.r.n_experts, k = p.r.top_k;
     int32_t* hist = reinterpret_cast<int32_t*>(sums + HALF * E);
+    for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
@@ -153,55 +197,71 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
             ++s;
             continue;
         }
-        for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
-        __syncthreads();
+        __syncthreads();                                          // the counts are zero
+        // pairs of the tokens that count
+        const int32_t pairs = static_cast<int32_t>(t1 - t0) * k;
+        for (int32_t i = threadIdx.x; i < pairs; i += THREADS) {
+            if (p.r.token_mask && p.r.token_mask[t0 + i / k] == 0) continue;
+            const int32_t id = __ldg(p.r.topk_ids + t0 * k + i);
+            if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+            else if (id >= E && p.status) atomicOr(p.status, MOE_DEV_BAD_EXPERT_ID);
+        }
         float acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
         float zz = 0.0f;
         int n = 0;
-        // the next token's row is on its way while this one is reduced
+        // the next tokens' rows are on their way while these are reduced
         float z[PER], next[PER];
-        int64_t t = t0 + warp;
+        int64_t t = t0 + warp * PACK + lane / L;
         bool live = t < t1 && counts_token(p.r.token_mask, t);
-        if (live) load_row<PER, VEC>(z, p.r.logits + t * E, lane, E);
-        while (t < t1) {
-            const int64_t tn = t + WARPS;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] = 0.0f;
+        if (live) load_row<L, PER, VEC>(z, p.r.logits + t * E, l, E);
+        for (int64_t tw = t0 + warp * PACK; tw < t1; tw += WARPS * PACK) {
+            const int64_t tn = t + WARPS * PACK;
             const bool live_next = tn < t1 && counts_token(p.r.token_mask, tn);
-            if (live_next) load_row<PER, VEC>(next, p.r.logits + tn * E, lane, E);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) next[i] = 0.0f;
+            if (live_next) load_row<L, PER, VEC>(next, p.r.logits + tn * E, l, E);
+            const float lse = softmax_row<L, PER>(z);
             if (live) {
-                if (lane < k) {
-                    const int32_t id = p.r.topk_ids[t * k + lane];
-                    if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
-                    else if (id >= E && p.status) atomicOr(p.status, MOE_DEV_BAD_EXPERT_ID);
-                }
-                const float lse = softmax_row<PER>(z);
 #pragma unroll
                 for (int i = 0; i < PER; ++i) acc[i] += z[i];
-                zz += lse * lse;
-                ++n;
+                if (l == 0) {
+                    zz += lse * lse;
+                    ++n;
+                }
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) z[i] = next[i];
             live = live_next;
             t = tn;
         }
+        // a warp's tokens, then the block's warps
+#pragma unroll
+        for (int d = L; d < 32; d <<= 1) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
+            zz += __shfl_xor_sync(0xffffffffu, zz, d);
+            n += __shfl_xor_sync(0xffffffffu, n, d);
+        }
         if (lane == 0) {
             zpart[warp] = zz;
             npart[warp] = n;
         }
-        if (warp >= HALF) {
+        if (warp >= HALF && lane < L) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = expert<PER, VEC>(lane, i);
+                const int e = expert<L, VEC>(l, i);
                 if (e < E) sums[(warp - HALF) * E + e] = acc[i];
             }
         }
         __syncthreads();
-        if (warp < HALF) {
+        if (warp < HALF && lane < L) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = expert<PER, VEC>(lane, i);
+                const int e = expert<L, VEC>(l, i);
                 if (e < E) sums[warp * E + e] += acc[i];
             }
         }
@@ -212,8 +272,8 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < HALF; ++w) v += sums[w * E + e];
-            p.psum[slot * E + e] = v;
-            p.pcount[slot * E + e] = hist[e];
+            p.part[slot * E + e] = make_float2(v, __int_as_float(hist[e]));
+            hist[e] = 0;
         }
         if (threadIdx.x == 0) {
             float zt = 0.0f;
@@ -222,8 +282,7 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
                 zt += zpart[w];
                 nt += npart[w];
             }
-            p.pz[slot] = zt;
-            p.pn[slot] = nt;
+            p.tokens[slot] = make_float2(zt, __int_as_float(nt));
         }
         __syncthreads();
         t0 = t1;
@@ -233,74 +292,72 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
 
 // Grid: 32 experts of a sequence per block.  The last block to finish adds the sequences up.
 __global__ void __launch_bounds__(32 * REDUCE_WARPS) balance_reduce_kernel(const BalanceParams p) {
-    __shared__ double sum[REDUCE_WARPS][32];
-    __shared__ int32_t cnt[REDUCE_WARPS][32];
-    __shared__ double zs[REDUCE_WARPS];
-    __shared__ int32_t ns[REDUCE_WARPS];
+    __shared__ Sum sum[REDUCE_WARPS][33];
+    __shared__ int32_t cnt[REDUCE_WARPS][33];
     __shared__ bool final_block;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t E = p.r.n_experts, S = p.r.n_seqs;
     const int32_t s = blockIdx.y, e = blockIdx.x * 32 + lane;
+    const Seqs seqs{p.r.seq_offsets, S, p.r.n_tokens};
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const Seqs seqs{p.r.seq_offsets, S, p.r.n_tokens};
     const int64_t t0 = seqs.bound(s), t1 = seqs.bound(s + 1);
     if (threadIdx.x == 0 && blockIdx.x == 0 && p.r.seq_offsets && p.status &&
         (t1 < t0 || t0 != p.r.seq_offsets[s] || t1 != p.r.seq_offsets[s + 1]))
         atomicOr(p.status, MOE_DEV_BAD_TABLE);
-    double v = 0.0, z = 0.0;
-    int32_t c = 0, n = 0;
-    if (t1 > t0) {
-        const int64_t b0 = t0 / p.chunk + s, b1 = (t1 - 1) / p.chunk + s;
-        if (e < E) {
-#pragma unroll 8
-            for (int64_t b = b0 + warp; b <= b1; b += REDUCE_WARPS) {
-                v += p.psum[b * E + e];
-                c += p.pcount[b * E + e];
-            }
-        }
-        if (blockIdx.x == 0) {
-            for (int64_t b = b0 + threadIdx.x; b <= b1; b += 32 * REDUCE_WARPS) {
-                z += p.pz[b];
-                n += p.pn[b];
-            }
+    const bool any = t1 > t0;
+    const int32_t b0 = any ? static_cast<int32_t>(t0 / p.chunk) + s : 0;
+    const int32_t b1 = any ? static_cast<int32_t>((t1 - 1) / p.chunk) + s : -1;
+    Sum v;
+    int32_t c = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int32_t b = b0 + warp; b <= b1; b += REDUCE_WARPS) {
+            const float2 x = p.part[static_cast<int64_t>(b) * E + e];
+            v.add(x.x);
+            c += __float_as_int(x.y);
         }
     }
     sum[warp][lane] = v;
     cnt[warp][lane] = c;
+    // the tokens of the sequence: another warp than the one that goes on with the experts
+    if (blockIdx.x == 0 && warp == 1) {
+        Sum z;
+        int32_t n = 0;
+        for (int32_t b = b0 + lane; b <= b1; b += 32) {
+            const float2 x = p.tokens[b];
+            z.add(x.x);
+            n += __float_as_int(x.y);
+        }
+        z.add_lanes();
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, d);
-        n += __shfl_xor_sync(0xffffffffu, n, d);
+        for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+        if (lane == 0) {
+            p.zsum[s] = z;
+            p.seq_tokens[s] = n;
+            __threadfence();
+        }
     }
+    __syncthreads();
+    // a warp has an expert, a lane one of the parts
+    static_assert(REDUCE_WARPS == 32, "as many warps as experts and as lanes");
+    v = sum[lane][warp];
+    c = cnt[lane][warp];
+    v.add_lanes();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+    __syncthreads();
+    const int32_t ew = blockIdx.x * 32 + warp;
     if (lane == 0) {
-        zs[warp] = z;
-        ns[warp] = n;
+        if (ew < E) p.counts[static_cast<int64_t>(s) * E + ew] = c;
+        sum[0][warp] = ew < E ? v.times(static_cast<float>(c)) : Sum();
     }
     __syncthreads();
     if (warp == 0) {
-        v = 0.0;
-        c = 0;
-        for (int w = 0; w < REDUCE_WARPS; ++w) {
-            v += sum[w][lane];
-            c += cnt[w][lane];
-        }
-        if (e < E) p.counts[static_cast<int64_t>(s) * E + e] = c;
-        v *= c;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        v = sum[0][lane];
+        v.add_lanes();
         if (lane == 0) {
             p.dots[static_cast<int64_t>(s) * gridDim.x + blockIdx.x] = v;
-            if (blockIdx.x == 0) {
-                z = 0.0;
-                n = 0;
-                for (int w = 0; w < REDUCE_WARPS; ++w) {
-                    z += zs[w];
-                    n += ns[w];
-                }
-                p.zsum[s] = z;
-                p.seq_tokens[s] = n;
-            }
             __threadfence();
             final_block = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
         }
@@ -308,44 +365,51 @@ __global__ void __launch_bounds__(32 * REDUCE_WARPS) balance_reduce_kernel(const
     __syncthreads();
     if (!final_block) return;
     __threadfence();
-    // every thread its sequences in order, then the threads in order
-    v = 0.0;
-    z = 0.0;
-    n = 0;
+    // every thread its sequences in order, then the threads in a tree
+    Sum bal, z;
+    int32_t n = 0;
     for (int32_t i = threadIdx.x; i < S; i += 32 * REDUCE_WARPS) {
         const int32_t ni = __ldcg(p.seq_tokens + i);
-        double d = 0.0;
-        for (unsigned b = 0; b < gridDim.x; ++b) d += __ldcg(p.dots + static_cast<int64_t>(i) * gridDim.x + b);
-        if (ni > 0) v += d / ni;
-        z += __ldcg(p.zsum + i);
+        Sum d;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(p.dots + static_cast<int64_t>(i) * gridDim.x + b));
+            Sum part;
+            part.hi = x.x;
+            part.lo = x.y;
+            d.add(part);
+        }
+        if (ni > 0) bal.add(d.times(1.0f / static_cast<float>(ni)));
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(p.zsum + i));
+        Sum part;
+        part.hi = x.x;
+        part.lo = x.y;
+        z.add(part);
         n += ni;
     }
+    bal.add_lanes();
+    z.add_lanes();
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        v += __shfl_xor_sync(0xffffffffu, v, d);
-        z += __shfl_xor_sync(0xffffffffu, z, d);
-        n += __shfl_xor_sync(0xffffffffu, n, d);
-    }
-    __syncthreads();
+    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
     if (lane == 0) {
-        sum[warp][0] = v;
-        cnt[warp][0] = n;
-        zs[warp] = z;
+        sum[0][warp] = bal;
+        sum[1][warp] = z;
+        cnt[0][warp] = n;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        v = 0.0;
-        z = 0.0;
-        n = 0;
-        for (int w = 0; w < REDUCE_WARPS; ++w) {
-            v += sum[w][0];
-            z += zs[w];
-            n += cnt[w][0];
+    if (warp == 0) {
+        bal = sum[0][lane];
+        z = sum[1][lane];
+        n = cnt[0][lane];
+        bal.add_lanes();
+        z.add_lanes();
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+        if (lane == 0) {
+            const float tokens = static_cast<float>(n > 0 ? n : 1);
+            p.losses[0] = bal.value() * static_cast<float>(E) / (static_cast<float>(p.r.top_k) * tokens);
+            p.losses[1] = z.value() / tokens;
+            p.seq_tokens[S] = n;
         }
-        const double tokens = n > 0 ? n : 1;
-        p.losses[0] = static_cast<float>(v * E / (p.r.top_k * tokens));
-        p.losses[1] = static_cast<float>(z / tokens);
-        p.seq_tokens[S] = n;
     }
 }
 
@@ -365,7 +429,10 @@ struct GradParams {
     float* d_logits;
     float* scale;
     float* block_max;
-    uint32_t* valid;
+    uint32_t* valid;              // nullable, as is what follows: all tokens count
+    int32_t* block_dirty;
+    const uint16_t* x;
+    int32_t hidden;
     int32_t* status;
 };
 
@@ -379,14 +446,28 @@ __device__ __forceinline__ float grad_scale(float m) {
     return ldexpf(1.0f, s > 120 ? 120 : (s < -120 ? -120 : s));
 }
 
+// Is one of the 8 values in 16 bytes infinite or NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite(const uint4& v) {
+    // all exponent bits set: adding one of them to the magnitude reaches the sign's place
+    constexpr uint32_t ONE = BF16 ? 0x00800080u : 0x04000400u;
+    return (((v.x & 0x7fff7fffu) + ONE) | ((v.y & 0x7fff7fffu) + ONE) | ((v.z & 0x7fff7fffu) + ONE) |
+            ((v.w & 0x7fff7fffu) + ONE)) & 0x80008000u;
+}
+
 // MAX: only the largest |d_z| of each block, which sets the power of two that
 // the values are stored times (fp16 would lose gradients of a mean over tokens
-// otherwise; bf16 has fp32's range and needs none).  Otherwise the values.
-template <int PER, bool VEC, bool BF16, bool MAX>
+// otherwise; bf16 has fp32's range and needs none).  Otherwise the values, and of the tokens that
+// do not count whether x holds something that a product with zero does not remove.
+template <int L, int PER, bool VEC, bool BF16, bool MAX>
 __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kernel(const GradParams p) {
     __shared__ float smax[WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int PACK = 32 / L;
+    // a token's routed gradients, by expert (a row per token that the block has at a time)
+    extern __shared__ float routed[];                             // [WARPS * PACK][L * PER + 4]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1);
     const int32_t E = p.r.n_experts, k = p.r.top_k;
+    float* mine = routed + (warp * PACK + lane / L) * (L * PER + 4);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     float scale = 1.0f;
@@ -409,14 +490,24 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kern
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.chunk;
     const int64_t last = first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens;
     const int64_t begin = seqs.bound(0), finish = seqs.bound(p.r.n_seqs);
-    if (!MAX) {
+    if (!MAX && p.valid) {
         // a bit per token that counts; whole steps of 64, zero past the end
+        uint32_t bad = 0;
         for (int64_t t = first + 32 * warp; t < first + p.chunk && t < (p.r.n_tokens + 63) / 64 * 64; t += THREADS) {
             const int64_t ti = t + lane;
             const bool v = ti < p.r.n_tokens && ti >= begin && ti < finish && counts_token(p.r.token_mask, ti);
             const uint32_t bits = __ballot_sync(0xffffffffu, v);
             if (lane == 0) p.valid[t >> 5] = bits;
+            for (uint32_t out = ~bits; out != 0; out &= out - 1) {
+                const int64_t to = t + __ffs(static_cast<int>(out)) - 1;
+                if (to >= p.r.n_tokens) break;
+                const uint4* row = reinterpret_cast<const uint4*>(p.x + to * p.hidden);
+#pragma unroll 4
+                for (int32_t i = lane; i < p.hidden / 8; i += 32) bad |= not_finite<BF16>(__ldg(row + i));
+            }
         }
+        const int any = __syncthreads_or(bad != 0);
+        if (threadIdx.x == 0) p.block_dirty[blockIdx.x] = any;
     }
     float cb = 0.0f, cz = 0.0f;
     if (p.d_losses) {
@@ -426,78 +517,122 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kern
             cz = p.d_losses[1] * 2.0f / n;
         }
     }
-    int32_t s = seqs.find(first + warp);
-    float largest = 0.0f;
-    for (int64_t t = first + warp; t < last; t += WARPS) {
-        while (s + 1 < p.r.n_seqs && seqs.bound(s + 1) <= t) ++s;
-        const bool live = t >= begin && t < finish && s >= 0 && counts_token(p.r.token_mask, t);
-        float d[PER];
+    int64_t t = first + warp * PACK + lane / L;
+    int32_t s = seqs.find(first + warp * PACK);
+    int64_t s_end = seqs.bound(s + 1);           // (of s = -1: where the first one starts)
+    int32_t base_of = -1;                        // the sequence whose counts are in base[]
+    float base[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) d[i] = 0.0f;
+    for (int i = 0; i < PER; ++i) base[i] = 0.0f;
+    float largest = 0.0f;
+    // the next tokens' logits, ids and routed gradients are on their way meanwhile
+    float z[PER], next[PER];
+    int32_t id = -1, id_next = -1;
+    float dw = 0.0f, dw_next = 0.0f;
+    auto ask = [&](int64_t at, float (&row)[PER], int32_t& i, float& w) {
+        const bool live = at < last && at >= begin && at < finish && counts_token(p.r.token_mask, at);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) row[j] = 0.0f;
+        i = -1;
+        w = 0.0f;
         if (live) {
-            float z[PER];
-            load_row<PER, VEC>(z, p.r.logits + t * E, lane, E);
-            const float per_count = cb != 0.0f ? cb / static_cast<float>(max(p.seq_tokens[s], 1)) : 0.0f;
-            if (cb != 0.0f) {
-                const int32_t* row = p.counts + static_cast<int64_t>(s) * E;
+            load_row<L, PER, VEC>(row, p.r.logits + at * E, l, E);
+            if (p.d_weights && l < k) {
+                i = __ldg(p.r.topk_ids + at * k + l);
+                w = __ldg(p.d_weights + at * k + l);
+            }
+        }
+        return live;
+    };
+    bool live = ask(t, z, id, dw);
+    for (int64_t tw = first + warp * PACK; tw < last; tw += WARPS * PACK) {
+        const int64_t tn = t + WARPS * PACK;
+        const bool live_next = ask(tn, next, id_next, dw_next);
+        if (cb != 0.0f) {
+            while (t >= s_end && s + 1 < p.r.n_seqs) {
+                ++s;
+                s_end = seqs.bound(s + 1);
+            }
+            if (live && s != base_of) {
+                base_of = s;
+                const float per_count = s >= 0 ? cb / static_cast<float>(max(p.seq_tokens[s], 1)) : 0.0f;
+                const int32_t* row = p.counts + static_cast<int64_t>(s >= 0 ? s : 0) * E;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = expert<PER, VEC>(lane, i);
-                    if (e < E) d[i] = per_count * static_cast<float>(__ldg(row + e));
+                    const int e = expert<L, VEC>(l, i);
+                    if (e < E) base[i] = per_count * static_cast<float>(__ldg(row + e));
                 }
             }
-            if (p.d_weights) {
-                int32_t id = -1;
-                float dw = 0.0f;
-                if (lane < k) {
-                    id = p.r.topk_ids[t * k + lane];
-                    dw = p.d_weights[t * k + lane];
-                    if (id >= E) {
-                        if (p.status) atomicOr(p.status, MOE_DEV_BAD_EXPERT_ID);
-                        id = -1;
-                    }
-                }
-                for (int j = 0; j < k; ++j) {
-                    const int32_t ej = __shfl_sync(0xffffffffu, id, j);
-                    const float wj = __shfl_sync(0xffffffffu, dw, j);
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        if (ej >= 0 && expert<PER, VEC>(lane, i) == ej) d[i] += wj;
-                }
-            }
-            const float lse = softmax_row<PER>(z);
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dot += z[i] * d[i];
-            const float shift = cz * lse - warp_sum(dot);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) d[i] = z[i] * (d[i] + shift);
         }
+        float d[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) d[i] = base[i];
+        if (p.d_weights) {
+            if (id >= E) {
+                if (p.status) atomicOr(p.status, MOE_DEV_BAD_EXPERT_ID);
+                id = -1;
+            }
+            // an expert named twice gets both, in their order, from either
+            float w = 0.0f;
+            for (int q = 0; q < k; ++q) {
+                const int from = (lane & ~(L - 1)) + q;
+                const int32_t iq = __shfl_sync(0xffffffffu, id, from);
+                const float wq = __shfl_sync(0xffffffffu, dw, from);
+                if (iq == id) w += wq;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine[l + L * i] = 0.0f;
+            __syncwarp();
+            if (id >= 0) mine[id] = w;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) d[i] += mine[expert<L, VEC>(l, i)];
+            __syncwarp();
+        }
+        const float lse = softmax_row<L, PER>(z);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) dot += z[i] * d[i];
+        const float shift = cz * lse - lanes_sum<L>(dot);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) d[i] = live ? z[i] * (d[i] + shift) : 0.0f;
         if (MAX) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) largest = fmaxf(largest, fabsf(d[i]));
-        } else {
+            for (int i = 0; i < PER; ++i)
+                if (expert<L, VEC>(l, i) < E) largest = fmaxf(largest, fabsf(d[i]));
+        } else if (t < last) {
             uint16_t* out = p.dz + t * p.ld;
             if (VEC) {
 #pragma unroll
-                for (int i = 0; i < PER; i += 4) {
-                    const int e = expert<PER, VEC>(lane, i);
-                    if (e < p.ld)                        // columns E .. ld - 1 are zeros
-                        *reinterpret_cast<uint2*>(out + e) =
-                            make_uint2(pack_16bit2<BF16>(d[i] * scale, d[i + 1] * scale),
-                                       pack_16bit2<BF16>(d[i + 2] * scale, d[i + 3] * scale));
+                for (int i = 0; i < PER; i += 8) {
+                    const int e = expert<L, VEC>(l, i);
+                    if (e < p.ld)                        // (columns E .. ld - 1 are not read)
+                        *reinterpret_cast<uint4*>(out + e) =
+                            make_uint4(pack_16bit2<BF16>(d[i] * scale, d[i + 1] * scale),
+                                       pack_16bit2<BF16>(d[i + 2] * scale, d[i + 3] * scale),
+                                       pack_16bit2<BF16>(d[i + 4] * scale, d[i + 5] * scale),
+                                       pack_16bit2<BF16>(d[i + 6] * scale, d[i + 7] * scale));
                     if (p.d_logits && e < E)
                         *reinterpret_cast<float4*>(p.d_logits + t * E + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                    if (p.d_logits && e + 4 < E)
+                        *reinterpret_cast<float4*>(p.d_logits + t * E + e + 4) =
+                            make_float4(d[i + 4], d[i + 5], d[i + 6], d[i + 7]);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = expert<PER, VEC>(lane, i);
+                    const int e = expert<L, VEC>(l, i);
                     if (e < p.ld) out[e] = static_cast<uint16_t>(pack_16bit2<BF16>(d[i] * scale, 0.0f) & 0xffffu);
                     if (p.d_logits && e < E) p.d_logits[t * E + e] = d[i];
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] = next[i];
+        live = live_next;
+        id = id_next;
+        dw = dw_next;
+        t = tn;
     }
     if (MAX) {
 #pragma unroll
@@ -537,7 +672,7 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, size_t s
 
 struct BalanceLayout {
     int32_t chunk, chunks, slots, expert_blocks;
-    int64_t psum, pcount, pz, pn, dots, zsum, done, bytes;
+    int64_t part, tokens, dots, zsum, done, bytes;
 };
 
 BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
@@ -553,10 +688,8 @@ BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs
         at += round256(n);
         return r;
     };
-    l.psum = take(int64_t{4} * l.slots * n_experts);
-    l.pcount = take(int64_t{4} * l.slots * n_experts);
-    l.pz = take(int64_t{4} * l.slots);
-    l.pn = take(int64_t{4} * l.slots);
+    l.part = take(int64_t{8} * l.slots * n_experts);
+    l.tokens = take(int64_t{8} * l.slots);
     l.dots = take(int64_t{8} * n_seqs * l.expert_blocks);
     l.zsum = take(int64_t{8} * n_seqs);
     l.done = take(4);
@@ -577,12 +710,10 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     p.r = a.r;
     p.chunk = l.chunk;
     p.n_slots = l.slots;
-    p.psum = reinterpret_cast<float*>(ws + l.psum);
-    p.pcount = reinterpret_cast<int32_t*>(ws + l.pcount);
-    p.pz = reinterpret_cast<float*>(ws + l.pz);
-    p.pn = reinterpret_cast<int32_t*>(ws + l.pn);
-    p.dots = reinterpret_cast<double*>(ws + l.dots);
-    p.zsum = reinterpret_cast<double*>(ws + l.zsum);
+    p.part = reinterpret_cast<float2*>(ws + l.part);
+    p.tokens = reinterpret_cast<float2*>(ws + l.tokens);
+    p.dots = reinterpret_cast<Sum*>(ws + l.dots);
+    p.zsum = reinterpret_cast<Sum*>(ws + l.zsum);
     p.done = reinterpret_cast<unsigned*>(ws + l.done);
     p.losses = a.losses;
     p.counts = a.counts;
@@ -591,9 +722,12 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     const int32_t E = a.r.n_experts;
     const bool vec = E % 4 == 0;
     const size_t smem = static_cast<size_t>(HALF + 1) * E * 4;
-    auto kernel = E <= 128 ? (vec ? balance_kernel<4, true> : balance_kernel<4, false>)
-                : E <= 256 ? (vec ? balance_kernel<8, true> : balance_kernel<8, false>)
-                           : (vec ? balance_kernel<32, true> : balance_kernel<32, false>);
+    auto kernel = E > 256 ? (vec ? balance_kernel<32, 32, true> : balance_kernel<32, 32, false>)
+                : !vec    ? balance_kernel<32, 8, false>
+                : E > 128 ? balance_kernel<32, 8, true>
+                : E > 64  ? balance_kernel<16, 8, true>
+                : E > 32  ? balance_kernel<8, 8, true>
+                          : balance_kernel<4, 8, true>;
     cudaError_t err = launch_pdl(kernel, dim3(static_cast<unsigned>(l.chunks)), THREADS, smem, stream, p);
     if (err != cudaSuccess) return err;
     return launch_pdl(balance_reduce_kernel, dim3(static_cast<unsigned>(l.expert_blocks), static_cast<unsigned>(a.r.n_seqs)),
@@ -609,11 +743,22 @@ template <bool BF16, bool MAX>
 static cudaError_t launch_gradient_pass(const GradParams& p, int blocks, cudaStream_t stream) {
     const int32_t E = p.r.n_experts;
     const bool vec = E % 4 == 0;
-    auto kernel = E <= 128 ? (vec ? logit_gradient_kernel<4, true, BF16, MAX> : logit_gradient_kernel<4, false, BF16, MAX>)
-                : E <= 256 ? (vec ? logit_gradient_kernel<8, true, BF16, MAX> : logit_gradient_kernel<8, false, BF16, MAX>)
-                           : (vec ? logit_gradient_kernel<32, true, BF16, MAX>
-                                  : logit_gradient_kernel<32, false, BF16, MAX>);
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), THREADS, 0, stream, p);
+    // 8 logits a lane, and a lane for each of a token's ids
+    const int k = p.r.top_k;
+    const int lanes = !vec || E > 128 ? 32 : E > 64 || k > 8 ? 16 : E > 32 || k > 4 ? 8 : 4;
+    const int per = E > 256 ? 32 : 8;
+    auto kernel = per == 32     ? (vec ? logit_gradient_kernel<32, 32, true, BF16, MAX> : logit_gradient_kernel<32, 32, false, BF16, MAX>)
+                : !vec          ? logit_gradient_kernel<32, 8, false, BF16, MAX>
+                : lanes == 32   ? logit_gradient_kernel<32, 8, true, BF16, MAX>
+                : lanes == 16   ? logit_gradient_kernel<16, 8, true, BF16, MAX>
+                : lanes == 8    ? logit_gradient_kernel<8, 8, true, BF16, MAX>
+                                : logit_gradient_kernel<4, 8, true, BF16, MAX>;
+    const size_t smem = static_cast<size_t>(WARPS) * (32 / lanes) * (lanes * per + 4) * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), THREADS, smem, stream, p);
 }
 
 cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients& g, cudaStream_t stream) {
@@ -630,6 +775,9 @@ cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients
     p.scale = g.scale;
     p.block_max = g.block_max;
     p.valid = g.valid;
+    p.block_dirty = g.block_dirty;
+    p.x = a.x;
+    p.hidden = a.hidden;
     p.status = a.status;
     const int blocks = router_grad_blocks(a.r.n_tokens);
     if (a.bf16) return launch_gradient_pass<true, false>(p, blocks, stream);

@@ -52,14 +52,16 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream);
 cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream);
 
 // Gradients of the logits (router_loss.cu) as an operand of the products: 16-bit
-// [n_tokens, ld], times the power of two in scale[0] (its inverse in scale[1]); a bit per token in
-// `valid` (1: it counts), whole 64-token steps, zero past the end.
+// [n_tokens, ld], times the power of two in scale[0] (its inverse in scale[1]).  Where some tokens may not
+// count, a bit per token in `valid` (1: it counts), whole 64-token steps, zero past the end, and per
+// block whether x holds an infinity or a NaN in one that does not; otherwise both are null.
 struct LogitGradients {
     uint16_t* dz;
     int32_t ld;
     float* scale;                 // [2]
     float* block_max;             // [router_grad_blocks()]
     uint32_t* valid;
+    int32_t* block_dirty;         // [router_grad_blocks()]
 };
 int router_grad_blocks(int64_t n_tokens);
 cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients& g, cudaStream_t stream);
