@@ -527,10 +527,10 @@ int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t c
  * within about 2e-3 of its root mean square, root mean square, whatever G's spectrum, so no
  * finer type is offered.  A matrix that holds an infinity or a NaN, or whose norm leaves fp32's
  * squares (1.8e19), becomes NaN; one of zeros stays zeros; the others of the stack do not see it.
- * Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude; where they let a norm grow past 2^9 the
- * result overflows.
+ * Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c| unless c is 0; where they let a norm grow past 2^9 the
+ * result overflows.  batch·steps·ceil(rows/128)·ceil(cols/128) is at most 2^29.
  * workspace: device memory of moe_orthogonalize_workspace_bytes() bytes, caller-owned;
- * calls that overlap on the GPU must not share it.  2 + 3·steps kernel launches; waits and
+ * calls that overlap on the GPU must not share it.  Three kernel launches; waits and
  * status_dev as in the feed-forward block. */
 moe_status_t moe_orthogonalize(int32_t dtype, const void* update, int64_t batch, int32_t rows, int32_t cols, int32_t steps,
                                float a, float b, float c, float eps, void* workspace, size_t workspace_bytes,

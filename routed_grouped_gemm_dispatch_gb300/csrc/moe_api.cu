@@ -659,9 +659,11 @@ moe_status_t moe_orthogonalize(int32_t dtype, const void* update, int64_t batch,
     if (batch < 0 || rows <= 0 || cols <= 0 || steps <= 0 || !(eps >= 0.0f) || !(eps <= 3.0e38f)) return MOE_ERR_SHAPE;
     for (float v : {a, b, c})
         if (!(v >= -MOE_ORTHO_MAX_COEFFICIENT && v <= MOE_ORTHO_MAX_COEFFICIENT)) return MOE_ERR_LIMIT;
+    if (c != 0.0f && !(b / (2.0f * c) >= -moe::ORTHO_MAX_SHIFT && b / (2.0f * c) <= moe::ORTHO_MAX_SHIFT)) return MOE_ERR_LIMIT;
     if (batch > MOE_ORTHO_MAX_BATCH || rows > MOE_ORTHO_MAX_SIZE || cols > MOE_ORTHO_MAX_SIZE || steps > MOE_ORTHO_MAX_STEPS)
         return MOE_ERR_LIMIT;
-    if (batch * ((rows + 127) / 128) * ((cols + 127) / 128) > (int64_t{1} << 30)) return MOE_ERR_LIMIT;
+    // the tiles of all products are numbered in 31 bits
+    if (batch * steps * ((rows + 127) / 128) * ((cols + 127) / 128) > (int64_t{1} << 29)) return MOE_ERR_LIMIT;
     if (batch == 0) return MOE_OK;
     if (!update || !out) return MOE_ERR_NULL;
     if (!aligned16(update) || !aligned16(out) || !aligned16(workspace)) return MOE_ERR_ALIGN;

@@ -2,29 +2,49 @@
 //     X₀ = G / max(‖G‖, eps)   (Frobenius norm)
 //     A = X·Xᵀ,  B = b·A + c·A²,  X ← a·X + B·X      `steps` times
 // with X taken with the fewer rows (a tall G is transposed on the way in and out; the
-// polynomial is the same from either side).  Three launches a step, each a list of 256-row
-// tiles over the whole stack (pair_tiles.cuh); A and B are symmetric, so only the
-// tiles on and below the diagonal are multiplied, and the others are stored from them.
+// polynomial is the same from either side).  A and B are symmetric, so only the tiles on and
+// below the diagonal are multiplied, and the others are stored from them.
 //
-// Numbers.  All operands are fp16 (11 bits at the rate of bf16's 8), times fixed powers of two
-// that keep them normal: X·2^6, A·2^10, B·2^6; sums are fp32.  X₀ is G times a power of
-// two, which is exact, and the rest of 1/‖G‖ enters the first step's fp32 sums.  Values whose
-// norm grows past 2^9 in a step (coefficients that diverge) overflow.
+// One launch for all steps of all matrices: a list of tiles, 256 rows high, that pairs of CTAs
+// take in order (pair_tiles.cuh).  A tile starts when the panels (256 rows) of what it multiplies
+// are complete, which counters in memory say:
+//     A(i, j)  of step k   X's panels i and j          all B(i, ·)·X of step k − 1
+//     B(i, j)              A's panels i and j          every A(i, ·) and A(·, i)
+//     X(i, n)              B's panel i                 every B(i, ·) and B(·, i)
+// The order makes them complete early: A by rows, B by columns, X by rows.  Nothing is
+// overwritten while it is read: X has two buffers, and a tile that may write a panel of A, B
+// or the older X has waited, through that chain, for all that read it.  A stack is walked in groups of
+// matrices, large enough that a tile's panels were finished a while ago, small enough that
+// what a group passes from product to product is still in L2.
 //
-// Rounding X to 11 bits adds noise in directions that a low-rank G does not have, and
-// a·X multiplies it by a = 3.44 a step.  So that term takes X with 22 bits: as
-// hi + lo·2^-11, two fp16 arrays (hi alone is the products' operand).  In 64-bit simulation
-// with these roundings, the root mean square error of five steps relative to that of the result:
-//                             Gaussian   rank M/4    rank 1
-//     X as hi alone            1.3e-3     1.4e-2     3.2e-2
-//     X as hi + lo             1.5e-3     1.3e-3     1.4e-3
-//     all operands bf16        1.1e-2     1.4e-1     3.4e-1
-// The last step adds `a` to B's diagonal instead: nothing amplifies its rounding any more, and
-// it spares the tile of X.  The result is rounded to bf16 (1.7e-3 by itself).
+// Numbers.  All operands are fp16 (11 bits at the rate of bf16's 8), times powers of two that
+// keep them normal: X·2^6, A·2^10, B·2^6; sums are fp32.  X₀ is G times a power of two, which
+// is exact, and the rest of 1/‖G‖ enters the first step's fp32 sums.  Values whose norm
+// grows past 2^9 in a step (coefficients that diverge) overflow.
+//
+// What a tile needs besides its sums would come from L2 beside the operands, whose way from there is
+// the bound, so as little as possible does:
+//  * B = c·(A + s)² − c·s², s = b/2c: A is stored with s on its diagonal, and B(i, j) is a product of its
+//    rows.  What the diagonal's rounding makes of B's own diagonal is put right from A's
+//    diagonal in fp32; off it, it is a relative 2^-12.  (c = 0: A's product gives B at once.)
+//  * a is on B's diagonal.  Its rounding scales a row of X by 1 ± 2^-12, which leaves the rank as it is.
+//  * Rounding X to 11 bits does not: it adds noise in directions that a low-rank G does not have,
+//    and a multiplies it by 3.44 a step.  So a·X takes X with some 15 bits: hi + lo·2^-13, fp16
+//    and e4m3 (hi alone is the products' operand).
+// In 64-bit simulation with these roundings, the root mean square error of five steps relative to that
+// of the result:
+//                                        Gaussian   rank M/4    rank 1
+//     X as hi alone                       0.9e-3     1.4e-2     3.2e-2
+//     as here                             1.3e-3     1.8e-3     2.8e-3
+//     A and X read, X as two fp16         1.5e-3     1.2e-3     1.4e-3
+//     all operands bf16                   1.1e-2     1.4e-1     3.4e-1
+// The last step's X is rounded to bf16 (1.7e-3 by itself).
 #include <cuda.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/moe_gb300.h"
@@ -39,9 +59,9 @@ using pairs::Tile;
 
 constexpr float X_SCALE = 64.0f;            // 2^6
 constexpr int X_EXPONENT = 6;
-constexpr float A_SCALE = 1024.0f;
 constexpr float B_SCALE = 64.0f;
-constexpr float LO_SCALE = 2048.0f;         // lo = (x - hi)·2^11
+constexpr float LO_SCALE = 8192.0f;         // lo = (x - hi)·2^13
+constexpr float MAX_A_SCALE = 1024.0f;      // of A, less where s is large
 constexpr int SUM_THREADS = 256;
 constexpr int MAX_SUM_BLOCKS = 512;         // of one matrix
 
@@ -73,16 +93,29 @@ __device__ __forceinline__ void values_of(const uint4& w, float (&v)[DTYPE == MO
     }
 }
 
+// Two remainders as e4m3 bytes (largest magnitude 448), the first in the low one, and back.
+__device__ __forceinline__ uint32_t pack_lo2(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x * LO_SCALE, y * LO_SCALE), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 unpack_lo2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return make_float2(f.x * (1.0f / LO_SCALE), f.y * (1.0f / LO_SCALE));
+}
+
 struct Prepare {
     const void* update;
     int64_t elements;             // of a matrix
-    int32_t M, N, ld;             // X is [M, ld], N of the columns in use
+    int32_t M, N, ld, ld_lo;      // X is [M, ld], N of the columns in use
     int32_t sum_blocks;
     float eps;
     float* sums;                  // [batch, sum_blocks]
     float* rest;                  // [batch]: what X₀ still has to be times
     uint16_t* hi;                 // [batch, M, ld]
-    uint16_t* lo;                 // nullable
+    uint8_t* lo;                  // [batch, M, ld_lo], nullable
+    int32_t* ready;               // [batch, counters], zeroed here for the products
+    int32_t* queue;
+    int32_t counters;
 };
 
 // Σ v² of a piece of a matrix.
@@ -131,6 +164,10 @@ __global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int64_t matrix = blockIdx.z;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int i = threadIdx.x; i < p.counters; i += 256) p.ready[matrix * p.counters + i] = 0;
+        if (matrix == 0 && threadIdx.x == 0) *p.queue = 0;
+    }
     float sum = 0.0f;
     for (int i = threadIdx.x; i < p.sum_blocks; i += 256) sum += p.sums[matrix * p.sum_blocks + i];
 #pragma unroll
@@ -174,11 +211,12 @@ __global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
             const float x = tile[r][c + 2 * j] * s, y = tile[r][c + 2 * j + 1] * s;
             h[j] = pack_16bit2<false>(x, y);
             const float2 back = unpack_16bit2<false>(h[j]);
-            l[j] = pack_16bit2<false>((x - back.x) * LO_SCALE, (y - back.y) * LO_SCALE);
+            l[j] = pack_lo2(x - back.x, y - back.y);
         }
-        const int64_t at = (matrix * p.M + m0 + r) * p.ld + n0 + c;
-        *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (p.lo) *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        const int64_t at = matrix * p.M + m0 + r;
+        *reinterpret_cast<uint4*>(p.hi + at * p.ld + n0 + c) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (p.lo)
+            *reinterpret_cast<uint2*>(p.lo + at * p.ld_lo + n0 + c) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
     }
 }
 
@@ -187,33 +225,45 @@ __global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
 // ---------------------------------------------------------------------------
 
 enum Kind { GRAM = 0, POLY = 1, APPLY = 2 };
+enum Map { X_ROWS, X_COLS = X_ROWS + 2, X_RIGHT = X_COLS + 2, A_ROWS = X_RIGHT + 2, A_COLS, B_ROWS, MAPS };
+static_assert(MAPS <= pairs::MAX_MAPS, "maps fit");
 
 struct OrthoProducts {
     int32_t total_tiles, n_maps;
     int32_t* status;
+    int32_t* queue;               // the next tile to take
+    int32_t* ready;               // [batch][3][panels]: warps that have stored their part of a panel
+    int32_t batch, group;         // matrices; of a group
     int32_t M, N;                 // X [M, N]
-    int32_t ld_x, ld_a;           // elements between rows of X; of A and B
-    int32_t tiles;                // of a matrix
-    int32_t n_tiles;              // APPLY: tile columns
-    int32_t steps;                // K steps of a tile
-    float scale;                  // of the sums
-    float add;                    // POLY: of A; APPLY: of X
-    float diagonal;               // POLY: added on the diagonal
-    const float* rest;            // per matrix, first step: GRAM times its square, APPLY times it (nullable)
-    const uint16_t* in_hi;        // POLY: A; APPLY: X (nullable)
-    const uint16_t* in_lo;        // APPLY: nullable
-    uint16_t* dst;                // A, B, X's hi, or the result
-    uint16_t* dst_lo;             // APPLY: nullable
-    int32_t final_step;           // APPLY: dst is the result, in bf16
-    int32_t tall;                 // ... transposed
+    int32_t ld_x, ld_a, ld_lo;    // elements between rows of X's hi; of A and B; of X's lo
+    int32_t panels;               // of 256 rows
+    int32_t cols_a, cols_x;       // tile columns of A and B, of X
+    int32_t tri;                  // tiles of A (or B)
+    int32_t steps;
+    float a, b, c;
+    float a_scale, shift;         // of A; on its diagonal
+    int32_t square;               // c is not 0: B is a product
+    int32_t has_lo;               // X₀ has one
+    const float* rest;            // [batch] what X₀ still has to be times
+    uint16_t* hi[2];              // X, in turn
+    uint8_t* lo[2];
+    float* diagonal;              // [batch, M] A's, as the sums have it
+    uint16_t* A;
+    uint16_t* B;
+    uint16_t* out;
+    int32_t tall;                 // out is transposed
 };
 
-// Tile l of the ones on and below the diagonal, row by row.
-__device__ __forceinline__ void triangle(int32_t l, int32_t& i, int32_t& j) {
-    i = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(l) + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > l) --i;
-    while ((i + 1) * (i + 2) / 2 <= l) ++i;
-    j = l - i * (i + 1) / 2;
+// Columns of 256-row panel q that lie on or below the diagonal, in tiles of BN.
+template <int BN>
+__device__ __forceinline__ int32_t row_tiles(const OrthoProducts& p, int32_t q) {
+    const int32_t n = (q + 1) * (256 / BN);
+    return n < p.cols_a ? n : p.cols_a;
+}
+// Tiles that store a part of panel q of A (or B).
+template <int BN>
+__device__ __forceinline__ int32_t panel_tiles(const OrthoProducts& p, int32_t q) {
+    return row_tiles<BN>(p, q) + (p.panels - 1 - q) * (256 / BN);
 }
 
 // The transpose of a warp's 32 rows x 64 columns (el: a row per lane), through its 4 KB of staging:
@@ -248,100 +298,268 @@ __device__ __forceinline__ void transpose_32x64(const uint4 (&el)[8], uint4 (&ou
     __syncwarp();
 }
 
-template <int KIND>
+// 64 bytes of each of a warp's 32 rows, as lines (lane 4g + i: piece i of rows g, 8 + g, ...)
+// from L2, where this launch itself has put them, and by way of `buf` as rows; and back.
+__device__ __forceinline__ void load_bytes_64(uint4 (&el)[4], const uint8_t* src0, int64_t stride, int lane, int32_t rows,
+                                              int32_t cols) {
+    const int piece = lane & 3, g = lane >> 2;
+    const uint8_t* s = src0 + static_cast<int64_t>(g) * stride + piece * 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        el[r] = make_uint4(0, 0, 0, 0);
+        if (8 * r + g < rows && piece * 16 < cols)
+            el[r] = __ldcg(reinterpret_cast<const uint4*>(s + static_cast<int64_t>(8 * r) * stride));
+    }
+}
+__device__ __forceinline__ uint4* byte_piece(uint8_t* buf, int row, int piece) {
+    return reinterpret_cast<uint4*>(buf + row * 64 + ((piece ^ ((row >> 1) & 3)) * 16));
+}
+__device__ __forceinline__ void bytes_to_rows(uint4 (&el)[4], uint8_t* buf, int lane) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *byte_piece(buf, 8 * r + (lane >> 2), lane & 3) = el[r];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) el[k] = *byte_piece(buf, lane, k);
+    __syncwarp();
+}
+__device__ __forceinline__ void store_bytes_64(const uint4 (&el)[4], uint8_t* buf, uint8_t* dst0, int64_t stride, int lane,
+                                               int32_t rows, int32_t cols) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *byte_piece(buf, lane, k) = el[k];
+    __syncwarp();
+    const int piece = lane & 3, g = lane >> 2;
+    uint8_t* d = dst0 + static_cast<int64_t>(g) * stride + piece * 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (8 * r + g < rows && piece * 16 < cols)
+            *reinterpret_cast<uint4*>(d + static_cast<int64_t>(8 * r) * stride) = *byte_piece(buf, 8 * r + g, piece);
+    __syncwarp();
+}
+
+template <int BN_>
 struct OrthoOp {
-    static constexpr int BN = 256;
+    static constexpr int BN = BN_;
     static constexpr bool BF16 = false;
     static constexpr bool MASKABLE = false;
+    static constexpr bool QUEUE = true;
     using Params = OrthoProducts;
-    enum { LEFT, RIGHT, MAPS };
 
     struct Place {
-        int32_t matrix, row, col;          // of the tile in its matrix
+        int32_t kind, step, matrix, i, j;          // panel of rows, tile column
     };
+    // Order: groups of matrices, their steps, the three products of a step, the group's matrices, tiles.
     static __device__ __forceinline__ Place place(const Params& p, int32_t t) {
         Place at;
-        at.matrix = t / p.tiles;
-        const int32_t l = t - at.matrix * p.tiles;
-        int32_t i, j;
-        if (KIND == APPLY) {
-            i = l / p.n_tiles;
-            j = l - i * p.n_tiles;
+        const int32_t symmetric = (1 + p.square) * p.tri;
+        const int32_t per_matrix = symmetric + p.panels * p.cols_x;
+        const int32_t per_group = p.group * p.steps * per_matrix;
+        const int32_t g = t / per_group;
+        int32_t r = t - g * per_group;
+        const int32_t first = g * p.group;
+        const int32_t n = p.batch - first < p.group ? p.batch - first : p.group;
+        at.step = r / (n * per_matrix);
+        r -= at.step * n * per_matrix;
+        int32_t m, l;
+        if (r < n * symmetric) {
+            at.kind = r < n * p.tri ? GRAM : POLY;
+            if (at.kind == POLY) r -= n * p.tri;
+            m = r / p.tri;
+            l = r - m * p.tri;
+            if (at.kind == GRAM) {
+                at.i = 0;
+                for (int32_t w; l >= (w = row_tiles<BN>(p, at.i)); ++at.i) l -= w;
+                at.j = l;
+            } else {
+                // column j starts in the panel that holds the diagonal
+                at.j = 0;
+                for (int32_t h; l >= (h = p.panels - at.j / (256 / BN)); ++at.j) l -= h;
+                at.i = at.j / (256 / BN) + l;
+            }
         } else {
-            triangle(l, i, j);
+            at.kind = APPLY;
+            r -= n * symmetric;
+            const int32_t per = p.panels * p.cols_x;
+            m = r / per;
+            l = r - m * per;
+            at.i = l / p.cols_x;
+            at.j = l - at.i * p.cols_x;
         }
-        at.row = i * 256;
-        at.col = j * BN;
+        at.matrix = first + m;
         return at;
     }
     static __device__ __forceinline__ Tile tile(const Params& p, int32_t t) {
         const Place at = place(p, t);
         Tile ti{};
-        ti.a_map = LEFT;
-        ti.b_map = RIGHT;
-        ti.b_mn = KIND == APPLY;           // B·X: rows of X are K
-        ti.a_row = at.row;
-        ti.b_row = at.col;
+        const int32_t x = at.step & 1;
+        ti.a_map = at.kind == GRAM ? X_ROWS + x : at.kind == POLY ? A_ROWS : B_ROWS;
+        ti.b_map = at.kind == GRAM ? X_COLS + x : at.kind == POLY ? A_COLS : X_RIGHT + x;
+        ti.b_mn = at.kind == APPLY;                // B·X: rows of X are K
+        ti.a_row = at.i * 256;
+        ti.b_row = at.j * BN;
         ti.batch = at.matrix;
-        ti.steps = p.steps;
+        ti.steps = ((at.kind == GRAM ? p.ld_x : p.M) + pairs::BK - 1) / pairs::BK;
         return ti;
     }
     static __device__ __forceinline__ bool dirty(const Params&) { return false; }
+
+    static __device__ __forceinline__ int32_t* counter(const Params& p, int32_t matrix, int32_t kind, int32_t panel) {
+        return p.ready + (static_cast<int64_t>(matrix) * 3 + kind) * p.panels + panel;
+    }
+    // By a whole warp: what tile t reads is complete.
+    static __device__ __forceinline__ bool wait(const Params& p, int32_t t, volatile int* abort) {
+        const Place at = place(p, t);
+        if (at.kind == GRAM && at.step == 0) return true;
+        const int lane = threadIdx.x & 31;
+        const int32_t from = at.kind == GRAM ? APPLY : at.kind == POLY || !p.square ? GRAM : POLY;
+        const int32_t q = lane == 0 || at.kind == APPLY ? at.i : at.j / (256 / BN);
+        // every one of a tile's 16 warps counts, in every step so far
+        const int32_t need = 16 * (at.kind == GRAM ? at.step * p.cols_x : (at.step + 1) * panel_tiles<BN>(p, q));
+        bool ok = true;
+        if (lane < 2) {
+            const int32_t* c = counter(p, at.matrix, from, q);
+            auto reached = [&] {
+                int32_t v;
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+                return v >= need;
+            };
+            if (!reached()) {
+                const uint64_t t0 = global_timer_ns();
+                while (ok && !reached()) {
+                    if (*abort) ok = false;
+                    else if (global_timer_ns() - t0 > pairs::WAIT_LIMIT_NS) {
+                        *abort = 1;
+                        ok = false;
+                    }
+                }
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
+        return ok;
+    }
 
     struct Finish {
         const Params& p;
         uint8_t* staging;
         int32_t row, odd, lane;
         Place at;
+        int32_t col0;                      // the tile's first column
         int32_t r0, rows;                  // the warp's first row, and how many of its 32 exist
-        float scale, add;
-        uint4 hi[KIND == GRAM ? 1 : 8], lo[KIND == APPLY ? 8 : 1];   // asked for ahead of the tile
+        bool first, last, with_lo, store_lo;
+        float rest;
+        uint4 lo[4];                       // X's, asked for ahead of the tile
 
         __device__ __forceinline__ Finish(const Params& p_, uint8_t* staging_, int32_t row_, int odd_, int lane_)
             : p(p_), staging(staging_), row(row_), odd(odd_), lane(lane_) {}
 
-        __device__ __forceinline__ int32_t width() const { return KIND == APPLY ? p.ld_x : p.ld_a; }
-        __device__ __forceinline__ int64_t element(int c) const {
-            return (static_cast<int64_t>(at.matrix) * p.M + r0) * width() + at.col + c * 64;
+        __device__ __forceinline__ int32_t width() const { return at.kind == APPLY ? p.ld_x : p.ld_a; }
+        __device__ __forceinline__ int64_t element(int c, int32_t ld) const {
+            return (static_cast<int64_t>(at.matrix) * p.M + r0) * ld + col0 + c * 64;
         }
         __device__ __forceinline__ void ask(int c) {
-            if constexpr (KIND != GRAM) {
-                const int32_t cols = width() - at.col - c * 64;
-                if (rows <= 0 || cols <= 0) return;
-                if (p.in_hi) load_lines_64(hi, p.in_hi + element(c), width(), lane, rows, cols);
-                if constexpr (KIND == APPLY)
-                    if (p.in_lo) load_lines_64(lo, p.in_lo + element(c), width(), lane, rows, cols);
-            }
+            const int32_t cols = p.ld_lo - col0 - c * 64;
+            if (with_lo && rows > 0 && cols > 0)
+                load_bytes_64(lo, p.lo[at.step & 1] + element(c, p.ld_lo), p.ld_lo, lane, rows, cols);
         }
         __device__ __forceinline__ bool before(int32_t t) {
             at = place(p, t);
-            r0 = at.row + row;
+            col0 = at.j * BN;
+            r0 = at.i * 256 + row;
             rows = p.M - r0;
             rows = rows > 32 ? 32 : rows;
-            scale = p.scale;
-            add = p.add;
-            if (p.rest) {
-                const float f = __ldg(p.rest + at.matrix);
-                scale *= KIND == GRAM ? f * f : f;
-                add *= f;
-            }
+            first = at.step == 0;
+            last = at.step + 1 == p.steps;
+            with_lo = at.kind == APPLY && !last && (!first || p.has_lo);
+            store_lo = at.kind == APPLY && at.step + 2 < p.steps;          // the last step reads hi alone
+            rest = first ? __ldg(p.rest + at.matrix) : 1.0f;
             ask(odd);
             return true;
         }
         __device__ __forceinline__ void pass(int c, uint32_t taddr) {
-            const int32_t cols = width() - at.col - c * 64;
+            const int32_t cols = width() - col0 - c * 64;
             if (rows <= 0 || cols <= 0) return;
-            MOE_DCHECK(at.row >= 0 && r0 < p.M && at.col + c * 64 < width() &&
-                           (static_cast<int64_t>(at.matrix) + 1) * p.tiles <= p.total_tiles,
+            MOE_DCHECK(at.matrix < p.batch && at.i < p.panels && at.step < p.steps && r0 >= 0 && r0 < p.M && col0 >= 0,
                        p.status);
-            if constexpr (KIND != GRAM) {
+            if (at.kind == APPLY) {
                 if (c != odd) ask(c);
-                if (p.in_hi) lines_to_rows(hi, staging, lane);
-                if constexpr (KIND == APPLY)
-                    if (p.in_lo) lines_to_rows(lo, staging, lane);
+                finish_x(c, taddr, cols);
+            } else {
+                finish_symmetric(c, taddr, cols);
             }
-            const bool bf16 = KIND == APPLY && p.final_step;
-            uint4 el[8], rest[KIND == APPLY ? 8 : 1];
+        }
+        // A or B: the sums, and on the diagonal what it takes to have B as (A + s)².
+        __device__ __forceinline__ void finish_symmetric(int c, uint32_t taddr, int32_t cols) {
+            const bool b_now = at.kind == POLY || !p.square;
+            const float to_a = rest * rest * (1.0f / (X_SCALE * X_SCALE));       // GRAM: the sums as A's values
+            const float unscale = 1.0f / (p.a_scale * p.a_scale);                // POLY: the sums as values
+            const float scale = at.kind == POLY ? p.c * B_SCALE * unscale : b_now ? p.b * B_SCALE * to_a : p.a_scale * to_a;
+            // does the diagonal pass through the warp's 32 rows and these 64 columns; which of mine is on it
+            const int32_t on = r0 + lane - col0 - c * 64;
+            const bool diagonal = static_cast<uint32_t>(r0 - col0 - c * 64) < 64u;
+            float* d_at = p.diagonal + static_cast<int64_t>(at.matrix) * p.M + r0 + lane;
+            const bool mine = diagonal && lane < rows;
+            const float a_ii = mine && at.kind == POLY ? __ldcg(d_at) : 0.0f;
+            uint4 el[8];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + hh * 32, v);
+                tmem_ld_wait();
+                float fixed = 0.0f;
+                if (diagonal) {
+                    // every lane's own diagonal element (of another half: unused)
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (hh * 32 + i == on) sum = __uint_as_float(v[i]);
+                    const bool here = mine && (on >> 5) == hh;
+                    if (at.kind == POLY) {
+                        const float q = __half2float(__float2half_rn((a_ii + p.shift) * p.a_scale)) / p.a_scale;
+                        const float s = q - a_ii;            // what the rounding made of the shift
+                        fixed = (p.b * a_ii + p.c * (sum * unscale - 2.0f * s * a_ii - s * s) + p.a) * B_SCALE;
+                    } else {
+                        const float a = sum * to_a;
+                        if (here && !b_now) *d_at = a;
+                        fixed = b_now ? (p.b * a + p.a) * B_SCALE : (a + p.shift) * p.a_scale;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float x = __uint_as_float(v[8 * k + 2 * j]) * scale;
+                        float y = __uint_as_float(v[8 * k + 2 * j + 1]) * scale;
+                        if (diagonal) {
+                            if (hh * 32 + 8 * k + 2 * j == on) x = fixed;
+                            if (hh * 32 + 8 * k + 2 * j + 1 == on) y = fixed;
+                        }
+                        w[j] = pack_16bit2<false>(x, y);
+                    }
+                    el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            uint16_t* dst = b_now ? p.B : p.A;
+            store_staged_64(el, staging, dst + element(c, p.ld_a), p.ld_a, lane, rows, cols);
+            if ((at.j + 1) * BN <= at.i * 256) {
+                // the tile across the diagonal
+                uint4 tr[8];
+                transpose_32x64(el, tr, staging, lane);
+                const int32_t m = r0 + (lane & 3) * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int32_t n = col0 + c * 64 + 8 * k + (lane >> 2);
+                    if (n < p.M && m < p.ld_a)
+                        *reinterpret_cast<uint4*>(dst + (static_cast<int64_t>(at.matrix) * p.M + n) * p.ld_a + m) = tr[k];
+                }
+            }
+        }
+        // X, or the result: the sums (B has a on its diagonal) and a·lo.
+        __device__ __forceinline__ void finish_x(int c, uint32_t taddr, int32_t cols) {
+            const float scale = rest * (last ? 1.0f / (B_SCALE * X_SCALE) : 1.0f / B_SCALE);
+            const float add = rest * p.a;
+            if (with_lo) bytes_to_rows(lo, staging, lane);
+            uint4 el[8];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 uint32_t v[32];
@@ -349,71 +567,57 @@ struct OrthoOp {
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4], wl[4];
+                    uint32_t w[4], l[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float x = __uint_as_float(v[8 * k + 2 * j]) * scale;
                         float y = __uint_as_float(v[8 * k + 2 * j + 1]) * scale;
-                        if constexpr (KIND != GRAM) {
-                            if (p.in_hi) {
-                                const uint32_t hw = reinterpret_cast<const uint32_t*>(&hi[4 * hh + k])[j];
-                                float2 f = unpack_16bit2<false>(hw);
-                                if constexpr (KIND == APPLY) {
-                                    if (p.in_lo) {
-                                        const float2 g = unpack_16bit2<false>(reinterpret_cast<const uint32_t*>(&lo[4 * hh + k])[j]);
-                                        f.x += g.x * (1.0f / LO_SCALE);
-                                        f.y += g.y * (1.0f / LO_SCALE);
-                                    }
-                                }
-                                x += add * f.x;
-                                y += add * f.y;
-                            }
+                        // columns 32 hh + 8 k + 2 j: bytes 8 k + 2 j of the half's 32
+                        uint32_t& word = reinterpret_cast<uint32_t*>(&lo[2 * hh + (k >> 1)])[2 * (k & 1) + (j >> 1)];
+                        if (with_lo) {
+                            const float2 f = unpack_lo2((word >> (16 * (j & 1))) & 0xffffu);
+                            x += add * f.x;
+                            y += add * f.y;
                         }
-                        if constexpr (KIND == POLY) {
-                            const int32_t col = at.col + c * 64 + hh * 32 + 8 * k + 2 * j;
-                            if (col == r0 + lane) x += p.diagonal;
-                            if (col + 1 == r0 + lane) y += p.diagonal;
+                        w[j] = last ? pack_16bit2<true>(x, y) : pack_16bit2<false>(x, y);
+                        if (store_lo) {
+                            const float2 back = unpack_16bit2<false>(w[j]);
+                            l[j] = pack_lo2(x - back.x, y - back.y);
                         }
-                        w[j] = bf16 ? pack_16bit2<true>(x, y) : pack_16bit2<false>(x, y);
-                        if constexpr (KIND == APPLY) {
-                            if (p.dst_lo) {
-                                const float2 back = unpack_16bit2<false>(w[j]);
-                                wl[j] = pack_16bit2<false>((x - back.x) * LO_SCALE, (y - back.y) * LO_SCALE);
-                            }
-                        }
+                        if (store_lo && (j & 1)) word = l[j - 1] | l[j] << 16;
                     }
                     el[4 * hh + k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if constexpr (KIND == APPLY)
-                        if (p.dst_lo) rest[4 * hh + k] = make_uint4(wl[0], wl[1], wl[2], wl[3]);
                 }
             }
-            if (KIND == APPLY && p.final_step) {
+            if (last) {
                 store_result(el, c);
                 return;
             }
-            store_staged_64(el, staging, p.dst + element(c), width(), lane, rows, cols);
-            if constexpr (KIND == APPLY)
-                if (p.dst_lo) store_staged_64(rest, staging, p.dst_lo + element(c), width(), lane, rows, cols);
-            if constexpr (KIND != APPLY) {
-                if (at.col + BN <= at.row) {
-                    // the tile across the diagonal
-                    uint4 tr[8];
-                    transpose_32x64(el, tr, staging, lane);
-                    const int32_t m = r0 + (lane & 3) * 8;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int32_t n = at.col + c * 64 + 8 * k + (lane >> 2);
-                        if (n < p.M && m < p.ld_a)
-                            *reinterpret_cast<uint4*>(p.dst + (static_cast<int64_t>(at.matrix) * p.M + n) * p.ld_a + m) = tr[k];
-                    }
-                }
+            store_staged_64(el, staging, p.hi[(at.step + 1) & 1] + element(c, p.ld_x), p.ld_x, lane, rows, cols);
+            if (store_lo)
+                store_bytes_64(lo, staging, p.lo[(at.step + 1) & 1] + element(c, p.ld_lo), p.ld_lo, lane, rows,
+                               p.ld_lo - col0 - c * 64);
+        }
+        // This warp's part of the tile is stored: for TMA loads and for the other SMs.
+        __device__ __forceinline__ void done() {
+            if (at.kind == APPLY && last) return;
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+                auto add_one = [&](int32_t panel) {
+                    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter(p, at.matrix, at.kind, panel)) : "memory");
+                };
+                add_one(at.i);
+                const int32_t across = at.j / (256 / BN);
+                if (at.kind != APPLY && across != at.i) add_one(across);
             }
         }
         // 64 columns of the warp's rows of the result [M, N], or [N, M] where it is tall.
         __device__ __forceinline__ void store_result(const uint4 (&el)[8], int c) {
-            const int32_t n0 = at.col + c * 64;
+            const int32_t n0 = col0 + c * 64;
             if (n0 >= p.N) return;
-            uint16_t* out = p.dst + static_cast<int64_t>(at.matrix) * p.M * p.N;
+            uint16_t* out = p.out + static_cast<int64_t>(at.matrix) * p.M * p.N;
             if (!p.tall) {
                 if ((p.N & 7) == 0) {
                     store_staged_64(el, staging, out + static_cast<int64_t>(r0) * p.N + n0, p.N, lane, rows, p.N - n0);
@@ -452,8 +656,9 @@ struct OrthoOp {
 
 struct OrthoLayout {
     bool tall;
-    int32_t M, N, ld_x, ld_a, sum_blocks;
-    int64_t hi[2], lo[2], A, B, sums, rest, bytes;
+    int32_t M, N, ld_x, ld_a, ld_lo, sum_blocks;
+    int64_t hi[2], lo[2], A, B, diagonal, sums, rest, ready, queue, bytes;
+    int32_t panels;
 };
 
 OrthoLayout ortho_layout(int64_t batch, int32_t rows, int32_t cols) {
@@ -463,6 +668,7 @@ OrthoLayout ortho_layout(int64_t batch, int32_t rows, int32_t cols) {
     l.N = l.tall ? rows : cols;
     l.ld_x = (l.N + 7) / 8 * 8;
     l.ld_a = (l.M + 7) / 8 * 8;
+    l.ld_lo = (l.N + 15) / 16 * 16;
     const int64_t blocks = (static_cast<int64_t>(rows) * cols + SUM_THREADS * 64 - 1) / (SUM_THREADS * 64);
     l.sum_blocks = static_cast<int32_t>(blocks > MAX_SUM_BLOCKS ? MAX_SUM_BLOCKS : blocks);
     int64_t at = 0;
@@ -474,12 +680,16 @@ OrthoLayout ortho_layout(int64_t batch, int32_t rows, int32_t cols) {
     const int64_t x = batch * l.M * l.ld_x * 2, a = batch * l.M * l.ld_a * 2;
     for (int i = 0; i < 2; ++i) {
         l.hi[i] = take(x);
-        l.lo[i] = take(x);
+        l.lo[i] = take(batch * l.M * l.ld_lo);
     }
     l.A = take(a);
     l.B = take(a);
+    l.diagonal = take(batch * l.M * 4);
     l.sums = take(batch * l.sum_blocks * 4);
     l.rest = take(batch * 4);
+    l.panels = (l.M + 255) / 256;
+    l.ready = take(batch * 3 * l.panels * 4);
+    l.queue = take(4);
     l.bytes = at;
     return l;
 }
@@ -512,28 +722,40 @@ cudaError_t launch_prepare(const Prepare& p, int64_t batch, bool tall, cudaStrea
                 : launch_pdl(prepare_kernel<DTYPE, false>, grid, 256, stream, p);
 }
 
-template <int KIND>
-cudaError_t launch_product(const void* left, const void* right, const OrthoLayout& l, int64_t batch, OrthoProducts p,
-                           cudaStream_t stream) {
-    using Op = OrthoOp<KIND>;
+template <int BN>
+cudaError_t launch_products(const OrthoLayout& l, int64_t batch, OrthoProducts& p, cudaStream_t stream) {
+    using Op = OrthoOp<BN>;
     pairs::Maps maps;
-    const int32_t ld_left = KIND == GRAM ? l.ld_x : l.ld_a, ld_right = KIND == POLY ? l.ld_a : l.ld_x;
-    // rows and their lengths in memory: columns up to the 16-byte boundary hold zeros
-    if (!pairs::map_3d(&maps.m[Op::LEFT], left, batch, l.M, ld_left, ld_left, pairs::BM) ||
-        !pairs::map_3d(&maps.m[Op::RIGHT], right, batch, l.M, ld_right, ld_right, KIND == APPLY ? pairs::BK : Op::BN / 2))
+    // rows with the columns up to their 16-byte boundary, which hold zeros
+    auto map = [&](int i, const void* base, int32_t ld, int box_rows) {
+        return pairs::map_3d(&maps.m[i], base, batch, l.M, ld, ld, box_rows);
+    };
+    for (int i = 0; i < 2; ++i)
+        if (!map(X_ROWS + i, p.hi[i], l.ld_x, pairs::BM) || !map(X_COLS + i, p.hi[i], l.ld_x, BN / 2) ||
+            !map(X_RIGHT + i, p.hi[i], l.ld_x, pairs::BK))
+            return cudaErrorInvalidValue;
+    if (!map(A_ROWS, p.A, l.ld_a, pairs::BM) || !map(A_COLS, p.A, l.ld_a, BN / 2) || !map(B_ROWS, p.B, l.ld_a, pairs::BM))
         return cudaErrorInvalidValue;
-    const int32_t m_tiles = pairs::ceil_div(l.M, 256);
-    p.n_maps = Op::MAPS;
-    p.M = l.M;
-    p.N = l.N;
-    p.ld_x = l.ld_x;
-    p.ld_a = l.ld_a;
-    p.n_tiles = pairs::ceil_div(l.ld_x, Op::BN);
-    p.tiles = KIND == APPLY ? m_tiles * p.n_tiles : m_tiles * (m_tiles + 1) / 2;
-    p.total_tiles = static_cast<int32_t>(batch) * p.tiles;
-    p.steps = pairs::ceil_div(KIND == GRAM ? l.ld_x : l.M, pairs::BK);
+    const int n_pairs = pairs::resident_pairs<Op>();
+    if (n_pairs == 0) return cudaErrorNoDevice;
+    p.n_maps = MAPS;
+    p.panels = l.panels;
+    p.cols_a = pairs::ceil_div(l.M, BN);
+    p.cols_x = pairs::ceil_div(l.ld_x, BN);
+    p.tri = 0;
+    for (int32_t q = 0; q < p.panels; ++q) {
+        const int32_t n = (q + 1) * (256 / BN);
+        p.tri += n < p.cols_a ? n : p.cols_a;
+    }
+    // twice as many tiles of A as there are pairs
+    const int64_t group = (2 * n_pairs + p.tri - 1) / p.tri;
+    p.group = static_cast<int32_t>(group < batch ? group : batch);
+    p.total_tiles = static_cast<int32_t>(batch) * p.steps * ((1 + p.square) * p.tri + p.panels * p.cols_x);
     return pairs::launch<Op>(maps, p, stream);
 }
+
+// Tiles of A over the stack, 256 columns wide.
+int64_t gram_tiles(const OrthoLayout& l, int64_t batch) { return batch * l.panels * (l.panels + 1) / 2; }
 
 }  // namespace
 
@@ -553,51 +775,53 @@ cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream) {
     pr.M = l.M;
     pr.N = l.N;
     pr.ld = l.ld_x;
+    pr.ld_lo = l.ld_lo;
     pr.sum_blocks = l.sum_blocks;
     pr.eps = a.eps;
     pr.sums = reinterpret_cast<float*>(ws + l.sums);
     pr.rest = reinterpret_cast<float*>(ws + l.rest);
     pr.hi = u16(l.hi[0]);
-    pr.lo = f32 ? u16(l.lo[0]) : nullptr;         // 16-bit values are hi by themselves
+    pr.lo = f32 ? ws + l.lo[0] : nullptr;         // 16-bit values are hi by themselves
+    pr.ready = reinterpret_cast<int32_t*>(ws + l.ready);
+    pr.queue = reinterpret_cast<int32_t*>(ws + l.queue);
+    pr.counters = 3 * l.panels;
     cudaError_t err = f32 ? launch_prepare<MOE_DTYPE_F32>(pr, a.batch, l.tall, stream)
                     : a.dtype == MOE_DTYPE_BF16 ? launch_prepare<MOE_DTYPE_BF16>(pr, a.batch, l.tall, stream)
                                                 : launch_prepare<MOE_DTYPE_F16>(pr, a.batch, l.tall, stream);
     if (err != cudaSuccess) return err;
-    for (int32_t k = 0; k < a.steps; ++k) {
-        const bool last = k + 1 == a.steps;
-        uint16_t* hi = u16(l.hi[k & 1]);
-        OrthoProducts g{};
-        g.status = a.status;
-        g.scale = A_SCALE / (X_SCALE * X_SCALE);
-        g.rest = k == 0 ? pr.rest : nullptr;
-        g.dst = u16(l.A);
-        if ((err = launch_product<GRAM>(hi, hi, l, a.batch, g, stream)) != cudaSuccess) return err;
-        OrthoProducts q{};
-        q.status = a.status;
-        q.scale = a.c * B_SCALE / (A_SCALE * A_SCALE);
-        q.add = a.b * B_SCALE / A_SCALE;
-        q.diagonal = last ? a.a * B_SCALE : 0.0f;
-        q.in_hi = u16(l.A);
-        q.dst = u16(l.B);
-        if ((err = launch_product<POLY>(u16(l.A), u16(l.A), l, a.batch, q, stream)) != cudaSuccess) return err;
-        OrthoProducts x{};
-        x.status = a.status;
-        x.scale = last ? 1.0f / (B_SCALE * X_SCALE) : 1.0f / B_SCALE;
-        x.rest = k == 0 ? pr.rest : nullptr;
-        if (last) {
-            x.final_step = 1;
-            x.tall = l.tall ? 1 : 0;
-            x.dst = a.out;
-        } else {
-            x.add = a.a;
-            x.in_hi = hi;
-            x.in_lo = k > 0 || f32 ? u16(l.lo[k & 1]) : nullptr;
-            x.dst = u16(l.hi[(k + 1) & 1]);
-            x.dst_lo = k + 2 < a.steps ? u16(l.lo[(k + 1) & 1]) : nullptr;
-        }
-        if ((err = launch_product<APPLY>(u16(l.B), hi, l, a.batch, x, stream)) != cudaSuccess) return err;
+    OrthoProducts p{};
+    p.status = a.status;
+    p.queue = pr.queue;
+    p.ready = pr.ready;
+    p.batch = static_cast<int32_t>(a.batch);
+    p.M = l.M;
+    p.N = l.N;
+    p.ld_x = l.ld_x;
+    p.ld_a = l.ld_a;
+    p.ld_lo = l.ld_lo;
+    p.steps = a.steps;
+    p.a = a.a;
+    p.b = a.b;
+    p.c = a.c;
+    p.square = a.c != 0.0f ? 1 : 0;
+    p.shift = p.square ? a.b / (2.0f * a.c) : 0.0f;
+    // A + s is at most about 2^14 in fp16
+    p.a_scale = MAX_A_SCALE;
+    while (p.a_scale * fabsf(p.shift) > 16384.0f) p.a_scale *= 0.5f;
+    p.has_lo = f32 ? 1 : 0;
+    p.rest = pr.rest;
+    for (int i = 0; i < 2; ++i) {
+        p.hi[i] = u16(l.hi[i]);
+        p.lo[i] = ws + l.lo[i];
     }
-    return cudaSuccess;
+    p.diagonal = reinterpret_cast<float*>(ws + l.diagonal);
+    p.A = u16(l.A);
+    p.B = u16(l.B);
+    p.out = a.out;
+    p.tall = l.tall ? 1 : 0;
+    // Narrower tiles where A has fewer than a round of the wide ones.
+    return gram_tiles(l, a.batch) >= 76 ? launch_products<256>(l, a.batch, p, stream)
+                                        : launch_products<128>(l, a.batch, p, stream);
 }
 
 }  // namespace moe

@@ -15,10 +15,19 @@
 //
 // An operation `Op` has
 //     BN, BF16, MASKABLE       tile columns, operand type, see below
+//     QUEUE                    see below
 //     Params                   with int32_t total_tiles, n_maps, *status
 //     tile(p, t)               what tile t multiplies (nothing where it has no steps)
 //     Finish(p, smem, ...)     per epilogue warp: before(t) ahead of the sums (false where
-//                              there are none), pass(c, taddr) for 64 columns of its 32 rows
+//                              there are none), pass(c, taddr) for 64 columns of its 32 rows;
+//                              with QUEUE done(), which publishes what the warp stored
+// QUEUE: pairs take tiles from a counter in memory (Params::queue, zero at the start) in the order of
+// their numbers instead of every n-th one, and a tile may need results of lower ones:
+// Op::wait(p, t, abort) returns once they are there.  Whoever holds the lowest unfinished
+// tile never waits for one that no running pair holds, so this needs no pair to be
+// resident beside another.  The even CTA's warp 0 takes a tile and hands its number to all
+// roles of both CTAs through a ring of QUEUE entries.
+//
 // MASKABLE: where Op::dirty(p) says so, rows of an M/N-major B (rows of K) whose bit
 // Op::valid64 gives as 0 are set to zero in shared memory before they are multiplied, so
 // that what stands there, a NaN say, meets nothing.  Each CTA then has its own "full"
@@ -45,7 +54,8 @@ constexpr int BM = 128;                        // rows of A per CTA
 constexpr int BK = 64;                         // K per stage
 constexpr int THREADS = 320;                   // producer, MMA and eight epilogue warps
 constexpr int EPI_WARPS = 8;
-constexpr int MAX_MAPS = 4;
+constexpr int MAX_MAPS = 10;
+constexpr int QUEUE = 4;                       // tiles that the roles of a pair may be apart
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int BOX_BYTES = BK * 128;            // an M/N-major box: 64 along M/N x BK rows of K
 constexpr int STAGING_BYTES = 32 * 128;        // per epilogue warp
@@ -72,10 +82,11 @@ struct Layout {
     static constexpr int STAGES = 196608 / STAGE_BYTES;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * STAGING_BYTES;
-    static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1;      // full, empty, peer, tfull, tempty, drain
+    static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1 + 2 * QUEUE;   // full, empty, peer, tfull, tempty, drain, queue
     static constexpr int OFF_TMEM_SLOT = OFF_BARS + NUM_BARS * 8;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
-    static constexpr int SMEM_BYTES = 1024 + OFF_ABORT + 4;
+    static constexpr int OFF_QUEUE = OFF_ABORT + 4;
+    static constexpr int SMEM_BYTES = 1024 + OFF_QUEUE + 4 * QUEUE;
     static constexpr int TMEM_COLS = 2 * BN;
     static_assert(SMEM_BYTES <= 227 * 1024, "the ring fits");
 };
@@ -107,6 +118,9 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     const uint32_t bar_tfull = bar_peer + 8 * STAGES;            // [2]
     const uint32_t bar_tempty = bar_tfull + 16;                  // [2] (used in the even CTA)
     const uint32_t bar_drain = bar_tempty + 16;                  // [1]
+    const uint32_t bar_qfull = bar_drain + 8;                    // [QUEUE]
+    const uint32_t bar_qempty = bar_qfull + 8 * QUEUE;           // [QUEUE] (used in the even CTA)
+    volatile int32_t* queue = reinterpret_cast<volatile int32_t*>(smem + L::OFF_QUEUE);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_TMEM_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ABORT);
 
@@ -127,6 +141,10 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             mbar_init(bar_tempty + 8 * a, 2 * EPI_WARPS);
         }
         mbar_init(bar_drain, 1);
+        for (int q = 0; q < QUEUE; ++q) {
+            mbar_init(bar_qfull + 8 * q, 1);
+            mbar_init(bar_qempty + 8 * q, 2 * EPI_WARPS + 2);    // every role but the one that fills it
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -151,6 +169,44 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     const uint32_t issue = elect_one();
     int64_t issued = 0;            // stages that warp 0 has filled
 
+    // The next tile of this warp's role; past the last one at the end.
+    uint32_t qslot = 0, qphase = 0;
+    int32_t t_next = pair;
+    const uint32_t leader_qempty = mapa_shared(bar_qempty, 0);
+    auto next_tile = [&]() -> int32_t {
+        if constexpr (!Op::QUEUE) {
+            const int32_t t = t_next;
+            t_next += n_pairs;
+            return t;
+        } else {
+            const bool there = mbar_wait_bounded<true>(bar_qfull + 8 * qslot, qphase, abort_flag, WAIT_LIMIT_NS);
+            if (!__all_sync(0xffffffffu, there)) return p.total_tiles;
+            const int32_t t = __shfl_sync(0xffffffffu, queue[qslot], 0);
+            if (lane == 0) mbar_arrive_cluster(leader_qempty + 8 * qslot);
+            if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
+            return t;
+        }
+    };
+    // The same for the role that fills the queue; it asks for the tile after it meanwhile.
+    auto take_tile = [&]() -> int32_t {
+        if constexpr (!Op::QUEUE) {
+            return next_tile();
+        } else {
+            const int32_t t = __shfl_sync(0xffffffffu, t_next, 0);
+            if (!mbar_wait_warp(bar_qempty + 8 * qslot, qphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) return p.total_tiles;
+            if (lane == 0) {
+                queue[qslot] = t;
+                const uint32_t peer = mapa_shared(smem_u32(const_cast<int32_t*>(&queue[qslot])), 1);
+                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer), "r"(t) : "memory");
+                mbar_arrive(bar_qfull + 8 * qslot);
+                mbar_arrive_cluster(mapa_shared(bar_qfull + 8 * qslot, 1));
+                if (t < p.total_tiles) t_next = atomicAdd(p.queue, 1);
+            }
+            if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
+            return t;
+        }
+    };
+
     if (warp == 0) {
         // ---- TMA producer, both CTAs
         const uint64_t policy = l2_policy_evict_normal();
@@ -159,9 +215,20 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t bytes = (masked ? 1 : 2) * L::STAGE_BYTES;
         uint32_t stage = 0, phase = 0;
         bool ok = true;
-        for (int32_t t = pair; t < p.total_tiles && ok; t += n_pairs) {
+        if constexpr (Op::QUEUE) {
+            if (leader && lane == 0) t_next = atomicAdd(p.queue, 1);
+            __syncwarp();
+        }
+        while (ok) {
+            const int32_t t = leader ? take_tile() : next_tile();
+            if (t >= p.total_tiles) break;
             const Tile ti = Op::tile(p, t);
             if (ti.steps == 0) continue;
+            if constexpr (Op::QUEUE) {
+                if (!Op::wait(p, t, abort_flag)) break;
+                // what generic stores wrote is read by TMA from here on
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
             const int32_t arow = ti.a_row + static_cast<int32_t>(rank) * BM;
             const int32_t brow = ti.b_row + static_cast<int32_t>(rank) * (BN / 2);
             const CUtensorMap* am = &maps.m[ti.a_map];
@@ -202,7 +269,9 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t leader_peer = mapa_shared(bar_peer, 0);
         uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
         bool ok = true;
-        for (int32_t t = pair; t < p.total_tiles && ok && (leader || masked); t += n_pairs) {
+        while (ok && (leader || masked)) {
+            const int32_t t = next_tile();
+            if (t >= p.total_tiles) break;
             const Tile ti = Op::tile(p, t);
             if (ti.steps == 0) continue;
             if (leader) {
@@ -285,7 +354,12 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t leader_tempty = mapa_shared(bar_tempty, 0);
         typename Op::Finish fin(p, staging, static_cast<int32_t>(rank) * BM + quarter * 32, odd, lane);
         uint32_t acc = 0, aphase = 0;
-        for (int32_t t = pair; t < p.total_tiles; t += n_pairs) {
+        while (true) {
+            const int32_t t = next_tile();
+            if (t >= p.total_tiles) break;
+            if constexpr (Op::QUEUE) {
+                if (!Op::wait(p, t, abort_flag)) break;
+            }
             if (!fin.before(t)) continue;
             // one answer for the whole warp, whose TMEM loads are collective
             if (!mbar_wait_warp(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS)) break;
@@ -300,6 +374,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 if (leader) mbar_arrive(bar_tempty + 8 * acc);
                 else mbar_arrive_cluster_relaxed(leader_tempty + 8 * acc);
             }
+            if constexpr (Op::QUEUE) fin.done();
             acc ^= 1u;
             if (acc == 0) aphase ^= 1u;
         }

@@ -74,6 +74,7 @@ struct GradOp {
     static constexpr int BN = TILE;
     static constexpr bool BF16 = BF16_;
     static constexpr bool MASKABLE = true;
+    static constexpr bool QUEUE = false;
     using Params = GradProducts;
     enum { DZ, W_T, DZ_T, X_T, MAPS };
 

@@ -79,6 +79,7 @@ struct Orthogonalize {
     int32_t* status;
 };
 
+constexpr float ORTHO_MAX_SHIFT = 1024.0f;         // |b / 2c|, where c is not 0
 int64_t orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols);
 cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream);
 

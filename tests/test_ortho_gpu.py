@@ -1,7 +1,7 @@
 """Orthogonalised updates against the iteration in 64 bits.
 
 Tolerances come from the iteration itself, run in 64 bits with the kernels' roundings and no others
-(fp16 operands, 22 bits of X in the a·X term, bf16 at the end): the same sizes of error enter
+(fp16 operands, some 15 bits of X in the a·X term, bf16 at the end): the same sizes of error enter
 at the same places, though not the same errors.  Their sums over many entries agree to a few percent, so
 the root mean square error may be 1.25 times the emulated one, and the largest of some 10^5 errors of
 nearly normal size 2.5 times.
@@ -28,30 +28,34 @@ def iterate(g, steps=5, abc=ABC, eps=1e-7, rounded=False):
     norm = x.flatten(1).norm(dim=1).clamp(min=eps)[:, None, None]
     tall = x.shape[1] > x.shape[2]
     x = (x.transpose(1, 2) if tall else x) / norm
-    full = x
-    if rounded and g.dtype == torch.float32:
-        x = r16(x, 64.0)                       # hi; 16-bit inputs are exact
+    if not rounded:
+        for _ in range(steps):
+            A = x @ x.transpose(1, 2)
+            x = a * x + (b * A + c * (A @ A)) @ x
+        return x.transpose(1, 2) if tall else x
+    eye = torch.eye(x.shape[1], dtype=x.dtype, device=x.device)
+    hi, lo = x, torch.zeros_like(x)
+    if g.dtype == torch.float32:               # 16-bit inputs are exact
+        hi = r16(x, 64.0)
+        lo = ((x - hi) * 64 * 8192).float().to(torch.float8_e4m3fn).double() / (64 * 8192)
     for k in range(steps):
-        last = k + 1 == steps
-        A = x @ x.transpose(1, 2)
-        if rounded:
-            A = r16(A, 1024.0)
-        B = b * A + c * (A @ A)
-        if rounded:
-            if last:
-                B = B + a * torch.eye(B.shape[1], dtype=B.dtype, device=B.device)
-            B = r16(B, 64.0)
-            full = B @ x + (0 if last else a * full)
-            hi = r16(full, 64.0)
-            if k + 2 < steps:
-                full = hi + r16(full - hi, 64.0 * 2048)
-            else:
-                full = hi if not last else full
-            x = hi
+        A = hi @ hi.transpose(1, 2)
+        d = A.diagonal(dim1=1, dim2=2)
+        if c != 0:
+            # (A + s)², s on the diagonal rounded with it, and put right on B's
+            q = r16(A * (1 - eye) + torch.diag_embed(d + b / (2 * c)), 1024.0)
+            B = c * (q @ q)
+            s = q.diagonal(dim1=1, dim2=2) - d
+            on = b * d + B.diagonal(dim1=1, dim2=2) - c * (2 * s * d + s * s)
         else:
-            x = full = a * x + B @ x
-    out = full.transpose(1, 2) if tall else full
-    return out.bfloat16().double() if rounded else out
+            B, on = b * A, b * d
+        B = r16(B * (1 - eye) + torch.diag_embed(on + a), 64.0)
+        full = B @ hi + (a * lo if k + 1 < steps else 0)
+        hi = r16(full, 64.0)
+        lo = ((full - hi) * 64 * 8192).float().to(torch.float8_e4m3fn).double() / (64 * 8192)
+        if k + 2 >= steps:
+            lo = torch.zeros_like(lo)
+    return (full.transpose(1, 2) if tall else full).bfloat16().double()
 
 
 def draw(kind, batch, rows, cols, dtype, seed=0, size=1e-3):
