@@ -764,6 +764,10 @@ int64_t orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols)
 }
 
 cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream) {
+    if (orthogonalize_is_small(a.rows, a.cols)) {
+        const cudaError_t err = launch_orthogonalize_small(a, stream);
+        if (err != cudaErrorNotSupported) return err;
+    }
     if (!tensor_map_encoder()) return cudaErrorNotSupported;
     const OrthoLayout l = ortho_layout(a.batch, a.rows, a.cols);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);

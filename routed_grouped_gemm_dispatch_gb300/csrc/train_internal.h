@@ -81,6 +81,10 @@ struct Orthogonalize {
 
 constexpr float ORTHO_MAX_SHIFT = 1024.0f;         // |b / 2c|, where c is not 0
 int64_t orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols);
+// Matrices of at most 128 rows or columns, by a cluster each; cudaErrorNotSupported where the device
+// cannot place one.
+bool orthogonalize_is_small(int32_t rows, int32_t cols);
+cudaError_t launch_orthogonalize_small(const Orthogonalize& a, cudaStream_t stream);
 cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream);
 
 }  // namespace moe

@@ -33,6 +33,13 @@ def iterate(g, steps=5, abc=ABC, eps=1e-7, rounded=False):
             A = x @ x.transpose(1, 2)
             x = a * x + (b * A + c * (A @ A)) @ x
         return x.transpose(1, 2) if tall else x
+    if x.shape[1] <= 128 and x.shape[2] <= 6144:
+        # on chip: a·X in 32 bits, but for the last step, which takes X as the products do
+        for k in range(steps):
+            hi = r16(x, 64.0)
+            A = r16(hi @ hi.transpose(1, 2), 1024.0)
+            x = a * (hi if k + 1 == steps else x) + r16(b * A + c * (A @ A), 64.0) @ hi
+        return (x.transpose(1, 2) if tall else x).bfloat16().double()
     eye = torch.eye(x.shape[1], dtype=x.dtype, device=x.device)
     hi, lo = x, torch.zeros_like(x)
     if g.dtype == torch.float32:               # 16-bit inputs are exact
@@ -87,7 +94,8 @@ def check(update, got, **kw):
 
 # sizes around the tiles' (128, 256), of whole and broken 16-byte rows, wide, square and tall
 SIZES = [(1, 64, 96), (1, 64, 2048), (2, 128, 128), (1, 129, 130), (3, 333, 1001), (1, 256, 256), (2, 257, 300), (1, 500, 200),
-         (1, 1001, 77), (2, 520, 264), (5, 96, 640), (1, 600, 1544), (1, 1408, 768)]
+         (1, 1001, 77), (2, 520, 264), (5, 96, 640), (1, 600, 1544), (1, 1408, 768), (1, 100, 6144), (2, 6100, 128), (1, 90, 6150), (40, 65, 129),
+         (200, 16, 40), (20, 128, 520)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
@@ -101,7 +109,7 @@ def test_sizes(batch, rows, cols, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("kind", ["low rank", "rank one", "rows of zeros"])
-@pytest.mark.parametrize("rows,cols", [(200, 520), (700, 300), (256, 1024)])
+@pytest.mark.parametrize("rows,cols", [(200, 520), (700, 300), (256, 1024), (64, 300), (2048, 100)])
 def test_spectra(kind, rows, cols, dtype):
     u = draw(kind, 2, rows, cols, dtype)
     check(u, moe.orthogonalize(u))
