@@ -63,7 +63,6 @@ constexpr float B_SCALE = 64.0f;
 constexpr float LO_SCALE = 8192.0f;         // lo = (x - hi)·2^13
 constexpr float MAX_A_SCALE = 1024.0f;      // of A, less where s is large
 constexpr int SUM_THREADS = 256;
-constexpr int MAX_SUM_BLOCKS = 512;         // of one matrix
 
 // ---------------------------------------------------------------------------
 // norms, and X₀
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(SUM_THREADS) square_sum_kernel(const Prepare p
     const int64_t step = static_cast<int64_t>(gridDim.x) * SUM_THREADS;
     float sum = 0.0f;
     if (VEC) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t i = first; i < p.elements / PER; i += step) {
             float v[PER];
             values_of<DTYPE>(__ldg(reinterpret_cast<const uint4*>(base) + i), v);
@@ -155,68 +154,158 @@ __global__ void __launch_bounds__(SUM_THREADS) square_sum_kernel(const Prepare p
     }
 }
 
-// X₀ up to the factor `rest`, in tiles of 64 rows x 64 columns of X.
-template <int DTYPE, bool TALL>
-__global__ void __launch_bounds__(256) prepare_kernel(const Prepare p) {
-    __shared__ float tile[64][65];
-    __shared__ float part[8];
-    __shared__ float power;
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
-    const int64_t matrix = blockIdx.z;
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        for (int i = threadIdx.x; i < p.counters; i += 256) p.ready[matrix * p.counters + i] = 0;
-        if (matrix == 0 && threadIdx.x == 0) *p.queue = 0;
-    }
+// What the norm makes of the values of a matrix: times `power`, a power of two, they are X₀·2^6 / `rest`.
+struct Norm {
+    float power, rest;
+};
+__device__ __forceinline__ Norm norm_of(const Prepare& p, int64_t matrix, float* part) {
     float sum = 0.0f;
-    for (int i = threadIdx.x; i < p.sum_blocks; i += 256) sum += p.sums[matrix * p.sum_blocks + i];
+    for (int i = threadIdx.x; i < p.sum_blocks; i += SUM_THREADS) sum += __ldg(p.sums + matrix * p.sum_blocks + i);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) sum += part[w];
-        float norm = sqrtf(sum);
-        if (norm < p.eps) norm = p.eps;                       // a NaN stays
-        float two_e = 0.0f, rest = 0.0f;
-        if (norm != 0.0f) {
-            int e = 0;
-            rest = __int_as_float(0x7fffffff);                // infinite (or NaN): so is the result, NaN
-            if (norm <= 3.4e38f) rest = 1.0f / frexpf(norm, &e);   // norm = f·2^e, f in [0.5, 1)
-            two_e = ldexpf(1.0f, X_EXPONENT - e);
-        }
-        power = two_e;
-        if (blockIdx.x == 0 && blockIdx.y == 0) p.rest[matrix] = rest;
+    sum = 0.0f;
+    for (int w = 0; w < SUM_THREADS / 32; ++w) sum += part[w];
+    float norm = sqrtf(sum);
+    if (norm < p.eps) norm = p.eps;                           // a NaN stays
+    Norm n{0.0f, 0.0f};
+    if (norm != 0.0f) {
+        int e = 0;
+        n.rest = __int_as_float(0x7fffffff);                  // infinite (or NaN): so is the result, NaN
+        if (norm <= 3.4e38f) n.rest = 1.0f / frexpf(norm, &e);    // norm = f·2^e, f in [0.5, 1)
+        n.power = ldexpf(1.0f, X_EXPONENT - e);
     }
-    const int32_t m0 = static_cast<int32_t>(blockIdx.y) * 64, n0 = static_cast<int32_t>(blockIdx.x) * 64;
-    const int32_t rows = TALL ? p.N : p.M, cols = TALL ? p.M : p.N;
-    const int32_t r0 = TALL ? n0 : m0, c0 = TALL ? m0 : n0;
-    constexpr int BYTES = DTYPE == MOE_DTYPE_F32 ? 4 : 2;
-    const uint8_t* base = static_cast<const uint8_t*>(p.update) + matrix * p.elements * BYTES;
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        float v = 0.0f;
-        if (r0 + r < rows && c0 + c < cols) v = value_at<DTYPE>(base, static_cast<int64_t>(r0 + r) * cols + c0 + c);
-        if (TALL) tile[c][r] = v;
-        else tile[r][c] = v;
+    return n;
+}
+
+// Eight values of X₀, as hi and (where it is kept) lo.
+__device__ __forceinline__ void store_x0(const Prepare& p, int64_t row, int32_t col, const float (&v)[8], float power) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float x = v[2 * j] * power, y = v[2 * j + 1] * power;
+        h[j] = pack_16bit2<false>(x, y);
+        const float2 back = unpack_16bit2<false>(h[j]);
+        l[j] = pack_lo2(x - back.x, y - back.y);
     }
-    __syncthreads();
-    const float s = power;
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        if (m0 + r >= p.M || n0 + c >= p.ld) continue;
-        uint32_t h[4], l[4];
+    *reinterpret_cast<uint4*>(p.hi + row * p.ld + col) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (p.lo) *reinterpret_cast<uint2*>(p.lo + row * p.ld_lo + col) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// Eight values from element i on, `n` of them there (the others zero).
+template <int DTYPE, bool VEC>
+__device__ __forceinline__ void load_eight(float (&v)[8], const void* base, int64_t i, int32_t n) {
+    if constexpr (VEC && DTYPE == MOE_DTYPE_F32) {
+        float a[4], b[4];
+        values_of<DTYPE>(__ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i)), a);
+        values_of<DTYPE>(__ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i + 4)), b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float x = tile[r][c + 2 * j] * s, y = tile[r][c + 2 * j + 1] * s;
-            h[j] = pack_16bit2<false>(x, y);
-            const float2 back = unpack_16bit2<false>(h[j]);
-            l[j] = pack_lo2(x - back.x, y - back.y);
+            v[j] = a[j];
+            v[4 + j] = b[j];
         }
-        const int64_t at = matrix * p.M + m0 + r;
-        *reinterpret_cast<uint4*>(p.hi + at * p.ld + n0 + c) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (p.lo)
-            *reinterpret_cast<uint2*>(p.lo + at * p.ld_lo + n0 + c) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    } else if constexpr (VEC) {
+        values_of<DTYPE>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i)), v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? value_at<DTYPE>(base, i + j) : 0.0f;
+    }
+}
+
+// X₀ up to the factor `rest`.  Grid: blocks x matrices.  VEC: the update's rows are whole 8 values.
+template <int DTYPE, bool VEC>
+__global__ void __launch_bounds__(SUM_THREADS) prepare_kernel(const Prepare p) {
+    __shared__ float part[SUM_THREADS / 32];
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const int64_t matrix = blockIdx.y;
+    const Norm n = norm_of(p, matrix, part);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < p.counters; i += SUM_THREADS) p.ready[matrix * p.counters + i] = 0;
+        if (threadIdx.x == 0) {
+            p.rest[matrix] = n.rest;
+            if (matrix == 0) *p.queue = 0;
+        }
+    }
+    constexpr int BYTES = DTYPE == MOE_DTYPE_F32 ? 4 : 2;
+    const uint8_t* base = static_cast<const uint8_t*>(p.update) + matrix * p.elements * BYTES;
+    const int32_t pieces = p.ld / 8;
+    const int64_t all = static_cast<int64_t>(p.M) * pieces, step = static_cast<int64_t>(gridDim.x) * SUM_THREADS;
+    // four pieces' loads ahead of their stores
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * SUM_THREADS + threadIdx.x; i0 < all; i0 += 4 * step) {
+        float v[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * step;
+            if (i >= all) break;
+            const int64_t row = VEC && p.lo == nullptr ? 0 : i / pieces;
+            const int32_t col = static_cast<int32_t>(i - row * pieces) * 8;
+            if (VEC) load_eight<DTYPE, true>(v[u], base, i * 8, 8);
+            else load_eight<DTYPE, false>(v[u], base, row * p.N + col, p.N - col);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * step;
+            if (i >= all) break;
+            if (VEC && p.lo == nullptr) {
+                // rows one after the other, as in the update
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = pack_16bit2<false>(v[u][2 * j] * n.power, v[u][2 * j + 1] * n.power);
+                reinterpret_cast<uint4*>(p.hi)[matrix * all + i] = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                const int64_t row = i / pieces;
+                store_x0(p, matrix * p.M + row, static_cast<int32_t>(i - row * pieces) * 8, v[u], n.power);
+            }
+        }
+    }
+}
+
+// The same from a tall update [N, M], in tiles of 64 rows x 64 columns of X.
+template <int DTYPE, bool VEC>
+__global__ void __launch_bounds__(SUM_THREADS) prepare_tall_kernel(const Prepare p) {
+    __shared__ float tile[64][65];
+    __shared__ float part[SUM_THREADS / 32];
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const int64_t matrix = blockIdx.y;
+    const Norm n = norm_of(p, matrix, part);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < p.counters; i += SUM_THREADS) p.ready[matrix * p.counters + i] = 0;
+        if (threadIdx.x == 0) {
+            p.rest[matrix] = n.rest;
+            if (matrix == 0) *p.queue = 0;
+        }
+    }
+    constexpr int BYTES = DTYPE == MOE_DTYPE_F32 ? 4 : 2;
+    const uint8_t* base = static_cast<const uint8_t*>(p.update) + matrix * p.elements * BYTES;
+    const int32_t tiles_m = (p.M + 63) / 64, tiles = tiles_m * ((p.ld + 63) / 64);
+    for (int32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int32_t n0 = t / tiles_m * 64, m0 = t % tiles_m * 64;
+        float v[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (threadIdx.x >> 3) + 32 * u, c = (threadIdx.x & 7) * 8;
+            const int32_t left = n0 + r < p.N ? p.M - m0 - c : 0;
+            if (VEC && left >= 8) load_eight<DTYPE, true>(v[u], base, static_cast<int64_t>(n0 + r) * p.M + m0 + c, 8);
+            else load_eight<DTYPE, false>(v[u], base, static_cast<int64_t>(n0 + r) * p.M + m0 + c, left);
+        }
+        __syncthreads();                          // the tile before is out
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) tile[(threadIdx.x & 7) * 8 + j][(threadIdx.x >> 3) + 32 * u] = v[u][j];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (threadIdx.x >> 3) + 32 * u, c = (threadIdx.x & 7) * 8;
+            if (m0 + r >= p.M || n0 + c >= p.ld) continue;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = tile[r][c + j];
+            store_x0(p, matrix * p.M + m0 + r, n0 + c, x, n.power);
+        }
     }
 }
 
@@ -669,8 +758,11 @@ OrthoLayout ortho_layout(int64_t batch, int32_t rows, int32_t cols) {
     l.ld_x = (l.N + 7) / 8 * 8;
     l.ld_a = (l.M + 7) / 8 * 8;
     l.ld_lo = (l.N + 15) / 16 * 16;
-    const int64_t blocks = (static_cast<int64_t>(rows) * cols + SUM_THREADS * 64 - 1) / (SUM_THREADS * 64);
-    l.sum_blocks = static_cast<int32_t>(blocks > MAX_SUM_BLOCKS ? MAX_SUM_BLOCKS : blocks);
+    // about eight blocks an SM over the stack, of at least 16 values a thread
+    int64_t blocks = (static_cast<int64_t>(rows) * cols + SUM_THREADS * 16 - 1) / (SUM_THREADS * 16);
+    const int64_t most = batch > 0 ? (8 * 152 + batch - 1) / batch : 1;
+    if (blocks > most) blocks = most;
+    l.sum_blocks = static_cast<int32_t>(blocks);
     int64_t at = 0;
     auto take = [&at](int64_t n) {
         const int64_t r = at;
@@ -716,10 +808,13 @@ cudaError_t launch_prepare(const Prepare& p, int64_t batch, bool tall, cudaStrea
                           ? launch_pdl(square_sum_kernel<DTYPE, true>, sum_grid, SUM_THREADS, stream, p)
                           : launch_pdl(square_sum_kernel<DTYPE, false>, sum_grid, SUM_THREADS, stream, p);
     if (err != cudaSuccess) return err;
-    const dim3 grid(static_cast<unsigned>((p.ld + 63) / 64), static_cast<unsigned>((p.M + 63) / 64),
-                    static_cast<unsigned>(batch));
-    return tall ? launch_pdl(prepare_kernel<DTYPE, true>, grid, 256, stream, p)
-                : launch_pdl(prepare_kernel<DTYPE, false>, grid, 256, stream, p);
+    // as many blocks as for the sums: about eight an SM over the stack
+    const bool rows8 = (tall ? p.M : p.N) % 8 == 0;
+    if (tall)
+        return rows8 ? launch_pdl(prepare_tall_kernel<DTYPE, true>, sum_grid, SUM_THREADS, stream, p)
+                     : launch_pdl(prepare_tall_kernel<DTYPE, false>, sum_grid, SUM_THREADS, stream, p);
+    return rows8 ? launch_pdl(prepare_kernel<DTYPE, true>, sum_grid, SUM_THREADS, stream, p)
+                 : launch_pdl(prepare_kernel<DTYPE, false>, sum_grid, SUM_THREADS, stream, p);
 }
 
 template <int BN>

@@ -47,7 +47,6 @@ static_assert(1024 + 384 / 64 * 128 * 128 + 2 * 128 * 128 + 128 * 128 * 4 <= SME
 
 constexpr int BOX_BYTES = ROWS * 128;         // 64 columns of 128 rows, 128-byte swizzle
 constexpr int AB_BYTES = 2 * BOX_BYTES;
-constexpr int EXCHANGE_BYTES = ROWS * ROWS * 4;
 constexpr int TMEM_A = 0, TMEM_X = 128, TMEM_COLS = 512;
 
 struct Small {
