@@ -321,7 +321,7 @@ struct OrthoProducts {
     int32_t total_tiles, n_maps;
     int32_t* status;
     int32_t* queue;               // the next tile to take
-    int32_t* ready;               // [batch][3][panels]: warps that have stored their part of a panel
+    int32_t* ready;               // [batch][3][panels]: CTAs that have stored their part of a tile of a panel
     int32_t batch, group;         // matrices; of a group
     int32_t M, N;                 // X [M, N]
     int32_t ld_x, ld_a, ld_lo;    // elements between rows of X's hi; of A and B; of X's lo
@@ -436,8 +436,22 @@ struct OrthoOp {
     struct Place {
         int32_t kind, step, matrix, i, j;          // panel of rows, tile column
     };
+    using Code = int2;                             // a Place
+    static_assert(MOE_ORTHO_MAX_SIZE <= 1 << 16 && MOE_ORTHO_MAX_STEPS <= 64, "a Place in 47 bits");
+    static __device__ __forceinline__ Code code(const Params& p, int32_t t) {
+        const Place at = number(p, t);
+        return make_int2(at.kind | at.step << 2 | at.i << 8 | at.j << 17, at.matrix);
+    }
+    static __device__ __forceinline__ void pack(const Code& c, int32_t& x, int32_t& y) {
+        x = c.x;
+        y = c.y;
+    }
+    static __device__ __forceinline__ Code unpack(int32_t x, int32_t y) { return make_int2(x, y); }
+    static __device__ __forceinline__ Place place(const Code& c) {
+        return Place{c.x & 3, c.x >> 2 & 63, c.y, c.x >> 8 & 511, c.x >> 17 & 1023};
+    }
     // Order: groups of matrices, their steps, the three products of a step, the group's matrices, tiles.
-    static __device__ __forceinline__ Place place(const Params& p, int32_t t) {
+    static __device__ __forceinline__ Place number(const Params& p, int32_t t) {
         Place at;
         const int32_t symmetric = (1 + p.square) * p.tri;
         const int32_t per_matrix = symmetric + p.panels * p.cols_x;
@@ -476,8 +490,8 @@ struct OrthoOp {
         at.matrix = first + m;
         return at;
     }
-    static __device__ __forceinline__ Tile tile(const Params& p, int32_t t) {
-        const Place at = place(p, t);
+    static __device__ __forceinline__ Tile tile(const Params& p, const Code& code) {
+        const Place at = place(code);
         Tile ti{};
         const int32_t x = at.step & 1;
         ti.a_map = at.kind == GRAM ? X_ROWS + x : at.kind == POLY ? A_ROWS : B_ROWS;
@@ -494,15 +508,15 @@ struct OrthoOp {
     static __device__ __forceinline__ int32_t* counter(const Params& p, int32_t matrix, int32_t kind, int32_t panel) {
         return p.ready + (static_cast<int64_t>(matrix) * 3 + kind) * p.panels + panel;
     }
-    // By a whole warp: what tile t reads is complete.
-    static __device__ __forceinline__ bool wait(const Params& p, int32_t t, volatile int* abort) {
-        const Place at = place(p, t);
+    // By a whole warp: returns when what the tile reads is complete (false: not in time).
+    static __device__ __forceinline__ bool wait(const Params& p, const Code& code, volatile int* abort) {
+        const Place at = place(code);
         if (at.kind == GRAM && at.step == 0) return true;
         const int lane = threadIdx.x & 31;
         const int32_t from = at.kind == GRAM ? APPLY : at.kind == POLY || !p.square ? GRAM : POLY;
         const int32_t q = lane == 0 || at.kind == APPLY ? at.i : at.j / (256 / BN);
-        // every one of a tile's 16 warps counts, in every step so far
-        const int32_t need = 16 * (at.kind == GRAM ? at.step * p.cols_x : (at.step + 1) * panel_tiles<BN>(p, q));
+        // both CTAs of every tile count, in every step so far
+        const int32_t need = 2 * (at.kind == GRAM ? at.step * p.cols_x : (at.step + 1) * panel_tiles<BN>(p, q));
         bool ok = true;
         if (lane < 2) {
             const int32_t* c = counter(p, at.matrix, from, q);
@@ -514,8 +528,9 @@ struct OrthoOp {
             if (!reached()) {
                 const uint64_t t0 = global_timer_ns();
                 while (ok && !reached()) {
-                    if (*abort) ok = false;
-                    else if (global_timer_ns() - t0 > pairs::WAIT_LIMIT_NS) {
+                    if (*abort) {
+                        ok = false;
+                    } else if (global_timer_ns() - t0 > pairs::WAIT_LIMIT_NS) {
                         *abort = 1;
                         ok = false;
                     }
@@ -525,6 +540,19 @@ struct OrthoOp {
         ok = __all_sync(0xffffffffu, ok);
         __syncwarp();
         return ok;
+    }
+    // By one thread, which has waited for those that stored: this CTA's part of the tile is there, for TMA
+    // loads and for the other SMs.
+    static __device__ __forceinline__ void publish(const Params& p, const Code& code) {
+        const Place at = place(code);
+        if (at.kind == APPLY && at.step + 1 == p.steps) return;
+        auto add_one = [&](int32_t panel) {
+            asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter(p, at.matrix, at.kind, panel)) : "memory");
+        };
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        add_one(at.i);
+        const int32_t across = at.j / (256 / BN);
+        if (at.kind != APPLY && across != at.i) add_one(across);
     }
 
     struct Finish {
@@ -550,8 +578,8 @@ struct OrthoOp {
             if (with_lo && rows > 0 && cols > 0)
                 load_bytes_64(lo, p.lo[at.step & 1] + element(c, p.ld_lo), p.ld_lo, lane, rows, cols);
         }
-        __device__ __forceinline__ bool before(int32_t t) {
-            at = place(p, t);
+        __device__ __forceinline__ bool before(const Code& code) {
+            at = place(code);
             col0 = at.j * BN;
             r0 = at.i * 256 + row;
             rows = p.M - r0;
@@ -686,21 +714,6 @@ struct OrthoOp {
             if (store_lo)
                 store_bytes_64(lo, staging, p.lo[(at.step + 1) & 1] + element(c, p.ld_lo), p.ld_lo, lane, rows,
                                p.ld_lo - col0 - c * 64);
-        }
-        // This warp's part of the tile is stored: for TMA loads and for the other SMs.
-        __device__ __forceinline__ void done() {
-            if (at.kind == APPLY && last) return;
-            asm volatile("fence.proxy.async;" ::: "memory");
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) {
-                auto add_one = [&](int32_t panel) {
-                    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter(p, at.matrix, at.kind, panel)) : "memory");
-                };
-                add_one(at.i);
-                const int32_t across = at.j / (256 / BN);
-                if (at.kind != APPLY && across != at.i) add_one(across);
-            }
         }
         // 64 columns of the warp's rows of the result [M, N], or [N, M] where it is tall.
         __device__ __forceinline__ void store_result(const uint4 (&el)[8], int c) {

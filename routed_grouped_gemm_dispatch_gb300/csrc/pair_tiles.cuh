@@ -17,16 +17,20 @@
 //     BN, BF16, MASKABLE       tile columns, operand type, see below
 //     QUEUE                    see below
 //     Params                   with int32_t total_tiles, n_maps, *status
-//     tile(p, t)               what tile t multiplies (nothing where it has no steps)
-//     Finish(p, smem, ...)     per epilogue warp: before(t) ahead of the sums (false where
-//                              there are none), pass(c, taddr) for 64 columns of its 32 rows;
-//                              with QUEUE done(), which publishes what the warp stored
+//     Code, code(p, t)         what all roles need to know of tile t: four or eight bytes
+//     tile(p, code)            what it multiplies (nothing where it has no steps)
+//     Finish(p, smem, ...)     per epilogue warp: before(code) ahead of the sums (false where
+//                              there are none), pass(c, taddr) for 64 columns of its 32 rows
+//
 // QUEUE: pairs take tiles from a counter in memory (Params::queue, zero at the start) in the order of
 // their numbers instead of every n-th one, and a tile may need results of lower ones:
-// Op::wait(p, t, abort) returns once they are there.  Whoever holds the lowest unfinished
-// tile never waits for one that no running pair holds, so this needs no pair to be
-// resident beside another.  The even CTA's warp 0 takes a tile and hands its number to all
-// roles of both CTAs through a ring of QUEUE entries.
+// Op::wait(p, code, abort) returns once they are there, Op::publish(p, code) says that this CTA's part
+// of a tile is.  Whoever holds the lowest unfinished tile never waits for one that no running
+// pair holds, so this needs no pair to be resident beside another.  The even CTA's warp 11 takes a
+// tile as soon as the one before is being copied, waits for what it reads, and hands its code to all
+// roles of both CTAs through a ring: all that costs some 3 us, which nobody waits for while there is
+// work.  Publishing waits for stores to arrive, which takes microseconds too where all SMs
+// store: warp 10 of either CTA does it.
 //
 // MASKABLE: where Op::dirty(p) says so, rows of an M/N-major B (rows of K) whose bit
 // Op::valid64 gives as 0 are set to zero in shared memory before they are multiplied, so
@@ -53,9 +57,10 @@ namespace pairs {
 constexpr int BM = 128;                        // rows of A per CTA
 constexpr int BK = 64;                         // K per stage
 constexpr int THREADS = 320;                   // producer, MMA and eight epilogue warps
+constexpr int THREADS_QUEUE = 384;             // with a queue: and one that publishes, one that takes tiles
 constexpr int EPI_WARPS = 8;
 constexpr int MAX_MAPS = 10;
-constexpr int QUEUE = 4;                       // tiles that the roles of a pair may be apart
+constexpr int QUEUE = 8;                       // tiles that the roles of a pair may be apart
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int BOX_BYTES = BK * 128;            // an M/N-major box: 64 along M/N x BK rows of K
 constexpr int STAGING_BYTES = 32 * 128;        // per epilogue warp
@@ -82,11 +87,11 @@ struct Layout {
     static constexpr int STAGES = 196608 / STAGE_BYTES;
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * STAGING_BYTES;
-    static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1 + 2 * QUEUE;   // full, empty, peer, tfull, tempty, drain, queue
-    static constexpr int OFF_TMEM_SLOT = OFF_BARS + NUM_BARS * 8;
+    static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1 + 3 * QUEUE + 1;   // full, empty, peer, tfull, tempty, drain, queue, stored, taken
+    static constexpr int OFF_QUEUE = OFF_BARS + NUM_BARS * 8;
+    static constexpr int OFF_TMEM_SLOT = OFF_QUEUE + 8 * QUEUE;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
-    static constexpr int OFF_QUEUE = OFF_ABORT + 4;
-    static constexpr int SMEM_BYTES = 1024 + OFF_QUEUE + 4 * QUEUE;
+    static constexpr int SMEM_BYTES = 1024 + OFF_ABORT + 4;
     static constexpr int TMEM_COLS = 2 * BN;
     static_assert(SMEM_BYTES <= 227 * 1024, "the ring fits");
 };
@@ -103,7 +108,7 @@ __device__ __forceinline__ void tma_load_3d_pair_if(uint32_t issue, uint32_t dst
 }
 
 template <class Op>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Op::QUEUE ? THREADS_QUEUE : THREADS, 1)
 pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename Op::Params p) {
     constexpr int BN = Op::BN;
     using L = Layout<BN>;
@@ -120,7 +125,11 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     const uint32_t bar_drain = bar_tempty + 16;                  // [1]
     const uint32_t bar_qfull = bar_drain + 8;                    // [QUEUE]
     const uint32_t bar_qempty = bar_qfull + 8 * QUEUE;           // [QUEUE] (used in the even CTA)
-    volatile int32_t* queue = reinterpret_cast<volatile int32_t*>(smem + L::OFF_QUEUE);
+    const uint32_t bar_stored = bar_qempty + 8 * QUEUE;          // [QUEUE] a tile's rows are stored by this CTA's warps
+    const uint32_t bar_taken = bar_stored + 8 * QUEUE;           // [1] (used in the even CTA) a tile is being copied
+    using Code = typename Op::Code;
+    static_assert(sizeof(Code) <= 8, "an entry of the queue");
+    volatile int2* queue = reinterpret_cast<volatile int2*>(smem + L::OFF_QUEUE);      // x: end of the list, y and x: a code
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_TMEM_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ABORT);
 
@@ -143,8 +152,10 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         mbar_init(bar_drain, 1);
         for (int q = 0; q < QUEUE; ++q) {
             mbar_init(bar_qfull + 8 * q, 1);
-            mbar_init(bar_qempty + 8 * q, 2 * EPI_WARPS + 2);    // every role but the one that fills it
+            mbar_init(bar_qempty + 8 * q, 2 * EPI_WARPS + 5);    // producers, MMA issuer, epilogues, publishers
+            mbar_init(bar_stored + 8 * q, EPI_WARPS);
         }
+        mbar_init(bar_taken, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -169,41 +180,30 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
     const uint32_t issue = elect_one();
     int64_t issued = 0;            // stages that warp 0 has filled
 
-    // The next tile of this warp's role; past the last one at the end.
+    // The next tile of this warp's role: its code, or false past the last one.
     uint32_t qslot = 0, qphase = 0;
-    int32_t t_next = pair;
+    int32_t t_static = pair;
     const uint32_t leader_qempty = mapa_shared(bar_qempty, 0);
-    auto next_tile = [&]() -> int32_t {
+    auto next_slot = [&]() {
+        if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
+    };
+    auto free_slot = [&]() {
+        if (lane == 0) mbar_arrive_cluster(leader_qempty + 8 * qslot);
+        next_slot();
+    };
+    auto next_tile = [&](Code& code, bool keep_slot = false) -> bool {
         if constexpr (!Op::QUEUE) {
-            const int32_t t = t_next;
-            t_next += n_pairs;
-            return t;
+            const int32_t t = t_static;
+            t_static += n_pairs;
+            code = Op::code(p, t);
+            return t < p.total_tiles;
         } else {
             const bool there = mbar_wait_bounded<true>(bar_qfull + 8 * qslot, qphase, abort_flag, WAIT_LIMIT_NS);
-            if (!__all_sync(0xffffffffu, there)) return p.total_tiles;
-            const int32_t t = __shfl_sync(0xffffffffu, queue[qslot], 0);
-            if (lane == 0) mbar_arrive_cluster(leader_qempty + 8 * qslot);
-            if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
-            return t;
-        }
-    };
-    // The same for the role that fills the queue; it asks for the tile after it meanwhile.
-    auto take_tile = [&]() -> int32_t {
-        if constexpr (!Op::QUEUE) {
-            return next_tile();
-        } else {
-            const int32_t t = __shfl_sync(0xffffffffu, t_next, 0);
-            if (!mbar_wait_warp(bar_qempty + 8 * qslot, qphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) return p.total_tiles;
-            if (lane == 0) {
-                queue[qslot] = t;
-                const uint32_t peer = mapa_shared(smem_u32(const_cast<int32_t*>(&queue[qslot])), 1);
-                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer), "r"(t) : "memory");
-                mbar_arrive(bar_qfull + 8 * qslot);
-                mbar_arrive_cluster(mapa_shared(bar_qfull + 8 * qslot, 1));
-                if (t < p.total_tiles) t_next = atomicAdd(p.queue, 1);
-            }
-            if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
-            return t;
+            if (!__all_sync(0xffffffffu, there)) return false;
+            const int32_t x = __shfl_sync(0xffffffffu, queue[qslot].x, 0), y = __shfl_sync(0xffffffffu, queue[qslot].y, 0);
+            if (!keep_slot) free_slot();
+            code = Op::unpack(x, y);
+            return x >= 0;
         }
     };
 
@@ -215,20 +215,15 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t bytes = (masked ? 1 : 2) * L::STAGE_BYTES;
         uint32_t stage = 0, phase = 0;
         bool ok = true;
-        if constexpr (Op::QUEUE) {
-            if (leader && lane == 0) t_next = atomicAdd(p.queue, 1);
-            __syncwarp();
-        }
-        while (ok) {
-            const int32_t t = leader ? take_tile() : next_tile();
-            if (t >= p.total_tiles) break;
-            const Tile ti = Op::tile(p, t);
-            if (ti.steps == 0) continue;
+        Code code;
+        while (ok && next_tile(code)) {
+            const Tile ti = Op::tile(p, code);
             if constexpr (Op::QUEUE) {
-                if (!Op::wait(p, t, abort_flag)) break;
+                if (leader && lane == 0) mbar_arrive(bar_taken);
                 // what generic stores wrote is read by TMA from here on
-                asm volatile("fence.proxy.async;" ::: "memory");
+                asm volatile("fence.proxy.async.global;" ::: "memory");
             }
+            if (ti.steps == 0) continue;
             const int32_t arow = ti.a_row + static_cast<int32_t>(rank) * BM;
             const int32_t brow = ti.b_row + static_cast<int32_t>(rank) * (BN / 2);
             const CUtensorMap* am = &maps.m[ti.a_map];
@@ -269,10 +264,9 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t leader_peer = mapa_shared(bar_peer, 0);
         uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
         bool ok = true;
-        while (ok && (leader || masked)) {
-            const int32_t t = next_tile();
-            if (t >= p.total_tiles) break;
-            const Tile ti = Op::tile(p, t);
+        Code code;
+        while (ok && (leader || masked) && next_tile(code)) {
+            const Tile ti = Op::tile(p, code);
             if (ti.steps == 0) continue;
             if (leader) {
                 if (!mbar_wait_warp(bar_tempty + 8 * acc, aphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
@@ -346,7 +340,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             mbar_wait_bounded(bar_drain, 0, &never, DRAIN_LIMIT_NS);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 2 + EPI_WARPS) {
         // ---- epilogue: a warp has 32 of the CTA's rows, and every other 64 columns
         const int quarter = warp & 3;
         const int odd = warp >= 6 ? 1 : 0;
@@ -354,13 +348,11 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint32_t leader_tempty = mapa_shared(bar_tempty, 0);
         typename Op::Finish fin(p, staging, static_cast<int32_t>(rank) * BM + quarter * 32, odd, lane);
         uint32_t acc = 0, aphase = 0;
+        Code code;
         while (true) {
-            const int32_t t = next_tile();
-            if (t >= p.total_tiles) break;
-            if constexpr (Op::QUEUE) {
-                if (!Op::wait(p, t, abort_flag)) break;
-            }
-            if (!fin.before(t)) continue;
+            const uint32_t slot = qslot;
+            if (!next_tile(code)) break;
+            if (!fin.before(code)) continue;
             // one answer for the whole warp, whose TMEM loads are collective
             if (!mbar_wait_warp(bar_tfull + 8 * acc, aphase, abort_flag, WAIT_LIMIT_NS)) break;
             tc_fence_after_sync();
@@ -374,9 +366,51 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 if (leader) mbar_arrive(bar_tempty + 8 * acc);
                 else mbar_arrive_cluster_relaxed(leader_tempty + 8 * acc);
             }
-            if constexpr (Op::QUEUE) fin.done();
+            if constexpr (Op::QUEUE) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_stored + 8 * slot);
+            }
             acc ^= 1u;
             if (acc == 0) aphase ^= 1u;
+        }
+    } else if constexpr (Op::QUEUE) {
+        if (warp == 2 + EPI_WARPS) {
+            // ---- publisher
+            Code code;
+            while (next_tile(code, true)) {
+                // (a slot's next tile may come only when this phase of its barrier has been seen)
+                if (!mbar_wait_warp(bar_stored + 8 * qslot, qphase, abort_flag, WAIT_LIMIT_NS)) break;
+                free_slot();
+                if (lane == 0) Op::publish(p, code);
+                __syncwarp();
+            }
+        } else if (leader) {
+            // ---- takes tiles, in whole-warp steps; lane 0 holds the number
+            uint32_t tphase = 0;
+            while (true) {
+                int32_t t = lane == 0 ? atomicAdd(p.queue, 1) : 0;
+                t = __shfl_sync(0xffffffffu, t, 0);
+                const bool end = t >= p.total_tiles;
+                Code code = Op::code(p, end ? 0 : t);
+                if (!end && !Op::wait(p, code, abort_flag)) break;
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                if (!mbar_wait_warp(bar_qempty + 8 * qslot, qphase ^ 1u, abort_flag, WAIT_LIMIT_NS)) break;
+                if (lane < 2) {
+                    // lane 0 for this CTA, lane 1 for the other
+                    int32_t x, y;
+                    Op::pack(code, x, y);
+                    if (end) x = -1;
+                    const uint32_t at = mapa_shared(sbase + L::OFF_QUEUE + 8 * qslot, static_cast<uint32_t>(lane));
+                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+                    mbar_arrive_cluster(mapa_shared(bar_qfull + 8 * qslot, static_cast<uint32_t>(lane)));
+                }
+                __syncwarp();
+                next_slot();
+                if (end) break;
+                // the next one when this one is being copied, not before: another pair may be free
+                if (!mbar_wait_warp(bar_taken, tphase, abort_flag, WAIT_LIMIT_NS)) break;
+                tphase ^= 1u;
+            }
         }
     }
     __syncwarp();
@@ -424,7 +458,7 @@ int resident_pairs() {
         attr[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(128);
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(Op::QUEUE ? THREADS_QUEUE : THREADS);
         cfg.dynamicSmemBytes = SMEM;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -448,7 +482,7 @@ cudaError_t launch(const Maps& maps, const typename Op::Params& p, cudaStream_t 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Op::QUEUE ? THREADS_QUEUE : THREADS);
     cfg.dynamicSmemBytes = Layout<Op::BN>::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;

@@ -76,6 +76,8 @@ struct GradOp {
     static constexpr bool MASKABLE = true;
     static constexpr bool QUEUE = false;
     using Params = GradProducts;
+    using Code = int32_t;            // a tile's number
+    static __device__ __forceinline__ Code code(const Params&, int32_t t) { return t; }
     enum { DZ, W_T, DZ_T, X_T, MAPS };
 
     // tiles: first the parts of d_W, part by part over the pieces, then d_x row by row
