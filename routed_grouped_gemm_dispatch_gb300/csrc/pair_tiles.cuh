@@ -188,7 +188,8 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         if (++qslot == QUEUE) { qslot = 0; qphase ^= 1u; }
     };
     auto free_slot = [&]() {
-        if (lane == 0) mbar_arrive_cluster(leader_qempty + 8 * qslot);
+        // (relaxed: the entry is in registers, and a release would wait for this thread's stores in flight)
+        if (lane == 0) mbar_arrive_cluster_relaxed(leader_qempty + 8 * qslot);
         next_slot();
     };
     auto next_tile = [&](Code& code, bool keep_slot = false) -> bool {
