@@ -326,7 +326,8 @@ struct OrthoProducts {
     int32_t M, N;                 // X [M, N]
     int32_t ld_x, ld_a, ld_lo;    // elements between rows of X's hi; of A and B; of X's lo
     int32_t panels;               // of 256 rows
-    int32_t cols_a, cols_x;       // tile columns of A and B, of X
+    int32_t width_a, width_x;     // columns of a tile of A and B, of X
+    int32_t cols_a, cols_x;       // tile columns
     int32_t tri;                  // tiles of A (or B)
     int32_t steps;
     float a, b, c;
@@ -343,16 +344,17 @@ struct OrthoProducts {
     int32_t tall;                 // out is transposed
 };
 
-// Columns of 256-row panel q that lie on or below the diagonal, in tiles of BN.
-template <int BN>
+// Tiles of A (or B) in 256-row panel q that lie on or below the diagonal.
 __device__ __forceinline__ int32_t row_tiles(const OrthoProducts& p, int32_t q) {
-    const int32_t n = (q + 1) * (256 / BN);
+    const int32_t n = p.width_a == 256 ? q + 1 : 2 * q + 2;
     return n < p.cols_a ? n : p.cols_a;
 }
+// The panel across the diagonal of tile column j.
+__device__ __forceinline__ int32_t panel_of(const OrthoProducts& p, int32_t j) { return p.width_a == 256 ? j : j >> 1; }
 // Tiles that store a part of panel q of A (or B).
-template <int BN>
 __device__ __forceinline__ int32_t panel_tiles(const OrthoProducts& p, int32_t q) {
-    return row_tiles<BN>(p, q) + (p.panels - 1 - q) * (256 / BN);
+    const int32_t below = p.panels - 1 - q;
+    return row_tiles(p, q) + (p.width_a == 256 ? below : 2 * below);
 }
 
 // The transpose of a warp's 32 rows x 64 columns (el: a row per lane), through its 4 KB of staging:
@@ -470,13 +472,13 @@ struct OrthoOp {
             l = r - m * p.tri;
             if (at.kind == GRAM) {
                 at.i = 0;
-                for (int32_t w; l >= (w = row_tiles<BN>(p, at.i)); ++at.i) l -= w;
+                for (int32_t w; l >= (w = row_tiles(p, at.i)); ++at.i) l -= w;
                 at.j = l;
             } else {
                 // column j starts in the panel that holds the diagonal
                 at.j = 0;
-                for (int32_t h; l >= (h = p.panels - at.j / (256 / BN)); ++at.j) l -= h;
-                at.i = at.j / (256 / BN) + l;
+                for (int32_t h; l >= (h = p.panels - panel_of(p, at.j)); ++at.j) l -= h;
+                at.i = panel_of(p, at.j) + l;
             }
         } else {
             at.kind = APPLY;
@@ -498,7 +500,8 @@ struct OrthoOp {
         ti.b_map = at.kind == GRAM ? X_COLS + x : at.kind == POLY ? A_COLS : X_RIGHT + x;
         ti.b_mn = at.kind == APPLY;                // B·X: rows of X are K
         ti.a_row = at.i * 256;
-        ti.b_row = at.j * BN;
+        ti.width = at.kind == APPLY ? p.width_x : p.width_a;
+        ti.b_row = at.j * ti.width;
         ti.batch = at.matrix;
         ti.steps = ((at.kind == GRAM ? p.ld_x : p.M) + pairs::BK - 1) / pairs::BK;
         return ti;
@@ -514,9 +517,9 @@ struct OrthoOp {
         if (at.kind == GRAM && at.step == 0) return true;
         const int lane = threadIdx.x & 31;
         const int32_t from = at.kind == GRAM ? APPLY : at.kind == POLY || !p.square ? GRAM : POLY;
-        const int32_t q = lane == 0 || at.kind == APPLY ? at.i : at.j / (256 / BN);
+        const int32_t q = lane == 0 || at.kind == APPLY ? at.i : panel_of(p, at.j);
         // both CTAs of every tile count, in every step so far
-        const int32_t need = 2 * (at.kind == GRAM ? at.step * p.cols_x : (at.step + 1) * panel_tiles<BN>(p, q));
+        const int32_t need = 2 * (at.kind == GRAM ? at.step * p.cols_x : (at.step + 1) * panel_tiles(p, q));
         bool ok = true;
         if (lane < 2) {
             const int32_t* c = counter(p, at.matrix, from, q);
@@ -551,7 +554,7 @@ struct OrthoOp {
         };
         asm volatile("fence.proxy.async.global;" ::: "memory");
         add_one(at.i);
-        const int32_t across = at.j / (256 / BN);
+        const int32_t across = panel_of(p, at.j);
         if (at.kind != APPLY && across != at.i) add_one(across);
     }
 
@@ -560,6 +563,7 @@ struct OrthoOp {
         uint8_t* staging;
         int32_t row, odd, lane;
         Place at;
+        int32_t tile_width;
         int32_t col0;                      // the tile's first column
         int32_t r0, rows;                  // the warp's first row, and how many of its 32 exist
         bool first, last, with_lo, store_lo;
@@ -569,6 +573,7 @@ struct OrthoOp {
         __device__ __forceinline__ Finish(const Params& p_, uint8_t* staging_, int32_t row_, int odd_, int lane_)
             : p(p_), staging(staging_), row(row_), odd(odd_), lane(lane_) {}
 
+        __device__ __forceinline__ int width_of() const { return tile_width; }
         __device__ __forceinline__ int32_t width() const { return at.kind == APPLY ? p.ld_x : p.ld_a; }
         __device__ __forceinline__ int64_t element(int c, int32_t ld) const {
             return (static_cast<int64_t>(at.matrix) * p.M + r0) * ld + col0 + c * 64;
@@ -580,7 +585,8 @@ struct OrthoOp {
         }
         __device__ __forceinline__ bool before(const Code& code) {
             at = place(code);
-            col0 = at.j * BN;
+            tile_width = at.kind == APPLY ? p.width_x : p.width_a;
+            col0 = at.j * tile_width;
             r0 = at.i * 256 + row;
             rows = p.M - r0;
             rows = rows > 32 ? 32 : rows;
@@ -658,7 +664,7 @@ struct OrthoOp {
             }
             uint16_t* dst = b_now ? p.B : p.A;
             store_staged_64(el, staging, dst + element(c, p.ld_a), p.ld_a, lane, rows, cols);
-            if ((at.j + 1) * BN <= at.i * 256) {
+            if (col0 + tile_width <= at.i * 256) {
                 // the tile across the diagonal
                 uint4 tr[8];
                 transpose_32x64(el, tr, staging, lane);
@@ -830,8 +836,40 @@ cudaError_t launch_prepare(const Prepare& p, int64_t batch, bool tall, cudaStrea
                  : launch_pdl(prepare_kernel<DTYPE, false>, sum_grid, SUM_THREADS, stream, p);
 }
 
+// How wide the tiles are, by the time that a product should take.  As measured (us): a stage of 64 along
+// K 0.2 for 256 x 128 tiles and 0.326 for 256 x 256 (both at the rate at which operands come from L2),
+// a tile at least 4 and 5.5, its epilogue 2.5 and 6 where no other tile hides it.  One matrix's products
+// wait for one another in whole rounds, a stack's overlap.  16 x 512 x 512 takes 125 us with
+// narrow tiles and 207 with wide ones, 64 x 300 x 1000 415 and 350, 2048 x 7168 456 with narrow ones and
+// 412 where X has wide ones.  Where A and X both want narrow ones they have a kernel of their own with
+// eight stages instead of six.
+struct Widths {
+    int a, x;
+};
+Widths widths(const OrthoLayout& l, int64_t batch, int n_pairs) {
+    auto time = [n_pairs, batch](int64_t tiles, int32_t k, bool wide) {
+        const float mma = static_cast<float>(pairs::ceil_div(k, pairs::BK)) * (wide ? 0.326f : 0.2f);
+        const float least = wide ? 5.5f : 4.0f, epilogue = wide ? 6.0f : 2.5f;
+        float rounds = static_cast<float>(tiles) / static_cast<float>(n_pairs);
+        if (batch == 1 || rounds < 1.0f) rounds = static_cast<float>((tiles + n_pairs - 1) / n_pairs);
+        return rounds * (mma > least ? mma : least) + epilogue;
+    };
+    const int64_t narrow = pairs::ceil_div(l.M, 128);
+    int64_t wide_a = 0, narrow_a = 0;
+    for (int32_t q = 0; q < l.panels; ++q) {
+        wide_a += q + 1;
+        narrow_a += 2 * q + 2 < narrow ? 2 * q + 2 : narrow;
+    }
+    const int64_t wide_x = static_cast<int64_t>(l.panels) * pairs::ceil_div(l.ld_x, 256);
+    const int64_t narrow_x = static_cast<int64_t>(l.panels) * pairs::ceil_div(l.ld_x, 128);
+    const float a_wide = time(batch * wide_a, l.ld_x, true) + time(batch * wide_a, l.M, true);
+    const float a_narrow = time(batch * narrow_a, l.ld_x, false) + time(batch * narrow_a, l.M, false);
+    return Widths{a_narrow < 0.9f * a_wide ? 128 : 256,
+                  time(batch * narrow_x, l.M, false) < time(batch * wide_x, l.M, true) ? 128 : 256};
+}
+
 template <int BN>
-cudaError_t launch_products(const OrthoLayout& l, int64_t batch, OrthoProducts& p, cudaStream_t stream) {
+cudaError_t launch_products(const OrthoLayout& l, int64_t batch, const Widths& w, OrthoProducts& p, cudaStream_t stream) {
     using Op = OrthoOp<BN>;
     pairs::Maps maps;
     // rows with the columns up to their 16-byte boundary, which hold zeros
@@ -839,31 +877,32 @@ cudaError_t launch_products(const OrthoLayout& l, int64_t batch, OrthoProducts& 
         return pairs::map_3d(&maps.m[i], base, batch, l.M, ld, ld, box_rows);
     };
     for (int i = 0; i < 2; ++i)
-        if (!map(X_ROWS + i, p.hi[i], l.ld_x, pairs::BM) || !map(X_COLS + i, p.hi[i], l.ld_x, BN / 2) ||
+        if (!map(X_ROWS + i, p.hi[i], l.ld_x, pairs::BM) || !map(X_COLS + i, p.hi[i], l.ld_x, w.a / 2) ||
             !map(X_RIGHT + i, p.hi[i], l.ld_x, pairs::BK))
             return cudaErrorInvalidValue;
-    if (!map(A_ROWS, p.A, l.ld_a, pairs::BM) || !map(A_COLS, p.A, l.ld_a, BN / 2) || !map(B_ROWS, p.B, l.ld_a, pairs::BM))
+    if (!map(A_ROWS, p.A, l.ld_a, pairs::BM) || !map(A_COLS, p.A, l.ld_a, w.a / 2) || !map(B_ROWS, p.B, l.ld_a, pairs::BM))
         return cudaErrorInvalidValue;
     const int n_pairs = pairs::resident_pairs<Op>();
     if (n_pairs == 0) return cudaErrorNoDevice;
     p.n_maps = MAPS;
     p.panels = l.panels;
-    p.cols_a = pairs::ceil_div(l.M, BN);
-    p.cols_x = pairs::ceil_div(l.ld_x, BN);
+    p.width_a = w.a;
+    p.width_x = w.x;
+    p.cols_a = pairs::ceil_div(l.M, w.a);
+    p.cols_x = pairs::ceil_div(l.ld_x, w.x);
     p.tri = 0;
     for (int32_t q = 0; q < p.panels; ++q) {
-        const int32_t n = (q + 1) * (256 / BN);
+        const int32_t n = (q + 1) * (256 / w.a);
         p.tri += n < p.cols_a ? n : p.cols_a;
     }
-    // twice as many tiles of A as there are pairs
-    const int64_t group = (2 * n_pairs + p.tri - 1) / p.tri;
-    p.group = static_cast<int32_t>(group < batch ? group : batch);
+    // Groups of matrices with about twice as many tiles of A as there are pairs.  (64 x 1408 x 2048 in groups of
+    // 4: 4.5 ms; 8: 3.8; 16: 3.8 to 4.0; 64: 4.1 to 4.2.)
+    const int64_t tiles = batch * p.tri / (2 * n_pairs);
+    const int64_t groups = tiles > 1 ? tiles : 1;
+    p.group = static_cast<int32_t>((batch + groups - 1) / groups);
     p.total_tiles = static_cast<int32_t>(batch) * p.steps * ((1 + p.square) * p.tri + p.panels * p.cols_x);
     return pairs::launch<Op>(maps, p, stream);
 }
-
-// Tiles of A over the stack, 256 columns wide.
-int64_t gram_tiles(const OrthoLayout& l, int64_t batch) { return batch * l.panels * (l.panels + 1) / 2; }
 
 }  // namespace
 
@@ -931,9 +970,11 @@ cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream) {
     p.B = u16(l.B);
     p.out = a.out;
     p.tall = l.tall ? 1 : 0;
-    // Narrower tiles where A has fewer than a round of the wide ones.
-    return gram_tiles(l, a.batch) >= 76 ? launch_products<256>(l, a.batch, p, stream)
-                                        : launch_products<128>(l, a.batch, p, stream);
+    const int n_pairs = pairs::resident_pairs<OrthoOp<256>>();
+    if (n_pairs == 0) return cudaErrorNoDevice;
+    const Widths w = widths(l, a.batch, n_pairs);
+    return w.a == 128 && w.x == 128 ? launch_products<128>(l, a.batch, w, p, stream)
+                                    : launch_products<256>(l, a.batch, w, p, stream);
 }
 
 }  // namespace moe

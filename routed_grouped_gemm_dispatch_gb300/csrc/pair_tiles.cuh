@@ -2,8 +2,8 @@
 // updates: C[m, n] = Σ_k A[m, k]·B[n, k] over a list of tiles that an operation
 // describes, with what becomes of the sums left to the operation too.
 //
-//  * Persistent clusters of two CTAs, one 2-SM MMA tile of M = 256 x N = Op::BN at a
-//    time: each CTA holds 128 rows of A and half of the tile's rows of B per stage
+//  * Persistent clusters of two CTAs, one 2-SM MMA tile of M = 256 x N = 128 or 256 (at most
+//    Op::BN) at a time: each CTA holds 128 rows of A and half of the tile's rows of B per stage
 //    (K = 64).  Warp 0 feeds the ring by TMA, warp 1 of the even CTA issues the MMAs
 //    into one of two TMEM accumulators, warps 2-9 of both CTAs finish the other one
 //    meanwhile.
@@ -14,13 +14,14 @@
 //    runs out ends the launch as in the other products.
 //
 // An operation `Op` has
-//     BN, BF16, MASKABLE       tile columns, operand type, see below
+//     BN, BF16, MASKABLE       most columns of a tile, operand type, see below
 //     QUEUE                    see below
 //     Params                   with int32_t total_tiles, n_maps, *status
 //     Code, code(p, t)         what all roles need to know of tile t: four or eight bytes
 //     tile(p, code)            what it multiplies (nothing where it has no steps)
 //     Finish(p, smem, ...)     per epilogue warp: before(code) ahead of the sums (false where
-//                              there are none), pass(c, taddr) for 64 columns of its 32 rows
+//                              there are none), width_of() its columns, pass(c, taddr)
+//                              for 64 of them, of the warp's 32 rows
 //
 // QUEUE: pairs take tiles from a counter in memory (Params::queue, zero at the start) in the order of
 // their numbers instead of every n-th one, and a tile may need results of lower ones:
@@ -71,20 +72,21 @@ struct Maps {
     CUtensorMap m[MAX_MAPS];
 };
 
-// What a tile multiplies: rows a_row .. + 255 of A by rows b_row .. + BN - 1 of B
+// What a tile multiplies: rows a_row .. + 255 of A by rows b_row .. + width - 1 of B
 // (coordinates in their own arrays), K steps k0 .. k0 + steps of 64.
 struct Tile {
     int32_t a_map, b_map;
     bool a_mn, b_mn;
     int32_t a_row, b_row, batch;
     int32_t k0, steps;
+    int32_t width;                 // 128 or 256 columns
 };
 
 template <int BN>
 struct Layout {
     static constexpr int B_BYTES = BN / 2 * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 196608 / STAGE_BYTES;
+    static constexpr int STAGES = 196608 / STAGE_BYTES;          // (a tile of 128 columns in stages for 256 leaves a quarter free)
     static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
     static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * STAGING_BYTES;
     static constexpr int NUM_BARS = 3 * STAGES + 2 + 2 + 1 + 3 * QUEUE + 1;   // full, empty, peer, tfull, tempty, drain, queue, stored, taken
@@ -213,7 +215,6 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
         const uint64_t policy = l2_policy_evict_normal();
         const uint32_t full0 = mapa_shared(bar_full, masked ? rank : 0u);
         const uint32_t expect = masked || leader ? issue : 0;
-        const uint32_t bytes = (masked ? 1 : 2) * L::STAGE_BYTES;
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         Code code;
@@ -226,7 +227,9 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             }
             if (ti.steps == 0) continue;
             const int32_t arow = ti.a_row + static_cast<int32_t>(rank) * BM;
-            const int32_t brow = ti.b_row + static_cast<int32_t>(rank) * (BN / 2);
+            const int32_t brow = ti.b_row + static_cast<int32_t>(rank) * (ti.width / 2);
+            const uint32_t bytes = static_cast<uint32_t>(masked ? 1 : 2) * (A_BYTES + static_cast<uint32_t>(ti.width) * BK);
+            const bool wide = BN == 256 && ti.width == 256;
             const CUtensorMap* am = &maps.m[ti.a_map];
             const CUtensorMap* bm = &maps.m[ti.b_map];
             MOE_DCHECK(ti.a_map >= 0 && ti.a_map < p.n_maps && ti.b_map >= 0 && ti.b_map < p.n_maps && ti.steps > 0 &&
@@ -250,9 +253,8 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                     tma_load_3d_pair_if(issue, sa, am, fb, k, arow, ti.batch, policy);
                 }
                 if (ti.b_mn) {
-#pragma unroll
-                    for (int b = 0; b < BN / 128; ++b)
-                        tma_load_3d_pair_if(issue, sb + b * BOX_BYTES, bm, fb, brow + b * 64, k, ti.batch, policy);
+                    tma_load_3d_pair_if(issue, sb, bm, fb, brow, k, ti.batch, policy);
+                    if (wide) tma_load_3d_pair_if(issue, sb + BOX_BYTES, bm, fb, brow + 64, k, ti.batch, policy);
                 } else {
                     tma_load_3d_pair_if(issue, sb, bm, fb, k, brow, ti.batch, policy);
                 }
@@ -274,7 +276,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 tc_fence_after_sync();
             }
             const uint32_t d_tmem = tmem_base + acc * BN;
-            const uint32_t idesc = idesc_16bit_f32acc(2 * BM, BN, Op::BF16, ti.a_mn, ti.b_mn);
+            const uint32_t idesc = idesc_16bit_f32acc(2 * BM, static_cast<uint32_t>(ti.width), Op::BF16, ti.a_mn, ti.b_mn);
             uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;         // the stage's 64 valid bits
             if constexpr (Op::MASKABLE) {
                 if (masked && Op::maskable(ti)) Op::valid64(p, ti.k0, w0, w1);
@@ -359,7 +361,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
 #pragma unroll 1
-            for (int c = odd; c < BN / 64; c += 2) fin.pass(c, taddr + c * 64);
+            for (int c = odd; c < fin.width_of() / 64; c += 2) fin.pass(c, taddr + c * 64);
             tc_fence_before_sync();
             // the accumulator may be reused once both CTAs have read their rows
             __syncwarp();

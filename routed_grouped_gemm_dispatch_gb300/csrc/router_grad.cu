@@ -83,6 +83,7 @@ struct GradOp {
     // tiles: first the parts of d_W, part by part over the pieces, then d_x row by row
     static __device__ __forceinline__ Tile tile(const Params& p, int32_t t) {
         Tile ti{};
+        ti.width = TILE;
         const int32_t parts = p.w_pairs * p.w_parts;
         if (t < parts) {
             const Part w = part_of(p, t % p.w_pairs, t / p.w_pairs);
@@ -130,6 +131,7 @@ struct GradOp {
             : p(p_), staging(staging_), row(row_), lane(lane_) {
             inv = __ldg(p.scale + 1);
         }
+        __device__ __forceinline__ int width_of() const { return TILE; }
         __device__ __forceinline__ bool before(int32_t t) {
             const int32_t parts = p.w_pairs * p.w_parts;
             part = t < parts;
