@@ -471,10 +471,12 @@ int resident_pairs() {
     return r.pairs;
 }
 
+// `most` pairs, or as many as fit on the device and have a tile.
 template <class Op>
-cudaError_t launch(const Maps& maps, const typename Op::Params& p, cudaStream_t stream) {
+cudaError_t launch(const Maps& maps, const typename Op::Params& p, cudaStream_t stream, int most = 1 << 20) {
     int pairs = resident_pairs<Op>();
     if (pairs == 0) return cudaErrorNoDevice;
+    if (pairs > most) pairs = most;
     if (pairs > p.total_tiles) pairs = p.total_tiles;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -8,6 +8,8 @@
 //    end, tile after tile, and cut into as many equal pieces as there are pairs.  The sums
 //    of a pair's part of a tile go to fp32 slot pair + tile: from one part to the next
 //    either of them grows, so no two share a slot.  They are added in pair order.
+//  * Half of the pairs do their part of d_W first and half their part of d_x, so that x is read
+//    while d_x is written: 16384 x 256 x 7168 in 92 us otherwise, 45 of them reading at 5.2 TB/s.
 //  * Operands are read as they lie: d_z by token rows for d_x, transposed for d_W.
 //  * Rows of x whose token does not count are multiplied by a d_z of zero.  If one of them holds an
 //    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
@@ -42,6 +44,9 @@ struct GradProducts {
     int32_t w_steps;                 // K steps of one
     int32_t w_pairs;                 // pieces that all of them are cut into
     int32_t w_parts;                 // tiles that a piece touches at most
+    int32_t x_tiles;                 // of d_x
+    int32_t n_pairs;                 // of the launch
+    int32_t x_rounds;                // d_x tiles of a pair
     uint16_t* d_x;
     float* slots;                    // [w_pairs + w_tiles][256][256]
     const float* scale;              // [1]: what undoes the power of two in d_z
@@ -76,17 +81,26 @@ struct GradOp {
     static constexpr bool MASKABLE = true;
     static constexpr bool QUEUE = false;
     using Params = GradProducts;
-    using Code = int32_t;            // a tile's number
-    static __device__ __forceinline__ Code code(const Params&, int32_t t) { return t; }
+    // Pair `pair`'s item: part k of piece `pair` of d_W, or tile k of d_x (neither: k < 0).
+    struct Code {
+        int32_t pair, k;
+    };
+    static __device__ __forceinline__ Code code(const Params& p, int32_t t) {
+        const int32_t pair = t % p.n_pairs;
+        int32_t k = t / p.n_pairs;
+        if (pair & 1) k = k < p.x_rounds ? k + p.w_parts : k - p.x_rounds;       // d_x first
+        if (k < p.w_parts) return Code{pair, pair < p.w_pairs ? k : -1};
+        const int32_t x = (k - p.w_parts) * p.n_pairs + pair;
+        return Code{-1, x < p.x_tiles ? x : -1};
+    }
     enum { DZ, W_T, DZ_T, X_T, MAPS };
 
-    // tiles: first the parts of d_W, part by part over the pieces, then d_x row by row
-    static __device__ __forceinline__ Tile tile(const Params& p, int32_t t) {
+    static __device__ __forceinline__ Tile tile(const Params& p, const Code& c) {
         Tile ti{};
         ti.width = TILE;
-        const int32_t parts = p.w_pairs * p.w_parts;
-        if (t < parts) {
-            const Part w = part_of(p, t % p.w_pairs, t / p.w_pairs);
+        if (c.k < 0) return ti;
+        if (c.pair >= 0) {
+            const Part w = part_of(p, c.pair, c.k);
             const int32_t m = w.tile / p.x_tiles_n;
             ti.a_map = DZ_T;
             ti.b_map = X_T;
@@ -96,12 +110,13 @@ struct GradOp {
             ti.k0 = w.k0;
             ti.steps = w.steps;
         } else {
-            const int32_t m = (t - parts) / p.x_tiles_n;
+            // row by row: concurrent pairs write whole rows of d_x
+            const int32_t m = c.k / p.x_tiles_n;
             ti.a_map = DZ;
             ti.b_map = W_T;
             ti.b_mn = true;
             ti.a_row = m * TILE;
-            ti.b_row = (t - parts - m * p.x_tiles_n) * TILE;
+            ti.b_row = (c.k - m * p.x_tiles_n) * TILE;
             ti.steps = (p.n_experts + pairs::BK - 1) / pairs::BK;
         }
         return ti;
@@ -132,20 +147,19 @@ struct GradOp {
             inv = __ldg(p.scale + 1);
         }
         __device__ __forceinline__ int width_of() const { return TILE; }
-        __device__ __forceinline__ bool before(int32_t t) {
-            const int32_t parts = p.w_pairs * p.w_parts;
-            part = t < parts;
+        __device__ __forceinline__ bool before(const Code& c) {
+            if (c.k < 0) return false;
+            part = c.pair >= 0;
             if (part) {
-                const int32_t piece = t % p.w_pairs;
-                const Part w = part_of(p, piece, t / p.w_pairs);
-                at = (static_cast<int64_t>(piece + w.tile) * TILE + row) * TILE;
+                const Part w = part_of(p, c.pair, c.k);
+                at = (static_cast<int64_t>(c.pair + w.tile) * TILE + row) * TILE;
                 rows = 32;
                 cols = TILE;
-                MOE_DCHECK(w.steps == 0 || (w.tile < p.w_tiles && piece + w.tile < p.w_pairs + p.w_tiles), p.status);
+                MOE_DCHECK(w.steps == 0 || (w.tile < p.w_tiles && c.pair + w.tile < p.w_pairs + p.w_tiles), p.status);
                 return w.steps > 0;
             }
-            const int32_t m = (t - parts) / p.x_tiles_n;
-            const int32_t col = (t - parts - m * p.x_tiles_n) * TILE;
+            const int32_t m = c.k / p.x_tiles_n;
+            const int32_t col = (c.k - m * p.x_tiles_n) * TILE;
             const int64_t first = static_cast<int64_t>(m) * TILE + row;
             const int64_t left = p.n_tokens - first;
             rows = left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left));
@@ -290,14 +304,19 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     p.w_pairs = weight_pieces(T, p.w_tiles, n_pairs);
     const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
     p.w_parts = static_cast<int32_t>((all + p.w_pairs - 1) / p.w_pairs + p.w_steps - 2) / p.w_steps + 1;
-    p.total_tiles = p.w_pairs * p.w_parts + pairs::ceil_div(T, TILE) * p.x_tiles_n;
+    p.x_tiles = pairs::ceil_div(T, TILE) * p.x_tiles_n;
+    // as many pairs as there is work for: a part or a tile each
+    const int32_t items = p.w_pairs + p.x_tiles;
+    p.n_pairs = items < n_pairs ? items : n_pairs;
+    p.x_rounds = (p.x_tiles + p.n_pairs - 1) / p.n_pairs;
+    p.total_tiles = p.n_pairs * (p.w_parts + p.x_rounds);
     p.d_x = a.d_x;
     p.slots = slots;
     p.scale = g.scale;
     p.valid = g.valid;
     p.dirty = g.block_dirty;
     p.n_dirty = g.valid ? router_grad_blocks(T) : 0;
-    cudaError_t err = pairs::launch<Op>(maps, p, stream);
+    cudaError_t err = pairs::launch<Op>(maps, p, stream, p.n_pairs);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
