@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const GradProducts p, u
 
 struct GradLayout {
     int32_t ld;
-    int64_t dz, scale, block_max, block_dirty, valid, slots, bytes;
+    int64_t dz, d_logits, scale, block_max, block_dirty, valid, slots, bytes;
 };
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -267,6 +267,7 @@ GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
         return r;
     };
     l.dz = take(n_tokens * l.ld * 2);
+    l.d_logits = take(n_tokens * n_experts * 4);
     l.scale = take(8);
     l.block_max = take(int64_t{4} * router_grad_blocks(n_tokens));
     l.block_dirty = take(int64_t{4} * router_grad_blocks(n_tokens));
@@ -344,6 +345,7 @@ cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream)
     LogitGradients g;
     g.dz = reinterpret_cast<uint16_t*>(ws + l.dz);
     g.ld = l.ld;
+    g.d_logits = reinterpret_cast<float*>(ws + l.d_logits);
     g.scale = reinterpret_cast<float*>(ws + l.scale);
     g.block_max = reinterpret_cast<float*>(ws + l.block_max);
     const bool some = a.r.token_mask != nullptr || a.r.seq_offsets != nullptr;

@@ -7,8 +7,8 @@
 //     g[t, e] = d_losses[0]·E / (k T T_s)·counts[s, e] + Σ_j [id[t, j] = e]·d_w[t, j]
 //     d_z = p ⊙ (g − Σ_e p g) + d_losses[1]·2/T·logsumexp(z)·p
 //
-// A group of 4 to 32 lanes has a token, 8 logits a lane (up to 32 above 256 experts), and a lane
-// has the same experts of every token, so that column sums over a warp's tokens stay in
+// A group of 4 to 16 lanes has a token, 16 logits a lane (32 lanes and up to 32 logits above 256
+// experts), and a lane has the same experts of every token, so that column sums over a warp's tokens stay in
 // registers until the end of a piece.  All is read once.  Sums over tokens are fp32 over the
 // tokens of a warp and of a block and pairs of fp32 (Sum) beyond, always in the same
 // order.  (FP64 is slow here: with it the second launch took 16 us, by itself, for 32 tokens.)
@@ -172,7 +172,7 @@ struct BalanceParams {
 // One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
 // from one part to the next either b or s grows, so no two share a slot.
 template <int L, int PER, bool VEC>
-__global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(const BalanceParams p) {
     extern __shared__ float sums[];                               // [HALF][E], then int [E]
     __shared__ float zpart[WARPS];
     __shared__ int npart[WARPS];
@@ -211,19 +211,15 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
         for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
         float zz = 0.0f;
         int n = 0;
-        // the next tokens' rows are on their way while these are reduced
-        float z[PER], next[PER];
-        int64_t t = t0 + warp * PACK + lane / L;
-        bool live = t < t1 && counts_token(p.r.token_mask, t);
+        const float* row = p.r.logits + (t0 + warp * PACK + lane / L) * E;
+        int32_t left = static_cast<int32_t>(t1 - t0) - warp * PACK - lane / L;      // tokens from this lane's on
+        const uint8_t* mask = p.r.token_mask ? p.r.token_mask + (t1 - left) : nullptr;
+        for (int32_t i0 = warp * PACK; i0 < static_cast<int32_t>(t1 - t0); i0 += WARPS * PACK) {
+            const bool live = left > 0 && (mask == nullptr || *mask != 0);
+            float z[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] = 0.0f;
-        if (live) load_row<L, PER, VEC>(z, p.r.logits + t * E, l, E);
-        for (int64_t tw = t0 + warp * PACK; tw < t1; tw += WARPS * PACK) {
-            const int64_t tn = t + WARPS * PACK;
-            const bool live_next = tn < t1 && counts_token(p.r.token_mask, tn);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) next[i] = 0.0f;
-            if (live_next) load_row<L, PER, VEC>(next, p.r.logits + tn * E, l, E);
+            for (int i = 0; i < PER; ++i) z[i] = 0.0f;
+            if (live) load_row<L, PER, VEC>(z, row, l, E);
             const float lse = softmax_row<L, PER>(z);
             if (live) {
 #pragma unroll
@@ -233,10 +229,9 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) balance_kernel(cons
                     ++n;
                 }
             }
-#pragma unroll
-            for (int i = 0; i < PER; ++i) z[i] = next[i];
-            live = live_next;
-            t = tn;
+            row += static_cast<int64_t>(WARPS * PACK) * E;
+            left -= WARPS * PACK;
+            if (mask) mask += WARPS * PACK;
         }
         // a warp's tokens, then the block's warps
 #pragma unroll
@@ -424,11 +419,12 @@ struct GradParams {
     const float* d_losses;
     const int32_t* counts;
     const int32_t* seq_tokens;
-    uint16_t* dz;
+    uint16_t* dz;                 // [n_tokens, ld], in bf16 by the first pass, in fp16 by the second
     int32_t ld;
-    float* d_logits;
+    float* d_logits;              // [n_tokens, E]; nullable in bf16
     float* scale;
-    float* block_max;
+    float* block_max;             // [blocks of the first pass]
+    int32_t n_blocks;
     uint32_t* valid;              // nullable, as is what follows: all tokens count
     int32_t* block_dirty;
     const uint16_t* x;
@@ -455,60 +451,29 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& v) {
             ((v.w & 0x7fff7fffu) + ONE)) & 0x80008000u;
 }
 
-// MAX: only the largest |d_z| of each block, which sets the power of two that
-// the values are stored times (fp16 would lose gradients of a mean over tokens
-// otherwise; bf16 has fp32's range and needs none).  Otherwise the values, and of the tokens that
-// do not count whether x holds something that a product with zero does not remove.
-template <int L, int PER, bool VEC, bool BF16, bool MAX>
-__global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kernel(const GradParams p) {
+// d_z, and of the tokens that do not count whether x holds something that a product with zero does not
+// remove.  bf16 operands are rounded here.  fp16 would lose gradients of a mean over tokens, so its
+// operands are d_z times a power of two that the largest of all sets: round_kernel, from the
+// fp32 values and the blocks' largest magnitudes that are left here.  (Computing d_z twice instead, once
+// for its maximum, took 8 us more for 16384 x 256.)
+template <int L, int PER, bool VEC, bool BF16>
+__global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_kernel(const GradParams p) {
     __shared__ float smax[WARPS];
     constexpr int PACK = 32 / L;
-    // a token's routed gradients, by expert (a row per token that the block has at a time)
-    extern __shared__ float routed[];                             // [WARPS * PACK][L * PER + 4]
+    constexpr int ROW = L * PER + 4;
+    // per token that the block has at a time: the counts' part of g, by expert, to which the routed
+    // gradients are added and taken off again
+    extern __shared__ float rows[];                               // [WARPS * PACK][ROW]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1);
     const int32_t E = p.r.n_experts, k = p.r.top_k;
-    float* mine = routed + (warp * PACK + lane / L) * (L * PER + 4);
+    float* mine = rows + (warp * PACK + lane / L) * ROW;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    float scale = 1.0f;
-    if (!MAX && !BF16) {
-        float m = 0.0f;
-        for (unsigned i = threadIdx.x; i < gridDim.x; i += THREADS) m = fmaxf(m, p.block_max[i]);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (lane == 0) smax[warp] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, smax[w]);
-        scale = grad_scale(m);
-    }
-    if (!MAX && blockIdx.x == 0 && threadIdx.x == 0) {
-        p.scale[0] = scale;
-        p.scale[1] = 1.0f / scale;
-    }
+    if (BF16 && blockIdx.x == 0 && threadIdx.x == 0) p.scale[0] = p.scale[1] = 1.0f;
     const Seqs seqs{p.r.seq_offsets, p.r.n_seqs, p.r.n_tokens};
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.chunk;
     const int64_t last = first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens;
     const int64_t begin = seqs.bound(0), finish = seqs.bound(p.r.n_seqs);
-    if (!MAX && p.valid) {
-        // a bit per token that counts; whole steps of 64, zero past the end
-        uint32_t bad = 0;
-        for (int64_t t = first + 32 * warp; t < first + p.chunk && t < (p.r.n_tokens + 63) / 64 * 64; t += THREADS) {
-            const int64_t ti = t + lane;
-            const bool v = ti < p.r.n_tokens && ti >= begin && ti < finish && counts_token(p.r.token_mask, ti);
-            const uint32_t bits = __ballot_sync(0xffffffffu, v);
-            if (lane == 0) p.valid[t >> 5] = bits;
-            for (uint32_t out = ~bits; out != 0; out &= out - 1) {
-                const int64_t to = t + __ffs(static_cast<int>(out)) - 1;
-                if (to >= p.r.n_tokens) break;
-                const uint4* row = reinterpret_cast<const uint4*>(p.x + to * p.hidden);
-#pragma unroll 4
-                for (int32_t i = lane; i < p.hidden / 8; i += 32) bad |= not_finite<BF16>(__ldg(row + i));
-            }
-        }
-        const int any = __syncthreads_or(bad != 0);
-        if (threadIdx.x == 0) p.block_dirty[blockIdx.x] = any;
-    }
     float cb = 0.0f, cz = 0.0f;
     if (p.d_losses) {
         const float n = static_cast<float>(p.seq_tokens[p.r.n_seqs]);
@@ -520,74 +485,65 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kern
     int64_t t = first + warp * PACK + lane / L;
     int32_t s = seqs.find(first + warp * PACK);
     int64_t s_end = seqs.bound(s + 1);           // (of s = -1: where the first one starts)
-    int32_t base_of = -1;                        // the sequence whose counts are in base[]
-    float base[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) base[i] = 0.0f;
+    int32_t base_of = -1;                        // the sequence whose counts are in `mine`
+    for (int i = l; i < L * PER; i += L) mine[i] = 0.0f;
+    __syncwarp();
     float largest = 0.0f;
-    // the next tokens' logits, ids and routed gradients are on their way meanwhile
-    float z[PER], next[PER];
-    int32_t id = -1, id_next = -1;
-    float dw = 0.0f, dw_next = 0.0f;
-    auto ask = [&](int64_t at, float (&row)[PER], int32_t& i, float& w) {
-        const bool live = at < last && at >= begin && at < finish && counts_token(p.r.token_mask, at);
+    for (int64_t tw = first + warp * PACK; tw < last; tw += WARPS * PACK, t += WARPS * PACK) {
+        const bool live = t < last && t >= begin && t < finish && counts_token(p.r.token_mask, t);
+        float z[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) row[j] = 0.0f;
-        i = -1;
-        w = 0.0f;
+        for (int i = 0; i < PER; ++i) z[i] = 0.0f;
+        int32_t id = -1;
+        float dw = 0.0f;
         if (live) {
-            load_row<L, PER, VEC>(row, p.r.logits + at * E, l, E);
+            load_row<L, PER, VEC>(z, p.r.logits + t * E, l, E);
             if (p.d_weights && l < k) {
-                i = __ldg(p.r.topk_ids + at * k + l);
-                w = __ldg(p.d_weights + at * k + l);
+                id = __ldg(p.r.topk_ids + t * k + l);
+                dw = __ldg(p.d_weights + t * k + l);
             }
         }
-        return live;
-    };
-    bool live = ask(t, z, id, dw);
-    for (int64_t tw = first + warp * PACK; tw < last; tw += WARPS * PACK) {
-        const int64_t tn = t + WARPS * PACK;
-        const bool live_next = ask(tn, next, id_next, dw_next);
         if (cb != 0.0f) {
             while (t >= s_end && s + 1 < p.r.n_seqs) {
                 ++s;
                 s_end = seqs.bound(s + 1);
             }
-            if (live && s != base_of) {
+            if (live && s != base_of && s >= 0) {
                 base_of = s;
-                const float per_count = s >= 0 ? cb / static_cast<float>(max(p.seq_tokens[s], 1)) : 0.0f;
-                const int32_t* row = p.counts + static_cast<int64_t>(s >= 0 ? s : 0) * E;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = expert<L, VEC>(l, i);
-                    if (e < E) base[i] = per_count * static_cast<float>(__ldg(row + e));
-                }
+                const float per_count = cb / static_cast<float>(max(p.seq_tokens[s], 1));
+                const int32_t* row = p.counts + static_cast<int64_t>(s) * E;
+                for (int e = l; e < E; e += L) mine[e] = per_count * static_cast<float>(__ldg(row + e));
             }
+            __syncwarp();
         }
-        float d[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) d[i] = base[i];
+        float base = 0.0f;
         if (p.d_weights) {
             if (id >= E) {
                 if (p.status) atomicOr(p.status, MOE_DEV_BAD_EXPERT_ID);
                 id = -1;
             }
-            // an expert named twice gets both, in their order, from either
-            float w = 0.0f;
-            for (int q = 0; q < k; ++q) {
-                const int from = (lane & ~(L - 1)) + q;
-                const int32_t iq = __shfl_sync(0xffffffffu, id, from);
-                const float wq = __shfl_sync(0xffffffffu, dw, from);
-                if (iq == id) w += wq;
+            // an expert named twice gets both, in their order, from either lane
+            const uint32_t same = __match_any_sync(0xffffffffu, id < 0 ? -1 - lane : id * 32 + lane / L);
+            if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
+                float w = 0.0f;
+                for (int q = 0; q < k; ++q) {
+                    const int from = (lane & ~(L - 1)) + q;
+                    const float wq = __shfl_sync(0xffffffffu, dw, from);
+                    if (same >> from & 1u) w += wq;
+                }
+                dw = w;
             }
+            if (id >= 0) base = mine[id];
+            __syncwarp();
+            if (id >= 0) mine[id] = base + dw;
+            __syncwarp();
+        }
+        float d[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) mine[l + L * i] = 0.0f;
+        for (int i = 0; i < PER; ++i) d[i] = mine[expert<L, VEC>(l, i)];
+        if (p.d_weights) {
             __syncwarp();
-            if (id >= 0) mine[id] = w;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < PER; ++i) d[i] += mine[expert<L, VEC>(l, i)];
-            __syncwarp();
+            if (id >= 0) mine[id] = base;
         }
         const float lse = softmax_row<L, PER>(z);
         float dot = 0.0f;
@@ -595,46 +551,54 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kern
         for (int i = 0; i < PER; ++i) dot += z[i] * d[i];
         const float shift = cz * lse - lanes_sum<L>(dot);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) d[i] = live ? z[i] * (d[i] + shift) : 0.0f;
-        if (MAX) {
+        for (int i = 0; i < PER; ++i) {
+            d[i] = live ? z[i] * (d[i] + shift) : 0.0f;
+            if (!BF16 && expert<L, VEC>(l, i) < E) largest = fmaxf(largest, fabsf(d[i]));
+        }
+        if (t >= last) continue;
+        if (VEC) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (expert<L, VEC>(l, i) < E) largest = fmaxf(largest, fabsf(d[i]));
-        } else if (t < last) {
-            uint16_t* out = p.dz + t * p.ld;
-            if (VEC) {
+            for (int i = 0; i < PER; i += 8) {
+                const int e = expert<L, VEC>(l, i);
+                if (BF16 && e < p.ld)                    // (columns E .. ld - 1 are not read)
+                    *reinterpret_cast<uint4*>(p.dz + t * p.ld + e) =
+                        make_uint4(pack_16bit2<true>(d[i], d[i + 1]), pack_16bit2<true>(d[i + 2], d[i + 3]),
+                                   pack_16bit2<true>(d[i + 4], d[i + 5]), pack_16bit2<true>(d[i + 6], d[i + 7]));
+                if (p.d_logits && e < E)
+                    *reinterpret_cast<float4*>(p.d_logits + t * E + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                if (p.d_logits && e + 4 < E)
+                    *reinterpret_cast<float4*>(p.d_logits + t * E + e + 4) =
+                        make_float4(d[i + 4], d[i + 5], d[i + 6], d[i + 7]);
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < PER; i += 8) {
-                    const int e = expert<L, VEC>(l, i);
-                    if (e < p.ld)                        // (columns E .. ld - 1 are not read)
-                        *reinterpret_cast<uint4*>(out + e) =
-                            make_uint4(pack_16bit2<BF16>(d[i] * scale, d[i + 1] * scale),
-                                       pack_16bit2<BF16>(d[i + 2] * scale, d[i + 3] * scale),
-                                       pack_16bit2<BF16>(d[i + 4] * scale, d[i + 5] * scale),
-                                       pack_16bit2<BF16>(d[i + 6] * scale, d[i + 7] * scale));
-                    if (p.d_logits && e < E)
-                        *reinterpret_cast<float4*>(p.d_logits + t * E + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-                    if (p.d_logits && e + 4 < E)
-                        *reinterpret_cast<float4*>(p.d_logits + t * E + e + 4) =
-                            make_float4(d[i + 4], d[i + 5], d[i + 6], d[i + 7]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = expert<L, VEC>(l, i);
-                    if (e < p.ld) out[e] = static_cast<uint16_t>(pack_16bit2<BF16>(d[i] * scale, 0.0f) & 0xffffu);
-                    if (p.d_logits && e < E) p.d_logits[t * E + e] = d[i];
-                }
+            for (int i = 0; i < PER; ++i) {
+                const int e = expert<L, VEC>(l, i);
+                if (BF16 && e < p.ld) p.dz[t * p.ld + e] = static_cast<uint16_t>(pack_16bit2<true>(d[i], 0.0f) & 0xffffu);
+                if (p.d_logits && e < E) p.d_logits[t * E + e] = d[i];
             }
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] = next[i];
-        live = live_next;
-        id = id_next;
-        dw = dw_next;
-        t = tn;
     }
-    if (MAX) {
+    if (p.valid) {
+        // a bit per token that counts; whole steps of 64, zero past the end
+        uint32_t bad = 0;
+        for (int64_t tv = first + 32 * warp; tv < first + p.chunk && tv < (p.r.n_tokens + 63) / 64 * 64; tv += THREADS) {
+            const int64_t ti = tv + lane;
+            const bool v = ti < p.r.n_tokens && ti >= begin && ti < finish && counts_token(p.r.token_mask, ti);
+            const uint32_t bits = __ballot_sync(0xffffffffu, v);
+            if (lane == 0) p.valid[tv >> 5] = bits;
+            for (uint32_t out = ~bits; out != 0; out &= out - 1) {
+                const int64_t to = tv + __ffs(static_cast<int>(out)) - 1;
+                if (to >= p.r.n_tokens) break;
+                const uint4* row = reinterpret_cast<const uint4*>(p.x + to * p.hidden);
+#pragma unroll 4
+                for (int32_t i = lane; i < p.hidden / 8; i += 32) bad |= not_finite<BF16>(__ldg(row + i));
+            }
+        }
+        const int any = __syncthreads_or(bad != 0);
+        if (threadIdx.x == 0) p.block_dirty[blockIdx.x] = any;
+    }
+    if (!BF16) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
         if (lane == 0) smax[warp] = largest;
@@ -643,6 +607,45 @@ __global__ void __launch_bounds__(THREADS, PER <= 8 ? 2 : 1) logit_gradient_kern
             for (int w = 0; w < WARPS; ++w) largest = fmaxf(largest, smax[w]);
             p.block_max[blockIdx.x] = largest;
         }
+    }
+}
+
+// fp16 operands from fp32 gradients, times the power of two.
+__global__ void __launch_bounds__(256) round_kernel(const GradParams p) {
+    __shared__ float smax[8];
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    float m = 0.0f;
+    for (int i = threadIdx.x; i < p.n_blocks; i += 256) m = fmaxf(m, p.block_max[i]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) smax[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, smax[w]);
+    const float scale = grad_scale(m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.scale[0] = scale;
+        p.scale[1] = 1.0f / scale;
+    }
+    const int32_t E = p.r.n_experts, pieces = p.ld / 8;
+    const int64_t all = p.r.n_tokens * pieces, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
+        float v[8];
+        if ((E & 7) == 0) {
+            // rows one after the other in both arrays
+            const float4* src = reinterpret_cast<const float4*>(p.d_logits) + 2 * i;
+            const float4 a = src[0], b = src[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const int64_t t = i / pieces;
+            const int32_t e = static_cast<int32_t>(i - t * pieces) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = e + j < E ? p.d_logits[t * E + e + j] : 0.0f;
+        }
+        *reinterpret_cast<uint4*>(p.dz + 8 * i) =
+            make_uint4(pack_16bit2<false>(v[0] * scale, v[1] * scale), pack_16bit2<false>(v[2] * scale, v[3] * scale),
+                       pack_16bit2<false>(v[4] * scale, v[5] * scale), pack_16bit2<false>(v[6] * scale, v[7] * scale));
     }
 }
 
@@ -723,11 +726,10 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     const bool vec = E % 4 == 0;
     const size_t smem = static_cast<size_t>(HALF + 1) * E * 4;
     auto kernel = E > 256 ? (vec ? balance_kernel<32, 32, true> : balance_kernel<32, 32, false>)
-                : !vec    ? balance_kernel<32, 8, false>
-                : E > 128 ? balance_kernel<32, 8, true>
-                : E > 64  ? balance_kernel<16, 8, true>
-                : E > 32  ? balance_kernel<8, 8, true>
-                          : balance_kernel<4, 8, true>;
+                : !vec    ? balance_kernel<16, 16, false>
+                : E > 128 ? balance_kernel<16, 16, true>
+                : E > 64  ? balance_kernel<8, 16, true>
+                          : balance_kernel<4, 16, true>;
     cudaError_t err = launch_pdl(kernel, dim3(static_cast<unsigned>(l.chunks)), THREADS, smem, stream, p);
     if (err != cudaSuccess) return err;
     return launch_pdl(balance_reduce_kernel, dim3(static_cast<unsigned>(l.expert_blocks), static_cast<unsigned>(a.r.n_seqs)),
@@ -739,39 +741,39 @@ int router_grad_blocks(int64_t n_tokens) {
     return static_cast<int>((n_tokens + c - 1) / c);
 }
 
-template <bool BF16, bool MAX>
-static cudaError_t launch_gradient_pass(const GradParams& p, int blocks, cudaStream_t stream) {
+template <bool BF16>
+static cudaError_t launch_gradient_pass(const GradParams& p, cudaStream_t stream) {
     const int32_t E = p.r.n_experts;
     const bool vec = E % 4 == 0;
-    // 8 logits a lane, and a lane for each of a token's ids
+    // 16 logits a lane, and a lane for each of a token's ids
     const int k = p.r.top_k;
-    const int lanes = !vec || E > 128 ? 32 : E > 64 || k > 8 ? 16 : E > 32 || k > 4 ? 8 : 4;
-    const int per = E > 256 ? 32 : 8;
-    auto kernel = per == 32     ? (vec ? logit_gradient_kernel<32, 32, true, BF16, MAX> : logit_gradient_kernel<32, 32, false, BF16, MAX>)
-                : !vec          ? logit_gradient_kernel<32, 8, false, BF16, MAX>
-                : lanes == 32   ? logit_gradient_kernel<32, 8, true, BF16, MAX>
-                : lanes == 16   ? logit_gradient_kernel<16, 8, true, BF16, MAX>
-                : lanes == 8    ? logit_gradient_kernel<8, 8, true, BF16, MAX>
-                                : logit_gradient_kernel<4, 8, true, BF16, MAX>;
+    const int lanes = E > 256 ? 32 : !vec || E > 128 || k > 8 ? 16 : E > 64 || k > 4 ? 8 : 4;
+    const int per = E > 256 ? 32 : 16;
+    auto kernel = per == 32     ? (vec ? logit_gradient_kernel<32, 32, true, BF16> : logit_gradient_kernel<32, 32, false, BF16>)
+                : !vec          ? logit_gradient_kernel<16, 16, false, BF16>
+                : lanes == 16   ? logit_gradient_kernel<16, 16, true, BF16>
+                : lanes == 8    ? logit_gradient_kernel<8, 16, true, BF16>
+                                : logit_gradient_kernel<4, 16, true, BF16>;
     const size_t smem = static_cast<size_t>(WARPS) * (32 / lanes) * (lanes * per + 4) * 4;
     if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (err != cudaSuccess) return err;
     }
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), THREADS, smem, stream, p);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.n_blocks)), THREADS, smem, stream, p);
 }
 
 cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients& g, cudaStream_t stream) {
     GradParams p{};
     p.r = a.r;
     p.chunk = chunk_tokens(a.r.n_tokens, 64);
+    p.n_blocks = router_grad_blocks(a.r.n_tokens);
     p.d_weights = a.d_topk_weights;
     p.d_losses = a.d_losses;
     p.counts = a.counts;
     p.seq_tokens = a.seq_tokens;
     p.dz = g.dz;
     p.ld = g.ld;
-    p.d_logits = a.d_logits;
+    p.d_logits = a.d_logits || a.bf16 ? a.d_logits : g.d_logits;
     p.scale = g.scale;
     p.block_max = g.block_max;
     p.valid = g.valid;
@@ -779,11 +781,11 @@ cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients
     p.x = a.x;
     p.hidden = a.hidden;
     p.status = a.status;
-    const int blocks = router_grad_blocks(a.r.n_tokens);
-    if (a.bf16) return launch_gradient_pass<true, false>(p, blocks, stream);
-    const cudaError_t err = launch_gradient_pass<false, true>(p, blocks, stream);
+    if (a.bf16) return launch_gradient_pass<true>(p, stream);
+    const cudaError_t err = launch_gradient_pass<false>(p, stream);
     if (err != cudaSuccess) return err;
-    return launch_gradient_pass<false, false>(p, blocks, stream);
+    const int64_t blocks = (a.r.n_tokens * (g.ld / 8) + 255) / 256, most = 8 * 152;
+    return launch_pdl(round_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, p);
 }
 
 }  // namespace moe

@@ -58,6 +58,7 @@ cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream)
 struct LogitGradients {
     uint16_t* dz;
     int32_t ld;
+    float* d_logits;              // [n_tokens, n_experts], fp16 only: d_z where the caller keeps none
     float* scale;                 // [2]
     float* block_max;             // [router_grad_blocks()]
     uint32_t* valid;
