@@ -497,8 +497,8 @@ int64_t moe_router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts,
  *   d_logits        out, nullable: d_z, [n_tokens, n_experts] fp32
  *   workspace       device memory of moe_router_backward_workspace_bytes() bytes, caller-owned;
  *                   calls that overlap on the GPU must not share it
- * Limits as in moe_router_balance.  Three kernel launches, four in fp16; waits and status_dev as
- * in the feed-forward block. */
+ * Limits as in moe_router_balance.  Two to four kernel launches; waits and status_dev as in the
+ * feed-forward block. */
 moe_status_t moe_router_backward(int32_t dtype, const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
                                  const uint16_t* router_w, int32_t n_experts, const float* logits,
                                  const int32_t* topk_ids, int32_t top_k, const float* d_topk_weights,

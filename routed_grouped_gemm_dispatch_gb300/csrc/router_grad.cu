@@ -2,7 +2,7 @@
 //     d_x = d_z·W_g       [T, H]     K = experts
 //     d_W = d_zᵀ·x        [E, H]     K = tokens
 // in one launch of tiles of 256 x 256 (pair_tiles.cuh), and a second that adds up the parts of
-// d_W.  x is read once, d_x written once; d_z and W_g stay in L2.
+// d_W where it has any.  x is read once, d_x written once; d_z and W_g stay in L2.
 //
 //  * d_W has few tiles (DeepSeek-V3-shaped: 28) and a long K, so its steps are laid end to
 //    end, tile after tile, and cut into as many equal pieces as there are pairs.  The sums
@@ -48,6 +48,7 @@ struct GradProducts {
     int32_t n_pairs;                 // of the launch
     int32_t x_rounds;                // d_x tiles of a pair
     uint16_t* d_x;
+    uint16_t* d_w;                   // where every piece is a whole tile (otherwise null)
     float* slots;                    // [w_pairs + w_tiles][256][256]
     const float* scale;              // [1]: what undoes the power of two in d_z
     const uint32_t* valid;           // a bit per token; null: all count
@@ -138,8 +139,9 @@ struct GradOp {
         uint8_t* staging;
         int32_t row, lane;           // first of the warp's rows inside the tile
         float inv;
-        bool part;
-        int64_t at;                  // of the warp's first row in d_x, or in the slots
+        bool part;                   // a part of d_W for the slots
+        uint16_t* dst;               // otherwise d_x or d_W
+        int64_t at;                  // of the warp's first row there
         int32_t rows, cols;
 
         __device__ __forceinline__ Finish(const Params& p_, uint8_t* staging_, int32_t row_, int, int lane_)
@@ -149,7 +151,7 @@ struct GradOp {
         __device__ __forceinline__ int width_of() const { return TILE; }
         __device__ __forceinline__ bool before(const Code& c) {
             if (c.k < 0) return false;
-            part = c.pair >= 0;
+            part = c.pair >= 0 && p.d_w == nullptr;
             if (part) {
                 const Part w = part_of(p, c.pair, c.k);
                 at = (static_cast<int64_t>(c.pair + w.tile) * TILE + row) * TILE;
@@ -158,14 +160,17 @@ struct GradOp {
                 MOE_DCHECK(w.steps == 0 || (w.tile < p.w_tiles && c.pair + w.tile < p.w_pairs + p.w_tiles), p.status);
                 return w.steps > 0;
             }
-            const int32_t m = c.k / p.x_tiles_n;
-            const int32_t col = (c.k - m * p.x_tiles_n) * TILE;
+            const bool w = c.pair >= 0;
+            const int32_t tile = w ? c.pair : c.k;               // (whole tiles: piece i is tile i)
+            const int32_t m = tile / p.x_tiles_n;
+            const int32_t col = (tile - m * p.x_tiles_n) * TILE;
             const int64_t first = static_cast<int64_t>(m) * TILE + row;
-            const int64_t left = p.n_tokens - first;
+            const int64_t left = (w ? p.n_experts : p.n_tokens) - first;
             rows = left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left));
             cols = p.hidden - col;
             at = first * p.hidden + col;
-            return true;
+            dst = w ? p.d_w : p.d_x;
+            return !w || c.k == 0;
         }
         __device__ __forceinline__ void pass(int c, uint32_t taddr) {
             if (rows <= 0 || c * 64 >= cols) return;
@@ -185,7 +190,8 @@ struct GradOp {
                 return;
             }
             MOE_DCHECK(at >= 0 && at + static_cast<int64_t>(rows - 1) * p.hidden + c * 64 +
-                                      (cols - c * 64 < 64 ? cols - c * 64 : 64) <= p.n_tokens * p.hidden,
+                                      (cols - c * 64 < 64 ? cols - c * 64 : 64) <=
+                                  (dst == p.d_x ? p.n_tokens : p.n_experts) * static_cast<int64_t>(p.hidden),
                        p.status);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -202,38 +208,56 @@ struct GradOp {
                     el[4 * hh + i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-            store_staged_64(el, staging, p.d_x + at + c * 64, p.hidden, lane, rows, cols - c * 64);
+            store_staged_64(el, staging, dst + at + c * 64, p.hidden, lane, rows, cols - c * 64);
         }
     };
 };
 
-// d_W from its parts: a thread has four columns of a row.
+// d_W from its parts: a block has 16 rows of a tile, a thread four columns of every fourth of them.
 template <bool BF16>
 __global__ void __launch_bounds__(256) join_parts_kernel(const GradProducts p, uint16_t* d_w) {
+    __shared__ int32_t range[2];
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) >> 4;
+    if (threadIdx.x == 0) {
+        // the piece that holds the tile's first step, and the one past its last
+        const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
+        const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps, t1 = t0 + p.w_steps;
+        int32_t i = static_cast<int32_t>(t0 * p.w_pairs / all);
+        while (piece_start(i + 1, p.w_pairs, all) <= t0) ++i;
+        range[0] = i;
+        while (i < p.w_pairs && piece_start(i, p.w_pairs, all) < t1) ++i;
+        range[1] = i;
+        MOE_DCHECK(range[0] >= 0 && range[1] <= p.w_pairs && range[0] < range[1], p.status);
+    }
+    __syncthreads();
+    const int32_t m = tile / p.x_tiles_n;
+    const int32_t h = (tile - m * p.x_tiles_n) * TILE + (static_cast<int32_t>(threadIdx.x) & 63) * 4;
+    const int32_t row = (static_cast<int32_t>(blockIdx.x) & 15) * 16 + (static_cast<int32_t>(threadIdx.x) >> 6);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int32_t tile = static_cast<int32_t>(blockIdx.x) >> 6;
-    const int32_t at = (static_cast<int32_t>(blockIdx.x) & 63) * 1024 + static_cast<int32_t>(threadIdx.x) * 4;
-    const int32_t m = tile / p.x_tiles_n;
-    const int32_t e = m * TILE + (at >> 8), h = (tile - m * p.x_tiles_n) * TILE + (at & 255);
-    if (e >= p.n_experts || h >= p.hidden) return;
-    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
-    const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps, t1 = t0 + p.w_steps;
-    // the piece that holds the tile's first step, and the ones after it
-    int32_t i = static_cast<int32_t>(t0 * p.w_pairs / all);
-    while (piece_start(i + 1, p.w_pairs, all) <= t0) ++i;
     const float inv = __ldg(p.scale + 1);
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (; i < p.w_pairs && piece_start(i, p.w_pairs, all) < t1; ++i) {
-        MOE_DCHECK(i + tile < p.w_pairs + p.w_tiles, p.status);
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p.slots + static_cast<int64_t>(i + tile) * TILE * TILE + at));
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
+    float4 v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int32_t i = range[0]; i < range[1]; ++i) {
+        const float4* src = reinterpret_cast<const float4*>(p.slots + (static_cast<int64_t>(i + tile) * TILE + row) * TILE) +
+                            (threadIdx.x & 63);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float4 x = __ldg(src + r * 4 * (TILE / 4));
+            v[r].x += x.x;
+            v[r].y += x.y;
+            v[r].z += x.z;
+            v[r].w += x.w;
+        }
     }
-    *reinterpret_cast<uint2*>(d_w + static_cast<int64_t>(e) * p.hidden + h) =
-        make_uint2(pack_16bit2<BF16>(v.x * inv, v.y * inv), pack_16bit2<BF16>(v.z * inv, v.w * inv));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int32_t e = m * TILE + row + 4 * r;
+        if (e < p.n_experts && h < p.hidden)
+            *reinterpret_cast<uint2*>(d_w + static_cast<int64_t>(e) * p.hidden + h) =
+                make_uint2(pack_16bit2<BF16>(v[r].x * inv, v[r].y * inv), pack_16bit2<BF16>(v[r].z * inv, v[r].w * inv));
+    }
 }
 
 struct GradLayout {
@@ -312,18 +336,19 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     p.x_rounds = (p.x_tiles + p.n_pairs - 1) / p.n_pairs;
     p.total_tiles = p.n_pairs * (p.w_parts + p.x_rounds);
     p.d_x = a.d_x;
+    p.d_w = p.w_pairs == p.w_tiles ? a.d_router_w : nullptr;
     p.slots = slots;
     p.scale = g.scale;
     p.valid = g.valid;
     p.dirty = g.block_dirty;
     p.n_dirty = g.valid ? router_grad_blocks(T) : 0;
     cudaError_t err = pairs::launch<Op>(maps, p, stream, p.n_pairs);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || p.d_w) return err;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles) * 64);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles) * 16);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = attr;

@@ -451,10 +451,39 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& v) {
             ((v.w & 0x7fff7fffu) + ONE)) & 0x80008000u;
 }
 
+// fp16 operands from fp32 gradients, times the power of two that their largest magnitude asks for: pieces
+// first, first + step, ...
+__device__ __forceinline__ void round_values(const GradParams& p, float largest, int64_t first, int64_t step) {
+    const float scale = grad_scale(largest);
+    if (first == 0) {
+        p.scale[0] = scale;
+        p.scale[1] = 1.0f / scale;
+    }
+    const int32_t E = p.r.n_experts, pieces = p.ld / 8;
+    const int64_t all = p.r.n_tokens * pieces;
+    for (int64_t i = first; i < all; i += step) {
+        float v[8];
+        if ((E & 7) == 0) {
+            // rows one after the other in both arrays
+            const float4* src = reinterpret_cast<const float4*>(p.d_logits) + 2 * i;
+            const float4 a = src[0], b = src[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const int64_t t = i / pieces;
+            const int32_t e = static_cast<int32_t>(i - t * pieces) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = e + j < E ? p.d_logits[t * E + e + j] : 0.0f;
+        }
+        *reinterpret_cast<uint4*>(p.dz + 8 * i) =
+            make_uint4(pack_16bit2<false>(v[0] * scale, v[1] * scale), pack_16bit2<false>(v[2] * scale, v[3] * scale),
+                       pack_16bit2<false>(v[4] * scale, v[5] * scale), pack_16bit2<false>(v[6] * scale, v[7] * scale));
+    }
+}
+
 // d_z, and of the tokens that do not count whether x holds something that a product with zero does not
 // remove.  bf16 operands are rounded here.  fp16 would lose gradients of a mean over tokens, so its
 // operands are d_z times a power of two that the largest of all sets: round_kernel, from the
-// fp32 values and the blocks' largest magnitudes that are left here.  (Computing d_z twice instead, once
+// fp32 values and the blocks' largest magnitudes that are left here (one block does it itself).  (Computing d_z twice instead, once
 // for its maximum, took 8 us more for 16384 x 256.)
 template <int L, int PER, bool VEC, bool BF16>
 __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_kernel(const GradParams p) {
@@ -603,14 +632,13 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
         for (int d = 16; d > 0; d >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
         if (lane == 0) smax[warp] = largest;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 0; w < WARPS; ++w) largest = fmaxf(largest, smax[w]);
-            p.block_max[blockIdx.x] = largest;
-        }
+        for (int w = 0; w < WARPS; ++w) largest = fmaxf(largest, smax[w]);
+        if (gridDim.x == 1) round_values(p, largest, threadIdx.x, THREADS);       // nobody else's to wait for
+        else if (threadIdx.x == 0) p.block_max[blockIdx.x] = largest;
     }
 }
 
-// fp16 operands from fp32 gradients, times the power of two.
+// The same for many blocks.
 __global__ void __launch_bounds__(256) round_kernel(const GradParams p) {
     __shared__ float smax[8];
     pdl_wait_prior_grid();
@@ -623,30 +651,7 @@ __global__ void __launch_bounds__(256) round_kernel(const GradParams p) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = fmaxf(m, smax[w]);
-    const float scale = grad_scale(m);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.scale[0] = scale;
-        p.scale[1] = 1.0f / scale;
-    }
-    const int32_t E = p.r.n_experts, pieces = p.ld / 8;
-    const int64_t all = p.r.n_tokens * pieces, step = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += step) {
-        float v[8];
-        if ((E & 7) == 0) {
-            // rows one after the other in both arrays
-            const float4* src = reinterpret_cast<const float4*>(p.d_logits) + 2 * i;
-            const float4 a = src[0], b = src[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const int64_t t = i / pieces;
-            const int32_t e = static_cast<int32_t>(i - t * pieces) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = e + j < E ? p.d_logits[t * E + e + j] : 0.0f;
-        }
-        *reinterpret_cast<uint4*>(p.dz + 8 * i) =
-            make_uint4(pack_16bit2<false>(v[0] * scale, v[1] * scale), pack_16bit2<false>(v[2] * scale, v[3] * scale),
-                       pack_16bit2<false>(v[4] * scale, v[5] * scale), pack_16bit2<false>(v[6] * scale, v[7] * scale));
-    }
+    round_values(p, m, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, static_cast<int64_t>(gridDim.x) * 256);
 }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -783,7 +788,7 @@ cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients
     p.status = a.status;
     if (a.bf16) return launch_gradient_pass<true>(p, stream);
     const cudaError_t err = launch_gradient_pass<false>(p, stream);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || p.n_blocks == 1) return err;
     const int64_t blocks = (a.r.n_tokens * (g.ld / 8) + 255) / 256, most = 8 * 152;
     return launch_pdl(round_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, p);
 }
