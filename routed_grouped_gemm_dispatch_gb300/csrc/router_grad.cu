@@ -4,12 +4,11 @@
 // in one launch of tiles of 256 x 256 (pair_tiles.cuh), and a second that adds up the parts of
 // d_W where it has any.  x is read once, d_x written once; d_z and W_g stay in L2.
 //
-//  * d_W has few tiles (DeepSeek-V3-shaped: 28) and a long K, so its steps are laid end to
-//    end, tile after tile, and cut into as many equal pieces as there are pairs.  The sums
-//    of a pair's part of a tile go to fp32 slot pair + tile: from one part to the next
-//    either of them grows, so no two share a slot.  They are added in pair order.
-//  * Half of the pairs do their part of d_W first and half their part of d_x, so that x is read
-//    while d_x is written: 16384 x 256 x 7168 in 92 us otherwise, 45 of them reading at 5.2 TB/s.
+//  * d_W has few tiles (DeepSeek-V3-shaped: 28) and a long K, so K is split into as many parts as
+//    pairs allow, whose sums go to fp32 slots and are added in their order.  Pairs that
+//    run at the same time have neighbouring columns of the same tokens, so DRAM is read in whole rows.
+//  * The pairs of every other part do their share of d_x first, so that x is read while d_x is
+//    written, and pairs without a part do more of it.
 //  * Operands are read as they lie: d_z by token rows for d_x, transposed for d_W.
 //  * Rows of x whose token does not count are multiplied by a d_z of zero.  If one of them holds an
 //    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
@@ -39,41 +38,21 @@ struct GradProducts {
     int32_t* status;
     int64_t n_tokens;
     int32_t n_experts, hidden;
-    int32_t x_tiles_n;               // column tiles, of both products
-    int32_t w_tiles;                 // tiles of d_W
-    int32_t w_steps;                 // K steps of one
-    int32_t w_pairs;                 // pieces that all of them are cut into
-    int32_t w_parts;                 // tiles that a piece touches at most
-    int32_t x_tiles;                 // of d_x
     int32_t n_pairs;                 // of the launch
-    int32_t x_rounds;                // d_x tiles of a pair
+    int32_t tiles_n;                 // column tiles, of both products
+    int32_t w_tiles, w_parts;        // tiles of d_W, and parts of each along K
+    int32_t w_steps;                 // K steps of a tile
+    int32_t w_items;                 // parts that a pair has at most
+    int32_t x_tiles;                 // of d_x
+    int32_t x_items, x_lead;         // those of a pair with w_items parts, and how many more the others have
     uint16_t* d_x;
-    uint16_t* d_w;                   // where every piece is a whole tile (otherwise null)
-    float* slots;                    // [w_pairs + w_tiles][256][256]
+    uint16_t* d_w;                   // where tiles are not split (otherwise null)
+    float* slots;                    // [w_parts][w_tiles][256][256]
     const float* scale;              // [1]: what undoes the power of two in d_z
     const uint32_t* valid;           // a bit per token; null: all count
     const int32_t* dirty;            // [n_dirty] is there something to remove from x
     int32_t n_dirty;
 };
-
-// Steps of d_W before piece i.
-__host__ __device__ __forceinline__ int64_t piece_start(int32_t i, int32_t w_pairs, int64_t all_steps) {
-    return all_steps * i / w_pairs;
-}
-
-// Part `part` of piece `piece` of d_W: a tile and steps of it (none: steps 0).
-struct Part {
-    int32_t tile, k0, steps;
-};
-__device__ __forceinline__ Part part_of(const GradProducts& p, int32_t piece, int32_t part) {
-    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
-    const int64_t b0 = piece_start(piece, p.w_pairs, all), b1 = piece_start(piece + 1, p.w_pairs, all);
-    const int32_t tile = static_cast<int32_t>(b0 / p.w_steps) + part;
-    const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps;
-    const int64_t from = b0 > t0 ? b0 : t0;
-    const int64_t to = b1 < t0 + p.w_steps ? b1 : t0 + p.w_steps;
-    return Part{tile, static_cast<int32_t>(from - t0), to > from ? static_cast<int32_t>(to - from) : 0};
-}
 
 template <bool BF16_>
 struct GradOp {
@@ -82,42 +61,49 @@ struct GradOp {
     static constexpr bool MASKABLE = true;
     static constexpr bool QUEUE = false;
     using Params = GradProducts;
-    // Pair `pair`'s item: part k of piece `pair` of d_W, or tile k of d_x (neither: k < 0).
+    // Part `part` of tile `tile` of d_W, or tile `tile` of d_x (part < 0); nothing where tile < 0.
     struct Code {
-        int32_t pair, k;
+        int32_t tile, part;
     };
     static __device__ __forceinline__ Code code(const Params& p, int32_t t) {
         const int32_t pair = t % p.n_pairs;
         int32_t k = t / p.n_pairs;
-        if (pair & 1) k = k < p.x_rounds ? k + p.w_parts : k - p.x_rounds;       // d_x first
-        if (k < p.w_parts) return Code{pair, pair < p.w_pairs ? k : -1};
-        const int32_t x = (k - p.w_parts) * p.n_pairs + pair;
-        return Code{-1, x < p.x_tiles ? x : -1};
+        const int32_t pieces = p.w_tiles * p.w_parts;
+        const int32_t busy = pieces - (p.w_items - 1) * p.n_pairs;       // pairs with w_items parts; the others have one less
+        const int32_t x_most = p.x_items + p.x_lead;
+        // every other part last
+        if (pair / p.w_tiles & 1) k = k < x_most ? k + p.w_items : k - x_most;
+        if (k < p.w_items) {
+            const int32_t piece = k * p.n_pairs + pair;
+            if (piece >= pieces) return Code{-1, 0};
+            const int32_t part = piece / p.w_tiles;
+            return Code{piece - part * p.w_tiles, part};
+        }
+        k -= p.w_items;
+        if (k >= p.x_items && pair < busy) return Code{-1, 0};
+        const int32_t x = k < p.x_items ? k * p.n_pairs + pair
+                                        : p.x_items * p.n_pairs + (k - p.x_items) * (p.n_pairs - busy) + pair - busy;
+        return Code{x < p.x_tiles ? x : -1, -1};
     }
     enum { DZ, W_T, DZ_T, X_T, MAPS };
 
     static __device__ __forceinline__ Tile tile(const Params& p, const Code& c) {
         Tile ti{};
         ti.width = TILE;
-        if (c.k < 0) return ti;
-        if (c.pair >= 0) {
-            const Part w = part_of(p, c.pair, c.k);
-            const int32_t m = w.tile / p.x_tiles_n;
+        if (c.tile < 0) return ti;
+        const int32_t m = c.tile / p.tiles_n;
+        ti.a_row = m * TILE;
+        ti.b_row = (c.tile - m * p.tiles_n) * TILE;
+        if (c.part >= 0) {
             ti.a_map = DZ_T;
             ti.b_map = X_T;
             ti.a_mn = ti.b_mn = true;
-            ti.a_row = m * TILE;
-            ti.b_row = (w.tile - m * p.x_tiles_n) * TILE;
-            ti.k0 = w.k0;
-            ti.steps = w.steps;
+            ti.k0 = static_cast<int32_t>(static_cast<int64_t>(p.w_steps) * c.part / p.w_parts);
+            ti.steps = static_cast<int32_t>(static_cast<int64_t>(p.w_steps) * (c.part + 1) / p.w_parts) - ti.k0;
         } else {
-            // row by row: concurrent pairs write whole rows of d_x
-            const int32_t m = c.k / p.x_tiles_n;
             ti.a_map = DZ;
             ti.b_map = W_T;
             ti.b_mn = true;
-            ti.a_row = m * TILE;
-            ti.b_row = (c.k - m * p.x_tiles_n) * TILE;
             ti.steps = (p.n_experts + pairs::BK - 1) / pairs::BK;
         }
         return ti;
@@ -150,27 +136,24 @@ struct GradOp {
         }
         __device__ __forceinline__ int width_of() const { return TILE; }
         __device__ __forceinline__ bool before(const Code& c) {
-            if (c.k < 0) return false;
-            part = c.pair >= 0 && p.d_w == nullptr;
+            if (c.tile < 0) return false;
+            part = c.part >= 0 && p.d_w == nullptr;
             if (part) {
-                const Part w = part_of(p, c.pair, c.k);
-                at = (static_cast<int64_t>(c.pair + w.tile) * TILE + row) * TILE;
+                at = ((static_cast<int64_t>(c.part) * p.w_tiles + c.tile) * TILE + row) * TILE;
                 rows = 32;
                 cols = TILE;
-                MOE_DCHECK(w.steps == 0 || (w.tile < p.w_tiles && c.pair + w.tile < p.w_pairs + p.w_tiles), p.status);
-                return w.steps > 0;
+                MOE_DCHECK(c.part < p.w_parts && c.tile < p.w_tiles, p.status);
+                return true;
             }
-            const bool w = c.pair >= 0;
-            const int32_t tile = w ? c.pair : c.k;               // (whole tiles: piece i is tile i)
-            const int32_t m = tile / p.x_tiles_n;
-            const int32_t col = (tile - m * p.x_tiles_n) * TILE;
+            const int32_t m = c.tile / p.tiles_n;
+            const int32_t col = (c.tile - m * p.tiles_n) * TILE;
             const int64_t first = static_cast<int64_t>(m) * TILE + row;
-            const int64_t left = (w ? p.n_experts : p.n_tokens) - first;
+            const int64_t left = (c.part >= 0 ? p.n_experts : p.n_tokens) - first;
             rows = left > 32 ? 32 : (left < 0 ? 0 : static_cast<int32_t>(left));
             cols = p.hidden - col;
             at = first * p.hidden + col;
-            dst = w ? p.d_w : p.d_x;
-            return !w || c.k == 0;
+            dst = c.part >= 0 ? p.d_w : p.d_x;
+            return true;
         }
         __device__ __forceinline__ void pass(int c, uint32_t taddr) {
             if (rows <= 0 || c * 64 >= cols) return;
@@ -213,51 +196,31 @@ struct GradOp {
     };
 };
 
-// d_W from its parts: a block has 16 rows of a tile, a thread four columns of every fourth of them.
+// d_W from its parts, in their order: a block has 4 rows of a tile, a thread four columns of one.
 template <bool BF16>
 __global__ void __launch_bounds__(256) join_parts_kernel(const GradProducts p, uint16_t* d_w) {
-    __shared__ int32_t range[2];
-    const int32_t tile = static_cast<int32_t>(blockIdx.x) >> 4;
-    if (threadIdx.x == 0) {
-        // the piece that holds the tile's first step, and the one past its last
-        const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
-        const int64_t t0 = static_cast<int64_t>(tile) * p.w_steps, t1 = t0 + p.w_steps;
-        int32_t i = static_cast<int32_t>(t0 * p.w_pairs / all);
-        while (piece_start(i + 1, p.w_pairs, all) <= t0) ++i;
-        range[0] = i;
-        while (i < p.w_pairs && piece_start(i, p.w_pairs, all) < t1) ++i;
-        range[1] = i;
-        MOE_DCHECK(range[0] >= 0 && range[1] <= p.w_pairs && range[0] < range[1], p.status);
-    }
-    __syncthreads();
-    const int32_t m = tile / p.x_tiles_n;
-    const int32_t h = (tile - m * p.x_tiles_n) * TILE + (static_cast<int32_t>(threadIdx.x) & 63) * 4;
-    const int32_t row = (static_cast<int32_t>(blockIdx.x) & 15) * 16 + (static_cast<int32_t>(threadIdx.x) >> 6);
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) >> 6;
+    const int32_t m = tile / p.tiles_n;
+    const int32_t row = (static_cast<int32_t>(blockIdx.x) & 63) * 4 + (static_cast<int32_t>(threadIdx.x) >> 6);
+    const int32_t e = m * TILE + row, h = (tile - m * p.tiles_n) * TILE + (static_cast<int32_t>(threadIdx.x) & 63) * 4;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
+    if (e >= p.n_experts || h >= p.hidden) return;
     const float inv = __ldg(p.scale + 1);
-    float4 v[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int32_t i = range[0]; i < range[1]; ++i) {
-        const float4* src = reinterpret_cast<const float4*>(p.slots + (static_cast<int64_t>(i + tile) * TILE + row) * TILE) +
-                            (threadIdx.x & 63);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float4 x = __ldg(src + r * 4 * (TILE / 4));
-            v[r].x += x.x;
-            v[r].y += x.y;
-            v[r].z += x.z;
-            v[r].w += x.w;
-        }
+    const float4* src = reinterpret_cast<const float4*>(p.slots + (static_cast<int64_t>(tile) * TILE + row) * TILE) +
+                        (threadIdx.x & 63);
+    const int64_t next = static_cast<int64_t>(p.w_tiles) * (TILE * TILE / 4);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int32_t i = 0; i < p.w_parts; ++i) {
+        const float4 x = __ldg(src + i * next);
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int32_t e = m * TILE + row + 4 * r;
-        if (e < p.n_experts && h < p.hidden)
-            *reinterpret_cast<uint2*>(d_w + static_cast<int64_t>(e) * p.hidden + h) =
-                make_uint2(pack_16bit2<BF16>(v[r].x * inv, v[r].y * inv), pack_16bit2<BF16>(v[r].z * inv, v[r].w * inv));
-    }
+    *reinterpret_cast<uint2*>(d_w + static_cast<int64_t>(e) * p.hidden + h) =
+        make_uint2(pack_16bit2<BF16>(v.x * inv, v.y * inv), pack_16bit2<BF16>(v.z * inv, v.w * inv));
 }
 
 struct GradLayout {
@@ -271,14 +234,13 @@ int32_t weight_tiles(int32_t n_experts, int32_t hidden) {
     return pairs::ceil_div(n_experts, TILE) * pairs::ceil_div(hidden, TILE);
 }
 
-// Pieces that the steps of d_W are cut into: one a pair, of MIN_PART steps at least, never
-// fewer than there are tiles (or pairs).
+// Parts of a tile of d_W along K: as many as there are pairs for, of MIN_PART steps at least.
 constexpr int32_t MAX_PAIRS = 76;
-int32_t weight_pieces(int64_t n_tokens, int32_t tiles, int32_t pairs_) {
-    const int64_t steps = static_cast<int64_t>(tiles) * pairs::ceil_div(n_tokens, pairs::BK);
-    int64_t n = steps / MIN_PART;
-    if (n < tiles) n = tiles;
-    return static_cast<int32_t>(n < pairs_ ? n : pairs_);
+int32_t weight_parts(int64_t n_tokens, int32_t tiles, int32_t pairs_) {
+    int64_t n = pairs_ / tiles;
+    const int64_t most = pairs::ceil_div(n_tokens, pairs::BK) / MIN_PART;
+    if (n > most) n = most;
+    return n > 1 ? static_cast<int32_t>(n) : 1;
 }
 
 GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
@@ -297,7 +259,8 @@ GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
     l.block_dirty = take(int64_t{4} * router_grad_blocks(n_tokens));
     l.valid = take((n_tokens + 63) / 64 * 8);
     const int32_t tiles = weight_tiles(n_experts, hidden);
-    l.slots = take(static_cast<int64_t>(weight_pieces(n_tokens, tiles, MAX_PAIRS) + tiles) * TILE * TILE * 4);
+    const int32_t parts = weight_parts(n_tokens, tiles, MAX_PAIRS);
+    l.slots = take(parts > 1 ? static_cast<int64_t>(parts) * tiles * TILE * TILE * 4 : 0);
     l.bytes = at;
     return l;
 }
@@ -323,20 +286,30 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     p.n_tokens = T;
     p.n_experts = E;
     p.hidden = H;
-    p.x_tiles_n = pairs::ceil_div(H, TILE);
+    p.tiles_n = pairs::ceil_div(H, TILE);
     p.w_tiles = weight_tiles(E, H);
     p.w_steps = pairs::ceil_div(T, pairs::BK);
-    p.w_pairs = weight_pieces(T, p.w_tiles, n_pairs);
-    const int64_t all = static_cast<int64_t>(p.w_tiles) * p.w_steps;
-    p.w_parts = static_cast<int32_t>((all + p.w_pairs - 1) / p.w_pairs + p.w_steps - 2) / p.w_steps + 1;
-    p.x_tiles = pairs::ceil_div(T, TILE) * p.x_tiles_n;
+    p.w_parts = weight_parts(T, p.w_tiles, n_pairs);
+    p.x_tiles = pairs::ceil_div(T, TILE) * p.tiles_n;
     // as many pairs as there is work for: a part or a tile each
-    const int32_t items = p.w_pairs + p.x_tiles;
+    const int32_t pieces = p.w_tiles * p.w_parts, items = pieces + p.x_tiles;
     p.n_pairs = items < n_pairs ? items : n_pairs;
-    p.x_rounds = (p.x_tiles + p.n_pairs - 1) / p.n_pairs;
-    p.total_tiles = p.n_pairs * (p.w_parts + p.x_rounds);
+    p.w_items = (pieces + p.n_pairs - 1) / p.n_pairs;
+    // pairs with one part less do more tiles of d_x meanwhile (us: a step of a part 0.36; a tile of d_x its
+    // steps and 0.4, its stores 1.7)
+    const int32_t free_pairs = p.w_items * p.n_pairs - pieces;
+    const float part = 0.36f * static_cast<float>(p.w_steps) / static_cast<float>(p.w_parts);
+    const float x_mma = 0.36f * static_cast<float>(pairs::ceil_div(E, pairs::BK)) + 0.4f;
+    p.x_lead = free_pairs > 0 ? static_cast<int32_t>(part / (x_mma > 1.7f ? x_mma : 1.7f)) : 0;
+    int64_t rest = p.x_tiles - static_cast<int64_t>(p.x_lead) * free_pairs;
+    if (rest < 0) {
+        p.x_lead = (p.x_tiles + free_pairs - 1) / free_pairs;
+        rest = 0;
+    }
+    p.x_items = static_cast<int32_t>((rest + p.n_pairs - 1) / p.n_pairs);
+    p.total_tiles = p.n_pairs * (p.w_items + p.x_items + p.x_lead);
     p.d_x = a.d_x;
-    p.d_w = p.w_pairs == p.w_tiles ? a.d_router_w : nullptr;
+    p.d_w = p.w_parts == 1 ? a.d_router_w : nullptr;
     p.slots = slots;
     p.scale = g.scale;
     p.valid = g.valid;
@@ -348,7 +321,7 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles) * 16);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles) * 64);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = attr;
