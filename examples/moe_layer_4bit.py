@@ -1,10 +1,11 @@
 """A mixture-of-experts layer with a shared expert: the shared expert trained in 16
-bits, then the whole layer served in 4 bits.
+bits, the router trained to spread its tokens over the experts, then the whole layer served in 4 bits.
 
     y[t] = Σ_j w[t, j]·expert[id[t, j]](x[t])  +  shared(x[t])
 
 Every step is a call of the library: routing, tables and packing as in 16 bits;
-gated_ffn and gated_ffn_backward for the shared expert; mx4_quantize for weights
+gated_ffn and gated_ffn_backward for the shared expert, router_balance and router_backward
+for the router, orthogonalize for both's updates; mx4_quantize for weights
 and activations, mx4_gate_up and mx4_down for the experts (the shared expert is
 the same two calls with one expert).
 
@@ -53,8 +54,13 @@ class SharedExpert:
         return moe.gated_ffn_backward(d_out, x, *self.weights(), s["gate"], s["up"], s["up_logits"])
 
 
-def train_shared_expert(expert, teacher, hidden, steps=20, tokens=512, lr=0.2, seed=1234):
-    """Plain gradient descent on ‖expert(x) − teacher(x)‖² / 2 per token; the losses."""
+def orthogonal_step(master, grad, lr):
+    """master −= lr · √max(1, rows/cols) · orthogonalised grad: an update whose singular values are alike."""
+    master.add_(moe.orthogonalize(grad).float(), alpha=-lr * max(1.0, master.shape[-2] / master.shape[-1]) ** 0.5)
+
+
+def train_shared_expert(expert, teacher, hidden, steps=20, tokens=512, lr=0.2, seed=1234, orthogonal=False):
+    """Gradient descent on ‖expert(x) − teacher(x)‖² / 2 per token, plain or with orthogonalised updates; the losses."""
     dt, dev = expert.gate_w.dtype, expert.gate_w.device
     g = torch.Generator(device=dev)
     g.manual_seed(seed)
@@ -66,9 +72,35 @@ def train_shared_expert(expert, teacher, hidden, steps=20, tokens=512, lr=0.2, s
         losses.append(float(d_out.square().sum()) / (2 * tokens))
         _, *grads = expert.backward(d_out.to(dt))
         for m, d in zip(master, grads):
-            m.add_(d.float(), alpha=-lr / tokens)
+            if orthogonal:
+                orthogonal_step(m, d, lr)
+            else:
+                m.add_(d.float(), alpha=-lr / tokens)
         expert.gate_w, expert.up_w, expert.down_w = (m.to(dt) for m in master)
     return losses
+
+
+def balance_step(x, router_w, top_k, balance_weight=1.0, z_weight=1e-3, scale=1024.0, **sequences):
+    """The router's losses, its counts per sequence and expert, and the gradient of its weights from
+    balance_weight · balance loss + z_weight · z loss.  ``scale``: of the gradients while they are
+    16-bit; ``sequences``: token_mask and seq_offsets where x holds packed or padded sequences."""
+    logits = torch.empty((x.shape[0], router_w.shape[0]), dtype=torch.float32, device=x.device)
+    ids, _ = moe.router_topk(x, router_w, top_k, logits=logits)
+    losses, counts, tokens = moe.router_balance(logits, ids, **sequences)
+    d_losses = torch.tensor([balance_weight * scale, z_weight * scale], device=x.device)
+    _, d_w = moe.router_backward(x, router_w, logits, ids, d_losses=d_losses, counts=counts, seq_tokens=tokens, **sequences)
+    return losses, counts, d_w.float() / scale
+
+
+def train_router(layer, x, steps=20, lr=0.02):
+    """Spreads the tokens of x over the layer's experts; (balance loss, z loss) of every step."""
+    master, seen = layer.router_w.float(), []
+    for _ in range(steps):
+        losses, _, d_w = balance_step(x, layer.router_w, layer.top_k)
+        seen.append(losses)
+        orthogonal_step(master, d_w, lr)
+        layer.router_w = master.half()
+    return torch.stack(seen).tolist()
 
 
 def route(x, router_w, top_k):
@@ -164,6 +196,9 @@ def main():
     teacher = SharedExpert(hidden, layer.shared.gate_w.shape[0], torch.float16, layer.device, seed=9)
     losses = train_shared_expert(layer.shared, teacher, hidden)
     print(f"shared expert: loss {losses[0]:.1f} -> {losses[-1]:.1f} in {len(losses)} steps")
+    x = torch.randn((4096, hidden), device=layer.device).half() + 0.1 * layer.router_w[:4].sum(0)
+    losses = train_router(layer, x)
+    print(f"router: balance loss {losses[0][0]:.3f} -> {losses[-1][0]:.3f} in {len(losses)} steps (1 is even)")
     layer.quantize()
     for tokens in (1, 64, 4096):
         x = torch.randn((tokens, hidden), device=layer.device).half()

@@ -746,6 +746,15 @@ def mx4_down(h, h_scales, down, down_scales, routed_expert_weights, group_sizes,
     return out
 
 
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, where the kernels run."""
+    import torch
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != d:
+            raise ValueError(f"tensors must be on the current device, cuda:{d}; one is on {t.device}")
+
+
 def _routing(logits, topk_ids, token_mask, seq_offsets):
     """Checked sizes (T, E, k, sequences) of what the router's losses and gradients read."""
     import torch
@@ -791,6 +800,9 @@ def router_balance(logits, topk_ids, token_mask=None, seq_offsets=None, losses=N
     router_balance_workspace_bytes(T, E, S) bytes."""
     import torch
     T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets)
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("router_balance records no autograd graph, but logits requires grad: call it under "
+                           "torch.no_grad() and take the gradients from router_backward")
     dev = logits.device
     outs = []
     for t, name, dt, shape in ((losses, "losses", torch.float32, (2,)), (counts, "counts", torch.int32, (S, E)),
@@ -802,6 +814,7 @@ def router_balance(logits, topk_ids, token_mask=None, seq_offsets=None, losses=N
             _shaped(t, name, dt, shape)
         outs.append(t)
     workspace = _workspace(workspace, router_balance_workspace_bytes(T, E, S), dev, stream)
+    _here(logits, topk_ids, token_mask, seq_offsets, workspace, *outs)
     _check(lib().moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, _ptr(token_mask), _ptr(seq_offsets),
                                     S, *[t.data_ptr() for t in outs], workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
@@ -853,6 +866,8 @@ def router_backward(x_tokens, router_w, logits, topk_ids, d_topk_weights=None, d
             _shaped(t, name, dt, like.shape)
         grads.append(t)
     workspace = _workspace(workspace, router_backward_workspace_bytes(T, E, H), logits.device, stream)
+    _here(x_tokens, router_w, logits, topk_ids, d_topk_weights, d_losses, counts, seq_tokens, token_mask, seq_offsets,
+          d_logits, workspace, *grads)
     _check(lib().moe_router_backward(code, x_tokens.data_ptr(), T, H, router_w.data_ptr(), E, logits.data_ptr(),
                                      topk_ids.data_ptr(), k, _ptr(d_topk_weights), _ptr(d_losses), _ptr(counts),
                                      _ptr(seq_tokens), _ptr(token_mask), _ptr(seq_offsets), S, workspace.data_ptr(),
@@ -885,6 +900,9 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     batch = shape[0] if len(shape) == 3 else 1
     if rows == 0 or cols == 0:
         raise ValueError(f"update must have rows and columns, got {tuple(shape)}")
+    if update.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("orthogonalize records no autograd graph, but update requires grad: call it under "
+                           "torch.no_grad()")
     a, b, c = (float(v) for v in coefficients)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=update.device)
@@ -892,6 +910,7 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     else:
         _shaped(out, "out", torch.bfloat16, shape)
     workspace = _workspace(workspace, orthogonalize_workspace_bytes(batch, rows, cols), update.device, stream)
+    _here(update, out, workspace)
     _check(lib().moe_orthogonalize(code, update.data_ptr(), batch, rows, cols, int(steps), a, b, c, float(eps),
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
                                    _status(status), _stream(stream)), "moe_orthogonalize")

@@ -63,6 +63,8 @@ constexpr float B_SCALE = 64.0f;
 constexpr float LO_SCALE = 8192.0f;         // lo = (x - hi)·2^13
 constexpr float MAX_A_SCALE = 1024.0f;      // of A, less where s is large
 constexpr int SUM_THREADS = 256;
+constexpr int SUM_VALUES = 8192;            // that a block sums at least
+constexpr int MAX_SUM_BLOCKS = 512;         // of one matrix
 
 // ---------------------------------------------------------------------------
 // norms, and X₀
@@ -777,11 +779,9 @@ OrthoLayout ortho_layout(int64_t batch, int32_t rows, int32_t cols) {
     l.ld_x = (l.N + 7) / 8 * 8;
     l.ld_a = (l.M + 7) / 8 * 8;
     l.ld_lo = (l.N + 15) / 16 * 16;
-    // about eight blocks an SM over the stack, of at least 16 values a thread
-    int64_t blocks = (static_cast<int64_t>(rows) * cols + SUM_THREADS * 16 - 1) / (SUM_THREADS * 16);
-    const int64_t most = batch > 0 ? (8 * 152 + batch - 1) / batch : 1;
-    if (blocks > most) blocks = most;
-    l.sum_blocks = static_cast<int32_t>(blocks);
+    // by the matrix alone, so that its norm is summed the same way in any stack
+    const int64_t blocks = (static_cast<int64_t>(rows) * cols + SUM_VALUES - 1) / SUM_VALUES;
+    l.sum_blocks = static_cast<int32_t>(blocks < MAX_SUM_BLOCKS ? blocks : MAX_SUM_BLOCKS);
     int64_t at = 0;
     auto take = [&at](int64_t n) {
         const int64_t r = at;
@@ -827,7 +827,7 @@ cudaError_t launch_prepare(const Prepare& p, int64_t batch, bool tall, cudaStrea
                           ? launch_pdl(square_sum_kernel<DTYPE, true>, sum_grid, SUM_THREADS, stream, p)
                           : launch_pdl(square_sum_kernel<DTYPE, false>, sum_grid, SUM_THREADS, stream, p);
     if (err != cudaSuccess) return err;
-    // as many blocks as for the sums: about eight an SM over the stack
+    // as many blocks as for the sums
     const bool rows8 = (tall ? p.M : p.N) % 8 == 0;
     if (tall)
         return rows8 ? launch_pdl(prepare_tall_kernel<DTYPE, true>, sum_grid, SUM_THREADS, stream, p)

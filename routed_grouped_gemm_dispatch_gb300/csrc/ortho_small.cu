@@ -138,28 +138,52 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     const void* g = static_cast<const uint8_t*>(p.update) + matrix * elements * (DTYPE == MOE_DTYPE_F32 ? 4 : 2);
     const int c0 = static_cast<int>(rank) * p.cols;
     const int n_cols = p.N - c0 < 0 ? 0 : (p.N - c0 < p.cols ? p.N - c0 : p.cols);
-    auto at = [&](int m, int n) {
-        return p.tall ? value_at<DTYPE>(g, static_cast<int64_t>(c0 + n) * p.M + m)
-                      : value_at<DTYPE>(g, static_cast<int64_t>(m) * p.N + c0 + n);
-    };
+    // read once: the values as they are wait in TMEM for the norm
+    const bool whole = !p.tall && (p.N & 7) == 0;         // rows of whole 16-byte pieces
     float sum = 0.0f;
-    if (p.tall) {
-        // contiguous
-        const int64_t first = static_cast<int64_t>(c0) * p.M;
-#pragma unroll 8
-        for (int i = tid; i < n_cols * p.M; i += THREADS) {
-            const float v = value_at<DTYPE>(g, first + i);
-            sum += v * v;
-        }
-    } else {
-        for (int m = warp; m < p.M; m += THREADS / 32) {
-#pragma unroll 4
-            for (int n = lane; n < n_cols; n += 32) {
-                const float v = at(m, n);
-                sum += v * v;
+    for (int col = half * 32; col < p.cols; col += 64) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        if (row < p.M && col < n_cols) {
+            if (whole) {
+                const int64_t first = static_cast<int64_t>(row) * p.N + c0 + col;
+                constexpr int PER = DTYPE == MOE_DTYPE_F32 ? 4 : 8;
+#pragma unroll
+                for (int k = 0; k < 32 / PER; ++k) {
+                    if (col + k * PER >= n_cols) break;
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const uint8_t*>(g) + (first + k * PER) * (DTYPE == MOE_DTYPE_F32 ? 4 : 2)));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (DTYPE == MOE_DTYPE_F32) {
+                            v[4 * k + j] = __uint_as_float(u[j]);
+                        } else {
+                            const float2 f = unpack_16bit2<DTYPE == MOE_DTYPE_BF16>(u[j]);
+                            v[8 * k + 2 * j] = f.x;
+                            v[8 * k + 2 * j + 1] = f.y;
+                        }
+                    }
+                }
+            } else {
+                // (tall: lanes have neighbouring values)
+                const int64_t first = p.tall ? static_cast<int64_t>(c0 + col) * p.M + row : static_cast<int64_t>(row) * p.N + c0 + col;
+                const int64_t step = p.tall ? p.M : 1;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (col + i < n_cols) v[i] = value_at<DTYPE>(g, first + i * step);
             }
         }
+        uint32_t t[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            sum += v[i] * v[i];
+            t[i] = __float_as_uint(v[i]);
+        }
+        tmem_st_32x32b_x32(taddr + TMEM_X + col, t);
     }
+    tmem_st_wait();
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) part[warp] = sum;
@@ -184,6 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     // enters both terms, whose slopes near 1 have opposite signs.)
     auto keep = [&](int col, const float (&v)[32], bool for_last) {
         uint32_t t[32];
+        MOE_DCHECK(col >= 0 && col + 32 <= p.cols && p.cols <= MAX_COLS && matrix < p.batch, p.status);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -200,11 +225,14 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         tmem_st_32x32b_x32(taddr + TMEM_X + col, t);
     };
     for (int col = half * 32; col < p.cols; col += 64) {
+        uint32_t t[32];
+        tmem_ld_32x32b_x32(taddr + TMEM_X + col, t);
+        tmem_ld_wait();
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             // (a small value times a large factor: in two steps, as the factor alone may be infinite)
-            const float x = row < p.M && col + i < n_cols ? at(row, col + i) : 0.0f;
+            const float x = __uint_as_float(t[i]);
             v[i] = norm < 1e-30f ? (norm > 0.0f ? x / norm * X_SCALE : 0.0f) : x * to_x;
         }
         keep(col, v, p.steps == 1);
@@ -245,6 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         // ---- its rows to the CTAs that add them up
         {
             const uint32_t owner = static_cast<uint32_t>(row / own);
+            MOE_DCHECK(owner < C && (static_cast<int>(rank) * own + row % own) * ROWS * 4 < ROWS * ROWS * 4, p.status);
             const uint32_t to = mapa_shared(smem_u32(ex), owner) +
                                 4u * static_cast<uint32_t>((static_cast<int>(rank) * own + row % own) * ROWS);
 #pragma unroll
@@ -267,6 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         for (int i = tid; i < own * (ROWS / 8); i += THREADS) {
             const int r = i / (ROWS / 8), col = i % (ROWS / 8) * 8;
             const int m = static_cast<int>(rank) * own + r;
+            MOE_DCHECK(m < ROWS && piece_at(m, col) + 16 <= AB_BYTES, p.status);
             float s[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = 0.0f;

@@ -67,7 +67,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// The row becomes its softmax; returns its logsumexp.  An exponential is 2^(z log2 e - top log2 e), the
+// The row becomes its softmax; returns its logsumexp.  (A row of minus infinities has no probability anywhere: all
+// zeros, and 0.)  An exponential is 2^(z log2 e - top log2 e), the
 // difference rounded once more and ex2.approx (2^-22): its rounding is an absolute error of the exponent, so the
 // relative error grows with the distance from the row's maximum, by 2^-24 of it.
 template <int L, int PER>
@@ -78,6 +79,7 @@ __device__ __forceinline__ float softmax_row(float (&z)[PER]) {
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     constexpr float LOG2E = 1.4426950408889634f;
+    if (top == -INFINITY) top = 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -85,10 +87,10 @@ __device__ __forceinline__ float softmax_row(float (&z)[PER]) {
         sum += z[i];
     }
     sum = lanes_sum<L>(sum);
-    const float inv = 1.0f / sum;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;            // (NaN stays NaN)
 #pragma unroll
     for (int i = 0; i < PER; ++i) z[i] *= inv;
-    return top + logf(sum);
+    return sum != 0.0f ? top + logf(sum) : 0.0f;
 }
 
 // Sequence bounds, held inside [0, n_tokens] whatever the array says.

@@ -206,3 +206,29 @@ def test_captured_and_on_two_streams():
         other = moe.orthogonalize(b, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(other, want)
+
+
+def test_large_calls_at_once():
+    """Two calls that each fill the device, on two streams: tiles go to whatever pairs run."""
+    a, b = draw("normal", 4, 600, 1544, torch.bfloat16, 1), draw("normal", 1, 1408, 768, torch.float32, 2)
+    c = draw("normal", 8, 100, 900, torch.float16, 3)
+    want = [moe.orthogonalize(v) for v in (a, b, c)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        got = [moe.orthogonalize(v, stream=s) for v, s in zip((a, b, c), streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_past_31_bits():
+    """A stack of more than 2^31 elements: the last matrix is what it is alone."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    u = torch.zeros((1100, 1024, 2048), dtype=torch.bfloat16, device="cuda")
+    last = draw("normal", 1, 1024, 2048, torch.bfloat16, 4)
+    u[-1], u[7] = last[0], last[0]
+    y = moe.orthogonalize(u, steps=2)
+    alone = moe.orthogonalize(last, steps=2)[0]
+    assert torch.equal(y[-1], alone) and torch.equal(y[7], alone)
+    assert not y[6].any() and not y[-2].any()

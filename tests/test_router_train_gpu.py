@@ -40,9 +40,17 @@ def sequences(s):
 
 
 def softmax(z):
-    top = z.max(axis=1, keepdims=True)
+    """And the logsumexp; of a row of minus infinities zeros."""
+    none = np.isneginf(z).all(axis=1, keepdims=True)
+    top = np.where(none, 0.0, z.max(axis=1, keepdims=True))
     e = np.exp(z - top)
-    return e / e.sum(axis=1, keepdims=True), (top + np.log(e.sum(axis=1, keepdims=True)))[:, 0]
+    total = np.where(none, 1.0, e.sum(axis=1, keepdims=True))
+    return e / total, np.where(none, 0.0, top + np.log(total))[:, 0]
+
+
+def finite_top(z):
+    top = z.max(axis=1)
+    return np.where(np.isneginf(top), 0.0, top)
 
 
 def reference(s):
@@ -62,7 +70,7 @@ def reference(s):
         bal += (counts[i] * p.sum(axis=0)).sum() / len(r)
         zl += (lse ** 2).sum()
         # lse: the maximum and a logarithm of a sum that is off by P_REL, each rounded
-        z_tol += (2 * np.abs(lse) * (P_REL + 4 * U * (np.abs(lse) + np.abs(z[r].max(axis=1)) + np.log(E)))).sum() + 64 * U * (lse ** 2).sum()
+        z_tol += (2 * np.abs(lse) * (P_REL + 4 * U * (np.abs(lse) + np.abs(finite_top(z[r])) + np.log(E)))).sum() + 64 * U * (lse ** 2).sum()
     m = max(n, 1)
     losses = np.array([bal * E / (k * m), zl / m])
     # sums over a warp's tokens and a block's warps in fp32, at most 64 additions at these sizes
@@ -126,7 +134,7 @@ def grads_reference(s, dw, dl, counts, tokens):
         zt = np.reshape(zt, (-1, 1)) if np.ndim(zt) else np.full((len(r), 1), zt)
         dz[r] = p * (g - dot + zt)
         size = mag + (p * mag).sum(axis=1, keepdims=True) + np.abs(zt)
-        lse_err = np.abs(zt) * (P_REL + 8 * U * (np.abs(z[r].max(axis=1)) + np.abs(lse) + np.log(E)))[:, None] / np.maximum(np.abs(lse), 1e-30)[:, None]
+        lse_err = np.abs(zt) * (P_REL + 8 * U * (np.abs(finite_top(z[r])) + np.abs(lse) + np.log(E)))[:, None] / np.maximum(np.abs(lse), 1e-30)[:, None]
         tol[r] = p * (2 * P_REL * size + lse_err)
     return dz, tol
 
@@ -216,6 +224,45 @@ def test_what_is_masked_meets_nothing(dtype):
         assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got_g, clean_g))
         assert torch.equal(got_g[0][out], torch.zeros_like(got_g[0][out]))
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min])
+def test_experts_that_are_masked(low):
+    """Logits of minus infinity, or of the type's lowest value: no probability, no gradient, and the others as they are."""
+    T, E, k, H = 130, 72, 4, 136
+    s = make(T, E, k, seed=21)
+    s["z"][:, ::3] = low
+    s["z"][5] = low                                      # none left, or with the lowest value one
+    if low != float("-inf"):
+        s["z"][5, 1] = 0.3
+    s["ids"] = torch.topk(s["z"], k, dim=1).indices.to(torch.int32)
+    s["ids"][5, 1:] = -1
+    x, w = torch.randn((T, H), device="cuda").half(), torch.randn((E, H), device="cuda").half()
+    dw, dl = torch.randn((T, k), device="cuda"), torch.tensor([1.0, 0.1], device="cuda")
+    losses, counts, tokens = moe.router_balance(s["z"], s["ids"])
+    want, c, n, tol = reference(s)
+    assert np.array_equal(counts.cpu().numpy(), c) and np.all(np.abs(losses.double().cpu().numpy() - want) <= tol)
+    d_z = torch.empty((T, E), device="cuda")
+    got = moe.router_backward(x, w, s["z"], s["ids"], dw, dl, counts, tokens, d_logits=d_z)
+    check_grads(s, x, w, dw, dl, got, d_z, c, n)
+    assert not d_z[:, ::3].any()
+
+
+def test_the_same_expert_twice():
+    """A token that names an expert twice or three times: both pairs count, and both gradients."""
+    T, E, k, H = 90, 20, 5, 64
+    s = make(T, E, k, seed=8)
+    s["ids"][:, 2] = s["ids"][:, 0]
+    s["ids"][::4, 4] = s["ids"][::4, 0]
+    x, w = torch.randn((T, H), device="cuda").half(), torch.randn((E, H), device="cuda").half()
+    dw, dl = torch.randn((T, k), device="cuda"), torch.tensor([1.0, 0.1], device="cuda")
+    losses, counts, tokens = moe.router_balance(s["z"], s["ids"])
+    want, c, n, tol = reference(s)
+    assert np.array_equal(counts.cpu().numpy(), c) and np.all(np.abs(losses.double().cpu().numpy() - want) <= tol)
+    got = moe.router_backward(x, w, s["z"], s["ids"], dw, dl, counts, tokens)
+    check_grads(s, x, w, dw, dl, got, None, c, n)
+    again = moe.router_backward(x, w, s["z"], s["ids"], dw, dl, counts, tokens)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, again))
 
 
 @pytest.mark.parametrize("T", [0, 5, 200])

@@ -124,6 +124,7 @@ def test_router_logits_refusals(L):
 def fake(L, monkeypatch):
     """Tensors made inside have a device, a type, sizes and strides, and no memory."""
     monkeypatch.setattr(moe, "_stream", lambda s: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with FakeTensorMode():
         yield lambda *shape, dt=torch.float32: torch.empty(shape, dtype=dt, device="cuda")
 
@@ -220,6 +221,7 @@ def test_allocations_are_recorded(name, n, given, monkeypatch):
     made, recorded, stream = [], [], Stream() if given else None
     monkeypatch.setattr(moe, "lib", lambda lib=NoLibrary(): lib)
     monkeypatch.setattr(moe, "_stream", lambda s: 0 if s is None else s.cuda_stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with FakeTensorMode(), warnings.catch_warnings():
         warnings.simplefilter("ignore")
         z, ids = torch.empty((4, 8), device="cuda"), torch.empty((4, 2), dtype=torch.int32, device="cuda")
@@ -239,3 +241,24 @@ def test_allocations_are_recorded(name, n, given, monkeypatch):
         getattr(moe, name)(*args, stream=stream)
     assert len(made) == n
     assert recorded == ([(id(t), stream) for t in made] if given else [])
+
+
+def test_other_devices_are_refused(fake, monkeypatch):
+    """The kernels run on the current device, whatever device the tensors are on."""
+    z, ids, x, w = fake(4, 8), fake(4, 2, dt=torch.int32), fake(4, 16, dt=torch.float16), fake(8, 16, dt=torch.float16)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: moe.router_balance(z, ids), lambda: moe.router_backward(x, w, z, ids), lambda: moe.orthogonalize(x)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_autograd_is_not_lost_silently(fake):
+    z, ids, u = fake(4, 8).requires_grad_(), fake(4, 2, dt=torch.int32), fake(4, 16).requires_grad_()
+    with pytest.raises(RuntimeError, match="router_backward"):
+        moe.router_balance(z, ids)
+    with pytest.raises(RuntimeError, match="no_grad"):
+        moe.orthogonalize(u)
+    with torch.no_grad(), pytest.raises(ValueError, match="losses must have shape"):
+        moe.router_balance(z, ids, losses=fake(3))
+    with torch.no_grad(), pytest.raises(TypeError, match="out must be"):
+        moe.orthogonalize(u, out=fake(4, 16))
