@@ -12,7 +12,10 @@
 //
 // One step takes about 6 us (64 x 2048) against 19 us of the tiles in L2.  Bound: the chain of
 // three products, two exchanges and three passes over registers, with one warp's latency
-// in each.  Roundings: the products' operands (fp16) and the result (bf16); a·X is fp32.
+// in each.  Roundings: X as an operand (fp16) and the result (bf16); a·X is fp32, and A and B are each the
+// sum of two fp16 matrices: with few rows there are few singular values, whose errors do not
+// average out, and a single B was most of it (20 x 2000: 2.4e-3 of the result, with two terms of A and B
+// 0.8e-3; the result's rounding by itself is 1.7e-3).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,10 +46,10 @@ constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 // All that an SM has, whatever is used of it: no other CTA that wants TMEM may be beside this one, as
 // two clusters that hold it on one SM each and wait for it on the other would wait for ever.
 constexpr int SMEM_BYTES = 225 * 1024;
-static_assert(1024 + 384 / 64 * 128 * 128 + 2 * 128 * 128 + 128 * 128 * 4 <= SMEM_BYTES, "the widest part fits");
+static_assert(1024 + 384 / 64 * 128 * 128 + 2 * 2 * 128 * 128 + 128 * 128 * 4 <= SMEM_BYTES, "the widest part fits");
 
 constexpr int BOX_BYTES = ROWS * 128;         // 64 columns of 128 rows, 128-byte swizzle
-constexpr int AB_BYTES = 2 * BOX_BYTES;
+constexpr int AB_BYTES = 2 * BOX_BYTES;       // of one term
 constexpr int TMEM_A = 0, TMEM_X = 128, TMEM_COLS = 512;
 
 struct Small {
@@ -84,6 +87,13 @@ __device__ __forceinline__ uint32_t piece_at(int row, int col) {
     return static_cast<uint32_t>((col >> 6) * BOX_BYTES + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) * 16));
 }
 
+// Two values as the sum of two fp16 pairs: their rounding, and that of what it left.
+__device__ __forceinline__ void two_terms(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_16bit2<false>(x, y);
+    const float2 f = unpack_16bit2<false>(hi);
+    lo = pack_16bit2<false>(x - f.x, y - f.y);
+}
+
 template <int DTYPE>
 __device__ __forceinline__ float value_at(const void* base, int64_t i) {
     if (DTYPE == MOE_DTYPE_F32) return __ldg(static_cast<const float*>(base) + i);
@@ -104,8 +114,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     __shared__ float sums[MAX_CLUSTER];
     const int x_bytes = p.cols / 64 * BOX_BYTES;
     uint8_t* xs = smem;                                   // hi
-    uint8_t* as = smem + x_bytes;                         // A, then B
-    uint8_t* ex = as + AB_BYTES;                          // [C][ROWS / C][ROWS] fp32: parts of this CTA's rows of A
+    uint8_t* as = smem + x_bytes;                         // A, then B: its rounding, and what that left
+    uint8_t* ex = as + 2 * AB_BYTES;                          // [C][ROWS / C][ROWS] fp32: parts of this CTA's rows of A
     const uint32_t bar = smem_u32(&bar_mem);
     volatile int* abort_flag = &abort_mem;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -314,14 +324,18 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
                     s[7] += hi.w;
                 }
             }
-            uint32_t w[4];
+            uint32_t w[4], l[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 constexpr float F = A_SCALE / (X_SCALE * X_SCALE);
-                w[j] = pack_16bit2<false>(s[2 * j] * F, s[2 * j + 1] * F);
+                two_terms(s[2 * j] * F, s[2 * j + 1] * F, w[j], l[j]);
             }
             const uint32_t off = smem_u32(as) + piece_at(m, col);
-            for (uint32_t q = 0; q < C; ++q) store_cluster4(mapa_shared(off, (rank + q) % C), w[0], w[1], w[2], w[3]);
+            for (uint32_t q = 0; q < C; ++q) {
+                const uint32_t to = mapa_shared(off, (rank + q) % C);
+                store_cluster4(to, w[0], w[1], w[2], w[3]);
+                store_cluster4(to + AB_BYTES, l[0], l[1], l[2], l[3]);
+            }
         }
         __syncwarp();
         cluster_sync_all();
@@ -330,8 +344,11 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         if (tid == 0) {
             const uint32_t idesc = idesc_16bit_f32acc(ROWS, n_a, false, false, false);
             for (int k = 0; k < m16 / 16; ++k) {
-                const uint64_t d = smem_desc_k_sw128(ab + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
-                tc_mma_f16(tmem + TMEM_A, d, d, idesc, k > 0 ? 1u : 0u);
+                const uint64_t hi = smem_desc_k_sw128(ab + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
+                const uint64_t lo = smem_desc_k_sw128(ab + AB_BYTES + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
+                tc_mma_f16(tmem + TMEM_A, hi, hi, idesc, k > 0 ? 1u : 0u);
+                tc_mma_f16(tmem + TMEM_A, hi, lo, idesc, 1u);
+                tc_mma_f16(tmem + TMEM_A, lo, hi, idesc, 1u);
             }
             tc_commit(bar);
         }
@@ -348,17 +365,20 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint4* piece = reinterpret_cast<uint4*>(as + piece_at(row, col + 8 * k));
-                const uint4 old = *piece;
+                uint4* rest = reinterpret_cast<uint4*>(as + AB_BYTES + piece_at(row, col + 8 * k));
+                const uint4 old = *piece, old_rest = *rest;
                 const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
-                uint32_t w[4];
+                const uint32_t ol[4] = {old_rest.x, old_rest.y, old_rest.z, old_rest.w};
+                uint32_t w[4], l[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack_16bit2<false>(ow[j]);
+                    const float2 f = unpack_16bit2<false>(ow[j]), e = unpack_16bit2<false>(ol[j]);
                     const float sq = p.c * (B_SCALE / (A_SCALE * A_SCALE)), lin = p.b * (B_SCALE / A_SCALE);
-                    w[j] = pack_16bit2<false>(lin * f.x + sq * __uint_as_float(v[8 * k + 2 * j]),
-                                              lin * f.y + sq * __uint_as_float(v[8 * k + 2 * j + 1]));
+                    two_terms(lin * (f.x + e.x) + sq * __uint_as_float(v[8 * k + 2 * j]),
+                              lin * (f.y + e.y) + sq * __uint_as_float(v[8 * k + 2 * j + 1]), w[j], l[j]);
                 }
                 *piece = make_uint4(w[0], w[1], w[2], w[3]);
+                *rest = make_uint4(l[0], l[1], l[2], l[3]);
             }
         }
         hand_over();
@@ -366,9 +386,13 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         if (tid == 0) {
             const uint32_t idesc = idesc_16bit_f32acc(ROWS, 64, false, false, true);
             for (int box = 0; box < p.cols / 64; ++box)
-                for (int k = 0; k < m16 / 16; ++k)
-                    tc_mma_f16(tmem + TMEM_X + box * 64, smem_desc_k_sw128(ab + (k >> 2) * BOX_BYTES) + (k & 3) * 2,
-                               smem_desc_mn_sw128(xb + box * BOX_BYTES, BOX_BYTES) + k * (2048 >> 4), idesc, 1u);
+                for (int k = 0; k < m16 / 16; ++k) {
+                    const uint64_t x = smem_desc_mn_sw128(xb + box * BOX_BYTES, BOX_BYTES) + k * (2048 >> 4);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+                        tc_mma_f16(tmem + TMEM_X + box * 64,
+                                   smem_desc_k_sw128(ab + term * AB_BYTES + (k >> 2) * BOX_BYTES) + (k & 3) * 2, x, idesc, 1u);
+                }
             tc_commit(bar);
         }
         __syncwarp();

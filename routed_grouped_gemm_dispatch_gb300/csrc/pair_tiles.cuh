@@ -73,13 +73,15 @@ struct Maps {
 };
 
 // What a tile multiplies: rows a_row .. + 255 of A by rows b_row .. + width - 1 of B
-// (coordinates in their own arrays), K steps k0 .. k0 + steps of 64.
+// (coordinates in their own arrays), K steps k0 .. k0 + steps of 64; with two terms, each step twice,
+// by A's next matrix the second time (`steps` counts both).
 struct Tile {
     int32_t a_map, b_map;
     bool a_mn, b_mn;
     int32_t a_row, b_row, batch;
     int32_t k0, steps;
     int32_t width;                 // 128 or 256 columns
+    int32_t two;                   // 1: two terms
 };
 
 template <int BN>
@@ -243,14 +245,15 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
                 const uint32_t fb = full0 + 8 * stage;
                 const uint32_t sa = sbase + stage * L::STAGE_BYTES;
                 const uint32_t sb = sa + A_BYTES;
-                const int32_t k = (ti.k0 + st) * BK;
+                const int32_t k = (ti.k0 + (st >> ti.two)) * BK;
+                const int32_t a_batch = ti.batch + (st & ti.two);
                 mbar_arrive_expect_tx_if(expect, bar_full + 8 * stage, bytes);
                 if (ti.a_mn) {
 #pragma unroll
                     for (int b = 0; b < BM / 64; ++b)
-                        tma_load_3d_pair_if(issue, sa + b * BOX_BYTES, am, fb, arow + b * 64, k, ti.batch, policy);
+                        tma_load_3d_pair_if(issue, sa + b * BOX_BYTES, am, fb, arow + b * 64, k, a_batch, policy);
                 } else {
-                    tma_load_3d_pair_if(issue, sa, am, fb, k, arow, ti.batch, policy);
+                    tma_load_3d_pair_if(issue, sa, am, fb, k, arow, a_batch, policy);
                 }
                 if (ti.b_mn) {
                     tma_load_3d_pair_if(issue, sb, bm, fb, brow, k, ti.batch, policy);
@@ -284,7 +287,7 @@ pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ typename 
             for (int32_t st = 0; st < ti.steps; ++st) {
                 uint32_t n0 = 0xffffffffu, n1 = 0xffffffffu;
                 if constexpr (Op::MASKABLE) {
-                    if (masked && st + 1 < ti.steps && Op::maskable(ti)) Op::valid64(p, ti.k0 + st + 1, n0, n1);
+                    if (masked && st + 1 < ti.steps && Op::maskable(ti)) Op::valid64(p, ti.k0 + ((st + 1) >> ti.two), n0, n1);
                 }
                 if (!mbar_wait_warp(bar_full + 8 * stage, phase, abort_flag, WAIT_LIMIT_NS)) {
                     ok = false;

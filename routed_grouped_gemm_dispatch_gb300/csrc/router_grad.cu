@@ -14,7 +14,12 @@
 //    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
 //    memory first.
 //
-// Rounding: d_z once (an operand of 16-bit products), d_x and d_W once from fp32.
+// Rounding: d_x and d_W once from fp32.  d_z, an operand of 16-bit products, once too where there are many
+// tokens: over thousands of them its roundings add half as much again as that of the result to the
+// mean square (the root mean square error of either output is √2 of a single rounding's, 2.4e-3 in bf16).
+// Over few tokens the same few roundings are in all of an output, so up to TWO_TERM_TOKENS d_z is two
+// 16-bit terms, its rounding and what that left, and every K step is taken with both.  (With two
+// terms throughout the products of 16384 x 256 x 7168 would be bound by the tensor pipe, at 124 us.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -32,6 +37,7 @@ using pairs::Tile;
 
 constexpr int TILE = 256;
 constexpr int MIN_PART = 8;          // K steps of a part of d_W at least
+constexpr int64_t TWO_TERM_TOKENS = 2048;
 
 struct GradProducts {
     int32_t total_tiles, n_maps;
@@ -39,6 +45,7 @@ struct GradProducts {
     int64_t n_tokens;
     int32_t n_experts, hidden;
     int32_t n_pairs;                 // of the launch
+    int32_t two;                     // 1: d_z is two terms
     int32_t tiles_n;                 // column tiles, of both products
     int32_t w_tiles, w_parts;        // tiles of d_W, and parts of each along K
     int32_t w_steps;                 // K steps of a tile
@@ -91,6 +98,7 @@ struct GradOp {
         Tile ti{};
         ti.width = TILE;
         if (c.tile < 0) return ti;
+        ti.two = p.two;
         const int32_t m = c.tile / p.tiles_n;
         ti.a_row = m * TILE;
         ti.b_row = (c.tile - m * p.tiles_n) * TILE;
@@ -99,12 +107,12 @@ struct GradOp {
             ti.b_map = X_T;
             ti.a_mn = ti.b_mn = true;
             ti.k0 = static_cast<int32_t>(static_cast<int64_t>(p.w_steps) * c.part / p.w_parts);
-            ti.steps = static_cast<int32_t>(static_cast<int64_t>(p.w_steps) * (c.part + 1) / p.w_parts) - ti.k0;
+            ti.steps = (static_cast<int32_t>(static_cast<int64_t>(p.w_steps) * (c.part + 1) / p.w_parts) - ti.k0) << p.two;
         } else {
             ti.a_map = DZ;
             ti.b_map = W_T;
             ti.b_mn = true;
-            ti.steps = (p.n_experts + pairs::BK - 1) / pairs::BK;
+            ti.steps = (p.n_experts + pairs::BK - 1) / pairs::BK << p.two;
         }
         return ti;
     }
@@ -252,7 +260,7 @@ GradLayout grad_layout(int64_t n_tokens, int32_t n_experts, int32_t hidden) {
         at += round256(n);
         return r;
     };
-    l.dz = take(n_tokens * l.ld * 2);
+    l.dz = take(n_tokens * l.ld * 2 * (n_tokens <= TWO_TERM_TOKENS ? 2 : 1));
     l.d_logits = take(n_tokens * n_experts * 4);
     l.scale = take(8);
     l.block_max = take(int64_t{4} * router_grad_blocks(n_tokens));
@@ -272,9 +280,10 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     const int64_t T = a.r.n_tokens;
     const int32_t E = a.r.n_experts, H = a.hidden;
     pairs::Maps maps;
-    if (!pairs::map_3d(&maps.m[Op::DZ], g.dz, 1, T, E, g.ld, pairs::BM) ||
+    const int terms = g.two ? 2 : 1;
+    if (!pairs::map_3d(&maps.m[Op::DZ], g.dz, terms, T, E, g.ld, pairs::BM) ||
         !pairs::map_3d(&maps.m[Op::W_T], a.router_w, 1, E, H, H, pairs::BK) ||
-        !pairs::map_3d(&maps.m[Op::DZ_T], g.dz, 1, T, E, g.ld, pairs::BK) ||
+        !pairs::map_3d(&maps.m[Op::DZ_T], g.dz, terms, T, E, g.ld, pairs::BK) ||
         !pairs::map_3d(&maps.m[Op::X_T], a.x, 1, T, H, H, pairs::BK))
         return cudaErrorInvalidValue;
     int n_pairs = pairs::resident_pairs<Op>();
@@ -286,6 +295,7 @@ cudaError_t launch_products(const RouterBackward& a, const LogitGradients& g, fl
     p.n_tokens = T;
     p.n_experts = E;
     p.hidden = H;
+    p.two = g.two ? 1 : 0;
     p.tiles_n = pairs::ceil_div(H, TILE);
     p.w_tiles = weight_tiles(E, H);
     p.w_steps = pairs::ceil_div(T, pairs::BK);
@@ -343,6 +353,7 @@ cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream)
     LogitGradients g;
     g.dz = reinterpret_cast<uint16_t*>(ws + l.dz);
     g.ld = l.ld;
+    g.two = a.r.n_tokens <= TWO_TERM_TOKENS;
     g.d_logits = reinterpret_cast<float*>(ws + l.d_logits);
     g.scale = reinterpret_cast<float*>(ws + l.scale);
     g.block_max = reinterpret_cast<float*>(ws + l.block_max);

@@ -422,6 +422,7 @@ struct GradParams {
     const int32_t* counts;
     const int32_t* seq_tokens;
     uint16_t* dz;                 // [n_tokens, ld], in bf16 by the first pass, in fp16 by the second
+    uint16_t* rest;               // [n_tokens, ld], nullable: what the rounding left
     int32_t ld;
     float* d_logits;              // [n_tokens, E]; nullable in bf16
     float* scale;
@@ -453,6 +454,20 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& v) {
             ((v.w & 0x7fff7fffu) + ONE)) & 0x80008000u;
 }
 
+// Eight values rounded, and what that left.
+template <bool BF16>
+__device__ __forceinline__ void store_eight(uint16_t* at, uint16_t* rest, const float (&v)[8]) {
+    uint32_t w[4], r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = pack_16bit2<BF16>(v[2 * j], v[2 * j + 1]);
+        const float2 f = unpack_16bit2<BF16>(w[j]);
+        r[j] = pack_16bit2<BF16>(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (rest) *reinterpret_cast<uint4*>(rest) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // fp16 operands from fp32 gradients, times the power of two that their largest magnitude asks for: pieces
 // first, first + step, ...
 __device__ __forceinline__ void round_values(const GradParams& p, float largest, int64_t first, int64_t step) {
@@ -476,9 +491,9 @@ __device__ __forceinline__ void round_values(const GradParams& p, float largest,
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = e + j < E ? p.d_logits[t * E + e + j] : 0.0f;
         }
-        *reinterpret_cast<uint4*>(p.dz + 8 * i) =
-            make_uint4(pack_16bit2<false>(v[0] * scale, v[1] * scale), pack_16bit2<false>(v[2] * scale, v[3] * scale),
-                       pack_16bit2<false>(v[4] * scale, v[5] * scale), pack_16bit2<false>(v[6] * scale, v[7] * scale));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= scale;
+        store_eight<false>(p.dz + 8 * i, p.rest ? p.rest + 8 * i : nullptr, v);
     }
 }
 
@@ -591,10 +606,10 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
 #pragma unroll
             for (int i = 0; i < PER; i += 8) {
                 const int e = expert<L, VEC>(l, i);
-                if (BF16 && e < p.ld)                    // (columns E .. ld - 1 are not read)
-                    *reinterpret_cast<uint4*>(p.dz + t * p.ld + e) =
-                        make_uint4(pack_16bit2<true>(d[i], d[i + 1]), pack_16bit2<true>(d[i + 2], d[i + 3]),
-                                   pack_16bit2<true>(d[i + 4], d[i + 5]), pack_16bit2<true>(d[i + 6], d[i + 7]));
+                if (BF16 && e < p.ld) {                  // (columns E .. ld - 1 are not read)
+                    const float v[8] = {d[i], d[i + 1], d[i + 2], d[i + 3], d[i + 4], d[i + 5], d[i + 6], d[i + 7]};
+                    store_eight<true>(p.dz + t * p.ld + e, p.rest ? p.rest + t * p.ld + e : nullptr, v);
+                }
                 if (p.d_logits && e < E)
                     *reinterpret_cast<float4*>(p.d_logits + t * E + e) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
                 if (p.d_logits && e + 4 < E)
@@ -605,7 +620,11 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = expert<L, VEC>(l, i);
-                if (BF16 && e < p.ld) p.dz[t * p.ld + e] = static_cast<uint16_t>(pack_16bit2<true>(d[i], 0.0f) & 0xffffu);
+                if (BF16 && e < p.ld) {
+                    const uint32_t w = pack_16bit2<true>(d[i], 0.0f) & 0xffffu;
+                    p.dz[t * p.ld + e] = static_cast<uint16_t>(w);
+                    if (p.rest) p.rest[t * p.ld + e] = static_cast<uint16_t>(pack_16bit2<true>(d[i] - unpack_16bit2<true>(w).x, 0.0f) & 0xffffu);
+                }
                 if (p.d_logits && e < E) p.d_logits[t * E + e] = d[i];
             }
         }
@@ -779,6 +798,7 @@ cudaError_t launch_logit_gradients(const RouterBackward& a, const LogitGradients
     p.counts = a.counts;
     p.seq_tokens = a.seq_tokens;
     p.dz = g.dz;
+    p.rest = g.two ? g.dz + a.r.n_tokens * g.ld : nullptr;
     p.ld = g.ld;
     p.d_logits = a.d_logits || a.bf16 ? a.d_logits : g.d_logits;
     p.scale = g.scale;

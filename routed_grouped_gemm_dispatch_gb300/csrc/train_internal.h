@@ -56,8 +56,9 @@ cudaError_t launch_router_backward(const RouterBackward& a, cudaStream_t stream)
 // count, a bit per token in `valid` (1: it counts), whole 64-token steps, zero past the end, and per
 // block whether x holds an infinity or a NaN in one that does not; otherwise both are null.
 struct LogitGradients {
-    uint16_t* dz;
+    uint16_t* dz;                 // [n_tokens, ld], and with `two` the same again of what its rounding left
     int32_t ld;
+    bool two;
     float* d_logits;              // [n_tokens, n_experts], fp16 only: d_z where the caller keeps none
     float* scale;                 // [2]
     float* block_max;             // [router_grad_blocks()]

@@ -34,11 +34,15 @@ def iterate(g, steps=5, abc=ABC, eps=1e-7, rounded=False):
             x = a * x + (b * A + c * (A @ A)) @ x
         return x.transpose(1, 2) if tall else x
     if x.shape[1] <= 128 and x.shape[2] <= 6144:
-        # on chip: a·X in 32 bits, but for the last step, which takes X as the products do
+        # on chip: a·X in 32 bits, but for the last step, which takes X as the products do; A and B in two terms
+        def two(v, scale):
+            hi = r16(v, scale)
+            return hi + r16(v - hi, scale)
+
         for k in range(steps):
             hi = r16(x, 64.0)
-            A = r16(hi @ hi.transpose(1, 2), 1024.0)
-            x = a * (hi if k + 1 == steps else x) + r16(b * A + c * (A @ A), 64.0) @ hi
+            A = two(hi @ hi.transpose(1, 2), 1024.0)
+            x = a * (hi if k + 1 == steps else x) + two(b * A + c * (A @ A), 64.0) @ hi
         return (x.transpose(1, 2) if tall else x).bfloat16().double()
     eye = torch.eye(x.shape[1], dtype=x.dtype, device=x.device)
     hi, lo = x, torch.zeros_like(x)

@@ -148,8 +148,10 @@ def check_grads(s, x, w, dw, dl, got, d_logits, counts, tokens):
     if d_logits is not None:
         err = np.abs(d_logits.double().cpu().numpy() - dz)
         assert np.all(err <= tol + 1e-43), (err - tol).max()
-    # the operand: d_z rounded once; below 2^-27 of the largest, fp16 keeps absolute steps
-    dz_tol = tol + (r + 2 * U) * (np.abs(dz) + tol) + np.abs(dz).max(initial=0) * 2.0 ** -38 + 2.0 ** -134
+    # the operand: d_z rounded once, up to 2048 tokens in two terms (each off by half a step); below 2^-27 of the
+    # largest, fp16 keeps absolute steps
+    dz_r = r if len(dz) > 2048 else r * r
+    dz_tol = tol + (dz_r + 2 * U) * (np.abs(dz) + tol) + np.abs(dz).max(initial=0) * 2.0 ** -38 + 2.0 ** -134
     live = np.zeros(len(dz), bool)
     for rows in sequences(s):
         live[rows] = True
@@ -160,7 +162,9 @@ def check_grads(s, x, w, dw, dl, got, d_logits, counts, tokens):
     def acc(k):
         return (k / 16 + 8) * 2.0 ** -23                              # fp32 sums on the tensor cores
 
-    for name, d, a, da, b, k in (("d_x", got[0], dz, dz_tol, wv, dz.shape[1]), ("d_w", got[1], dz.T, dz_tol.T, xv, len(dz))):
+    two = 1 if len(dz) > 2048 else 2             # terms of a sum
+    for name, d, a, da, b, k in (("d_x", got[0], dz, dz_tol, wv, two * dz.shape[1]),
+                                 ("d_w", got[1], dz.T, dz_tol.T, xv, two * len(dz))):
         want = a @ b
         bound = da @ np.abs(b) + acc(k) * (np.abs(a) @ np.abs(b))
         bound += r * (np.abs(want) + bound) + tiny
