@@ -36,21 +36,28 @@ namespace {
 
 constexpr int ROWS = 128;
 constexpr int THREADS = 256;                  // a row of TMEM per thread, columns halved between warps w and w + 4
-constexpr int MAX_COLS = 384;                 // of X per CTA: beside A's 128 in 512 columns of TMEM
+// Columns of X per CTA at most: beside A's (64 or 128) in 512 columns of TMEM.
+__host__ __device__ constexpr int a_columns(int M) { return M <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int max_columns(int M) { return 512 - a_columns(M); }
 constexpr int MAX_CLUSTER = 16;
 constexpr float X_SCALE = 64.0f;              // operands times powers of two, as in ortho.cu
 constexpr float A_SCALE = 1024.0f;
 constexpr float B_SCALE = 64.0f;
+constexpr int BOX_BYTES = ROWS * 128;         // 64 columns of 128 rows, 128-byte swizzle
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 // All that an SM has, whatever is used of it: no other CTA that wants TMEM may be beside this one, as
 // two clusters that hold it on one SM each and wait for it on the other would wait for ever.
 constexpr int SMEM_BYTES = 225 * 1024;
-static_assert(1024 + 384 / 64 * 128 * 128 + 2 * 2 * 128 * 128 + 128 * 128 * 4 <= SMEM_BYTES, "the widest part fits");
+// X, two terms of A, and the parts of A's rows on their way.
+constexpr int shared_bytes(int M, int cols) {
+    return 1024 + cols / 64 * BOX_BYTES + 2 * a_columns(M) / 64 * BOX_BYTES + ROWS * a_columns(M) * 4;
+}
 
-constexpr int BOX_BYTES = ROWS * 128;         // 64 columns of 128 rows, 128-byte swizzle
-constexpr int AB_BYTES = 2 * BOX_BYTES;       // of one term
-constexpr int TMEM_A = 0, TMEM_X = 128, TMEM_COLS = 512;
+constexpr int TMEM_A = 0, TMEM_COLS = 512;
+
+static_assert(shared_bytes(64, max_columns(64)) <= SMEM_BYTES && shared_bytes(128, max_columns(128)) <= SMEM_BYTES,
+              "the widest parts fit");
 
 struct Small {
     const void* update;
@@ -112,10 +119,12 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     __shared__ int abort_mem;
     __shared__ float part[THREADS / 32];
     __shared__ float sums[MAX_CLUSTER];
-    const int x_bytes = p.cols / 64 * BOX_BYTES;
+    const int an = a_columns(p.M);                        // A's rows and columns that there is room for
+    const int x_bytes = p.cols / 64 * BOX_BYTES, a_bytes = an / 64 * BOX_BYTES;
+    const uint32_t TMEM_X = static_cast<uint32_t>(an);
     uint8_t* xs = smem;                                   // hi
     uint8_t* as = smem + x_bytes;                         // A, then B: its rounding, and what that left
-    uint8_t* ex = as + 2 * AB_BYTES;                          // [C][ROWS / C][ROWS] fp32: parts of this CTA's rows of A
+    uint8_t* ex = as + 2 * a_bytes;                       // [C][an / C][an] fp32: parts of this CTA's rows of A
     const uint32_t bar = smem_u32(&bar_mem);
     volatile int* abort_flag = &abort_mem;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -124,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     const uint32_t rank = cluster_cta_rank();
     const int64_t matrix = blockIdx.x / C;
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const int own = ROWS / static_cast<int>(C);           // rows of A that a CTA adds up
+    const int own = an / static_cast<int>(C);             // rows of A that a CTA adds up
 
     if (tid == 0) {
         mbar_init(bar, 1);
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     // enters both terms, whose slopes near 1 have opposite signs.)
     auto keep = [&](int col, const float (&v)[32], bool for_last) {
         uint32_t t[32];
-        MOE_DCHECK(col >= 0 && col + 32 <= p.cols && p.cols <= MAX_COLS && matrix < p.batch, p.status);
+        MOE_DCHECK(col >= 0 && col + 32 <= p.cols && p.cols <= max_columns(p.M) && matrix < p.batch, p.status);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -248,6 +257,12 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         keep(col, v, p.steps == 1);
     }
 
+    // rows of A that no CTA owns stay zero (the products take 128)
+    if (an < ROWS)
+        for (int i = tid; i < 2 * (ROWS - an) * 8; i += THREADS) {
+            const int r = an + (i >> 3) % (ROWS - an), term = (i >> 3) / (ROWS - an);
+            *reinterpret_cast<uint4*>(as + term * a_bytes + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
     uint32_t phase = 0;
     // The MMAs that thread 0 has issued are done.
     auto finished = [&]() {
@@ -282,13 +297,13 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         finished();
         // ---- its rows to the CTAs that add them up
         {
-            const uint32_t owner = static_cast<uint32_t>(row / own);
-            MOE_DCHECK(owner < C && (static_cast<int>(rank) * own + row % own) * ROWS * 4 < ROWS * ROWS * 4, p.status);
+            const uint32_t owner = row < an ? static_cast<uint32_t>(row / own) : 0u;
+            MOE_DCHECK(owner < C && static_cast<int>(rank) * own + row % own < an, p.status);
             const uint32_t to = mapa_shared(smem_u32(ex), owner) +
-                                4u * static_cast<uint32_t>((static_cast<int>(rank) * own + row % own) * ROWS);
+                                4u * static_cast<uint32_t>((static_cast<int>(rank) * own + row % own) * an);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int col = half * 64 + c * 32;
+                const int col = half * 32 + c * 64;
                 if (col >= static_cast<int>(n_a)) break;
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(taddr + TMEM_A + col, v);
@@ -303,16 +318,17 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         __syncwarp();
         cluster_sync_all();
         // ---- this CTA's rows of A, in rank order, to all CTAs
-        for (int i = tid; i < own * (ROWS / 8); i += THREADS) {
-            const int r = i / (ROWS / 8), col = i % (ROWS / 8) * 8;
+        const int per_row = an == 64 ? 3 : 4;              // log2 of a row's pieces
+        for (int i = tid; i < own << per_row; i += THREADS) {
+            const int r = i >> per_row, col = (i & ((1 << per_row) - 1)) * 8;
             const int m = static_cast<int>(rank) * own + r;
-            MOE_DCHECK(m < ROWS && piece_at(m, col) + 16 <= AB_BYTES, p.status);
+            MOE_DCHECK(m < an && piece_at(m, col) + 16 <= static_cast<uint32_t>(a_bytes), p.status);
             float s[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = 0.0f;
             if (m < p.M && col < static_cast<int>(n_a)) {
                 for (uint32_t q = 0; q < C; ++q) {
-                    const float4* src = reinterpret_cast<const float4*>(ex + 4 * ((static_cast<int>(q) * own + r) * ROWS + col));
+                    const float4* src = reinterpret_cast<const float4*>(ex + 4 * ((static_cast<int>(q) * own + r) * an + col));
                     const float4 lo = src[0], hi = src[1];
                     s[0] += lo.x;
                     s[1] += lo.y;
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
             for (uint32_t q = 0; q < C; ++q) {
                 const uint32_t to = mapa_shared(off, (rank + q) % C);
                 store_cluster4(to, w[0], w[1], w[2], w[3]);
-                store_cluster4(to + AB_BYTES, l[0], l[1], l[2], l[3]);
+                store_cluster4(to + a_bytes, l[0], l[1], l[2], l[3]);
             }
         }
         __syncwarp();
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
             const uint32_t idesc = idesc_16bit_f32acc(ROWS, n_a, false, false, false);
             for (int k = 0; k < m16 / 16; ++k) {
                 const uint64_t hi = smem_desc_k_sw128(ab + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
-                const uint64_t lo = smem_desc_k_sw128(ab + AB_BYTES + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
+                const uint64_t lo = smem_desc_k_sw128(ab + a_bytes + (k >> 2) * BOX_BYTES) + (k & 3) * 2;
                 tc_mma_f16(tmem + TMEM_A, hi, hi, idesc, k > 0 ? 1u : 0u);
                 tc_mma_f16(tmem + TMEM_A, hi, lo, idesc, 1u);
                 tc_mma_f16(tmem + TMEM_A, lo, hi, idesc, 1u);
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         // ---- B, in A's place (its reads are done)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int col = half * 64 + c * 32;
+            const int col = half * 32 + c * 64;
             if (col >= static_cast<int>(n_a)) break;
             uint32_t v[32];
             tmem_ld_32x32b_x32(taddr + TMEM_A + col, v);
@@ -365,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint4* piece = reinterpret_cast<uint4*>(as + piece_at(row, col + 8 * k));
-                uint4* rest = reinterpret_cast<uint4*>(as + AB_BYTES + piece_at(row, col + 8 * k));
+                uint4* rest = reinterpret_cast<uint4*>(as + a_bytes + piece_at(row, col + 8 * k));
                 const uint4 old = *piece, old_rest = *rest;
                 const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
                 const uint32_t ol[4] = {old_rest.x, old_rest.y, old_rest.z, old_rest.w};
@@ -391,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
                         tc_mma_f16(tmem + TMEM_X + box * 64,
-                                   smem_desc_k_sw128(ab + term * AB_BYTES + (k >> 2) * BOX_BYTES) + (k & 3) * 2, x, idesc, 1u);
+                                   smem_desc_k_sw128(ab + term * a_bytes + (k >> 2) * BOX_BYTES) + (k & 3) * 2, x, idesc, 1u);
                 }
             tc_commit(bar);
         }
@@ -494,11 +510,11 @@ cudaError_t launch_small(const Orthogonalize& o, cudaStream_t stream) {
     // The fewest CTAs that hold X; then more of them while each still gets 64 columns and all
     // matrices of the stack run at once.
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && columns_of(N, cluster) > MAX_COLS) cluster *= 2;
+    while (cluster < MAX_CLUSTER && columns_of(N, cluster) > max_columns(M)) cluster *= 2;
     while (cluster < MAX_CLUSTER && columns_of(N, cluster) > 64 &&
            o.batch <= resident_clusters<DTYPE>(2 * cluster))
         cluster *= 2;
-    if (columns_of(N, cluster) > MAX_COLS || resident_clusters<DTYPE>(cluster) == 0)
+    if (columns_of(N, cluster) > max_columns(M) || resident_clusters<DTYPE>(cluster) == 0)
         return cudaErrorNotSupported;
     Small p{};
     p.update = o.update;
@@ -535,7 +551,7 @@ cudaError_t launch_small(const Orthogonalize& o, cudaStream_t stream) {
 
 bool orthogonalize_is_small(int32_t rows, int32_t cols) {
     const int32_t M = rows < cols ? rows : cols, N = rows < cols ? cols : rows;
-    return M <= ROWS && N <= MAX_CLUSTER * MAX_COLS;
+    return M <= ROWS && N <= MAX_CLUSTER * max_columns(M);
 }
 
 cudaError_t launch_orthogonalize_small(const Orthogonalize& o, cudaStream_t stream) {

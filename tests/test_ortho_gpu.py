@@ -33,7 +33,7 @@ def iterate(g, steps=5, abc=ABC, eps=1e-7, rounded=False):
             A = x @ x.transpose(1, 2)
             x = a * x + (b * A + c * (A @ A)) @ x
         return x.transpose(1, 2) if tall else x
-    if x.shape[1] <= 128 and x.shape[2] <= 6144:
+    if x.shape[1] <= 128 and x.shape[2] <= 16 * (448 if x.shape[1] <= 64 else 384):
         # on chip: a·X in 32 bits, but for the last step, which takes X as the products do; A and B in two terms
         def two(v, scale):
             hi = r16(v, scale)
@@ -98,7 +98,8 @@ def check(update, got, **kw):
 
 # sizes around the tiles' (128, 256), of whole and broken 16-byte rows, wide, square and tall
 SIZES = [(1, 64, 96), (1, 64, 2048), (2, 128, 128), (1, 129, 130), (3, 333, 1001), (1, 256, 256), (2, 257, 300), (1, 500, 200),
-         (1, 1001, 77), (2, 520, 264), (5, 96, 640), (1, 600, 1544), (1, 1408, 768), (1, 100, 6144), (2, 6100, 128), (1, 90, 6150), (40, 65, 129),
+         (1, 1001, 77), (2, 520, 264), (5, 96, 640), (1, 600, 1544), (1, 1408, 768), (1, 100, 6144), (2, 6100, 128), (1, 90, 6150), (40, 65, 129), (1, 64, 7168), (1, 7100, 40),
+         (2, 40, 7200),
          (200, 16, 40), (20, 128, 520)]
 
 
