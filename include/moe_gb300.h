@@ -454,7 +454,8 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
 #define MOE_TRAIN_MAX_TOKENS (1 << 24)
 #define MOE_TRAIN_MAX_SEQS   65535
 
-/* Workspace bytes of moe_router_balance; -1 for arguments out of range. */
+/* Workspace bytes of moe_router_balance (0 for up to 64 tokens and sequences, which need none); -1 for
+ * arguments out of range. */
 int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_seqs);
 
 /* Balance loss, z loss and per-expert counts:
@@ -471,7 +472,7 @@ int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, 
  *   workspace   device memory of moe_router_balance_workspace_bytes() bytes, caller-owned;
  *               calls that overlap on the GPU must not share it
  * Limits: n_experts <= MOE_MAX_EXPERTS, top_k <= min(n_experts, MOE_ROUTER_MAX_TOPK).
- * Sums over tokens are taken in an order that does not change between calls.  Two kernel launches. */
+ * Sums over tokens are taken in an order that does not change between calls.  One or two kernel launches. */
 moe_status_t moe_router_balance(const float* logits, const int32_t* topk_ids, int64_t n_tokens, int32_t n_experts,
                                 int32_t top_k, const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seqs,
                                 float* losses, int32_t* counts, int32_t* seq_tokens, void* workspace,

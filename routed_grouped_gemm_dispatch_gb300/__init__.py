@@ -746,44 +746,80 @@ def mx4_down(h, h_scales, down, down_scales, routed_expert_weights, group_sizes,
     return out
 
 
-def _here(*tensors):
-    """Refuses tensors of another device than the current one, where the kernels run."""
+def _placed(t, name, dtype, shape, d):
+    """A tensor of this type and shape on the current device ``d``, where the kernels run."""
+    # the common case in one expression; what follows names what is wrong
+    try:
+        if t.get_device() == d and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
+    _shaped(t, name, dtype, shape)
+    if t.device.index != d:
+        raise ValueError(f"tensors must be on the current device, cuda:{d}; {name} is on {t.device}")
+    return t
+
+
+def _current(stream):
+    """The current device and the handle of the stream to use."""
     import torch
     d = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != d:
-            raise ValueError(f"tensors must be on the current device, cuda:{d}; one is on {t.device}")
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return d, raw(d)
+    return d, _stream(stream)
 
 
-def _routing(logits, topk_ids, token_mask, seq_offsets):
+def _routing(logits, topk_ids, token_mask, seq_offsets, d):
     """Checked sizes (T, E, k, sequences) of what the router's losses and gradients read."""
     import torch
-    T, E = _dev(logits, "logits", torch.float32, 2).shape
-    k = _dev(topk_ids, "topk_ids", torch.int32, 2).shape[1]
-    if topk_ids.shape[0] != T:
-        raise ValueError(f"topk_ids must have a row per token, {T}, got {topk_ids.shape[0]}")
+    f32, i32 = torch.float32, torch.int32
+    if getattr(logits, "dtype", None) is not f32 or logits.dim() != 2:
+        _dev(logits, "logits", f32, 2)
+    if getattr(topk_ids, "dtype", None) is not i32 or topk_ids.dim() != 2:
+        _dev(topk_ids, "topk_ids", i32, 2)
+    T, E = logits.shape
+    n, k = topk_ids.shape
+    if n != T:
+        raise ValueError(f"topk_ids must have a row per token, {T}, got {n}")
+    _placed(logits, "logits", f32, (T, E), d)
+    _placed(topk_ids, "topk_ids", i32, (T, k), d)
     if token_mask is not None:
         dt = getattr(token_mask, "dtype", None)
         if dt not in (torch.bool, torch.uint8):
             raise TypeError(f"token_mask must be bool or uint8, got {dt}")
-        _shaped(token_mask, "token_mask", dt, (T,))
+        _placed(token_mask, "token_mask", dt, (T,), d)
     if seq_offsets is None:
         return T, E, k, 1
-    n = _dev(seq_offsets, "seq_offsets", torch.int32, 1).numel()
+    n = _dev(seq_offsets, "seq_offsets", i32, 1).numel()
     if n < 2:
         raise ValueError(f"seq_offsets must hold the bounds of a sequence at least, got {n} of them")
+    _placed(seq_offsets, "seq_offsets", i32, (n,), d)
     return T, E, k, n - 1
 
 
-def _workspace(t, nbytes, device, stream):
-    """A workspace of that many bytes, or the given one."""
+def _new(like, shape, dtype, stream):
+    """A tensor for a call's result or workspace."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        _used_on(stream, t)
+    return t
+
+
+def _workspace(t, nbytes, like, d, stream):
+    """Address and bytes of a workspace of that many bytes, or of the given one, and the tensor."""
     import torch
     if t is None:
-        t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-        _used_on(stream, t)
-    else:
-        _dev(t, "workspace", getattr(t, "dtype", None))
-    return t
+        if nbytes <= 0:
+            return 0, 0, None
+        t = _new(like, (nbytes,), torch.uint8, stream)
+        return t.data_ptr(), nbytes, t
+    dt = getattr(t, "dtype", None)
+    _dev(t, "workspace", dt)
+    _placed(t, "workspace", dt, t.shape, d)
+    return t.data_ptr(), t.numel() * t.element_size(), t
 
 
 def router_balance(logits, topk_ids, token_mask=None, seq_offsets=None, losses=None, counts=None, seq_tokens=None,
@@ -797,29 +833,27 @@ def router_balance(logits, topk_ids, token_mask=None, seq_offsets=None, losses=N
     ``token_mask`` [T] (bool or uint8): tokens with 0 do not count.  ``seq_offsets`` [S + 1]
     int32: packed sequences, each balanced by itself (one of all tokens without);
     tokens in none do not count.  ``workspace``: a device tensor of at least
-    router_balance_workspace_bytes(T, E, S) bytes."""
+    router_balance_workspace_bytes(T, E, S) bytes.  No autograd graph is recorded."""
     import torch
-    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    d, handle = _current(stream)
+    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets, d)
     if logits.requires_grad and torch.is_grad_enabled():
         raise RuntimeError("router_balance records no autograd graph, but logits requires grad: call it under "
                            "torch.no_grad() and take the gradients from router_backward")
-    dev = logits.device
-    outs = []
-    for t, name, dt, shape in ((losses, "losses", torch.float32, (2,)), (counts, "counts", torch.int32, (S, E)),
-                               (seq_tokens, "seq_tokens", torch.int32, (S + 1,))):
-        if t is None:
-            t = torch.empty(shape, dtype=dt, device=dev)
-            _used_on(stream, t)
-        else:
-            _shaped(t, name, dt, shape)
-        outs.append(t)
-    workspace = _workspace(workspace, router_balance_workspace_bytes(T, E, S), dev, stream)
-    _here(logits, topk_ids, token_mask, seq_offsets, workspace, *outs)
-    _check(lib().moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, _ptr(token_mask), _ptr(seq_offsets),
-                                    S, *[t.data_ptr() for t in outs], workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
-           "moe_router_balance")
-    return tuple(outs)
+    losses = _new(logits, (2,), f32, stream) if losses is None else _placed(losses, "losses", f32, (2,), d)
+    counts = _new(logits, (S, E), i32, stream) if counts is None else _placed(counts, "counts", i32, (S, E), d)
+    if seq_tokens is None:
+        seq_tokens = _new(logits, (S + 1,), i32, stream)
+    else:
+        _placed(seq_tokens, "seq_tokens", i32, (S + 1,), d)
+    L = lib()
+    ws, nbytes, workspace = _workspace(workspace, L.moe_router_balance_workspace_bytes(T, E, S), logits, d, stream)
+    st = L.moe_router_balance(logits.data_ptr(), topk_ids.data_ptr(), T, E, k, _ptr(token_mask), _ptr(seq_offsets), S,
+                              losses.data_ptr(), counts.data_ptr(), seq_tokens.data_ptr(), ws, nbytes, _status(status),
+                              handle)
+    _check(st, "moe_router_balance")
+    return losses, counts, seq_tokens
 
 
 def router_balance_workspace_bytes(n_tokens: int, n_experts: int, n_seqs: int = 1) -> int:
@@ -838,43 +872,38 @@ def router_backward(x_tokens, router_w, logits, topk_ids, d_topk_weights=None, d
     written, not added to.  ``workspace``: a device tensor of at least
     router_backward_workspace_bytes(T, E, hidden) bytes."""
     import torch
-    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets)
+    f32, i32 = torch.float32, torch.int32
+    d, handle = _current(stream)
+    T, E, k, S = _routing(logits, topk_ids, token_mask, seq_offsets, d)
     dt = getattr(x_tokens, "dtype", None)
     code = _dtype_code(dt, "x_tokens")
-    H = _dev(x_tokens, "x_tokens", dt, 2).shape[1]
-    if x_tokens.shape[0] != T:
-        raise ValueError(f"x_tokens must have a row per token, {T}, got {x_tokens.shape[0]}")
-    _shaped(router_w, "router_w", dt, (E, H))
+    n, H = _dev(x_tokens, "x_tokens", dt, 2).shape
+    if n != T:
+        raise ValueError(f"x_tokens must have a row per token, {T}, got {n}")
+    _placed(x_tokens, "x_tokens", dt, (T, H), d)
+    _placed(router_w, "router_w", dt, (E, H), d)
     if d_topk_weights is not None:
-        _shaped(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
+        _placed(d_topk_weights, "d_topk_weights", f32, (T, k), d)
     if d_losses is not None:
-        _shaped(d_losses, "d_losses", torch.float32, (2,))
+        _placed(d_losses, "d_losses", f32, (2,), d)
         if counts is None or seq_tokens is None:
             raise ValueError("d_losses goes with the counts and seq_tokens that router_balance returned")
     if counts is not None:
-        _shaped(counts, "counts", torch.int32, (S, E))
+        _placed(counts, "counts", i32, (S, E), d)
     if seq_tokens is not None:
-        _shaped(seq_tokens, "seq_tokens", torch.int32, (S + 1,))
+        _placed(seq_tokens, "seq_tokens", i32, (S + 1,), d)
     if d_logits is not None:
-        _shaped(d_logits, "d_logits", torch.float32, (T, E))
-    grads = []
-    for t, name, like in ((d_x, "d_x", x_tokens), (d_router_w, "d_router_w", router_w)):
-        if t is None:
-            t = torch.empty_like(like)
-            _used_on(stream, t)
-        else:
-            _shaped(t, name, dt, like.shape)
-        grads.append(t)
-    workspace = _workspace(workspace, router_backward_workspace_bytes(T, E, H), logits.device, stream)
-    _here(x_tokens, router_w, logits, topk_ids, d_topk_weights, d_losses, counts, seq_tokens, token_mask, seq_offsets,
-          d_logits, workspace, *grads)
-    _check(lib().moe_router_backward(code, x_tokens.data_ptr(), T, H, router_w.data_ptr(), E, logits.data_ptr(),
-                                     topk_ids.data_ptr(), k, _ptr(d_topk_weights), _ptr(d_losses), _ptr(counts),
-                                     _ptr(seq_tokens), _ptr(token_mask), _ptr(seq_offsets), S, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), grads[0].data_ptr(),
-                                     grads[1].data_ptr(), _ptr(d_logits), _status(status), _stream(stream)),
-           "moe_router_backward")
-    return tuple(grads)
+        _placed(d_logits, "d_logits", f32, (T, E), d)
+    d_x = _new(x_tokens, (T, H), dt, stream) if d_x is None else _placed(d_x, "d_x", dt, (T, H), d)
+    d_router_w = _new(x_tokens, (E, H), dt, stream) if d_router_w is None else _placed(d_router_w, "d_router_w", dt, (E, H), d)
+    L = lib()
+    ws, nbytes, workspace = _workspace(workspace, L.moe_router_backward_workspace_bytes(T, E, H), logits, d, stream)
+    st = L.moe_router_backward(code, x_tokens.data_ptr(), T, H, router_w.data_ptr(), E, logits.data_ptr(),
+                               topk_ids.data_ptr(), k, _ptr(d_topk_weights), _ptr(d_losses), _ptr(counts),
+                               _ptr(seq_tokens), _ptr(token_mask), _ptr(seq_offsets), S, ws, nbytes, d_x.data_ptr(),
+                               d_router_w.data_ptr(), _ptr(d_logits), _status(status), handle)
+    _check(st, "moe_router_backward")
+    return d_x, d_router_w
 
 
 def router_backward_workspace_bytes(n_tokens: int, n_experts: int, hidden: int) -> int:
@@ -903,17 +932,16 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     if update.requires_grad and torch.is_grad_enabled():
         raise RuntimeError("orthogonalize records no autograd graph, but update requires grad: call it under "
                            "torch.no_grad()")
-    a, b, c = (float(v) for v in coefficients)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=update.device)
-        _used_on(stream, out)
-    else:
-        _shaped(out, "out", torch.bfloat16, shape)
-    workspace = _workspace(workspace, orthogonalize_workspace_bytes(batch, rows, cols), update.device, stream)
-    _here(update, out, workspace)
-    _check(lib().moe_orthogonalize(code, update.data_ptr(), batch, rows, cols, int(steps), a, b, c, float(eps),
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
-                                   _status(status), _stream(stream)), "moe_orthogonalize")
+    a, b, c = coefficients
+    d, handle = _current(stream)
+    _placed(update, "update", dt, shape, d)
+    bf16 = torch.bfloat16
+    out = _new(update, shape, bf16, stream) if out is None else _placed(out, "out", bf16, shape, d)
+    L = lib()
+    ws, nbytes, workspace = _workspace(workspace, L.moe_orthogonalize_workspace_bytes(batch, rows, cols), update, d, stream)
+    st = L.moe_orthogonalize(code, update.data_ptr(), batch, rows, cols, int(steps), float(a), float(b), float(c),
+                             float(eps), ws, nbytes, out.data_ptr(), _status(status), handle)
+    _check(st, "moe_orthogonalize")
     return out
 
 

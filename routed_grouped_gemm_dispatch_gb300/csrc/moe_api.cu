@@ -589,8 +589,8 @@ moe_status_t moe_router_balance(const float* logits, const int32_t* topk_ids, in
     if (moe_status_t s = check_routing(a.r)) return s;
     if ((n_tokens > 0 && (!logits || !topk_ids)) || !losses || !counts || !seq_tokens) return MOE_ERR_NULL;
     if (!aligned16(logits) || !aligned16(workspace)) return MOE_ERR_ALIGN;
-    if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_router_balance_workspace_bytes(n_tokens, n_experts, n_seqs))
-        return MOE_ERR_WORKSPACE;
+    const int64_t need = moe_router_balance_workspace_bytes(n_tokens, n_experts, n_seqs);
+    if (need > 0 && (!workspace || static_cast<int64_t>(workspace_bytes) < need)) return MOE_ERR_WORKSPACE;
     if (moe_status_t s = check_device()) return s;
     a.losses = losses;
     a.counts = counts;

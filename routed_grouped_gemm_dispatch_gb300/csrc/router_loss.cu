@@ -160,6 +160,7 @@ struct BalanceParams {
     Routing r;
     int32_t chunk;                // tokens of a block
     int32_t n_slots;
+    int32_t alone;                // one block does it all: no slots
     float2* part;                 // [n_slots, E] Σ p of a block's tokens of one sequence, and (as an int) their pairs
     float2* tokens;               // [n_slots] Σ logsumexp², and (as an int) the tokens that count
     Sum* dots;                    // [n_seqs, expert blocks] Σ_e counts·Σ p
@@ -171,8 +172,17 @@ struct BalanceParams {
     int32_t* status;
 };
 
+// From Σ_s 1/T_s·Σ_e counts·Σ p, Σ logsumexp² and the tokens that count.
+__device__ __forceinline__ void store_losses(const BalanceParams& p, const Sum& balance, const Sum& z, int32_t n) {
+    const float tokens = static_cast<float>(n > 0 ? n : 1);
+    p.losses[0] = balance.value() * static_cast<float>(p.r.n_experts) / (static_cast<float>(p.r.top_k) * tokens);
+    p.losses[1] = z.value() / tokens;
+    p.seq_tokens[p.r.n_seqs] = n;
+}
+
 // One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
-// from one part to the next either b or s grows, so no two share a slot.
+// from one part to the next either b or s grows, so no two share a slot.  Few tokens have one block, which
+// adds up its parts itself.
 template <int L, int PER, bool VEC>
 __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(const BalanceParams p) {
     extern __shared__ float sums[];                               // [HALF][E], then int [E]
@@ -185,10 +195,24 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
     for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    if (!p.alone && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     const Seqs seqs{p.r.seq_offsets, p.r.n_seqs, p.r.n_tokens};
     const int64_t first = static_cast<int64_t>(blockIdx.x) * p.chunk;
     const int64_t last = first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens;
+    // alone: the losses so far (thread 0), and zeros for the sequences without tokens
+    Sum balance, zs;
+    int32_t all = 0;
+    __shared__ Sum dots[WARPS];
+    if (p.alone) {
+        bool bad = false;
+        for (int32_t i = threadIdx.x; i < p.r.n_seqs; i += THREADS) {
+            p.seq_tokens[i] = 0;
+            if (p.r.seq_offsets)
+                bad |= p.r.seq_offsets[i] > p.r.seq_offsets[i + 1] || p.r.seq_offsets[i] < 0 || p.r.seq_offsets[i + 1] > p.r.n_tokens;
+        }
+        if (bad && p.status) atomicOr(p.status, MOE_DEV_BAD_TABLE);
+        for (int32_t i = threadIdx.x; i < p.r.n_seqs * E; i += THREADS) p.counts[i] = 0;
+    }
     int32_t s = seqs.find(first);
     if (s < 0) s = 0;
     int64_t t0 = first > seqs.bound(0) ? first : seqs.bound(0);
@@ -199,6 +223,18 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
             ++s;
             continue;
         }
+        const float* row = p.r.logits + (t0 + warp * PACK + lane / L) * E;
+        int32_t left = static_cast<int32_t>(t1 - t0) - warp * PACK - lane / L;      // tokens from this lane's on
+        const uint8_t* mask = p.r.token_mask ? p.r.token_mask + (t1 - left) : nullptr;
+        float z[PER];
+        bool live = false;
+        auto ask = [&]() {
+            live = left > 0 && (mask == nullptr || *mask != 0);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) z[i] = 0.0f;
+            if (live) load_row<L, PER, VEC>(z, row, l, E);
+        };
+        ask();                                                    // on its way while the pairs are counted
         __syncthreads();                                          // the counts are zero
         // pairs of the tokens that count
         const int32_t pairs = static_cast<int32_t>(t1 - t0) * k;
@@ -213,15 +249,7 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
         for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
         float zz = 0.0f;
         int n = 0;
-        const float* row = p.r.logits + (t0 + warp * PACK + lane / L) * E;
-        int32_t left = static_cast<int32_t>(t1 - t0) - warp * PACK - lane / L;      // tokens from this lane's on
-        const uint8_t* mask = p.r.token_mask ? p.r.token_mask + (t1 - left) : nullptr;
         for (int32_t i0 = warp * PACK; i0 < static_cast<int32_t>(t1 - t0); i0 += WARPS * PACK) {
-            const bool live = left > 0 && (mask == nullptr || *mask != 0);
-            float z[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) z[i] = 0.0f;
-            if (live) load_row<L, PER, VEC>(z, row, l, E);
             const float lse = softmax_row<L, PER>(z);
             if (live) {
 #pragma unroll
@@ -234,6 +262,7 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
             row += static_cast<int64_t>(WARPS * PACK) * E;
             left -= WARPS * PACK;
             if (mask) mask += WARPS * PACK;
+            ask();
         }
         // a warp's tokens, then the block's warps
 #pragma unroll
@@ -264,13 +293,26 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
         }
         __syncthreads();
         const int64_t slot = static_cast<int64_t>(blockIdx.x) + s;
-        MOE_DCHECK(slot < p.n_slots && t0 >= 0 && t1 <= p.r.n_tokens, p.status);
+        MOE_DCHECK((p.alone || slot < p.n_slots) && t0 >= 0 && t1 <= p.r.n_tokens, p.status);
+        Sum dot;
         for (int e = threadIdx.x; e < E; e += THREADS) {
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < HALF; ++w) v += sums[w * E + e];
-            p.part[slot * E + e] = make_float2(v, __int_as_float(hist[e]));
+            if (p.alone) {
+                p.counts[static_cast<int64_t>(s) * E + e] = hist[e];
+                Sum one;
+                one.hi = v;
+                dot.add(one.times(static_cast<float>(hist[e])));
+            } else {
+                p.part[slot * E + e] = make_float2(v, __int_as_float(hist[e]));
+            }
             hist[e] = 0;
+        }
+        if (p.alone) {
+            dot.add_lanes();
+            if (lane == 0) dots[warp] = dot;
+            __syncthreads();
         }
         if (threadIdx.x == 0) {
             float zt = 0.0f;
@@ -279,12 +321,22 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
                 zt += zpart[w];
                 nt += npart[w];
             }
-            p.tokens[slot] = make_float2(zt, __int_as_float(nt));
+            if (p.alone) {
+                Sum d;
+                for (int w = 0; w < WARPS; ++w) d.add(dots[w]);
+                if (nt > 0) balance.add(d.times(1.0f / static_cast<float>(nt)));
+                zs.add(zt);
+                all += nt;
+                p.seq_tokens[s] = nt;
+            } else {
+                p.tokens[slot] = make_float2(zt, __int_as_float(nt));
+            }
         }
         __syncthreads();
         t0 = t1;
         ++s;
     }
+    if (p.alone && threadIdx.x == 0) store_losses(p, balance, zs, all);
 }
 
 // Grid: 32 experts of a sequence per block.  The last block to finish adds the sequences up.
@@ -362,31 +414,26 @@ __global__ void __launch_bounds__(32 * REDUCE_WARPS) balance_reduce_kernel(const
     __syncthreads();
     if (!final_block) return;
     __threadfence();
-    // every thread its sequences in order, then the threads in a tree
+    // every warp its sequences in order, a lane each of their parts; then the warps in a tree
+    static_assert(MOE_MAX_EXPERTS <= 32 * 32, "a lane for every block of experts");
     Sum bal, z;
     int32_t n = 0;
-    for (int32_t i = threadIdx.x; i < S; i += 32 * REDUCE_WARPS) {
+    for (int32_t i = warp; i < S; i += REDUCE_WARPS) {
+        float2 x = make_float2(0.0f, 0.0f);
+        if (lane < static_cast<int>(gridDim.x))
+            x = __ldcg(reinterpret_cast<const float2*>(p.dots + static_cast<int64_t>(i) * gridDim.x + lane));
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p.zsum + i));
         const int32_t ni = __ldcg(p.seq_tokens + i);
-        Sum d;
-        for (unsigned b = 0; b < gridDim.x; ++b) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(p.dots + static_cast<int64_t>(i) * gridDim.x + b));
-            Sum part;
-            part.hi = x.x;
-            part.lo = x.y;
-            d.add(part);
-        }
+        Sum d, one;
+        d.hi = x.x;
+        d.lo = x.y;
+        d.add_lanes();
         if (ni > 0) bal.add(d.times(1.0f / static_cast<float>(ni)));
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(p.zsum + i));
-        Sum part;
-        part.hi = x.x;
-        part.lo = x.y;
-        z.add(part);
+        one.hi = y.x;
+        one.lo = y.y;
+        z.add(one);
         n += ni;
     }
-    bal.add_lanes();
-    z.add_lanes();
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
     if (lane == 0) {
         sum[0][warp] = bal;
         sum[1][warp] = z;
@@ -402,10 +449,7 @@ __global__ void __launch_bounds__(32 * REDUCE_WARPS) balance_reduce_kernel(const
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
         if (lane == 0) {
-            const float tokens = static_cast<float>(n > 0 ? n : 1);
-            p.losses[0] = bal.value() * static_cast<float>(E) / (static_cast<float>(p.r.top_k) * tokens);
-            p.losses[1] = z.value() / tokens;
-            p.seq_tokens[S] = n;
+            store_losses(p, bal, z, n);
         }
     }
 }
@@ -699,14 +743,20 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Tokens (and sequences) up to which one block does it all, in one launch without a workspace: 32 x 128 takes 8.0 us in two.
+constexpr int64_t ALONE_TOKENS = 64;
+
 struct BalanceLayout {
+    bool alone;
     int32_t chunk, chunks, slots, expert_blocks;
     int64_t part, tokens, dots, zsum, done, bytes;
 };
 
 BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
     BalanceLayout l;
-    l.chunk = n_tokens > 0 ? chunk_tokens(n_tokens, WARPS) : WARPS;
+    l.alone = n_tokens <= ALONE_TOKENS && n_seqs <= ALONE_TOKENS;
+    l.chunk = l.alone ? ALONE_TOKENS : chunk_tokens(n_tokens, WARPS);
+    if (l.chunk == 0) l.chunk = WARPS;
     l.chunks = static_cast<int32_t>((n_tokens + l.chunk - 1) / l.chunk);
     if (l.chunks == 0) l.chunks = 1;
     l.slots = l.chunks + n_seqs;
@@ -722,7 +772,7 @@ BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs
     l.dots = take(int64_t{8} * n_seqs * l.expert_blocks);
     l.zsum = take(int64_t{8} * n_seqs);
     l.done = take(4);
-    l.bytes = at;
+    l.bytes = l.alone ? 0 : at;
     return l;
 }
 
@@ -739,6 +789,7 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     p.r = a.r;
     p.chunk = l.chunk;
     p.n_slots = l.slots;
+    p.alone = l.alone ? 1 : 0;
     p.part = reinterpret_cast<float2*>(ws + l.part);
     p.tokens = reinterpret_cast<float2*>(ws + l.tokens);
     p.dots = reinterpret_cast<Sum*>(ws + l.dots);
@@ -757,7 +808,7 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
                 : E > 64  ? balance_kernel<8, 16, true>
                           : balance_kernel<4, 16, true>;
     cudaError_t err = launch_pdl(kernel, dim3(static_cast<unsigned>(l.chunks)), THREADS, smem, stream, p);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || l.alone) return err;
     return launch_pdl(balance_reduce_kernel, dim3(static_cast<unsigned>(l.expert_blocks), static_cast<unsigned>(a.r.n_seqs)),
                       32 * REDUCE_WARPS, 0, stream, p);
 }

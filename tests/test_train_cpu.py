@@ -18,7 +18,7 @@ def L():
     return moe.lib()
 
 
-BAL = dict(z=0x1000, ids=0x2000, T=50, E=24, k=3, mask=0x3000, offs=0x4000, S=4, losses=0x5000, counts=0x6000, tokens=0x7000,
+BAL = dict(z=0x1000, ids=0x2000, T=500, E=24, k=3, mask=0x3000, offs=0x4000, S=4, losses=0x5000, counts=0x6000, tokens=0x7000,
            ws=0x8000, n=1 << 20)
 
 
@@ -51,9 +51,10 @@ def test_balance_refusals(L):
     sizes(bal, L)
     for key in ("losses", "counts", "tokens"):
         assert bal(L, **{key: None}) == NULL
-    need = L.moe_router_balance_workspace_bytes(50, 24, 4)
+    need = L.moe_router_balance_workspace_bytes(500, 24, 4)
+    assert L.moe_router_balance_workspace_bytes(64, 24, 64) == 0               # needs none
     assert need > 0 and bal(L, n=need - 1) == WORKSPACE
-    for bad in ((-1, 24, 4), (50, 0, 4), (50, 1025, 4), (50, 24, 0), (50, 24, 65536), ((1 << 24) + 1, 24, 1)):
+    for bad in ((-1, 24, 4), (500, 0, 4), (500, 1025, 4), (500, 24, 0), (500, 24, 65536), ((1 << 24) + 1, 24, 1)):
         assert L.moe_router_balance_workspace_bytes(*bad) == -1
 
 
@@ -125,6 +126,7 @@ def fake(L, monkeypatch):
     """Tensors made inside have a device, a type, sizes and strides, and no memory."""
     monkeypatch.setattr(moe, "_stream", lambda s: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
     with FakeTensorMode():
         yield lambda *shape, dt=torch.float32: torch.empty(shape, dtype=dt, device="cuda")
 
@@ -222,6 +224,7 @@ def test_allocations_are_recorded(name, n, given, monkeypatch):
     monkeypatch.setattr(moe, "lib", lambda lib=NoLibrary(): lib)
     monkeypatch.setattr(moe, "_stream", lambda s: 0 if s is None else s.cuda_stream)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
     with FakeTensorMode(), warnings.catch_warnings():
         warnings.simplefilter("ignore")
         z, ids = torch.empty((4, 8), device="cuda"), torch.empty((4, 2), dtype=torch.int32, device="cuda")
@@ -229,15 +232,15 @@ def test_allocations_are_recorded(name, n, given, monkeypatch):
         args = {"router_balance": (z, ids), "router_backward": (x, w, z, ids), "orthogonalize": (x,)}[name]
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((id(t), s)))
         inside = []
-        for f in ("empty", "empty_like"):
-            def spy(*a, _f=getattr(torch, f), **k):
+        for owner, f in ((torch, "empty"), (torch, "empty_like")):
+            def spy(*a, _f=getattr(owner, f), **k):
                 inside.append(1)
                 r = _f(*a, **k)
                 inside.pop()
                 if not inside:
                     made.append(r)
                 return r
-            monkeypatch.setattr(torch, f, spy)
+            monkeypatch.setattr(owner, f, spy)
         getattr(moe, name)(*args, stream=stream)
     assert len(made) == n
     assert recorded == ([(id(t), stream) for t in made] if given else [])
