@@ -448,14 +448,15 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
  * hold.  Below, T is the number of tokens that count, T_s that of sequence s, k = top_k,
  * E = n_experts, z the logits, p = softmax(z); a logit of -infinity has p = 0, and a token with
  * no other (p = 0 everywhere) adds nothing but its T and its ids.  Offsets that decrease or leave the range
- * set MOE_DEV_BAD_TABLE and leave the outputs undefined.  Negative ids (moe_router_topk's for a token with too few
+ * set MOE_DEV_BAD_TABLE and leave the outputs undefined.  No output overlaps an input, another output or the
+ * workspace.  Negative ids (moe_router_topk's for a token with too few
  * ranked logits) are skipped, ids >= n_experts too, which set MOE_DEV_BAD_EXPERT_ID.
  * ------------------------------------------------------------------------- */
 #define MOE_TRAIN_MAX_TOKENS (1 << 24)
 #define MOE_TRAIN_MAX_SEQS   65535
 
-/* Workspace bytes of moe_router_balance (0 for up to 64 tokens and sequences, which need none); -1 for
- * arguments out of range. */
+/* Workspace bytes of moe_router_balance (0 for few tokens in one or two sequences, which need none); -1
+ * for arguments out of range. */
 int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_seqs);
 
 /* Balance loss, z loss and per-expert counts:
@@ -525,13 +526,15 @@ int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t c
  * which brings the singular values of G near 1 and keeps its singular vectors (a, b, c =
  * 3.4445, -4.775, 2.0315 in five steps: into about 0.7 .. 1.2 from 0.01 of the norm on).
  *   update  [batch, rows, cols], `dtype` MOE_DTYPE_F16, _BF16 or _F32
- *   out     out: [batch, rows, cols] bf16; must not overlap update
+ *   out     out: [batch, rows, cols] bf16
  * Any rows and cols.  Products are of fp16 operands with fp32 sums: with such coefficients the result is
- * within about 2e-3 of its root mean square, root mean square, whatever G's spectrum, so no
- * finer type is offered.  A matrix that holds an infinity or a NaN, or whose norm leaves fp32's
- * squares (1.8e19), becomes NaN; one of zeros stays zeros; the others of the stack do not see it.
- * Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c| unless c is 0; where they let a norm grow past 2^9 the
- * result overflows.  batch·steps·ceil(rows/128)·ceil(cols/128) is at most 2^29.
+ * within 2e-3 to 3e-3 of the exact one (root mean square, relative to that of the exact one, rounding to
+ * bf16 included) whatever G's spectrum, so no finer type is offered.  A matrix that holds an infinity or
+ * a NaN, or whose norm leaves fp32's squares (1.8e19), becomes NaN; one of zeros stays zeros (values
+ * below 1e-22, whose squares are below fp32's, count as zeros in the norm); the others of the stack do
+ * not see it.  Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c|
+ * unless c is 0; where they let a norm grow past 2^9 the result overflows.
+ * batch·steps·ceil(rows/128)·ceil(cols/128) is at most 2^29.
  * workspace: device memory of moe_orthogonalize_workspace_bytes() bytes, caller-owned;
  * calls that overlap on the GPU must not share it.  Three kernel launches; waits and
  * status_dev as in the feed-forward block. */

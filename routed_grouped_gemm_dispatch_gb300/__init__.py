@@ -869,7 +869,7 @@ def router_backward(x_tokens, router_w, logits, topk_ids, d_topk_weights=None, d
     and shapes, float16 or bfloat16; hidden a multiple of 8.  ``token_mask`` and
     ``seq_offsets`` as in router_balance: a token that does not count has a gradient of zero.
     ``d_logits`` (fp32 [T, E]) receives the gradients of the logits.  Supplied buffers are
-    written, not added to.  ``workspace``: a device tensor of at least
+    written, not added to, and overlap no input.  ``workspace``: a device tensor of at least
     router_backward_workspace_bytes(T, E, hidden) bytes."""
     import torch
     f32, i32 = torch.float32, torch.int32
@@ -917,7 +917,8 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     singular values come near 1.  ``update`` [rows, cols] or a stack [batch, rows, cols] of any sizes,
     float16, bfloat16 or float32 (a gradient, or a momentum); returns bfloat16 of its shape
     (``out`` may be supplied).  Each matrix of a stack is taken by itself.  Products
-    are of 16-bit operands with fp32 sums: the result is within about 2e-3 of its size.
+    are of 16-bit operands with fp32 sums: the result is within 2e-3 to 3e-3 of the exact one, root mean
+    square, bf16's own rounding included.  ``out`` does not overlap ``update``.
     ``workspace``: a device tensor of at least orthogonalize_workspace_bytes(batch, rows, cols) bytes."""
     import torch
     dt = getattr(update, "dtype", None)

@@ -21,9 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "../../include/moe_gb300.h"
 #include "moe_internal.h"
@@ -468,37 +466,41 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     }
 }
 
-// Clusters of `size` CTAs that fit on the device at once (0: none), asked once per device and size.
+// Clusters of `size` CTAs (a power of two) that fit on the device at once (0: none), asked once per
+// device and size.
 template <int DTYPE>
 int resident_clusters(int size) {
-    static std::mutex mu;
-    static std::map<std::pair<int, int>, int> known;
+    struct Entry {
+        std::once_flag once;
+        int clusters = 0;
+    };
+    constexpr int MAX_DEVICES = 16;
+    static Entry table[MAX_DEVICES][MAX_CLUSTER];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_pair(dev, size);
-    auto it = known.find(key);
-    if (it != known.end()) return it->second;
-    int n = 0;
-    if (cudaFuncSetAttribute(ortho_small_kernel<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             SMEM_BYTES) == cudaSuccess &&
-        cudaFuncSetAttribute(ortho_small_kernel<DTYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(size);
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(size));
-        cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, ortho_small_kernel<DTYPE>, &cfg) != cudaSuccess) n = 0;
-    }
-    cudaGetLastError();
-    known.emplace(key, n);
-    return n;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= MAX_DEVICES || size > MAX_CLUSTER) return 0;
+    Entry& r = table[dev][size - 1];
+    std::call_once(r.once, [&r, size] {
+        if (cudaFuncSetAttribute(ortho_small_kernel<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SMEM_BYTES) == cudaSuccess &&
+            cudaFuncSetAttribute(ortho_small_kernel<DTYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                cudaSuccess) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(size));
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = SMEM_BYTES;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, ortho_small_kernel<DTYPE>, &cfg) == cudaSuccess) r.clusters = n;
+        }
+        cudaGetLastError();
+    });
+    return r.clusters;
 }
 
 int32_t columns_of(int32_t N, int cluster) { return ((N + cluster - 1) / cluster + 63) / 64 * 64; }

@@ -181,8 +181,8 @@ __device__ __forceinline__ void store_losses(const BalanceParams& p, const Sum& 
 }
 
 // One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
-// from one part to the next either b or s grows, so no two share a slot.  Few tokens have one block, which
-// adds up its parts itself.
+// from one part to the next either b or s grows, so no two share a slot.  Few tokens in at most two sequences have
+// one block, which adds up its parts itself.
 template <int L, int PER, bool VEC>
 __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(const BalanceParams p) {
     extern __shared__ float sums[];                               // [HALF][E], then int [E]
@@ -743,8 +743,10 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Tokens (and sequences) up to which one block does it all, in one launch without a workspace: 32 x 128 takes 8.0 us in two.
+// Tokens and sequences up to which one block does it all, in one launch without a workspace.  Every sequence is a
+// round of its own there: 64 x 128 in 1, 2 and 4 sequences takes 4.3, 6.4 and 11 us, and 9 in two launches.
 constexpr int64_t ALONE_TOKENS = 64;
+constexpr int32_t ALONE_SEQS = 2;
 
 struct BalanceLayout {
     bool alone;
@@ -754,7 +756,7 @@ struct BalanceLayout {
 
 BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
     BalanceLayout l;
-    l.alone = n_tokens <= ALONE_TOKENS && n_seqs <= ALONE_TOKENS;
+    l.alone = n_tokens <= ALONE_TOKENS && n_seqs <= ALONE_SEQS;
     l.chunk = l.alone ? ALONE_TOKENS : chunk_tokens(n_tokens, WARPS);
     if (l.chunk == 0) l.chunk = WARPS;
     l.chunks = static_cast<int32_t>((n_tokens + l.chunk - 1) / l.chunk);

@@ -52,7 +52,8 @@ def test_balance_refusals(L):
     for key in ("losses", "counts", "tokens"):
         assert bal(L, **{key: None}) == NULL
     need = L.moe_router_balance_workspace_bytes(500, 24, 4)
-    assert L.moe_router_balance_workspace_bytes(64, 24, 64) == 0               # needs none
+    assert L.moe_router_balance_workspace_bytes(64, 24, 2) == 0                # needs none
+    assert L.moe_router_balance_workspace_bytes(64, 24, 3) > 0 and L.moe_router_balance_workspace_bytes(65, 24, 1) > 0
     assert need > 0 and bal(L, n=need - 1) == WORKSPACE
     for bad in ((-1, 24, 4), (500, 0, 4), (500, 1025, 4), (500, 24, 0), (500, 24, 65536), ((1 << 24) + 1, 24, 1)):
         assert L.moe_router_balance_workspace_bytes(*bad) == -1
