@@ -455,7 +455,7 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
 #define MOE_TRAIN_MAX_TOKENS (1 << 24)
 #define MOE_TRAIN_MAX_SEQS   65535
 
-/* Workspace bytes of moe_router_balance (0 for few tokens in one or two sequences, which need none); -1
+/* Workspace bytes of moe_router_balance (0 for few tokens and sequences, which need none); -1
  * for arguments out of range. */
 int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, int32_t n_seqs);
 

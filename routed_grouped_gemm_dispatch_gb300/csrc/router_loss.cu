@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "../../include/moe_gb300.h"
 #include "moe_internal.h"
@@ -29,6 +31,7 @@ constexpr int WARPS = 16;
 constexpr int THREADS = 32 * WARPS;
 constexpr int REDUCE_WARPS = 32;
 constexpr int HALF = WARPS / 2;
+constexpr int MAX_CLUSTER = 16;
 
 // Value i of lane l of a token's L lanes is expert `expert(l, i)`.  VEC: E is a multiple of 4 and rows
 // are whole 16-byte pieces.
@@ -160,7 +163,6 @@ struct BalanceParams {
     Routing r;
     int32_t chunk;                // tokens of a block
     int32_t n_slots;
-    int32_t alone;                // one block does it all: no slots
     float2* part;                 // [n_slots, E] Σ p of a block's tokens of one sequence, and (as an int) their pairs
     float2* tokens;               // [n_slots] Σ logsumexp², and (as an int) the tokens that count
     Sum* dots;                    // [n_seqs, expert blocks] Σ_e counts·Σ p
@@ -180,39 +182,18 @@ __device__ __forceinline__ void store_losses(const BalanceParams& p, const Sum& 
     p.seq_tokens[p.r.n_seqs] = n;
 }
 
-// One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
-// from one part to the next either b or s grows, so no two share a slot.  Few tokens in at most two sequences have
-// one block, which adds up its parts itself.
-template <int L, int PER, bool VEC>
-__global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(const BalanceParams p) {
-    extern __shared__ float sums[];                               // [HALF][E], then int [E]
+// Tokens first .. last - 1 of a block, one sequence after the other: store(s, e, Σ p, pairs) by a
+// thread for each expert, store(s, Σ logsumexp², tokens that count) by one.  shared: [HALF][E] floats, then
+// [E] counts, which are zero (a barrier may be still to come).  Ends with a barrier.
+template <int L, int PER, bool VEC, class Store>
+__device__ __forceinline__ void add_tokens(const BalanceParams& p, int64_t first, int64_t last, float* sums, const Store& store) {
     __shared__ float zpart[WARPS];
     __shared__ int npart[WARPS];
     constexpr int PACK = 32 / L;                                  // tokens a warp has at a time
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (L - 1);
     const int32_t E = p.r.n_experts, k = p.r.top_k;
     int32_t* hist = reinterpret_cast<int32_t*>(sums + HALF * E);
-    for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
-    if (!p.alone && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     const Seqs seqs{p.r.seq_offsets, p.r.n_seqs, p.r.n_tokens};
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.chunk;
-    const int64_t last = first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens;
-    // alone: the losses so far (thread 0), and zeros for the sequences without tokens
-    Sum balance, zs;
-    int32_t all = 0;
-    __shared__ Sum dots[WARPS];
-    if (p.alone) {
-        bool bad = false;
-        for (int32_t i = threadIdx.x; i < p.r.n_seqs; i += THREADS) {
-            p.seq_tokens[i] = 0;
-            if (p.r.seq_offsets)
-                bad |= p.r.seq_offsets[i] > p.r.seq_offsets[i + 1] || p.r.seq_offsets[i] < 0 || p.r.seq_offsets[i + 1] > p.r.n_tokens;
-        }
-        if (bad && p.status) atomicOr(p.status, MOE_DEV_BAD_TABLE);
-        for (int32_t i = threadIdx.x; i < p.r.n_seqs * E; i += THREADS) p.counts[i] = 0;
-    }
     int32_t s = seqs.find(first);
     if (s < 0) s = 0;
     int64_t t0 = first > seqs.bound(0) ? first : seqs.bound(0);
@@ -292,27 +273,13 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
             }
         }
         __syncthreads();
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) + s;
-        MOE_DCHECK((p.alone || slot < p.n_slots) && t0 >= 0 && t1 <= p.r.n_tokens, p.status);
-        Sum dot;
+        MOE_DCHECK(t0 >= 0 && t1 <= p.r.n_tokens && s >= 0 && s < p.r.n_seqs, p.status);
         for (int e = threadIdx.x; e < E; e += THREADS) {
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < HALF; ++w) v += sums[w * E + e];
-            if (p.alone) {
-                p.counts[static_cast<int64_t>(s) * E + e] = hist[e];
-                Sum one;
-                one.hi = v;
-                dot.add(one.times(static_cast<float>(hist[e])));
-            } else {
-                p.part[slot * E + e] = make_float2(v, __int_as_float(hist[e]));
-            }
+            store(s, e, v, hist[e]);
             hist[e] = 0;
-        }
-        if (p.alone) {
-            dot.add_lanes();
-            if (lane == 0) dots[warp] = dot;
-            __syncthreads();
         }
         if (threadIdx.x == 0) {
             float zt = 0.0f;
@@ -321,22 +288,149 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(con
                 zt += zpart[w];
                 nt += npart[w];
             }
-            if (p.alone) {
-                Sum d;
-                for (int w = 0; w < WARPS; ++w) d.add(dots[w]);
-                if (nt > 0) balance.add(d.times(1.0f / static_cast<float>(nt)));
-                zs.add(zt);
-                all += nt;
-                p.seq_tokens[s] = nt;
-            } else {
-                p.tokens[slot] = make_float2(zt, __int_as_float(nt));
-            }
+            store(s, zt, nt);
         }
         __syncthreads();
         t0 = t1;
         ++s;
     }
-    if (p.alone && threadIdx.x == 0) store_losses(p, balance, zs, all);
+}
+
+// One block per `chunk` tokens.  The part of sequence s in block b goes to slot b + s:
+// from one part to the next either b or s grows, so no two share a slot.
+struct StoreSlot {
+    const BalanceParams& p;
+    __device__ __forceinline__ int64_t slot(int32_t s) const {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) + s;
+        MOE_DCHECK(i < p.n_slots, p.status);
+        return i;
+    }
+    __device__ __forceinline__ void operator()(int32_t s, int32_t e, float v, int32_t n) const {
+        p.part[slot(s) * p.r.n_experts + e] = make_float2(v, __int_as_float(n));
+    }
+    __device__ __forceinline__ void operator()(int32_t s, float z, int32_t n) const {
+        p.tokens[slot(s)] = make_float2(z, __int_as_float(n));
+    }
+};
+
+template <int L, int PER, bool VEC>
+__global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_kernel(const BalanceParams p) {
+    extern __shared__ float sums[];                               // [HALF][E], then int [E]
+    for (int e = threadIdx.x; e < p.r.n_experts; e += THREADS) sums[HALF * p.r.n_experts + e] = 0.0f;
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.chunk;
+    add_tokens<L, PER, VEC>(p, first, first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens, sums, StoreSlot{p});
+}
+
+// Few tokens: all of it by one cluster, whose CTAs have `chunk` tokens each.  Their parts stay in shared memory;
+// CTA i of C adds up the parts of sequences i, i + C, ... and the first CTA the sequences.
+struct StoreShared {
+    float2* part;                 // [n_seqs, E], as in the slots
+    float2* tokens;               // [n_seqs]
+    int32_t E;
+    __device__ __forceinline__ void operator()(int32_t s, int32_t e, float v, int32_t n) const {
+        part[s * E + e] = make_float2(v, __int_as_float(n));
+    }
+    __device__ __forceinline__ void operator()(int32_t s, float z, int32_t n) const {
+        tokens[s] = make_float2(z, __int_as_float(n));
+    }
+};
+
+__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int L, int PER, bool VEC>
+__global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) balance_cluster_kernel(const BalanceParams p) {
+    extern __shared__ float sums[];                               // [HALF][E], int [E], then StoreShared's
+    __shared__ Sum dots[WARPS];
+    __shared__ float2 final_sums[MAX_CLUSTER][2];                 // of the first CTA: Σ 1/T_s·Σ counts·Σ p, Σ logsumexp²
+    __shared__ int32_t final_tokens[MAX_CLUSTER];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t E = p.r.n_experts, S = p.r.n_seqs;
+    const int32_t rank = static_cast<int32_t>(blockIdx.x), C = static_cast<int32_t>(gridDim.x);
+    float2* part = reinterpret_cast<float2*>(sums + (HALF + 1) * E + (E & 1));
+    const StoreShared store{part, part + S * E, E};
+    for (int e = threadIdx.x; e < E; e += THREADS) sums[HALF * E + e] = 0.0f;
+    for (int i = threadIdx.x; i < S * E + S; i += THREADS) part[i] = make_float2(0.0f, 0.0f);
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    if (p.r.seq_offsets && rank == 0 && static_cast<int32_t>(threadIdx.x) < S && p.status) {
+        const int32_t a = p.r.seq_offsets[threadIdx.x], b = p.r.seq_offsets[threadIdx.x + 1];
+        if (a > b || a < 0 || b > p.r.n_tokens) atomicOr(p.status, MOE_DEV_BAD_TABLE);
+    }
+    const int64_t first = static_cast<int64_t>(rank) * p.chunk;
+    add_tokens<L, PER, VEC>(p, first, first + p.chunk < p.r.n_tokens ? first + p.chunk : p.r.n_tokens, sums, store);
+    auto sync_all = [C] {
+        if (C > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+    sync_all();
+    Sum bal, z;                                                   // of this CTA's sequences, by its first thread
+    int32_t n = 0;
+    for (int32_t s = rank; s < S; s += C) {
+        Sum dot;
+        for (int32_t e = threadIdx.x; e < E; e += THREADS) {
+            const uint32_t at = smem_u32(part + s * E + e);
+            Sum v;
+            int32_t c = 0;
+#pragma unroll 8
+            for (int32_t r = 0; r < C; ++r) {
+                const float2 x = load_cluster2(mapa_shared(at, static_cast<uint32_t>(r)));
+                v.add(x.x);
+                c += __float_as_int(x.y);
+            }
+            p.counts[static_cast<int64_t>(s) * E + e] = c;
+            dot.add(v.times(static_cast<float>(c)));
+        }
+        dot.add_lanes();
+        if (lane == 0) dots[warp] = dot;
+        __syncthreads();
+        if (warp == 0) {
+            float2 x = make_float2(0.0f, 0.0f);
+            if (lane < C) x = load_cluster2(mapa_shared(smem_u32(store.tokens + s), static_cast<uint32_t>(lane)));
+            Sum zs, d;
+            int32_t ns = __float_as_int(x.y);
+            zs.add(x.x);
+            zs.add_lanes();
+            if (lane < WARPS) d = dots[lane];
+            d.add_lanes();
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) ns += __shfl_xor_sync(0xffffffffu, ns, i);
+            if (ns > 0) bal.add(d.times(1.0f / static_cast<float>(ns)));
+            z.add(zs);
+            n += ns;
+            if (lane == 0) p.seq_tokens[s] = ns;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const uint32_t to = mapa_shared(smem_u32(&final_sums[rank][0]), 0), n_to = mapa_shared(smem_u32(&final_tokens[rank]), 0);
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(bal.hi), "f"(bal.lo) : "memory");
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + 8), "f"(z.hi), "f"(z.lo) : "memory");
+        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(n_to), "r"(n) : "memory");
+    }
+    sync_all();
+    if (rank == 0 && warp == 0) {
+        Sum b, y;
+        int32_t m = 0;
+        if (lane < C) {
+            b.hi = final_sums[lane][0].x;
+            b.lo = final_sums[lane][0].y;
+            y.hi = final_sums[lane][1].x;
+            y.lo = final_sums[lane][1].y;
+            m = final_tokens[lane];
+        }
+        b.add_lanes();
+        y.add_lanes();
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) m += __shfl_xor_sync(0xffffffffu, m, i);
+        if (lane == 0) store_losses(p, b, y, m);
+    }
 }
 
 // Grid: 32 experts of a sequence per block.  The last block to finish adds the sequences up.
@@ -728,38 +822,60 @@ int32_t chunk_tokens(int64_t n_tokens, int step) {
     return static_cast<int32_t>((c + step - 1) / step * step);
 }
 
-template <class... Args>
-cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr[1];
+template <class Params>
+cudaError_t launch_pdl(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                       const std::remove_const_t<Params>& p, int cluster = 1) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Tokens and sequences up to which one block does it all, in one launch without a workspace.  Every sequence is a
-// round of its own there: 64 x 128 in 1, 2 and 4 sequences takes 4.3, 6.4 and 11 us, and 9 in two launches.
-constexpr int64_t ALONE_TOKENS = 64;
-constexpr int32_t ALONE_SEQS = 2;
+// Lanes of a token, for its logits.
+int balance_lanes(int32_t n_experts) {
+    return n_experts > 256 ? 32 : n_experts % 4 != 0 || n_experts > 128 ? 16 : n_experts > 64 ? 8 : 4;
+}
+
+// CTAs of the cluster that does it all in one launch without a workspace; 0: too much for it.  As measured (us), one
+// launch and two: 64 tokens of 64 experts 4.3 and 8.8, 4097 in 5 sequences 8.5 and 13.8, 16384 13.4 and 10.5; a round
+// of all warps of 16 CTAs takes 0.8 to 1.1, and every sequence of a CTA is a round of its own.
+constexpr int32_t CLUSTER_ROUNDS = 4;
+constexpr int32_t CLUSTER_SEQS = 32;
+int64_t cluster_shared_bytes(int32_t n_experts, int32_t n_seqs) {
+    return int64_t{4} * (HALF + 1) * n_experts + 8 + int64_t{8} * n_seqs * (n_experts + 1);
+}
+int32_t balance_cluster(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
+    const int64_t round = WARPS * 32 / balance_lanes(n_experts);          // tokens that a CTA has at a time
+    if (n_tokens > CLUSTER_ROUNDS * MAX_CLUSTER * round || n_seqs > CLUSTER_SEQS ||
+        cluster_shared_bytes(n_experts, n_seqs) > 47 * 1024)
+        return 0;
+    int32_t c = 1;
+    while (c < MAX_CLUSTER && (n_tokens > 2 * c * round || n_seqs > 2 * c)) c *= 2;
+    return c;
+}
 
 struct BalanceLayout {
-    bool alone;
-    int32_t chunk, chunks, slots, expert_blocks;
+    int32_t cluster, chunk, chunks, slots, expert_blocks;
     int64_t part, tokens, dots, zsum, done, bytes;
 };
 
 BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
     BalanceLayout l;
-    l.alone = n_tokens <= ALONE_TOKENS && n_seqs <= ALONE_SEQS;
-    l.chunk = l.alone ? ALONE_TOKENS : chunk_tokens(n_tokens, WARPS);
+    l.cluster = balance_cluster(n_tokens, n_experts, n_seqs);
+    l.chunk = l.cluster ? static_cast<int32_t>((n_tokens + l.cluster - 1) / l.cluster) : chunk_tokens(n_tokens, n_tokens < int64_t{WARPS} * n_seqs ? 4 : WARPS);   // (short sequences are rounds, too)
     if (l.chunk == 0) l.chunk = WARPS;
-    l.chunks = static_cast<int32_t>((n_tokens + l.chunk - 1) / l.chunk);
+    l.chunks = l.cluster ? l.cluster : static_cast<int32_t>((n_tokens + l.chunk - 1) / l.chunk);
     if (l.chunks == 0) l.chunks = 1;
     l.slots = l.chunks + n_seqs;
     l.expert_blocks = (n_experts + 31) / 32;
@@ -774,8 +890,30 @@ BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs
     l.dots = take(int64_t{8} * n_seqs * l.expert_blocks);
     l.zsum = take(int64_t{8} * n_seqs);
     l.done = take(4);
-    l.bytes = l.alone ? 0 : at;
+    l.bytes = l.cluster ? 0 : at;
     return l;
+}
+
+// Clusters of more than 8 CTAs have to be allowed, once per device.
+cudaError_t balance_clusters_allowed() {
+    struct Entry {
+        std::once_flag once;
+        cudaError_t err = cudaSuccess;
+    };
+    constexpr int MAX_DEVICES = 16;
+    static Entry table[MAX_DEVICES];
+    int dev = 0;
+    const cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
+    Entry& r = table[dev];
+    std::call_once(r.once, [&r] {
+        for (auto kernel : {balance_cluster_kernel<32, 32, true>, balance_cluster_kernel<32, 32, false>,
+                            balance_cluster_kernel<16, 16, false>, balance_cluster_kernel<16, 16, true>,
+                            balance_cluster_kernel<8, 16, true>, balance_cluster_kernel<4, 16, true>})
+            if (r.err == cudaSuccess) r.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    return r.err;
 }
 
 }  // namespace
@@ -791,7 +929,6 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     p.r = a.r;
     p.chunk = l.chunk;
     p.n_slots = l.slots;
-    p.alone = l.alone ? 1 : 0;
     p.part = reinterpret_cast<float2*>(ws + l.part);
     p.tokens = reinterpret_cast<float2*>(ws + l.tokens);
     p.dots = reinterpret_cast<Sum*>(ws + l.dots);
@@ -803,14 +940,26 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     p.status = a.status;
     const int32_t E = a.r.n_experts;
     const bool vec = E % 4 == 0;
+    const int lanes = balance_lanes(E);
+    if (l.cluster) {
+        const cudaError_t ready = balance_clusters_allowed();
+        if (ready != cudaSuccess) return ready;
+        auto kernel = lanes == 32   ? (vec ? balance_cluster_kernel<32, 32, true> : balance_cluster_kernel<32, 32, false>)
+                      : !vec        ? balance_cluster_kernel<16, 16, false>
+                      : lanes == 16 ? balance_cluster_kernel<16, 16, true>
+                      : lanes == 8  ? balance_cluster_kernel<8, 16, true>
+                                    : balance_cluster_kernel<4, 16, true>;
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(l.cluster)), THREADS,
+                          static_cast<size_t>(cluster_shared_bytes(E, a.r.n_seqs)), stream, p, l.cluster);
+    }
     const size_t smem = static_cast<size_t>(HALF + 1) * E * 4;
-    auto kernel = E > 256 ? (vec ? balance_kernel<32, 32, true> : balance_kernel<32, 32, false>)
-                : !vec    ? balance_kernel<16, 16, false>
-                : E > 128 ? balance_kernel<16, 16, true>
-                : E > 64  ? balance_kernel<8, 16, true>
-                          : balance_kernel<4, 16, true>;
-    cudaError_t err = launch_pdl(kernel, dim3(static_cast<unsigned>(l.chunks)), THREADS, smem, stream, p);
-    if (err != cudaSuccess || l.alone) return err;
+    auto kernel = lanes == 32   ? (vec ? balance_kernel<32, 32, true> : balance_kernel<32, 32, false>)
+                  : !vec        ? balance_kernel<16, 16, false>
+                  : lanes == 16 ? balance_kernel<16, 16, true>
+                  : lanes == 8  ? balance_kernel<8, 16, true>
+                                : balance_kernel<4, 16, true>;
+    const cudaError_t err = launch_pdl(kernel, dim3(static_cast<unsigned>(l.chunks)), THREADS, smem, stream, p);
+    if (err != cudaSuccess) return err;
     return launch_pdl(balance_reduce_kernel, dim3(static_cast<unsigned>(l.expert_blocks), static_cast<unsigned>(a.r.n_seqs)),
                       32 * REDUCE_WARPS, 0, stream, p);
 }

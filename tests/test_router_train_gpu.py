@@ -80,7 +80,8 @@ def reference(s):
 SHAPES = [(1, 1, 1, 1, False), (1, 4, 2, 1, False), (2, 3, 3, 1, True), (7, 5, 1, 2, False), (31, 64, 6, 1, True),
           (32, 128, 8, 1, False), (33, 130, 8, 3, True), (64, 256, 16, 1, False), (129, 257, 4, 2, True),
           (300, 1024, 8, 5, True), (301, 1021, 16, 1, False), (1000, 60, 6, 400, True), (4097, 64, 6, 5, True),
-          (9000, 255, 8, 1, True), (16384, 256, 8, 4, False)]
+          (9000, 255, 8, 1, True), (16384, 256, 8, 4, False), (66, 64, 6, 31, True), (5000, 48, 4, 32, True),
+          (2048, 200, 8, 1, False), (1500, 1000, 8, 1, True), (700, 129, 8, 9, False), (1025, 128, 6, 3, True), (70, 96, 6, 50, True), (16, 1024, 8, 16, False)]
 
 
 @pytest.mark.parametrize("T,E,k,seqs,masked", SHAPES)

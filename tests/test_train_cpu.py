@@ -18,7 +18,7 @@ def L():
     return moe.lib()
 
 
-BAL = dict(z=0x1000, ids=0x2000, T=500, E=24, k=3, mask=0x3000, offs=0x4000, S=4, losses=0x5000, counts=0x6000, tokens=0x7000,
+BAL = dict(z=0x1000, ids=0x2000, T=50000, E=24, k=3, mask=0x3000, offs=0x4000, S=4, losses=0x5000, counts=0x6000, tokens=0x7000,
            ws=0x8000, n=1 << 20)
 
 
@@ -51,9 +51,9 @@ def test_balance_refusals(L):
     sizes(bal, L)
     for key in ("losses", "counts", "tokens"):
         assert bal(L, **{key: None}) == NULL
-    need = L.moe_router_balance_workspace_bytes(500, 24, 4)
+    need = L.moe_router_balance_workspace_bytes(50000, 24, 4)
     assert L.moe_router_balance_workspace_bytes(64, 24, 2) == 0                # needs none
-    assert L.moe_router_balance_workspace_bytes(64, 24, 3) > 0 and L.moe_router_balance_workspace_bytes(65, 24, 1) > 0
+    assert L.moe_router_balance_workspace_bytes(64, 24, 400) > 0 and L.moe_router_balance_workspace_bytes(1 << 20, 24, 1) > 0
     assert need > 0 and bal(L, n=need - 1) == WORKSPACE
     for bad in ((-1, 24, 4), (500, 0, 4), (500, 1025, 4), (500, 24, 0), (500, 24, 65536), ((1 << 24) + 1, 24, 1)):
         assert L.moe_router_balance_workspace_bytes(*bad) == -1
