@@ -63,7 +63,7 @@ constexpr float B_SCALE = 64.0f;
 constexpr float LO_SCALE = 8192.0f;         // lo = (x - hi)·2^13
 constexpr float MAX_A_SCALE = 1024.0f;      // of A, less where s is large
 constexpr int SUM_THREADS = 256;
-constexpr int SUM_VALUES = 8192;            // that a block sums at least
+constexpr int SUM_VALUES = 2048;            // that a block sums at least
 constexpr int MAX_SUM_BLOCKS = 512;         // of one matrix
 
 // ---------------------------------------------------------------------------
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(SUM_THREADS) square_sum_kernel(const Prepare p
             for (int j = 0; j < PER; ++j) sum += v[j] * v[j];
         }
     } else {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t i = first; i < p.elements; i += step) {
             const float v = value_at<DTYPE>(base, i);
             sum += v * v;
