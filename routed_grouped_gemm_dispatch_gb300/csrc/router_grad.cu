@@ -14,6 +14,11 @@
 //    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
 //    memory first.
 //
+// Bound: HBM.  16384 x 256 x 7168 moves 467 MB in these products (255 read, 212 written), at 4.5 TB/s over
+// a launch of 103 us (cold, by itself) with the tensor pipe 51% busy; the whole call takes 124 as a graph, its
+// bytes 73 at the rate of a copy.  4097 x 64 x 2048 takes 23.6 (bytes 5.2) and 32 x 128 x 2048 12.1 (0.2):
+// the chain of launches, fill, K loop and stores.
+//
 // Rounding: d_x and d_W once from fp32.  d_z, an operand of 16-bit products, once too where there are many
 // tokens: over thousands of them its roundings add half as much again as that of the result to the
 // mean square (the root mean square error of either output is √2 of a single rounding's, 2.4e-3 in bf16).

@@ -12,6 +12,12 @@
 // registers until the end of a piece.  All is read once.  Sums over tokens are fp32 over the
 // tokens of a warp and of a block and pairs of fp32 (Sum) beyond, always in the same
 // order.  (FP64 is slow here: with it the second launch took 16 us, by itself, for 32 tokens.)
+//
+// Bound: latency.  The losses of 16384 x 256 (17 MB, 2.6 us of HBM) take 16.6 us in two launches: a block's 64
+// tokens are two rounds of loads, exponentials and sums over lanes, then come its warps' sums, and a
+// second launch that waits for the first, reads the parts and counts its blocks.  One cluster needs no second
+// launch: 4097 x 64 in five sequences 9.4 us, 32 x 128 4.0.  The gradients of 16384 x 256 logits take
+// 15 us cold (34 MB), their rounding 8.5.
 #include <cuda_runtime.h>
 
 #include <cstdint>
