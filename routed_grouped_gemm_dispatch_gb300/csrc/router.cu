@@ -85,8 +85,8 @@ struct RouterParams {
     int32_t off_bars;
     int32_t* topk_ids;
     float* topk_weights;
-    float* logits;         // nullable: [n_tokens, n_experts]
     int32_t* status;
+    float* logits;         // LOGITS: [n_tokens, n_experts]
 };
 
 // Shared-memory layout for n_pad experts, S CTAs per cluster (or a pair that
@@ -197,7 +197,8 @@ __device__ __forceinline__ void merge_topk(float (&v)[K], int32_t (&e)[K], const
 // (>= top_k).  PAIR (with S = 1): clusters of two CTAs, each with its own
 // tile, share one 2-SM MMA of M = 256 tokens: each CTA loads its tile's x
 // and half of W_g's rows, so each SM receives a third fewer bytes.
-template <int S, int KMAX, bool PAIR>
+// LOGITS: also stores the logits (of its own, as the branch alone took 2% of the others' time).
+template <int S, int KMAX, bool PAIR, bool LOGITS>
 __global__ void __launch_bounds__(R_THREADS, 1)
 router_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
               const RouterParams p) {
@@ -617,7 +618,7 @@ router_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 }
             }
             // the logits themselves, for a loss and its gradient
-            if (p.logits != nullptr && live) {
+            if (LOGITS && live) {
                 float* out = p.logits + t * n_e;
                 for (int q = 0; q < nq; ++q) {
                     const float4 v = chunk(q);
@@ -679,6 +680,21 @@ bool router_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, 
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool LOGITS>
+auto router_kernel_for(int kmax, int64_t sp, bool pair) {
+    if (pair)
+        return kmax == 4 ? router_kernel<1, 4, true, LOGITS>
+             : kmax == 8 ? router_kernel<1, 8, true, LOGITS> : router_kernel<1, 16, true, LOGITS>;
+    if (kmax == 4)
+        return sp >= 8 ? router_kernel<8, 4, false, LOGITS> : sp == 4 ? router_kernel<4, 4, false, LOGITS>
+             : sp == 2 ? router_kernel<2, 4, false, LOGITS> : router_kernel<1, 4, false, LOGITS>;
+    if (kmax == 8)
+        return sp >= 8 ? router_kernel<8, 8, false, LOGITS> : sp == 4 ? router_kernel<4, 8, false, LOGITS>
+             : sp == 2 ? router_kernel<2, 8, false, LOGITS> : router_kernel<1, 8, false, LOGITS>;
+    return sp >= 8 ? router_kernel<8, 16, false, LOGITS> : sp == 4 ? router_kernel<4, 16, false, LOGITS>
+         : sp == 2 ? router_kernel<2, 16, false, LOGITS> : router_kernel<1, 16, false, LOGITS>;
+}
+
 }  // namespace
 
 cudaError_t launch_router(const uint16_t* x, int64_t n_tokens, int32_t hidden, const uint16_t* router_w,
@@ -723,17 +739,9 @@ cudaError_t launch_router(const uint16_t* x, int64_t n_tokens, int32_t hidden, c
            layout_for(split * 2, false, &L))
         split *= 2;
     const int kmax = top_k <= 4 ? 4 : top_k <= 8 ? 8 : 16;
-    auto kernel_for = [kmax](int64_t sp, bool pair) {
-        if (pair) return kmax == 4 ? router_kernel<1, 4, true> : kmax == 8 ? router_kernel<1, 8, true>
-                                                                             : router_kernel<1, 16, true>;
-        if (kmax == 4)
-            return sp >= 8 ? router_kernel<8, 4, false> : sp == 4 ? router_kernel<4, 4, false>
-                 : sp == 2 ? router_kernel<2, 4, false> : router_kernel<1, 4, false>;
-        if (kmax == 8)
-            return sp >= 8 ? router_kernel<8, 8, false> : sp == 4 ? router_kernel<4, 8, false>
-                 : sp == 2 ? router_kernel<2, 8, false> : router_kernel<1, 8, false>;
-        return sp >= 8 ? router_kernel<8, 16, false> : sp == 4 ? router_kernel<4, 16, false>
-             : sp == 2 ? router_kernel<2, 16, false> : router_kernel<1, 16, false>;
+    const bool keep = logits != nullptr;
+    auto kernel_for = [kmax, keep](int64_t sp, bool pair) {
+        return keep ? router_kernel_for<true>(kmax, sp, pair) : router_kernel_for<false>(kmax, sp, pair);
     };
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -747,11 +755,11 @@ cudaError_t launch_router(const uint16_t* x, int64_t n_tokens, int32_t hidden, c
     // a cluster shape the device can place (clusters live inside one GPC);
     // the answer is cached per device, kernel and shared-memory size
     static std::mutex mu;
-    static std::map<std::tuple<int, int, int64_t, bool, size_t>, bool> placeable;
+    static std::map<std::tuple<int, int, int64_t, bool, bool, size_t>, bool> placeable;
     auto placeable_for = [&](int64_t sp, bool pair) -> int {   // 1 yes, 0 no, -1 error
         const int64_t cl = pair ? 2 : sp;
         std::lock_guard<std::mutex> lock(mu);
-        const auto key = std::make_tuple(dev, kmax, sp, pair, L.smem);
+        const auto key = std::make_tuple(dev, kmax, sp, pair, keep, L.smem);
         auto it = placeable.find(key);
         if (it == placeable.end()) {
             if (cudaFuncSetAttribute(kernel_for(sp, pair), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
