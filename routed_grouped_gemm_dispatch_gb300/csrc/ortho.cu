@@ -33,11 +33,11 @@
 //    and e4m3 (hi alone is the products' operand).
 // Bound.  A stack: the operands' way from L2, whose 0.2 us for 64 along K of a 256 x 128 tile is 1.6 PFLOP/s
 // on all pairs (0.326 and 2.0 for 256 x 256), and the tiles' empty rows (1408 are 5.5 panels); 64 x
-// 1408 x 2048 takes 3.68 ms where its operations are 2.45 at the measured rate of bf16, and 4.2 back to back under the
-// power cap.  One matrix: besides, each product waits for the one before, with some 7 us from its
-// operands' completion to its own where it has few tiles (poll, fill, K loop, epilogue, publishing), and
-// few whole rounds of tiles: 2816 x 2048 272 us (operations 113), 2048 x 7168 439 (253), 3 x 333 x 1001
-// 115 (2.8).
+// 1408 x 2048 takes 3.65 ms where its operations are 2.45 at the measured rate of bf16, and 4.1 back to back under the
+// power cap.  One matrix: besides, each product waits for the one before, with some 6.5 us from its
+// operands' completion to its own where it has few tiles (a poll that sees it 1.4, copies and K loop 2 to 3.5,
+// epilogue 1.5 to 2, publishing 0.8), and few whole rounds of tiles: 2816 x 2048 261 us (operations 113),
+// 2048 x 7168 426 (253), 3 x 333 x 1001 108 (2.8).
 //
 // In 64-bit simulation with these roundings, the root mean square error of five steps relative to that
 // of the result:
