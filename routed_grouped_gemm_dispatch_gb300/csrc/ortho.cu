@@ -34,10 +34,10 @@
 // Bound.  A stack: the operands' way from L2, whose 0.2 us for 64 along K of a 256 x 128 tile is 1.6 PFLOP/s
 // on all pairs (0.326 and 2.0 for 256 x 256), and the tiles' empty rows (1408 are 5.5 panels); 64 x
 // 1408 x 2048 takes 3.65 ms where its operations are 2.45 at the measured rate of bf16, and 4.1 back to back under the
-// power cap.  One matrix: besides, each product waits for the one before, with some 6.5 us from its
+// power cap.  One matrix: besides, each product waits for the one before, with some 6.3 us from its
 // operands' completion to its own where it has few tiles (a poll that sees it 1.4, copies and K loop 2 to 3.5,
-// epilogue 1.5 to 2, publishing 0.8), and few whole rounds of tiles: 2816 x 2048 261 us (operations 113),
-// 2048 x 7168 426 (253), 3 x 333 x 1001 108 (2.8).
+// epilogue 1.5, publishing 0.7), and few whole rounds of tiles: 2816 x 2048 257 us (operations 113),
+// 2048 x 7168 422 (253), 3 x 333 x 1001 104 (2.8).
 //
 // In 64-bit simulation with these roundings, the root mean square error of five steps relative to that
 // of the result:
@@ -553,14 +553,14 @@ struct OrthoOp {
         return ok;
     }
     // By one thread, which has waited for those that stored: this CTA's part of the tile is there, for TMA
-    // loads and for the other SMs.
+    // loads and for the other SMs.  (One fence for both counters: two releases, 3 x 333 x 1001 107 us instead of 104.)
     static __device__ __forceinline__ void publish(const Params& p, const Code& code) {
         const Place at = place(code);
         if (at.kind == APPLY && at.step + 1 == p.steps) return;
         auto add_one = [&](int32_t panel) {
-            asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter(p, at.matrix, at.kind, panel)) : "memory");
+            asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(counter(p, at.matrix, at.kind, panel)) : "memory");
         };
-        asm volatile("fence.proxy.async.global;" ::: "memory");
+        asm volatile("fence.proxy.async.global;\n\tfence.acq_rel.gpu;" ::: "memory");
         add_one(at.i);
         const int32_t across = panel_of(p, at.j);
         if (at.kind != APPLY && across != at.i) add_one(across);
