@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    cluster_arrive_relaxed();      // this CTA runs; the others may write into its shared memory
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_mem, 0);
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) part[warp] = sum;
     __syncthreads();
+    cluster_wait_acquire();        // all CTAs of the cluster run (asked for ahead of the loads of X)
     if (tid < static_cast<int>(C)) {
         sum = 0.0f;
         for (int w = 0; w < THREADS / 32; ++w) sum += part[w];
