@@ -734,6 +734,7 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
         if (p.d_weights) {
             __syncwarp();
             if (id >= 0) mine[id] = base;
+            __syncwarp();                                         // before the next token's lanes read or replace it
         }
         const float lse = softmax_row<L, PER>(z);
         float dot = 0.0f;
