@@ -530,9 +530,9 @@ int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t c
  * Any rows and cols.  Products are of fp16 operands with fp32 sums: with such coefficients the result is
  * within 2e-3 to 3e-3 of the exact one (root mean square, relative to that of the exact one, rounding to
  * bf16 included) whatever G's spectrum, so no finer type is offered.  A matrix that holds an infinity or
- * a NaN, or whose norm leaves fp32's squares (1.8e19), becomes NaN; one of zeros stays zeros (values
- * below 1e-22, whose squares are below fp32's, count as zeros in the norm); the others of the stack do
- * not see it.  Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c|
+ * a NaN, or whose norm leaves fp32's squares (1.8e19), becomes NaN; one of zeros stays zeros, whatever
+ * eps is (0 too); the others of the stack do not see it.  The norm is taken as at least
+ * 2^-69·√(rows·cols), that of entries of 1.7e-21, below which fp32's squares do not give it.  Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c|
  * unless c is 0; where they let a norm grow past 2^9 the result overflows.
  * batch·steps·ceil(rows/128)·ceil(cols/128) is at most 2^29.
  * workspace: device memory of moe_orthogonalize_workspace_bytes() bytes, caller-owned;

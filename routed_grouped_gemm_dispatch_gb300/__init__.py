@@ -916,7 +916,8 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     with A = X·Xᵀ and a, b, c the ``coefficients``: the singular vectors stay and the
     singular values come near 1.  ``update`` [rows, cols] or a stack [batch, rows, cols] of any sizes,
     float16, bfloat16 or float32 (a gradient, or a momentum); returns bfloat16 of its shape
-    (``out`` may be supplied).  Each matrix of a stack is taken by itself.  Products
+    (``out`` may be supplied).  Each matrix of a stack is taken by itself; one of zeros stays zeros
+    whatever ``eps`` is (a norm is taken as at least that of entries of 1.7e-21).  Products
     are of 16-bit operands with fp32 sums: the result is within 2e-3 to 3e-3 of the exact one, root mean
     square, bf16's own rounding included.  ``out`` does not overlap ``update``.
     ``workspace``: a device tensor of at least orthogonalize_workspace_bytes(batch, rows, cols) bytes."""

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/moe_gb300.h"
@@ -670,7 +671,8 @@ moe_status_t moe_orthogonalize(int32_t dtype, const void* update, int64_t batch,
     if (!workspace || static_cast<int64_t>(workspace_bytes) < moe_orthogonalize_workspace_bytes(batch, rows, cols))
         return MOE_ERR_WORKSPACE;
     if (moe_status_t s = check_device()) return s;
-    moe::Orthogonalize o{dtype, update, batch, rows, cols, steps, a, b, c, eps, out, workspace, status_dev};
+    const float least = moe::ORTHO_LEAST_VALUE * std::sqrt(static_cast<float>(rows) * static_cast<float>(cols));
+    moe::Orthogonalize o{dtype, update, batch, rows, cols, steps, a, b, c, eps > least ? eps : least, out, workspace, status_dev};
     return from_cuda(moe::launch_orthogonalize(o, static_cast<cudaStream_t>(stream)));
 }
 

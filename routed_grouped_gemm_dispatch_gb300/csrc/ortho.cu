@@ -117,7 +117,7 @@ struct Prepare {
     int64_t elements;             // of a matrix
     int32_t M, N, ld, ld_lo;      // X is [M, ld], N of the columns in use
     int32_t sum_blocks;
-    float eps;
+    float least_norm;
     float* sums;                  // [batch, sum_blocks]
     float* rest;                  // [batch]: what X₀ still has to be times
     uint16_t* hi;                 // [batch, M, ld]
@@ -178,14 +178,12 @@ __device__ __forceinline__ Norm norm_of(const Prepare& p, int64_t matrix, float*
     sum = 0.0f;
     for (int w = 0; w < SUM_THREADS / 32; ++w) sum += part[w];
     float norm = sqrtf(sum);
-    if (norm < p.eps) norm = p.eps;                           // a NaN stays
-    Norm n{0.0f, 0.0f};
-    if (norm != 0.0f) {
-        int e = 0;
-        n.rest = __int_as_float(0x7fffffff);                  // infinite (or NaN): so is the result, NaN
-        if (norm <= 3.4e38f) n.rest = 1.0f / frexpf(norm, &e);    // norm = f·2^e, f in [0.5, 1)
-        n.power = ldexpf(1.0f, X_EXPONENT - e);
-    }
+    if (norm < p.least_norm) norm = p.least_norm;             // a NaN stays
+    int e = 0;
+    Norm n;
+    n.rest = __int_as_float(0x7fffffff);                      // infinite (or NaN): so is the result, NaN
+    if (norm <= 3.4e38f) n.rest = 1.0f / frexpf(norm, &e);    // norm = f·2^e, f in [0.5, 1), e >= -69
+    n.power = ldexpf(1.0f, X_EXPONENT - e);
     return n;
 }
 
@@ -915,7 +913,7 @@ cudaError_t launch_orthogonalize(const Orthogonalize& a, cudaStream_t stream) {
     pr.ld = l.ld_x;
     pr.ld_lo = l.ld_lo;
     pr.sum_blocks = l.sum_blocks;
-    pr.eps = a.eps;
+    pr.least_norm = a.least_norm;
     pr.sums = reinterpret_cast<float*>(ws + l.sums);
     pr.rest = reinterpret_cast<float*>(ws + l.rest);
     pr.hi = u16(l.hi[0]);

@@ -63,7 +63,7 @@ struct Small {
     int32_t M, N;                 // of X
     int32_t cols;                 // a CTA's columns, a multiple of 64
     int32_t steps;
-    float a, b, c, eps;
+    float a, b, c, least_norm;
     int32_t tall;                 // update is [N, M]
     uint16_t* out;
     int32_t* status;
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
     sum = 0.0f;
     for (uint32_t i = 0; i < C; ++i) sum += sums[i];
     float norm = sqrtf(sum);
-    if (norm < p.eps) norm = p.eps;                       // a NaN stays
-    float to_x = norm > 0.0f ? X_SCALE / norm : 0.0f;     // times a value: X₀·2^6
+    if (norm < p.least_norm) norm = p.least_norm;         // a NaN stays
+    float to_x = X_SCALE / norm;                          // times a value: X₀·2^6 (at most 2^75)
     if (!(norm <= 3.4e38f)) to_x = __int_as_float(0x7fffffff);
     // a chunk of 32 columns: the operand to shared memory, and a times it (as the sums of B·hi come: times
     // B_SCALE) to TMEM
@@ -249,11 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Small p) 
         tmem_ld_wait();
         float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            // (a small value times a large factor: in two steps, as the factor alone may be infinite)
-            const float x = __uint_as_float(t[i]);
-            v[i] = norm < 1e-30f ? (norm > 0.0f ? x / norm * X_SCALE : 0.0f) : x * to_x;
-        }
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(t[i]) * to_x;
         keep(col, v, p.steps == 1);
     }
 
@@ -530,7 +526,7 @@ cudaError_t launch_small(const Orthogonalize& o, cudaStream_t stream) {
     p.a = o.a;
     p.b = o.b;
     p.c = o.c;
-    p.eps = o.eps;
+    p.least_norm = o.least_norm;
     p.tall = tall ? 1 : 0;
     p.out = o.out;
     p.status = o.status;

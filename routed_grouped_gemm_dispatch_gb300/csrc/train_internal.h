@@ -75,13 +75,16 @@ struct Orthogonalize {
     int32_t rows, cols;
     int32_t steps;
     float a, b, c;
-    float eps;
+    float least_norm;             // what a norm is taken as at least: eps, or ORTHO_LEAST_VALUE in every entry
     uint16_t* out;                // [batch, rows, cols], bf16
     void* workspace;
     int32_t* status;
 };
 
 constexpr float ORTHO_MAX_SHIFT = 1024.0f;         // |b / 2c|, where c is not 0
+// 2^-69: squares of smaller values have fewer than 11 bits in fp32 (its steps are 2^-149), and a norm of theirs
+// means nothing; one that is too small would let X₀ overflow.
+constexpr float ORTHO_LEAST_VALUE = 1.6940658945086007e-21f;
 int64_t orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t cols);
 // Matrices of at most 128 rows or columns, by a cluster each; cudaErrorNotSupported where the device
 // cannot place one.

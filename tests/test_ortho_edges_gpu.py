@@ -25,3 +25,28 @@ def test_blocks_that_start_apart(batch, rows, cols):
         got.append(moe.orthogonalize(u))
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+TINY = 2.0 ** -69                # a root mean square below which fp32's squares no longer give the norm
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, torch.finfo(torch.float32).tiny, 2.0 ** -122, 1e-30, 1e-7])
+@pytest.mark.parametrize("rows,cols", [(64, 96), (130, 200), (400, 150)])
+def test_zeros_whatever_eps(rows, cols, eps):
+    """A matrix of zeros stays zeros however small eps is, and its neighbour is what it is."""
+    for dt in (torch.float32, torch.bfloat16):
+        u = ortho.draw("normal", 2, rows, cols, dt)
+        want = moe.orthogonalize(u)
+        u[0] = 0
+        got = moe.orthogonalize(u, eps=eps)
+        assert not got[0].any() and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("size", [1e-19, 1e-20, 5e-22, 3e-23])
+@pytest.mark.parametrize("rows,cols", [(64, 96), (130, 200), (400, 150)])
+def test_values_whose_squares_leave_fp32(rows, cols, size):
+    """The norm is no less than that of entries of 2^-69, so nothing is divided by a norm that fp32 lost.  Squares of
+    2^-138 are off by 2^-12 of themselves at most (fp32 has steps of 2^-149), which moves the norm and the first X by half of
+    that: below the roundings that the tolerance already counts."""
+    u = ortho.draw("normal", 2, rows, cols, torch.float32, size=size)
+    ortho.check(u, moe.orthogonalize(u, eps=0.0), eps=TINY * (rows * cols) ** 0.5)
