@@ -465,6 +465,7 @@ int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, 
  *     losses[1]    = 1/T · Σ_t logsumexp(z[t])²
  * With one sequence losses[0] is E·Σ_e f_e·P_e, f_e the share of pairs and P_e the mean
  * probability of expert e; with several, the mean of theirs weighted by T_s.  Both are 0 where T is.
+ * losses[1] is infinite where the sum of squares leaves fp32 (a row of the type's lowest value, say).
  *   logits      [n_tokens, n_experts] fp32 (moe_router_topk_logits'), 16-byte aligned
  *   topk_ids    [n_tokens, top_k] int32
  *   losses      out: [2] fp32

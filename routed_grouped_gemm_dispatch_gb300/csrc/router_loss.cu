@@ -132,13 +132,15 @@ struct Seqs {
     }
 };
 
-// An fp32 sum with what its additions lost (an exact sum of two, and of a product).
+// An fp32 sum with what its additions lost (an exact sum of two, and of a product).  Once it is infinite it stays so:
+// there is nothing that an infinity lost.
 struct Sum {
     float hi = 0.0f, lo = 0.0f;
     __device__ __forceinline__ void add(float x) {
         const float s = __fadd_rn(hi, x);
         const float b = __fsub_rn(s, hi);
-        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        const float lost = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        lo += fabsf(s) == INFINITY ? 0.0f : lost;
         hi = s;
     }
     __device__ __forceinline__ void add(const Sum& o) {

@@ -38,3 +38,15 @@ def test_neighbouring_tokens_share_experts(T, E, k, seqs, dtype):
             moe.router_backward(x, w, s["z"], s["ids"], a, b, counts if b is not None else None,
                                 tokens if b is not None else None, d_logits=again, **kw)
             assert torch.equal(again, d_logits)
+
+
+@pytest.mark.parametrize("T,E,seqs", [(5, 12, 1), (700, 64, 3), (40000, 64, 2), (2000, 1000, 40)])
+def test_a_row_of_lowest_values(T, E, seqs):
+    """Its logsumexp squared is beyond fp32: the z loss is infinite, as the formula's is once rounded, and nothing else is."""
+    s = router.make(T, E, 2, seqs, seed=T)
+    s["z"][T // 2] = torch.finfo(torch.float32).min
+    losses, counts, tokens = moe.router_balance(s["z"], s["ids"], seq_offsets=s["offs"])
+    want, c, n, tol = router.reference(s)
+    assert want[1] > 1e70 and float(losses[1]) == float("inf")
+    assert abs(float(losses[0]) - want[0]) <= tol[0]
+    assert (counts.cpu().numpy() == c).all() and (tokens.cpu().numpy() == n).all()
