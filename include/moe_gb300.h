@@ -448,7 +448,7 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
  * hold.  Below, T is the number of tokens that count, T_s that of sequence s, k = top_k,
  * E = n_experts, z the logits, p = softmax(z); a logit of -infinity has p = 0, and a token with
  * no other (p = 0 everywhere) adds nothing but its T and its ids.  Offsets that decrease or leave the range
- * set MOE_DEV_BAD_TABLE and leave the outputs undefined.  No output overlaps an input, another output or the
+ * set MOE_DEV_BAD_TABLE (in every call that has tokens) and leave the outputs undefined.  No output overlaps an input, another output or the
  * workspace.  Negative ids (moe_router_topk's for a token with too few
  * ranked logits) are skipped, ids >= n_experts too, which set MOE_DEV_BAD_EXPERT_ID.
  * ------------------------------------------------------------------------- */

@@ -776,6 +776,13 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
             }
         }
     }
+    if (p.r.seq_offsets && p.status) {
+        for (int32_t i = static_cast<int32_t>(blockIdx.x) * THREADS + static_cast<int32_t>(threadIdx.x); i < p.r.n_seqs;
+             i += static_cast<int32_t>(gridDim.x) * THREADS) {
+            const int32_t lo = __ldg(p.r.seq_offsets + i), hi = __ldg(p.r.seq_offsets + i + 1);
+            if (lo > hi || lo < 0 || hi > p.r.n_tokens) atomicOr(p.status, MOE_DEV_BAD_TABLE);
+        }
+    }
     if (p.valid) {
         // a bit per token that counts; whole steps of 64, zero past the end
         uint32_t bad = 0;

@@ -50,3 +50,24 @@ def test_a_row_of_lowest_values(T, E, seqs):
     assert want[1] > 1e70 and float(losses[1]) == float("inf")
     assert abs(float(losses[0]) - want[0]) <= tol[0]
     assert (counts.cpu().numpy() == c).all() and (tokens.cpu().numpy() == n).all()
+
+
+BAD_OFFSETS = [[0, 60, 30, 100], [0, 101], [-1, 100], [0, 2 ** 31 - 1], [-2 ** 31, 50, 100]]
+
+
+@pytest.mark.parametrize("offs", BAD_OFFSETS + [list(range(0, 90, 2)) + [80, 100]])
+def test_bad_offsets_are_reported_by_both(offs):
+    """By the losses in one launch (few sequences) and in two, and by the gradients."""
+    T, E, k = 100, 32, 4
+    for extra in (0, 20000):
+        s = router.make(T + extra, E, k, seed=2)
+        o = torch.tensor([v + extra if v >= 0 and v < 2 ** 31 - 1 and i == len(offs) - 1 else v for i, v in enumerate(offs)],
+                         dtype=torch.int32, device="cuda")
+        x, w = torch.zeros((T + extra, 8), device="cuda").half(), torch.zeros((E, 8), device="cuda").half()
+        dw = torch.zeros((T + extra, k), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        _, counts, tokens = moe.router_balance(s["z"], s["ids"], seq_offsets=o, status=status)
+        assert int(status) == moe.MOE_DEV_BAD_TABLE
+        status.zero_()
+        moe.router_backward(x, w, s["z"], s["ids"], dw, seq_offsets=o, status=status)
+        assert int(status) == moe.MOE_DEV_BAD_TABLE
