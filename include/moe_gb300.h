@@ -490,8 +490,8 @@ int64_t moe_router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts,
  *     d_x        = round16( round16(d_z)·router_w )     [n_tokens, hidden]
  *     d_router_w = round16( round16(d_z)ᵀ·x )           [n_experts, hidden]
  * All 16-bit arrays are of `dtype` (MOE_DTYPE_F16 or _BF16).  (In fp16 d_z is rounded times a
- * power of two that depends on its largest magnitude, so none of it is lost to fp16's range; up to 2048
- * tokens, where a rounding of d_z would not average out, it is not rounded but held in two terms.)
+ * power of two that depends on its largest finite magnitude, so only what is below 2^-38 of that is lost to fp16's
+ * range; up to 2048 tokens, where a rounding of d_z would not average out, it is not rounded but held in two terms.)
  *   x_tokens        [n_tokens, hidden], hidden a multiple of 8, at most MOE_FFN_MAX_WIDTH
  *   router_w        [n_experts, hidden]
  *   logits, topk_ids as in moe_router_balance

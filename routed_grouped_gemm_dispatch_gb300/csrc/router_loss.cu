@@ -584,7 +584,7 @@ struct GradParams {
 // 2^s that brings a largest magnitude m into [2^13, 2^14): fp16 then holds values down to
 // 2^-27 of it with all their bits, and sums of products stay far inside fp32.
 __device__ __forceinline__ float grad_scale(float m) {
-    if (!(m > 0.0f) || m > 3.0e38f) return 1.0f;
+    if (!(m > 0.0f)) return 1.0f;
     int x;
     frexpf(m, &x);
     const int s = 14 - x;
@@ -743,11 +743,14 @@ __global__ void __launch_bounds__(THREADS, PER <= 16 ? 2 : 1) logit_gradient_ker
 #pragma unroll
         for (int i = 0; i < PER; ++i) dot += z[i] * d[i];
         const float shift = cz * lse - lanes_sum<L>(dot);
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             d[i] = live ? z[i] * (d[i] + shift) : 0.0f;
-            if (!BF16 && expert<L, VEC>(l, i) < E) largest = fmaxf(largest, fabsf(d[i]));
+            if (!BF16 && expert<L, VEC>(l, i) < E) top = fmaxf(top, fabsf(d[i]));
         }
+        // (an infinity, beside which nothing of the token is finite, is one at any scale, and the others keep theirs)
+        if (!BF16 && top < INFINITY) largest = fmaxf(largest, top);
         if (t >= last) continue;
         if (VEC) {
 #pragma unroll

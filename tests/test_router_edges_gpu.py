@@ -71,3 +71,31 @@ def test_bad_offsets_are_reported_by_both(offs):
         status.zero_()
         moe.router_backward(x, w, s["z"], s["ids"], dw, seq_offsets=o, status=status)
         assert int(status) == moe.MOE_DEV_BAD_TABLE
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan"), 3.4e38])
+@pytest.mark.parametrize("T", [200, 5000])
+def test_one_gradient_that_is_not_finite(T, bad):
+    """The other tokens' gradients are as exact beside it as they are without, in fp16 too."""
+    E, k, H = 64, 6, 256
+    s = router.make(T, E, k, seed=4)
+    x, w = torch.randn((T, H), device="cuda").half(), (torch.randn((E, H), device="cuda") * 1e3).half()
+    dw = torch.randn((T, k), device="cuda") * 1e-7
+    hit = T // 2
+    dw[hit, 1] = bad
+    d_x, _ = moe.router_backward(x, w, s["z"], s["ids"], dw)
+    assert not torch.isfinite(d_x[hit].float()).any()
+    others = torch.arange(T, device="cuda") != hit
+    part = {"z": s["z"][others], "ids": s["ids"][others], "mask": None, "offs": None}
+    dz, tol = router.grads_reference(part, dw[others].double().cpu().numpy(), None, None, [T - 1, T - 1])
+    largest = abs(dz).max()
+    if bad == 3.4e38:                   # finite, and so one of those that the common power of two is for
+        largest = abs(router.grads_reference(s, dw.double().cpu().numpy(), None, None, [T, T])[0]).max()
+    # d_z as an operand: in two terms up to 2048 tokens, one rounding beyond, and half of fp16's least step, 2^-25, where the
+    # largest is at 2^13 at least, 2^-38 of it; then 64 products, d_x's own rounding and its least step
+    r, wv = 2.0 ** -11, w.double().cpu().numpy()
+    want = dz @ wv
+    dz_tol = tol + ((r if T > 2048 else r * r) + 2.0 ** -23) * (abs(dz) + tol) + largest * 2.0 ** -38
+    bound = dz_tol @ abs(wv) + (2 * E / 16 + 8) * 2.0 ** -23 * (abs(dz) @ abs(wv))
+    bound += r * (abs(want) + bound) + 2.0 ** -25
+    assert (abs(d_x[others].double().cpu().numpy() - want) <= bound).all()
