@@ -132,22 +132,21 @@ struct Seqs {
     }
 };
 
-// An fp32 sum with what its additions lost (an exact sum of two, and of a product).  Once it is infinite it stays so:
-// there is nothing that an infinity lost.
+// An fp32 sum with what its additions lost (an exact sum of two, and of a product).  What an infinite one lost is NaN,
+// and not part of its value.
 struct Sum {
     float hi = 0.0f, lo = 0.0f;
     __device__ __forceinline__ void add(float x) {
         const float s = __fadd_rn(hi, x);
         const float b = __fsub_rn(s, hi);
-        const float lost = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
-        lo += fabsf(s) == INFINITY ? 0.0f : lost;
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
         hi = s;
     }
     __device__ __forceinline__ void add(const Sum& o) {
         add(o.hi);
         lo += o.lo;
     }
-    __device__ __forceinline__ float value() const { return hi + lo; }
+    __device__ __forceinline__ float value() const { return fabsf(hi) == INFINITY ? hi : hi + lo; }
     __device__ __forceinline__ Sum times(float f) const {
         Sum r;
         r.hi = __fmul_rn(hi, f);
