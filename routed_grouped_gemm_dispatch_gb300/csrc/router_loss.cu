@@ -870,13 +870,14 @@ int balance_lanes(int32_t n_experts) {
 // of all warps of 16 CTAs takes 0.8 to 1.1, and every sequence of a CTA is a round of its own.
 constexpr int32_t CLUSTER_ROUNDS = 4;
 constexpr int32_t CLUSTER_SEQS = 32;
+constexpr int64_t CLUSTER_SHARED_BYTES = 47 * 1024;
 int64_t cluster_shared_bytes(int32_t n_experts, int32_t n_seqs) {
     return int64_t{4} * (HALF + 1) * n_experts + 8 + int64_t{8} * n_seqs * (n_experts + 1);
 }
 int32_t balance_cluster(int64_t n_tokens, int32_t n_experts, int32_t n_seqs) {
     const int64_t round = WARPS * 32 / balance_lanes(n_experts);          // tokens that a CTA has at a time
     if (n_tokens > CLUSTER_ROUNDS * MAX_CLUSTER * round || n_seqs > CLUSTER_SEQS ||
-        cluster_shared_bytes(n_experts, n_seqs) > 47 * 1024)
+        cluster_shared_bytes(n_experts, n_seqs) > CLUSTER_SHARED_BYTES)
         return 0;
     int32_t c = 1;
     while (c < MAX_CLUSTER && (n_tokens > 2 * c * round || n_seqs > 2 * c)) c *= 2;
@@ -912,26 +913,44 @@ BalanceLayout balance_layout(int64_t n_tokens, int32_t n_experts, int32_t n_seqs
     return l;
 }
 
-// Clusters of more than 8 CTAs have to be allowed, once per device.
-cudaError_t balance_clusters_allowed() {
+// The largest cluster, a power of two, that the current device can place of any variant, asked once per device (more
+// than 8 CTAs have to be allowed, and a part of a device may not have room for them); 0 on an error.
+int32_t placeable_cluster() {
     struct Entry {
         std::once_flag once;
-        cudaError_t err = cudaSuccess;
+        int32_t ctas = 0;
     };
     constexpr int MAX_DEVICES = 16;
     static Entry table[MAX_DEVICES];
     int dev = 0;
-    const cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= MAX_DEVICES) return 0;
     Entry& r = table[dev];
     std::call_once(r.once, [&r] {
+        int32_t all = MAX_CLUSTER;
         for (auto kernel : {balance_cluster_kernel<32, 32, true>, balance_cluster_kernel<32, 32, false>,
                             balance_cluster_kernel<16, 16, false>, balance_cluster_kernel<16, 16, true>,
-                            balance_cluster_kernel<8, 16, true>, balance_cluster_kernel<4, 16, true>})
-            if (r.err == cudaSuccess) r.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                            balance_cluster_kernel<8, 16, true>, balance_cluster_kernel<4, 16, true>}) {
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            for (; all > 0; all /= 2) {
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = static_cast<unsigned>(all);
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cudaLaunchConfig_t cfg{};
+                cfg.gridDim = dim3(static_cast<unsigned>(all));
+                cfg.blockDim = dim3(THREADS);
+                cfg.dynamicSmemBytes = CLUSTER_SHARED_BYTES;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) break;
+            }
+        }
+        cudaGetLastError();
+        r.ctas = all;
     });
-    return r.err;
+    return r.ctas;
 }
 
 }  // namespace
@@ -960,15 +979,18 @@ cudaError_t launch_router_balance(const RouterBalance& a, cudaStream_t stream) {
     const bool vec = E % 4 == 0;
     const int lanes = balance_lanes(E);
     if (l.cluster) {
-        const cudaError_t ready = balance_clusters_allowed();
-        if (ready != cudaSuccess) return ready;
+        // (any number of CTAs will do, with more tokens each; there is no workspace for the two launches)
+        const int32_t most = placeable_cluster();
+        if (most == 0) return cudaErrorNoDevice;
+        const int32_t ctas = l.cluster < most ? l.cluster : most;
+        if (ctas < l.cluster) p.chunk = static_cast<int32_t>((a.r.n_tokens + ctas - 1) / ctas);
         auto kernel = lanes == 32   ? (vec ? balance_cluster_kernel<32, 32, true> : balance_cluster_kernel<32, 32, false>)
                       : !vec        ? balance_cluster_kernel<16, 16, false>
                       : lanes == 16 ? balance_cluster_kernel<16, 16, true>
                       : lanes == 8  ? balance_cluster_kernel<8, 16, true>
                                     : balance_cluster_kernel<4, 16, true>;
-        return launch_pdl(kernel, dim3(static_cast<unsigned>(l.cluster)), THREADS,
-                          static_cast<size_t>(cluster_shared_bytes(E, a.r.n_seqs)), stream, p, l.cluster);
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), THREADS,
+                          static_cast<size_t>(cluster_shared_bytes(E, a.r.n_seqs)), stream, p, ctas);
     }
     const size_t smem = static_cast<size_t>(HALF + 1) * E * 4;
     auto kernel = lanes == 32   ? (vec ? balance_kernel<32, 32, true> : balance_kernel<32, 32, false>)
