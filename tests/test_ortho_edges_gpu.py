@@ -50,3 +50,33 @@ def test_values_whose_squares_leave_fp32(rows, cols, size):
     that: below the roundings that the tolerance already counts."""
     u = ortho.draw("normal", 2, rows, cols, torch.float32, size=size)
     ortho.check(u, moe.orthogonalize(u, eps=0.0), eps=TINY * (rows * cols) ** 0.5)
+
+
+# By the widths that the tiles of A and of X get: narrow and wide, wide and narrow, both wide (both narrow: most of
+# test_ortho_gpu), with whole and ragged panels, wide and tall
+WIDTHS = [(5, 130, 7170), (3, 5000, 257), (16, 256, 1704), (16, 513, 520), (24, 520, 513), (16, 513, 700), (16, 701, 513),
+          (40, 400, 520), (8, 1001, 900), (9, 1024, 768)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["normal", "low rank"])
+@pytest.mark.parametrize("batch,rows,cols", WIDTHS)
+def test_tiles_of_every_width(batch, rows, cols, kind, dtype):
+    u = ortho.draw(kind, batch, rows, cols, dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # (a workspace of NaN: nothing of it is read before it is written)
+    ws = torch.full((moe.orthogonalize_workspace_bytes(batch, rows, cols),), 0xFF, dtype=torch.uint8, device="cuda")
+    got = moe.orthogonalize(u, workspace=ws, status=status)
+    ortho.check(u, got)
+    assert int(status) == 0 and torch.equal(got, moe.orthogonalize(u))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 9), (5, 1), (2, 3), (8, 8), (17, 5), (40, 33)])
+def test_many_tiny_matrices(rows, cols):
+    """Matrices with few entries, enough of them for their errors' root mean square to be that of the emulation: the same
+    bound as for large ones, over all."""
+    u = ortho.draw("normal", 4000 // min(rows, cols) + 100, rows, cols, torch.float32)
+    got, want, sim = moe.orthogonalize(u).double(), ortho.iterate(u), ortho.iterate(u, rounded=True)
+    err, ref = got - want, sim - want
+    assert float(err.square().mean().sqrt()) <= 1.25 * float(ref.square().mean().sqrt())
+    assert float(err.abs().max()) <= 2.5 * float(ref.abs().max())

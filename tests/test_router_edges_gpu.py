@@ -1,6 +1,7 @@
 """The router's losses and gradients where neighbouring tokens share experts, with peaked logits, and at sizes and tables
 that the other tests leave out; against the formulas in 64 bits, with the tolerances of test_router_train_gpu unless
 a test derives its own."""
+import numpy as np
 import pytest
 import torch
 
@@ -99,3 +100,99 @@ def test_one_gradient_that_is_not_finite(T, bad):
     bound = dz_tol @ abs(wv) + (2 * E / 16 + 8) * 2.0 ** -23 * (abs(dz) @ abs(wv))
     bound += r * (abs(want) + bound) + 2.0 ** -25
     assert (abs(d_x[others].double().cpu().numpy() - want) <= bound).all()
+
+
+U = router.U
+
+
+def peaked_reference(s, dw, dl):
+    """Losses and d_z in 64 bits, and how far 32 bits may be off, for logits at any distance from their row's maximum.
+
+    An exponential is 2^((z − top)·log2 e): the difference, the constant and the product are rounded by u each, so at a distance D
+    it is off by 3u·D of itself, ex2 by 4u more, and it may be 2^-126 less (results below are flushed to zero).  The sum
+    adds its terms' errors and at most 37 additions, u each; the reciprocal and the product take 3u.  So a probability is off by
+    (3D + 3·Σ p·D + 48)·u of itself, and the logarithm of the sum by (3·Σ p·D + 41)·u."""
+    z, ids = s["z"].double().cpu().numpy(), s["ids"].cpu().numpy()
+    (T, E), k = z.shape, ids.shape[1]
+    rows = router.sequences(s)
+    n = max(sum(map(len, rows)), 1)
+    bal = zl = bal_tol = zl_tol = 0.0
+    dz, tol = np.zeros((T, E)), np.zeros((T, E))
+    for r in rows:
+        if not len(r):
+            continue
+        p, lse = router.softmax(z[r])
+        top = z[r].max(axis=1)
+        D = top[:, None] - z[r]
+        mean_D = (p * D).sum(axis=1, keepdims=True)
+        p_tol = p * (3 * D + 3 * mean_D + 48) * U + 2.0 ** -125
+        lse_tol = ((3 * mean_D[:, 0] + 41) + 2 * np.abs(lse - top) + np.abs(lse)) * U
+        counts = np.bincount(ids[r].reshape(-1), minlength=E)
+        # sums over tokens: at most 64 additions in fp32, pairs of fp32 beyond
+        bal += (counts * p.sum(axis=0)).sum() / len(r)
+        bal_tol += (counts * (p_tol + 68 * U * p).sum(axis=0)).sum() / len(r)
+        zl += (lse ** 2).sum()
+        zl_tol += (2 * np.abs(lse) * lse_tol + 68 * U * lse ** 2).sum()
+        g, mag = np.zeros((len(r), E)), np.zeros((len(r), E))
+        g += dl[0] * E / (k * n * len(r)) * counts
+        mag += np.abs(g)
+        for j in range(k):
+            np.add.at(g, (np.arange(len(r)), ids[r, j]), dw[r, j])
+            np.add.at(mag, (np.arange(len(r)), ids[r, j]), np.abs(dw[r, j]))
+        zt = (dl[1] * 2 / n * lse)[:, None]
+        zt_tol = (np.abs(dl[1]) * 2 / n * lse_tol)[:, None] + 4 * U * np.abs(zt)
+        dot = (p * g).sum(axis=1, keepdims=True)
+        # g by a few operations; its product with p summed over at most 37 additions
+        dot_tol = ((p_tol + 48 * U * p) * mag).sum(axis=1, keepdims=True)
+        dz[r] = p * (g - dot + zt)
+        size = mag + (p * mag).sum(axis=1, keepdims=True) + np.abs(zt)
+        tol[r] = p_tol * size + p * (dot_tol + zt_tol + 16 * U * size)
+    return (np.array([bal * E / (k * n), zl / n]), np.array([bal_tol * E / (k * n), zl_tol / n]) * (1 + 16 * U), dz, tol)
+
+
+@pytest.mark.parametrize("spread", [3.0, 10.0, 30.0])
+@pytest.mark.parametrize("T,E,k,seqs,masked", [(300, 64, 6, 1, False), (5000, 128, 8, 5, True), (700, 130, 4, 1, False),
+                                               (30000, 60, 6, 3, True), (2500, 1000, 8, 40, False)])
+def test_peaked_logits(T, E, k, seqs, masked, spread):
+    """A router that is sure: most experts' probabilities are tiny or zero."""
+    s = router.make(T, E, k, seqs, masked, seed=T + int(spread), spread=spread)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    x, w = torch.zeros((T, 8), device="cuda").half(), torch.zeros((E, 8), device="cuda").half()
+    dw, dl = torch.randn((T, k), generator=g, device="cuda"), torch.tensor([8.0, 0.5], device="cuda")
+    kw = dict(token_mask=s["mask"], seq_offsets=s["offs"])
+    losses, counts, tokens = moe.router_balance(s["z"], s["ids"], **kw)
+    want, tol, dz, dz_tol = peaked_reference(s, dw.double().cpu().numpy(), dl.double().cpu().numpy())
+    assert (abs(losses.double().cpu().numpy() - want) <= tol).all()
+    d_logits = torch.empty((T, E), device="cuda")
+    moe.router_backward(x, w, s["z"], s["ids"], dw, dl, counts, tokens, d_logits=d_logits, **kw)
+    assert (abs(d_logits.double().cpu().numpy() - dz) <= dz_tol + 1e-43).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_what_is_left_out_of_many_tokens(dtype):
+    """Sequences that leave tokens out at both ends, a mask, and NaN in all of those: the losses in two launches, and d_W in
+    parts, as they are without."""
+    T, E, k, H = 20000, 64, 6, 264
+    s = router.make(T, E, k, 1, True, seed=3)
+    s["offs"] = torch.tensor([5, 9000, 9000, 19000], dtype=torch.int32, device="cuda")
+    out = ~s["mask"]
+    out[:5] = True
+    out[19000:] = True
+    x, w = torch.randn((T, H), device="cuda").to(dtype), torch.randn((E, H), device="cuda").to(dtype)
+    dw, dl = torch.randn((T, k), device="cuda"), torch.tensor([3.0, 0.25], device="cuda")
+    kw = dict(token_mask=s["mask"], seq_offsets=s["offs"])
+    clean = moe.router_balance(s["z"], s["ids"], **kw)
+    want, c, n, tol = router.reference(s)
+    assert (abs(clean[0].double().cpu().numpy() - want) <= tol).all()
+    assert (clean[1].cpu().numpy() == c).all() and (clean[2].cpu().numpy() == n).all()
+    clean_g = moe.router_backward(x, w, s["z"], s["ids"], dw, dl, *clean[1:], **kw)
+    router.check_grads(s, x, w, dw, dl, clean_g, None, c, n)
+    z, xb, dwb, ids = s["z"].clone(), x.clone(), dw.clone(), s["ids"].clone()
+    z[out], xb[out], dwb[out], ids[out] = float("nan"), float("nan"), float("nan"), 10 ** 6
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = moe.router_balance(z, ids, status=status, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, clean))
+    got_g = moe.router_backward(xb, w, z, ids, dwb, dl, *got[1:], status=status, **kw)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got_g, clean_g))
+    assert not got_g[0][out].any() and int(status) == 0
