@@ -80,3 +80,46 @@ def test_many_tiny_matrices(rows, cols):
     err, ref = got - want, sim - want
     assert float(err.square().mean().sqrt()) <= 1.25 * float(ref.square().mean().sqrt())
     assert float(err.abs().max()) <= 2.5 * float(ref.abs().max())
+
+
+def test_the_largest_matrix():
+    """65536 x 65536, more than 2^32 elements: a diagonal of ±1 in some order stays one, and its values follow the polynomial of
+    one number.  (Every sum has a single term: X, A and B are rounded to 11 bits in each step and the result to bf16.)"""
+    n = 65536
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    at = torch.randperm(n, generator=g, device="cuda")
+    sign = torch.randint(0, 2, (n,), generator=g, device="cuda").mul_(2).sub_(1).bfloat16()
+    u = torch.zeros((n, n), dtype=torch.bfloat16, device="cuda")
+    u[torch.arange(n, device="cuda"), at] = sign
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = moe.orthogonalize(u, steps=2, status=status)
+    assert int(status) == 0
+    x, (a, b, c) = 1 / 256, ortho.ABC
+    for _ in range(2):
+        x = a * x + b * x ** 3 + c * x ** 5
+    got = y[torch.arange(n, device="cuda"), at] * sign
+    # two steps whose B (a on its diagonal, 3.4) and X are off by 2^-12 each, then bf16's 2^-8 at most
+    assert float((got.double() / x - 1).abs().max()) <= 2.0 ** -8 + 6 * 2.0 ** -12
+    y[torch.arange(n, device="cuda"), at] = 0
+    assert not any(bool(part.any()) for part in y.split(4096))
+
+
+@pytest.mark.parametrize("rows,cols,steps", [(2, 2, 5), (129, 130, 2)])
+def test_the_most_matrices(rows, cols, steps):
+    n = 65535
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    u = torch.randn((n, rows, cols), generator=g, device="cuda", dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = moe.orthogonalize(u, steps=steps, status=status)
+    assert int(status) == 0 and y.shape == u.shape
+    for part in (slice(0, 50), slice(n // 2, n // 2 + 50), slice(n - 50, n)):
+        want, sim = ortho.iterate(u[part], steps=steps), ortho.iterate(u[part], steps=steps, rounded=True)
+        err, ref = y[part].double() - want, sim - want
+        assert float(err.square().mean().sqrt()) <= 1.25 * float(ref.square().mean().sqrt())
+        assert float(err.abs().max()) <= 2.5 * float(ref.abs().max())

@@ -196,3 +196,70 @@ def test_what_is_left_out_of_many_tokens(dtype):
     got_g = moe.router_backward(xb, w, z, ids, dwb, dl, *got[1:], status=status, **kw)
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got_g, clean_g))
     assert not got_g[0][out].any() and int(status) == 0
+
+
+def test_the_most_tokens():
+    """2^24 of them: losses, counts and gradients against 64 bits, on the device."""
+    T, E, k, H = 1 << 24, 5, 2, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    z = torch.randn((T, E), generator=g, device="cuda")
+    ids = torch.topk(z, k, dim=1).indices.to(torch.int32)
+    mask = torch.rand((T,), generator=g, device="cuda") >= 0.25
+    x, w = torch.randn((T, H), generator=g, device="cuda").half(), torch.randn((E, H), generator=g, device="cuda").half()
+    dw, dl = torch.randn((T, k), generator=g, device="cuda"), torch.tensor([2.0 ** 24, 2.0 ** 22], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    losses, counts, tokens = moe.router_balance(z, ids, token_mask=mask, status=status)
+    d_z = torch.empty((T, E), device="cuda")
+    d_x, d_w = moe.router_backward(x, w, z, ids, dw, dl, counts, tokens, token_mask=mask, d_logits=d_z, status=status)
+    assert int(status) == 0
+    live = mask.double()[:, None]
+    n = int(mask.sum())
+    assert tokens.tolist() == [n, n]
+    assert torch.equal(counts[0].long(), torch.bincount(ids[mask].reshape(-1).long(), minlength=E))
+    zd = z.double()
+    p, lse = torch.softmax(zd, dim=1), torch.logsumexp(zd, dim=1)
+    f, P = counts[0].double(), (p * live).sum(dim=0)
+    want = torch.stack(((f * P).sum() / n * E / (k * n), (lse.square() * live[:, 0]).sum() / n))
+    # a block has 2^24 / 304 tokens, of which a lane adds every 32nd in fp32, then lanes, warps and blocks
+    assert bool(((losses.double() - want).abs() <= (router.P_REL + (55200 / 32 + 70) * U) * 2 * want).all())
+    share = float(dl[0]) * E / (k * n * n) * f
+    gz = share + torch.zeros_like(p).scatter_add_(1, ids.long(), dw.double())
+    zt = (float(dl[1]) * 2 / n * lse)[:, None]
+    ref = p * (gz - (p * gz).sum(dim=1, keepdim=True) + zt) * live
+    mag = gz.abs() + share
+    size = mag + (p * mag).sum(dim=1, keepdim=True) + zt.abs() + float(dl[1]) * 2 / n
+    tol = p * 2 * router.P_REL * size * live
+    assert bool(((d_z.double() - ref).abs() <= tol).all())
+    r = 2.0 ** -11
+    tol = tol + (r + 2 * U) * (ref.abs() + tol) + ref.abs().max() * 2.0 ** -38 * live
+    for got, a, da, b, terms in ((d_x, ref, tol, w.double(), E), (d_w, ref.t(), tol.t(), x.double(), T)):
+        want = a @ b
+        bound = da @ b.abs() + (terms / 16 + 8) * 2.0 ** -23 * (a.abs() @ b.abs())
+        bound += r * (want.abs() + bound) + 2.0 ** -25
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+
+def test_the_most_sequences():
+    T, E, k, S, H = 150000, 40, 3, 65535, 16
+    s = router.make(T, E, k, S, True, seed=5)
+    losses, counts, tokens = moe.router_balance(s["z"], s["ids"], token_mask=s["mask"], seq_offsets=s["offs"])
+    want, c, n, tol = router.reference(s)
+    assert (counts.cpu().numpy() == c).all() and (tokens.cpu().numpy() == n).all()
+    assert (abs(losses.double().cpu().numpy() - want) <= tol).all()
+    x, w = torch.randn((T, H), device="cuda").half(), torch.randn((E, H), device="cuda").half()
+    dw, dl = torch.randn((T, k), device="cuda"), torch.tensor([3e5, 1e4], device="cuda")
+    d_logits = torch.empty((T, E), device="cuda")
+    got = moe.router_backward(x, w, s["z"], s["ids"], dw, dl, counts, tokens, token_mask=s["mask"], seq_offsets=s["offs"],
+                              d_logits=d_logits)
+    router.check_grads(s, x, w, dw, dl, got, d_logits, c, n)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_the_widest_tokens(dtype):
+    T, E, k, H = 3, 3, 2, 1 << 20
+    s = router.make(T, E, k, seed=6)
+    x, w = torch.randn((T, H), device="cuda").to(dtype), torch.randn((E, H), device="cuda").to(dtype)
+    dw = torch.randn((T, k), device="cuda")
+    got = moe.router_backward(x, w, s["z"], s["ids"], dw)
+    router.check_grads(s, x, w, dw, None, got, None, None, [T, T])
