@@ -123,3 +123,18 @@ def test_the_most_matrices(rows, cols, steps):
         err, ref = y[part].double() - want, sim - want
         assert float(err.square().mean().sqrt()) <= 1.25 * float(ref.square().mean().sqrt())
         assert float(err.abs().max()) <= 2.5 * float(ref.abs().max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("share", [1e-2, 1e-4, 1e-6])
+@pytest.mark.parametrize("rows,cols", [(64, 512), (200, 520), (1000, 600)])
+def test_norms_far_below_eps(rows, cols, share, dtype):
+    """Where eps is much more than the norm, fp16 holds X times 2^6 in steps of 2^-24, uniformly off by 2^-25/√3 at root mean
+    square: 2.7e-10 of X, in the first one up to twice that (what is left of 1/eps beside a power of two is below 2).  The products
+    do not matter there, so a step multiplies by a = 3.4445: errors of five X add up to 2.7e-10·√((2a⁵)² + a⁸ + a⁶ + a⁴ + a²)
+    = 2.7e-7, and the result's own rounding is as ever."""
+    u = ortho.draw("normal", 2, rows, cols, dtype)
+    eps = float(u[0].float().norm()) / share
+    got, want = moe.orthogonalize(u, eps=eps), ortho.iterate(u, eps=eps)
+    err = (got.double() - want).square().mean().sqrt()
+    assert float(err) <= 2.5e-3 * float(want.square().mean().sqrt()) + 2.8e-7
