@@ -444,8 +444,8 @@ moe_status_t moe_mx4_down(const uint8_t* h, const uint8_t* h_scales, int64_t tot
  * [0, n_tokens]; sequence s holds tokens seq_offsets[s] .. seq_offsets[s + 1] - 1.  NULL with
  * n_seqs = 1: all tokens are one sequence.  token_mask [n_tokens] bytes, nullable: tokens with
  * 0 do not count.  A token that is masked or in no sequence enters no sum and gets a
- * gradient of zero, and its logits, ids, routed weights and x are not used whatever they
- * hold.  Below, T is the number of tokens that count, T_s that of sequence s, k = top_k,
+ * gradient of zero (d_x where router_w is finite: it is zero times that), and its logits, ids, routed weights and x are
+ * not used whatever they hold.  Below, T is the number of tokens that count, T_s that of sequence s, k = top_k,
  * E = n_experts, z the logits, p = softmax(z); a logit of -infinity has p = 0, and a token with
  * no other (p = 0 everywhere) adds nothing but its T and its ids.  Offsets that decrease or leave the range
  * set MOE_DEV_BAD_TABLE (in every call that has tokens) and leave the outputs undefined.  No output overlaps an input, another output or the
@@ -471,7 +471,7 @@ int64_t moe_router_balance_workspace_bytes(int64_t n_tokens, int32_t n_experts, 
  *   losses      out: [2] fp32
  *   counts      out: [n_seqs, n_experts] int32
  *   seq_tokens  out: [n_seqs + 1] int32, T_s of each sequence, then T
- *   workspace   device memory of moe_router_balance_workspace_bytes() bytes, caller-owned;
+ *   workspace   device memory of moe_router_balance_workspace_bytes() bytes, 16-byte aligned, caller-owned;
  *               calls that overlap on the GPU must not share it
  * Limits: n_experts <= MOE_MAX_EXPERTS, top_k <= min(n_experts, MOE_ROUTER_MAX_TOPK).
  * Sums over tokens are taken in an order that does not change between calls.  One or two kernel launches. */
@@ -502,6 +502,7 @@ int64_t moe_router_backward_workspace_bytes(int64_t n_tokens, int32_t n_experts,
  *   d_logits        out, nullable: d_z, [n_tokens, n_experts] fp32
  *   workspace       device memory of moe_router_backward_workspace_bytes() bytes, caller-owned;
  *                   calls that overlap on the GPU must not share it
+ * x_tokens, router_w, logits, d_x, d_router_w, d_logits and workspace are 16-byte aligned.
  * Limits as in moe_router_balance.  Two to four kernel launches; waits and status_dev as in the
  * feed-forward block. */
 moe_status_t moe_router_backward(int32_t dtype, const uint16_t* x_tokens, int64_t n_tokens, int32_t hidden,
@@ -528,9 +529,11 @@ int64_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t rows, int32_t c
  * 3.4445, -4.775, 2.0315 in five steps: into about 0.7 .. 1.2 from 0.01 of the norm on).
  *   update  [batch, rows, cols], `dtype` MOE_DTYPE_F16, _BF16 or _F32
  *   out     out: [batch, rows, cols] bf16
- * Any rows and cols.  Products are of fp16 operands with fp32 sums: with such coefficients the result is
+ * Any rows and cols.  update, out and workspace are 16-byte aligned (a matrix inside a stack of odd sizes is not always).
+ * Products are of fp16 operands with fp32 sums: with such coefficients the result is
  * within 2e-3 to 3e-3 of the exact one (root mean square, relative to that of the exact one, rounding to
- * bf16 included) whatever G's spectrum, so no finer type is offered.  A matrix that holds an infinity or
+ * bf16 included) whatever G's spectrum, so no finer type is offered; where ‖G‖ is far below eps and the result nearly
+ * zero, an absolute 3e-7 besides (fp16's steps).  A matrix that holds an infinity or
  * a NaN, or whose norm leaves fp32's squares (1.8e19), becomes NaN; one of zeros stays zeros, whatever
  * eps is (0 too); the others of the stack do not see it.  The norm is taken as at least
  * 2^-69·√(rows·cols), that of entries of 1.7e-21, below which fp32's squares do not give it.  Coefficients are at most MOE_ORTHO_MAX_COEFFICIENT in magnitude, |b| at most 2048 |c|

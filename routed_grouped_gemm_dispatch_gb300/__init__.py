@@ -869,7 +869,8 @@ def router_backward(x_tokens, router_w, logits, topk_ids, d_topk_weights=None, d
     and shapes, float16 or bfloat16; hidden a multiple of 8.  ``token_mask`` and
     ``seq_offsets`` as in router_balance: a token that does not count has a gradient of zero.
     ``d_logits`` (fp32 [T, E]) receives the gradients of the logits.  Supplied buffers are
-    written, not added to, and overlap no input.  ``workspace``: a device tensor of at least
+    written, not added to, and overlap no input.  All but the ids, routed gradients, losses, counts and what describes the
+    sequences start on 16-byte boundaries.  ``workspace``: a device tensor of at least
     router_backward_workspace_bytes(T, E, hidden) bytes."""
     import torch
     f32, i32 = torch.float32, torch.int32
@@ -919,7 +920,8 @@ def orthogonalize(update, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315)
     (``out`` may be supplied).  Each matrix of a stack is taken by itself; one of zeros stays zeros
     whatever ``eps`` is (a norm is taken as at least that of entries of 1.7e-21).  Products
     are of 16-bit operands with fp32 sums: the result is within 2e-3 to 3e-3 of the exact one, root mean
-    square, bf16's own rounding included.  ``out`` does not overlap ``update``.
+    square, bf16's own rounding included.  ``out`` does not overlap ``update``, and both start on 16-byte boundaries (a
+    matrix of a stack of odd sizes, or a view into a buffer of several, may not: clone it, or pass the stack).
     ``workspace``: a device tensor of at least orthogonalize_workspace_bytes(batch, rows, cols) bytes."""
     import torch
     dt = getattr(update, "dtype", None)

@@ -19,7 +19,9 @@
 //
 // Numbers.  All operands are fp16 (11 bits at the rate of bf16's 8), times powers of two that
 // keep them normal: X·2^6, A·2^10, B·2^6; sums are fp32.  X₀ is G times a power of two, which
-// is exact, and the rest of 1/‖G‖ enters the first step's fp32 sums.  Values whose norm
+// is exact for 16-bit values but for those below 2^-20 of the norm (fp16 holds them in steps of 2^-24, 2^-30 of the
+// norm: less than the result's own rounding in any matrix whose norm is at least eps), and the rest of 1/‖G‖ enters the
+// first step's fp32 sums.  Values whose norm
 // grows past 2^9 in a step (coefficients that diverge) overflow.
 //
 // What a tile needs besides its sums would come from L2 beside the operands, whose way from there is
@@ -33,11 +35,11 @@
 //    and e4m3 (hi alone is the products' operand).
 // Bound.  A stack: the operands' way from L2, whose 0.2 us for 64 along K of a 256 x 128 tile is 1.6 PFLOP/s
 // on all pairs (0.326 and 2.0 for 256 x 256), and the tiles' empty rows (1408 are 5.5 panels); 64 x
-// 1408 x 2048 takes 3.65 ms where its operations are 2.45 at the measured rate of bf16, and 4.1 back to back under the
+// 1408 x 2048 takes 3.7 ms where its operations are 2.45 at the measured rate of bf16, and 4.1 to 4.3 back to back under the
 // power cap.  One matrix: besides, each product waits for the one before, with some 6.3 us from its
 // operands' completion to its own where it has few tiles (a poll that sees it 1.4, copies and K loop 2 to 3.5,
 // epilogue 1.5, publishing 0.7), and few whole rounds of tiles: 2816 x 2048 257 us (operations 113),
-// 2048 x 7168 422 (253), 3 x 333 x 1001 104 (2.8).
+// 2048 x 7168 425 to 445 (253), 3 x 333 x 1001 104 (2.8).
 //
 // In 64-bit simulation with these roundings, the root mean square error of five steps relative to that
 // of the result:

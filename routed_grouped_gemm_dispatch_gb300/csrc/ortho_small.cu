@@ -10,7 +10,7 @@
 //     A², B = b·A + c·A² in every CTA, a·X + B·X of its columns.
 // The same bytes are a K-major operand for X·Xᵀ and an M/N-major one for B·X.
 //
-// 64 x 2048 takes 34 us, 6 a step, against 100 of the tiles in L2.  Bound: the chain of
+// 64 x 2048 takes 32.4 us, 6 a step, against 100 of the tiles in L2.  Bound: the chain of
 // three products, two exchanges and three passes over registers, with one warp's latency
 // in each (the tensor pipe is busy for 0.7% of it).  Roundings: X as an operand (fp16) and the result (bf16); a·X is fp32, and A and B are each the
 // sum of two fp16 matrices: with few rows there are few singular values, whose errors do not

@@ -197,7 +197,8 @@ __device__ __forceinline__ void merge_topk(float (&v)[K], int32_t (&e)[K], const
 // (>= top_k).  PAIR (with S = 1): clusters of two CTAs, each with its own
 // tile, share one 2-SM MMA of M = 256 tokens: each CTA loads its tile's x
 // and half of W_g's rows, so each SM receives a third fewer bytes.
-// LOGITS: also stores the logits (of its own, as the branch alone took 2% of the others' time).
+// LOGITS: also stores the logits (of its own, as the branch alone took 2% of the others' time; 16384 tokens of 256 experts,
+// hidden 7168: 55 us without and 59.5 with).
 template <int S, int KMAX, bool PAIR, bool LOGITS>
 __global__ void __launch_bounds__(R_THREADS, 1)
 router_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,

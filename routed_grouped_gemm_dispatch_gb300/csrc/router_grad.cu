@@ -14,10 +14,11 @@
 //    infinity or a NaN, which the pass over the logits looks for, they are cleared in shared
 //    memory first.
 //
-// Bound: HBM.  16384 x 256 x 7168 moves 467 MB in these products (255 read, 212 written), at 4.5 TB/s over
-// a launch of 103 us (cold, by itself) with the tensor pipe 51% busy; the whole call takes 124 as a graph, its
-// bytes 73 at the rate of a copy.  4097 x 64 x 2048 takes 23.6 (bytes 5.2) and 32 x 128 x 2048 12.1 (0.2):
-// the chain of launches, fill, K loop and stores.
+// Bound: no single unit.  16384 x 256 x 7168 moves 467 MB in these products (255 read, 212 written; 69 us at the rate of a
+// copy) in a launch of 104 us (cold, by itself), with DRAM at 56% of its peak, L2 at 44% (1142 MB go to the SMs: W_g's and
+// d_z's tiles again for every tile), the tensor pipe at 51% and the SMs active for 89% of the time; which waits keep
+// all of them below their limits has not been taken apart.  The whole call takes 123 to 125 as a graph.
+// 4097 x 64 x 2048 takes 23.7 (bytes 5.2) and 32 x 128 x 2048 12.1 (0.2): the chain of launches, fill, K loop and stores.
 //
 // Rounding: d_x and d_W once from fp32.  d_z, an operand of 16-bit products, once too where there are many
 // tokens: over thousands of them its roundings add half as much again as that of the result to the

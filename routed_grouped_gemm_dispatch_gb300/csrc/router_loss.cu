@@ -13,10 +13,11 @@
 // tokens of a warp and of a block and pairs of fp32 (Sum) beyond, always in the same
 // order.  (FP64 is slow here: with it the second launch took 16 us, by itself, for 32 tokens.)
 //
-// Bound: latency.  The losses of 16384 x 256 (17 MB, 2.6 us of HBM) take 16.6 us in two launches: a block's 64
+// Bound: latency.  The losses of 16384 x 256 (17 MB, 2.6 us of HBM) take 15.5 to 17 us in two launches: a block's 64
 // tokens are two rounds of loads, exponentials and sums over lanes, then come its warps' sums, and a
-// second launch that waits for the first, reads the parts and counts its blocks.  One cluster needs no second
-// launch: 4097 x 64 in five sequences 9.4 us, 32 x 128 4.0.  The gradients of 16384 x 256 logits take
+// second launch that waits for the first, reads the parts and counts its blocks.  (No unit is busy: 21% of the SMs' issue
+// rate in the first launch.)  One cluster needs no second
+// launch: 4097 x 64 in five sequences 9.4 us, 32 x 128 3.9.  The gradients of 16384 x 256 logits take
 // 15 us cold (34 MB), their rounding 8.5.
 #include <cuda_runtime.h>
 
@@ -77,9 +78,9 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // The row becomes its softmax; returns its logsumexp.  (A row of minus infinities has no probability anywhere: all
-// zeros, and 0.)  An exponential is 2^(z log2 e - top log2 e), the
-// difference rounded once more and ex2.approx (2^-22): its rounding is an absolute error of the exponent, so the
-// relative error grows with the distance from the row's maximum, by 2^-24 of it.
+// zeros, and 0.)  An exponential is 2^((z - top) log2 e) by ex2.approx (2^-22).  The difference, the constant and the
+// product are rounded by 2^-24 each, which is an absolute error of the exponent: at a distance D from the row's maximum
+// the exponential is off by 3·2^-24·D of itself besides, and below 2^-126 it is 0.
 template <int L, int PER>
 __device__ __forceinline__ float softmax_row(float (&z)[PER]) {
     float top = z[0];
